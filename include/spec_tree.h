@@ -468,6 +468,84 @@ spec_status tree_kv_commit_paged(const void* k_tree, const void* v_tree, void* k
                                  const int32_t* accept_path, const spec_tree* tree, int32_t B, int32_t Hkv,
                                  int32_t D, spec_dtype dt, void* ws, size_t ws_bytes, spec_stream_t s);
 
+/* Workspace bytes kv_append and kv_append_paged need (their status word only). */
+size_t kv_append_workspace_size(void);
+
+/*
+ * Append new tokens of a ragged batch to the KV cache, keys rotated to their
+ * positions on the way, and rotate their queries in the same launch.  The tokens
+ * of sequence b are rows seq_start[b] .. seq_start[b + 1] - 1 of the projections;
+ * token number i of them goes to cache position prefix_len[b] + i and is rotated
+ * as position
+ *     pos = pos_base + prefix_len[b] + i,  angles  phi_j = pos * freq[j]:
+ *     x' = x cos(phi_j) - y sin(phi_j),    y' = x sin(phi_j) + y cos(phi_j)
+ * for the pairs (x, y) = elements (j, j + rot/2) of a head, or (2j, 2j + 1) when
+ * interleaved; elements rot .. D - 1 pass unchanged.  Values are copied.  Angles
+ * are taken in 64 bits, the rotation in 32, rounded once to dt.
+ * prefix_len is read, not advanced: the layers of a model append at the same place.
+ *
+ *   q, k, v       device, rows of Hq, Hkv and Hkv heads x D (dense), q_stride, k_stride and
+ *                 v_stride elements between tokens: slices of one packed projection, say.  q may
+ *                 be NULL (then q_out too).  16-byte aligned, strides multiples of 16 bytes
+ *   N             rows of the projections, 0 .. 2^28
+ *   seq_start     device [B + 1], not decreasing, within 0 .. N; rows before the first and behind
+ *                 the last sequence are neither read into the cache nor written to q_out
+ *   prefix_len    device [B]
+ *   pos_base      device [1] added to every position (the length of a shared prefix), or NULL
+ *   freq          device float64 [rot / 2], radians per position; NULL with rot = 0
+ *   rot           even, 0 .. D: leading elements of a head that are rotated
+ *   k_cache, v_cache  device [B, Hkv, Lmax, D] (dt), updated in place
+ *   q_out         device [N, Hq, D] (dt); it must not overlap q, k or v
+ *   ws            >= kv_append_workspace_size() bytes, 16-byte aligned
+ * Shapes: D a multiple of 16 bytes, D <= 1024, 1 <= B <= 65535, Lmax <= 2^22.
+ * A sequence with a negative prefix_len or whose tokens would pass Lmax, and
+ * offsets that decrease or leave 0 .. N, are reported as SPEC_EINVAL in the
+ * status word; such a sequence's rows are left unchanged, and its q_out too.
+ */
+spec_status kv_append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, int32_t N, const int32_t* seq_start, int32_t B, int32_t Hq, int32_t Hkv,
+                      int32_t D, const int32_t* prefix_len, const int32_t* pos_base, const double* freq,
+                      int32_t rot, int32_t interleaved, void* k_cache, void* v_cache, int32_t Lmax,
+                      spec_dtype dt, void* q_out, void* ws, size_t ws_bytes, spec_stream_t s);
+
+/*
+ * kv_append into a paged cache, the layout tree_attention_paged reads: position
+ * p of sequence b is row p % block_size of pool block block_table[b, p / block_size].
+ *
+ *   k_pool, v_pool  device [num_blocks, Hkv, block_size, D] (dt), updated in place
+ *   block_table     device [B, max_blocks] int32; only the entries of blocks the append writes
+ *                   are read.  A block that is written belongs to one sequence
+ *   block_size      positive; max_blocks * block_size <= 2^22
+ *   the rest as kv_append, with max_blocks * block_size for Lmax.
+ * Tokens whose block lies outside 0 .. num_blocks-1 are not written (their q_out
+ * neither) and SPEC_EINVAL goes to the status word.
+ */
+spec_status kv_append_paged(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, int32_t N, const int32_t* seq_start, int32_t B, int32_t Hq,
+                            int32_t Hkv, int32_t D, const int32_t* prefix_len, const int32_t* pos_base,
+                            const double* freq, int32_t rot, int32_t interleaved, void* k_pool, void* v_pool,
+                            int32_t num_blocks, const int32_t* block_table, int32_t max_blocks,
+                            int32_t block_size, spec_dtype dt, void* q_out, void* ws, size_t ws_bytes,
+                            spec_stream_t s);
+
+/*
+ * The tree nodes' projections, rotated and laid out for tree attention: node i of
+ * sequence b is row b * T + i of q, k and v and is rotated (kv_append) as position
+ *     pos_base + prefix_len[b] + depth[i],
+ * the position it would have on its path.  A one-node tree is the form for
+ * single tokens.  The rotated keys are the ones tree_kv_commit copies.
+ *
+ *   q, k, v             device, B * T rows, strides as in kv_append
+ *   q_out               device [B, Hq, T, D] (dt) out
+ *   k_tree, v_tree      device [B, Hkv, T, D] (dt) out; no output may overlap q, k or v
+ *   the rest as kv_append.  The call has no workspace and no device status.
+ */
+spec_status tree_rope(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, const spec_tree* tree, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                      const int32_t* prefix_len, const int32_t* pos_base, const double* freq, int32_t rot,
+                      int32_t interleaved, spec_dtype dt, void* q_out, void* k_tree, void* v_tree,
+                      spec_stream_t s);
+
 /* Message of the last failed call on this host thread ("" if none). */
 const char* spec_last_error(void);
 

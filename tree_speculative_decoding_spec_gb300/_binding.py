@@ -60,6 +60,7 @@ def _load():
                           "tree_speculative_decoding_spec_gb300.build)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, sz, i32, u64, f32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_uint64, ctypes.c_float
+    i64 = ctypes.c_int64
     tp = ctypes.POINTER(spec_tree)
     sig = {
         "spec_tree_device_bytes": (sz, [i32]),
@@ -87,6 +88,13 @@ def _load():
         "tree_kv_commit": (i32, [vp, vp, vp, vp, vp, vp, vp, tp, i32, i32, i32, i32, i32, vp, sz, vp]),
         "tree_kv_commit_paged": (i32, [vp, vp, vp, vp, i32, vp, i32, i32, vp, vp, vp, tp, i32, i32, i32, i32, vp, sz,
                                        vp]),
+        "kv_append_workspace_size": (sz, []),
+        "kv_append": (i32, [vp, vp, vp, i64, i64, i64, i32, vp, i32, i32, i32, i32, vp, vp, vp, i32, i32, vp, vp, i32,
+                            i32, vp, vp, sz, vp]),
+        "kv_append_paged": (i32, [vp, vp, vp, i64, i64, i64, i32, vp, i32, i32, i32, i32, vp, vp, vp, i32, i32, vp, vp,
+                                  i32, vp, i32, i32, i32, vp, vp, sz, vp]),
+        "tree_rope": (i32, [vp, vp, vp, i64, i64, i64, tp, i32, i32, i32, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp,
+                            vp]),
         "spec_philox_uniform": (i32, [u64, u64, i32, i32, vp, vp, vp]),
         "spec_last_error": (ctypes.c_char_p, []),
         "spec_read_device_status": (i32, [vp, _i32p, vp]),
@@ -625,6 +633,165 @@ def tree_accept_typical(logits_p, node_tok, tree, temperature=1.0, epsilon=0.09,
             int(seed), int(offset), _ptr(accept_len), _ptr(accept_path), _ptr(next_token), _ptr(margin), _ptr(ws),
             ws.numel(), _stream(stream)))
     return accept_len, accept_path, next_token, margin
+
+
+def _new(stream, device, dtype, *shape):
+    """A tensor this binding allocates for a call on `stream`: its memory must outlive the call there."""
+    t = torch.empty(*shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _rows(t, name, dtype, device, lead):
+    """Check token rows [*lead, heads, D] with dense heads and evenly spaced tokens; returns (heads, D, token stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(lead) + 2 or tuple(t.shape[:-2]) != tuple(lead):
+        raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, heads, D], got {tuple(t.shape)}")
+    H, D = t.shape[-2:]
+    st = t.stride()
+    if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
+        raise ValueError(f"{name}: a token's heads must be dense")
+    # the stride of the innermost token dimension longer than one, and the outer ones in step with it
+    step, span = None, 1
+    for n, k in zip(reversed(lead), reversed(st[:-2])):
+        if n > 1:
+            if step is None:
+                step = k
+            elif k != span * step:
+                raise ValueError(f"{name}: tokens must be evenly spaced")
+            span *= n
+    return H, D, H * D if step is None else step
+
+
+def _rope_args(freq, rot_max, pos_base, dev):
+    rot = 0
+    if freq is not None:
+        _need(freq, "freq", dtype=torch.float64, ndim=1, device=dev)
+        rot = 2 * freq.shape[0]
+        if rot > rot_max:
+            raise ValueError(f"freq has {freq.shape[0]} entries for heads of {rot_max}")
+    if pos_base is not None:
+        _need(pos_base, "pos_base", dtype=torch.int32, device=dev)
+        if pos_base.numel() != 1:
+            raise ValueError("pos_base must hold one value")
+    return rot
+
+
+def kv_append_workspace_size():
+    return int(_lib.kv_append_workspace_size())
+
+
+def _append_args(q, k, v, seq_start, prefix_len, freq, pos_base, q_out, ws, stream):
+    if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor [N, Hkv, D]")
+    dev, N = k.device, k.shape[0]
+    Hkv, D, ks = _rows(k, "k", k.dtype, dev, (N,))
+    Hv, Dv, vs = _rows(v, "v", k.dtype, dev, (N,))
+    if (Hv, Dv) != (Hkv, D):
+        raise ValueError("v must match k")
+    Hq, qs = 0, 0
+    if q is not None:
+        Hq, Dq, qs = _rows(q, "q", k.dtype, dev, (N,))
+        if Dq != D:
+            raise ValueError("q must have k's head dimension")
+        if q_out is None:
+            q_out = _new(stream, dev, k.dtype, N, Hq, D)
+        _need(q_out, "q_out", dtype=k.dtype, ndim=3, device=dev)
+        if tuple(q_out.shape) != (N, Hq, D):
+            raise ValueError("q_out must be [N, Hq, D]")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _need(seq_start, "seq_start", dtype=torch.int32, ndim=1, device=dev)
+    _need(prefix_len, "prefix_len", dtype=torch.int32, ndim=1, device=dev)
+    B = prefix_len.shape[0]
+    if seq_start.shape[0] != B + 1:
+        raise ValueError("seq_start must be [B + 1]")
+    rot = _rope_args(freq, D, pos_base, dev)
+    if ws is None:
+        ws = _new(stream, dev, torch.uint8, kv_append_workspace_size())
+    _need(ws, "ws", device=dev)
+    return dev, N, B, Hq, Hkv, D, qs, ks, vs, rot, q_out, ws
+
+
+def kv_append(q, k, v, seq_start, prefix_len, k_cache, v_cache, freq=None, interleaved=False, pos_base=None, q_out=None,
+              ws=None, stream=None):
+    """Append ragged new tokens to contiguous caches, keys rotated on the way: returns (q_out or None, ws).
+
+    q [N, Hq, D] (or None), k, v [N, Hkv, D]: token rows, slices of a packed projection allowed; seq_start [B + 1];
+    caches [B, Hkv, Lmax, D] updated in place; freq float64 [rot / 2] radians per position (None: no rotation)."""
+    dev, N, B, Hq, Hkv, D, qs, ks, vs, rot, q_out, ws = _append_args(q, k, v, seq_start, prefix_len, freq, pos_base, q_out,
+                                                                     ws, stream)
+    _need(k_cache, "k_cache", dtype=k.dtype, ndim=4, device=dev)
+    _need(v_cache, "v_cache", dtype=k.dtype, ndim=4, device=dev)
+    Lmax = k_cache.shape[2]
+    if tuple(k_cache.shape) != (B, Hkv, Lmax, D) or v_cache.shape != k_cache.shape:
+        raise ValueError("caches must be [B, Hkv, Lmax, D]")
+    with torch.cuda.device(dev):
+        _check("kv_append", _lib.kv_append(
+            _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, N, _ptr(seq_start), B, Hq, Hkv, D, _ptr(prefix_len), _ptr(pos_base),
+            _ptr(freq), rot, int(interleaved), _ptr(k_cache), _ptr(v_cache), Lmax, _dtype_code(k), _ptr(q_out), _ptr(ws),
+            ws.nbytes, _stream(stream)))
+    return q_out, ws
+
+
+def kv_append_paged(q, k, v, seq_start, prefix_len, k_pool, v_pool, block_table, freq=None, interleaved=False,
+                    pos_base=None, q_out=None, ws=None, stream=None):
+    """kv_append into a paged cache: pools [num_blocks, Hkv, block_size, D], block_table [B, max_blocks] int32."""
+    dev, N, B, Hq, Hkv, D, qs, ks, vs, rot, q_out, ws = _append_args(q, k, v, seq_start, prefix_len, freq, pos_base, q_out,
+                                                                     ws, stream)
+    _need(k_pool, "k_pool", dtype=k.dtype, ndim=4, device=dev)
+    _need(v_pool, "v_pool", dtype=k.dtype, ndim=4, device=dev)
+    num_blocks, bs = k_pool.shape[0], k_pool.shape[2]
+    if tuple(k_pool.shape) != (num_blocks, Hkv, bs, D) or v_pool.shape != k_pool.shape:
+        raise ValueError("pools must be [num_blocks, Hkv, block_size, D]")
+    _need(block_table, "block_table", dtype=torch.int32, ndim=2, device=dev)
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_blocks]")
+    with torch.cuda.device(dev):
+        _check("kv_append_paged", _lib.kv_append_paged(
+            _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, N, _ptr(seq_start), B, Hq, Hkv, D, _ptr(prefix_len), _ptr(pos_base),
+            _ptr(freq), rot, int(interleaved), _ptr(k_pool), _ptr(v_pool), num_blocks, _ptr(block_table),
+            block_table.shape[1], bs, _dtype_code(k), _ptr(q_out), _ptr(ws), ws.nbytes, _stream(stream)))
+    return q_out, ws
+
+
+def tree_rope(q, k, v, prefix_len, tree, freq=None, interleaved=False, pos_base=None, q_out=None, k_out=None, v_out=None,
+              stream=None):
+    """Rotate the tree nodes' projections q [B, T, Hq, D], k, v [B, T, Hkv, D] to their depths:
+    returns (q [B, Hq, T, D], k_tree, v_tree [B, Hkv, T, D]), the inputs of tree attention."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, T, Hq, D]")
+    dev, (B, T) = q.device, q.shape[:2]
+    if T != tree.T:
+        raise ValueError(f"q has {T} nodes, the tree {tree.T}")
+    Hq, D, qs = _rows(q, "q", q.dtype, dev, (B, T))
+    Hkv, Dk, ks = _rows(k, "k", q.dtype, dev, (B, T))
+    Hv, Dv, vs = _rows(v, "v", q.dtype, dev, (B, T))
+    if Dk != D or (Hv, Dv) != (Hkv, D):
+        raise ValueError("k and v must match, with q's head dimension")
+    _need(prefix_len, "prefix_len", dtype=torch.int32, ndim=1, device=dev)
+    if prefix_len.shape[0] != B:
+        raise ValueError("prefix_len must be [B]")
+    rot = _rope_args(freq, D, pos_base, dev)
+    outs = []
+    for name, t, H in (("q_out", q_out, Hq), ("k_out", k_out, Hkv), ("v_out", v_out, Hkv)):
+        if t is None:
+            t = _new(stream, dev, q.dtype, B, H, T, D)
+        _need(t, name, dtype=q.dtype, ndim=4, device=dev)
+        if tuple(t.shape) != (B, H, T, D):
+            raise ValueError(f"{name} must be {(B, H, T, D)}")
+        outs.append(t)
+    with torch.cuda.device(dev):
+        _check("tree_rope", _lib.tree_rope(
+            _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, tree.ref(), B, Hq, Hkv, D, _ptr(prefix_len), _ptr(pos_base), _ptr(freq),
+            rot, int(interleaved), _dtype_code(q), _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), _stream(stream)))
+    return tuple(outs)
 
 
 def spec_philox_uniform(seed, offset, B, T, device=None, stream=None):
