@@ -468,6 +468,104 @@ spec_status tree_kv_commit_paged(const void* k_tree, const void* v_tree, void* k
                                  const int32_t* accept_path, const spec_tree* tree, int32_t B, int32_t Hkv,
                                  int32_t D, spec_dtype dt, void* ws, size_t ws_bytes, spec_stream_t s);
 
+/*
+ * What happens to a score between the product and the softmax (NULL: nothing).
+ * With P the query's position and p the key's, positions counted over the shared
+ * prefix, the cached prefix and a node's depth:
+ *     x = scale q.k
+ *     x = softcap * tanh(x / softcap)       if softcap > 0
+ *     x = x - slopes[h] * (P - p)           if slopes, h the query head
+ *     the key is seen only if P - p < window, if window > 0 (the query itself always is)
+ */
+typedef struct {
+    float softcap;          /* 0: none; else >= 1e-6, finite */
+    int32_t window;         /* 0: none */
+    const float* slopes;    /* device [Hq], finite, or NULL */
+} spec_score;
+
+/* Workspace bytes tree_attention_shared and its paged form (Lshared = shared_blocks * block_size,
+ * Lmax = max_blocks * block_size) need on the current device (0 on invalid arguments). */
+size_t tree_attention_shared_workspace_size(const spec_tree* tree, int32_t B, int32_t Hq, int32_t Hkv,
+                                            int32_t Lshared, int32_t Lmax, int32_t D, spec_dtype dt);
+
+/*
+ * Tree attention of a batch whose sequences share a long prefix (a system prompt, a
+ * document, the samples of one prompt): sequence b's keys are the shared ones, then its
+ * own cached ones, then its tree's.  The result is tree_attention's over their
+ * concatenation; the shared keys are read once for as many sequences as fill a
+ * block of query rows, not once per sequence.
+ *     keys  = k_shared[:shared_len], k_cache[b, :prefix_len[b]], k_tree[b, a] for a in anc*(i)
+ *     out   = softmax(x) . values,  lse = log(sum exp(x)),  x the scores (spec_score)
+ *
+ *   q                 device [B, Hq, T, D]
+ *   k_shared, v_shared  device [Hkv, Lshared, D]
+ *   shared_len        device [1], in 0 .. Lshared (clamped)
+ *   k_cache, v_cache  device [B, Hkv, Lmax, D]: the sequences' own keys behind the shared ones;
+ *                     rows >= prefix_len[b] do not affect the result but must be readable
+ *   prefix_len        device [B], each in 0 .. Lmax (clamped), without the shared keys
+ *   k_tree, v_tree    device [B, Hkv, T, D]
+ *   score             host, or NULL
+ *   out               device [B, Hq, T, D] in dt, the inputs' type (tree_attention's is float32)
+ *   lse               device [B, Hq, T] float32, or NULL
+ *   scale             > 0, or 0 for the usual 1/sqrt(D)
+ * Shapes: Hq % Hkv == 0, D in {64, 128}, 1 <= Lshared, Lmax <= 2^22; T = 1 is the form for
+ * single tokens.  With bf16 inputs the softmax's weights are rounded to bf16 before they
+ * weigh the values; their sum, and everything else, is in 32 bits.  Values of keys that a
+ * node does not see (of other branches, or in front of its window) weigh zero and must be
+ * finite to do so.
+ */
+spec_status tree_attention_shared(const void* q, const void* k_shared, const void* v_shared,
+                                  const int32_t* shared_len, int32_t Lshared, const void* k_cache,
+                                  const void* v_cache, const int32_t* prefix_len, const void* k_tree,
+                                  const void* v_tree, const spec_tree* tree, int32_t B, int32_t Hq, int32_t Hkv,
+                                  int32_t Lmax, int32_t D, float scale, const spec_score* score, spec_dtype dt,
+                                  void* out, float* lse, void* ws, size_t ws_bytes, spec_stream_t s);
+
+/*
+ * tree_attention_shared over a paged cache: shared and own keys in the blocks of one pool.
+ *   k_pool, v_pool  device [num_blocks, Hkv, block_size, D]
+ *   shared_table    device [shared_blocks] int32: the shared prefix's blocks in order; the first
+ *                   ceil(shared_len / block_size) entries are read
+ *   block_table     device [B, max_blocks] int32: each sequence's own blocks, the first
+ *                   ceil(prefix_len[b] / block_size) entries are read
+ *   block_size      a positive multiple of 16; max_blocks and shared_blocks times it <= 2^22
+ *   the rest as tree_attention_shared.
+ * A table entry outside 0 .. num_blocks-1 is reported as SPEC_EINVAL in the status word and
+ * no memory outside the pool is read; what the sequences that use the block get is undefined.
+ */
+spec_status tree_attention_shared_paged(const void* q, const void* k_pool, const void* v_pool, int32_t num_blocks,
+                                        const int32_t* shared_table, int32_t shared_blocks,
+                                        const int32_t* shared_len, const int32_t* block_table, int32_t max_blocks,
+                                        int32_t block_size, const int32_t* prefix_len, const void* k_tree,
+                                        const void* v_tree, const spec_tree* tree, int32_t B, int32_t Hq,
+                                        int32_t Hkv, int32_t D, float scale, const spec_score* score,
+                                        spec_dtype dt, void* out, float* lse, void* ws, size_t ws_bytes,
+                                        spec_stream_t s);
+
+/* Workspace bytes tree_attention_scored and its paged form (Lmax = max_blocks * block_size) need
+ * on the current device (0 on invalid arguments). */
+size_t tree_attention_scored_workspace_size(const spec_tree* tree, int32_t B, int32_t Hq, int32_t Hkv,
+                                            int32_t Lmax, int32_t D, spec_dtype dt);
+
+/*
+ * Tree attention with transformed scores: tree_attention_shared without a shared prefix, for
+ * models that cap their scores, bias them by distance or look back over a window.  Keys in
+ * front of every node's window are not read.
+ */
+spec_status tree_attention_scored(const void* q, const void* k_cache, const void* v_cache, const int32_t* prefix_len,
+                                  const void* k_tree, const void* v_tree, const spec_tree* tree, int32_t B,
+                                  int32_t Hq, int32_t Hkv, int32_t Lmax, int32_t D, float scale,
+                                  const spec_score* score, spec_dtype dt, void* out, float* lse, void* ws,
+                                  size_t ws_bytes, spec_stream_t s);
+
+/* tree_attention_scored over a paged cache (tree_attention_shared_paged's, without the shared blocks). */
+spec_status tree_attention_scored_paged(const void* q, const void* k_pool, const void* v_pool, int32_t num_blocks,
+                                        const int32_t* block_table, int32_t max_blocks, int32_t block_size,
+                                        const int32_t* prefix_len, const void* k_tree, const void* v_tree,
+                                        const spec_tree* tree, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                        float scale, const spec_score* score, spec_dtype dt, void* out, float* lse,
+                                        void* ws, size_t ws_bytes, spec_stream_t s);
+
 /* Workspace bytes kv_append and kv_append_paged need (their status word only). */
 size_t kv_append_workspace_size(void);
 

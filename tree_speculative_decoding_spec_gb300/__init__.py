@@ -12,6 +12,8 @@ __all__ = [
     "tree_attention", "tree_attention_workspace_size", "tree_attention_noalloc",
     "tree_attention_noalloc_status",
     "tree_attention_paged", "tree_attention_paged_workspace_size",
+    "tree_attention_shared", "tree_attention_shared_paged", "tree_attention_shared_workspace_size",
+    "tree_attention_scored", "tree_attention_scored_paged", "tree_attention_scored_workspace_size",
     "tree_accept", "tree_accept_workspace_size", "tree_accept_typical",
     "tree_kv_commit", "tree_kv_commit_paged", "tree_kv_commit_workspace_size",
     "kv_append", "kv_append_paged", "kv_append_workspace_size", "tree_rope",

@@ -44,6 +44,10 @@ class spec_head(ctypes.Structure):
                 ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("W2", ctypes.c_void_p)]
 
 
+class spec_score(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p)]
+
+
 class spec_trace_entry(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_int32), ("total_ms", ctypes.c_double)]
 
@@ -62,6 +66,7 @@ def _load():
     vp, sz, i32, u64, f32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_uint64, ctypes.c_float
     i64 = ctypes.c_int64
     tp = ctypes.POINTER(spec_tree)
+    sp = ctypes.POINTER(spec_score)
     sig = {
         "spec_tree_device_bytes": (sz, [i32]),
         "spec_tree_build": (i32, [vp, vp, i32, vp, sz, tp, vp]),
@@ -88,6 +93,16 @@ def _load():
         "tree_kv_commit": (i32, [vp, vp, vp, vp, vp, vp, vp, tp, i32, i32, i32, i32, i32, vp, sz, vp]),
         "tree_kv_commit_paged": (i32, [vp, vp, vp, vp, i32, vp, i32, i32, vp, vp, vp, tp, i32, i32, i32, i32, vp, sz,
                                        vp]),
+        "tree_attention_shared_workspace_size": (sz, [tp, i32, i32, i32, i32, i32, i32, i32]),
+        "tree_attention_scored_workspace_size": (sz, [tp, i32, i32, i32, i32, i32, i32]),
+        "tree_attention_shared": (i32, [vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, tp, i32, i32, i32, i32, i32, f32, sp, i32,
+                                        vp, vp, vp, sz, vp]),
+        "tree_attention_shared_paged": (i32, [vp, vp, vp, i32, vp, i32, vp, vp, i32, i32, vp, vp, vp, tp, i32, i32, i32,
+                                              i32, f32, sp, i32, vp, vp, vp, sz, vp]),
+        "tree_attention_scored": (i32, [vp, vp, vp, vp, vp, vp, tp, i32, i32, i32, i32, i32, f32, sp, i32, vp, vp, vp, sz,
+                                        vp]),
+        "tree_attention_scored_paged": (i32, [vp, vp, vp, i32, vp, i32, i32, vp, vp, vp, tp, i32, i32, i32, i32, f32, sp,
+                                              i32, vp, vp, vp, sz, vp]),
         "kv_append_workspace_size": (sz, []),
         "kv_append": (i32, [vp, vp, vp, i64, i64, i64, i32, vp, i32, i32, i32, i32, vp, vp, vp, i32, i32, vp, vp, i32,
                             i32, vp, vp, sz, vp]),
@@ -633,6 +648,172 @@ def tree_accept_typical(logits_p, node_tok, tree, temperature=1.0, epsilon=0.09,
             int(seed), int(offset), _ptr(accept_len), _ptr(accept_path), _ptr(next_token), _ptr(margin), _ptr(ws),
             ws.numel(), _stream(stream)))
     return accept_len, accept_path, next_token, margin
+
+
+def tree_attention_shared_workspace_size(tree, B, Hq, Hkv, Lshared, Lmax, D, dtype):
+    n = _lib.tree_attention_shared_workspace_size(tree.ref(), B, Hq, Hkv, Lshared, Lmax, D, dtype)
+    if n == 0:
+        raise SpecError("tree_attention_shared_workspace_size", 1, _lib.spec_last_error().decode())
+    return int(n)
+
+
+def tree_attention_scored_workspace_size(tree, B, Hq, Hkv, Lmax, D, dtype):
+    n = _lib.tree_attention_scored_workspace_size(tree.ref(), B, Hq, Hkv, Lmax, D, dtype)
+    if n == 0:
+        raise SpecError("tree_attention_scored_workspace_size", 1, _lib.spec_last_error().decode())
+    return int(n)
+
+
+def _attn_args(q, k_tree, v_tree, prefix_len, tree, Hkv, scale, softcap, window, slopes, out, lse, want_lse, stream):
+    """The checks and outputs the shared and scored attention calls have in common."""
+    _need(q, "q", ndim=4)
+    dev = q.device
+    B, Hq, T, D = q.shape
+    if T != tree.T:
+        raise ValueError(f"q has {T} nodes, the tree {tree.T}")
+    for name, t in (("k_tree", k_tree), ("v_tree", v_tree)):
+        _need(t, name, dtype=q.dtype, ndim=4, device=dev)
+        if tuple(t.shape) != (B, Hkv, T, D):
+            raise ValueError(f"{name} must be {(B, Hkv, T, D)}")
+    _need(prefix_len, "prefix_len", dtype=torch.int32, ndim=1, device=dev)
+    if prefix_len.shape[0] != B:
+        raise ValueError("prefix_len must be [B]")
+    score = None
+    if softcap or window or slopes is not None:
+        if slopes is not None:
+            _need(slopes, "slopes", dtype=torch.float32, ndim=1, device=dev)
+            if slopes.shape[0] != Hq:
+                raise ValueError("slopes must be [Hq]")
+        score = ctypes.byref(spec_score(float(softcap), int(window), 0 if slopes is None else slopes.data_ptr()))
+    if out is None:
+        out = _new(stream, dev, q.dtype, B, Hq, T, D)
+    _need(out, "out", dtype=q.dtype, ndim=4, device=dev)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is None and want_lse:
+        lse = _new(stream, dev, torch.float32, B, Hq, T)
+    if lse is not None:
+        _need(lse, "lse", dtype=torch.float32, ndim=3, device=dev)
+        if tuple(lse.shape) != (B, Hq, T):
+            raise ValueError("lse must be [B, Hq, T]")
+    return dev, B, Hq, D, 0.0 if scale is None else float(scale), score, out, lse
+
+
+def _own_cache(q, k_cache, v_cache):
+    _need(k_cache, "k_cache", dtype=q.dtype, ndim=4, device=q.device)
+    _need(v_cache, "v_cache", dtype=q.dtype, ndim=4, device=q.device)
+    B, D = q.shape[0], q.shape[-1]
+    Hkv, Lmax = k_cache.shape[1], k_cache.shape[2]
+    if tuple(k_cache.shape) != (B, Hkv, Lmax, D) or v_cache.shape != k_cache.shape:
+        raise ValueError("caches must be [B, Hkv, Lmax, D]")
+    return Hkv, Lmax
+
+
+def _own_pages(q, k_pool, v_pool, block_table):
+    _need(k_pool, "k_pool", dtype=q.dtype, ndim=4, device=q.device)
+    _need(v_pool, "v_pool", dtype=q.dtype, ndim=4, device=q.device)
+    num_blocks, Hkv, bs, D = k_pool.shape
+    if D != q.shape[-1] or v_pool.shape != k_pool.shape:
+        raise ValueError("pools must be [num_blocks, Hkv, block_size, D]")
+    _need(block_table, "block_table", dtype=torch.int32, ndim=2, device=q.device)
+    if block_table.shape[0] != q.shape[0]:
+        raise ValueError("block_table must be [B, max_blocks]")
+    return num_blocks, Hkv, bs, block_table.shape[1]
+
+
+def _shared_len(shared_len, dev):
+    _need(shared_len, "shared_len", dtype=torch.int32, device=dev)
+    if shared_len.numel() != 1:
+        raise ValueError("shared_len must hold one value")
+
+
+def _attn_ws(ws, size, args, stream, dev):
+    if ws is None:
+        ws = _new(stream, dev, torch.uint8, size(*args))
+    _need(ws, "ws", device=dev)
+    return ws
+
+
+def tree_attention_shared(q, k_shared, v_shared, shared_len, k_cache, v_cache, prefix_len, k_tree, v_tree, tree, scale=None,
+                          softcap=0.0, window=0, slopes=None, out=None, lse=None, want_lse=True, ws=None, stream=None):
+    """Tree attention behind a prefix the batch shares: returns (out [B,Hq,T,D] in q's type, lse [B,Hq,T] or None).
+
+    k_shared, v_shared [Hkv, Lshared, D] with shared_len [1] int32 keys in use; k_cache, v_cache [B, Hkv, Lmax, D]
+    and prefix_len [B]: each sequence's own keys behind them.  softcap, window, slopes [Hq]: see spec_score."""
+    _need(q, "q", ndim=4)
+    Hkv, Lmax = _own_cache(q, k_cache, v_cache)
+    dev, B, Hq, D, scale, score, out, lse = _attn_args(q, k_tree, v_tree, prefix_len, tree, Hkv, scale, softcap, window,
+                                                       slopes, out, lse, want_lse, stream)
+    _need(k_shared, "k_shared", dtype=q.dtype, ndim=3, device=dev)
+    _need(v_shared, "v_shared", dtype=q.dtype, ndim=3, device=dev)
+    Ls = k_shared.shape[1]
+    if tuple(k_shared.shape) != (Hkv, Ls, D) or v_shared.shape != k_shared.shape:
+        raise ValueError("shared keys and values must be [Hkv, Lshared, D]")
+    _shared_len(shared_len, dev)
+    dt = _dtype_code(q)
+    with torch.cuda.device(dev):
+        ws = _attn_ws(ws, tree_attention_shared_workspace_size, (tree, B, Hq, Hkv, Ls, Lmax, D, dt), stream, dev)
+        _check("tree_attention_shared", _lib.tree_attention_shared(
+            _ptr(q), _ptr(k_shared), _ptr(v_shared), _ptr(shared_len), Ls, _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len),
+            _ptr(k_tree), _ptr(v_tree), tree.ref(), B, Hq, Hkv, Lmax, D, scale, score, dt, _ptr(out), _ptr(lse), _ptr(ws),
+            ws.nbytes, _stream(stream)))
+    return out, lse
+
+
+def tree_attention_shared_paged(q, k_pool, v_pool, shared_table, shared_len, block_table, prefix_len, k_tree, v_tree, tree,
+                                scale=None, softcap=0.0, window=0, slopes=None, out=None, lse=None, want_lse=True, ws=None,
+                                stream=None):
+    """tree_attention_shared over a paged cache: shared_table [shared_blocks] and block_table [B, max_blocks] int32
+    name blocks of the pools [num_blocks, Hkv, block_size, D]."""
+    _need(q, "q", ndim=4)
+    num_blocks, Hkv, bs, max_blocks = _own_pages(q, k_pool, v_pool, block_table)
+    dev, B, Hq, D, scale, score, out, lse = _attn_args(q, k_tree, v_tree, prefix_len, tree, Hkv, scale, softcap, window,
+                                                       slopes, out, lse, want_lse, stream)
+    _need(shared_table, "shared_table", dtype=torch.int32, ndim=1, device=dev)
+    _shared_len(shared_len, dev)
+    n = shared_table.shape[0]
+    dt = _dtype_code(q)
+    with torch.cuda.device(dev):
+        ws = _attn_ws(ws, tree_attention_shared_workspace_size, (tree, B, Hq, Hkv, n * bs, max_blocks * bs, D, dt), stream, dev)
+        _check("tree_attention_shared_paged", _lib.tree_attention_shared_paged(
+            _ptr(q), _ptr(k_pool), _ptr(v_pool), num_blocks, _ptr(shared_table), n, _ptr(shared_len), _ptr(block_table),
+            max_blocks, bs, _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree), tree.ref(), B, Hq, Hkv, D, scale, score, dt,
+            _ptr(out), _ptr(lse), _ptr(ws), ws.nbytes, _stream(stream)))
+    return out, lse
+
+
+def tree_attention_scored(q, k_cache, v_cache, prefix_len, k_tree, v_tree, tree, scale=None, softcap=0.0, window=0,
+                          slopes=None, out=None, lse=None, want_lse=True, ws=None, stream=None):
+    """Tree attention with scores capped by softcap * tanh(x / softcap), biased by -slopes[h] * distance and cut to a
+    window of positions: returns (out [B,Hq,T,D] in q's type, lse [B,Hq,T] or None)."""
+    _need(q, "q", ndim=4)
+    Hkv, Lmax = _own_cache(q, k_cache, v_cache)
+    dev, B, Hq, D, scale, score, out, lse = _attn_args(q, k_tree, v_tree, prefix_len, tree, Hkv, scale, softcap, window,
+                                                       slopes, out, lse, want_lse, stream)
+    dt = _dtype_code(q)
+    with torch.cuda.device(dev):
+        ws = _attn_ws(ws, tree_attention_scored_workspace_size, (tree, B, Hq, Hkv, Lmax, D, dt), stream, dev)
+        _check("tree_attention_scored", _lib.tree_attention_scored(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree), tree.ref(), B, Hq, Hkv,
+            Lmax, D, scale, score, dt, _ptr(out), _ptr(lse), _ptr(ws), ws.nbytes, _stream(stream)))
+    return out, lse
+
+
+def tree_attention_scored_paged(q, k_pool, v_pool, block_table, prefix_len, k_tree, v_tree, tree, scale=None, softcap=0.0,
+                                window=0, slopes=None, out=None, lse=None, want_lse=True, ws=None, stream=None):
+    """tree_attention_scored over a paged cache: pools [num_blocks, Hkv, block_size, D], block_table [B, max_blocks] int32."""
+    _need(q, "q", ndim=4)
+    num_blocks, Hkv, bs, max_blocks = _own_pages(q, k_pool, v_pool, block_table)
+    dev, B, Hq, D, scale, score, out, lse = _attn_args(q, k_tree, v_tree, prefix_len, tree, Hkv, scale, softcap, window,
+                                                       slopes, out, lse, want_lse, stream)
+    dt = _dtype_code(q)
+    with torch.cuda.device(dev):
+        ws = _attn_ws(ws, tree_attention_scored_workspace_size, (tree, B, Hq, Hkv, max_blocks * bs, D, dt), stream, dev)
+        _check("tree_attention_scored_paged", _lib.tree_attention_scored_paged(
+            _ptr(q), _ptr(k_pool), _ptr(v_pool), num_blocks, _ptr(block_table), max_blocks, bs, _ptr(prefix_len),
+            _ptr(k_tree), _ptr(v_tree), tree.ref(), B, Hq, Hkv, D, scale, score, dt, _ptr(out), _ptr(lse), _ptr(ws),
+            ws.nbytes, _stream(stream)))
+    return out, lse
 
 
 def _new(stream, device, dtype, *shape):

@@ -1,0 +1,511 @@
+// tree_attention_shared, tree_attention_scored and their paged forms: tree
+// attention over a prefix that the whole batch shares, and with capped, biased
+// and windowed scores.
+//
+// For query head h, sequence b, node i (position P = Ls + L_b + depth[i]) and a
+// key at position p that the node sees (every shared and cached key, and of the
+// tree its ancestors and itself; with a window only p > P - window):
+//     x = scale q.k;   x = cap tanh(x / cap);   x = x - slope[h] (P - p)
+//     out = sum exp(x) v / sum exp(x),   lse = log sum exp(x)
+// The sums run in one pass over the keys with a running maximum, in base 2 and
+// in 32 bits; splits of the keys and the shared part are joined by their
+// (max, sum, O).  See attention_shared.cuh for how the work is cut.
+//
+// This file: the CUDA-core items (fp32), the join, the host side.  bf16 items
+// are in attention_shared_tc.cu.
+#include <algorithm>
+#include <cmath>
+
+#include "attention_shared.cuh"
+
+namespace spec {
+namespace shr {
+
+// ---------------------------------------------------------------- CUDA-core items
+
+constexpr int FR = 64;   // rows of a block
+constexpr int FK = 64;   // keys of a tile
+
+// 256 threads; thread (rg, kg) = (t / 16, t % 16) holds rows 4 rg .. 4 rg + 3, keys
+// kg + 16 j of a tile and output columns 4 kg .. of each 64.  fp32 operands have no
+// tensor-core product of their own precision, so the FMA units bound this kernel:
+// 16 FMAs per 8 shared-memory loads in the score loop.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
+    constexpr int LD = D + 4, LP = FK + 4, DT = D / 16;
+    extern __shared__ float4 smem4[];
+    float* Qs = reinterpret_cast<float*>(smem4);
+    float* Ks = Qs + FR * LD;
+    float* Vs = Ks + FK * LD;
+    float* Ps = Vs + FK * LD;
+    const int t = threadIdx.x, rg = t >> 4, kg = t & 15;
+    const Plan plan = make_plan(p);
+    if (blockIdx.x == 0 && t < 32) publish_plan(p, plan);
+    const T* q = static_cast<const T*>(p.q);
+    const float scale2 = p.scale * kLog2e, cap2 = p.softcap * kLog2e, incap = p.softcap > 0.f ? p.scale / p.softcap : 0.f;
+
+    for (int id = blockIdx.x; id < plan.items; id += gridDim.x) {
+        const Item it = find_item(p, plan, id);
+        __syncthreads();   // the last item's Q and P are read
+        for (int idx = t; idx < FR * (D / 4); idx += 256) {
+            const int r = idx / (D / 4), c4 = idx % (D / 4);
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            if (r < it.rows) load4(q + row_of_q(p, it, r) * D + c4 * 4, v);
+            *reinterpret_cast<float4*>(&Qs[r * LD + c4 * 4]) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        int node[4], pos[4];
+        float slope2[4], m_run[4], l_run[4], o[4][DT];
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+            const int r = min(4 * rg + ii, it.rows - 1);
+            const int b = it.b + (p.gT < p.RB ? r / p.gT : 0);
+            const int i = p.gT < p.RB ? r % p.gT : it.rb * p.RB + r;
+            node[ii] = i % p.T;
+            pos[ii] = plan.Ls + own_len(p, b) + p.depth[node[ii]];
+            slope2[ii] = p.slopes ? p.slopes[it.kvh * p.g + i / p.T] * kLog2e : 0.f;
+            m_run[ii] = -INFINITY;
+            l_run[ii] = 0.f;
+#pragma unroll
+            for (int e = 0; e < DT; ++e) o[ii][e] = 0.f;
+        }
+        const int first = it.shared ? plan.sT0 : own_first(p, it.L);
+        const int n_pre = it.shared ? plan.nS : own_tiles(p, it.L) - ceil_div(p.T, FK);
+        for (int tile = it.t0; tile < it.t1; ++tile) {
+            const bool tree = !it.shared && tile >= n_pre;
+            const int j0 = (tree ? tile - n_pre : first + tile) * FK;
+            const int j_end = tree ? p.T : it.shared ? plan.Ls : it.L;
+            __syncthreads();
+            for (int idx = t; idx < FK * (D / 4); idx += 256) {
+                const int jl = idx / (D / 4), c4 = idx % (D / 4);
+                const int j = j0 + jl;
+                float kv[4] = {0.f, 0.f, 0.f, 0.f}, vv[4] = {0.f, 0.f, 0.f, 0.f};
+                if (j < j_end) {
+                    const T *ksrc, *vsrc;
+                    size_t row;
+                    bool ok = true;
+                    if (tree) {
+                        ksrc = static_cast<const T*>(p.kt);
+                        vsrc = static_cast<const T*>(p.vt);
+                        row = (static_cast<size_t>(it.b) * p.Hkv + it.kvh) * p.T + j;
+                    } else if (p.pg.table) {   // the key's pool block and row
+                        const int blk = it.shared ? p.shared_table[j / p.pg.bs]
+                                                  : p.pg.table[static_cast<size_t>(it.b) * p.pg.max_blocks + j / p.pg.bs];
+                        ok = blk >= 0 && blk < p.pg.num_blocks;
+                        ksrc = static_cast<const T*>(p.kc);
+                        vsrc = static_cast<const T*>(p.vc);
+                        row = (static_cast<size_t>(ok ? blk : 0) * p.Hkv + it.kvh) * p.pg.bs + j % p.pg.bs;
+                    } else if (it.shared) {
+                        ksrc = static_cast<const T*>(p.ks);
+                        vsrc = static_cast<const T*>(p.vs);
+                        row = static_cast<size_t>(it.kvh) * p.Lshared + j;
+                    } else {
+                        ksrc = static_cast<const T*>(p.kc);
+                        vsrc = static_cast<const T*>(p.vc);
+                        row = (static_cast<size_t>(it.b) * p.Hkv + it.kvh) * p.Lmax + j;
+                    }
+                    if (ok) {
+                        load4(ksrc + row * D + c4 * 4, kv);
+                        load4(vsrc + row * D + c4 * 4, vv);
+                    } else {
+                        flag_status(p.ws, SPEC_EINVAL);   // the key reads as zeros
+                    }
+                }
+                *reinterpret_cast<float4*>(&Ks[jl * LD + c4 * 4]) = make_float4(kv[0], kv[1], kv[2], kv[3]);
+                *reinterpret_cast<float4*>(&Vs[jl * LD + c4 * 4]) = make_float4(vv[0], vv[1], vv[2], vv[3]);
+            }
+            __syncthreads();
+
+            float s[4][4];
+#pragma unroll
+            for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) s[ii][jj] = 0.f;
+#pragma unroll 4
+            for (int dd = 0; dd < D; dd += 4) {
+                float4 qa[4], kb[4];
+#pragma unroll
+                for (int ii = 0; ii < 4; ++ii) qa[ii] = *reinterpret_cast<const float4*>(&Qs[(4 * rg + ii) * LD + dd]);
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) kb[jj] = *reinterpret_cast<const float4*>(&Ks[(kg + 16 * jj) * LD + dd]);
+#pragma unroll
+                for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj)
+                        s[ii][jj] += qa[ii].x * kb[jj].x + qa[ii].y * kb[jj].y + qa[ii].z * kb[jj].z + qa[ii].w * kb[jj].w;
+            }
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                const int j = j0 + kg + 16 * jj;
+                const bool in = j < j_end;
+                const int kpos = tree ? (in ? plan.Ls + it.L + p.depth[j] : 0) : it.shared ? j : plan.Ls + j;
+#pragma unroll
+                for (int ii = 0; ii < 4; ++ii) {
+                    const int far = pos[ii] - kpos;
+                    bool ok = in && (p.window <= 0 || far < p.window);
+                    if (tree && ok) ok = (p.anc[static_cast<size_t>(node[ii]) * p.words + (j >> 6)] >> (j & 63)) & 1ull;
+                    float x = p.softcap > 0.f ? cap2 * tanhf(s[ii][jj] * incap) : s[ii][jj] * scale2;
+                    x -= slope2[ii] * static_cast<float>(far);
+                    s[ii][jj] = ok ? x : -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int ii = 0; ii < 4; ++ii) {
+                float mt = fmaxf(fmaxf(s[ii][0], s[ii][1]), fmaxf(s[ii][2], s[ii][3]));
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+                const float m_new = fmaxf(m_run[ii], mt);
+                const float ref = m_new == -INFINITY ? 0.f : m_new;   // nothing seen so far
+                const float alpha = exp2f(m_run[ii] - ref);
+                float pr[4], lt = 0.f;
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) { pr[jj] = exp2f(s[ii][jj] - ref); lt += pr[jj]; }
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, off);
+                l_run[ii] = l_run[ii] * alpha + lt;
+                m_run[ii] = m_new;
+#pragma unroll
+                for (int e = 0; e < DT; ++e) o[ii][e] *= alpha;
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) Ps[(4 * rg + ii) * LP + kg + 16 * jj] = pr[jj];
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int j = 0; j < FK; ++j) {
+                float pj[4];
+#pragma unroll
+                for (int ii = 0; ii < 4; ++ii) pj[ii] = Ps[(4 * rg + ii) * LP + j];
+#pragma unroll
+                for (int h = 0; h < DT / 4; ++h) {
+                    const float4 v = *reinterpret_cast<const float4*>(&Vs[j * LD + h * 64 + kg * 4]);
+#pragma unroll
+                    for (int ii = 0; ii < 4; ++ii) {
+                        o[ii][h * 4 + 0] += pj[ii] * v.x;
+                        o[ii][h * 4 + 1] += pj[ii] * v.y;
+                        o[ii][h * 4 + 2] += pj[ii] * v.z;
+                        o[ii][h * 4 + 3] += pj[ii] * v.w;
+                    }
+                }
+            }
+        }
+        const int stride = it.shared ? p.rowsS : p.rowsO;
+        float4* part = (it.shared ? p.part_s : p.part_o) + static_cast<size_t>(it.index) * (D / 4 + 1) * stride;
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+            const int r = 4 * rg + ii;
+            if (r >= it.rows) continue;
+            if (it.direct) {
+                const size_t row = row_of_q(p, it, r);
+                const float inv = 1.f / l_run[ii];
+#pragma unroll
+                for (int h = 0; h < DT / 4; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        static_cast<T*>(p.out)[row * D + h * 64 + kg * 4 + e] = from_f32<T>(o[ii][h * 4 + e] * inv);
+                if (p.lse && kg == 0) p.lse[row] = (m_run[ii] + log2f(l_run[ii])) * kLn2;
+            } else {
+                if (kg == 0) part[r] = make_float4(m_run[ii], l_run[ii], 0.f, 0.f);
+#pragma unroll
+                for (int h = 0; h < DT / 4; ++h)
+                    part[static_cast<size_t>(1 + h * 16 + kg) * stride + r] =
+                        make_float4(o[ii][h * 4 + 0], o[ii][h * 4 + 1], o[ii][h * 4 + 2], o[ii][h * 4 + 3]);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- the join
+
+// One CTA of four warps per (sequence, KV head, 32 rows of its gT): lane = row, each warp a
+// quarter of the columns, so the partials are read as whole 512-byte lines; the output goes
+// through shared memory to leave as whole rows.  Bound by reading the partials once.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) k_attn_shared_join(const Params p, int n_rg) {
+    constexpr int C = D / 4 / 4;   // float4 columns per warp
+    __shared__ T tile[32][D + 16 / sizeof(T)];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r0 = blockIdx.x % n_rg * 32, col = blockIdx.x / n_rg;
+    const int kvh = col % p.Hkv, b = col / p.Hkv;
+    const int i = r0 + lane;                      // row within gT
+    griddep_wait();
+    const Plan t = *reinterpret_cast<const Plan*>(static_cast<unsigned char*>(p.ws) + kPlanOffset);
+    const int first = p.cum[b], nsO = p.cum[b + 1] - first;
+    if (t.nsS + nsO == 1) return;                 // written by its item
+    const int rb = r0 / p.RB;                     // 32 divides RB
+    const int sb = p.gT >= p.RB ? b * p.n_rbO + rb : b / p.nbb;
+    const int rS = p.gT >= p.RB ? i % p.RB : (b % p.nbb) * p.gT + i;
+    const int rO = i % p.RB;
+    const bool in = i < p.gT;
+    const size_t strideS = static_cast<size_t>(D / 4 + 1) * p.rowsS, strideO = static_cast<size_t>(D / 4 + 1) * p.rowsO;
+    const float4* ps = p.part_s + static_cast<size_t>((kvh * p.n_rbS + sb) * t.nsS) * strideS + rS;
+    const float4* po = p.part_o + static_cast<size_t>(first * p.Hkv * p.n_rbO + (kvh * p.n_rbO + rb) * nsO) * strideO + rO;
+    float M = -INFINITY;
+    if (in) {
+        for (int k = 0; k < t.nsS; ++k) M = fmaxf(M, ps[k * strideS].x);
+        for (int k = 0; k < nsO; ++k) M = fmaxf(M, po[k * strideO].x);
+    }
+    const float ref = M == -INFINITY ? 0.f : M;
+    float l = 0.f;
+    float4 acc[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4* base, int rows) {
+        const float4 h = base[0];
+        const float w = exp2f(h.x - ref);
+        // a split in which the row saw nothing (one of NaN scores alone has a NaN sum, and counts)
+        if (h.x == -INFINITY && h.y == 0.f) return;
+        l += w * h.y;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float4 v = base[static_cast<size_t>(1 + warp * C + c) * rows];
+            acc[c].x += w * v.x; acc[c].y += w * v.y; acc[c].z += w * v.z; acc[c].w += w * v.w;
+        }
+    };
+    if (in) {
+        for (int k = 0; k < t.nsS; ++k) add(ps + k * strideS, p.rowsS);
+        for (int k = 0; k < nsO; ++k) add(po + k * strideO, p.rowsO);
+    }
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        T* d = &tile[lane][(warp * C + c) * 4];
+        d[0] = from_f32<T>(acc[c].x * inv); d[1] = from_f32<T>(acc[c].y * inv);
+        d[2] = from_f32<T>(acc[c].z * inv); d[3] = from_f32<T>(acc[c].w * inv);
+    }
+    const size_t row0 = (static_cast<size_t>(b) * p.Hq + kvh * p.g) * p.T + r0;
+    if (in && warp == 0 && p.lse) p.lse[row0 + lane] = (M + log2f(l)) * kLn2;
+    __syncthreads();
+    constexpr int E = 16 / sizeof(T);
+    for (int x = threadIdx.x; x < 32 * (D / E); x += 128) {
+        const int r = x / (D / E), c = x % (D / E);
+        if (r0 + r < p.gT)
+            *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (row0 + r) * D + c * E) =
+                *reinterpret_cast<const uint4*>(&tile[r][c * E]);
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+HostPlan host_plan(Params& p, bool tc, bool shared, int ctas) {
+    HostPlan h{};
+    h.tc = tc;
+    p.g = p.Hq / p.Hkv;
+    p.gT = p.g * p.T;
+    p.RB = tc ? 128 : FR;
+    p.KT = tc ? 128 : FK;
+    p.nbb = p.gT >= p.RB ? 1 : p.RB / p.gT;
+    p.n_rbO = (p.gT + p.RB - 1) / p.RB;
+    p.n_rbS = p.gT >= p.RB ? p.B * p.n_rbO : (p.B + p.nbb - 1) / p.nbb;
+    p.rowsO = std::min(p.gT, p.RB);
+    p.rowsS = p.nbb * p.rowsO;
+    p.ctas = ctas;
+    p.max_extra = 4 * ctas;
+    p.fixed = 2.5f;
+    const size_t per_row = sizeof(float) * (p.D + 4);
+    const size_t items_s = shared ? static_cast<size_t>(p.Hkv) * p.n_rbS + p.max_extra : 0;
+    const size_t items_o = static_cast<size_t>(p.B) * p.Hkv * p.n_rbO + p.max_extra;
+    h.cum_off = kWsHeader;
+    h.part_s_off = h.cum_off + round_up(sizeof(int32_t) * (static_cast<size_t>(p.B) + 1), 256);
+    h.part_o_off = h.part_s_off + round_up(items_s * p.rowsS * per_row, 256);
+    h.total = h.part_o_off + round_up(items_o * p.rowsO * per_row, 256);
+    return h;
+}
+
+static spec_status check_shapes(const spec_tree* t, int B, int Hq, int Hkv, int Ls, int Lmax, int D, spec_dtype dt) {
+    spec_status st = check_tree(t);
+    if (st != SPEC_OK) return st;
+    if (dt != SPEC_F32 && dt != SPEC_BF16) return fail(SPEC_EINVAL, "dtype %d unknown", static_cast<int>(dt));
+    if (B < 1 || B > 65535) return fail(SPEC_EINVAL, "B = %d out of 1..65535", B);
+    if (Hkv < 1 || Hq < Hkv || Hq % Hkv || Hq > 1024) return fail(SPEC_EINVAL, "Hq = %d must be a multiple of Hkv = %d, at most 1024", Hq, Hkv);
+    if (D != 64 && D != 128) return fail(SPEC_EUNSUPPORTED, "D = %d: only 64 and 128 are built", D);
+    if (Lmax < 1 || Lmax > (1 << 22)) return fail(SPEC_EINVAL, "Lmax = %d out of 1..2^22", Lmax);
+    if (Ls < 0 || Ls > (1 << 22)) return fail(SPEC_EINVAL, "the shared capacity %d is out of 1..2^22", Ls);
+    const int64_t rows = static_cast<int64_t>(B) * Hq * t->T;
+    if (rows > (1ll << 30)) return fail(SPEC_EINVAL, "B * Hq * T = %lld query rows exceed 2^30", static_cast<long long>(rows));
+    return SPEC_OK;
+}
+
+static Params shapes(const spec_tree* t, int B, int Hq, int Hkv, int Ls, int Lmax, int D) {
+    Params p{};
+    p.B = B; p.T = t->T; p.Hq = Hq; p.Hkv = Hkv; p.D = D; p.words = t->words;
+    p.Lshared = Ls; p.Lmax = Lmax;
+    return p;
+}
+
+static size_t workspace(const spec_tree* t, int B, int Hq, int Hkv, int Ls, int Lmax, int D, spec_dtype dt) {
+    if (check_shapes(t, B, Hq, Hkv, Ls, Lmax, D, dt) != SPEC_OK) return 0;
+    Params p = shapes(t, B, Hq, Hkv, Ls, Lmax, D);
+    return host_plan(p, dt == SPEC_BF16 && attn_shared_tc_supported(D), Ls > 0, device_sm_count()).total;
+}
+
+template <typename T, int D>
+static spec_status run_fma(const Params& p, cudaStream_t s) {
+    const size_t smem = sizeof(float) * (FR * (D + 4) + 2 * FK * (D + 4) + FR * (FK + 4));
+    SPEC_CUDA_TRY(cudaFuncSetAttribute(k_attn_shared_fma<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+    SPEC_CUDA_TRY(launch("attn_shared_fma", k_attn_shared_fma<T, D>, dim3(p.ctas), dim3(256), smem, s, p));
+    return SPEC_OK;
+}
+
+template <typename T>
+static spec_status join(const Params& p, cudaStream_t s) {
+    const int n_rg = (p.gT + 31) / 32;
+    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.Hkv * n_rg));
+    SPEC_CUDA_TRY(launch_ex("attn_shared_join", p.D == 64 ? k_attn_shared_join<T, 64> : k_attn_shared_join<T, 128>, grid,
+                            dim3(128), 0, s, true, p, n_rg));
+    return SPEC_OK;
+}
+
+// Every entry point: sizes and pointers in p, with p.shared_len set when there is a shared prefix.
+static spec_status run(Params p, const spec_tree* tree, spec_dtype dt, float scale, const spec_score* score, size_t ws_bytes,
+                       cudaStream_t s) {
+    const bool shared = p.shared_len != nullptr;
+    spec_status st = check_shapes(tree, p.B, p.Hq, p.Hkv, p.Lshared, p.Lmax, p.D, dt);
+    if (st != SPEC_OK) return st;
+    if (!p.pg.table && (static_cast<int64_t>(p.B) * p.Hkv * p.Lmax > INT32_MAX || static_cast<int64_t>(p.Hkv) * p.Lshared > INT32_MAX))
+        return fail(SPEC_EINVAL, "a cache of B * Hkv * Lmax (or Hkv * Lshared) >= 2^31 rows");
+    if (!p.q || !p.kc || !p.vc || !p.prefix_len || !p.kt || !p.vt || !p.out)
+        return fail(SPEC_EINVAL, "q, the cache, prefix_len, tree K/V and out must not be NULL");
+    if (scale == 0.f) scale = 1.f / sqrtf(static_cast<float>(p.D));   // the usual 1/sqrt(D)
+    if (!(scale > 0.f) || !(scale < 1e30f)) return fail(SPEC_EINVAL, "scale must be positive and finite, or 0");
+    p.scale = scale;
+    if (score) {
+        if (!(score->softcap >= 0.f) || !(score->softcap < 1e30f)) return fail(SPEC_EINVAL, "softcap must be positive and finite, or 0");
+        if (score->softcap > 0.f && score->softcap < 1e-6f) return fail(SPEC_EINVAL, "softcap = %g is below 1e-6", score->softcap);
+        if (score->window < 0) return fail(SPEC_EINVAL, "window = %d must be positive, or 0", score->window);
+        p.softcap = score->softcap;
+        p.window = score->window;
+        p.slopes = score->slopes;
+    }
+    if (!aligned16(p.q) || !aligned16(p.kc) || !aligned16(p.vc) || !aligned16(p.ks) || !aligned16(p.vs) || !aligned16(p.kt) ||
+        !aligned16(p.vt) || !aligned16(p.out))
+        return fail(SPEC_EALIGN, "tensors must be 16-byte aligned");
+    if (!aligned4(p.prefix_len) || !aligned4(p.shared_len) || !aligned4(p.slopes) || !aligned4(p.lse) ||
+        !aligned4(p.pg.table) || !aligned4(p.shared_table))
+        return fail(SPEC_EALIGN, "lengths, tables, slopes and lse must be 4-byte aligned");
+    p.depth = tree->depth;
+    p.anc = tree->anc;
+    const HostPlan h = host_plan(p, dt == SPEC_BF16 && attn_shared_tc_supported(p.D), shared, device_sm_count());
+    if (!p.ws || ws_bytes < h.total) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, h.total);
+    if (!aligned16(p.ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
+    unsigned char* base = static_cast<unsigned char*>(p.ws);
+    p.cum = reinterpret_cast<int32_t*>(base + h.cum_off);
+    p.part_s = reinterpret_cast<float4*>(base + h.part_s_off);
+    p.part_o = reinterpret_cast<float4*>(base + h.part_o_off);
+    SPEC_CUDA_TRY(reset_device_status(p.ws, s));
+    if (h.tc) {
+        st = attn_shared_tc_run(p, p.ctas, s);
+    } else if (dt == SPEC_BF16) {
+        using T = __nv_bfloat16;
+        st = p.D == 64 ? run_fma<T, 64>(p, s) : run_fma<T, 128>(p, s);
+    } else {
+        st = p.D == 64 ? run_fma<float, 64>(p, s) : run_fma<float, 128>(p, s);
+    }
+    if (st != SPEC_OK) return st;
+    return dt == SPEC_BF16 ? join<__nv_bfloat16>(p, s) : join<float>(p, s);
+}
+
+static spec_status check_pool(int num_blocks, const int32_t* table, int max_blocks, int bs, int Hkv) {
+    if (bs < 16 || bs % 16 != 0) return fail(SPEC_EINVAL, "block_size = %d: a positive multiple of 16", bs);
+    if (num_blocks < 1 || max_blocks < 1) return fail(SPEC_EINVAL, "num_blocks = %d, max_blocks = %d must be positive", num_blocks, max_blocks);
+    if (static_cast<int64_t>(max_blocks) * bs > (1 << 22))
+        return fail(SPEC_EINVAL, "max_blocks * block_size = %lld > 2^22", static_cast<long long>(max_blocks) * bs);
+    if (static_cast<int64_t>(num_blocks) * std::max(Hkv, 1) * bs > INT32_MAX)
+        return fail(SPEC_EINVAL, "pool of %d blocks too large (num_blocks * Hkv * block_size rows >= 2^31)", num_blocks);
+    if (!table) return fail(SPEC_EINVAL, "a block table must not be NULL");
+    return SPEC_OK;
+}
+
+}  // namespace shr
+}  // namespace spec
+
+using namespace spec;
+
+extern "C" size_t tree_attention_shared_workspace_size(const spec_tree* tree, int32_t B, int32_t Hq, int32_t Hkv,
+                                                       int32_t Lshared, int32_t Lmax, int32_t D, spec_dtype dt) {
+    clear_error();
+    if (Lshared < 1) {
+        fail(SPEC_EINVAL, "Lshared = %d must be positive", Lshared);
+        return 0;
+    }
+    return shr::workspace(tree, B, Hq, Hkv, Lshared, Lmax, D, dt);
+}
+
+extern "C" size_t tree_attention_scored_workspace_size(const spec_tree* tree, int32_t B, int32_t Hq, int32_t Hkv,
+                                                       int32_t Lmax, int32_t D, spec_dtype dt) {
+    clear_error();
+    return shr::workspace(tree, B, Hq, Hkv, 0, Lmax, D, dt);
+}
+
+extern "C" spec_status tree_attention_shared(const void* q, const void* k_shared, const void* v_shared,
+                                             const int32_t* shared_len, int32_t Lshared, const void* k_cache,
+                                             const void* v_cache, const int32_t* prefix_len, const void* k_tree,
+                                             const void* v_tree, const spec_tree* tree, int32_t B, int32_t Hq, int32_t Hkv,
+                                             int32_t Lmax, int32_t D, float scale, const spec_score* score, spec_dtype dt,
+                                             void* out, float* lse, void* ws, size_t ws_bytes, spec_stream_t s) {
+    clear_error();
+    spec_status st = check_tree(tree);
+    if (st != SPEC_OK) return st;
+    if (!k_shared || !v_shared || !shared_len) return fail(SPEC_EINVAL, "the shared keys, values and length must not be NULL");
+    if (Lshared < 1) return fail(SPEC_EINVAL, "Lshared = %d must be positive", Lshared);
+    shr::Params p = shr::shapes(tree, B, Hq, Hkv, Lshared, Lmax, D);
+    p.q = q; p.ks = k_shared; p.vs = v_shared; p.kc = k_cache; p.vc = v_cache; p.kt = k_tree; p.vt = v_tree;
+    p.shared_len = shared_len; p.prefix_len = prefix_len;
+    p.out = out; p.lse = lse; p.ws = ws;
+    return shr::run(p, tree, dt, scale, score, ws_bytes, reinterpret_cast<cudaStream_t>(s));
+}
+
+extern "C" spec_status tree_attention_shared_paged(const void* q, const void* k_pool, const void* v_pool, int32_t num_blocks,
+                                                   const int32_t* shared_table, int32_t shared_blocks,
+                                                   const int32_t* shared_len, const int32_t* block_table,
+                                                   int32_t max_blocks, int32_t block_size, const int32_t* prefix_len,
+                                                   const void* k_tree, const void* v_tree, const spec_tree* tree, int32_t B,
+                                                   int32_t Hq, int32_t Hkv, int32_t D, float scale, const spec_score* score,
+                                                   spec_dtype dt, void* out, float* lse, void* ws, size_t ws_bytes,
+                                                   spec_stream_t s) {
+    clear_error();
+    spec_status st = check_tree(tree);
+    if (st != SPEC_OK) return st;
+    st = shr::check_pool(num_blocks, block_table, max_blocks, block_size, Hkv);
+    if (st != SPEC_OK) return st;
+    st = shr::check_pool(num_blocks, shared_table, shared_blocks, block_size, Hkv);
+    if (st != SPEC_OK) return st;
+    if (!shared_len) return fail(SPEC_EINVAL, "shared_len must not be NULL");
+    shr::Params p = shr::shapes(tree, B, Hq, Hkv, shared_blocks * block_size, max_blocks * block_size, D);
+    p.q = q; p.kc = k_pool; p.vc = v_pool; p.kt = k_tree; p.vt = v_tree;
+    p.pg.table = block_table; p.pg.max_blocks = max_blocks; p.pg.bs = block_size; p.pg.num_blocks = num_blocks;
+    p.shared_table = shared_table;
+    p.shared_len = shared_len; p.prefix_len = prefix_len;
+    p.out = out; p.lse = lse; p.ws = ws;
+    return shr::run(p, tree, dt, scale, score, ws_bytes, reinterpret_cast<cudaStream_t>(s));
+}
+
+extern "C" spec_status tree_attention_scored(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* prefix_len, const void* k_tree, const void* v_tree,
+                                             const spec_tree* tree, int32_t B, int32_t Hq, int32_t Hkv, int32_t Lmax,
+                                             int32_t D, float scale, const spec_score* score, spec_dtype dt, void* out,
+                                             float* lse, void* ws, size_t ws_bytes, spec_stream_t s) {
+    clear_error();
+    spec_status st = check_tree(tree);
+    if (st != SPEC_OK) return st;
+    shr::Params p = shr::shapes(tree, B, Hq, Hkv, 0, Lmax, D);
+    p.q = q; p.kc = k_cache; p.vc = v_cache; p.kt = k_tree; p.vt = v_tree; p.prefix_len = prefix_len;
+    p.out = out; p.lse = lse; p.ws = ws;
+    return shr::run(p, tree, dt, scale, score, ws_bytes, reinterpret_cast<cudaStream_t>(s));
+}
+
+extern "C" spec_status tree_attention_scored_paged(const void* q, const void* k_pool, const void* v_pool, int32_t num_blocks,
+                                                   const int32_t* block_table, int32_t max_blocks, int32_t block_size,
+                                                   const int32_t* prefix_len, const void* k_tree, const void* v_tree,
+                                                   const spec_tree* tree, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                                   float scale, const spec_score* score, spec_dtype dt, void* out,
+                                                   float* lse, void* ws, size_t ws_bytes, spec_stream_t s) {
+    clear_error();
+    spec_status st = check_tree(tree);
+    if (st != SPEC_OK) return st;
+    st = shr::check_pool(num_blocks, block_table, max_blocks, block_size, Hkv);
+    if (st != SPEC_OK) return st;
+    shr::Params p = shr::shapes(tree, B, Hq, Hkv, 0, max_blocks * block_size, D);
+    p.q = q; p.kc = k_pool; p.vc = v_pool; p.kt = k_tree; p.vt = v_tree; p.prefix_len = prefix_len;
+    p.pg.table = block_table; p.pg.max_blocks = max_blocks; p.pg.bs = block_size; p.pg.num_blocks = num_blocks;
+    p.out = out; p.lse = lse; p.ws = ws;
+    return shr::run(p, tree, dt, scale, score, ws_bytes, reinterpret_cast<cudaStream_t>(s));
+}
