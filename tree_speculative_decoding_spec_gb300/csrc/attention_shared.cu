@@ -30,8 +30,9 @@ constexpr int FK = 64;   // keys of a tile
 // kg + 16 j of a tile and output columns 4 kg .. of each 64.  fp32 operands have no
 // tensor-core product of their own precision, so the FMA units bound this kernel:
 // 16 FMAs per 8 shared-memory loads in the score loop.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
+    using T = float;
     constexpr int LD = D + 4, LP = FK + 4, DT = D / 16;
     extern __shared__ float4 smem4[];
     float* Qs = reinterpret_cast<float*>(smem4);
@@ -292,7 +293,7 @@ HostPlan host_plan(Params& p, bool tc, bool shared, int ctas) {
     p.gT = p.g * p.T;
     p.RB = tc ? 128 : FR;
     p.KT = tc ? 128 : FK;
-    p.nbb = p.gT >= p.RB ? 1 : p.RB / p.gT;
+    p.nbb = p.gT >= p.RB ? 1 : std::min(p.RB / p.gT, p.B);
     p.n_rbO = (p.gT + p.RB - 1) / p.RB;
     p.n_rbS = p.gT >= p.RB ? p.B * p.n_rbO : (p.B + p.nbb - 1) / p.nbb;
     p.rowsO = std::min(p.gT, p.RB);
@@ -334,14 +335,14 @@ static Params shapes(const spec_tree* t, int B, int Hq, int Hkv, int Ls, int Lma
 static size_t workspace(const spec_tree* t, int B, int Hq, int Hkv, int Ls, int Lmax, int D, spec_dtype dt) {
     if (check_shapes(t, B, Hq, Hkv, Ls, Lmax, D, dt) != SPEC_OK) return 0;
     Params p = shapes(t, B, Hq, Hkv, Ls, Lmax, D);
-    return host_plan(p, dt == SPEC_BF16 && attn_shared_tc_supported(D), Ls > 0, device_sm_count()).total;
+    return host_plan(p, dt == SPEC_BF16, Ls > 0, device_sm_count()).total;
 }
 
-template <typename T, int D>
+template <int D>
 static spec_status run_fma(const Params& p, cudaStream_t s) {
     const size_t smem = sizeof(float) * (FR * (D + 4) + 2 * FK * (D + 4) + FR * (FK + 4));
-    SPEC_CUDA_TRY(cudaFuncSetAttribute(k_attn_shared_fma<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-    SPEC_CUDA_TRY(launch("attn_shared_fma", k_attn_shared_fma<T, D>, dim3(p.ctas), dim3(256), smem, s, p));
+    SPEC_CUDA_TRY(cudaFuncSetAttribute(k_attn_shared_fma<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+    SPEC_CUDA_TRY(launch("attn_shared_fma", k_attn_shared_fma<D>, dim3(p.ctas), dim3(256), smem, s, p));
     return SPEC_OK;
 }
 
@@ -383,7 +384,7 @@ static spec_status run(Params p, const spec_tree* tree, spec_dtype dt, float sca
         return fail(SPEC_EALIGN, "lengths, tables, slopes and lse must be 4-byte aligned");
     p.depth = tree->depth;
     p.anc = tree->anc;
-    const HostPlan h = host_plan(p, dt == SPEC_BF16 && attn_shared_tc_supported(p.D), shared, device_sm_count());
+    const HostPlan h = host_plan(p, dt == SPEC_BF16, shared, device_sm_count());
     if (!p.ws || ws_bytes < h.total) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, h.total);
     if (!aligned16(p.ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
     unsigned char* base = static_cast<unsigned char*>(p.ws);
@@ -393,11 +394,8 @@ static spec_status run(Params p, const spec_tree* tree, spec_dtype dt, float sca
     SPEC_CUDA_TRY(reset_device_status(p.ws, s));
     if (h.tc) {
         st = attn_shared_tc_run(p, p.ctas, s);
-    } else if (dt == SPEC_BF16) {
-        using T = __nv_bfloat16;
-        st = p.D == 64 ? run_fma<T, 64>(p, s) : run_fma<T, 128>(p, s);
     } else {
-        st = p.D == 64 ? run_fma<float, 64>(p, s) : run_fma<float, 128>(p, s);
+        st = p.D == 64 ? run_fma<64>(p, s) : run_fma<128>(p, s);
     }
     if (st != SPEC_OK) return st;
     return dt == SPEC_BF16 ? join<__nv_bfloat16>(p, s) : join<float>(p, s);

@@ -227,7 +227,6 @@ struct HostPlan {
 HostPlan host_plan(Params& p, bool tc, bool shared, int ctas);
 
 // The tensor-core items (bf16, D 64 or 128).
-bool attn_shared_tc_supported(int D);
 spec_status attn_shared_tc_run(const Params& p, int blocks, cudaStream_t s);
 
 }  // namespace shr

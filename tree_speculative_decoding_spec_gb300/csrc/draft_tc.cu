@@ -402,6 +402,21 @@ cudaError_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows,
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t n3, uint64_t n2, uint64_t n1, uint64_t cols,
+                              uint32_t b3, uint32_t b1) {
+    auto fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[4] = {cols, n1, n2, n3};
+    const cuuint64_t strides[3] = {cols * 2, n1 * cols * 2, n2 * n1 * cols * 2};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(kBK), b1, 1, b3};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // The merge kernel keeps one list head per 128-token slice, at most 1024 slices.
 bool draft_tc_supported(int d, int V) {
     return d >= 8 && d % 8 == 0 && V >= 1 && (V + kBM - 1) / kBM <= 1024 && encode_fn() != nullptr;

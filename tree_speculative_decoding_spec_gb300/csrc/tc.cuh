@@ -87,6 +87,14 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// 4-D tiled load of the box at (x, y1, y2, y3), innermost first; the rules of tma_load_2d.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y1, int y2, int y3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y1), "r"(y2), "r"(y3)
+        : "memory");
+}
+
 // Bring a 2-D tensor-map box into L2 ahead of its load (no shared memory, no barrier;
 // the same coordinate rules as a load).
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
@@ -306,6 +314,40 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parit
     }
 }
 
+// ---------------------------------------------------------------- softmax arithmetic
+
+// Packed two-lane fp32 arithmetic (sm_100 family): one instruction for a pair of
+// scores halves the softmax's FFMA and FADD count, and the 3-input max does the
+// same for the row maximum.
+__device__ __forceinline__ unsigned long long pk2(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void upk2(unsigned long long r, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ unsigned long long ffma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ unsigned long long fadd2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // ---------------------------------------------------------------- host: tensor maps
 
 // Encode a 2-D bf16 tensor map (rows x cols, row stride `ld` elements) with a
@@ -313,6 +355,11 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parit
 // elements read as zero.
 cudaError_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
                               uint32_t box_rows);
+
+// A 4-D bf16 tensor map of densely packed [n3][n2][n1][cols] with a box of b3 x 1 x b1 x 64 and
+// the 128-byte swizzle: the box's b3 * b1 rows land one after the other.  Out-of-bounds elements read as zero.
+cudaError_t make_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t n3, uint64_t n2, uint64_t n1, uint64_t cols,
+                              uint32_t b3, uint32_t b1);
 
 }  // namespace tc
 }  // namespace spec
