@@ -45,8 +45,8 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
     const T* q = static_cast<const T*>(p.q);
     const float scale2 = p.scale * kLog2e, cap2 = p.softcap * kLog2e, incap = p.softcap > 0.f ? p.scale / p.softcap : 0.f;
 
-    for (int id = blockIdx.x; id < plan.items; id += gridDim.x) {
-        const Item it = find_item(p, plan, id);
+    Walk walk(p, plan, blockIdx.x);
+    for (Item it; walk.next(p, plan, it);) {
         __syncthreads();   // the last item's Q and P are read
         for (int idx = t; idx < FR * (D / 4); idx += 256) {
             const int r = idx / (D / 4), c4 = idx % (D / 4);
@@ -229,20 +229,23 @@ __global__ void __launch_bounds__(128) k_attn_shared_join(const Params p, int n_
     const int i = r0 + lane;                      // row within gT
     griddep_wait();
     const Plan t = *reinterpret_cast<const Plan*>(static_cast<unsigned char*>(p.ws) + kPlanOffset);
-    const int first = p.cum[b], nsO = p.cum[b + 1] - first;
-    if (t.nsS + nsO == 1) return;                 // written by its item
     const int rb = r0 / p.RB;                     // 32 divides RB
     const int sb = p.gT >= p.RB ? b * p.n_rbO + rb : b / p.nbb;
+    const int colS = kvh * p.n_rbS + sb, colO = kvh * p.n_rbO + rb, cols = p.Hkv * p.n_rbO;
+    const int n = own_tiles(p, own_len(p, b));
+    const Cuts kO(p, t.q, p.cum[b] + colO * (n + p.fixO), p.fixO, n), kS(p, t.q, colS * (t.nS + p.fixS), p.fixS, t.nS);
+    const int nsS = t.nS ? kS.count : 0, nsO = kO.count;
+    if (nsS + nsO == 1) return;                   // written by its item
     const int rS = p.gT >= p.RB ? i % p.RB : (b % p.nbb) * p.gT + i;
     const int rO = i % p.RB;
     const bool in = i < p.gT;
     const size_t strideS = static_cast<size_t>(D / 4 + 1) * p.rowsS, strideO = static_cast<size_t>(D / 4 + 1) * p.rowsO;
-    const float4* ps = p.part_s + static_cast<size_t>((kvh * p.n_rbS + sb) * t.nsS) * strideS + rS;
-    const float4* po = p.part_o + static_cast<size_t>(first * p.Hkv * p.n_rbO + (kvh * p.n_rbO + rb) * nsO) * strideO + rO;
+    auto ps = [&](int k) { return p.part_s + kS.slot(colS, p.Hkv * p.n_rbS, k) * strideS + rS; };
+    auto po = [&](int k) { return p.part_o + kO.slot(b * cols + colO, p.B * cols, k) * strideO + rO; };
     float M = -INFINITY;
     if (in) {
-        for (int k = 0; k < t.nsS; ++k) M = fmaxf(M, ps[k * strideS].x);
-        for (int k = 0; k < nsO; ++k) M = fmaxf(M, po[k * strideO].x);
+        for (int k = 0; k < nsS; ++k) M = fmaxf(M, ps(k)->x);
+        for (int k = 0; k < nsO; ++k) M = fmaxf(M, po(k)->x);
     }
     const float ref = M == -INFINITY ? 0.f : M;
     float l = 0.f;
@@ -262,8 +265,8 @@ __global__ void __launch_bounds__(128) k_attn_shared_join(const Params p, int n_
         }
     };
     if (in) {
-        for (int k = 0; k < t.nsS; ++k) add(ps + k * strideS, p.rowsS);
-        for (int k = 0; k < nsO; ++k) add(po + k * strideO, p.rowsO);
+        for (int k = 0; k < nsS; ++k) add(ps(k), p.rowsS);
+        for (int k = 0; k < nsO; ++k) add(po(k), p.rowsO);
     }
     const float inv = 1.f / l;
 #pragma unroll
@@ -291,21 +294,22 @@ HostPlan host_plan(Params& p, bool tc, bool shared, int ctas) {
     h.tc = tc;
     p.g = p.Hq / p.Hkv;
     p.gT = p.g * p.T;
-    p.RB = tc ? 128 : FR;
-    p.KT = tc ? 128 : FK;
+    p.RB = tc ? kTcRows : FR;
+    p.KT = tc ? kTcKeys : FK;
     p.nbb = p.gT >= p.RB ? 1 : std::min(p.RB / p.gT, p.B);
     p.n_rbO = (p.gT + p.RB - 1) / p.RB;
     p.n_rbS = p.gT >= p.RB ? p.B * p.n_rbO : (p.B + p.nbb - 1) / p.nbb;
     p.rowsO = std::min(p.gT, p.RB);
     p.rowsS = p.nbb * p.rowsO;
     p.ctas = ctas;
-    p.max_extra = 4 * ctas;
-    p.fixed = 2.5f;
+    p.fixS = tc ? (p.rowsS > 128 ? 5 : 3) : 2;
+    p.fixO = tc ? (p.rowsO > 128 ? 5 : 3) : 2;
+    p.min_piece = 4;
     const size_t per_row = sizeof(float) * (p.D + 4);
-    const size_t items_s = shared ? static_cast<size_t>(p.Hkv) * p.n_rbS + p.max_extra : 0;
-    const size_t items_o = static_cast<size_t>(p.B) * p.Hkv * p.n_rbO + p.max_extra;
+    const size_t items_s = shared ? static_cast<size_t>(p.Hkv) * p.n_rbS + ctas : 0;   // one slot per column and per cut
+    const size_t items_o = static_cast<size_t>(p.B) * p.Hkv * p.n_rbO + ctas;
     h.cum_off = kWsHeader;
-    h.part_s_off = h.cum_off + round_up(sizeof(int32_t) * (static_cast<size_t>(p.B) + 1), 256);
+    h.part_s_off = h.cum_off + round_up(sizeof(int32_t) * static_cast<size_t>(p.B), 256);
     h.part_o_off = h.part_s_off + round_up(items_s * p.rowsS * per_row, 256);
     h.total = h.part_o_off + round_up(items_o * p.rowsO * per_row, 256);
     return h;
@@ -321,6 +325,10 @@ static spec_status check_shapes(const spec_tree* t, int B, int Hq, int Hkv, int 
     if (Lmax < 1 || Lmax > (1 << 22)) return fail(SPEC_EINVAL, "Lmax = %d out of 1..2^22", Lmax);
     if (Ls < 0 || Ls > (1 << 22)) return fail(SPEC_EINVAL, "the shared capacity %d is out of 1..2^22", Ls);
     const int64_t rows = static_cast<int64_t>(B) * Hq * t->T;
+    // 64-key tiles of all columns, each at most 64 rows high and a few tiles of fixed cost longer
+    const int64_t blocks = static_cast<int64_t>(Hkv) * ((static_cast<int64_t>(Hq / Hkv) * t->T + FR - 1) / FR);
+    const int64_t line = blocks * B * ((Lmax + 63) / 64 + (t->T + 63) / 64 + (Ls + 63) / 64 + 16);
+    if (line > INT32_MAX / 2) return fail(SPEC_EINVAL, "B * Hkv * (Lmax + the shared capacity) is too large for one call (%lld tiles)", static_cast<long long>(line));
     if (rows > (1ll << 30)) return fail(SPEC_EINVAL, "B * Hq * T = %lld query rows exceed 2^30", static_cast<long long>(rows));
     return SPEC_OK;
 }

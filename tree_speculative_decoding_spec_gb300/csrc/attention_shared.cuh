@@ -9,12 +9,15 @@
 //   shared  one (KV head, block of RB rows) against the shared keys; here a block
 //           holds the rows of as many whole sequences as fit (nbb of them), so
 //           that a shared key is read once for all of those
-// Every column's key tiles (KT keys each) are cut into splits of about `chunk`
-// tiles, one item each.  The cut follows the lengths, which only the device
-// knows: a warp of every CTA reads them and works out the same Plan.  An item
-// leaves (max, sum, unnormalised O) of its rows in its own part of the
-// workspace; the join merges a row's items.  A row that has a single item gets
-// its output from there directly.
+// All columns' key tiles (KT keys each) are laid end to end, each column led by a few
+// tiles for what an item costs beside its tiles, and the line is cut into equal parts,
+// one per CTA; a column that a cut crosses is that many items more.  So the CTAs finish
+// together, with one split per CTA more than there are columns (cutting every column
+// into equal splits left the last round of them part empty: 306 tiles on the longest of
+// 152 CTAs where the mean was 233).  The cut follows the lengths, which only the device
+// knows: a warp of every CTA reads them and works out the same line.  An item leaves
+// (max, sum, unnormalised O) of its rows in its own part of the workspace; the join
+// merges a row's items.  A row that has a single item gets its output from there directly.
 #pragma once
 
 #include "attention_tc.cuh"
@@ -26,13 +29,15 @@ namespace shr {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+constexpr int kTcRows = 256, kTcKeys = 64;   // rows of a block and keys of a tile, tensor-core items
+
 struct Params {
     int B, T, g, gT, Hq, Hkv, D, words;
     int Lshared, Lmax;                 // capacities
     int RB, KT;                        // rows of a block, keys of a tile
     int nbb, n_rbO, n_rbS, rowsO, rowsS;
-    int ctas, max_extra;               // CTAs the plan fills; bound on splits beyond one per column
-    float fixed;                       // cost of an item beyond its tiles, in tiles
+    int ctas;                          // parts of the line
+    int fixS, fixO, min_piece;         // cost of an item beside its tiles (shared, own), in tiles; the shortest split
     float scale, softcap;              // softcap 0: none
     int window;                        // 0: none
     const float* slopes;               // [Hq] or NULL
@@ -46,16 +51,16 @@ struct Params {
     void* out;
     float* lse;
     void* ws;                          // status word, then the Plan, then cum [B + 1], then the items
-    int32_t* cum;                      // splits of the sequences before b, one column each
+    int32_t* cum;                      // place on the line of each sequence's first column [B]
     float4 *part_s, *part_o;           // items: [D / 4 + 1][rows] float4: (m, l, -, -), then O
 };
 
 struct Plan {
     int Ls;          // shared keys
     int sT0, nS;     // first shared tile any row sees, and how many from there
-    int chunk;       // tiles of a split, at most
-    int nsS;         // splits of a shared column
-    int itemsS, items;
+    int q;           // tiles of a CTA's part of the line
+    int colsS;       // shared columns on the line
+    int own0;        // place of the own columns
 };
 
 constexpr int kPlanOffset = 64;        // bytes into the workspace header
@@ -72,61 +77,54 @@ __device__ __forceinline__ int own_tiles(const Params& p, int L) {   // with the
 }
 __device__ __forceinline__ int own_len(const Params& p, int b) { return min(max(p.prefix_len[b], 0), p.Lmax); }
 
-// A whole warp works out the plan (every lane gets it).  Cost of a cut with splits of c tiles,
-// W tiles in all: if it has at most one item per CTA, c + fixed; else the items are handed out
-// as CTAs get free, W / ctas tiles and fixed * items / ctas beside them, and half an item at the end.
+// A whole warp works out the plan (every lane gets it).
 __device__ __forceinline__ Plan make_plan(const Params& p) {
-    const int lane = threadIdx.x & 31;
-    long long own = 0;
-    int longest = 0, least = 0x7fffffff;
-    for (int b = lane; b < p.B; b += 32) {
-        const int L = own_len(p, b), n = own_tiles(p, L);
-        own += n;
-        longest = max(longest, n);
+    int own = 0, least = 0x7fffffff;
+    for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+        const int L = own_len(p, b);
+        own += own_tiles(p, L) + p.fixO;
         least = min(least, L);
     }
     for (int o = 16; o > 0; o >>= 1) {
         own += __shfl_xor_sync(0xffffffffu, own, o);
-        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
         least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
     }
     Plan t;
     t.Ls = p.shared_len ? min(max(*p.shared_len, 0), p.Lshared) : 0;
     t.sT0 = p.window > 0 ? max(0, t.Ls + least - p.window + 1) / p.KT : 0;
     t.nS = max(0, ceil_div(t.Ls, p.KT) - t.sT0);
-    const int colsS = p.Hkv * p.n_rbS, colsO = p.Hkv * p.n_rbO;
-    const long long W = static_cast<long long>(colsS) * t.nS + own * colsO;
-    const long long cols = (t.nS ? colsS : 0) + static_cast<long long>(p.B) * colsO;
-    longest = max(longest, t.nS);
-    const int floor_c = static_cast<int>((W + p.max_extra - 1) / p.max_extra);   // bounds the items
-    // 32 candidates at even distances up to the longest column
-    int c = max(floor_c, static_cast<int>((static_cast<long long>(longest) * (lane + 1) + 31) / 32));
-    // about W / c + cols / 2 items; the last candidate cuts nothing
-    const float items = lane == 31 ? static_cast<float>(cols) : fmaxf(static_cast<float>(W) / c + 0.5f * cols, static_cast<float>(cols));
-    const float n = static_cast<float>(p.ctas);
-    float cost = items <= n ? c + p.fixed : (static_cast<float>(W) + p.fixed * items) / n + 0.5f * (c + p.fixed);
-    for (int o = 16; o > 0; o >>= 1) {
-        const float c2 = __shfl_xor_sync(0xffffffffu, cost, o);
-        const int k2 = __shfl_xor_sync(0xffffffffu, c, o);
-        if (c2 < cost || (c2 == cost && k2 > c)) { cost = c2; c = k2; }
-    }
-    t.chunk = max(c, 1);
-    t.nsS = ceil_div(t.nS, t.chunk);
-    t.itemsS = colsS * t.nsS;
-    int ns = 0;
-    for (int b = lane; b < p.B; b += 32) ns += ceil_div(own_tiles(p, own_len(p, b)), t.chunk);
-    for (int o = 16; o > 0; o >>= 1) ns += __shfl_xor_sync(0xffffffffu, ns, o);
-    t.items = t.itemsS + ns * colsO;
+    t.colsS = t.nS ? p.Hkv * p.n_rbS : 0;
+    t.own0 = t.colsS * (t.nS + p.fixS);
+    const int total = t.own0 + own * p.Hkv * p.n_rbO;
+    t.q = max(ceil_div(total, p.ctas), max(p.fixS, p.fixO) + p.min_piece);
     return t;
 }
 
-// The plan and the sequences' split offsets, for the join: one warp of the grid writes them.
+// The items of the column of n tiles whose place on the line is s: the line is cut at multiples of
+// q, save where less than min_piece tiles of the column would be left on one side.  Item k
+// belongs to CTA owner + k.
+struct Cuts {
+    int owner, count, base, q, n;
+    __device__ __forceinline__ Cuts(const Params& p, int q_, int s, int fixed, int n_) : q(q_), n(n_) {
+        base = s + fixed;                                            // place of the column's first tile
+        const int i0 = min(ceil_div(base + p.min_piece, q), p.ctas); // first cut
+        const int i1 = max(base + n - p.min_piece, 0) / q;           // last cut
+        owner = i0 - 1;
+        count = max(0, i1 - i0 + 1) + 1;
+    }
+    __device__ __forceinline__ int begin(int k) const { return k == 0 ? 0 : (owner + k) * q - base; }
+    __device__ __forceinline__ int end(int k) const { return k == count - 1 ? n : (owner + k + 1) * q - base; }
+    // the workspace slot among `cols` columns: one per column, one per cut of the line
+    __device__ __forceinline__ int slot(int col, int cols, int k) const { return k == 0 ? col : cols + owner + k; }
+};
+
+// The plan and the sequences' places, for the join: one warp of the grid writes them.
 __device__ __forceinline__ void publish_plan(const Params& p, const Plan& t) {
     const int lane = threadIdx.x & 31;
-    int before = 0;
+    int before = t.own0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
-        const int n = b < p.B ? ceil_div(own_tiles(p, own_len(p, b)), t.chunk) : 0;
+        const int n = b < p.B ? (own_tiles(p, own_len(p, b)) + p.fixO) * p.Hkv * p.n_rbO : 0;
         int at = n;
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, at, o);
@@ -135,10 +133,7 @@ __device__ __forceinline__ void publish_plan(const Params& p, const Plan& t) {
         if (b < p.B) p.cum[b] = before + at - n;
         before += __shfl_sync(0xffffffffu, at, 31);
     }
-    if (lane == 0) {
-        p.cum[p.B] = before;
-        *reinterpret_cast<Plan*>(static_cast<unsigned char*>(p.ws) + kPlanOffset) = t;
-    }
+    if (lane == 0) *reinterpret_cast<Plan*>(static_cast<unsigned char*>(p.ws) + kPlanOffset) = t;
 }
 
 struct Item {
@@ -148,66 +143,93 @@ struct Item {
     int rows;        // rows of the block, over all its sequences
     int L;           // the sequence's cached keys (own items)
     int t0, t1;      // tiles [t0, t1) of the column: own ones count from own_first, the tree's last
-    int index;       // among the items of its kind
+    int index;       // workspace slot among those of its kind
     int direct;      // the rows' only item: write their output
 };
 
-// Item number `id`; a whole warp, every lane gets it.
-__device__ __forceinline__ Item find_item(const Params& p, const Plan& t, int id) {
-    const int lane = threadIdx.x & 31;
-    Item it;
-    if (id < t.itemsS) {
-        const int col = id / t.nsS, split = id - col * t.nsS;
-        const int sb = col % p.n_rbS;
-        it.shared = 1;
-        it.kvh = col / p.n_rbS;
-        it.b = p.gT >= p.RB ? sb / p.n_rbO : sb * p.nbb;
-        it.rb = p.gT >= p.RB ? sb % p.n_rbO : 0;
-        it.rows = p.gT >= p.RB ? min(p.RB, p.gT - it.rb * p.RB) : min(p.nbb, p.B - it.b) * p.gT;
-        it.L = 0;
-        it.t0 = static_cast<int>(static_cast<long long>(t.nS) * split / t.nsS);
-        it.t1 = static_cast<int>(static_cast<long long>(t.nS) * (split + 1) / t.nsS);
-        it.index = id;
-        it.direct = 0;
-        return it;
-    }
-    const int cols = p.Hkv * p.n_rbO;
-    const int at = (id - t.itemsS) / cols;      // number of the split over all sequences, one column each
-    int before = 0;
-    for (int b0 = 0;; b0 += 32) {
-        const int b = b0 + lane;
-        const int L = b < p.B ? own_len(p, b) : 0;
-        const int tiles = b < p.B ? own_tiles(p, L) : 0;
-        const int n = ceil_div(tiles, t.chunk);
-        int end = n;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, end, o);
-            if (lane >= o) end += y;
+// The items of one CTA in the line's order; a whole warp, every lane gets them.
+struct Walk {
+    int cta, colS;             // next shared column
+    int b, base, col, L, n;    // next own column: sequence, place of its first column, column, keys, tiles
+    __device__ __forceinline__ Walk(const Params& p, const Plan& t, int cta_) : cta(cta_) {
+        const int lane = threadIdx.x & 31;
+        const int x = max(0, cta * t.q - max(p.fixS, p.fixO) - p.min_piece);   // no earlier column has an item here
+        colS = t.nS ? min(x / (t.nS + p.fixS), t.colsS) : 0;
+        b = p.B;
+        base = t.own0;
+        col = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int i = b0 + lane;
+            const int Li = i < p.B ? own_len(p, i) : 0;
+            const int ni = i < p.B ? own_tiles(p, Li) : 0;
+            const int w = i < p.B ? (ni + p.fixO) * p.Hkv * p.n_rbO : 0;
+            int end = w;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, i < p.B && x < base + end);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                b = b0 + l;
+                base += __shfl_sync(0xffffffffu, end - w, l);
+                L = __shfl_sync(0xffffffffu, Li, l);
+                n = __shfl_sync(0xffffffffu, ni, l);
+                col = max(0, x - base) / (n + p.fixO);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, end, 31);
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, at < before + end);
-        if (hit || b0 + 32 >= p.B) {
-            const int l = hit ? __ffs(hit) - 1 : 31;
-            const int first = before + __shfl_sync(0xffffffffu, end - n, l);
-            const int ns = __shfl_sync(0xffffffffu, n, l), tl = __shfl_sync(0xffffffffu, tiles, l);
-            // items of one sequence: (KV head, block, split); the splits of all columns of the
-            // sequences before it come first
-            const int r = (id - t.itemsS) - first * cols;
-            const int col = r / ns, split = r - col * ns;
+    }
+    __device__ __forceinline__ bool next(const Params& p, const Plan& t, Item& it) {
+        for (; colS < t.colsS;) {
+            const int c = colS++;
+            const Cuts k(p, t.q, c * (t.nS + p.fixS), p.fixS, t.nS);
+            if (k.owner > cta) return false;
+            if (k.owner + k.count <= cta) continue;
+            const int sb = c % p.n_rbS, i = cta - k.owner;
+            it.shared = 1;
+            it.kvh = c / p.n_rbS;
+            it.b = p.gT >= p.RB ? sb / p.n_rbO : sb * p.nbb;
+            it.rb = p.gT >= p.RB ? sb % p.n_rbO : 0;
+            it.rows = p.gT >= p.RB ? min(p.RB, p.gT - it.rb * p.RB) : min(p.nbb, p.B - it.b) * p.gT;
+            it.L = 0;
+            it.t0 = k.begin(i);
+            it.t1 = k.end(i);
+            it.index = k.slot(c, p.Hkv * p.n_rbS, i);
+            it.direct = 0;
+            return true;
+        }
+        const int cols = p.Hkv * p.n_rbO;
+        while (b < p.B) {
+            if (col == cols) {
+                base += cols * (n + p.fixO);
+                col = 0;
+                if (++b == p.B) break;
+                L = own_len(p, b);
+                n = own_tiles(p, L);
+                continue;
+            }
+            const int c = col++;
+            const Cuts k(p, t.q, base + c * (n + p.fixO), p.fixO, n);
+            if (k.owner > cta) return false;
+            if (k.owner + k.count <= cta) continue;
+            const int i = cta - k.owner;
             it.shared = 0;
-            it.b = b0 + l;
-            it.L = __shfl_sync(0xffffffffu, L, l);
-            it.kvh = col / p.n_rbO;
-            it.rb = col % p.n_rbO;
+            it.b = b;
+            it.L = L;
+            it.kvh = c / p.n_rbO;
+            it.rb = c % p.n_rbO;
             it.rows = min(p.RB, p.gT - it.rb * p.RB);
-            it.t0 = static_cast<int>(static_cast<long long>(tl) * split / ns);
-            it.t1 = static_cast<int>(static_cast<long long>(tl) * (split + 1) / ns);
-            it.index = id - t.itemsS;
-            it.direct = t.nsS + ns == 1;
-            return it;
+            it.t0 = k.begin(i);
+            it.t1 = k.end(i);
+            it.index = k.slot(b * cols + c, p.B * cols, i);
+            it.direct = t.nS == 0 && k.count == 1;
+            return true;
         }
-        before += __shfl_sync(0xffffffffu, end, 31);
+        return false;
     }
-}
+};
 
 // The row of q and out that row r of the item's block is.
 __device__ __forceinline__ size_t row_of_q(const Params& p, const Item& it, int r) {

@@ -1,28 +1,39 @@
 // Tensor-core (tcgen05) items of the shared-prefix and scored tree attention:
 // bf16, head dim 64 or 128.
 //
-// One persistent CTA per SM takes items blockIdx.x, blockIdx.x + gridDim.x, ...
-// of the cut that attention_shared.cuh describes: 128 query rows against a range
-// of 128-key tiles.  Eleven warps, all of which walk the same items:
-//   warp 8       TMA: the item's Q block, then its K and V tiles into a ring that
-//                runs on across items
-//   warps 9, 10  MMA, one thread each: thread g takes the tiles whose running
-//                number J (over all items of the CTA) has J % 2 == g -- S_J = Q K_J^T
-//                into score buffer g, O_g += P_J V_J with P_J read from TMEM
-//   warps 0-3 / 4-7: two softmax groups, group J % 2 for tile J, one thread per
-//                query row: S from TMEM, score transform and masks, running maximum
-//                and sum in base 2 and 32 bits, P back as bf16 pairs over the first
-//                half of the score buffer.  P is rounded to bf16 because the product
-//                takes both operands in one type and V is bf16; the sum l is taken
-//                before the rounding.  At the end of an item the groups exchange
-//                (m, l) and each merges one half of the columns of both O.
-// A thread's MMAs run in issue order, so S_{J+2} may overwrite the buffer PV_J
-// reads, and S_J complete implies PV_{J-2} complete.  Barriers whose phases both
-// MMA threads pass: q_empty (each commits after its last S of the item), o_final
-// (after its last PV); o_empty lets the next item's first PV overwrite O once
-// every softmax warp has read it.
-// V rows that no row sees (past the lengths, past the tree) are zeroed before PV
-// reads them: their weight is zero, but zero times a stale infinity is not.
+// One persistent CTA per SM takes items of the cut that attention_shared.cuh
+// describes: up to 256 query rows against a range of 64-key tiles.  Twelve warps:
+//   warp 11      schedule: works out the plan and puts its CTA's items into a ring of
+//                descriptors that the other roles read
+//   warp 8       TMA: the item's Q rows, then its K and V tiles into a ring that runs
+//                on across items
+//   warps 9, 10  MMA, one thread each, thread g for softmax group g
+//   warps 0-3 / 4-7: two softmax groups, one thread per query row
+// Key tiles are 64 keys long where the work is cut; there are two ways through an item:
+//   pair (more than 128 rows): group g owns rows 128 g .. and takes every tile, two of
+//     them at a time (128 keys), so one K/V tile in shared memory serves 256 rows and L2
+//     carries half the bytes that two 128-row CTAs would read.  S is M 128, N 128: a
+//     product with both operands in shared memory reads A again for every 128 x N, and at
+//     N 64 takes as long as at N 128 (measured: 8 products 500 cycles either way).
+//   narrow (at most 128 rows, bound by memory): both groups work on the same rows and take
+//     alternate 64-key tiles; each group has two score buffers, so that S of its next tile
+//     runs while it works on this one, and small tiles keep more loads in flight.  At the
+//     item's end the groups exchange (max, sum) and each joins half the columns of both O.
+// Per tile and group: S = Q K^T into the group's score buffer; the softmax thread reads
+// its row, transforms and masks it, keeps the running maximum and sum in base 2 and 32
+// bits and writes P as bf16 pairs over the first half of the buffer; O += P V with P read
+// from TMEM.  P is rounded to bf16 because the product takes both operands in one type
+// and V is bf16; the sum is taken before the rounding.
+// A thread's MMAs run in issue order, so an S may overwrite the buffer an earlier PV
+// reads.  O is rescaled only when a row's maximum grows by more than 2^8, once the
+// group's previous PV is complete (in a pair S complete says so; a narrow item waits).
+// V rows that no row sees (past the lengths, past the tree) are zeroed before PV reads
+// them: their weight is zero, but zero times a stale infinity is not.
+// The ring's stages hold K and V of one narrow tile, or K or V of one pair tile, so both
+// kinds of item run through the same ring.  Barrier phases that one of the MMA threads
+// skips (it has no part in a tile) are behind it by construction: landing barriers are
+// used every second round of the stages, and both threads pass q_full and o_empty at every
+// item.
 // Waits are bounded (2 s); on expiry SPEC_ETIMEOUT goes to the status word, every
 // role leaves its loops, and the CTA drains its own loads and MMAs before it
 // frees TMEM.
@@ -37,36 +48,311 @@ namespace shr {
 
 using namespace tc;
 
-constexpr int kRows = 128;       // query rows of a block (MMA M)
-constexpr int kKeys = 128;       // keys of a tile
-constexpr int kThreads = 352;
-constexpr int kHalf = 128 * 128; // bytes of 128 rows x 64 columns
+constexpr int kRows = 128;        // query rows of a group (MMA M)
+constexpr int kBlock = kTcRows;   // of a block: two groups
+constexpr int kKeys = kTcKeys;    // keys of a tile
+constexpr int kThreads = 384;
+constexpr int kItems = 4;         // item descriptors in flight
+constexpr int kQHalf = kBlock * 128;    // bytes of a 64-column half of the Q block
+constexpr int kHalf = kKeys * 128;      // of a 64-key tile; a 128-key tile's is twice that
 
 template <int D> struct Cfg {
     static constexpr int kH = D / 64;                      // 64-column halves
-    static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kFull = 2 * kStages;              // landing barriers: each belongs to one MMA thread
-    static constexpr int kQ = kH * kHalf;
-    static constexpr int kStage = 2 * kH * kHalf;          // K, then V
-    static constexpr int kTail = 256 + 2 * kRows * 8;      // barriers, exchange of (m, l)
-    static constexpr int kSmem = kQ + kStages * kStage + kTail;
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kFull = 2 * kStages;              // landing barriers
+    static constexpr int kQ = kH * kQHalf;
+    static constexpr int kStage = 2 * kH * kHalf;          // K, then V of 64 keys; K or V of 128
+    static constexpr int kBars = 5 + 4 + 4 + 2 + 2 + 2 + kFull + kStages + 2 * kItems;
+    static constexpr int kExchange = 512 + kItems * 64;    // barriers and flags, descriptors
+    static constexpr int kSmem = kQ + kStages * kStage + kExchange + 2 * kRows * 8;
 };
-constexpr uint32_t kTmemCols = 512;   // S0 [0,128) S1 [128,256) O0 [256, 256 + D) O1 behind it
-constexpr uint32_t kO = 2 * kKeys;
+constexpr uint32_t kTmemCols = 512;   // scores of group g at 128 g (narrow: buffer b at 128 g + 64 b); O of group g at 256 + D g
+constexpr uint32_t kO = 256;
 
 struct Maps {
     CUtensorMap q_own, q_shared, kc, vc, ks, vs, kt, vt;
 };
 
-// Bounded wait of a whole warp: every lane gets the same answer.
+// What the roles need to know of an item, 64 bytes.
+struct Desc {
+    int valid, shared, pair, direct;
+    int b, kvh, rb, rows;
+    int first, n_pre, end, Ls;     // first key tile, tiles before the tree's, keys before the tree's, shared keys
+    int t0, tiles, index, L;
+};
+static_assert(sizeof(Desc) == 64, "four descriptors");
+
+// The tiles of an item as its way through counts them: `width` 64-key tiles at a time, none
+// across the border between prefix and tree.
+struct Tiles {
+    int width, pre, count;   // tiles of the prefix, tiles in all
+    __device__ __forceinline__ explicit Tiles(const Desc& it) {
+        width = it.pair ? 2 : 1;
+        const int n_pre = min(max(it.n_pre - it.t0, 0), it.tiles);
+        pre = (n_pre + width - 1) / width;
+        count = pre + (it.tiles - n_pre + width - 1) / width;
+    }
+};
+struct Tile {
+    bool tree;
+    int k0, nvalid;          // first key (of the source's), keys that any row can see
+    __device__ __forceinline__ Tile(const Params& p, const Desc& it, const Tiles& ts, int j) {
+        tree = j >= ts.pre;
+        const int first = tree ? max(it.t0 - it.n_pre, 0) + (j - ts.pre) * ts.width : it.first + it.t0 + j * ts.width;
+        // a pair tile ends with the item's part of the column
+        const int last = tree ? it.t0 + it.tiles - it.n_pre : it.first + min(it.t0 + it.tiles, it.n_pre);
+        k0 = first * kKeys;
+        nvalid = min(min(ts.width, last - first) * kKeys, (tree ? p.T : it.end) - k0);
+    }
+};
+
+// Wait for a phase, bounded (2 s, or another role's abort).  The clock is read only now and then:
+// most waits here are short, and reading it takes as long as they do.
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 31u) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (*abort_flag || now - t0 > 2000000000ull) return false;
+        }
+    }
+    return true;
+}
+// The same by a whole warp: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort_flag));
+    return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag));
 }
 
 __device__ __forceinline__ float rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// One query row's place: position, slope (times log2 e), ancestor words.
+struct Row {
+    bool in;
+    int pos;
+    float slope2;
+    const uint64_t* anc;
+};
+
+// 64 scores of the thread's row, from TMEM and back.
+__device__ __forceinline__ void load64(uint32_t addr, float (&x)[64]) {
+    uint32_t r0[32], r1[32];
+    tmem_ld32(addr, r0);
+    tmem_ld32(addr + 32, r1);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        x[e] = __uint_as_float(r0[e]);
+        x[e + 32] = __uint_as_float(r1[e]);
+    }
+}
+__device__ __forceinline__ void store64(uint32_t addr, const float (&x)[64]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t r[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(x[16 * q + e]);
+        tmem_st16(addr + 16 * q, r);
+    }
+}
+__device__ __forceinline__ float max64(const float (&x)[64]) {
+    float m[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        m[e] = fmax3(fmax3(x[e], x[e + 8], x[e + 16]), fmax3(x[e + 24], x[e + 32], x[e + 40]), fmaxf(x[e + 48], x[e + 56]));
+    return fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
+}
+
+// cap2 tanh(s k) for 64 raw scores s, cap2 = softcap log2 e, k = scale / softcap.  Where the whole
+// warp's |s k| stay within 0.7 (caps sit far above ordinary scores) by tanh(u) = u (1 + u^2 P(u^2)):
+// P of degree 4 in u^2 fitted to the function on [0, 0.49] by weighted least squares, its weights
+// iterated towards an even relative error, 1.6e-8 at most; eight packed products for two scores,
+// on the FMA units that the softmax leaves idle.  Else as cap2 (1 - 2 / (e^(2u) + 1)), two
+// special-function operations a score, the pipe the exponentials need (a 128-key tile of the 32K
+// capped layer: 4000 cycles).  `in`: the lane's row is one of the
+// block, `whole`: so is every key: what stale memory made of others must not choose the way, or
+// results would vary with it.
+__device__ __forceinline__ void cap64(float (&x)[64], float scale2, float k, float cap2, bool in, bool whole) {
+    float a[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        a[e] = fmax3(fmax3(fabsf(x[e]), fabsf(x[e + 8]), fabsf(x[e + 16])), fmax3(fabsf(x[e + 24]), fabsf(x[e + 32]), fabsf(x[e + 40])),
+                     fmaxf(fabsf(x[e + 48]), fabsf(x[e + 56])));
+    const float most = fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7])) * k;
+    if (whole && k < 100.f && __all_sync(0xffffffffu, !in || most <= 0.7f)) {
+        const float z = k * k, z2 = z * z;
+        const float c0 = -0.33333189899901133f * z, c1 = 0.13329110734967342f * z2, c2 = -0.053558861130687065f * z2 * z,
+                    c3 = 0.02009196966007083f * z2 * z2, c4 = -0.005138661857974488f * z2 * z2 * z;
+        const unsigned long long p0 = pk2(c0, c0), p1 = pk2(c1, c1), p2 = pk2(c2, c2), p3 = pk2(c3, c3), p4 = pk2(c4, c4);
+        const unsigned long long sc = pk2(scale2, scale2), zero = pk2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+            const unsigned long long v = pk2(x[e], x[e + 1]);
+            const unsigned long long w = ffma2(v, v, zero);
+            unsigned long long q = ffma2(w, p4, p3);
+            q = ffma2(w, q, p2);
+            q = ffma2(w, q, p1);
+            q = ffma2(w, q, p0);
+            q = ffma2(w, q, zero);
+            const unsigned long long lin = ffma2(v, sc, zero);
+            upk2(ffma2(lin, q, lin), x[e], x[e + 1]);
+        }
+    } else {
+        const float k2 = 2.f * kLog2e * k;
+#pragma unroll
+        for (int e = 0; e < 64; ++e) x[e] = fmaf(-2.f * cap2, rcp(ex2(x[e] * k2) + 1.f), cap2);
+    }
+}
+
+// One softmax thread's work on a tile of 64 * halves keys: wait for S, transform, mask, running
+// maximum (rescaling O where it grew), weights back as bf16 pairs over the scores.  Two passes
+// over the scores, 64 at a time, transformed and masked ones written back in between: a row of
+// 128 in registers, all of it unrolled, is code that the instruction cache does not hold (a
+// first tile took 9 us, one in a hundred afterwards 2 us).
+// pv_bar: the barrier of the group's previous PV, NULL where S complete implies it.
+// landed(): called once S is complete; release(h): the weights of keys 64 h .. are in place.
+template <int D, bool kScored, typename Landed, typename Release>
+__device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, const Tile& tl, const Row& row, int halves, bool warp_in,
+                                             uint32_t s_addr, uint32_t o_addr, float& m_used, float& l, uint64_t* s_bar,
+                                             uint32_t s_parity, uint64_t* pv_bar, uint32_t pv_parity, volatile int* abort_flag,
+                                             Landed landed, Release release) {
+    uint64_t seen0 = ~0ull, seen1 = ~0ull;   // of the tree: the node's ancestors and itself
+    if (tl.tree && warp_in) {
+        seen0 = row.anc[tl.k0 >> 6];
+        if (tl.nvalid > 64) seen1 = row.anc[(tl.k0 >> 6) + 1];
+    }
+    if (!warp_wait(s_bar, s_parity, abort_flag)) return false;
+    tc_fence_after();
+    if (!landed()) return false;
+    if (!warp_in) {
+        for (int h = 0; h < halves; ++h) release(h);
+        return true;
+    }
+    const float scale2 = p.scale * kLog2e;
+    const bool transformed = kScored && (p.softcap > 0.f || p.slopes);
+    const float in_scale = transformed ? 1.f : scale2;   // what the exponent's FFMA still multiplies by
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int h = 0; h < halves; ++h) {
+        float x[64];
+        load64(s_addr + 64 * h, x);
+        bool changed = transformed;
+        const int nv = min(max(tl.nvalid - 64 * h, 0), 64);
+        uint64_t bits = nv >= 64 ? ~0ull : (1ull << nv) - 1ull;
+        bits &= h ? seen1 : seen0;
+        bool masked = tl.tree || nv < 64;
+        if constexpr (kScored) {
+            const int k0 = tl.k0 + 64 * h;
+            const int kbase = it.shared ? k0 : it.Ls + k0;      // position of the first key (not the tree's)
+            const int depth = row.pos - it.Ls - it.L;           // (own items) the node's
+            if (p.softcap > 0.f) cap64(x, scale2, p.scale / p.softcap, p.softcap * kLog2e, row.in, nv == 64);
+            if (p.slopes) {
+                const float f = p.softcap > 0.f ? 1.f : scale2;
+                if (tl.tree) {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        if (4 * q < nv) {   // the encoded tree pads its arrays to 16 bytes
+                            const int4 d = *reinterpret_cast<const int4*>(p.depth + k0 + 4 * q);
+                            x[4 * q] = fmaf(x[4 * q], f, -row.slope2 * static_cast<float>(depth - d.x));
+                            x[4 * q + 1] = fmaf(x[4 * q + 1], f, -row.slope2 * static_cast<float>(depth - d.y));
+                            x[4 * q + 2] = fmaf(x[4 * q + 2], f, -row.slope2 * static_cast<float>(depth - d.z));
+                            x[4 * q + 3] = fmaf(x[4 * q + 3], f, -row.slope2 * static_cast<float>(depth - d.w));
+                        }
+                } else {
+                    const float b0 = row.slope2 * static_cast<float>(kbase - row.pos);
+                    const unsigned long long f2 = pk2(f, f), b2 = pk2(b0, b0), s2 = pk2(row.slope2, row.slope2);
+#pragma unroll
+                    for (int e = 0; e < 64; e += 2)
+                        upk2(ffma2(pk2(x[e], x[e + 1]), f2, ffma2(s2, pk2(static_cast<float>(e), static_cast<float>(e + 1)), b2)), x[e], x[e + 1]);
+                }
+            }
+            if (p.window > 0) {
+                if (tl.tree) {
+                    if (p.window <= SPEC_MAX_DEPTH)
+                        for (uint64_t left = bits; left; left &= left - 1) {
+                            const int e = __ffsll(static_cast<long long>(left)) - 1;
+                            if (depth - p.depth[k0 + e] >= p.window) bits &= ~(1ull << e);
+                        }
+                } else {
+                    const int lo = min(max(row.pos - p.window + 1 - kbase, 0), 64);   // first key seen
+                    bits &= lo >= 64 ? 0ull : ~0ull << lo;
+                    masked = masked || __any_sync(0xffffffffu, lo > 0);
+                }
+            }
+        }
+        if (masked) {
+            const uint32_t w0 = static_cast<uint32_t>(bits), w1 = static_cast<uint32_t>(bits >> 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                if (!((w0 >> e) & 1u)) x[e] = -INFINITY;
+                if (!((w1 >> e) & 1u)) x[e + 32] = -INFINITY;
+            }
+            changed = true;
+        }
+        if (changed) store64(s_addr + 64 * h, x);
+        top = fmaxf(top, max64(x));
+    }
+    if constexpr (kScored) tmem_st_wait();
+    else if (tl.tree || tl.nvalid < 64 * halves) tmem_st_wait();
+    const float tmax = top * in_scale;
+    // the reference maximum moves only when the row's grew by more than 2^8; the TMEM
+    // accesses are the whole warp's, so its rows rescale together (by 1 where nothing grew)
+    float m_new = m_used, alpha = 1.f;
+    bool rescale = false;
+    if (tmax > m_used + 8.f) {
+        if (m_used != -INFINITY) {
+            rescale = true;
+            alpha = ex2(m_used - tmax);
+        }
+        m_new = tmax;
+    }
+    if (__any_sync(0xffffffffu, rescale)) {
+        if (pv_bar && !warp_wait(pv_bar, pv_parity, abort_flag)) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o_addr + c * 16, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(o_addr + c * 16, o);
+        }
+        l *= alpha;
+    }
+    m_used = m_new;
+    const float nmref = m_used == -INFINITY ? 0.f : -m_used;
+    const unsigned long long sc2 = pk2(in_scale, in_scale), nm2 = pk2(nmref, nmref);
+#pragma unroll 1
+    for (int h = 0; h < halves; ++h) {
+        float x[64];
+        load64(s_addr + 64 * h, x);
+#pragma unroll
+        for (int qc = 0; qc < 2; ++qc) {
+            uint32_t packed[16];
+            unsigned long long acc2 = pk2(0.f, 0.f);
+#pragma unroll
+            for (int h2 = 0; h2 < 16; ++h2) {
+                const int e0 = qc * 32 + 2 * h2;
+                float x0, x1;
+                upk2(ffma2(pk2(x[e0], x[e0 + 1]), sc2, nm2), x0, x1);
+                const float a0 = ex2(x0), a1 = ex2(x1);
+                acc2 = fadd2(acc2, pk2(a0, a1));
+                const __nv_bfloat162 pr = __floats2bfloat162_rn(a0, a1);   // .x (lower key) low
+                packed[h2] = *reinterpret_cast<const uint32_t*>(&pr);
+            }
+            float acc0, acc1;
+            upk2(acc2, acc0, acc1);
+            l += acc0 + acc1;
+            tmem_st16(s_addr + 32 * h + 16 * qc, packed);
+        }
+        release(h);
+    }
+    return true;
 }
 
 template <int D, bool kScored>
@@ -76,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
     if ((smem_u32(smem) & 1023u) != 0) {   // the swizzle counts address bits: a base elsewhere would scramble tiles
         if (threadIdx.x == 0) flag_status(p.ws, SPEC_EUNSUPPORTED);
         if (blockIdx.x == 0) {             // nothing to join
-            for (int b = threadIdx.x; b <= p.B; b += kThreads) p.cum[b] = 0;
-            if (threadIdx.x == 0) *reinterpret_cast<Plan*>(static_cast<unsigned char*>(p.ws) + kPlanOffset) = Plan{};
+            for (int b = threadIdx.x; b < p.B; b += kThreads) p.cum[b] = 0;
+            if (threadIdx.x == 0) *reinterpret_cast<Plan*>(static_cast<unsigned char*>(p.ws) + kPlanOffset) = Plan{0, 0, 0, 0x3fffffff, 0, 0};
         }
         return;
     }
@@ -89,15 +375,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
     uint64_t* o_final = bars + 2;
     uint64_t* o_empty = bars + 3;
     uint64_t* drain = bars + 4;
-    uint64_t* s_full = bars + 5;                  // [group]
-    uint64_t* p_full = bars + 7;                  // [group]
-    uint64_t* ml_full = bars + 9;                 // [group]
-    uint64_t* kv_full = bars + 11;                // [J % kFull]
+    uint64_t* s_full = bars + 5;                  // [group][buffer]
+    uint64_t* p_full = s_full + 4;                // [group][buffer]
+    uint64_t* ml_full = p_full + 4;               // [group]
+    uint64_t* pv_done = ml_full + 2;              // [group]
+    uint64_t* turn = pv_done + 2;                 // [group]
+    uint64_t* item_full = turn + 2;               // [slot]
+    uint64_t* item_empty = item_full + kItems;    // [slot]
+    uint64_t* kv_full = item_empty + kItems;      // [J % kFull]
     uint64_t* kv_empty = kv_full + C::kFull;      // [stage]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + C::kStages);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((11 + C::kFull + C::kStages) * 8 + 8 <= 256, "barriers and flags end before the exchange");
-    float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bars) + 256);   // [group][row]
+    static_assert(C::kBars * 8 + 8 <= 512, "barriers and flags end before the descriptors");
+    Desc* desc = reinterpret_cast<Desc*>(reinterpret_cast<uint8_t*>(bars) + 512);            // [slot]
+    float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bars) + C::kExchange); // [group][row]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -106,395 +397,405 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
         mbar_init(o_final, 2);
         mbar_init(o_empty, 8);
         mbar_init(drain, 2);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&ml_full[i], 4);
+            mbar_init(&pv_done[i], 1);
+            mbar_init(&turn[i], 1);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], 11);   // TMA, two MMA, eight softmax warps
         }
         for (int i = 0; i < C::kFull; ++i) mbar_init(&kv_full[i], 1);
-        for (int i = 0; i < C::kStages; ++i) mbar_init(&kv_empty[i], 1);
+        for (int i = 0; i < C::kStages; ++i) mbar_init(&kv_empty[i], 2);
         *abort_flag = 0;
         fence_mbar_init();
+        mbar_arrive(&turn[0]);   // thread 0 has the first turn
     }
     if (warp == 0) tmem_alloc(tmem_slot, kTmemCols);
-    const Plan plan = make_plan(p);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_launch();   // the join may start launching: it waits for the partials
-    if (blockIdx.x == 0 && warp == 7) publish_plan(p, plan);
 
-    const int tree_tiles = ceil_div(p.T, kKeys);
-    int J = 0;          // running tile number, the same in every role
+    int U = 0;          // running number of stage uses, the same in every role
     int n = 0;          // running item number
     bool ok = true;
     int q_loads = 0;    // (TMA) items whose Q was requested
+    // item n's descriptor; a whole warp
+    auto get_item = [&](Desc& it) -> bool {
+        if (!(ok = warp_wait(&item_full[n % kItems], (n / kItems) & 1, abort_flag))) return false;
+        it = desc[n % kItems];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[n % kItems]);
+        return it.valid != 0;
+    };
 
-    if (warp == 8) {
+    if (warp == 11) {
+        const Plan plan = make_plan(p);
+        if (blockIdx.x == 0) publish_plan(p, plan);
+        const int tree_tiles = ceil_div(p.T, kKeys);
+        Walk walk(p, plan, blockIdx.x);
+        for (;; ++n) {
+            Item it;
+            Desc d;
+            d.valid = walk.next(p, plan, it);
+            if (d.valid) {
+                d.shared = it.shared;
+                d.pair = it.rows > kRows;
+                d.direct = it.direct;
+                d.b = it.b; d.kvh = it.kvh; d.rb = it.rb; d.rows = it.rows;
+                d.first = it.shared ? plan.sT0 : own_first(p, it.L);
+                d.n_pre = it.shared ? plan.nS : own_tiles(p, it.L) - tree_tiles;
+                d.end = it.shared ? plan.Ls : it.L;
+                d.Ls = plan.Ls;
+                d.t0 = it.t0; d.tiles = it.t1 - it.t0; d.index = it.index; d.L = it.L;
+            }
+            if (n >= kItems && !(ok = warp_wait(&item_empty[n % kItems], ((n / kItems) - 1) & 1, abort_flag))) break;
+            if (lane == 0) {
+                desc[n % kItems] = d;
+                mbar_arrive(&item_full[n % kItems]);
+            }
+            if (!d.valid) break;
+        }
+    } else if (warp == 8) {
         const uint32_t q_bytes_own = static_cast<uint32_t>(p.rowsO) * 128 * C::kH;
         const uint32_t q_bytes_shared = static_cast<uint32_t>(p.rowsS) * 128 * C::kH;
         const int tree_rows = min(p.T, kKeys);
-        for (int id = blockIdx.x; ok && id < plan.items; id += gridDim.x, ++n) {
-            const Item it = find_item(p, plan, id);
-            const int first = it.shared ? plan.sT0 : own_first(p, it.L);
-            const int n_pre = it.shared ? plan.nS : own_tiles(p, it.L) - tree_tiles;
-            const int end = it.shared ? plan.Ls : it.L;
-            // Q once the last item's scores are done; from the second item on behind its first
-            // tile, whose stage frees without this item's Q
+        const bool paged = p.pg.table != nullptr;
+        Desc it;
+        for (; ok && get_item(it); ++n) {
+            // Q once the last item's scores are done; from the second item on behind the item's first
+            // load, whose stage frees without this item's Q
             auto load_q = [&]() -> bool {
                 if (n > 0 && !warp_wait(q_empty, (n - 1) & 1, abort_flag)) return false;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(q_full, it.shared ? q_bytes_shared : q_bytes_own);
                     for (int h = 0; h < C::kH; ++h)
-                        tma_load_4d(sQ + h * kHalf, it.shared ? &mp.q_shared : &mp.q_own, q_full, 64 * h, it.rb * kRows, it.kvh, it.b);
+                        tma_load_4d(sQ + h * kQHalf, it.shared ? &mp.q_shared : &mp.q_own, q_full, 64 * h, it.rb * kBlock, it.kvh, it.b);
                 }
                 q_loads = n + 1;
                 return true;
             };
             if (n == 0) load_q();
-            for (int t = it.t0; t < it.t1; ++t, ++J) {
-                const int s = J % C::kStages;
-                uint8_t* st = sKV + s * C::kStage;
-                uint64_t* bar = &kv_full[J % C::kFull];
-                const bool tree = !it.shared && t >= n_pre;
-                const int k0 = (tree ? t - n_pre : first + t) * kKeys;
-                // the lane's pool block, looked up while the stage is still in use
-                const bool paged = !tree && p.pg.table;
-                const int pieces = paged ? min(kKeys / page_rows, (end - k0 + page_rows - 1) / page_rows) : 0;
-                const int piece = lane >> 1;
+            const Tiles ts(it);
+            // paged: the lane's piece of the tile, one pool block's rows; narrow tiles take K and V by even and odd lanes
+            const int piece = it.pair ? lane : lane >> 1;
+            const int* table = it.shared ? p.shared_table : p.pg.table + static_cast<size_t>(it.b) * p.pg.max_blocks;
+            auto page_of = [&](int j) -> int {
+                if (!paged || j >= ts.pre) return 0;
+                const Tile tl(p, it, ts, j);
+                return piece * page_rows < tl.nvalid ? table[(tl.k0 + piece * page_rows) / p.pg.bs] : 0;
+            };
+            const int half = ts.width * kHalf;
+            int blk = page_of(0);
+            for (int j = 0; ok && j < ts.count; ++j) {
+                const Tile tl(p, it, ts, j);
+                const bool pieces = paged && !tl.tree;
+                const int blk_next = page_of(j + 1);   // looked up a tile ahead
                 int row = 0;
-                if (piece < pieces) {
-                    const int pos = k0 + piece * page_rows;
-                    int blk = it.shared ? p.shared_table[pos / p.pg.bs]
-                                        : p.pg.table[static_cast<size_t>(it.b) * p.pg.max_blocks + pos / p.pg.bs];
+                if (pieces && piece * page_rows < tl.nvalid) {
                     if (blk < 0 || blk >= p.pg.num_blocks) {
                         flag_status(p.ws, SPEC_EINVAL);
                         blk = 0;
                     }
-                    row = (blk * p.Hkv + it.kvh) * p.pg.bs + pos % p.pg.bs;
+                    row = (blk * p.Hkv + it.kvh) * p.pg.bs + (tl.k0 + piece * page_rows) % p.pg.bs;
                 }
-                if (J >= C::kStages && !(ok = warp_wait(&kv_empty[s], ((J / C::kStages) - 1) & 1, abort_flag))) break;
-                const int rows = paged ? pieces * page_rows : tree ? tree_rows : kKeys;
-                if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(rows) * 128 * C::kH * 2);
-                __syncwarp();
-                if (paged) {
-                    // lane = 2 piece + (K or V)
-                    if (piece < pieces) {
-                        uint8_t* dst = st + (lane & 1) * (C::kStage / 2) + piece * page_rows * 128;
-                        for (int h = 0; h < C::kH; ++h)
-                            tma_load_2d(dst + h * kHalf, lane & 1 ? &mp.vc : &mp.kc, bar, 64 * h, row);
+                const int box = pieces ? page_rows : tl.tree ? tree_rows : kKeys;
+                const int boxes = (tl.nvalid + box - 1) / box;
+                for (int part = 0; part < ts.width; ++part) {   // pair: K, then V
+                    const int s = U % C::kStages;
+                    uint8_t* st = sKV + s * C::kStage;
+                    uint64_t* bar = &kv_full[U % C::kFull];
+                    if (U >= C::kStages && !(ok = warp_wait(&kv_empty[s], ((U / C::kStages) - 1) & 1, abort_flag))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * box) * 128 * C::kH * (it.pair ? 1 : 2));
+                    __syncwarp();
+                    if (pieces) {
+                        if (piece * page_rows < tl.nvalid) {
+                            const int v = it.pair ? part : lane & 1;
+                            uint8_t* dst = st + (it.pair ? 0 : v * (C::kStage / 2)) + piece * page_rows * 128;
+                            for (int h = 0; h < C::kH; ++h) tma_load_2d(dst + h * half, v ? &mp.vc : &mp.kc, bar, 64 * h, row);
+                        }
+                    } else if (lane < 2 * C::kH && (!it.pair || lane / C::kH < boxes)) {
+                        // lane = (narrow: K or V; pair: 64 keys) * kH + half
+                        const int h = lane % C::kH, x = lane / C::kH;
+                        const int v = it.pair ? part : x;
+                        const CUtensorMap* m = tl.tree ? (v ? &mp.vt : &mp.kt) : it.shared ? (v ? &mp.vs : &mp.ks) : (v ? &mp.vc : &mp.kc);
+                        const int r0 = tl.tree ? (it.b * p.Hkv + it.kvh) * p.T
+                                               : it.shared ? it.kvh * p.Lshared : (it.b * p.Hkv + it.kvh) * p.Lmax;
+                        tma_load_2d(st + (it.pair ? x * kHalf : v * (C::kStage / 2)) + h * half, m, bar, 64 * h,
+                                    r0 + tl.k0 + (it.pair ? x * kKeys : 0));
                     }
-                } else if (lane < 2 * C::kH) {
-                    // lane = (K or V) * kH + half
-                    const int v = lane / C::kH, h = lane % C::kH;
-                    const CUtensorMap* m = tree ? (v ? &mp.vt : &mp.kt) : it.shared ? (v ? &mp.vs : &mp.ks) : (v ? &mp.vc : &mp.kc);
-                    const int r0 = tree ? (it.b * p.Hkv + it.kvh) * p.T : it.shared ? it.kvh * p.Lshared : (it.b * p.Hkv + it.kvh) * p.Lmax;
-                    tma_load_2d(st + v * (C::kStage / 2) + h * kHalf, m, bar, 64 * h, r0 + k0);
+                    ++U;
+                    if (n > 0 && j == 0 && part == 0 && !(ok = load_q())) break;
                 }
-                if (n > 0 && t == it.t0 && !(ok = load_q())) {
-                    ++J;
-                    break;
-                }
+                blk = blk_next;
             }
         }
     } else if (warp == 9 || warp == 10) {
         const int g = warp - 9;
-        const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
         const uint32_t idesc_o = idesc_bf16_f32_bmn(kRows, D);
-        const uint64_t qd = sdesc_k128(smem_u32(sQ));
-        const uint32_t sb = tmem + g * kKeys;             // this thread's score buffer
-        const uint32_t ob = tmem + kO + g * D;            // and its O
-        uint32_t p_phase = 0;
-        for (int id = blockIdx.x; ok && id < plan.items; id += gridDim.x, ++n) {
-            const Item it = find_item(p, plan, id);
-            const int first = it.shared ? plan.sT0 : own_first(p, it.L);
-            const int n_pre = it.shared ? plan.nS : own_tiles(p, it.L) - tree_tiles;
-            const int end = it.shared ? plan.Ls : it.L;
-            const int tiles = it.t1 - it.t0;
-            if (lane == 0) {
-                auto issue_s = [&](int j) -> bool {       // tile j of the item
-                    const int jj = J + j;
-                    if (!mbar_wait_or_abort(&kv_full[jj % C::kFull], (jj / C::kFull) & 1, abort_flag)) return false;
-                    tc_fence_after();
-                    const uint64_t kd = sdesc_k128(smem_u32(sKV + (jj % C::kStages) * C::kStage));
+        uint32_t p_phase = 0, t_phase = 0;                // bit b: phase of p_full[g][b]; of turn[g]
+        // S of the K tile in `stage` into column `dst`: Q block `block`; in a pair the turn goes
+        // to the other thread while the last products are still running
+        auto issue_s = [&](uint32_t dst, int block, int stage, int width) {
+            const uint64_t qd = sdesc_k128(smem_u32(sQ) + block * (kRows * 128));
+            const uint64_t kd = sdesc_k128(smem_u32(sKV + stage * C::kStage));
+            const uint32_t idesc_s = idesc_bf16_f32(kRows, width * kKeys);
+            const int half = width * kHalf;
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
-                        mma_bf16(sb, qd + (off >> 4), kd + (off >> 4), idesc_s, k > 0 ? 1u : 0u);
-                    }
-                    mma_commit(&s_full[g]);
-                    return true;
-                };
-                int j = (J & 1) == g ? 0 : 1;             // this thread's first tile
-                ok = mbar_wait_or_abort(q_full, n & 1, abort_flag);
-                if (ok && j < tiles) ok = issue_s(j);
-                bool q_done = false, o_clear = n == 0;
-                if (ok && j + 2 >= tiles) {               // no further S: the Q block may go
-                    mma_commit(q_empty);
-                    q_done = true;
+            for (int k = 0; k < D / 16; ++k)
+                mma_bf16(dst, qd + (((k >> 2) * kQHalf + (k & 3) * 32) >> 4), kd + (((k >> 2) * half + (k & 3) * 32) >> 4), idesc_s,
+                         k > 0 ? 1u : 0u);
+        };
+        auto pass_turn = [&]() { mbar_arrive(&turn[g ^ 1]); };
+        // O += P (column `src`) V (at v, halves `half` bytes apart) for keys 64 h .. of the tile, whole steps of 16
+        auto issue_pv = [&](uint32_t src, uint32_t v, int half, int h, int nvalid, bool first) {
+            const uint64_t vd = sdesc_mn128(v, half, 1024) + h * (kHalf >> 4);
+            const uint32_t o = tmem + kO + g * D;
+            src += h * (kKeys / 2);
+            nvalid -= h * kKeys;
+            if (nvalid >= kKeys) {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                    mma_bf16_ts(o, src + k * 8, vd + ((k * 2048) >> 4), idesc_o, (first && k == 0) ? 0u : 1u);
+            } else {
+#pragma unroll 1
+                for (int k = 0; k * 16 < nvalid; ++k)
+                    mma_bf16_ts(o, src + k * 8, vd + ((k * 2048) >> 4), idesc_o, (first && k == 0) ? 0u : 1u);
+            }
+        };
+        // landing barrier and stage of a stage use, kept as counters: no division per tile
+        struct Use {
+            int at, round;
+            __device__ __forceinline__ explicit Use(int u) : at(u % C::kFull), round((u / C::kFull) & 1) {}
+            __device__ __forceinline__ void two_on() {
+                at += 2;
+                if (at >= C::kFull) {
+                    at -= C::kFull;
+                    round ^= 1;
                 }
-                for (bool first_pv = true; ok && j < tiles; j += 2, first_pv = false) {
-                    const int jj = J + j, t = it.t0 + j;
-                    if (!(ok = mbar_wait_or_abort(&p_full[g], p_phase, abort_flag))) break;
-                    p_phase ^= 1u;
-                    if (!o_clear) {
-                        if (!(ok = mbar_wait_or_abort(o_empty, (n - 1) & 1, abort_flag))) break;
-                        o_clear = true;
+            }
+            __device__ __forceinline__ int stage() const { return at < C::kStages ? at : at - C::kStages; }
+        };
+        Desc it;
+        for (; ok && get_item(it); ++n) {
+            const Tiles ts(it);
+            if (lane == 0) {
+                auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && bounded_wait(bar, parity, abort_flag); };
+                auto wait_p = [&](int buf) {
+                    const bool r = wait(&p_full[2 * g + buf], (p_phase >> buf) & 1u);
+                    p_phase ^= 1u << buf;
+                    return r;
+                };
+                auto wait_turn = [&]() {
+                    const bool r = wait(&turn[g], t_phase);
+                    t_phase ^= 1u;
+                    return r;
+                };
+                wait(q_full, n & 1);
+                bool o_clear = n == 0;
+                auto clear_o = [&]() {                    // once in every item
+                    if (!o_clear) wait(o_empty, (n - 1) & 1);
+                    o_clear = true;
+                    return ok;
+                };
+                if (it.pair) {
+                    // The threads take turns, PV and the next S at a time: group 1's softmax then runs half a
+                    // period behind group 0's and each batch has the tensor pipe to itself.  Without turns the
+                    // batches share the pipe, both groups wait twice as long at the same time and then leave
+                    // it idle at the same time (2685 cycles per 128 x 128 scores); one thread issuing for both
+                    // leaves it idle in its waits and commits (1890).
+                    // Stages are released by the softmax groups: a group's S of its next tile complete says
+                    // that its products before it are, and a commit costs the issuing thread some 250 cycles.
+                    Use k_use(U), v_use(U + 1);
+                    if (wait(&kv_full[k_use.at], k_use.round) && wait_turn()) {
+                        tc_fence_after();
+                        issue_s(tmem + g * 128, g, k_use.stage(), 2);
+                        pass_turn();
+                        mma_commit(&s_full[2 * g]);
                     }
-                    tc_fence_after();
-                    // keys of the tile that any row can see: whole steps of 16
-                    const bool tree = !it.shared && t >= n_pre;
-                    const int nvalid = tree ? min(kKeys, p.T - (t - n_pre) * kKeys) : min(kKeys, end - (first + t) * kKeys);
-                    const int steps = (nvalid + 15) / 16;
-                    const uint64_t vd = sdesc_mn128(smem_u32(sKV + (jj % C::kStages) * C::kStage + C::kStage / 2), kHalf, 1024);
-                    if (steps == kKeys / 16) {
-#pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)
-                            mma_bf16_ts(ob, sb + k * 8, vd + ((k * 2048) >> 4), idesc_o, (first_pv && k == 0) ? 0u : 1u);
-                    } else {
-                        for (int k = 0; k < steps; ++k)
-                            mma_bf16_ts(ob, sb + k * 8, vd + ((k * 2048) >> 4), idesc_o, (first_pv && k == 0) ? 0u : 1u);
+                    for (int j = 0; ok && j < ts.count; ++j) {
+                        const bool more = j + 1 < ts.count;
+                        if (!more) mma_commit(q_empty);
+                        k_use.two_on();
+                        const int nvalid = Tile(p, it, ts, j).nvalid;
+                        if (!wait(&kv_full[v_use.at], v_use.round) || !clear_o()) break;
+                        if (more && !wait(&kv_full[k_use.at], k_use.round)) break;
+                        if (!wait_p(0) || !wait_turn()) break;
+                        tc_fence_after();
+                        issue_pv(tmem + g * 128, smem_u32(sKV + v_use.stage() * C::kStage), 2 * kHalf, 0, nvalid, j == 0);
+                        if (!wait_p(1)) break;
+                        tc_fence_after();
+                        issue_pv(tmem + g * 128, smem_u32(sKV + v_use.stage() * C::kStage), 2 * kHalf, 1, nvalid, false);
+                        if (more) issue_s(tmem + g * 128, g, k_use.stage(), 2);
+                        pass_turn();
+                        if (more) mma_commit(&s_full[2 * g]);
+                        v_use.two_on();
                     }
-                    mma_commit(&kv_empty[jj % C::kStages]);
-                    if (j + 2 < tiles && !(ok = issue_s(j + 2))) break;
-                    if (!q_done && j + 4 >= tiles) {
-                        mma_commit(q_empty);
-                        q_done = true;
+                } else {
+                    // thread g for group g: every second tile, the next one's S early where its K is there
+                    const int cnt = (ts.count - g + 1) / 2;
+                    Use s_use(U + g), v_use(U + g);
+                    if (cnt == 0) mma_commit(q_empty);
+                    int issued = 0, done = 0;
+                    while (ok && done < cnt) {
+                        if (issued == done || (issued < cnt && issued - done < 2 && mbar_try_wait(&kv_full[s_use.at], s_use.round))) {
+                            if (!wait(&kv_full[s_use.at], s_use.round)) break;
+                            tc_fence_after();
+                            const int buf = issued & 1;
+                            issue_s(tmem + g * 128 + buf * kKeys, 0, s_use.stage(), 1);
+                            mma_commit(&s_full[2 * g + buf]);
+                            s_use.two_on();
+                            if (++issued == cnt) mma_commit(q_empty);
+                            continue;
+                        }
+                        const int buf = done & 1;
+                        if (!wait_p(buf) || !clear_o()) break;
+                        tc_fence_after();
+                        issue_pv(tmem + g * 128 + buf * kKeys, smem_u32(sKV + v_use.stage() * C::kStage + C::kStage / 2), kHalf, 0,
+                                 Tile(p, it, ts, g + 2 * done).nvalid, done == 0);
+                        mma_commit(&kv_empty[v_use.stage()]);
+                        mma_commit(&pv_done[g]);
+                        v_use.two_on();
+                        ++done;
                     }
+                    clear_o();
                 }
                 if (ok) mma_commit(o_final);
             }
-            J += tiles;
+            U += ts.width * ts.count;
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
         if (lane == 0) mma_commit(drain);
         __syncwarp();
     } else {
         const int grp = warp >> 2;
-        const int r = (warp & 3) * 32 + lane;              // row of the block = TMEM lane
+        const int tl_row = (warp & 3) * 32 + lane;         // TMEM lane
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t s_col = grp * kKeys, o_col = kO + grp * D;
-        const float scale2 = p.scale * kLog2e;
-        const bool transformed = kScored && (p.softcap > 0.f || p.slopes);
-        const float cap2 = p.softcap * kLog2e, capin = p.softcap > 0.f ? 2.f * kLog2e * p.scale / p.softcap : 0.f;
-        const float in_scale = transformed ? 1.f : scale2;   // what the exponent's FFMA still multiplies by
-        uint32_t s_phase = 0;
-        for (int id = blockIdx.x; ok && id < plan.items; id += gridDim.x, ++n) {
-            const Item it = find_item(p, plan, id);
-            const int first = it.shared ? plan.sT0 : own_first(p, it.L);
-            const int n_pre = it.shared ? plan.nS : own_tiles(p, it.L) - tree_tiles;
-            const int end = it.shared ? plan.Ls : it.L;
-            const int tiles = it.t1 - it.t0;
+        const uint32_t s_base = lane_base + grp * 128, o_addr = lane_base + kO + grp * D;
+        uint32_t s_phase = 0, ml_phase = 0;                // bit b: phase of s_full[grp][b]
+        int narrow = 0;                                    // narrow tiles this group has finished
+        Desc it;
+        for (; ok && get_item(it); ++n) {
+            const Tiles ts(it);
+            const int r0 = it.pair ? grp * kRows : 0;
+            const int r = r0 + tl_row;                     // row of the block
             // the row: its place in gT, node, position, slope (rows past the block repeat its last)
-            const bool warp_in = (warp & 3) * 32 < it.rows;
+            const bool warp_in = r0 + (warp & 3) * 32 < it.rows;
             const bool in = r < it.rows;
             const int rr = min(r, it.rows - 1);
-            const int ib = p.gT < kRows ? rr / p.gT : 0;
-            const int i = p.gT < kRows ? rr - ib * p.gT : it.rb * kRows + rr;
+            const int ib = p.gT < kBlock ? rr / p.gT : 0;
+            const int i = p.gT < kBlock ? rr - ib * p.gT : it.rb * kBlock + rr;
             const int head = i / p.T, node = i - head * p.T;
-            int pos = 0;
-            float slope2 = 0.f;
-            if (kScored) {
-                pos = plan.Ls + own_len(p, it.b + ib) + p.depth[node];
-                if (p.slopes) slope2 = p.slopes[it.kvh * p.g + head] * kLog2e;
+            Row row{in, 0, 0.f, p.anc + static_cast<size_t>(node) * p.words};
+            if constexpr (kScored) {
+                row.pos = it.Ls + (it.shared ? own_len(p, it.b + ib) : it.L) + p.depth[node];
+                if (p.slopes) row.slope2 = p.slopes[it.kvh * p.g + head] * kLog2e;
             }
-            const uint64_t* anc_row = p.anc + static_cast<size_t>(node) * p.words;
             float m_used = -INFINITY, l = 0.f;
-            for (int j = (J & 1) == grp ? 0 : 1; j < tiles; j += 2) {
-                const int t = it.t0 + j;
-                const bool tree = !it.shared && t >= n_pre;
-                const int k0 = (tree ? t - n_pre : first + t) * kKeys;
-                const int nvalid = min(kKeys, (tree ? p.T : end) - k0);
-                if (!(ok = warp_wait(&s_full[grp], s_phase, abort_flag))) break;
-                s_phase ^= 1u;
-                tc_fence_after();
-                if (warp_in) {
-                    float sv[kKeys];
-                    {
-                        uint32_t s0[32], s1[32], s2[32], s3[32];
-                        tmem_ld32(lane_base + s_col, s0);
-                        tmem_ld32(lane_base + s_col + 32, s1);
-                        tmem_ld32(lane_base + s_col + 64, s2);
-                        tmem_ld32(lane_base + s_col + 96, s3);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            sv[e] = __uint_as_float(s0[e]);
-                            sv[e + 32] = __uint_as_float(s1[e]);
-                            sv[e + 64] = __uint_as_float(s2[e]);
-                            sv[e + 96] = __uint_as_float(s3[e]);
-                        }
+            for (int j = it.pair ? 0 : grp, k = 0; j < ts.count; j += it.pair ? 1 : 2, ++k) {
+                const Tile tl(p, it, ts, j);
+                const int buf = it.pair ? 0 : k & 1;
+                uint64_t* s_bar = &s_full[2 * grp + buf];
+                const uint32_t parity = (s_phase >> buf) & 1u;
+                s_phase ^= 1u << buf;
+                auto landed = [&]() -> bool {
+                    if (it.pair && (warp & 3) == 0 && lane == 0) {
+                        // the group's S of this tile and PV of the last one are complete: K and the last V may go
+                        mbar_arrive(&kv_empty[(U + 2 * j) % C::kStages]);
+                        if (j > 0) mbar_arrive(&kv_empty[(U + 2 * j - 1) % C::kStages]);
                     }
-                    const int kbase = it.shared ? k0 : plan.Ls + k0;   // position of the tile's first key (not the tree's)
-                    if (kScored) {
-                        if (p.softcap > 0.f) {
-                            // cap tanh(x / cap) = cap (1 - 2 / (2^(2 log2e x / cap) + 1))
-#pragma unroll
-                            for (int e = 0; e < kKeys; ++e) sv[e] = fmaf(-2.f * cap2, rcp(ex2(sv[e] * capin) + 1.f), cap2);
-                        } else if (p.slopes) {
-#pragma unroll
-                            for (int e = 0; e < kKeys; ++e) sv[e] *= scale2;
+                    if (tl.nvalid & 15) {
+                        // zero V from the last key to the end of its step of 16, once it has landed (narrow: with
+                        // K); of a pair's V both groups read all of it, and each zeroes before its own PV may start
+                        const int use = U + (it.pair ? 2 * j + 1 : j);
+                        if (it.pair && !warp_wait(&kv_full[use % C::kFull], (use / C::kFull) & 1, abort_flag)) return false;
+                        uint8_t* sv_tile = sKV + (use % C::kStages) * C::kStage + (it.pair ? 0 : C::kStage / 2);
+                        const int pad = 16 - (tl.nvalid & 15);
+                        for (int x = tl_row; x < pad * 8 * C::kH; x += kRows) {
+                            const int v_row = tl.nvalid + x / (8 * C::kH), y = x % (8 * C::kH);
+                            *reinterpret_cast<uint4*>(sv_tile + (y >> 3) * ts.width * kHalf + v_row * 128 + (y & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
                         }
-                        if (p.slopes) {
-                            if (tree) {
-                                const int lp = pos - plan.Ls - it.L;   // the node's depth
-#pragma unroll
-                                for (int e = 0; e < kKeys; ++e)
-                                    if (e < nvalid) sv[e] -= slope2 * static_cast<float>(lp - p.depth[k0 + e]);
-                            } else {
-                                const float b0 = slope2 * static_cast<float>(kbase - pos);
-#pragma unroll
-                                for (int e = 0; e < kKeys; ++e) sv[e] += fmaf(slope2, static_cast<float>(e), b0);
-                            }
-                        }
+                        fence_proxy_async_smem();
                     }
-                    // masks: whole tiles without one take the short way
-                    const int lo = kScored && p.window > 0 && !tree ? pos - p.window + 1 - kbase : 0;   // first key seen
-                    const bool windowed = kScored && p.window > 0 && (tree ? p.window <= SPEC_MAX_DEPTH : lo > 0);
-                    if (tree || nvalid < kKeys || __any_sync(0xffffffffu, windowed)) {
-                        uint64_t bits[2];
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            const int nv = min(max(nvalid - 64 * w, 0), 64);
-                            bits[w] = nv >= 64 ? ~0ull : ((1ull << nv) - 1ull);
-                            if (kScored && !tree) {
-                                const int nl = min(max(lo - 64 * w, 0), 64);
-                                bits[w] &= nl >= 64 ? 0ull : ~0ull << nl;
-                            }
-                        }
-                        if (tree) {   // only the node's ancestors and itself
-                            const int w0 = k0 >> 6;
-                            bits[0] &= anc_row[w0];
-                            bits[1] &= w0 + 1 < p.words ? anc_row[w0 + 1] : 0ull;
-                            if (windowed) {
-                                const int lp = pos - plan.Ls - it.L;
-#pragma unroll
-                                for (int w = 0; w < 2; ++w)
-                                    for (uint64_t left = bits[w]; left; left &= left - 1) {
-                                        const int e = __ffsll(static_cast<long long>(left)) - 1;
-                                        if (lp - p.depth[k0 + 64 * w + e] >= p.window) bits[w] &= ~(1ull << e);
-                                    }
-                            }
-                        }
-#pragma unroll
-                        for (int e = 0; e < kKeys; ++e)
-                            if (!((bits[e >> 6] >> (e & 63)) & 1ull)) sv[e] = -INFINITY;
-                    }
-                    float mx[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        mx[e] = fmax3(fmax3(sv[e], sv[e + 16], sv[e + 32]), fmax3(sv[e + 48], sv[e + 64], sv[e + 80]),
-                                      fmax3(sv[e + 96], sv[e + 112], -INFINITY));
-                    mx[0] = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmax3(mx[6], mx[7], mx[8]));
-                    mx[0] = fmax3(fmax3(mx[0], mx[9], mx[10]), fmax3(mx[11], mx[12], mx[13]), fmaxf(mx[14], mx[15]));
-                    const float tmax = mx[0] * in_scale;
-                    // the reference maximum moves only when the row's grew by more than 2^8; the TMEM
-                    // accesses are the whole warp's, so its rows rescale together (by 1 where nothing grew)
-                    float m_new = m_used, alpha = 1.f;
-                    bool rescale = false;
-                    if (tmax > m_used + 8.f) {
-                        if (m_used != -INFINITY) {
-                            rescale = true;
-                            alpha = ex2(m_used - tmax);
-                        }
-                        m_new = tmax;
-                    }
-                    if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t o[16];
-                            tmem_ld16(lane_base + o_col + c * 16, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st16(lane_base + o_col + c * 16, o);
-                        }
-                        l *= alpha;
-                    }
-                    m_used = m_new;
-                    const float nmref = m_used == -INFINITY ? 0.f : -m_used;
-                    const unsigned long long sc2 = pk2(in_scale, in_scale), nm2 = pk2(nmref, nmref);
-                    float ps[4];
-#pragma unroll
-                    for (int qc = 0; qc < 4; ++qc) {
-                        uint32_t packed[16];
-                        unsigned long long acc2 = pk2(0.f, 0.f);
-#pragma unroll
-                        for (int h2 = 0; h2 < 16; ++h2) {
-                            const int e0 = qc * 32 + 2 * h2;
-                            float x0, x1;
-                            upk2(ffma2(pk2(sv[e0], sv[e0 + 1]), sc2, nm2), x0, x1);
-                            const float a0 = ex2(x0), a1 = ex2(x1);
-                            acc2 = fadd2(acc2, pk2(a0, a1));
-                            const __nv_bfloat162 pr = __floats2bfloat162_rn(a0, a1);   // .x (lower key) low
-                            packed[h2] = *reinterpret_cast<const uint32_t*>(&pr);
-                        }
-                        float acc0, acc1;
-                        upk2(acc2, acc0, acc1);
-                        ps[qc] = acc0 + acc1;
-                        tmem_st16(lane_base + s_col + qc * 16, packed);
-                    }
-                    l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                    return true;
+                };
+                // a pair's halves go to PV one after the other: it starts while the second half is computed
+                auto release = [&](int h) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * grp + (it.pair ? h : buf)]);
+                };
+                ok = softmax_tile<D, kScored>(p, it, tl, row, ts.width, warp_in, s_base + buf * kKeys, o_addr, m_used, l, s_bar, parity,
+                                              it.pair ? nullptr : &pv_done[grp], (narrow - 1) & 1, abort_flag, landed, release);
+                if (!ok) break;
+                if (!it.pair) {
+                    // the stage's second arrival, beside PV's commit (a pair's come from both groups)
+                    if ((warp & 3) == 0 && lane == 0) mbar_arrive(&kv_empty[(U + j) % C::kStages]);
+                    ++narrow;
                 }
-                if (nvalid & 15) {
-                    // zero V from the last key to the end of its step of 16 (S_J complete: V_J has landed)
-                    uint8_t* sv_tile = sKV + ((J + j) % C::kStages) * C::kStage + C::kStage / 2;
-                    const int pad = 16 - (nvalid & 15);
-                    for (int x = (warp & 3) * 32 + lane; x < pad * 8 * C::kH; x += kRows) {
-                        const int row = nvalid + x / (8 * C::kH), c = x % (8 * C::kH);
-                        *reinterpret_cast<uint4*>(sv_tile + (c >> 3) * kHalf + row * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[grp]);
             }
             if (!ok) break;
-            // the item's end: (m, l) across the groups, then each group joins half the columns
+            // the item's end: in a pair each group has its rows' whole (m, l, O); otherwise (m, l)
+            // across the groups, then each joins half the columns
             if (!(ok = warp_wait(o_final, n & 1, abort_flag))) break;
             tc_fence_after();
-            ml[grp * kRows + r] = make_float2(m_used, l);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ml_full[grp]);
-            if (!(ok = warp_wait(&ml_full[grp ^ 1], n & 1, abort_flag))) break;
-            if (warp_in) {
-                const float2 other = ml[(grp ^ 1) * kRows + r];
-                const float m = fmaxf(m_used, other.x);
+            if (it.pair && (warp & 3) == 0 && lane == 0) mbar_arrive(&kv_empty[(U + 2 * ts.count - 1) % C::kStages]);
+            float m = m_used, lsum = l, a0 = 1.f, a1 = 0.f;   // weights of the group's own O and the other's
+            bool has_own = true, has_other = false;
+            if (!it.pair) {
+                ml[grp * kRows + tl_row] = make_float2(m_used, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ml_full[grp]);
+                if (!(ok = warp_wait(&ml_full[grp ^ 1], ml_phase, abort_flag))) break;
+                ml_phase ^= 1u;
+                const float2 other = ml[(grp ^ 1) * kRows + tl_row];
+                m = fmaxf(m_used, other.x);
                 const float ref = m == -INFINITY ? 0.f : m;
-                const float mine = ex2(m_used - ref), theirs = ex2(other.x - ref);
-                const float a0 = grp == 0 ? mine : theirs, a1 = grp == 0 ? theirs : mine;
-                const float lsum = mine * l + theirs * other.y;
-                const bool has0 = tiles > 1 || (J & 1) == 0, has1 = tiles > 1 || (J & 1) == 1;   // a group without a tile left O as it was
+                a0 = ex2(m_used - ref);
+                a1 = ex2(other.x - ref);
+                lsum = a0 * l + a1 * other.y;
+                has_own = ts.count > 1 || grp == 0;    // a group without a tile left O as it was
+                has_other = ts.count > 1 || grp == 1;
+            }
+            if (warp_in) {
                 const int stride = it.shared ? p.rowsS : p.rowsO;
-                float4* part = (it.shared ? p.part_s : p.part_o) + static_cast<size_t>(it.index) * (D / 4 + 1) * stride;
+                float4* part = (it.shared ? p.part_s : p.part_o) + static_cast<size_t>(it.index) * (D / 4 + 1) * stride + r;
                 const float inv = it.direct ? 1.f / lsum : 1.f;
-                const size_t row = row_of_q(p, it, rr);
-                if (in && grp == 0) {
-                    if (!it.direct) part[r] = make_float4(m, lsum, 0.f, 0.f);
-                    else if (p.lse) p.lse[row] = (m + log2f(lsum)) * kLn2;
+                const size_t q_row = (static_cast<size_t>(it.b + ib) * p.Hq + it.kvh * p.g) * p.T + i;
+                if (in && (it.pair || grp == 0)) {
+                    if (!it.direct) part[0] = make_float4(m, lsum, 0.f, 0.f);
+                    else if (p.lse) p.lse[q_row] = (m + log2f(lsum)) * kLn2;
                 }
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const int c0 = grp * (D / 2) + c * 32;
+                a0 *= inv;
+                a1 *= inv;
+                const int c_end = it.pair ? D : (grp + 1) * (D / 2);
+#pragma unroll 1
+                for (int c0 = it.pair ? 0 : grp * (D / 2); c0 < c_end; c0 += 32) {
                     uint32_t o0[32], o1[32];
-                    tmem_ld32(lane_base + kO + c0, o0);
-                    tmem_ld32(lane_base + kO + D + c0, o1);
+                    tmem_ld32(o_addr + c0, o0);
+                    if (has_other) tmem_ld32(lane_base + kO + (grp ^ 1) * D + c0, o1);
                     tmem_ld_wait();
                     float v[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const float x0 = has0 ? a0 * __uint_as_float(o0[e]) : 0.f;
-                        v[e] = (has1 ? fmaf(a1, __uint_as_float(o1[e]), x0) : x0) * inv;
+                        v[e] = has_own ? a0 * __uint_as_float(o0[e]) : 0.f;
+                        if (has_other) v[e] = fmaf(a1, __uint_as_float(o1[e]), v[e]);
                     }
                     if (in && !it.direct) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            part[static_cast<size_t>(1 + c0 / 4 + e) * stride + r] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                            part[static_cast<size_t>(1 + c0 / 4 + e) * stride] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     } else if (in) {
-                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * D + c0;
+                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + q_row * D + c0;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t w[4];
@@ -511,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_empty);
-            J += tiles;
+            U += ts.width * ts.count;
         }
     }
     if (!ok) {
@@ -526,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
     if (*abort_flag) {
         // a wait ran out: let this CTA's own loads and MMAs land before it ends
         if (warp == 8) {
-            for (int j = max(0, J - C::kFull); j < J; ++j) mbar_wait(&kv_full[j % C::kFull], (j / C::kFull) & 1, 100000000ull);
+            for (int j = max(0, U - C::kFull); j < U; ++j) mbar_wait(&kv_full[j % C::kFull], (j / C::kFull) & 1, 100000000ull);
             if (q_loads > 0) mbar_wait(q_full, (q_loads - 1) & 1, 100000000ull);
         }
         if ((warp == 9 || warp == 10) && lane == 0) mbar_wait(drain, 0, 100000000ull);
@@ -542,6 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
 
 template <int D, bool kScored>
 static spec_status launch_items(const Maps& m, const Params& p, int page_rows, int blocks, cudaStream_t s) {
+    static_assert(Cfg<D>::kSmem <= 232448, "shared memory of one CTA");
     auto kern = k_attn_shared_tc<D, kScored>;
     SPEC_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem));
     SPEC_CUDA_TRY(launch("attn_shared_tc", kern, dim3(blocks), dim3(kThreads), Cfg<D>::kSmem, s, m, p, page_rows));
@@ -552,7 +854,7 @@ spec_status attn_shared_tc_run(const Params& p, int blocks, cudaStream_t s) {
     Maps m;
     memset(&m, 0, sizeof(m));
     const uint64_t B = p.B, Hkv = p.Hkv, T = p.T, D = p.D;
-    const uint32_t b1 = static_cast<uint32_t>(std::min(p.gT, kRows));
+    const uint32_t b1 = static_cast<uint32_t>(std::min(p.gT, kBlock));
     SPEC_CUDA_TRY(make_tmap_bf16_4d(&m.q_own, p.q, B, Hkv, p.gT, D, 1, b1));
     SPEC_CUDA_TRY(make_tmap_bf16_2d(&m.kt, p.kt, B * Hkv * T, D, D, static_cast<uint32_t>(std::min(p.T, kKeys))));
     SPEC_CUDA_TRY(make_tmap_bf16_2d(&m.vt, p.vt, B * Hkv * T, D, D, static_cast<uint32_t>(std::min(p.T, kKeys))));
