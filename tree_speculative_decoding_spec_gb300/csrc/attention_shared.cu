@@ -24,7 +24,7 @@ namespace shr {
 // ---------------------------------------------------------------- CUDA-core items
 
 constexpr int FR = 64;   // rows of a block
-constexpr int FK = 64;   // keys of a tile
+constexpr int FK = kTile;   // keys of a tile
 
 // 256 threads; thread (rg, kg) = (t / 16, t % 16) holds rows 4 rg .. 4 rg + 3, keys
 // kg + 16 j of a tile and output columns 4 kg .. of each 64.  fp32 operands have no
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
             for (int e = 0; e < DT; ++e) o[ii][e] = 0.f;
         }
         const int first = it.shared ? plan.sT0 : own_first(p, it.L);
-        const int n_pre = it.shared ? plan.nS : own_tiles(p, it.L) - ceil_div(p.T, FK);
+        const int n_pre = it.shared ? plan.nS : own_tiles(p, it.L) - tiles_of(p.T);
         for (int tile = it.t0; tile < it.t1; ++tile) {
             const bool tree = !it.shared && tile >= n_pre;
             const int j0 = (tree ? tile - n_pre : first + tile) * FK;
@@ -295,7 +295,6 @@ HostPlan host_plan(Params& p, bool tc, bool shared, int ctas) {
     p.g = p.Hq / p.Hkv;
     p.gT = p.g * p.T;
     p.RB = tc ? kTcRows : FR;
-    p.KT = tc ? kTcKeys : FK;
     p.nbb = p.gT >= p.RB ? 1 : std::min(p.RB / p.gT, p.B);
     p.n_rbO = (p.gT + p.RB - 1) / p.RB;
     p.n_rbS = p.gT >= p.RB ? p.B * p.n_rbO : (p.B + p.nbb - 1) / p.nbb;

@@ -9,7 +9,7 @@
 //   shared  one (KV head, block of RB rows) against the shared keys; here a block
 //           holds the rows of as many whole sequences as fit (nbb of them), so
 //           that a shared key is read once for all of those
-// All columns' key tiles (KT keys each) are laid end to end, each column led by a few
+// All columns' key tiles (64 keys each) are laid end to end, each column led by a few
 // tiles for what an item costs beside its tiles, and the line is cut into equal parts,
 // one per CTA; a column that a cut crosses is that many items more.  So the CTAs finish
 // together, with one split per CTA more than there are columns (cutting every column
@@ -29,12 +29,13 @@ namespace shr {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-constexpr int kTcRows = 256, kTcKeys = 64;   // rows of a block and keys of a tile, tensor-core items
+constexpr int kTile = 64;       // keys of a tile
+constexpr int kTcRows = 256;    // rows of a block, tensor-core items
 
 struct Params {
     int B, T, g, gT, Hq, Hkv, D, words;
     int Lshared, Lmax;                 // capacities
-    int RB, KT;                        // rows of a block, keys of a tile
+    int RB;                            // rows of a block
     int nbb, n_rbO, n_rbS, rowsO, rowsS;
     int ctas;                          // parts of the line
     int fixS, fixO, min_piece;         // cost of an item beside its tiles (shared, own), in tiles; the shortest split
@@ -66,14 +67,17 @@ struct Plan {
 constexpr int kPlanOffset = 64;        // bytes into the workspace header
 static_assert(kPlanOffset + sizeof(Plan) <= kWsHeader, "the plan fits in the header");
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// A division is some forty instructions; the scheduling code runs once per item, cold, and its
+// length is what it costs.
+static __device__ __noinline__ int divide(int a, int b) { return a / b; }
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 
 // Tiles of sequence length L that its root (the node that looks furthest back) sees.
 __device__ __forceinline__ int own_first(const Params& p, int L) {
-    return p.window > 0 ? max(0, L - p.window + 1) / p.KT : 0;
+    return p.window > 0 ? max(0, L - p.window + 1) / kTile : 0;
 }
 __device__ __forceinline__ int own_tiles(const Params& p, int L) {   // with the tree's
-    return max(0, ceil_div(L, p.KT) - own_first(p, L)) + ceil_div(p.T, p.KT);
+    return max(0, tiles_of(L) - own_first(p, L)) + tiles_of(p.T);
 }
 __device__ __forceinline__ int own_len(const Params& p, int b) { return min(max(p.prefix_len[b], 0), p.Lmax); }
 
@@ -91,12 +95,12 @@ __device__ __forceinline__ Plan make_plan(const Params& p) {
     }
     Plan t;
     t.Ls = p.shared_len ? min(max(*p.shared_len, 0), p.Lshared) : 0;
-    t.sT0 = p.window > 0 ? max(0, t.Ls + least - p.window + 1) / p.KT : 0;
-    t.nS = max(0, ceil_div(t.Ls, p.KT) - t.sT0);
+    t.sT0 = p.window > 0 ? max(0, t.Ls + least - p.window + 1) / kTile : 0;
+    t.nS = max(0, tiles_of(t.Ls) - t.sT0);
     t.colsS = t.nS ? p.Hkv * p.n_rbS : 0;
     t.own0 = t.colsS * (t.nS + p.fixS);
     const int total = t.own0 + own * p.Hkv * p.n_rbO;
-    t.q = max(ceil_div(total, p.ctas), max(p.fixS, p.fixO) + p.min_piece);
+    t.q = max(divide(total + p.ctas - 1, p.ctas), max(p.fixS, p.fixO) + p.min_piece);
     return t;
 }
 
@@ -107,8 +111,8 @@ struct Cuts {
     int owner, count, base, q, n;
     __device__ __forceinline__ Cuts(const Params& p, int q_, int s, int fixed, int n_) : q(q_), n(n_) {
         base = s + fixed;                                            // place of the column's first tile
-        const int i0 = min(ceil_div(base + p.min_piece, q), p.ctas); // first cut
-        const int i1 = max(base + n - p.min_piece, 0) / q;           // last cut
+        const int i0 = min(divide(base + p.min_piece + q - 1, q), p.ctas); // first cut
+        const int i1 = divide(max(base + n - p.min_piece, 0), q);    // last cut
         owner = i0 - 1;
         count = max(0, i1 - i0 + 1) + 1;
     }
@@ -154,7 +158,7 @@ struct Walk {
     __device__ __forceinline__ Walk(const Params& p, const Plan& t, int cta_) : cta(cta_) {
         const int lane = threadIdx.x & 31;
         const int x = max(0, cta * t.q - max(p.fixS, p.fixO) - p.min_piece);   // no earlier column has an item here
-        colS = t.nS ? min(x / (t.nS + p.fixS), t.colsS) : 0;
+        colS = t.nS ? min(divide(x, t.nS + p.fixS), t.colsS) : 0;
         b = p.B;
         base = t.own0;
         col = 0;
@@ -175,7 +179,7 @@ struct Walk {
                 base += __shfl_sync(0xffffffffu, end - w, l);
                 L = __shfl_sync(0xffffffffu, Li, l);
                 n = __shfl_sync(0xffffffffu, ni, l);
-                col = max(0, x - base) / (n + p.fixO);
+                col = divide(max(0, x - base), n + p.fixO);
                 break;
             }
             base += __shfl_sync(0xffffffffu, end, 31);
@@ -187,11 +191,12 @@ struct Walk {
             const Cuts k(p, t.q, c * (t.nS + p.fixS), p.fixS, t.nS);
             if (k.owner > cta) return false;
             if (k.owner + k.count <= cta) continue;
-            const int sb = c % p.n_rbS, i = cta - k.owner;
+            const int i = cta - k.owner;
             it.shared = 1;
-            it.kvh = c / p.n_rbS;
-            it.b = p.gT >= p.RB ? sb / p.n_rbO : sb * p.nbb;
-            it.rb = p.gT >= p.RB ? sb % p.n_rbO : 0;
+            it.kvh = divide(c, p.n_rbS);
+            const int sb = c - it.kvh * p.n_rbS;
+            it.b = p.gT >= p.RB ? divide(sb, p.n_rbO) : sb * p.nbb;
+            it.rb = p.gT >= p.RB ? sb - it.b * p.n_rbO : 0;
             it.rows = p.gT >= p.RB ? min(p.RB, p.gT - it.rb * p.RB) : min(p.nbb, p.B - it.b) * p.gT;
             it.L = 0;
             it.t0 = k.begin(i);
@@ -218,8 +223,8 @@ struct Walk {
             it.shared = 0;
             it.b = b;
             it.L = L;
-            it.kvh = c / p.n_rbO;
-            it.rb = c % p.n_rbO;
+            it.kvh = divide(c, p.n_rbO);
+            it.rb = c - it.kvh * p.n_rbO;
             it.rows = min(p.RB, p.gT - it.rb * p.RB);
             it.t0 = k.begin(i);
             it.t1 = k.end(i);

@@ -50,7 +50,7 @@ using namespace tc;
 
 constexpr int kRows = 128;        // query rows of a group (MMA M)
 constexpr int kBlock = kTcRows;   // of a block: two groups
-constexpr int kKeys = kTcKeys;    // keys of a tile
+constexpr int kKeys = kTile;    // keys of a tile
 constexpr int kThreads = 384;
 constexpr int kItems = 4;         // item descriptors in flight
 constexpr int kQHalf = kBlock * 128;    // bytes of a 64-column half of the Q block
@@ -72,6 +72,14 @@ constexpr uint32_t kO = 256;
 struct Maps {
     CUtensorMap q_own, q_shared, kc, vc, ks, vs, kt, vt;
 };
+
+// One lane of the warp, the same at every call, as a condition the compiler knows to be uniform:
+// the issuing code around the products comes out a third shorter than behind lane == 0.
+__device__ __forceinline__ bool elected() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
 
 // What the roles need to know of an item, 64 bytes.
 struct Desc {
@@ -96,7 +104,10 @@ struct Tiles {
 struct Tile {
     bool tree;
     int k0, nvalid;          // first key (of the source's), keys that any row can see
-    __device__ __forceinline__ Tile(const Params& p, const Desc& it, const Tiles& ts, int j) {
+    // in the order they are worked off: from the item's end, where a bias by distance is largest (the
+    // other way a row's maximum grows, and O is rescaled, at every tile)
+    __device__ __forceinline__ Tile(const Params& p, const Desc& it, const Tiles& ts, int back) {
+        const int j = ts.count - 1 - back;
         tree = j >= ts.pre;
         const int first = tree ? max(it.t0 - it.n_pre, 0) + (j - ts.pre) * ts.width : it.first + it.t0 + j * ts.width;
         // a pair tile ends with the item's part of the column
@@ -108,7 +119,7 @@ struct Tile {
 
 // Wait for a phase, bounded (2 s, or another role's abort).  The clock is read only now and then:
 // most waits here are short, and reading it takes as long as they do.
-__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+static __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
     uint64_t t0 = 0;
     for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
         if ((i & 31u) == 0) {
@@ -118,6 +129,9 @@ __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, vol
         }
     }
     return true;
+}
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    return mbar_try_wait(bar, parity) || slow_wait(bar, parity, abort_flag);
 }
 // The same by a whole warp: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -168,10 +182,10 @@ __device__ __forceinline__ float max64(const float (&x)[64]) {
 }
 
 // cap2 tanh(s k) for 64 raw scores s, cap2 = softcap log2 e, k = scale / softcap.  Where the whole
-// warp's |s k| stay within 0.7 (caps sit far above ordinary scores) by tanh(u) = u (1 + u^2 P(u^2)):
-// P of degree 4 in u^2 fitted to the function on [0, 0.49] by weighted least squares, its weights
-// iterated towards an even relative error, 1.6e-8 at most; eight packed products for two scores,
-// on the FMA units that the softmax leaves idle.  Else as cap2 (1 - 2 / (e^(2u) + 1)), two
+// warp's |s k| stay small (caps sit far above ordinary scores) by tanh(u) = u (1 + u^2 P(u^2)): P of
+// degree 1 up to |u| = 0.16 and of degree 4 up to 0.7, fitted by weighted least squares whose
+// weights are iterated towards an even relative error, 3.5e-8 and 1.6e-8 at most; five and eight
+// packed products for two scores, on the FMA units that the softmax leaves idle.  Else as cap2 (1 - 2 / (e^(2u) + 1)), two
 // special-function operations a score, the pipe the exponentials need (a 128-key tile of the 32K
 // capped layer: 4000 cycles).  `in`: the lane's row is one of the
 // block, `whole`: so is every key: what stale memory made of others must not choose the way, or
@@ -183,12 +197,23 @@ __device__ __forceinline__ void cap64(float (&x)[64], float scale2, float k, flo
         a[e] = fmax3(fmax3(fabsf(x[e]), fabsf(x[e + 8]), fabsf(x[e + 16])), fmax3(fabsf(x[e + 24]), fabsf(x[e + 32]), fabsf(x[e + 40])),
                      fmaxf(fabsf(x[e + 48]), fabsf(x[e + 56])));
     const float most = fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7])) * k;
-    if (whole && k < 100.f && __all_sync(0xffffffffu, !in || most <= 0.7f)) {
-        const float z = k * k, z2 = z * z;
+    const float z = k * k, z2 = z * z;
+    const unsigned long long sc = pk2(scale2, scale2), zero = pk2(0.f, 0.f);
+    if (whole && k < 100.f && __all_sync(0xffffffffu, !in || most <= 0.16f)) {
+        const float c0 = -0.33331832037990994f * z, c1 = 0.13143139243852983f * z2;
+        const unsigned long long p0 = pk2(c0, c0), p1 = pk2(c1, c1);
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+            const unsigned long long v = pk2(x[e], x[e + 1]);
+            const unsigned long long w = ffma2(v, v, zero);
+            const unsigned long long q = ffma2(w, ffma2(w, p1, p0), zero);
+            const unsigned long long lin = ffma2(v, sc, zero);
+            upk2(ffma2(lin, q, lin), x[e], x[e + 1]);
+        }
+    } else if (whole && k < 100.f && __all_sync(0xffffffffu, !in || most <= 0.7f)) {
         const float c0 = -0.33333189899901133f * z, c1 = 0.13329110734967342f * z2, c2 = -0.053558861130687065f * z2 * z,
                     c3 = 0.02009196966007083f * z2 * z2, c4 = -0.005138661857974488f * z2 * z2 * z;
         const unsigned long long p0 = pk2(c0, c0), p1 = pk2(c1, c1), p2 = pk2(c2, c2), p3 = pk2(c3, c3), p4 = pk2(c4, c4);
-        const unsigned long long sc = pk2(scale2, scale2), zero = pk2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
             const unsigned long long v = pk2(x[e], x[e + 1]);
@@ -314,13 +339,12 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
         if (pv_bar && !warp_wait(pv_bar, pv_parity, abort_flag)) return false;
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld16(o_addr + c * 16, o);
-            tmem_ld_wait();
+        for (int c = 0; c < D; c += 64) {
+            float o[64];
+            load64(o_addr + c, o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st16(o_addr + c * 16, o);
+            for (int e = 0; e < 64; ++e) o[e] *= alpha;
+            store64(o_addr + c, o);
         }
         l *= alpha;
     }
@@ -439,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
     if (warp == 11) {
         const Plan plan = make_plan(p);
         if (blockIdx.x == 0) publish_plan(p, plan);
-        const int tree_tiles = ceil_div(p.T, kKeys);
+        const int tree_tiles = tiles_of(p.T);
         Walk walk(p, plan, blockIdx.x);
         for (;; ++n) {
             Item it;
@@ -488,9 +512,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
             const int piece = it.pair ? lane : lane >> 1;
             const int* table = it.shared ? p.shared_table : p.pg.table + static_cast<size_t>(it.b) * p.pg.max_blocks;
             auto page_of = [&](int j) -> int {
-                if (!paged || j >= ts.pre) return 0;
+                if (!paged || j >= ts.count) return 0;
                 const Tile tl(p, it, ts, j);
-                return piece * page_rows < tl.nvalid ? table[(tl.k0 + piece * page_rows) / p.pg.bs] : 0;
+                return !tl.tree && piece * page_rows < tl.nvalid ? table[(tl.k0 + piece * page_rows) / p.pg.bs] : 0;
             };
             const int half = ts.width * kHalf;
             int blk = page_of(0);
@@ -538,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
             }
         }
     } else if (warp == 9 || warp == 10) {
+        const bool leader = elected();
         const int g = warp - 9;
         const uint32_t idesc_o = idesc_bf16_f32_bmn(kRows, D);
         uint32_t p_phase = 0, t_phase = 0;                // bit b: phase of p_full[g][b]; of turn[g]
@@ -586,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
         Desc it;
         for (; ok && get_item(it); ++n) {
             const Tiles ts(it);
-            if (lane == 0) {
+            if (leader) {
                 auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && bounded_wait(bar, parity, abort_flag); };
                 auto wait_p = [&](int buf) {
                     const bool r = wait(&p_full[2 * g + buf], (p_phase >> buf) & 1u);
@@ -670,9 +695,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
                 if (ok) mma_commit(o_final);
             }
             U += ts.width * ts.count;
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            ok = __all_sync(0xffffffffu, ok);
         }
-        if (lane == 0) mma_commit(drain);
+        if (leader) mma_commit(drain);
         __syncwarp();
     } else {
         const int grp = warp >> 2;
@@ -830,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
             for (int j = max(0, U - C::kFull); j < U; ++j) mbar_wait(&kv_full[j % C::kFull], (j / C::kFull) & 1, 100000000ull);
             if (q_loads > 0) mbar_wait(q_full, (q_loads - 1) & 1, 100000000ull);
         }
-        if ((warp == 9 || warp == 10) && lane == 0) mbar_wait(drain, 0, 100000000ull);
+        if (warp == 9 || warp == 10) mbar_wait(drain, 0, 100000000ull);
     }
     __syncthreads();
     if (warp == 0) {
