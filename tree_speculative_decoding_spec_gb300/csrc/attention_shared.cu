@@ -216,74 +216,96 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
 
 // ---------------------------------------------------------------- the join
 
-// One CTA of four warps per (sequence, KV head, 32 rows of its gT): lane = row, each warp a
-// quarter of the columns, so the partials are read as whole 512-byte lines; the output goes
-// through shared memory to leave as whole rows.  Bound by reading the partials once.
+// One CTA of four warps per (sequence, KV head, 32 rows of its gT), each warp a quarter of the
+// columns.  Lanes are rows, so the partials are read as whole lines; with fewer than 32 rows the
+// lanes left over take other parts of the same rows (lane = part * R + row), and shuffles add
+// them up.  The output goes through shared memory to leave as whole rows.  Bound by reading the
+// partials once, and for few rows by the latency of the look-ups before that.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) k_attn_shared_join(const Params p, int n_rg) {
+__global__ void __launch_bounds__(128) k_attn_shared_join(const Params p, int n_rg, int R) {
     constexpr int C = D / 4 / 4;   // float4 columns per warp
     __shared__ T tile[32][D + 16 / sizeof(T)];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r0 = blockIdx.x % n_rg * 32, col = blockIdx.x / n_rg;
-    const int kvh = col % p.Hkv, b = col / p.Hkv;
-    const int i = r0 + lane;                      // row within gT
+    const int col = divide(blockIdx.x, n_rg), r0 = (blockIdx.x - col * n_rg) * 32;
+    const int b = divide(col, p.Hkv), kvh = col - b * p.Hkv;
+    const int lr = lane & (R - 1), sub = divide(lane, R), subs = divide(32, R);
+    const int i = r0 + lr;                        // row within gT
+    const int n = own_tiles(p, own_len(p, b));
     griddep_wait();
     const Plan t = *reinterpret_cast<const Plan*>(static_cast<unsigned char*>(p.ws) + kPlanOffset);
-    const int rb = r0 / p.RB;                     // 32 divides RB
-    const int sb = p.gT >= p.RB ? b * p.n_rbO + rb : b / p.nbb;
+    const int rb = divide(r0, p.RB);              // 32 divides RB
+    const int sb = p.gT >= p.RB ? b * p.n_rbO + rb : divide(b, p.nbb);
     const int colS = kvh * p.n_rbS + sb, colO = kvh * p.n_rbO + rb, cols = p.Hkv * p.n_rbO;
-    const int n = own_tiles(p, own_len(p, b));
-    const Cuts kO(p, t.q, p.cum[b] + colO * (n + p.fixO), p.fixO, n), kS(p, t.q, colS * (t.nS + p.fixS), p.fixS, t.nS);
-    const int nsS = t.nS ? kS.count : 0, nsO = kO.count;
-    if (nsS + nsO == 1) return;                   // written by its item
-    const int rS = p.gT >= p.RB ? i % p.RB : (b % p.nbb) * p.gT + i;
-    const int rO = i % p.RB;
+    const Cuts kO(p, t.q, Place(p, false, n), p.cum[b], colO, p.n_rbO), kS(p, t.q, Place(p, true, t.nS), 0, colS, p.per);
+    const int nsS = (t.nS ? kS.count : 0) * p.repS, parts = nsS + kO.count * p.repO;
+    if (parts == 1) return;                       // written by its item
+    const int rO = i - rb * p.RB, rS = p.gT >= p.RB ? rO : (b - sb * p.nbb) * p.gT + i;
     const bool in = i < p.gT;
-    const size_t strideS = static_cast<size_t>(D / 4 + 1) * p.rowsS, strideO = static_cast<size_t>(D / 4 + 1) * p.rowsO;
-    auto ps = [&](int k) { return p.part_s + kS.slot(colS, p.Hkv * p.n_rbS, k) * strideS + rS; };
-    auto po = [&](int k) { return p.part_o + kO.slot(b * cols + colO, p.B * cols, k) * strideO + rO; };
-    float M = -INFINITY;
-    if (in) {
-        for (int k = 0; k < nsS; ++k) M = fmaxf(M, ps(k)->x);
-        for (int k = 0; k < nsO; ++k) M = fmaxf(M, po(k)->x);
-    }
-    const float ref = M == -INFINITY ? 0.f : M;
-    float l = 0.f;
+    // part k: of the shared items, then of the own ones; item k / rep, copy k % rep (1 or 4)
+    auto part = [&](int k, int& rows) -> const float4* {
+        const bool shared = k < nsS;
+        const int rep = shared ? p.repS : p.repO, cap = shared ? p.rowsS : p.rowsO;
+        const int x = shared ? k : k - nsS, item = rep == 1 ? x : x >> 2, copy = rep == 1 ? 0 : x & 3;
+        const int slot = shared ? kS.slot(colS, p.Hkv * p.n_rbS, item) : kO.slot(b * cols + colO, p.B * cols, item);
+        rows = cap * rep;
+        return (shared ? p.part_s : p.part_o) + static_cast<size_t>(slot) * (D / 4 + 1) * rows + copy * cap + (shared ? rS : rO);
+    };
+    float M = -INFINITY, l = 0.f;
     float4 acc[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float4* base, int rows) {
-        const float4 h = base[0];
-        const float w = exp2f(h.x - ref);
-        // a split in which the row saw nothing (one of NaN scores alone has a NaN sum, and counts)
-        if (h.x == -INFINITY && h.y == 0.f) return;
-        l += w * h.y;
+    if (in) {
+        for (int k = sub; k < parts; k += subs) {
+            int rows;
+            const float4* base = part(k, rows);
+            const float4 h = base[0];
+            float4 v[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) v[c] = base[static_cast<size_t>(1 + warp * C + c) * rows];
+            // a part in which the row saw nothing (one of NaN scores alone has a NaN sum, and counts)
+            if (h.x == -INFINITY && h.y == 0.f) continue;
+            const float m = fmaxf(M, h.x), ref = m == -INFINITY ? 0.f : m;
+            const float keep = exp2f(M - ref), w = exp2f(h.x - ref);
+            M = m;
+            l = l * keep + w * h.y;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                acc[c].x = acc[c].x * keep + w * v[c].x; acc[c].y = acc[c].y * keep + w * v[c].y;
+                acc[c].z = acc[c].z * keep + w * v[c].z; acc[c].w = acc[c].w * keep + w * v[c].w;
+            }
+        }
+    }
+    for (int o = R; o < 32; o <<= 1) {            // the lanes of the same row
+        const float M2 = __shfl_xor_sync(0xffffffffu, M, o), m = fmaxf(M, M2), ref = m == -INFINITY ? 0.f : m;
+        const float keep = exp2f(M - ref), w = exp2f(M2 - ref);
+        M = m;
+        const float l2 = __shfl_xor_sync(0xffffffffu, l, o);
+        l = l * keep + l2 * w;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const float4 v = base[static_cast<size_t>(1 + warp * C + c) * rows];
-            acc[c].x += w * v.x; acc[c].y += w * v.y; acc[c].z += w * v.z; acc[c].w += w * v.w;
+            const float4 a2 = make_float4(__shfl_xor_sync(0xffffffffu, acc[c].x, o), __shfl_xor_sync(0xffffffffu, acc[c].y, o),
+                                          __shfl_xor_sync(0xffffffffu, acc[c].z, o), __shfl_xor_sync(0xffffffffu, acc[c].w, o));
+            acc[c].x = acc[c].x * keep + a2.x * w; acc[c].y = acc[c].y * keep + a2.y * w;
+            acc[c].z = acc[c].z * keep + a2.z * w; acc[c].w = acc[c].w * keep + a2.w * w;
         }
-    };
-    if (in) {
-        for (int k = 0; k < nsS; ++k) add(ps(k), p.rowsS);
-        for (int k = 0; k < nsO; ++k) add(po(k), p.rowsO);
     }
     const float inv = 1.f / l;
+    if (sub == 0) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        T* d = &tile[lane][(warp * C + c) * 4];
-        d[0] = from_f32<T>(acc[c].x * inv); d[1] = from_f32<T>(acc[c].y * inv);
-        d[2] = from_f32<T>(acc[c].z * inv); d[3] = from_f32<T>(acc[c].w * inv);
+        for (int c = 0; c < C; ++c) {
+            T* d = &tile[lr][(warp * C + c) * 4];
+            d[0] = from_f32<T>(acc[c].x * inv); d[1] = from_f32<T>(acc[c].y * inv);
+            d[2] = from_f32<T>(acc[c].z * inv); d[3] = from_f32<T>(acc[c].w * inv);
+        }
     }
     const size_t row0 = (static_cast<size_t>(b) * p.Hq + kvh * p.g) * p.T + r0;
-    if (in && warp == 0 && p.lse) p.lse[row0 + lane] = (M + log2f(l)) * kLn2;
+    if (in && sub == 0 && warp == 0 && p.lse) p.lse[row0 + lr] = (M + log2f(l)) * kLn2;
     __syncthreads();
     constexpr int E = 16 / sizeof(T);
-    for (int x = threadIdx.x; x < 32 * (D / E); x += 128) {
+    const int rows = min(32, p.gT - r0);
+    for (int x = threadIdx.x; x < rows * (D / E); x += 128) {
         const int r = x / (D / E), c = x % (D / E);
-        if (r0 + r < p.gT)
-            *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (row0 + r) * D + c * E) =
-                *reinterpret_cast<const uint4*>(&tile[r][c * E]);
+        *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (row0 + r) * D + c * E) = *reinterpret_cast<const uint4*>(&tile[r][c * E]);
     }
 }
 
@@ -301,16 +323,28 @@ HostPlan host_plan(Params& p, bool tc, bool shared, int ctas) {
     p.rowsO = std::min(p.gT, p.RB);
     p.rowsS = p.nbb * p.rowsO;
     p.ctas = ctas;
-    p.fixS = tc ? (p.rowsS > 128 ? 5 : 3) : 2;
-    p.fixO = tc ? (p.rowsO > 128 ? 5 : 3) : 2;
-    p.min_piece = 4;
+    p.per = p.gT >= p.RB ? p.n_rbO : 1;
+    // costs in thirds of a pair's tile (1820 cycles): a narrow tile is bound by memory or by its
+    // softmax at two thirds of that, an item's rows take some 8000 or 5500 cycles to start and store
+    const int last = p.gT - (p.n_rbO - 1) * p.RB;
+    p.wF = 3;
+    p.fixF = tc ? 15 : 6;
+    auto cost = [&](int rows, int& w, int& fix) {
+        w = tc && rows <= kTcRows / 2 ? 2 : 3;
+        fix = tc ? (w == 3 ? 15 : 10) : 6;
+    };
+    cost(p.gT >= p.RB ? last : p.rowsS, p.wS, p.fixS);
+    cost(last, p.wO, p.fixO);
+    p.repS = tc && p.rowsS <= 32 ? 4 : 1;
+    p.repO = tc && p.rowsO <= 32 ? 4 : 1;
+    p.min_piece = 2;
     const size_t per_row = sizeof(float) * (p.D + 4);
     const size_t items_s = shared ? static_cast<size_t>(p.Hkv) * p.n_rbS + ctas : 0;   // one slot per column and per cut
     const size_t items_o = static_cast<size_t>(p.B) * p.Hkv * p.n_rbO + ctas;
     h.cum_off = kWsHeader;
     h.part_s_off = h.cum_off + round_up(sizeof(int32_t) * static_cast<size_t>(p.B), 256);
-    h.part_o_off = h.part_s_off + round_up(items_s * p.rowsS * per_row, 256);
-    h.total = h.part_o_off + round_up(items_o * p.rowsO * per_row, 256);
+    h.part_o_off = h.part_s_off + round_up(items_s * p.rowsS * p.repS * per_row, 256);
+    h.total = h.part_o_off + round_up(items_o * p.rowsO * p.repO * per_row, 256);
     return h;
 }
 
@@ -324,9 +358,9 @@ static spec_status check_shapes(const spec_tree* t, int B, int Hq, int Hkv, int 
     if (Lmax < 1 || Lmax > (1 << 22)) return fail(SPEC_EINVAL, "Lmax = %d out of 1..2^22", Lmax);
     if (Ls < 0 || Ls > (1 << 22)) return fail(SPEC_EINVAL, "the shared capacity %d is out of 1..2^22", Ls);
     const int64_t rows = static_cast<int64_t>(B) * Hq * t->T;
-    // 64-key tiles of all columns, each at most 64 rows high and a few tiles of fixed cost longer
+    // the line's length, were every block 64 rows high
     const int64_t blocks = static_cast<int64_t>(Hkv) * ((static_cast<int64_t>(Hq / Hkv) * t->T + FR - 1) / FR);
-    const int64_t line = blocks * B * ((Lmax + 63) / 64 + (t->T + 63) / 64 + (Ls + 63) / 64 + 16);
+    const int64_t line = 3 * blocks * B * ((Lmax + 63) / 64 + (t->T + 63) / 64 + (Ls + 63) / 64 + 8);
     if (line > INT32_MAX / 2) return fail(SPEC_EINVAL, "B * Hkv * (Lmax + the shared capacity) is too large for one call (%lld tiles)", static_cast<long long>(line));
     if (rows > (1ll << 30)) return fail(SPEC_EINVAL, "B * Hq * T = %lld query rows exceed 2^30", static_cast<long long>(rows));
     return SPEC_OK;
@@ -356,9 +390,11 @@ static spec_status run_fma(const Params& p, cudaStream_t s) {
 template <typename T>
 static spec_status join(const Params& p, cudaStream_t s) {
     const int n_rg = (p.gT + 31) / 32;
+    int R = 1;   // rows a CTA joins, a power of two
+    while (R < 32 && R < p.gT) R *= 2;
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.Hkv * n_rg));
     SPEC_CUDA_TRY(launch_ex("attn_shared_join", p.D == 64 ? k_attn_shared_join<T, 64> : k_attn_shared_join<T, 128>, grid,
-                            dim3(128), 0, s, true, p, n_rg));
+                            dim3(128), 0, s, true, p, n_rg, R));
     return SPEC_OK;
 }
 

@@ -9,9 +9,9 @@
 //   shared  one (KV head, block of RB rows) against the shared keys; here a block
 //           holds the rows of as many whole sequences as fit (nbb of them), so
 //           that a shared key is read once for all of those
-// All columns' key tiles (64 keys each) are laid end to end, each column led by a few
-// tiles for what an item costs beside its tiles, and the line is cut into equal parts,
-// one per CTA; a column that a cut crosses is that many items more.  So the CTAs finish
+// All columns' key tiles (64 keys each) are laid end to end, each as long as its cost, each
+// column led by what an item costs beside its tiles, and the line is cut into equal
+// parts, one per CTA; a column that a cut crosses is that many items more.  So the CTAs finish
 // together, with one split per CTA more than there are columns (cutting every column
 // into equal splits left the last round of them part empty: 306 tiles on the longest of
 // 152 CTAs where the mean was 233).  The cut follows the lengths, which only the device
@@ -38,7 +38,11 @@ struct Params {
     int RB;                            // rows of a block
     int nbb, n_rbO, n_rbS, rowsO, rowsS;
     int ctas;                          // parts of the line
-    int fixS, fixO, min_piece;         // cost of an item beside its tiles (shared, own), in tiles; the shortest split
+    int per;                           // blocks of one sequence's rows a shared column may be one of (1 when it holds whole sequences)
+    // a tile's cost and an item's beside its tiles: blocks with more rows behind them, the last (or only) one
+    int wF, wS, wO, fixF, fixS, fixO;
+    int min_piece;                     // tiles of the shortest split
+    int repS, repO;                    // copies of a row in an item (see attention_shared_tc.cu)
     float scale, softcap;              // softcap 0: none
     int window;                        // 0: none
     const float* slopes;               // [Hq] or NULL
@@ -59,7 +63,7 @@ struct Params {
 struct Plan {
     int Ls;          // shared keys
     int sT0, nS;     // first shared tile any row sees, and how many from there
-    int q;           // tiles of a CTA's part of the line
+    int q;           // length of a CTA's part of the line
     int colsS;       // shared columns on the line
     int own0;        // place of the own columns
 };
@@ -81,12 +85,24 @@ __device__ __forceinline__ int own_tiles(const Params& p, int L) {   // with the
 }
 __device__ __forceinline__ int own_len(const Params& p, int b) { return min(max(p.prefix_len[b], 0), p.Lmax); }
 
+// Place of column c (of those with `per` blocks to a group of rows) relative to the first, n tiles each.
+struct Place {
+    int full, group;   // length of a full block's column; of a group
+    int w, fix, n;     // of the last block's
+    __device__ __forceinline__ Place(const Params& p, bool shared, int n_) : n(n_) {
+        w = shared ? p.wS : p.wO;
+        fix = shared ? p.fixS : p.fixO;
+        full = n * p.wF + p.fixF;
+        group = ((shared ? p.per : p.n_rbO) - 1) * full + n * w + fix;
+    }
+};
+
 // A whole warp works out the plan (every lane gets it).
 __device__ __forceinline__ Plan make_plan(const Params& p) {
     int own = 0, least = 0x7fffffff;
     for (int b = threadIdx.x & 31; b < p.B; b += 32) {
         const int L = own_len(p, b);
-        own += own_tiles(p, L) + p.fixO;
+        own += Place(p, false, own_tiles(p, L)).group;
         least = min(least, L);
     }
     for (int o = 16; o > 0; o >>= 1) {
@@ -98,26 +114,30 @@ __device__ __forceinline__ Plan make_plan(const Params& p) {
     t.sT0 = p.window > 0 ? max(0, t.Ls + least - p.window + 1) / kTile : 0;
     t.nS = max(0, tiles_of(t.Ls) - t.sT0);
     t.colsS = t.nS ? p.Hkv * p.n_rbS : 0;
-    t.own0 = t.colsS * (t.nS + p.fixS);
-    const int total = t.own0 + own * p.Hkv * p.n_rbO;
-    t.q = max(divide(total + p.ctas - 1, p.ctas), max(p.fixS, p.fixO) + p.min_piece);
+    t.own0 = t.nS ? Place(p, true, t.nS).group * p.Hkv * divide(p.n_rbS, p.per) : 0;
+    const int total = t.own0 + own * p.Hkv;
+    t.q = max(divide(total + p.ctas - 1, p.ctas), p.fixF + 3 * p.min_piece);
     return t;
 }
 
-// The items of the column of n tiles whose place on the line is s: the line is cut at multiples of
-// q, save where less than min_piece tiles of the column would be left on one side.  Item k
-// belongs to CTA owner + k.
+// The items of column c of those with n tiles, `first` the place of column 0: the line is cut at
+// multiples of q, save where less than min_piece tiles of the column would be left on one side.
+// Item k belongs to CTA owner + k.
 struct Cuts {
-    int owner, count, base, q, n;
-    __device__ __forceinline__ Cuts(const Params& p, int q_, int s, int fixed, int n_) : q(q_), n(n_) {
-        base = s + fixed;                                            // place of the column's first tile
-        const int i0 = min(divide(base + p.min_piece + q - 1, q), p.ctas); // first cut
-        const int i1 = divide(max(base + n - p.min_piece, 0), q);    // last cut
+    int owner, count, base, q, w, n;
+    __device__ __forceinline__ Cuts(const Params& p, int q_, const Place& pl, int first, int c, int per) : q(q_), n(pl.n) {
+        const int g = per == 1 ? c : divide(c, per), r = c - g * per;
+        const bool last = r == per - 1;
+        w = last ? pl.w : p.wF;
+        base = first + g * pl.group + r * pl.full + (last ? pl.fix : p.fixF);      // place of the column's first tile
+        const int i0 = min(divide(base + p.min_piece * w + q - 1, q), p.ctas);      // first cut
+        const int i1 = divide(max(base + (n - p.min_piece) * w, 0), q);             // last cut
         owner = i0 - 1;
         count = max(0, i1 - i0 + 1) + 1;
     }
-    __device__ __forceinline__ int begin(int k) const { return k == 0 ? 0 : (owner + k) * q - base; }
-    __device__ __forceinline__ int end(int k) const { return k == count - 1 ? n : (owner + k + 1) * q - base; }
+    __device__ __forceinline__ int tile(int place) const { return w == 3 ? (place - base) / 3 : w == 2 ? (place - base) / 2 : place - base; }
+    __device__ __forceinline__ int begin(int k) const { return k == 0 ? 0 : tile((owner + k) * q); }
+    __device__ __forceinline__ int end(int k) const { return k == count - 1 ? n : tile((owner + k + 1) * q); }
     // the workspace slot among `cols` columns: one per column, one per cut of the line
     __device__ __forceinline__ int slot(int col, int cols, int k) const { return k == 0 ? col : cols + owner + k; }
 };
@@ -128,7 +148,7 @@ __device__ __forceinline__ void publish_plan(const Params& p, const Plan& t) {
     int before = t.own0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
-        const int n = b < p.B ? (own_tiles(p, own_len(p, b)) + p.fixO) * p.Hkv * p.n_rbO : 0;
+        const int n = b < p.B ? Place(p, false, own_tiles(p, own_len(p, b))).group * p.Hkv : 0;
         int at = n;
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, at, o);
@@ -157,8 +177,8 @@ struct Walk {
     int b, base, col, L, n;    // next own column: sequence, place of its first column, column, keys, tiles
     __device__ __forceinline__ Walk(const Params& p, const Plan& t, int cta_) : cta(cta_) {
         const int lane = threadIdx.x & 31;
-        const int x = max(0, cta * t.q - max(p.fixS, p.fixO) - p.min_piece);   // no earlier column has an item here
-        colS = t.nS ? min(divide(x, t.nS + p.fixS), t.colsS) : 0;
+        const int x = max(0, cta * t.q - p.fixF - 3 * p.min_piece);   // no earlier column has an item here
+        colS = t.nS ? min(divide(x, Place(p, true, t.nS).group) * p.per, t.colsS) : 0;
         b = p.B;
         base = t.own0;
         col = 0;
@@ -166,7 +186,7 @@ struct Walk {
             const int i = b0 + lane;
             const int Li = i < p.B ? own_len(p, i) : 0;
             const int ni = i < p.B ? own_tiles(p, Li) : 0;
-            const int w = i < p.B ? (ni + p.fixO) * p.Hkv * p.n_rbO : 0;
+            const int w = i < p.B ? Place(p, false, ni).group * p.Hkv : 0;
             int end = w;
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, end, o);
@@ -179,7 +199,7 @@ struct Walk {
                 base += __shfl_sync(0xffffffffu, end - w, l);
                 L = __shfl_sync(0xffffffffu, Li, l);
                 n = __shfl_sync(0xffffffffu, ni, l);
-                col = divide(max(0, x - base), n + p.fixO);
+                col = divide(max(0, x - base), Place(p, false, n).group) * p.n_rbO;
                 break;
             }
             base += __shfl_sync(0xffffffffu, end, 31);
@@ -188,7 +208,7 @@ struct Walk {
     __device__ __forceinline__ bool next(const Params& p, const Plan& t, Item& it) {
         for (; colS < t.colsS;) {
             const int c = colS++;
-            const Cuts k(p, t.q, c * (t.nS + p.fixS), p.fixS, t.nS);
+            const Cuts k(p, t.q, Place(p, true, t.nS), 0, c, p.per);
             if (k.owner > cta) return false;
             if (k.owner + k.count <= cta) continue;
             const int i = cta - k.owner;
@@ -208,7 +228,7 @@ struct Walk {
         const int cols = p.Hkv * p.n_rbO;
         while (b < p.B) {
             if (col == cols) {
-                base += cols * (n + p.fixO);
+                base += p.Hkv * Place(p, false, n).group;
                 col = 0;
                 if (++b == p.B) break;
                 L = own_len(p, b);
@@ -216,7 +236,7 @@ struct Walk {
                 continue;
             }
             const int c = col++;
-            const Cuts k(p, t.q, base + c * (n + p.fixO), p.fixO, n);
+            const Cuts k(p, t.q, Place(p, false, n), base, c, p.n_rbO);
             if (k.owner > cta) return false;
             if (k.owner + k.count <= cta) continue;
             const int i = cta - k.owner;
@@ -229,7 +249,7 @@ struct Walk {
             it.t0 = k.begin(i);
             it.t1 = k.end(i);
             it.index = k.slot(b * cols + c, p.B * cols, i);
-            it.direct = t.nS == 0 && k.count == 1;
+            it.direct = t.nS == 0 && k.count == 1 && p.repO == 1;
             return true;
         }
         return false;

@@ -19,6 +19,11 @@
 //     alternate 64-key tiles; each group has two score buffers, so that S of its next tile
 //     runs while it works on this one, and small tiles keep more loads in flight.  At the
 //     item's end the groups exchange (max, sum) and each joins half the columns of both O.
+//     At most 32 rows (single tokens above all) are there four times, once for each warp's
+//     TMEM lanes: warp w takes keys 16 w .. of a tile, weights of the others stay zero in
+//     its lanes, and each copy leaves its own (max, sum, O).  A warp's chain per tile is
+//     that of 16 scores instead of 64 with three warps idle (1900 cycles, more than a
+//     tile takes to arrive).
 // Per tile and group: S = Q K^T into the group's score buffer; the softmax thread reads
 // its row, transforms and masks it, keeps the running maximum and sum in base 2 and 32
 // bits and writes P as bf16 pairs over the first half of the buffer; O += P V with P read
@@ -121,8 +126,8 @@ struct Tile {
 // most waits here are short, and reading it takes as long as they do.
 static __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
     uint64_t t0 = 0;
-    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-        if ((i & 31u) == 0) {
+    for (uint32_t i = 1; !mbar_try_wait_hint(bar, parity, 20000u); ++i) {
+        if ((i & 15u) == 0) {
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) t0 = now;
             if (*abort_flag || now - t0 > 2000000000ull) return false;
@@ -233,6 +238,37 @@ __device__ __forceinline__ void cap64(float (&x)[64], float scale2, float k, flo
     }
 }
 
+// A tile's maximum `tmax` joins the row's.  The reference moves only when it grew by more than 2^8; the
+// TMEM accesses are the whole warp's, so its rows rescale together (by 1 where nothing grew).
+template <int D>
+__device__ __forceinline__ bool grow(float tmax, bool in, float& m_used, float& l, uint32_t o_addr, uint64_t* pv_bar, uint32_t pv_parity,
+                                     volatile int* abort_flag) {
+    float m_new = m_used, alpha = 1.f;
+    bool rescale = false;
+    if (tmax > m_used + 8.f) {
+        if (m_used != -INFINITY) {
+            rescale = in;   // rows past the block hold whatever memory held
+            alpha = ex2(m_used - tmax);
+        }
+        m_new = tmax;
+    }
+    m_used = m_new;
+    if (__any_sync(0xffffffffu, rescale)) {
+        if (pv_bar && !warp_wait(pv_bar, pv_parity, abort_flag)) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 64) {
+            float o[64];
+            load64(o_addr + c, o);
+#pragma unroll
+            for (int e = 0; e < 64; ++e) o[e] *= alpha;
+            store64(o_addr + c, o);
+        }
+        l *= alpha;
+    }
+    return true;
+}
+
 // One softmax thread's work on a tile of 64 * halves keys: wait for S, transform, mask, running
 // maximum (rescaling O where it grew), weights back as bf16 pairs over the scores.  Two passes
 // over the scores, 64 at a time, transformed and masked ones written back in between: a row of
@@ -323,32 +359,7 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
     }
     if constexpr (kScored) tmem_st_wait();
     else if (tl.tree || tl.nvalid < 64 * halves) tmem_st_wait();
-    const float tmax = top * in_scale;
-    // the reference maximum moves only when the row's grew by more than 2^8; the TMEM
-    // accesses are the whole warp's, so its rows rescale together (by 1 where nothing grew)
-    float m_new = m_used, alpha = 1.f;
-    bool rescale = false;
-    if (tmax > m_used + 8.f) {
-        if (m_used != -INFINITY) {
-            rescale = true;
-            alpha = ex2(m_used - tmax);
-        }
-        m_new = tmax;
-    }
-    if (__any_sync(0xffffffffu, rescale)) {
-        if (pv_bar && !warp_wait(pv_bar, pv_parity, abort_flag)) return false;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
-            float o[64];
-            load64(o_addr + c, o);
-#pragma unroll
-            for (int e = 0; e < 64; ++e) o[e] *= alpha;
-            store64(o_addr + c, o);
-        }
-        l *= alpha;
-    }
-    m_used = m_new;
+    if (!grow<D>(top * in_scale, row.in, m_used, l, o_addr, pv_bar, pv_parity, abort_flag)) return false;
     const float nmref = m_used == -INFINITY ? 0.f : -m_used;
     const unsigned long long sc2 = pk2(in_scale, in_scale), nm2 = pk2(nmref, nmref);
 #pragma unroll 1
@@ -379,8 +390,89 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
     return true;
 }
 
+// The same for an item of at most 32 rows with the rows' four copies: this warp's 16 keys of a 64-key
+// tile.  Weights of the other keys are zero in its lanes.
+template <int D, bool kScored, typename Landed, typename Release>
+__device__ __forceinline__ bool softmax_few(const Params& p, const Desc& it, const Tile& tl, const Row& row, int copy, uint32_t s_addr,
+                                            uint32_t o_addr, float& m_used, float& l, uint64_t* s_bar, uint32_t s_parity,
+                                            uint64_t* pv_bar, uint32_t pv_parity, volatile int* abort_flag, Landed landed, Release release) {
+    const int e0 = 16 * copy, k0 = tl.k0 + e0;
+    const int nv = min(max(tl.nvalid - e0, 0), 16);
+    uint32_t bits = (1u << nv) - 1u;
+    if (tl.tree) bits &= static_cast<uint32_t>(row.anc[tl.k0 >> 6] >> e0);
+    const int kbase = it.shared ? k0 : it.Ls + k0;      // position of the first key (not the tree's)
+    const int depth = row.pos - it.Ls - it.L;           // (own items) the node's
+    float bias[16];
+    if constexpr (kScored) {
+        if (p.slopes) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) bias[e] = fmaf(row.slope2, static_cast<float>(e), row.slope2 * static_cast<float>(kbase - row.pos));
+            if (tl.tree) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) bias[e] = e < nv ? -row.slope2 * static_cast<float>(depth - p.depth[k0 + e]) : 0.f;
+            }
+        }
+        if (p.window > 0) {
+            if (tl.tree) {
+                if (p.window <= SPEC_MAX_DEPTH)
+                    for (uint32_t left = bits; left; left &= left - 1) {
+                        const int e = __ffs(static_cast<int>(left)) - 1;
+                        if (depth - p.depth[k0 + e] >= p.window) bits &= ~(1u << e);
+                    }
+            } else {
+                const int lo = min(max(row.pos - p.window + 1 - kbase, 0), 16);   // first key seen
+                bits &= ~0u << lo;
+            }
+        }
+    }
+    if (!warp_wait(s_bar, s_parity, abort_flag)) return false;
+    tc_fence_after();
+    if (!landed()) return false;
+    const float scale2 = p.scale * kLog2e;
+    uint32_t raw[16];
+    tmem_ld16(s_addr + e0, raw);
+    tmem_ld_wait();
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(raw[e]) * scale2;
+    if constexpr (kScored) {
+        if (p.softcap > 0.f) {   // see cap64
+            const float cap2 = p.softcap * kLog2e, k2 = 2.f / p.softcap;   // x is log2 e times the score
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = fmaf(-2.f * cap2, rcp(ex2(x[e] * k2) + 1.f), cap2);
+        }
+        if (p.slopes) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] += bias[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (!((bits >> e) & 1u)) x[e] = -INFINITY;
+    const float top = fmax3(fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8])),
+                            fmax3(x[9], x[10], x[11]), fmax3(fmax3(x[12], x[13], x[14]), x[15], x[15]));
+    if (!grow<D>(top, row.in, m_used, l, o_addr, pv_bar, pv_parity, abort_flag)) return false;
+    const float nmref = m_used == -INFINITY ? 0.f : -m_used;
+    uint32_t packed[8];
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+        const float a0 = ex2(x[e] + nmref), a1 = ex2(x[e + 1] + nmref);
+        sum += a0 + a1;
+        const __nv_bfloat162 pr = __floats2bfloat162_rn(a0, a1);   // .x (lower key) low
+        packed[e / 2] = *reinterpret_cast<const uint32_t*>(&pr);
+    }
+    l += sum;
+    const uint32_t none[8] = {};
+#pragma unroll
+    for (int c = 1; c < 4; ++c) tmem_st8(s_addr + 8 * ((copy + c) & 3), none);
+    tmem_st8(s_addr + 8 * copy, packed);
+    release(0);
+    return true;
+}
+
 template <int D, bool kScored>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_constant__ Maps mp, const Params p, const int page_rows) {
+__global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_constant__ Maps mp, const Params p, const int page_log) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if ((smem_u32(smem) & 1023u) != 0) {   // the swizzle counts address bits: a base elsewhere would scramble tiles
@@ -451,12 +543,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
     int n = 0;          // running item number
     bool ok = true;
     int q_loads = 0;    // (TMA) items whose Q was requested
-    // item n's descriptor; a whole warp
-    auto get_item = [&](Desc& it) -> bool {
-        if (!(ok = warp_wait(&item_full[n % kItems], (n / kItems) & 1, abort_flag))) return false;
-        it = desc[n % kItems];
+    // item number i's descriptor; a whole warp
+    auto get_item = [&](Desc& it, int i) -> bool {
+        if (!(ok = warp_wait(&item_full[i % kItems], (i / kItems) & 1, abort_flag))) return false;
+        it = desc[i % kItems];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&item_empty[n % kItems]);
+        if (lane == 0) mbar_arrive(&item_empty[i % kItems]);
         return it.valid != 0;
     };
 
@@ -488,77 +580,86 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
             if (!d.valid) break;
         }
     } else if (warp == 8) {
-        const uint32_t q_bytes_own = static_cast<uint32_t>(p.rowsO) * 128 * C::kH;
-        const uint32_t q_bytes_shared = static_cast<uint32_t>(p.rowsS) * 128 * C::kH;
-        const int tree_rows = min(p.T, kKeys);
+        const bool leader = elected();
+        const uint32_t q_bytes_own = static_cast<uint32_t>(p.rowsO * p.repO) * 128 * C::kH;
+        const uint32_t q_bytes_shared = static_cast<uint32_t>(p.rowsS * p.repS) * 128 * C::kH;
         const bool paged = p.pg.table != nullptr;
+        const int box_log = paged ? page_log : 6;             // rows of a box of the cache's maps
+        int at = 0;                                           // the next use's landing barrier
         Desc it;
-        for (; ok && get_item(it); ++n) {
-            // Q once the last item's scores are done; from the second item on behind the item's first
-            // load, whose stage frees without this item's Q
-            auto load_q = [&]() -> bool {
-                if (n > 0 && !warp_wait(q_empty, (n - 1) & 1, abort_flag)) return false;
-                if (lane == 0) {
+        for (; ok && get_item(it, n); ++n) {
+            const Tiles ts(it);
+            const int* table = it.shared ? p.shared_table : p.pg.table + static_cast<size_t>(it.b) * p.pg.max_blocks;
+            const int pre_row = it.shared ? it.kvh * p.Lshared : (it.b * p.Hkv + it.kvh) * p.Lmax;   // contiguous
+            const int tree_row = (it.b * p.Hkv + it.kvh) * p.T;
+            // Q as soon as the last item's scores are done: the first uses' stages free without it
+            bool q_due = true;
+            auto load_q = [&](bool now) -> bool {
+                if (n > 0 && !(now ? warp_wait(q_empty, (n - 1) & 1, abort_flag) : __all_sync(0xffffffffu, mbar_test(q_empty, (n - 1) & 1))))
+                    return !now;
+                if (leader) {
                     mbar_arrive_expect_tx(q_full, it.shared ? q_bytes_shared : q_bytes_own);
-                    for (int h = 0; h < C::kH; ++h)
-                        tma_load_4d(sQ + h * kQHalf, it.shared ? &mp.q_shared : &mp.q_own, q_full, 64 * h, it.rb * kBlock, it.kvh, it.b);
+                    for (int c = 0; c < (it.shared ? p.repS : p.repO); ++c)
+                        for (int h = 0; h < C::kH; ++h)
+                            tma_load_4d(sQ + h * kQHalf + c * (32 * 128), it.shared ? &mp.q_shared : &mp.q_own, q_full, 64 * h,
+                                        it.rb * kBlock, it.kvh, it.b);
                 }
                 q_loads = n + 1;
+                q_due = false;
                 return true;
             };
-            if (n == 0) load_q();
-            const Tiles ts(it);
-            // paged: the lane's piece of the tile, one pool block's rows; narrow tiles take K and V by even and odd lanes
-            const int piece = it.pair ? lane : lane >> 1;
-            const int* table = it.shared ? p.shared_table : p.pg.table + static_cast<size_t>(it.b) * p.pg.max_blocks;
-            auto page_of = [&](int j) -> int {
-                if (!paged || j >= ts.count) return 0;
-                const Tile tl(p, it, ts, j);
-                return !tl.tree && piece * page_rows < tl.nvalid ? table[(tl.k0 + piece * page_rows) / p.pg.bs] : 0;
-            };
-            const int half = ts.width * kHalf;
-            int blk = page_of(0);
-            for (int j = 0; ok && j < ts.count; ++j) {
-                const Tile tl(p, it, ts, j);
-                const bool pieces = paged && !tl.tree;
-                const int blk_next = page_of(j + 1);   // looked up a tile ahead
-                int row = 0;
-                if (pieces && piece * page_rows < tl.nvalid) {
-                    if (blk < 0 || blk >= p.pg.num_blocks) {
-                        flag_status(p.ws, SPEC_EINVAL);
-                        blk = 0;
-                    }
-                    row = (blk * p.Hkv + it.kvh) * p.pg.bs + (tl.k0 + piece * page_rows) % p.pg.bs;
-                }
-                const int box = pieces ? page_rows : tl.tree ? tree_rows : kKeys;
-                const int boxes = (tl.nvalid + box - 1) / box;
-                for (int part = 0; part < ts.width; ++part) {   // pair: K, then V
-                    const int s = U % C::kStages;
-                    uint8_t* st = sKV + s * C::kStage;
-                    uint64_t* bar = &kv_full[U % C::kFull];
-                    if (U >= C::kStages && !(ok = warp_wait(&kv_empty[s], ((U / C::kStages) - 1) & 1, abort_flag))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * box) * 128 * C::kH * (it.pair ? 1 : 2));
-                    __syncwarp();
-                    if (pieces) {
-                        if (piece * page_rows < tl.nvalid) {
-                            const int v = it.pair ? part : lane & 1;
-                            uint8_t* dst = st + (it.pair ? 0 : v * (C::kStage / 2)) + piece * page_rows * 128;
-                            for (int h = 0; h < C::kH; ++h) tma_load_2d(dst + h * half, v ? &mp.vc : &mp.kc, bar, 64 * h, row);
+            const int half = ts.width * kHalf, uses = ts.width * ts.count;
+            // the rows of 32 boxes at a time, one per lane: lane = tile * 2^plog + box (a look-up in the block
+            // table and some fifty instructions for each tile on its own took 1700 cycles, more than the tile)
+            const int plog = (it.pair ? 7 : 6) - box_log, batch = 32 >> plog;
+            int use = 0;
+            for (int j0 = 0; ok && j0 < ts.count; j0 += batch) {
+                int row, meta;
+                {
+                    const Tile tl(p, it, ts, min(j0 + (lane >> plog), ts.count - 1));
+                    const int log = tl.tree ? 6 : box_log, off = (lane & ((1 << plog) - 1)) << log;
+                    row = (tl.tree ? tree_row : pre_row) + tl.k0 + off;
+                    meta = ((tl.nvalid + (1 << log) - 1) >> log) + (tl.tree ? 256 : 0);   // boxes
+                    if (paged && !tl.tree && off < tl.nvalid) {
+                        const int x = divide(tl.k0 + off, p.pg.bs);
+                        int blk = table[x];
+                        if (blk < 0 || blk >= p.pg.num_blocks) {
+                            flag_status(p.ws, SPEC_EINVAL);
+                            blk = 0;
                         }
-                    } else if (lane < 2 * C::kH && (!it.pair || lane / C::kH < boxes)) {
-                        // lane = (narrow: K or V; pair: 64 keys) * kH + half
-                        const int h = lane % C::kH, x = lane / C::kH;
-                        const int v = it.pair ? part : x;
-                        const CUtensorMap* m = tl.tree ? (v ? &mp.vt : &mp.kt) : it.shared ? (v ? &mp.vs : &mp.ks) : (v ? &mp.vc : &mp.kc);
-                        const int r0 = tl.tree ? (it.b * p.Hkv + it.kvh) * p.T
-                                               : it.shared ? it.kvh * p.Lshared : (it.b * p.Hkv + it.kvh) * p.Lmax;
-                        tma_load_2d(st + (it.pair ? x * kHalf : v * (C::kStage / 2)) + h * half, m, bar, 64 * h,
-                                    r0 + tl.k0 + (it.pair ? x * kKeys : 0));
+                        row = (blk * p.Hkv + it.kvh) * p.pg.bs + (tl.k0 + off - x * p.pg.bs);
                     }
-                    ++U;
-                    if (n > 0 && j == 0 && part == 0 && !(ok = load_q())) break;
                 }
-                blk = blk_next;
+                const int j_end = min(j0 + batch, ts.count);
+                for (int j = j0; ok && j < j_end; ++j) {
+                    const int src = (j - j0) << plog;
+                    const int m = __shfl_sync(0xffffffffu, meta, src), boxes = m & 255;
+                    const bool tree = m > 255;
+                    const int rows = tree ? min(p.T, kKeys) : 1 << box_log, log = tree ? 6 : box_log;
+                    const CUtensorMap* mk = tree ? &mp.kt : it.shared && !paged ? &mp.ks : &mp.kc;
+                    const CUtensorMap* mv = tree ? &mp.vt : it.shared && !paged ? &mp.vs : &mp.vc;
+                    for (int part = 0; part < ts.width; ++part, ++use) {   // pair: K, then V; narrow: both at once
+                        const int stage = at < C::kStages ? at : at - C::kStages;
+                        uint8_t* st = sKV + stage * C::kStage;
+                        uint64_t* bar = &kv_full[at];
+                        if (U >= C::kStages && !(ok = warp_wait(&kv_empty[stage], at < C::kStages ? 1u : 0u, abort_flag))) break;
+                        if (leader) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * rows) * 128 * C::kH * (it.pair ? 1 : 2));
+                        for (int i = 0; i < boxes; ++i) {
+                            const int r = __shfl_sync(0xffffffffu, row, src + i);
+                            if (leader) {
+                                uint8_t* dst = st + ((i << log) * 128);
+#pragma unroll
+                                for (int h = 0; h < C::kH; ++h) tma_load_2d(dst + h * half, part ? mv : mk, bar, 64 * h, r);
+                                if (!it.pair)
+#pragma unroll
+                                    for (int h = 0; h < C::kH; ++h) tma_load_2d(dst + C::kStage / 2 + h * half, mv, bar, 64 * h, r);
+                            }
+                        }
+                        ++U;
+                        if (++at == C::kFull) at = 0;
+                        if (q_due && !(ok = load_q(n == 0 || use == C::kStages - 1 || use == uses - 1))) break;
+                    }
+                }
             }
         }
     } else if (warp == 9 || warp == 10) {
@@ -609,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
             __device__ __forceinline__ int stage() const { return at < C::kStages ? at : at - C::kStages; }
         };
         Desc it;
-        for (; ok && get_item(it); ++n) {
+        for (; ok && get_item(it, n); ++n) {
             const Tiles ts(it);
             if (leader) {
                 auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && bounded_wait(bar, parity, abort_flag); };
@@ -664,31 +765,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
                         v_use.two_on();
                     }
                 } else {
-                    // thread g for group g: every second tile, the next one's S early where its K is there
+                    // thread g for group g: every second tile; S of the next and PV of the last, whichever is ready
                     const int cnt = (ts.count - g + 1) / 2;
                     Use s_use(U + g), v_use(U + g);
                     if (cnt == 0) mma_commit(q_empty);
                     int issued = 0, done = 0;
-                    while (ok && done < cnt) {
-                        if (issued == done || (issued < cnt && issued - done < 2 && mbar_try_wait(&kv_full[s_use.at], s_use.round))) {
-                            if (!wait(&kv_full[s_use.at], s_use.round)) break;
+                    uint64_t idle_since = 0;
+                    for (uint32_t idle = 1; ok && done < cnt; ++idle) {
+                        const int buf = done & 1;
+                        if (issued < cnt && issued - done < 2 && mbar_test(&kv_full[s_use.at], s_use.round)) {
                             tc_fence_after();
-                            const int buf = issued & 1;
-                            issue_s(tmem + g * 128 + buf * kKeys, 0, s_use.stage(), 1);
-                            mma_commit(&s_full[2 * g + buf]);
+                            issue_s(tmem + g * 128 + (issued & 1) * kKeys, 0, s_use.stage(), 1);
+                            mma_commit(&s_full[2 * g + (issued & 1)]);
                             s_use.two_on();
                             if (++issued == cnt) mma_commit(q_empty);
+                        } else if (issued > done && mbar_test(&p_full[2 * g + buf], (p_phase >> buf) & 1u)) {
+                            p_phase ^= 1u << buf;
+                            if (!clear_o()) break;
+                            tc_fence_after();
+                            issue_pv(tmem + g * 128 + buf * kKeys, smem_u32(sKV + v_use.stage() * C::kStage + C::kStage / 2), kHalf, 0,
+                                     Tile(p, it, ts, g + 2 * done).nvalid, done == 0);
+                            mma_commit(&kv_empty[v_use.stage()]);
+                            mma_commit(&pv_done[g]);
+                            v_use.two_on();
+                            ++done;
+                        } else {
+                            if ((idle & 1023u) == 0) {   // bounded like the other waits
+                                const uint64_t now = globaltimer_ns();
+                                if (idle_since == 0) idle_since = now;
+                                ok = !*abort_flag && now - idle_since <= 2000000000ull;
+                            }
                             continue;
                         }
-                        const int buf = done & 1;
-                        if (!wait_p(buf) || !clear_o()) break;
-                        tc_fence_after();
-                        issue_pv(tmem + g * 128 + buf * kKeys, smem_u32(sKV + v_use.stage() * C::kStage + C::kStage / 2), kHalf, 0,
-                                 Tile(p, it, ts, g + 2 * done).nvalid, done == 0);
-                        mma_commit(&kv_empty[v_use.stage()]);
-                        mma_commit(&pv_done[g]);
-                        v_use.two_on();
-                        ++done;
+                        idle = 0;
+                        idle_since = 0;
                     }
                     clear_o();
                 }
@@ -706,23 +816,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
         const uint32_t s_base = lane_base + grp * 128, o_addr = lane_base + kO + grp * D;
         uint32_t s_phase = 0, ml_phase = 0;                // bit b: phase of s_full[grp][b]
         int narrow = 0;                                    // narrow tiles this group has finished
-        Desc it;
-        for (; ok && get_item(it); ++n) {
-            const Tiles ts(it);
-            const int r0 = it.pair ? grp * kRows : 0;
-            const int r = r0 + tl_row;                     // row of the block
-            // the row: its place in gT, node, position, slope (rows past the block repeat its last)
-            const bool warp_in = r0 + (warp & 3) * 32 < it.rows;
-            const bool in = r < it.rows;
-            const int rr = min(r, it.rows - 1);
-            const int ib = p.gT < kBlock ? rr / p.gT : 0;
-            const int i = p.gT < kBlock ? rr - ib * p.gT : it.rb * kBlock + rr;
-            const int head = i / p.T, node = i - head * p.T;
-            Row row{in, 0, 0.f, p.anc + static_cast<size_t>(node) * p.words};
+        // the thread's row of an item: its place in gT, node, position, slope (rows past the block repeat its last)
+        struct At {
+            Row row;
+            int r, ib, i;
+        };
+        auto row_of = [&](const Desc& d) -> At {
+            At at;
+            at.r = (d.shared ? p.repS : p.repO) > 1 ? lane : (d.pair ? grp * kRows : 0) + tl_row;
+            const int rr = min(at.r, d.rows - 1);
+            at.ib = p.gT < kBlock ? rr / p.gT : 0;
+            at.i = p.gT < kBlock ? rr - at.ib * p.gT : d.rb * kBlock + rr;
+            const int head = at.i / p.T, node = at.i - head * p.T;
+            at.row = Row{at.r < d.rows, 0, 0.f, p.anc + static_cast<size_t>(node) * p.words};
             if constexpr (kScored) {
-                row.pos = it.Ls + (it.shared ? own_len(p, it.b + ib) : it.L) + p.depth[node];
-                if (p.slopes) row.slope2 = p.slopes[it.kvh * p.g + head] * kLog2e;
+                at.row.pos = d.Ls + (d.shared ? own_len(p, d.b + at.ib) : d.L) + p.depth[node];
+                if (p.slopes) at.row.slope2 = p.slopes[d.kvh * p.g + head] * kLog2e;
             }
+            return at;
+        };
+        Desc it;
+        At at{};
+        bool more = get_item(it, 0);
+        if (more) at = row_of(it);
+        for (; more; ++n) {
+            const Tiles ts(it);
+            const bool few = (it.shared ? p.repS : p.repO) > 1;
+            const int r = at.r;
+            const bool warp_in = few || (it.pair ? grp * kRows : 0) + (warp & 3) * 32 < it.rows;
+            const bool in = at.row.in;
+            const Row& row = at.row;
             float m_used = -INFINITY, l = 0.f;
             for (int j = it.pair ? 0 : grp, k = 0; j < ts.count; j += it.pair ? 1 : 2, ++k) {
                 const Tile tl(p, it, ts, j);
@@ -759,8 +882,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_full[2 * grp + (it.pair ? h : buf)]);
                 };
-                ok = softmax_tile<D, kScored>(p, it, tl, row, ts.width, warp_in, s_base + buf * kKeys, o_addr, m_used, l, s_bar, parity,
-                                              it.pair ? nullptr : &pv_done[grp], (narrow - 1) & 1, abort_flag, landed, release);
+                uint64_t* pv_bar = it.pair ? nullptr : &pv_done[grp];
+                const uint32_t s_addr = s_base + buf * kKeys;
+                ok = few ? softmax_few<D, kScored>(p, it, tl, row, warp & 3, s_addr, o_addr, m_used, l, s_bar, parity, pv_bar,
+                                                   (narrow - 1) & 1, abort_flag, landed, release)
+                         : softmax_tile<D, kScored>(p, it, tl, row, ts.width, warp_in, s_addr, o_addr, m_used, l, s_bar, parity, pv_bar,
+                                                    (narrow - 1) & 1, abort_flag, landed, release);
                 if (!ok) break;
                 if (!it.pair) {
                     // the stage's second arrival, beside PV's commit (a pair's come from both groups)
@@ -769,6 +896,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
                 }
             }
             if (!ok) break;
+            // the next item's row, looked up while the last products run
+            Desc next;
+            At next_at{};
+            more = get_item(next, n + 1);
+            if (!ok) break;
+            if (more) next_at = row_of(next);
             // the item's end: in a pair each group has its rows' whole (m, l, O); otherwise (m, l)
             // across the groups, then each joins half the columns
             if (!(ok = warp_wait(o_final, n & 1, abort_flag))) break;
@@ -792,10 +925,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
                 has_other = ts.count > 1 || grp == 1;
             }
             if (warp_in) {
-                const int stride = it.shared ? p.rowsS : p.rowsO;
-                float4* part = (it.shared ? p.part_s : p.part_o) + static_cast<size_t>(it.index) * (D / 4 + 1) * stride + r;
+                const int cap = it.shared ? p.rowsS : p.rowsO, stride = cap * (few ? 4 : 1);
+                float4* part = (it.shared ? p.part_s : p.part_o) + static_cast<size_t>(it.index) * (D / 4 + 1) * stride +
+                               (few ? (warp & 3) * cap : 0) + r;
                 const float inv = it.direct ? 1.f / lsum : 1.f;
-                const size_t q_row = (static_cast<size_t>(it.b + ib) * p.Hq + it.kvh * p.g) * p.T + i;
+                const size_t q_row = (static_cast<size_t>(it.b + at.ib) * p.Hq + it.kvh * p.g) * p.T + at.i;
                 if (in && (it.pair || grp == 0)) {
                     if (!it.direct) part[0] = make_float4(m, lsum, 0.f, 0.f);
                     else if (p.lse) p.lse[q_row] = (m + log2f(lsum)) * kLn2;
@@ -838,6 +972,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
             __syncwarp();
             if (lane == 0) mbar_arrive(o_empty);
             U += ts.width * ts.count;
+            it = next;
+            at = next_at;
         }
     }
     if (!ok) {
@@ -867,11 +1003,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
 // ---------------------------------------------------------------- host
 
 template <int D, bool kScored>
-static spec_status launch_items(const Maps& m, const Params& p, int page_rows, int blocks, cudaStream_t s) {
+static spec_status launch_items(const Maps& m, const Params& p, int page_log, int blocks, cudaStream_t s) {
     static_assert(Cfg<D>::kSmem <= 232448, "shared memory of one CTA");
     auto kern = k_attn_shared_tc<D, kScored>;
     SPEC_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem));
-    SPEC_CUDA_TRY(launch("attn_shared_tc", kern, dim3(blocks), dim3(kThreads), Cfg<D>::kSmem, s, m, p, page_rows));
+    SPEC_CUDA_TRY(launch("attn_shared_tc", kern, dim3(blocks), dim3(kThreads), Cfg<D>::kSmem, s, m, p, page_log));
     return SPEC_OK;
 }
 
@@ -883,14 +1019,14 @@ spec_status attn_shared_tc_run(const Params& p, int blocks, cudaStream_t s) {
     SPEC_CUDA_TRY(make_tmap_bf16_4d(&m.q_own, p.q, B, Hkv, p.gT, D, 1, b1));
     SPEC_CUDA_TRY(make_tmap_bf16_2d(&m.kt, p.kt, B * Hkv * T, D, D, static_cast<uint32_t>(std::min(p.T, kKeys))));
     SPEC_CUDA_TRY(make_tmap_bf16_2d(&m.vt, p.vt, B * Hkv * T, D, D, static_cast<uint32_t>(std::min(p.T, kKeys))));
-    int page_rows = 0;
+    int page_log = 0;
     if (p.pg.table) {
         // a box lies inside one block and one tile: the largest power of two that divides both
-        page_rows = 16;
-        while (page_rows < kKeys && p.pg.bs % (2 * page_rows) == 0) page_rows *= 2;
+        page_log = 4;
+        while ((1 << page_log) < kKeys && p.pg.bs % (2 << page_log) == 0) ++page_log;
         const uint64_t rows = static_cast<uint64_t>(p.pg.num_blocks) * Hkv * p.pg.bs;
-        SPEC_CUDA_TRY(make_tmap_bf16_2d(&m.kc, p.kc, rows, D, D, page_rows));
-        SPEC_CUDA_TRY(make_tmap_bf16_2d(&m.vc, p.vc, rows, D, D, page_rows));
+        SPEC_CUDA_TRY(make_tmap_bf16_2d(&m.kc, p.kc, rows, D, D, 1u << page_log));
+        SPEC_CUDA_TRY(make_tmap_bf16_2d(&m.vc, p.vc, rows, D, D, 1u << page_log));
     } else {
         SPEC_CUDA_TRY(make_tmap_bf16_2d(&m.kc, p.kc, B * Hkv * p.Lmax, D, D, kKeys));
         SPEC_CUDA_TRY(make_tmap_bf16_2d(&m.vc, p.vc, B * Hkv * p.Lmax, D, D, kKeys));
@@ -904,8 +1040,8 @@ spec_status attn_shared_tc_run(const Params& p, int blocks, cudaStream_t s) {
     }
     const bool scored = p.softcap > 0.f || p.window > 0 || p.slopes;
     if (p.D == 64)
-        return scored ? launch_items<64, true>(m, p, page_rows, blocks, s) : launch_items<64, false>(m, p, page_rows, blocks, s);
-    return scored ? launch_items<128, true>(m, p, page_rows, blocks, s) : launch_items<128, false>(m, p, page_rows, blocks, s);
+        return scored ? launch_items<64, true>(m, p, page_log, blocks, s) : launch_items<64, false>(m, p, page_log, blocks, s);
+    return scored ? launch_items<128, true>(m, p, page_log, blocks, s) : launch_items<128, false>(m, p, page_log, blocks, s);
 }
 
 }  // namespace shr
