@@ -257,12 +257,13 @@ __device__ __forceinline__ bool grow(float tmax, bool in, float& m_used, float& 
         if (pv_bar && !warp_wait(pv_bar, pv_parity, abort_flag)) return false;
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
-            float o[64];
-            load64(o_addr + c, o);
+        for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_addr + c, o);
+            tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 64; ++e) o[e] *= alpha;
-            store64(o_addr + c, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(o_addr + c, o);
         }
         l *= alpha;
     }
@@ -387,6 +388,89 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
         }
         release(h);
     }
+    return true;
+}
+
+// The same for a pair's 128 keys with plain scores, in a straight line: the maximum 64 scores at a
+// time, then the exponentials 32 at a time with the next 32 on their way from TMEM.  (All 128 in
+// registers would save the second reading and spill as much.)  The second half's exponentials
+// run while the first half is in PV.
+template <int D, typename Landed, typename Release>
+__device__ __forceinline__ bool softmax_pair(const Params& p, const Tile& tl, const Row& row, bool warp_in, uint32_t s_addr, uint32_t o_addr,
+                                             float& m_used, float& l, uint64_t* s_bar, uint32_t s_parity, volatile int* abort_flag,
+                                             Landed landed, Release release) {
+    if (!warp_wait(s_bar, s_parity, abort_flag)) return false;
+    tc_fence_after();
+    if (!landed()) return false;
+    if (!warp_in) {
+        release(0);
+        release(1);
+        return true;
+    }
+    float top = -INFINITY;
+    if (tl.tree || tl.nvalid < 128) {
+        // hidden keys become -inf, in place
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            float x[64];
+            load64(s_addr + 64 * h, x);
+            const int nv = min(max(tl.nvalid - 64 * h, 0), 64);
+            uint64_t bits = nv >= 64 ? ~0ull : (1ull << nv) - 1ull;
+            if (tl.tree && nv > 0) bits &= row.anc[(tl.k0 >> 6) + h];   // only the node's ancestors and itself
+            const uint32_t w0 = static_cast<uint32_t>(bits), w1 = static_cast<uint32_t>(bits >> 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                if (!((w0 >> e) & 1u)) x[e] = -INFINITY;
+                if (!((w1 >> e) & 1u)) x[e + 32] = -INFINITY;
+            }
+            store64(s_addr + 64 * h, x);
+            top = fmaxf(top, max64(x));
+        }
+        tmem_st_wait();
+    } else {
+        float x[64];
+        load64(s_addr, x);
+        top = max64(x);
+        load64(s_addr + 64, x);
+        top = fmaxf(top, max64(x));
+    }
+    uint32_t a[32], b[32];
+    tmem_ld32(s_addr, a);
+    const float scale2 = p.scale * kLog2e;
+    if (!grow<D>(top * scale2, row.in, m_used, l, o_addr, nullptr, 0, abort_flag)) return false;
+    const float nmref = m_used == -INFINITY ? 0.f : -m_used;
+    const unsigned long long sc2 = pk2(scale2, scale2), nm2 = pk2(nmref, nmref);
+    auto weigh = [&](const uint32_t (&x)[32], int c) {   // weights 32 c .. of the row, to columns 16 c ..
+        uint32_t packed[16];
+        unsigned long long acc2 = pk2(0.f, 0.f);
+#pragma unroll
+        for (int h2 = 0; h2 < 16; ++h2) {
+            float x0, x1;
+            upk2(ffma2(pk2(__uint_as_float(x[2 * h2]), __uint_as_float(x[2 * h2 + 1])), sc2, nm2), x0, x1);
+            const float a0 = ex2(x0), a1 = ex2(x1);
+            acc2 = fadd2(acc2, pk2(a0, a1));
+            const __nv_bfloat162 pr = __floats2bfloat162_rn(a0, a1);   // .x (lower key) low
+            packed[h2] = *reinterpret_cast<const uint32_t*>(&pr);
+        }
+        float acc0, acc1;
+        upk2(acc2, acc0, acc1);
+        l += acc0 + acc1;
+        tmem_st16(s_addr + 16 * c, packed);
+    };
+    // (weights go where scores have been read: 0 .. 31 behind scores 0 .. 63, 32 .. 63 behind 64 .. 127)
+    tmem_ld_wait();
+    tmem_ld32(s_addr + 32, b);
+    weigh(a, 0);
+    tmem_ld_wait();
+    tmem_ld32(s_addr + 64, a);
+    weigh(b, 1);
+    release(0);
+    tmem_ld_wait();
+    tmem_ld32(s_addr + 96, b);
+    weigh(a, 2);
+    tmem_ld_wait();
+    weigh(b, 3);
+    release(1);
     return true;
 }
 
@@ -835,11 +919,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
             }
             return at;
         };
-        Desc it;
+        // the softmax threads read descriptors where they are: their registers hold scores
+        auto look_at = [&](int i) -> bool {
+            ok = warp_wait(&item_full[i % kItems], (i / kItems) & 1, abort_flag);
+            return ok && desc[i % kItems].valid != 0;
+        };
+        bool more = look_at(0);
         At at{};
-        bool more = get_item(it, 0);
-        if (more) at = row_of(it);
+        if (more) at = row_of(desc[0]);
         for (; more; ++n) {
+            const Desc& it = desc[n % kItems];
             const Tiles ts(it);
             const bool few = (it.shared ? p.repS : p.repO) > 1;
             const int r = at.r;
@@ -884,10 +973,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
                 };
                 uint64_t* pv_bar = it.pair ? nullptr : &pv_done[grp];
                 const uint32_t s_addr = s_base + buf * kKeys;
-                ok = few ? softmax_few<D, kScored>(p, it, tl, row, warp & 3, s_addr, o_addr, m_used, l, s_bar, parity, pv_bar,
-                                                   (narrow - 1) & 1, abort_flag, landed, release)
-                         : softmax_tile<D, kScored>(p, it, tl, row, ts.width, warp_in, s_addr, o_addr, m_used, l, s_bar, parity, pv_bar,
-                                                    (narrow - 1) & 1, abort_flag, landed, release);
+                if (few)
+                    ok = softmax_few<D, kScored>(p, it, tl, row, warp & 3, s_addr, o_addr, m_used, l, s_bar, parity, pv_bar,
+                                                 (narrow - 1) & 1, abort_flag, landed, release);
+                else if (!kScored && it.pair)
+                    ok = softmax_pair<D>(p, tl, row, warp_in, s_addr, o_addr, m_used, l, s_bar, parity, abort_flag, landed, release);
+                else
+                    ok = softmax_tile<D, kScored>(p, it, tl, row, ts.width, warp_in, s_addr, o_addr, m_used, l, s_bar, parity, pv_bar,
+                                                  (narrow - 1) & 1, abort_flag, landed, release);
                 if (!ok) break;
                 if (!it.pair) {
                     // the stage's second arrival, beside PV's commit (a pair's come from both groups)
@@ -897,11 +990,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
             }
             if (!ok) break;
             // the next item's row, looked up while the last products run
-            Desc next;
             At next_at{};
-            more = get_item(next, n + 1);
+            more = look_at(n + 1);
             if (!ok) break;
-            if (more) next_at = row_of(next);
+            if (more) next_at = row_of(desc[(n + 1) % kItems]);
             // the item's end: in a pair each group has its rows' whole (m, l, O); otherwise (m, l)
             // across the groups, then each joins half the columns
             if (!(ok = warp_wait(o_final, n & 1, abort_flag))) break;
@@ -972,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
             __syncwarp();
             if (lane == 0) mbar_arrive(o_empty);
             U += ts.width * ts.count;
-            it = next;
+            if (lane == 0) mbar_arrive(&item_empty[n % kItems]);
             at = next_at;
         }
     }
