@@ -26,5 +26,6 @@ __all__ = [
 def __getattr__(name):
     if name in __all__:
         from . import _binding
-        return getattr(_binding, name)
+        value = globals()[name] = getattr(_binding, name)   # found here without a search from now on
+        return value
     raise AttributeError(name)

@@ -664,74 +664,102 @@ def tree_attention_scored_workspace_size(tree, B, Hq, Hkv, Lmax, D, dtype):
     return int(n)
 
 
-def _attn_args(q, k_tree, v_tree, prefix_len, tree, Hkv, scale, softcap, window, slopes, out, lse, want_lse, stream):
-    """The checks and outputs the shared and scored attention calls have in common."""
-    _need(q, "q", ndim=4)
-    dev = q.device
-    B, Hq, T, D = q.shape
+# The serving calls below run once per layer and step, some for microseconds, so their checks are kept
+# short: one test that passes, and the lengthy one that names the fault only where it fails.  Pointers
+# go to the library as plain integers, and the current device is left alone where it is the tensors'.
+
+def _at(t, name, dtype, index, *shape):
+    """The address of a contiguous tensor of this type, device and shape."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index >= 0 and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtype=dtype, ndim=len(shape), device=torch.device("cuda", index) if index >= 0 else None)
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _one(t, name, index):
+    """The address of an int32 tensor that holds one value."""
+    if isinstance(t, torch.Tensor) and t.numel() == 1:
+        return _at(t, name, torch.int32, index, *t.shape)
+    _need(t, name, dtype=torch.int32)
+    raise ValueError(f"{name} must hold one value")
+
+
+def _buffer(ws, index):
+    if isinstance(ws, torch.Tensor) and ws.get_device() == index and ws.is_contiguous():
+        return ws.data_ptr()   # its size is checked by the library (SPEC_EWORKSPACE)
+    _need(ws, "ws", device=torch.device("cuda", index))
+
+
+def _new(stream, index, dtype, *shape):
+    """A tensor this binding allocates for a call on `stream`: its memory must outlive the call there."""
+    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _call(name, index, stream, *args):
+    """Call the entry point on `stream`, or on the current one of device `index`."""
+    fn = getattr(_lib, name)
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status != 0:
+        _check(name, status)
+
+
+def _queries(q, name="q"):
+    if not isinstance(q, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not q.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if q.dim() != 4:
+        raise ValueError(f"{name} must have 4 dimensions, got {tuple(q.shape)}")
+    return q.get_device(), q.dtype, _dtype_code(q), q.shape
+
+
+def _pool(k_pool):
+    if not isinstance(k_pool, torch.Tensor):
+        raise TypeError("k_pool must be a torch.Tensor")
+    if k_pool.dim() != 4:
+        raise ValueError("pools must be [num_blocks, Hkv, block_size, D]")
+    return k_pool.shape
+
+
+def _attn(name, size, lengths, keys, q, prefix_len, k_tree, v_tree, tree, Hkv, dims, scale, softcap, window, slopes, out, lse,
+          want_lse, ws, stream):
+    """What the shared and scored attention calls have in common: the checks, the outputs and the call.  `lengths`
+    go to the workspace's size, `keys` are the arguments that say where the keys are, `dims` those behind Hkv."""
+    index, dtype, dt, (B, Hq, T, D) = _queries(q)
     if T != tree.T:
         raise ValueError(f"q has {T} nodes, the tree {tree.T}")
-    for name, t in (("k_tree", k_tree), ("v_tree", v_tree)):
-        _need(t, name, dtype=q.dtype, ndim=4, device=dev)
-        if tuple(t.shape) != (B, Hkv, T, D):
-            raise ValueError(f"{name} must be {(B, Hkv, T, D)}")
-    _need(prefix_len, "prefix_len", dtype=torch.int32, ndim=1, device=dev)
-    if prefix_len.shape[0] != B:
-        raise ValueError("prefix_len must be [B]")
+    qp = _at(q, "q", dtype, index, B, Hq, T, D)
+    kp, vp = _at(k_tree, "k_tree", dtype, index, B, Hkv, T, D), _at(v_tree, "v_tree", dtype, index, B, Hkv, T, D)
+    pp = _at(prefix_len, "prefix_len", torch.int32, index, B)
     score = None
     if softcap or window or slopes is not None:
-        if slopes is not None:
-            _need(slopes, "slopes", dtype=torch.float32, ndim=1, device=dev)
-            if slopes.shape[0] != Hq:
-                raise ValueError("slopes must be [Hq]")
-        score = ctypes.byref(spec_score(float(softcap), int(window), 0 if slopes is None else slopes.data_ptr()))
+        sl = None if slopes is None else _at(slopes, "slopes", torch.float32, index, Hq)
+        score = ctypes.byref(spec_score(float(softcap), int(window), sl))
     if out is None:
-        out = _new(stream, dev, q.dtype, B, Hq, T, D)
-    _need(out, "out", dtype=q.dtype, ndim=4, device=dev)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
+        out = _new(stream, index, dtype, B, Hq, T, D)
+    op = _at(out, "out", dtype, index, B, Hq, T, D)
     if lse is None and want_lse:
-        lse = _new(stream, dev, torch.float32, B, Hq, T)
-    if lse is not None:
-        _need(lse, "lse", dtype=torch.float32, ndim=3, device=dev)
-        if tuple(lse.shape) != (B, Hq, T):
-            raise ValueError("lse must be [B, Hq, T]")
-    return dev, B, Hq, D, 0.0 if scale is None else float(scale), score, out, lse
-
-
-def _own_cache(q, k_cache, v_cache):
-    _need(k_cache, "k_cache", dtype=q.dtype, ndim=4, device=q.device)
-    _need(v_cache, "v_cache", dtype=q.dtype, ndim=4, device=q.device)
-    B, D = q.shape[0], q.shape[-1]
-    Hkv, Lmax = k_cache.shape[1], k_cache.shape[2]
-    if tuple(k_cache.shape) != (B, Hkv, Lmax, D) or v_cache.shape != k_cache.shape:
-        raise ValueError("caches must be [B, Hkv, Lmax, D]")
-    return Hkv, Lmax
-
-
-def _own_pages(q, k_pool, v_pool, block_table):
-    _need(k_pool, "k_pool", dtype=q.dtype, ndim=4, device=q.device)
-    _need(v_pool, "v_pool", dtype=q.dtype, ndim=4, device=q.device)
-    num_blocks, Hkv, bs, D = k_pool.shape
-    if D != q.shape[-1] or v_pool.shape != k_pool.shape:
-        raise ValueError("pools must be [num_blocks, Hkv, block_size, D]")
-    _need(block_table, "block_table", dtype=torch.int32, ndim=2, device=q.device)
-    if block_table.shape[0] != q.shape[0]:
-        raise ValueError("block_table must be [B, max_blocks]")
-    return num_blocks, Hkv, bs, block_table.shape[1]
-
-
-def _shared_len(shared_len, dev):
-    _need(shared_len, "shared_len", dtype=torch.int32, device=dev)
-    if shared_len.numel() != 1:
-        raise ValueError("shared_len must hold one value")
-
-
-def _attn_ws(ws, size, args, stream, dev):
+        lse = _new(stream, index, torch.float32, B, Hq, T)
+    lp = None if lse is None else _at(lse, "lse", torch.float32, index, B, Hq, T)
     if ws is None:
-        ws = _new(stream, dev, torch.uint8, size(*args))
-    _need(ws, "ws", device=dev)
-    return ws
+        if torch.cuda.current_device() == index:
+            n = size(tree, B, Hq, Hkv, *lengths, D, dt)
+        else:
+            with torch.cuda.device(index):
+                n = size(tree, B, Hq, Hkv, *lengths, D, dt)
+        ws = _new(stream, index, torch.uint8, n)
+    wp = _buffer(ws, index)
+    _call(name, index, stream, qp, *keys, pp, kp, vp, tree.ref(), B, Hq, Hkv, *dims, D, 0.0 if scale is None else float(scale),
+          score, dt, op, lp, wp, ws.nbytes)
+    return out, lse
 
 
 def tree_attention_shared(q, k_shared, v_shared, shared_len, k_cache, v_cache, prefix_len, k_tree, v_tree, tree, scale=None,
@@ -740,24 +768,14 @@ def tree_attention_shared(q, k_shared, v_shared, shared_len, k_cache, v_cache, p
 
     k_shared, v_shared [Hkv, Lshared, D] with shared_len [1] int32 keys in use; k_cache, v_cache [B, Hkv, Lmax, D]
     and prefix_len [B]: each sequence's own keys behind them.  softcap, window, slopes [Hq]: see spec_score."""
-    _need(q, "q", ndim=4)
-    Hkv, Lmax = _own_cache(q, k_cache, v_cache)
-    dev, B, Hq, D, scale, score, out, lse = _attn_args(q, k_tree, v_tree, prefix_len, tree, Hkv, scale, softcap, window,
-                                                       slopes, out, lse, want_lse, stream)
-    _need(k_shared, "k_shared", dtype=q.dtype, ndim=3, device=dev)
-    _need(v_shared, "v_shared", dtype=q.dtype, ndim=3, device=dev)
-    Ls = k_shared.shape[1]
-    if tuple(k_shared.shape) != (Hkv, Ls, D) or v_shared.shape != k_shared.shape:
-        raise ValueError("shared keys and values must be [Hkv, Lshared, D]")
-    _shared_len(shared_len, dev)
-    dt = _dtype_code(q)
-    with torch.cuda.device(dev):
-        ws = _attn_ws(ws, tree_attention_shared_workspace_size, (tree, B, Hq, Hkv, Ls, Lmax, D, dt), stream, dev)
-        _check("tree_attention_shared", _lib.tree_attention_shared(
-            _ptr(q), _ptr(k_shared), _ptr(v_shared), _ptr(shared_len), Ls, _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len),
-            _ptr(k_tree), _ptr(v_tree), tree.ref(), B, Hq, Hkv, Lmax, D, scale, score, dt, _ptr(out), _ptr(lse), _ptr(ws),
-            ws.nbytes, _stream(stream)))
-    return out, lse
+    index, dtype, _, (B, _, _, D) = _queries(q)
+    _, Hkv, Lmax, _ = _queries(k_cache, "k_cache")[3]
+    Ls = k_shared.shape[1] if isinstance(k_shared, torch.Tensor) and k_shared.dim() == 3 else 0
+    keys = (_at(k_shared, "k_shared", dtype, index, Hkv, Ls, D), _at(v_shared, "v_shared", dtype, index, Hkv, Ls, D),
+            _one(shared_len, "shared_len", index), Ls, _at(k_cache, "k_cache", dtype, index, B, Hkv, Lmax, D),
+            _at(v_cache, "v_cache", dtype, index, B, Hkv, Lmax, D))
+    return _attn("tree_attention_shared", tree_attention_shared_workspace_size, (Ls, Lmax), keys, q, prefix_len, k_tree, v_tree,
+                 tree, Hkv, (Lmax,), scale, softcap, window, slopes, out, lse, want_lse, ws, stream)
 
 
 def tree_attention_shared_paged(q, k_pool, v_pool, shared_table, shared_len, block_table, prefix_len, k_tree, v_tree, tree,
@@ -765,76 +783,52 @@ def tree_attention_shared_paged(q, k_pool, v_pool, shared_table, shared_len, blo
                                 stream=None):
     """tree_attention_shared over a paged cache: shared_table [shared_blocks] and block_table [B, max_blocks] int32
     name blocks of the pools [num_blocks, Hkv, block_size, D]."""
-    _need(q, "q", ndim=4)
-    num_blocks, Hkv, bs, max_blocks = _own_pages(q, k_pool, v_pool, block_table)
-    dev, B, Hq, D, scale, score, out, lse = _attn_args(q, k_tree, v_tree, prefix_len, tree, Hkv, scale, softcap, window,
-                                                       slopes, out, lse, want_lse, stream)
-    _need(shared_table, "shared_table", dtype=torch.int32, ndim=1, device=dev)
-    _shared_len(shared_len, dev)
-    n = shared_table.shape[0]
-    dt = _dtype_code(q)
-    with torch.cuda.device(dev):
-        ws = _attn_ws(ws, tree_attention_shared_workspace_size, (tree, B, Hq, Hkv, n * bs, max_blocks * bs, D, dt), stream, dev)
-        _check("tree_attention_shared_paged", _lib.tree_attention_shared_paged(
-            _ptr(q), _ptr(k_pool), _ptr(v_pool), num_blocks, _ptr(shared_table), n, _ptr(shared_len), _ptr(block_table),
-            max_blocks, bs, _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree), tree.ref(), B, Hq, Hkv, D, scale, score, dt,
-            _ptr(out), _ptr(lse), _ptr(ws), ws.nbytes, _stream(stream)))
-    return out, lse
+    index, dtype, _, (B, _, _, D) = _queries(q)
+    blocks, Hkv, bs, _ = _pool(k_pool)
+    n = shared_table.shape[0] if isinstance(shared_table, torch.Tensor) and shared_table.dim() == 1 else 0
+    most = block_table.shape[1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else 0
+    keys = (_at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), _at(v_pool, "v_pool", dtype, index, blocks, Hkv, bs, D), blocks,
+            _at(shared_table, "shared_table", torch.int32, index, n), n, _one(shared_len, "shared_len", index),
+            _at(block_table, "block_table", torch.int32, index, B, most), most, bs)
+    return _attn("tree_attention_shared_paged", tree_attention_shared_workspace_size, (n * bs, most * bs), keys, q, prefix_len,
+                 k_tree, v_tree, tree, Hkv, (), scale, softcap, window, slopes, out, lse, want_lse, ws, stream)
 
 
 def tree_attention_scored(q, k_cache, v_cache, prefix_len, k_tree, v_tree, tree, scale=None, softcap=0.0, window=0,
                           slopes=None, out=None, lse=None, want_lse=True, ws=None, stream=None):
     """Tree attention with scores capped by softcap * tanh(x / softcap), biased by -slopes[h] * distance and cut to a
     window of positions: returns (out [B,Hq,T,D] in q's type, lse [B,Hq,T] or None)."""
-    _need(q, "q", ndim=4)
-    Hkv, Lmax = _own_cache(q, k_cache, v_cache)
-    dev, B, Hq, D, scale, score, out, lse = _attn_args(q, k_tree, v_tree, prefix_len, tree, Hkv, scale, softcap, window,
-                                                       slopes, out, lse, want_lse, stream)
-    dt = _dtype_code(q)
-    with torch.cuda.device(dev):
-        ws = _attn_ws(ws, tree_attention_scored_workspace_size, (tree, B, Hq, Hkv, Lmax, D, dt), stream, dev)
-        _check("tree_attention_scored", _lib.tree_attention_scored(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree), tree.ref(), B, Hq, Hkv,
-            Lmax, D, scale, score, dt, _ptr(out), _ptr(lse), _ptr(ws), ws.nbytes, _stream(stream)))
-    return out, lse
+    index, dtype, _, (B, _, _, D) = _queries(q)
+    _, Hkv, Lmax, _ = _queries(k_cache, "k_cache")[3]
+    keys = (_at(k_cache, "k_cache", dtype, index, B, Hkv, Lmax, D), _at(v_cache, "v_cache", dtype, index, B, Hkv, Lmax, D))
+    return _attn("tree_attention_scored", tree_attention_scored_workspace_size, (Lmax,), keys, q, prefix_len, k_tree, v_tree,
+                 tree, Hkv, (Lmax,), scale, softcap, window, slopes, out, lse, want_lse, ws, stream)
 
 
 def tree_attention_scored_paged(q, k_pool, v_pool, block_table, prefix_len, k_tree, v_tree, tree, scale=None, softcap=0.0,
                                 window=0, slopes=None, out=None, lse=None, want_lse=True, ws=None, stream=None):
     """tree_attention_scored over a paged cache: pools [num_blocks, Hkv, block_size, D], block_table [B, max_blocks] int32."""
-    _need(q, "q", ndim=4)
-    num_blocks, Hkv, bs, max_blocks = _own_pages(q, k_pool, v_pool, block_table)
-    dev, B, Hq, D, scale, score, out, lse = _attn_args(q, k_tree, v_tree, prefix_len, tree, Hkv, scale, softcap, window,
-                                                       slopes, out, lse, want_lse, stream)
-    dt = _dtype_code(q)
-    with torch.cuda.device(dev):
-        ws = _attn_ws(ws, tree_attention_scored_workspace_size, (tree, B, Hq, Hkv, max_blocks * bs, D, dt), stream, dev)
-        _check("tree_attention_scored_paged", _lib.tree_attention_scored_paged(
-            _ptr(q), _ptr(k_pool), _ptr(v_pool), num_blocks, _ptr(block_table), max_blocks, bs, _ptr(prefix_len),
-            _ptr(k_tree), _ptr(v_tree), tree.ref(), B, Hq, Hkv, D, scale, score, dt, _ptr(out), _ptr(lse), _ptr(ws),
-            ws.nbytes, _stream(stream)))
-    return out, lse
+    index, dtype, _, (B, _, _, D) = _queries(q)
+    blocks, Hkv, bs, _ = _pool(k_pool)
+    most = block_table.shape[1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else 0
+    keys = (_at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), _at(v_pool, "v_pool", dtype, index, blocks, Hkv, bs, D), blocks,
+            _at(block_table, "block_table", torch.int32, index, B, most), most, bs)
+    return _attn("tree_attention_scored_paged", tree_attention_scored_workspace_size, (most * bs,), keys, q, prefix_len, k_tree,
+                 v_tree, tree, Hkv, (), scale, softcap, window, slopes, out, lse, want_lse, ws, stream)
 
 
-def _new(stream, device, dtype, *shape):
-    """A tensor this binding allocates for a call on `stream`: its memory must outlive the call there."""
-    t = torch.empty(*shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
-def _rows(t, name, dtype, device, lead):
-    """Check token rows [*lead, heads, D] with dense heads and evenly spaced tokens; returns (heads, D, token stride)."""
+def _rows(t, name, dtype, index, lead):
+    """Check token rows [*lead, heads, D] with dense heads and evenly spaced tokens; returns (address, heads, D, stride)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(lead) + 2 or tuple(t.shape[:-2]) != tuple(lead):
-        raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, heads, D], got {tuple(t.shape)}")
-    H, D = t.shape[-2:]
+    shape = t.shape
+    if shape[:-2] != lead:
+        raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, heads, D], got {tuple(shape)}")
+    H, D = shape[-2:]
     st = t.stride()
     if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
         raise ValueError(f"{name}: a token's heads must be dense")
@@ -847,57 +841,58 @@ def _rows(t, name, dtype, device, lead):
             elif k != span * step:
                 raise ValueError(f"{name}: tokens must be evenly spaced")
             span *= n
-    return H, D, H * D if step is None else step
+    return t.data_ptr(), H, D, H * D if step is None else step
 
 
-def _rope_args(freq, rot_max, pos_base, dev):
-    rot = 0
+def _rope_args(freq, D, pos_base, index):
+    """(freq's address, the width rotated, pos_base's address)"""
+    fp, rot = None, 0
     if freq is not None:
-        _need(freq, "freq", dtype=torch.float64, ndim=1, device=dev)
+        if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
+            raise ValueError("freq must be a tensor [rot / 2]")
         rot = 2 * freq.shape[0]
-        if rot > rot_max:
-            raise ValueError(f"freq has {freq.shape[0]} entries for heads of {rot_max}")
-    if pos_base is not None:
-        _need(pos_base, "pos_base", dtype=torch.int32, device=dev)
-        if pos_base.numel() != 1:
-            raise ValueError("pos_base must hold one value")
-    return rot
+        fp = _at(freq, "freq", torch.float64, index, rot // 2)
+        if rot > D:
+            raise ValueError(f"freq has {rot // 2} entries for heads of {D}")
+    return fp, rot, None if pos_base is None else _one(pos_base, "pos_base", index)
 
 
 def kv_append_workspace_size():
     return int(_lib.kv_append_workspace_size())
 
 
-def _append_args(q, k, v, seq_start, prefix_len, freq, pos_base, q_out, ws, stream):
-    if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 3:
-        raise ValueError("k must be a CUDA tensor [N, Hkv, D]")
-    dev, N = k.device, k.shape[0]
-    Hkv, D, ks = _rows(k, "k", k.dtype, dev, (N,))
-    Hv, Dv, vs = _rows(v, "v", k.dtype, dev, (N,))
+def _append(name, q, k, v, seq_start, prefix_len, freq, interleaved, pos_base, q_out, ws, stream, index, B, cache):
+    """What both forms of kv_append have in common; `cache` are the arguments that say where the rows go."""
+    N, Hkv, D = k.shape
+    kp, _, _, ks = _rows(k, "k", k.dtype, index, (N,))
+    vp, Hv, Dv, vs = _rows(v, "v", k.dtype, index, (N,))
     if (Hv, Dv) != (Hkv, D):
         raise ValueError("v must match k")
-    Hq, qs = 0, 0
+    qp, Hq, qs, op = None, 0, 0, None
     if q is not None:
-        Hq, Dq, qs = _rows(q, "q", k.dtype, dev, (N,))
+        qp, Hq, Dq, qs = _rows(q, "q", k.dtype, index, (N,))
         if Dq != D:
             raise ValueError("q must have k's head dimension")
         if q_out is None:
-            q_out = _new(stream, dev, k.dtype, N, Hq, D)
-        _need(q_out, "q_out", dtype=k.dtype, ndim=3, device=dev)
-        if tuple(q_out.shape) != (N, Hq, D):
-            raise ValueError("q_out must be [N, Hq, D]")
+            q_out = _new(stream, index, k.dtype, N, Hq, D)
+        op = _at(q_out, "q_out", k.dtype, index, N, Hq, D)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _need(seq_start, "seq_start", dtype=torch.int32, ndim=1, device=dev)
-    _need(prefix_len, "prefix_len", dtype=torch.int32, ndim=1, device=dev)
-    B = prefix_len.shape[0]
-    if seq_start.shape[0] != B + 1:
-        raise ValueError("seq_start must be [B + 1]")
-    rot = _rope_args(freq, D, pos_base, dev)
+    sp = _at(seq_start, "seq_start", torch.int32, index, B + 1)
+    pp = _at(prefix_len, "prefix_len", torch.int32, index, B)
+    fp, rot, bp = _rope_args(freq, D, pos_base, index)
     if ws is None:
-        ws = _new(stream, dev, torch.uint8, kv_append_workspace_size())
-    _need(ws, "ws", device=dev)
-    return dev, N, B, Hq, Hkv, D, qs, ks, vs, rot, q_out, ws
+        ws = _new(stream, index, torch.uint8, kv_append_workspace_size())
+    wp = _buffer(ws, index)
+    _call(name, index, stream, qp, kp, vp, qs, ks, vs, N, sp, B, Hq, Hkv, D, pp, bp, fp, rot, int(interleaved), *cache,
+          _dtype_code(k), op, wp, ws.nbytes)
+    return q_out, ws
+
+
+def _new_rows(k):
+    if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor [N, Hkv, D]")
+    return k.get_device(), k.dtype, k.shape
 
 
 def kv_append(q, k, v, seq_start, prefix_len, k_cache, v_cache, freq=None, interleaved=False, pos_base=None, q_out=None,
@@ -906,73 +901,44 @@ def kv_append(q, k, v, seq_start, prefix_len, k_cache, v_cache, freq=None, inter
 
     q [N, Hq, D] (or None), k, v [N, Hkv, D]: token rows, slices of a packed projection allowed; seq_start [B + 1];
     caches [B, Hkv, Lmax, D] updated in place; freq float64 [rot / 2] radians per position (None: no rotation)."""
-    dev, N, B, Hq, Hkv, D, qs, ks, vs, rot, q_out, ws = _append_args(q, k, v, seq_start, prefix_len, freq, pos_base, q_out,
-                                                                     ws, stream)
-    _need(k_cache, "k_cache", dtype=k.dtype, ndim=4, device=dev)
-    _need(v_cache, "v_cache", dtype=k.dtype, ndim=4, device=dev)
-    Lmax = k_cache.shape[2]
-    if tuple(k_cache.shape) != (B, Hkv, Lmax, D) or v_cache.shape != k_cache.shape:
-        raise ValueError("caches must be [B, Hkv, Lmax, D]")
-    with torch.cuda.device(dev):
-        _check("kv_append", _lib.kv_append(
-            _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, N, _ptr(seq_start), B, Hq, Hkv, D, _ptr(prefix_len), _ptr(pos_base),
-            _ptr(freq), rot, int(interleaved), _ptr(k_cache), _ptr(v_cache), Lmax, _dtype_code(k), _ptr(q_out), _ptr(ws),
-            ws.nbytes, _stream(stream)))
-    return q_out, ws
+    index, dtype, (_, Hkv, D) = _new_rows(k)
+    B, _, Lmax, _ = _queries(k_cache, "k_cache")[3]
+    cache = (_at(k_cache, "k_cache", dtype, index, B, Hkv, Lmax, D), _at(v_cache, "v_cache", dtype, index, B, Hkv, Lmax, D), Lmax)
+    return _append("kv_append", q, k, v, seq_start, prefix_len, freq, interleaved, pos_base, q_out, ws, stream, index, B, cache)
 
 
 def kv_append_paged(q, k, v, seq_start, prefix_len, k_pool, v_pool, block_table, freq=None, interleaved=False,
                     pos_base=None, q_out=None, ws=None, stream=None):
     """kv_append into a paged cache: pools [num_blocks, Hkv, block_size, D], block_table [B, max_blocks] int32."""
-    dev, N, B, Hq, Hkv, D, qs, ks, vs, rot, q_out, ws = _append_args(q, k, v, seq_start, prefix_len, freq, pos_base, q_out,
-                                                                     ws, stream)
-    _need(k_pool, "k_pool", dtype=k.dtype, ndim=4, device=dev)
-    _need(v_pool, "v_pool", dtype=k.dtype, ndim=4, device=dev)
-    num_blocks, bs = k_pool.shape[0], k_pool.shape[2]
-    if tuple(k_pool.shape) != (num_blocks, Hkv, bs, D) or v_pool.shape != k_pool.shape:
-        raise ValueError("pools must be [num_blocks, Hkv, block_size, D]")
-    _need(block_table, "block_table", dtype=torch.int32, ndim=2, device=dev)
-    if block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_blocks]")
-    with torch.cuda.device(dev):
-        _check("kv_append_paged", _lib.kv_append_paged(
-            _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, N, _ptr(seq_start), B, Hq, Hkv, D, _ptr(prefix_len), _ptr(pos_base),
-            _ptr(freq), rot, int(interleaved), _ptr(k_pool), _ptr(v_pool), num_blocks, _ptr(block_table),
-            block_table.shape[1], bs, _dtype_code(k), _ptr(q_out), _ptr(ws), ws.nbytes, _stream(stream)))
-    return q_out, ws
+    index, dtype, (_, Hkv, D) = _new_rows(k)
+    blocks, _, bs, _ = _pool(k_pool)
+    B, most = block_table.shape if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else (0, 0)
+    cache = (_at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), _at(v_pool, "v_pool", dtype, index, blocks, Hkv, bs, D), blocks,
+             _at(block_table, "block_table", torch.int32, index, B, most), most, bs)
+    return _append("kv_append_paged", q, k, v, seq_start, prefix_len, freq, interleaved, pos_base, q_out, ws, stream, index, B, cache)
 
 
 def tree_rope(q, k, v, prefix_len, tree, freq=None, interleaved=False, pos_base=None, q_out=None, k_out=None, v_out=None,
               stream=None):
     """Rotate the tree nodes' projections q [B, T, Hq, D], k, v [B, T, Hkv, D] to their depths:
     returns (q [B, Hq, T, D], k_tree, v_tree [B, Hkv, T, D]), the inputs of tree attention."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
-        raise ValueError("q must be a CUDA tensor [B, T, Hq, D]")
-    dev, (B, T) = q.device, q.shape[:2]
+    index, dtype, dt, (B, T, Hq, D) = _queries(q)
     if T != tree.T:
         raise ValueError(f"q has {T} nodes, the tree {tree.T}")
-    Hq, D, qs = _rows(q, "q", q.dtype, dev, (B, T))
-    Hkv, Dk, ks = _rows(k, "k", q.dtype, dev, (B, T))
-    Hv, Dv, vs = _rows(v, "v", q.dtype, dev, (B, T))
+    qp, _, _, qs = _rows(q, "q", dtype, index, (B, T))
+    kp, Hkv, Dk, ks = _rows(k, "k", dtype, index, (B, T))
+    vp, Hv, Dv, vs = _rows(v, "v", dtype, index, (B, T))
     if Dk != D or (Hv, Dv) != (Hkv, D):
         raise ValueError("k and v must match, with q's head dimension")
-    _need(prefix_len, "prefix_len", dtype=torch.int32, ndim=1, device=dev)
-    if prefix_len.shape[0] != B:
-        raise ValueError("prefix_len must be [B]")
-    rot = _rope_args(freq, D, pos_base, dev)
-    outs = []
-    for name, t, H in (("q_out", q_out, Hq), ("k_out", k_out, Hkv), ("v_out", v_out, Hkv)):
-        if t is None:
-            t = _new(stream, dev, q.dtype, B, H, T, D)
-        _need(t, name, dtype=q.dtype, ndim=4, device=dev)
-        if tuple(t.shape) != (B, H, T, D):
-            raise ValueError(f"{name} must be {(B, H, T, D)}")
-        outs.append(t)
-    with torch.cuda.device(dev):
-        _check("tree_rope", _lib.tree_rope(
-            _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, tree.ref(), B, Hq, Hkv, D, _ptr(prefix_len), _ptr(pos_base), _ptr(freq),
-            rot, int(interleaved), _dtype_code(q), _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), _stream(stream)))
-    return tuple(outs)
+    pp = _at(prefix_len, "prefix_len", torch.int32, index, B)
+    fp, rot, bp = _rope_args(freq, D, pos_base, index)
+    q_out = _new(stream, index, dtype, B, Hq, T, D) if q_out is None else q_out
+    k_out = _new(stream, index, dtype, B, Hkv, T, D) if k_out is None else k_out
+    v_out = _new(stream, index, dtype, B, Hkv, T, D) if v_out is None else v_out
+    _call("tree_rope", index, stream, qp, kp, vp, qs, ks, vs, tree.ref(), B, Hq, Hkv, D, pp, bp, fp, rot, int(interleaved), dt,
+          _at(q_out, "q_out", dtype, index, B, Hq, T, D), _at(k_out, "k_out", dtype, index, B, Hkv, T, D),
+          _at(v_out, "v_out", dtype, index, B, Hkv, T, D))
+    return q_out, k_out, v_out
 
 
 def spec_philox_uniform(seed, offset, B, T, device=None, stream=None):

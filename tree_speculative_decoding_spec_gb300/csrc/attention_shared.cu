@@ -76,11 +76,17 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
             const int j0 = (tree ? tile - n_pre : first + tile) * FK;
             const int j_end = tree ? p.T : it.shared ? plan.Ls : it.L;
             __syncthreads();
-            for (int idx = t; idx < FK * (D / 4); idx += 256) {
-                const int jl = idx / (D / 4), c4 = idx % (D / 4);
-                const int j = j0 + jl;
-                float kv[4] = {0.f, 0.f, 0.f, 0.f}, vv[4] = {0.f, 0.f, 0.f, 0.f};
-                if (j < j_end) {
+            // four keys' and values' loads in flight per thread
+#pragma unroll 1
+            for (int x0 = t; x0 < FK * (D / 4); x0 += 4 * 256) {
+                float kv[4][4], vv[4][4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int jl = (x0 + u * 256) / (D / 4), c4 = (x0 + u * 256) % (D / 4);
+                    const int j = j0 + jl;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) kv[u][e] = vv[u][e] = 0.f;
+                    if (j >= j_end) continue;
                     const T *ksrc, *vsrc;
                     size_t row;
                     bool ok = true;
@@ -105,14 +111,18 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
                         row = (static_cast<size_t>(it.b) * p.Hkv + it.kvh) * p.Lmax + j;
                     }
                     if (ok) {
-                        load4(ksrc + row * D + c4 * 4, kv);
-                        load4(vsrc + row * D + c4 * 4, vv);
+                        load4(ksrc + row * D + c4 * 4, kv[u]);
+                        load4(vsrc + row * D + c4 * 4, vv[u]);
                     } else {
                         flag_status(p.ws, SPEC_EINVAL);   // the key reads as zeros
                     }
                 }
-                *reinterpret_cast<float4*>(&Ks[jl * LD + c4 * 4]) = make_float4(kv[0], kv[1], kv[2], kv[3]);
-                *reinterpret_cast<float4*>(&Vs[jl * LD + c4 * 4]) = make_float4(vv[0], vv[1], vv[2], vv[3]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int jl = (x0 + u * 256) / (D / 4), c4 = (x0 + u * 256) % (D / 4);
+                    *reinterpret_cast<float4*>(&Ks[jl * LD + c4 * 4]) = make_float4(kv[u][0], kv[u][1], kv[u][2], kv[u][3]);
+                    *reinterpret_cast<float4*>(&Vs[jl * LD + c4 * 4]) = make_float4(vv[u][0], vv[u][1], vv[u][2], vv[u][3]);
+                }
             }
             __syncthreads();
 
@@ -255,23 +265,37 @@ __global__ void __launch_bounds__(128) k_attn_shared_join(const Params p, int n_
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (in) {
-        for (int k = sub; k < parts; k += subs) {
-            int rows;
-            const float4* base = part(k, rows);
-            const float4 h = base[0];
-            float4 v[C];
-#pragma unroll
-            for (int c = 0; c < C; ++c) v[c] = base[static_cast<size_t>(1 + warp * C + c) * rows];
-            // a part in which the row saw nothing (one of NaN scores alone has a NaN sum, and counts)
-            if (h.x == -INFINITY && h.y == 0.f) continue;
-            const float m = fmaxf(M, h.x), ref = m == -INFINITY ? 0.f : m;
-            const float keep = exp2f(M - ref), w = exp2f(h.x - ref);
-            M = m;
-            l = l * keep + w * h.y;
+        for (int k = sub; k < parts; k += 2 * subs) {   // two parts' lines in flight
+            const bool two = k + subs < parts;
+            int rows0, rows1;
+            const float4 *at0 = part(k, rows0), *at1 = part(two ? k + subs : k, rows1);
+            const float4 h0 = at0[0];
+            float4 h1 = at1[0], v0[C], v1[C];
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                acc[c].x = acc[c].x * keep + w * v[c].x; acc[c].y = acc[c].y * keep + w * v[c].y;
-                acc[c].z = acc[c].z * keep + w * v[c].z; acc[c].w = acc[c].w * keep + w * v[c].w;
+                v0[c] = at0[static_cast<size_t>(1 + warp * C + c) * rows0];
+                v1[c] = at1[static_cast<size_t>(1 + warp * C + c) * rows1];
+            }
+            if (!two) h1 = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            // a part in which the row saw nothing (one of NaN scores alone has a NaN sum, and counts)
+            const bool none0 = h0.x == -INFINITY && h0.y == 0.f, none1 = h1.x == -INFINITY && h1.y == 0.f;
+            const float m = fmaxf(M, fmaxf(h0.x, h1.x)), ref = m == -INFINITY ? 0.f : m;
+            const float keep = exp2f(M - ref), w0 = exp2f(h0.x - ref), w1 = exp2f(h1.x - ref);
+            M = m;
+            l *= keep;
+            if (!none0) l += w0 * h0.y;
+            if (!none1) l += w1 * h1.y;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                acc[c].x *= keep; acc[c].y *= keep; acc[c].z *= keep; acc[c].w *= keep;
+                if (!none0) {
+                    acc[c].x += w0 * v0[c].x; acc[c].y += w0 * v0[c].y;
+                    acc[c].z += w0 * v0[c].z; acc[c].w += w0 * v0[c].w;
+                }
+                if (!none1) {
+                    acc[c].x += w1 * v1[c].x; acc[c].y += w1 * v1[c].y;
+                    acc[c].z += w1 * v1[c].z; acc[c].w += w1 * v1[c].w;
+                }
             }
         }
     }
@@ -328,16 +352,16 @@ HostPlan host_plan(Params& p, bool tc, bool shared, int ctas) {
     // softmax at two thirds of that, an item's rows take some 8000 or 5500 cycles to start and store
     const int last = p.gT - (p.n_rbO - 1) * p.RB;
     p.wF = 3;
-    p.fixF = tc ? 15 : 6;
+    p.fixF = tc ? 15 : 3;
     auto cost = [&](int rows, int& w, int& fix) {
         w = tc && rows <= kTcRows / 2 ? 2 : 3;
-        fix = tc ? (w == 3 ? 15 : 10) : 6;
+        fix = !tc ? 3 : w == 3 ? 15 : rows > 32 ? 10 : 6;
     };
     cost(p.gT >= p.RB ? last : p.rowsS, p.wS, p.fixS);
     cost(last, p.wO, p.fixO);
     p.repS = tc && p.rowsS <= 32 ? 4 : 1;
     p.repO = tc && p.rowsO <= 32 ? 4 : 1;
-    p.min_piece = 2;
+    p.min_piece = tc ? 2 : 1;
     const size_t per_row = sizeof(float) * (p.D + 4);
     const size_t items_s = shared ? static_cast<size_t>(p.Hkv) * p.n_rbS + ctas : 0;   // one slot per column and per cut
     const size_t items_o = static_cast<size_t>(p.B) * p.Hkv * p.n_rbO + ctas;
