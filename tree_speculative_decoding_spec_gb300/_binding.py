@@ -668,9 +668,13 @@ def tree_attention_scored_workspace_size(tree, B, Hq, Hkv, Lmax, D, dtype):
 # short: one test that passes, and the lengthy one that names the fault only where it fails.  Pointers
 # go to the library as plain integers, and the current device is left alone where it is the tensors'.
 
+_Tensor, _i32 = torch.Tensor, torch.int32
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream   # of a device in use
+
+
 def _at(t, name, dtype, index, *shape):
     """The address of a contiguous tensor of this type, device and shape."""
-    if isinstance(t, torch.Tensor) and t.get_device() == index >= 0 and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+    if isinstance(t, _Tensor) and t.get_device() == index >= 0 and t.dtype is dtype and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     _need(t, name, dtype=dtype, ndim=len(shape), device=torch.device("cuda", index) if index >= 0 else None)
     raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -678,8 +682,8 @@ def _at(t, name, dtype, index, *shape):
 
 def _one(t, name, index):
     """The address of an int32 tensor that holds one value."""
-    if isinstance(t, torch.Tensor) and t.numel() == 1:
-        return _at(t, name, torch.int32, index, *t.shape)
+    if isinstance(t, _Tensor) and t.numel() == 1:
+        return _at(t, name, _i32, index, *t.shape)
     _need(t, name, dtype=torch.int32)
     raise ValueError(f"{name} must hold one value")
 
@@ -701,8 +705,8 @@ def _new(stream, index, dtype, *shape):
 def _call(name, index, stream, *args):
     """Call the entry point on `stream`, or on the current one of device `index`."""
     fn = getattr(_lib, name)
-    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _device() == index:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -738,7 +742,7 @@ def _attn(name, size, lengths, keys, q, prefix_len, k_tree, v_tree, tree, Hkv, d
         raise ValueError(f"q has {T} nodes, the tree {tree.T}")
     qp = _at(q, "q", dtype, index, B, Hq, T, D)
     kp, vp = _at(k_tree, "k_tree", dtype, index, B, Hkv, T, D), _at(v_tree, "v_tree", dtype, index, B, Hkv, T, D)
-    pp = _at(prefix_len, "prefix_len", torch.int32, index, B)
+    pp = _at(prefix_len, "prefix_len", _i32, index, B)
     score = None
     if softcap or window or slopes is not None:
         sl = None if slopes is None else _at(slopes, "slopes", torch.float32, index, Hq)
@@ -750,7 +754,7 @@ def _attn(name, size, lengths, keys, q, prefix_len, k_tree, v_tree, tree, Hkv, d
         lse = _new(stream, index, torch.float32, B, Hq, T)
     lp = None if lse is None else _at(lse, "lse", torch.float32, index, B, Hq, T)
     if ws is None:
-        if torch.cuda.current_device() == index:
+        if _device() == index:
             n = size(tree, B, Hq, Hkv, *lengths, D, dt)
         else:
             with torch.cuda.device(index):
@@ -788,8 +792,8 @@ def tree_attention_shared_paged(q, k_pool, v_pool, shared_table, shared_len, blo
     n = shared_table.shape[0] if isinstance(shared_table, torch.Tensor) and shared_table.dim() == 1 else 0
     most = block_table.shape[1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else 0
     keys = (_at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), _at(v_pool, "v_pool", dtype, index, blocks, Hkv, bs, D), blocks,
-            _at(shared_table, "shared_table", torch.int32, index, n), n, _one(shared_len, "shared_len", index),
-            _at(block_table, "block_table", torch.int32, index, B, most), most, bs)
+            _at(shared_table, "shared_table", _i32, index, n), n, _one(shared_len, "shared_len", index),
+            _at(block_table, "block_table", _i32, index, B, most), most, bs)
     return _attn("tree_attention_shared_paged", tree_attention_shared_workspace_size, (n * bs, most * bs), keys, q, prefix_len,
                  k_tree, v_tree, tree, Hkv, (), scale, softcap, window, slopes, out, lse, want_lse, ws, stream)
 
@@ -812,14 +816,14 @@ def tree_attention_scored_paged(q, k_pool, v_pool, block_table, prefix_len, k_tr
     blocks, Hkv, bs, _ = _pool(k_pool)
     most = block_table.shape[1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else 0
     keys = (_at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), _at(v_pool, "v_pool", dtype, index, blocks, Hkv, bs, D), blocks,
-            _at(block_table, "block_table", torch.int32, index, B, most), most, bs)
+            _at(block_table, "block_table", _i32, index, B, most), most, bs)
     return _attn("tree_attention_scored_paged", tree_attention_scored_workspace_size, (most * bs,), keys, q, prefix_len, k_tree,
                  v_tree, tree, Hkv, (), scale, softcap, window, slopes, out, lse, want_lse, ws, stream)
 
 
 def _rows(t, name, dtype, index, lead):
     """Check token rows [*lead, heads, D] with dense heads and evenly spaced tokens; returns (address, heads, D, stride)."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != index or index < 0:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
@@ -878,8 +882,8 @@ def _append(name, q, k, v, seq_start, prefix_len, freq, interleaved, pos_base, q
         op = _at(q_out, "q_out", k.dtype, index, N, Hq, D)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    sp = _at(seq_start, "seq_start", torch.int32, index, B + 1)
-    pp = _at(prefix_len, "prefix_len", torch.int32, index, B)
+    sp = _at(seq_start, "seq_start", _i32, index, B + 1)
+    pp = _at(prefix_len, "prefix_len", _i32, index, B)
     fp, rot, bp = _rope_args(freq, D, pos_base, index)
     if ws is None:
         ws = _new(stream, index, torch.uint8, kv_append_workspace_size())
@@ -914,7 +918,7 @@ def kv_append_paged(q, k, v, seq_start, prefix_len, k_pool, v_pool, block_table,
     blocks, _, bs, _ = _pool(k_pool)
     B, most = block_table.shape if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else (0, 0)
     cache = (_at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), _at(v_pool, "v_pool", dtype, index, blocks, Hkv, bs, D), blocks,
-             _at(block_table, "block_table", torch.int32, index, B, most), most, bs)
+             _at(block_table, "block_table", _i32, index, B, most), most, bs)
     return _append("kv_append_paged", q, k, v, seq_start, prefix_len, freq, interleaved, pos_base, q_out, ws, stream, index, B, cache)
 
 
@@ -930,7 +934,7 @@ def tree_rope(q, k, v, prefix_len, tree, freq=None, interleaved=False, pos_base=
     vp, Hv, Dv, vs = _rows(v, "v", dtype, index, (B, T))
     if Dk != D or (Hv, Dv) != (Hkv, D):
         raise ValueError("k and v must match, with q's head dimension")
-    pp = _at(prefix_len, "prefix_len", torch.int32, index, B)
+    pp = _at(prefix_len, "prefix_len", _i32, index, B)
     fp, rot, bp = _rope_args(freq, D, pos_base, index)
     q_out = _new(stream, index, dtype, B, Hq, T, D) if q_out is None else q_out
     k_out = _new(stream, index, dtype, B, Hkv, T, D) if k_out is None else k_out

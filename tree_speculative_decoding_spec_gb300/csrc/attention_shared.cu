@@ -348,17 +348,25 @@ HostPlan host_plan(Params& p, bool tc, bool shared, int ctas) {
     p.rowsS = p.nbb * p.rowsO;
     p.ctas = ctas;
     p.per = p.gT >= p.RB ? p.n_rbO : 1;
-    // costs in thirds of a pair's tile (1820 cycles): a narrow tile is bound by memory or by its
-    // softmax at two thirds of that, an item's rows take some 8000 or 5500 cycles to start and store
+    // Costs in thirds of a pair's tile (1700 cycles): a narrow tile is bound by memory or by its softmax at
+    // two thirds of that; an item's rows take some 8000, 5500 or (few rows) 3500 cycles to start and store.  An
+    // own column of plain scores ends in a partial tile and the tree's masks, worth another 14 (70B trees over
+    // 16K shared keys: the CTAs with own columns ran 450K cycles where the others ran 408K, 254 us without, 225
+    // with); where scores are transformed every tile is as slow as those are.  fp32 items start at no cost: a
+    // call that has fewer tiles than CTAs is cut into single ones (small scored case 28 us at 3, 23 at 0).
     const int last = p.gT - (p.n_rbO - 1) * p.RB;
+    const bool plain = !(p.softcap > 0.f || p.window > 0 || p.slopes);
     p.wF = 3;
-    p.fixF = tc ? 15 : 3;
-    auto cost = [&](int rows, int& w, int& fix) {
+    p.fixF = tc ? 15 : 0;
+    p.tailF = tc && plain ? 14 : 0;
+    auto cost = [&](int rows, int& w, int& fix, int& tail) {
         w = tc && rows <= kTcRows / 2 ? 2 : 3;
-        fix = !tc ? 3 : w == 3 ? 15 : rows > 32 ? 10 : 6;
+        fix = !tc ? 0 : w == 3 ? 15 : rows > 32 ? 10 : 6;
+        tail = w == 3 ? p.tailF : 0;
     };
-    cost(p.gT >= p.RB ? last : p.rowsS, p.wS, p.fixS);
-    cost(last, p.wO, p.fixO);
+    int none;
+    cost(p.gT >= p.RB ? last : p.rowsS, p.wS, p.fixS, none);
+    cost(last, p.wO, p.fixO, p.tailO);
     p.repS = tc && p.rowsS <= 32 ? 4 : 1;
     p.repO = tc && p.rowsO <= 32 ? 4 : 1;
     p.min_piece = tc ? 2 : 1;

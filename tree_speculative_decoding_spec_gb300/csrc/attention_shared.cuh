@@ -41,6 +41,7 @@ struct Params {
     int per;                           // blocks of one sequence's rows a shared column may be one of (1 when it holds whole sequences)
     // a tile's cost and an item's beside its tiles: blocks with more rows behind them, the last (or only) one
     int wF, wS, wO, fixF, fixS, fixO;
+    int tailF, tailO;                  // of an own column's partial tile and its tree's masks, behind its tiles
     int min_piece;                     // tiles of the shortest split
     int repS, repO;                    // copies of a row in an item (see attention_shared_tc.cu)
     float scale, softcap;              // softcap 0: none
@@ -92,8 +93,8 @@ struct Place {
     __device__ __forceinline__ Place(const Params& p, bool shared, int n_) : n(n_) {
         w = shared ? p.wS : p.wO;
         fix = shared ? p.fixS : p.fixO;
-        full = n * p.wF + p.fixF;
-        group = ((shared ? p.per : p.n_rbO) - 1) * full + n * w + fix;
+        full = n * p.wF + p.fixF + (shared ? 0 : p.tailF);
+        group = ((shared ? p.per : p.n_rbO) - 1) * full + n * w + fix + (shared ? 0 : p.tailO);
     }
 };
 
