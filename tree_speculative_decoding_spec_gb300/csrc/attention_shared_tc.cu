@@ -186,71 +186,95 @@ __device__ __forceinline__ float max64(const float (&x)[64]) {
     return fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
 
-// cap2 tanh(s k) for 64 raw scores s, cap2 = softcap log2 e, k = scale / softcap.  Where the whole
-// warp's |s k| stay small (caps sit far above ordinary scores) by tanh(u) = u (1 + u^2 P(u^2)): P of
-// degree 1 up to |u| = 0.16 and of degree 4 up to 0.7, fitted by weighted least squares whose
-// weights are iterated towards an even relative error, 3.5e-8 and 1.6e-8 at most; five and eight
-// packed products for two scores, on the FMA units that the softmax leaves idle.  Else as cap2 (1 - 2 / (e^(2u) + 1)), two
-// special-function operations a score, the pipe the exponentials need (a 128-key tile of the 32K
-// capped layer: 4000 cycles).  `in`: the lane's row is one of the
-// block, `whole`: so is every key: what stale memory made of others must not choose the way, or
-// results would vary with it.
-__device__ __forceinline__ void cap64(float (&x)[64], float scale2, float k, float cap2, bool in, bool whole) {
-    float a[8];
+__device__ __forceinline__ float min64(const float (&x)[64]) {
+    float m[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        a[e] = fmax3(fmax3(fabsf(x[e]), fabsf(x[e + 8]), fabsf(x[e + 16])), fmax3(fabsf(x[e + 24]), fabsf(x[e + 32]), fabsf(x[e + 40])),
-                     fmaxf(fabsf(x[e + 48]), fabsf(x[e + 56])));
-    const float most = fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7])) * k;
-    const float z = k * k, z2 = z * z;
-    const unsigned long long sc = pk2(scale2, scale2), zero = pk2(0.f, 0.f);
-    if (whole && k < 100.f && __all_sync(0xffffffffu, !in || most <= 0.16f)) {
-        const float c0 = -0.33331832037990994f * z, c1 = 0.13143139243852983f * z2;
-        const unsigned long long p0 = pk2(c0, c0), p1 = pk2(c1, c1);
-#pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-            const unsigned long long v = pk2(x[e], x[e + 1]);
-            const unsigned long long w = ffma2(v, v, zero);
-            const unsigned long long q = ffma2(w, ffma2(w, p1, p0), zero);
-            const unsigned long long lin = ffma2(v, sc, zero);
-            upk2(ffma2(lin, q, lin), x[e], x[e + 1]);
-        }
-    } else if (whole && k < 100.f && __all_sync(0xffffffffu, !in || most <= 0.7f)) {
-        const float c0 = -0.33333189899901133f * z, c1 = 0.13329110734967342f * z2, c2 = -0.053558861130687065f * z2 * z,
-                    c3 = 0.02009196966007083f * z2 * z2, c4 = -0.005138661857974488f * z2 * z2 * z;
-        const unsigned long long p0 = pk2(c0, c0), p1 = pk2(c1, c1), p2 = pk2(c2, c2), p3 = pk2(c3, c3), p4 = pk2(c4, c4);
-#pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-            const unsigned long long v = pk2(x[e], x[e + 1]);
-            const unsigned long long w = ffma2(v, v, zero);
-            unsigned long long q = ffma2(w, p4, p3);
-            q = ffma2(w, q, p2);
-            q = ffma2(w, q, p1);
-            q = ffma2(w, q, p0);
-            q = ffma2(w, q, zero);
-            const unsigned long long lin = ffma2(v, sc, zero);
-            upk2(ffma2(lin, q, lin), x[e], x[e + 1]);
-        }
-    } else {
-        const float k2 = 2.f * kLog2e * k;
-#pragma unroll
-        for (int e = 0; e < 64; ++e) x[e] = fmaf(-2.f * cap2, rcp(ex2(x[e] * k2) + 1.f), cap2);
-    }
+        m[e] = fmin3(fmin3(x[e], x[e + 8], x[e + 16]), fmin3(x[e + 24], x[e + 32], x[e + 40]), fminf(x[e + 48], x[e + 56]));
+    return fmin3(fmin3(m[0], m[1], m[2]), fmin3(m[3], m[4], m[5]), fminf(m[6], m[7]));
 }
 
-// A tile's maximum `tmax` joins the row's.  The reference moves only when it grew by more than 2^8; the
-// TMEM accesses are the whole warp's, so its rows rescale together (by 1 where nothing grew).
+// 2^arg(x) of 64 scores, two at a time, as bf16 pairs to TMEM; returns their sum before the rounding.
+template <typename Arg>
+__device__ __forceinline__ float weigh64(const float (&x)[64], uint32_t addr, Arg arg) {
+    unsigned long long acc2 = pk2(0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t packed[8];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            const int e = 16 * q + 2 * h;
+            float x0, x1;
+            upk2(arg(pk2(x[e], x[e + 1])), x0, x1);
+            const float a0 = ex2(x0), a1 = ex2(x1);
+            acc2 = fadd2(acc2, pk2(a0, a1));
+            const __nv_bfloat162 pr = __floats2bfloat162_rn(a0, a1);   // .x (lower key) low
+            packed[h] = *reinterpret_cast<const uint32_t*>(&pr);
+        }
+        tmem_st8(addr + 8 * q, packed);
+    }
+    float acc0, acc1;
+    upk2(acc2, acc0, acc1);
+    return acc0 + acc1;
+}
+
+// cap2 tanh(s k) of raw scores s, cap2 = softcap log2 e, k = scale / softcap.  Where the whole warp's
+// |s k| stay small (caps sit far above ordinary scores) by tanh(u) = u (1 + u^2 P(u^2)): P of degree 1
+// up to |u| = 0.16 and of degree 4 up to 0.7, fitted by weighted least squares whose weights are
+// iterated towards an even relative error, 3.5e-8 and 1.6e-8 at most; on the FMA units that the softmax
+// leaves idle, and the last product is the exponent's: s (cap2 k (1 + ...)) - reference.  Else as
+// cap2 (1 - 2 / (e^(2u) + 1)), two special-function operations a score, the pipe the exponentials need.
+struct Cap {
+    float k, cap2, scale2;
+    __device__ __forceinline__ explicit Cap(const Params& p) : k(p.scale / p.softcap), cap2(p.softcap * kLog2e), scale2(p.scale * kLog2e) {}
+    __device__ __forceinline__ float operator()(float s) const { return fmaf(-2.f * cap2, rcp(ex2(s * (2.f * kLog2e * k)) + 1.f), cap2); }
+    // the largest |s k| of the warp's rows; what stale memory made of others must not choose the way, or
+    // results would vary with it
+    __device__ __forceinline__ bool below(float most, float limit, bool in) const {
+        return k < 100.f && __all_sync(0xffffffffu, !in || most * k <= limit);
+    }
+    struct Small {
+        unsigned long long p0, p1, sc;
+        __device__ __forceinline__ explicit Small(const Cap& c) {
+            const float z = c.k * c.k, c0 = -0.33331832037990994f * z * c.scale2, c1 = 0.13143139243852983f * z * z * c.scale2;
+            p0 = pk2(c0, c0), p1 = pk2(c1, c1), sc = pk2(c.scale2, c.scale2);
+        }
+        __device__ __forceinline__ unsigned long long factor(unsigned long long v) const {
+            const unsigned long long w = ffma2(v, v, pk2(0.f, 0.f));
+            return ffma2(w, ffma2(w, p1, p0), sc);
+        }
+    };
+    struct Middle {
+        unsigned long long p0, p1, p2, p3, p4, sc;
+        __device__ __forceinline__ explicit Middle(const Cap& c) {
+            const float z = c.k * c.k, z2 = z * z, s = c.scale2;
+            const float c0 = -0.33333189899901133f * z * s, c1 = 0.13329110734967342f * z2 * s, c2 = -0.053558861130687065f * z2 * z * s,
+                        c3 = 0.02009196966007083f * z2 * z2 * s, c4 = -0.005138661857974488f * z2 * z2 * z * s;
+            p0 = pk2(c0, c0), p1 = pk2(c1, c1), p2 = pk2(c2, c2), p3 = pk2(c3, c3), p4 = pk2(c4, c4), sc = pk2(s, s);
+        }
+        __device__ __forceinline__ unsigned long long factor(unsigned long long v) const {
+            const unsigned long long w = ffma2(v, v, pk2(0.f, 0.f));
+            return ffma2(w, ffma2(w, ffma2(w, ffma2(w, ffma2(w, p4, p3), p2), p1), p0), sc);
+        }
+    };
+};
+
+// A tile's maximum `tmax` joins the row's.  The reference moves only when it grew by more than 2^8, and
+// to a whole number: what was weighed against the old one is then off by a power of two, and O and the
+// `p_cols` columns of weights at p_addr (the tile's first half, not yet given to PV) are rescaled
+// without rounding.  The TMEM accesses are the whole warp's, so its rows rescale together (by 1 where
+// nothing grew).
 template <int D>
-__device__ __forceinline__ bool grow(float tmax, bool in, float& m_used, float& l, uint32_t o_addr, uint64_t* pv_bar, uint32_t pv_parity,
-                                     volatile int* abort_flag) {
+__device__ __forceinline__ bool grow(float tmax, bool in, float& m_used, float& l, uint32_t o_addr, uint32_t p_addr, int p_cols,
+                                     uint64_t* pv_bar, uint32_t pv_parity, volatile int* abort_flag) {
     float m_new = m_used, alpha = 1.f;
     bool rescale = false;
     if (tmax > m_used + 8.f) {
+        m_new = ceilf(tmax);
         if (m_used != -INFINITY) {
             rescale = in;   // rows past the block hold whatever memory held
-            alpha = ex2(m_used - tmax);
+            alpha = ex2(m_used - m_new);
         }
-        m_new = tmax;
     }
     m_used = m_new;
     if (__any_sync(0xffffffffu, rescale)) {
@@ -265,16 +289,31 @@ __device__ __forceinline__ bool grow(float tmax, bool in, float& m_used, float& 
             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
             tmem_st16(o_addr + c, o);
         }
+        tmem_st_wait();
+        const __nv_bfloat162 a2 = __float2bfloat162_rn(alpha);
+#pragma unroll 1
+        for (int c = 0; c < p_cols; c += 16) {
+            uint32_t w[16];
+            tmem_ld16(p_addr + c, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), a2);
+                w[e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            tmem_st16(p_addr + c, w);
+        }
         l *= alpha;
     }
     return true;
 }
 
-// One softmax thread's work on a tile of 64 * halves keys: wait for S, transform, mask, running
-// maximum (rescaling O where it grew), weights back as bf16 pairs over the scores.  Two passes
-// over the scores, 64 at a time, transformed and masked ones written back in between: a row of
-// 128 in registers, all of it unrolled, is code that the instruction cache does not hold (a
-// first tile took 9 us, one in a hundred afterwards 2 us).
+// One softmax thread's work on a tile of 64 * halves keys: wait for S, then 64 scores at a time
+// transform, mask, running maximum (rescaling what was weighed so far where it grew) and the weights
+// back as bf16 pairs over scores already read.  (A row of 128 in registers, all of it unrolled with
+// its transforms, is code that the instruction cache does not hold: a first tile took 9 us, one in a
+// hundred afterwards 2 us.  Transformed scores written back and read again by a second pass took
+// 1200 cycles more per 128 keys.)
 // pv_bar: the barrier of the group's previous PV, NULL where S complete implies it.
 // landed(): called once S is complete; release(h): the weights of keys 64 h .. are in place.
 template <int D, bool kScored, typename Landed, typename Release>
@@ -295,25 +334,66 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
         return true;
     }
     const float scale2 = p.scale * kLog2e;
-    const bool transformed = kScored && (p.softcap > 0.f || p.slopes);
-    const float in_scale = transformed ? 1.f : scale2;   // what the exponent's FFMA still multiplies by
-    float top = -INFINITY;
+    const bool capped = kScored && p.softcap > 0.f, biased = kScored && p.slopes;
+    const float in_scale = capped || biased ? 1.f : scale2;   // what the exponent's FFMA still multiplies by
 #pragma unroll 1
     for (int h = 0; h < halves; ++h) {
         float x[64];
         load64(s_addr + 64 * h, x);
-        bool changed = transformed;
         const int nv = min(max(tl.nvalid - 64 * h, 0), 64);
         uint64_t bits = nv >= 64 ? ~0ull : (1ull << nv) - 1ull;
         bits &= h ? seen1 : seen0;
         bool masked = tl.tree || nv < 64;
+        auto reach = [&](float top) {   // the half's maximum
+            return grow<D>(top, row.in, m_used, l, o_addr, s_addr, 32 * h, pv_bar, pv_parity, abort_flag);
+        };
+        auto reference = [&]() {
+            const float r = m_used == -INFINITY ? 0.f : -m_used;
+            return pk2(r, r);
+        };
+        const uint32_t w_addr = s_addr + 32 * h;
         if constexpr (kScored) {
             const int k0 = tl.k0 + 64 * h;
             const int kbase = it.shared ? k0 : it.Ls + k0;      // position of the first key (not the tree's)
             const int depth = row.pos - it.Ls - it.L;           // (own items) the node's
-            if (p.softcap > 0.f) cap64(x, scale2, p.scale / p.softcap, p.softcap * kLog2e, row.in, nv == 64);
-            if (p.slopes) {
-                const float f = p.softcap > 0.f ? 1.f : scale2;
+            if (p.window > 0) {
+                if (tl.tree) {
+                    if (p.window <= SPEC_MAX_DEPTH)
+                        for (uint64_t left = bits; left; left &= left - 1) {
+                            const int e = __ffsll(static_cast<long long>(left)) - 1;
+                            if (depth - p.depth[k0 + e] >= p.window) bits &= ~(1ull << e);
+                        }
+                } else {
+                    const int lo = min(max(row.pos - p.window + 1 - kbase, 0), 64);   // first key seen
+                    bits &= lo >= 64 ? 0ull : ~0ull << lo;
+                    masked = masked || __any_sync(0xffffffffu, lo > 0);
+                }
+            }
+            if (capped) {
+                const Cap cap(p);
+                if (!masked && !biased) {
+                    // the cap keeps the order, so the raw scores' extremes give the capped ones' maximum
+                    const float top = max64(x), most = fmaxf(top, -min64(x));
+                    if (cap.below(most, 0.16f, row.in)) {
+                        if (!reach(cap(top))) return false;
+                        const Cap::Small f(cap);
+                        const unsigned long long nm2 = reference();
+                        l += weigh64(x, w_addr, [&](unsigned long long v) { return ffma2(v, f.factor(v), nm2); });
+                        continue;
+                    }
+                    if (cap.below(most, 0.7f, row.in)) {
+                        if (!reach(cap(top))) return false;
+                        const Cap::Middle f(cap);
+                        const unsigned long long nm2 = reference();
+                        l += weigh64(x, w_addr, [&](unsigned long long v) { return ffma2(v, f.factor(v), nm2); });
+                        continue;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 64; ++e) x[e] = cap(x[e]);
+            }
+            if (biased) {
+                const float f = capped ? 1.f : scale2;
                 if (tl.tree) {
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
@@ -332,19 +412,6 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
                         upk2(ffma2(pk2(x[e], x[e + 1]), f2, ffma2(s2, pk2(static_cast<float>(e), static_cast<float>(e + 1)), b2)), x[e], x[e + 1]);
                 }
             }
-            if (p.window > 0) {
-                if (tl.tree) {
-                    if (p.window <= SPEC_MAX_DEPTH)
-                        for (uint64_t left = bits; left; left &= left - 1) {
-                            const int e = __ffsll(static_cast<long long>(left)) - 1;
-                            if (depth - p.depth[k0 + e] >= p.window) bits &= ~(1ull << e);
-                        }
-                } else {
-                    const int lo = min(max(row.pos - p.window + 1 - kbase, 0), 64);   // first key seen
-                    bits &= lo >= 64 ? 0ull : ~0ull << lo;
-                    masked = masked || __any_sync(0xffffffffu, lo > 0);
-                }
-            }
         }
         if (masked) {
             const uint32_t w0 = static_cast<uint32_t>(bits), w1 = static_cast<uint32_t>(bits >> 32);
@@ -353,41 +420,12 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
                 if (!((w0 >> e) & 1u)) x[e] = -INFINITY;
                 if (!((w1 >> e) & 1u)) x[e + 32] = -INFINITY;
             }
-            changed = true;
         }
-        if (changed) store64(s_addr + 64 * h, x);
-        top = fmaxf(top, max64(x));
+        if (!reach(max64(x) * in_scale)) return false;
+        const unsigned long long sc2 = pk2(in_scale, in_scale), nm2 = reference();
+        l += weigh64(x, w_addr, [&](unsigned long long v) { return ffma2(v, sc2, nm2); });
     }
-    if constexpr (kScored) tmem_st_wait();
-    else if (tl.tree || tl.nvalid < 64 * halves) tmem_st_wait();
-    if (!grow<D>(top * in_scale, row.in, m_used, l, o_addr, pv_bar, pv_parity, abort_flag)) return false;
-    const float nmref = m_used == -INFINITY ? 0.f : -m_used;
-    const unsigned long long sc2 = pk2(in_scale, in_scale), nm2 = pk2(nmref, nmref);
-#pragma unroll 1
-    for (int h = 0; h < halves; ++h) {
-        float x[64];
-        load64(s_addr + 64 * h, x);
-#pragma unroll
-        for (int qc = 0; qc < 2; ++qc) {
-            uint32_t packed[16];
-            unsigned long long acc2 = pk2(0.f, 0.f);
-#pragma unroll
-            for (int h2 = 0; h2 < 16; ++h2) {
-                const int e0 = qc * 32 + 2 * h2;
-                float x0, x1;
-                upk2(ffma2(pk2(x[e0], x[e0 + 1]), sc2, nm2), x0, x1);
-                const float a0 = ex2(x0), a1 = ex2(x1);
-                acc2 = fadd2(acc2, pk2(a0, a1));
-                const __nv_bfloat162 pr = __floats2bfloat162_rn(a0, a1);   // .x (lower key) low
-                packed[h2] = *reinterpret_cast<const uint32_t*>(&pr);
-            }
-            float acc0, acc1;
-            upk2(acc2, acc0, acc1);
-            l += acc0 + acc1;
-            tmem_st16(s_addr + 32 * h + 16 * qc, packed);
-        }
-        release(h);
-    }
+    for (int h = 0; h < halves; ++h) release(h);
     return true;
 }
 
@@ -437,7 +475,7 @@ __device__ __forceinline__ bool softmax_pair(const Params& p, const Tile& tl, co
     uint32_t a[32], b[32];
     tmem_ld32(s_addr, a);
     const float scale2 = p.scale * kLog2e;
-    if (!grow<D>(top * scale2, row.in, m_used, l, o_addr, nullptr, 0, abort_flag)) return false;
+    if (!grow<D>(top * scale2, row.in, m_used, l, o_addr, 0, 0, nullptr, 0, abort_flag)) return false;
     const float nmref = m_used == -INFINITY ? 0.f : -m_used;
     const unsigned long long sc2 = pk2(scale2, scale2), nm2 = pk2(nmref, nmref);
     auto weigh = [&](const uint32_t (&x)[32], int c) {   // weights 32 c .. of the row, to columns 16 c ..
@@ -535,7 +573,7 @@ __device__ __forceinline__ bool softmax_few(const Params& p, const Desc& it, con
         if (!((bits >> e) & 1u)) x[e] = -INFINITY;
     const float top = fmax3(fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8])),
                             fmax3(x[9], x[10], x[11]), fmax3(fmax3(x[12], x[13], x[14]), x[15], x[15]));
-    if (!grow<D>(top, row.in, m_used, l, o_addr, pv_bar, pv_parity, abort_flag)) return false;
+    if (!grow<D>(top, row.in, m_used, l, o_addr, 0, 0, pv_bar, pv_parity, abort_flag)) return false;
     const float nmref = m_used == -INFINITY ? 0.f : -m_used;
     uint32_t packed[8];
     float sum = 0.f;
