@@ -226,14 +226,15 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
 
 // ---------------------------------------------------------------- the join
 
-// One CTA of four warps per (sequence, KV head, 32 rows of its gT), each warp a quarter of the
-// columns.  Lanes are rows, so the partials are read as whole lines; with fewer than 32 rows the
+// One CTA of eight warps per (sequence, KV head, 32 rows of its gT), each warp an eighth of the
+// columns (four warps with twice the columns each: 1.5 us more in most cases).  Lanes are rows, so the partials are read as whole lines; with fewer than 32 rows the
 // lanes left over take other parts of the same rows (lane = part * R + row), and shuffles add
 // them up.  The output goes through shared memory to leave as whole rows.  Bound by reading the
 // partials once, and for few rows by the latency of the look-ups before that.
+constexpr int kJoin = 256;
 template <typename T, int D>
-__global__ void __launch_bounds__(128) k_attn_shared_join(const Params p, int n_rg, int R) {
-    constexpr int C = D / 4 / 4;   // float4 columns per warp
+__global__ void __launch_bounds__(kJoin) k_attn_shared_join(const Params p, int n_rg, int R) {
+    constexpr int C = D / 4 / (kJoin / 32);   // float4 columns per warp
     __shared__ T tile[32][D + 16 / sizeof(T)];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = divide(blockIdx.x, n_rg), r0 = (blockIdx.x - col * n_rg) * 32;
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(128) k_attn_shared_join(const Params p, int n_
     __syncthreads();
     constexpr int E = 16 / sizeof(T);
     const int rows = min(32, p.gT - r0);
-    for (int x = threadIdx.x; x < rows * (D / E); x += 128) {
+    for (int x = threadIdx.x; x < rows * (D / E); x += kJoin) {
         const int r = x / (D / E), c = x % (D / E);
         *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (row0 + r) * D + c * E) = *reinterpret_cast<const uint4*>(&tile[r][c * E]);
     }
@@ -348,21 +349,29 @@ HostPlan host_plan(Params& p, bool tc, bool shared, int ctas) {
     p.rowsS = p.nbb * p.rowsO;
     p.ctas = ctas;
     p.per = p.gT >= p.RB ? p.n_rbO : 1;
-    // Costs in thirds of a pair's tile (1700 cycles): a narrow tile is bound by memory or by its softmax at
-    // two thirds of that; an item's rows take some 8000, 5500 or (few rows) 3500 cycles to start and store.  An
-    // own column of plain scores ends in a partial tile and the tree's masks, worth another 14 (70B trees over
-    // 16K shared keys: the CTAs with own columns ran 450K cycles where the others ran 408K, 254 us without, 225
-    // with); where scores are transformed every tile is as slow as those are.  fp32 items start at no cost: a
-    // call that has fewer tiles than CTAs is cut into single ones (small scored case 28 us at 3, 23 at 0).
+    // Costs.  fp32: tiles alone, so that a call with fewer tiles than CTAs is cut into single ones (small scored
+    // case 28 us where an item's start counted as a tile, 23 where it counts nothing).  Tensor cores, in thirds
+    // of a pair's tile (1700 cycles): a narrow tile, bound by memory or by its softmax, takes two thirds of that,
+    // an item's rows some 8000, 5500 or (few rows) 3500 cycles to start and store.  An own column of plain
+    // scores ends in a partial tile and the tree's masks, worth another 14 (70B trees over 16K shared keys: the
+    // CTAs with own columns ran 450K cycles where the others ran 408K, 254 us without, 225 with); where scores
+    // are transformed every tile is as slow as those.  Capped scores take the softmax longer, a pair's two
+    // groups in turn on the same units: a narrow tile is four sevenths (32K capped 281 us at two thirds, 269).
+    struct Costs {
+        int pair, narrow, fix_pair, fix_narrow, fix_few, tail;
+    };
+    const Costs c = !tc ? Costs{1, 1, 0, 0, 0, 0}
+                    : p.softcap > 0.f ? Costs{7, 4, 35, 23, 14, 0}
+                    : Costs{3, 2, 15, 10, 6, p.window > 0 || p.slopes ? 0 : 14};
     const int last = p.gT - (p.n_rbO - 1) * p.RB;
-    const bool plain = !(p.softcap > 0.f || p.window > 0 || p.slopes);
-    p.wF = 3;
-    p.fixF = tc ? 15 : 0;
-    p.tailF = tc && plain ? 14 : 0;
+    p.wF = c.pair;
+    p.fixF = c.fix_pair;
+    p.tailF = c.tail;
     auto cost = [&](int rows, int& w, int& fix, int& tail) {
-        w = tc && rows <= kTcRows / 2 ? 2 : 3;
-        fix = !tc ? 0 : w == 3 ? 15 : rows > 32 ? 10 : 6;
-        tail = w == 3 ? p.tailF : 0;
+        const bool pair = rows > kTcRows / 2;
+        w = pair ? c.pair : c.narrow;
+        fix = pair ? c.fix_pair : rows > 32 ? c.fix_narrow : c.fix_few;
+        tail = pair ? c.tail : 0;
     };
     int none;
     cost(p.gT >= p.RB ? last : p.rowsS, p.wS, p.fixS, none);
@@ -390,10 +399,11 @@ static spec_status check_shapes(const spec_tree* t, int B, int Hq, int Hkv, int 
     if (Lmax < 1 || Lmax > (1 << 22)) return fail(SPEC_EINVAL, "Lmax = %d out of 1..2^22", Lmax);
     if (Ls < 0 || Ls > (1 << 22)) return fail(SPEC_EINVAL, "the shared capacity %d is out of 1..2^22", Ls);
     const int64_t rows = static_cast<int64_t>(B) * Hq * t->T;
-    // the line's length, were every block 64 rows high
-    const int64_t blocks = static_cast<int64_t>(Hkv) * ((static_cast<int64_t>(Hq / Hkv) * t->T + FR - 1) / FR);
-    const int64_t line = 3 * blocks * B * ((Lmax + 63) / 64 + (t->T + 63) / 64 + (Ls + 63) / 64 + 8);
-    if (line > INT32_MAX / 2) return fail(SPEC_EINVAL, "B * Hkv * (Lmax + the shared capacity) is too large for one call (%lld tiles)", static_cast<long long>(line));
+    // the line's length at the largest costs
+    const int high = dt == SPEC_BF16 ? kTcRows : FR;
+    const int64_t blocks = static_cast<int64_t>(Hkv) * ((static_cast<int64_t>(Hq / Hkv) * t->T + high - 1) / high);
+    const int64_t tiles = blocks * B * ((Lmax + 63) / 64 + (t->T + 63) / 64 + (Ls + 63) / 64 + 14);
+    if (7 * tiles > INT32_MAX / 2) return fail(SPEC_EINVAL, "B * Hkv * (Lmax + the shared capacity) is too large for one call (%lld tiles)", static_cast<long long>(tiles));
     if (rows > (1ll << 30)) return fail(SPEC_EINVAL, "B * Hq * T = %lld query rows exceed 2^30", static_cast<long long>(rows));
     return SPEC_OK;
 }
@@ -426,7 +436,7 @@ static spec_status join(const Params& p, cudaStream_t s) {
     while (R < 32 && R < p.gT) R *= 2;
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.Hkv * n_rg));
     SPEC_CUDA_TRY(launch_ex("attn_shared_join", p.D == 64 ? k_attn_shared_join<T, 64> : k_attn_shared_join<T, 128>, grid,
-                            dim3(128), 0, s, true, p, n_rg, R));
+                            dim3(kJoin), 0, s, true, p, n_rg, R));
     return SPEC_OK;
 }
 

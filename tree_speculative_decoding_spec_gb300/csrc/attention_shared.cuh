@@ -117,7 +117,7 @@ __device__ __forceinline__ Plan make_plan(const Params& p) {
     t.colsS = t.nS ? p.Hkv * p.n_rbS : 0;
     t.own0 = t.nS ? Place(p, true, t.nS).group * p.Hkv * divide(p.n_rbS, p.per) : 0;
     const int total = t.own0 + own * p.Hkv;
-    t.q = max(divide(total + p.ctas - 1, p.ctas), p.fixF + 3 * p.min_piece);
+    t.q = max(divide(total + p.ctas - 1, p.ctas), p.fixF + p.wF * p.min_piece);
     return t;
 }
 
@@ -136,7 +136,7 @@ struct Cuts {
         owner = i0 - 1;
         count = max(0, i1 - i0 + 1) + 1;
     }
-    __device__ __forceinline__ int tile(int place) const { return w == 3 ? (place - base) / 3 : w == 2 ? (place - base) / 2 : place - base; }
+    __device__ __forceinline__ int tile(int place) const { return divide(place - base, w); }
     __device__ __forceinline__ int begin(int k) const { return k == 0 ? 0 : tile((owner + k) * q); }
     __device__ __forceinline__ int end(int k) const { return k == count - 1 ? n : tile((owner + k + 1) * q); }
     // the workspace slot among `cols` columns: one per column, one per cut of the line
@@ -178,7 +178,7 @@ struct Walk {
     int b, base, col, L, n;    // next own column: sequence, place of its first column, column, keys, tiles
     __device__ __forceinline__ Walk(const Params& p, const Plan& t, int cta_) : cta(cta_) {
         const int lane = threadIdx.x & 31;
-        const int x = max(0, cta * t.q - p.fixF - 3 * p.min_piece);   // no earlier column has an item here
+        const int x = max(0, cta * t.q - p.fixF - p.wF * p.min_piece);   // no earlier column has an item here
         colS = t.nS ? min(divide(x, Place(p, true, t.nS).group) * p.per, t.colsS) : 0;
         b = p.B;
         base = t.own0;
