@@ -40,6 +40,10 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
     float* Vs = Ks + FK * LD;
     float* Ps = Vs + FK * LD;
     const int t = threadIdx.x, rg = t >> 4, kg = t & 15;
+    __shared__ int bad;
+    if (t == 0) bad = 0;
+    griddep_wait();
+    griddep_launch();   // the join may start launching: it waits for the partials
     const Plan plan = make_plan(p);
     if (blockIdx.x == 0 && t < 32) publish_plan(p, plan);
     const T* q = static_cast<const T*>(p.q);
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
                         load4(ksrc + row * D + c4 * 4, kv[u]);
                         load4(vsrc + row * D + c4 * 4, vv[u]);
                     } else {
-                        flag_status(p.ws, SPEC_EINVAL);   // the key reads as zeros
+                        bad = 1;   // the key reads as zeros
                     }
                 }
 #pragma unroll
@@ -222,6 +226,8 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
             }
         }
     }
+    __syncthreads();
+    if (t == 0) p.cta_status[blockIdx.x] = bad ? SPEC_EINVAL : SPEC_OK;
 }
 
 // ---------------------------------------------------------------- the join
@@ -243,6 +249,12 @@ __global__ void __launch_bounds__(kJoin) k_attn_shared_join(const Params p, int 
     const int i = r0 + lr;                        // row within gT
     const int n = own_tiles(p, own_len(p, b));
     griddep_wait();
+    if (blockIdx.x == 0 && warp == 0) {           // the call's status
+        int worst = SPEC_OK;
+        for (int i = lane; i < p.ctas; i += 32) worst = max(worst, p.cta_status[i]);
+        for (int o = 16; o > 0; o >>= 1) worst = max(worst, __shfl_xor_sync(0xffffffffu, worst, o));
+        if (lane == 0) *static_cast<int4*>(p.ws) = make_int4(worst, 0, 0, 0);
+    }
     const Plan t = *reinterpret_cast<const Plan*>(static_cast<unsigned char*>(p.ws) + kPlanOffset);
     const int rb = divide(r0, p.RB);              // 32 divides RB
     const int sb = p.gT >= p.RB ? b * p.n_rbO + rb : divide(b, p.nbb);
@@ -382,7 +394,8 @@ HostPlan host_plan(Params& p, bool tc, bool shared, int ctas) {
     const size_t per_row = sizeof(float) * (p.D + 4);
     const size_t items_s = shared ? static_cast<size_t>(p.Hkv) * p.n_rbS + ctas : 0;   // one slot per column and per cut
     const size_t items_o = static_cast<size_t>(p.B) * p.Hkv * p.n_rbO + ctas;
-    h.cum_off = kWsHeader;
+    h.status_off = kWsHeader;
+    h.cum_off = h.status_off + round_up(sizeof(int32_t) * static_cast<size_t>(ctas), 256);
     h.part_s_off = h.cum_off + round_up(sizeof(int32_t) * static_cast<size_t>(p.B), 256);
     h.part_o_off = h.part_s_off + round_up(items_s * p.rowsS * p.repS * per_row, 256);
     h.total = h.part_o_off + round_up(items_o * p.rowsO * p.repO * per_row, 256);
@@ -425,7 +438,7 @@ template <int D>
 static spec_status run_fma(const Params& p, cudaStream_t s) {
     const size_t smem = sizeof(float) * (FR * (D + 4) + 2 * FK * (D + 4) + FR * (FK + 4));
     SPEC_CUDA_TRY(cudaFuncSetAttribute(k_attn_shared_fma<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-    SPEC_CUDA_TRY(launch("attn_shared_fma", k_attn_shared_fma<D>, dim3(p.ctas), dim3(256), smem, s, p));
+    SPEC_CUDA_TRY(launch_ex("attn_shared_fma", k_attn_shared_fma<D>, dim3(p.ctas), dim3(256), smem, s, true, p));
     return SPEC_OK;
 }
 
@@ -473,10 +486,10 @@ static spec_status run(Params p, const spec_tree* tree, spec_dtype dt, float sca
     if (!p.ws || ws_bytes < h.total) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, h.total);
     if (!aligned16(p.ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
     unsigned char* base = static_cast<unsigned char*>(p.ws);
+    p.cta_status = reinterpret_cast<int32_t*>(base + h.status_off);
     p.cum = reinterpret_cast<int32_t*>(base + h.cum_off);
     p.part_s = reinterpret_cast<float4*>(base + h.part_s_off);
     p.part_o = reinterpret_cast<float4*>(base + h.part_o_off);
-    SPEC_CUDA_TRY(reset_device_status(p.ws, s));
     if (h.tc) {
         st = attn_shared_tc_run(p, p.ctas, s);
     } else {

@@ -56,7 +56,8 @@ struct Params {
     const void *q, *kc, *vc, *ks, *vs, *kt, *vt;
     void* out;
     float* lse;
-    void* ws;                          // status word, then the Plan, then cum [B + 1], then the items
+    void* ws;                          // status word and Plan, the CTAs' statuses, cum [B], the items
+    int32_t* cta_status;               // [ctas]
     int32_t* cum;                      // place on the line of each sequence's first column [B]
     float4 *part_s, *part_o;           // items: [D / 4 + 1][rows] float4: (m, l, -, -), then O
 };
@@ -268,7 +269,7 @@ __device__ __forceinline__ size_t row_of_q(const Params& p, const Item& it, int 
 
 struct HostPlan {
     bool tc;
-    size_t cum_off, part_s_off, part_o_off, total;
+    size_t status_off, cum_off, part_s_off, part_o_off, total;
 };
 
 // Fills the shape fields of p that follow from the sizes, and the workspace layout.

@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if ((smem_u32(smem) & 1023u) != 0) {   // the swizzle counts address bits: a base elsewhere would scramble tiles
-        if (threadIdx.x == 0) flag_status(p.ws, SPEC_EUNSUPPORTED);
+        griddep_wait();
+        if (threadIdx.x == 0) p.cta_status[blockIdx.x] = SPEC_EUNSUPPORTED;
         if (blockIdx.x == 0) {             // nothing to join
             for (int b = threadIdx.x; b < p.B; b += kThreads) p.cum[b] = 0;
             if (threadIdx.x == 0) *reinterpret_cast<Plan*>(static_cast<unsigned char*>(p.ws) + kPlanOffset) = Plan{0, 0, 0, 0x3fffffff, 0, 0};
@@ -624,11 +625,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
     uint64_t* kv_empty = kv_full + C::kFull;      // [stage]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + C::kStages);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert(C::kBars * 8 + 8 <= 512, "barriers and flags end before the descriptors");
+    int* status = reinterpret_cast<int*>(tmem_slot + 2);   // of this CTA: the join takes the largest
+    static_assert(C::kBars * 8 + 12 <= 512, "barriers and flags end before the descriptors");
     Desc* desc = reinterpret_cast<Desc*>(reinterpret_cast<uint8_t*>(bars) + 512);            // [slot]
     float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bars) + C::kExchange); // [group][row]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Plan plan{};
+    if (warp == 11) {   // its look-ups run beside the set-up
+        griddep_wait();
+        plan = make_plan(p);
+    }
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 2);
@@ -651,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
         for (int i = 0; i < C::kFull; ++i) mbar_init(&kv_full[i], 1);
         for (int i = 0; i < C::kStages; ++i) mbar_init(&kv_empty[i], 2);
         *abort_flag = 0;
+        *status = SPEC_OK;
         fence_mbar_init();
         mbar_arrive(&turn[0]);   // thread 0 has the first turn
     }
@@ -659,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    griddep_wait();
     griddep_launch();   // the join may start launching: it waits for the partials
 
     int U = 0;          // running number of stage uses, the same in every role
@@ -675,7 +684,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
     };
 
     if (warp == 11) {
-        const Plan plan = make_plan(p);
         if (blockIdx.x == 0) publish_plan(p, plan);
         const int tree_tiles = tiles_of(p.T);
         Walk walk(p, plan, blockIdx.x);
@@ -746,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
                         const int x = divide(tl.k0 + off, p.pg.bs);
                         int blk = table[x];
                         if (blk < 0 || blk >= p.pg.num_blocks) {
-                            flag_status(p.ws, SPEC_EINVAL);
+                            atomicMax(status, SPEC_EINVAL);
                             blk = 0;
                         }
                         row = (blk * p.Hkv + it.kvh) * p.pg.bs + (tl.k0 + off - x * p.pg.bs);
@@ -881,8 +889,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
                         if (!wait_p(1)) break;
                         tc_fence_after();
                         issue_pv(tmem + g * 128, smem_u32(sKV + v_use.stage() * C::kStage), 2 * kHalf, 1, nvalid, false);
-                        if (more) issue_s(tmem + g * 128, g, k_use.stage(), 2);
                         pass_turn();
+                        if (more) issue_s(tmem + g * 128, g, k_use.stage(), 2);
                         if (more) mma_commit(&s_full[2 * g]);
                         v_use.two_on();
                     }
@@ -1108,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
     }
     if (!ok) {
         if (lane == 0) {
-            flag_status(p.ws, SPEC_ETIMEOUT);
+            atomicMax(status, SPEC_ETIMEOUT);
             *abort_flag = 1;
         }
         __syncwarp();
@@ -1124,6 +1132,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
         if (warp == 9 || warp == 10) mbar_wait(drain, 0, 100000000ull);
     }
     __syncthreads();
+    if (threadIdx.x == 0) p.cta_status[blockIdx.x] = *status;
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
@@ -1137,7 +1146,7 @@ static spec_status launch_items(const Maps& m, const Params& p, int page_log, in
     static_assert(Cfg<D>::kSmem <= 232448, "shared memory of one CTA");
     auto kern = k_attn_shared_tc<D, kScored>;
     SPEC_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem));
-    SPEC_CUDA_TRY(launch("attn_shared_tc", kern, dim3(blocks), dim3(kThreads), Cfg<D>::kSmem, s, m, p, page_log));
+    SPEC_CUDA_TRY(launch_ex("attn_shared_tc", kern, dim3(blocks), dim3(kThreads), Cfg<D>::kSmem, s, true, m, p, page_log));
     return SPEC_OK;
 }
 
