@@ -505,7 +505,8 @@ size_t tree_attention_shared_workspace_size(const spec_tree* tree, int32_t B, in
  *   prefix_len        device [B], each in 0 .. Lmax (clamped), without the shared keys
  *   k_tree, v_tree    device [B, Hkv, T, D]
  *   score             host, or NULL
- *   out               device [B, Hq, T, D] in dt, the inputs' type (tree_attention's is float32)
+ *   out               device [B, Hq, T, D] in dt, the inputs' type (tree_attention's is float32);
+ *                     it must not overlap an input
  *   lse               device [B, Hq, T] float32, or NULL
  *   scale             > 0, or 0 for the usual 1/sqrt(D)
  * Shapes: Hq % Hkv == 0, D in {64, 128}, 1 <= Lshared, Lmax <= 2^22; T = 1 is the form for

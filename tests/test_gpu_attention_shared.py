@@ -385,3 +385,79 @@ def test_binding_refuses():
     c.block, c.kp, c.vp = 8, c.kp[:, :, :8].contiguous(), c.vp[:, :, :8].contiguous()
     with pytest.raises(c.st.SpecError, match="multiple of 16"):
         c.call()
+
+
+RISING = {
+    # 256 rows against 128 keys at a time, 128 rows and fewer against 64, few rows
+    "rows-256": dict(B=1, Hq=4, Hkv=1, D=128, T=64, lens=(700,), Lmax=700),
+    "rows-128": dict(B=2, Hq=4, Hkv=2, D=64, T=40, lens=(500, 130), Lmax=500, Ls=300),
+    "few-rows": dict(B=3, Hq=4, Hkv=2, D=128, T=2, lens=(400, 64, 9), Lmax=400, Ls=200),
+}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", [dict(), dict(softcap=300.0), dict(slopes=True)], ids=["plain", "cap", "bias"])
+@pytest.mark.parametrize("name", list(RISING))
+def test_maxima_that_keep_rising(name, score, dtype):
+    """Keys that grow along the line: the running maximum moves in every tile, also between a tile's halves."""
+    import torch
+    c = Case(dtype, **RISING[name], **score, gain=4.0)
+    n = c.Ls + c.Lmax
+    ramp = torch.linspace(0.1, 30.0, n, device="cuda")[:, None]
+    c.kc.mul_(ramp[c.Ls:])
+    if c.Ls:
+        c.ks.mul_(ramp[:c.Ls])
+    ws = c.workspace()
+    c.check(*c.call(ws=ws))
+    assert c.st.spec_read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("T", [64, 9, 1])
+@pytest.mark.parametrize("cap", [500.0, 50.0, 10.0, 3.0, 0.5])
+def test_caps_near_and_far_from_the_scores(cap, T):
+    """Whole tiles whose scores are small, middling and large beside the cap."""
+    for dtype in ("bf16", "f32"):
+        c = Case(dtype, B=2, Hq=8, Hkv=2, D=128, T=T, lens=(640, 200), Lmax=640, Ls=256, softcap=cap)
+        c.check(*c.call())
+
+
+def test_calls_in_a_row_wait_for_each_other():
+    """Inputs written just before a call and overwritten just after it, one workspace, nothing waited for in between."""
+    import torch
+    cases = [Case("bf16", B=4, Hq=8, Hkv=2, D=128, T=T, lens=(300, 17, 90, 0), Lmax=320, Ls=200, seed=i)
+             for i, T in enumerate((1, 9, 64, 3))]
+    alone = [c.call() for c in cases]
+    ws = max((c.workspace() for c in cases), key=len)
+    args = [(_i32([c.shared_len]), _i32(c.lens)) for c in cases]
+    names = ("q", "ks", "vs", "kc", "vc", "kt", "vt")
+    room = [{n: torch.empty_like(getattr(c, n)) for n in names} for c in cases]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(24):
+        c, x, (sl, L) = cases[i % 4], room[i % 4], args[i % 4]
+        for n in names:
+            x[n].copy_(getattr(c, n))
+        got.append(c.st.tree_attention_shared(x["q"], x["ks"], x["vs"], sl, x["kc"], x["vc"], L, x["kt"], x["vt"], c.tree, ws=ws))
+        for n in names:
+            x[n].fill_(float("nan"))
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, alone[i % 4][0]) and torch.equal(lse, alone[i % 4][1])
+
+
+def test_binding_names_what_is_wrong():
+    import torch
+    c = Case("bf16", B=2, Hq=4, Hkv=2, D=64, T=3, lens=(4, 3), Lmax=16, Ls=16)
+    st, L, sl = c.st, _i32(c.lens), _i32([16])
+    good = dict(q=c.q, k_shared=c.ks, v_shared=c.vs, shared_len=sl, k_cache=c.kc, v_cache=c.vc, prefix_len=L, k_tree=c.kt, v_tree=c.vt,
+                tree=c.tree)
+    st.tree_attention_shared(**good)
+    for wrong, err, text in (({"q": c.q.cpu()}, ValueError, "q must be a CUDA tensor"), ({"q": [1]}, TypeError, "q must be a torch.Tensor"),
+                             ({"q": c.q.half()}, TypeError, "float32 or bfloat16"), ({"q": c.q[0]}, ValueError, "4 dimensions"),
+                             ({"k_tree": c.kt.float()}, TypeError, "k_tree must be"), ({"v_tree": c.vt[:, :1]}, ValueError, "v_tree"),
+                             ({"k_cache": c.kc.transpose(1, 2)}, ValueError, "k_cache"), ({"v_cache": c.vc.cpu()}, ValueError, "v_cache"),
+                             ({"k_shared": c.ks[0]}, ValueError, "k_shared"), ({"shared_len": _i32([1, 2])}, ValueError, "one value"),
+                             ({"shared_len": sl.long()}, TypeError, "shared_len"), ({"prefix_len": _i32([1])}, ValueError, "prefix_len"),
+                             ({"tree": st.spec_tree_build([-1])}, ValueError, "the tree 1"), ({"out": c.q}, st.SpecError, "overlaps"),
+                             ({"ws": torch.empty(64, dtype=torch.uint8)}, ValueError, "ws must be a CUDA tensor")):
+        with pytest.raises(err, match=text):
+            st.tree_attention_shared(**{**good, **wrong})

@@ -294,3 +294,28 @@ def test_binding_refuses():
         x = z(6, 2, 64, device="cuda")
         kc = z(1, 2, 9, 64, device="cuda")
         st.kv_append(x, x, x, _dev32([0, 6]), _dev32([0]), kc, kc.clone(), q_out=x)
+
+
+def test_single_rows_and_odd_strides():
+    """One token of one sequence, tokens far apart, and a batch without tokens in front of one that has them."""
+    import torch
+    st = lib()
+    g = torch.Generator().manual_seed(1)
+    for dtype in ("bf16", "f32"):
+        wide = _rand(g, dtype, 9, 40, 64)                      # tokens 40 heads apart
+        q, k, v = wide[::4, :6], wide[::4, 6:8], wide[::4, 8:10]   # three tokens, every fourth row
+        freq = 100.0 ** (-np.arange(16) / 16)
+        kc, vc = _rand(g, dtype, 4, 2, 8, 64), _rand(g, dtype, 4, 2, 8, 64)
+        k0, v0 = _np(kc), _np(vc)
+        start, L = _dev32([0, 0, 1, 1, 3]), _dev32([3, 7, 8, 5])
+        q_out, ws = st.kv_append(q, k, v, start, L, kc, vc, freq=torch.tensor(freq, device="cuda"), interleaved=True)
+        assert st.spec_read_device_status(ws) == 0
+        ref_q, ref_k, ref_v, _ = rope.kv_append(_np(q), _np(k), _np(v), [0, 0, 1, 1, 3], [3, 7, 8, 5], k0, v0, freq, interleaved=True)
+        _assert_rotated(_np(q_out), ref_q, _np(q), freq, True, dtype, "q")
+        untouched = np.ones(k0.shape[:1] + k0.shape[2:3], dtype=bool)
+        untouched[1, 7] = untouched[3, 5] = untouched[3, 6] = False
+        for got, ref, old in ((_np(kc), ref_k, k0), (_np(vc), ref_v, v0)):
+            assert (got.transpose(0, 2, 1, 3)[untouched] == old.transpose(0, 2, 1, 3)[untouched]).all()
+        _assert_rotated(_np(kc)[1, :, 7], ref_k[1, :, 7], _np(k)[0], freq, True, dtype, "k")
+        _assert_rotated(_np(kc)[3, :, 5:7].transpose(1, 0, 2), ref_k[3, :, 5:7].transpose(1, 0, 2), _np(k)[1:], freq, True, dtype, "k")
+        assert (_np(vc)[3, :, 5:7] == ref_v[3, :, 5:7]).all()

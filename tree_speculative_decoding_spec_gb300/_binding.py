@@ -774,10 +774,10 @@ def tree_attention_shared(q, k_shared, v_shared, shared_len, k_cache, v_cache, p
     and prefix_len [B]: each sequence's own keys behind them.  softcap, window, slopes [Hq]: see spec_score."""
     index, dtype, _, (B, _, _, D) = _queries(q)
     _, Hkv, Lmax, _ = _queries(k_cache, "k_cache")[3]
-    Ls = k_shared.shape[1] if isinstance(k_shared, torch.Tensor) and k_shared.dim() == 3 else 0
+    own = _at(k_cache, "k_cache", dtype, index, B, Hkv, Lmax, D), _at(v_cache, "v_cache", dtype, index, B, Hkv, Lmax, D)
+    Ls = k_shared.shape[1] if isinstance(k_shared, _Tensor) and k_shared.dim() == 3 else 0
     keys = (_at(k_shared, "k_shared", dtype, index, Hkv, Ls, D), _at(v_shared, "v_shared", dtype, index, Hkv, Ls, D),
-            _one(shared_len, "shared_len", index), Ls, _at(k_cache, "k_cache", dtype, index, B, Hkv, Lmax, D),
-            _at(v_cache, "v_cache", dtype, index, B, Hkv, Lmax, D))
+            _one(shared_len, "shared_len", index), Ls, *own)
     return _attn("tree_attention_shared", tree_attention_shared_workspace_size, (Ls, Lmax), keys, q, prefix_len, k_tree, v_tree,
                  tree, Hkv, (Lmax,), scale, softcap, window, slopes, out, lse, want_lse, ws, stream)
 
@@ -789,8 +789,8 @@ def tree_attention_shared_paged(q, k_pool, v_pool, shared_table, shared_len, blo
     name blocks of the pools [num_blocks, Hkv, block_size, D]."""
     index, dtype, _, (B, _, _, D) = _queries(q)
     blocks, Hkv, bs, _ = _pool(k_pool)
-    n = shared_table.shape[0] if isinstance(shared_table, torch.Tensor) and shared_table.dim() == 1 else 0
-    most = block_table.shape[1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else 0
+    n = shared_table.shape[0] if isinstance(shared_table, _Tensor) and shared_table.dim() == 1 else 0
+    most = block_table.shape[1] if isinstance(block_table, _Tensor) and block_table.dim() == 2 else 0
     keys = (_at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), _at(v_pool, "v_pool", dtype, index, blocks, Hkv, bs, D), blocks,
             _at(shared_table, "shared_table", _i32, index, n), n, _one(shared_len, "shared_len", index),
             _at(block_table, "block_table", _i32, index, B, most), most, bs)
@@ -814,7 +814,7 @@ def tree_attention_scored_paged(q, k_pool, v_pool, block_table, prefix_len, k_tr
     """tree_attention_scored over a paged cache: pools [num_blocks, Hkv, block_size, D], block_table [B, max_blocks] int32."""
     index, dtype, _, (B, _, _, D) = _queries(q)
     blocks, Hkv, bs, _ = _pool(k_pool)
-    most = block_table.shape[1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else 0
+    most = block_table.shape[1] if isinstance(block_table, _Tensor) and block_table.dim() == 2 else 0
     keys = (_at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), _at(v_pool, "v_pool", dtype, index, blocks, Hkv, bs, D), blocks,
             _at(block_table, "block_table", _i32, index, B, most), most, bs)
     return _attn("tree_attention_scored_paged", tree_attention_scored_workspace_size, (most * bs,), keys, q, prefix_len, k_tree,
@@ -916,7 +916,7 @@ def kv_append_paged(q, k, v, seq_start, prefix_len, k_pool, v_pool, block_table,
     """kv_append into a paged cache: pools [num_blocks, Hkv, block_size, D], block_table [B, max_blocks] int32."""
     index, dtype, (_, Hkv, D) = _new_rows(k)
     blocks, _, bs, _ = _pool(k_pool)
-    B, most = block_table.shape if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else (0, 0)
+    B, most = block_table.shape if isinstance(block_table, _Tensor) and block_table.dim() == 2 else (0, 0)
     cache = (_at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), _at(v_pool, "v_pool", dtype, index, blocks, Hkv, bs, D), blocks,
              _at(block_table, "block_table", _i32, index, B, most), most, bs)
     return _append("kv_append_paged", q, k, v, seq_start, prefix_len, freq, interleaved, pos_base, q_out, ws, stream, index, B, cache)

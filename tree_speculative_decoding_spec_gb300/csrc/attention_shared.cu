@@ -480,6 +480,14 @@ static spec_status run(Params p, const spec_tree* tree, spec_dtype dt, float sca
     if (!aligned4(p.prefix_len) || !aligned4(p.shared_len) || !aligned4(p.slopes) || !aligned4(p.lse) ||
         !aligned4(p.pg.table) || !aligned4(p.shared_table))
         return fail(SPEC_EALIGN, "lengths, tables, slopes and lse must be 4-byte aligned");
+    const int64_t es = dt == SPEC_BF16 ? 2 : 4, out_bytes = static_cast<int64_t>(p.B) * p.Hq * p.T * p.D * es;
+    auto on_out = [&](const void* x, int64_t bytes) {   // items write out while others still read their rows
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p.out), b = reinterpret_cast<uintptr_t>(x);
+        return a < b + static_cast<uintptr_t>(bytes) && b < a + static_cast<uintptr_t>(out_bytes);
+    };
+    const int64_t tree_bytes = static_cast<int64_t>(p.B) * p.Hkv * p.T * p.D * es;
+    if (on_out(p.q, out_bytes) || on_out(p.kt, tree_bytes) || on_out(p.vt, tree_bytes))
+        return fail(SPEC_EINVAL, "out overlaps q, k_tree or v_tree");
     p.depth = tree->depth;
     p.anc = tree->anc;
     const HostPlan h = host_plan(p, dt == SPEC_BF16, shared, device_sm_count());
