@@ -194,41 +194,28 @@ __device__ __forceinline__ float min64(const float (&x)[64]) {
     return fmin3(fmin3(m[0], m[1], m[2]), fmin3(m[3], m[4], m[5]), fminf(m[6], m[7]));
 }
 
-// 2^arg(x) of N scores as bf16 pairs to TMEM; returns their sum before the rounding.  Sixteen at a
-// time, the next ones' arguments between the exponentials and what is made of them: left to itself, pair
-// by pair, one warp takes 555 cycles for 64 scores where this takes 377 (capped ones 856 and 602).
-template <int N, typename At, typename Arg>
-__device__ __forceinline__ float weigh(uint32_t addr, At at, Arg arg) {
-    unsigned long long y[8], s0 = pk2(0.f, 0.f), s1 = s0;
-    auto arguments = [&](int q) {
+// 2^arg(x) of 64 scores, two at a time, as bf16 pairs to TMEM; returns their sum before the rounding.
+template <typename Arg>
+__device__ __forceinline__ float weigh64(const float (&x)[64], uint32_t addr, Arg arg) {
+    unsigned long long acc2 = pk2(0.f, 0.f);
 #pragma unroll
-        for (int h = 0; h < 8; ++h) y[h] = arg(pk2(at(16 * q + 2 * h), at(16 * q + 2 * h + 1)));
-    };
-    arguments(0);
-#pragma unroll
-    for (int q = 0; q < N / 16; ++q) {
-        float w[16];
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-            float x0, x1;
-            upk2(y[h], x0, x1);
-            w[2 * h] = ex2(x0);
-            w[2 * h + 1] = ex2(x1);
-        }
-        if (q + 1 < N / 16) arguments(q + 1);
+    for (int q = 0; q < 4; ++q) {
         uint32_t packed[8];
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
-            unsigned long long& s = h & 1 ? s1 : s0;
-            s = fadd2(s, pk2(w[2 * h], w[2 * h + 1]));
-            const __nv_bfloat162 pr = __floats2bfloat162_rn(w[2 * h], w[2 * h + 1]);   // .x (lower key) low
+            const int e = 16 * q + 2 * h;
+            float x0, x1;
+            upk2(arg(pk2(x[e], x[e + 1])), x0, x1);
+            const float a0 = ex2(x0), a1 = ex2(x1);
+            acc2 = fadd2(acc2, pk2(a0, a1));
+            const __nv_bfloat162 pr = __floats2bfloat162_rn(a0, a1);   // .x (lower key) low
             packed[h] = *reinterpret_cast<const uint32_t*>(&pr);
         }
         tmem_st8(addr + 8 * q, packed);
     }
-    float a0, a1;
-    upk2(fadd2(s0, s1), a0, a1);
-    return a0 + a1;
+    float acc0, acc1;
+    upk2(acc2, acc0, acc1);
+    return acc0 + acc1;
 }
 
 // cap2 tanh(s k) of raw scores s, cap2 = softcap log2 e, k = scale / softcap.  Where the whole warp's
@@ -391,14 +378,14 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
                         if (!reach(cap(top))) return false;
                         const Cap::Small f(cap);
                         const unsigned long long nm2 = reference();
-                        l += weigh<64>(w_addr, [&](int e) { return x[e]; }, [&](unsigned long long v) { return ffma2(v, f.factor(v), nm2); });
+                        l += weigh64(x, w_addr, [&](unsigned long long v) { return ffma2(v, f.factor(v), nm2); });
                         continue;
                     }
                     if (cap.below(most, 0.7f, row.in)) {
                         if (!reach(cap(top))) return false;
                         const Cap::Middle f(cap);
                         const unsigned long long nm2 = reference();
-                        l += weigh<64>(w_addr, [&](int e) { return x[e]; }, [&](unsigned long long v) { return ffma2(v, f.factor(v), nm2); });
+                        l += weigh64(x, w_addr, [&](unsigned long long v) { return ffma2(v, f.factor(v), nm2); });
                         continue;
                     }
                 }
@@ -436,7 +423,7 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
         }
         if (!reach(max64(x) * in_scale)) return false;
         const unsigned long long sc2 = pk2(in_scale, in_scale), nm2 = reference();
-        l += weigh<64>(w_addr, [&](int e) { return x[e]; }, [&](unsigned long long v) { return ffma2(v, sc2, nm2); });
+        l += weigh64(x, w_addr, [&](unsigned long long v) { return ffma2(v, sc2, nm2); });
     }
     for (int h = 0; h < halves; ++h) release(h);
     return true;
@@ -491,23 +478,36 @@ __device__ __forceinline__ bool softmax_pair(const Params& p, const Tile& tl, co
     if (!grow<D>(top * scale2, row.in, m_used, l, o_addr, 0, 0, nullptr, 0, abort_flag)) return false;
     const float nmref = m_used == -INFINITY ? 0.f : -m_used;
     const unsigned long long sc2 = pk2(scale2, scale2), nm2 = pk2(nmref, nmref);
-    auto part = [&](const uint32_t (&x)[32], int c) {   // weights 32 c .. of the row, to columns 16 c ..
-        l += weigh<32>(s_addr + 16 * c, [&](int e) { return __uint_as_float(x[e]); },
-                       [&](unsigned long long v) { return ffma2(v, sc2, nm2); });
+    auto weigh = [&](const uint32_t (&x)[32], int c) {   // weights 32 c .. of the row, to columns 16 c ..
+        uint32_t packed[16];
+        unsigned long long acc2 = pk2(0.f, 0.f);
+#pragma unroll
+        for (int h2 = 0; h2 < 16; ++h2) {
+            float x0, x1;
+            upk2(ffma2(pk2(__uint_as_float(x[2 * h2]), __uint_as_float(x[2 * h2 + 1])), sc2, nm2), x0, x1);
+            const float a0 = ex2(x0), a1 = ex2(x1);
+            acc2 = fadd2(acc2, pk2(a0, a1));
+            const __nv_bfloat162 pr = __floats2bfloat162_rn(a0, a1);   // .x (lower key) low
+            packed[h2] = *reinterpret_cast<const uint32_t*>(&pr);
+        }
+        float acc0, acc1;
+        upk2(acc2, acc0, acc1);
+        l += acc0 + acc1;
+        tmem_st16(s_addr + 16 * c, packed);
     };
     // (weights go where scores have been read: 0 .. 31 behind scores 0 .. 63, 32 .. 63 behind 64 .. 127)
     tmem_ld_wait();
     tmem_ld32(s_addr + 32, b);
-    part(a, 0);
+    weigh(a, 0);
     tmem_ld_wait();
     tmem_ld32(s_addr + 64, a);
-    part(b, 1);
+    weigh(b, 1);
     release(0);
     tmem_ld_wait();
     tmem_ld32(s_addr + 96, b);
-    part(a, 2);
+    weigh(a, 2);
     tmem_ld_wait();
-    part(b, 3);
+    weigh(b, 3);
     release(1);
     return true;
 }
