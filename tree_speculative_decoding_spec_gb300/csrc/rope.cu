@@ -18,10 +18,13 @@
 // tokens.  Its data does not depend on the sequence the token belongs to, so
 // every thread issues the loads of its first unit before the CTA looks that up.
 // Eight CTAs an SM (32 registers a thread) keep the loads in flight: three units of
-// a thread loaded together took 64 registers and 58 us where this takes 50 (prompts of
-// 6569 tokens, 64 and 8 heads of 128: 269 MB, 5.4 TB/s of a copy's 6.8), half a token
-// per CTA 52.  32 trees of 64 nodes, 84 MB: 19.5 us; a single token of each of 64
-// sequences 3.9 us, one tree of 64 nodes 3.4 us, launch and look-ups.
+// a thread loaded together took 64 registers and 58 us where one at a time took 50.
+// What is left beside the loads is issue and shared memory: (cos, sin) laid out so
+// that neighbouring units read neighbouring 16 bytes, and heads found by a product
+// with a reciprocal, brought 50 to 44 us.  Prompts of 6569 tokens, 64 and 8 heads of
+// 128 (269 MB): 44 us, 6.1 TB/s of a copy's 6.8; 32 trees of 64 nodes (84 MB): 16.8 us;
+// one token of each of 64 sequences 3.8 us and one tree of 64 nodes 3.3 us, launch
+// and look-ups.
 #include <algorithm>
 
 #include "common.cuh"
@@ -51,7 +54,11 @@ struct Params {
     // tree
     const int32_t* depth;
     int T;
+    uint32_t inv_per, inv_nc;         // 2^32 over the units of a q or k head, of a v head, rounded up (0: one unit)
 };
+
+// u / d by its rounded-up reciprocal: exact while u * d < 2^32 (here u < 2^18, d <= 2^8).
+__device__ __forceinline__ int quotient(int u, uint32_t inv) { return inv ? static_cast<int>(__umulhi(static_cast<uint32_t>(u), inv)) : u; }
 
 // Where one token goes.
 struct Token {
@@ -185,7 +192,8 @@ __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
 template <typename T, int STYLE>
 __global__ void __launch_bounds__(kThreads, 8) k_rope(const Params p) {
     constexpr int E = Chunk<T>::E;
-    __shared__ float2 s_cs[kMaxD / 2];
+    // (cos, sin) of pair j; half style: two pairs of a unit as 16 bytes, neighbouring units side by side
+    __shared__ __align__(16) float2 s_cs[kMaxD / 2];
     __shared__ Token s_tok;
     int n = blockIdx.x;
     if (p.seq_start && --n < 0) {     // the append's extra CTA: the first, or the call would end with it
@@ -207,17 +215,17 @@ __global__ void __launch_bounds__(kThreads, 8) k_rope(const Params p) {
         Unit w;
         if (u < uq) {
             w.kind = 0;
-            w.head = u / per;
+            w.head = quotient(u, p.inv_per);
             w.c = u - w.head * per;
             w.src = static_cast<const T*>(p.q) + n * p.qs + static_cast<int64_t>(w.head) * p.D;
         } else if (u < uq + uk) {
             w.kind = 1;
-            w.head = (u - uq) / per;
+            w.head = quotient(u - uq, p.inv_per);
             w.c = u - uq - w.head * per;
             w.src = static_cast<const T*>(p.k) + n * p.ks + static_cast<int64_t>(w.head) * p.D;
         } else {
             w.kind = 2;
-            w.head = (u - uq - uk) / nc;
+            w.head = quotient(u - uq - uk, p.inv_nc);
             w.c = u - uq - uk - w.head * nc;
             w.src = static_cast<const T*>(p.v) + n * p.vs + static_cast<int64_t>(w.head) * p.D;
         }
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 8) k_rope(const Params p) {
         const double turns = s_tok.pos * (p.freq[j] * 0.15915494309189533577);   // 1 / (2 pi)
         float sn, cs;
         sincospif(2.f * static_cast<float>(turns - rint(turns)), &sn, &cs);
-        s_cs[j] = make_float2(cs, sn);
+        s_cs[STYLE == kHalf ? 2 * (((j % E) >> 1) * np + j / E) + (j & 1) : j] = make_float2(cs, sn);
     }
     __syncthreads();
     const int64_t hq = p.seq_start ? p.D : static_cast<int64_t>(p.T) * p.D;
@@ -259,10 +267,12 @@ __global__ void __launch_bounds__(kThreads, 8) k_rope(const Params p) {
             unpack(a, x);
             unpack(b, y);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float2 cs = s_cs[w.c * E + e];
+            for (int e = 0; e < E; e += 2) {
+                const float4 cs = reinterpret_cast<const float4*>(s_cs)[(e >> 1) * np + w.c];
                 xo[e] = x[e] * cs.x - y[e] * cs.y;
                 yo[e] = x[e] * cs.y + y[e] * cs.x;
+                xo[e + 1] = x[e + 1] * cs.z - y[e + 1] * cs.w;
+                yo[e + 1] = x[e + 1] * cs.w + y[e + 1] * cs.z;
             }
             a = pack(xo);
             *reinterpret_cast<uint4*>(dst + (w.c + np) * E) = pack(yo);
@@ -332,11 +342,14 @@ bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
 }
 
 template <typename T>
-spec_status run(const char* name, const Params& p, int tokens, cudaStream_t s) {
+spec_status run(const char* name, Params& p, int tokens, cudaStream_t s) {
     constexpr int E = Chunk<T>::E;
     const int style = p.interleaved ? (p.rot % E ? kScalar : kPairs) : (p.rot % (2 * E) ? kScalar : kHalf);
     const int nc = p.D / E;
     const int per = style == kHalf ? nc - p.rot / 2 / E : nc;
+    auto inverse = [](int d) { return d == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + d - 1) / d); };
+    p.inv_per = inverse(per);
+    p.inv_nc = inverse(nc);
     const int64_t total = static_cast<int64_t>((p.q ? p.Hq : 0) + p.Hkv) * per + static_cast<int64_t>(p.Hkv) * nc;
     // one CTA per token, or as many as give every SM four CTAs while each thread still has a unit
     const int most = static_cast<int>((total + kThreads - 1) / kThreads);
