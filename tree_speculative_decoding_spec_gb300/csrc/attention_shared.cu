@@ -23,22 +23,35 @@ namespace shr {
 
 // ---------------------------------------------------------------- CUDA-core items
 
-constexpr int FR = 64;   // rows of a block
+constexpr int FR = 64;   // rows of a block, at most
 constexpr int FK = kTile;   // keys of a tile
 
-// 256 threads; thread (rg, kg) = (t / 16, t % 16) holds rows 4 rg .. 4 rg + 3, keys
-// kg + 16 j of a tile and output columns 4 kg .. of each 64.  fp32 operands have no
-// tensor-core product of their own precision, so the FMA units bound this kernel:
-// 16 FMAs per 8 shared-memory loads in the score loop.
-template <int D>
-__global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
+// 256 threads; thread (rg, kg) = (t / 16, t % 16) holds R rows from R rg, keys kg + 16 j of a tile and
+// output columns 4 kg .. of each 64.  fp32 operands have no tensor-core product of their own precision,
+// so the FMA units and the shared memory that feeds them bound this kernel: at R = 4, 16 FMAs per 8
+// loads of 16 bytes for two keys in the score loop; a 64 x 64 tile of head dim 128 takes some 9 us of the 4.2 that
+// its FMAs alone would.  The next tile's keys and values arrive meanwhile (cp.async, two buffers); rows
+// are 16, 32 or 64 to a block as the call needs them, and items of head dim 64 go two to an SM: 8
+// sequences of 2368 keys and 13 nodes, 8 heads of 128, took 265 us before these three and 131 with them,
+// 21 of 896 keys and 12 nodes, 4 heads of 64, 65 and 41, and two trees of 75 nodes behind 3840 keys 84 and 75.
+__device__ __forceinline__ void copy_async16(float* dst, const float* src, bool ok) {   // zeros where not ok
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <int D, int R>
+__global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_attn_shared_fma(const Params p) {
     using T = float;
+    constexpr int FR = 16 * R;   // rows of a block
     constexpr int LD = D + 4, LP = FK + 4, DT = D / 16;
     extern __shared__ float4 smem4[];
     float* Qs = reinterpret_cast<float*>(smem4);
-    float* Ks = Qs + FR * LD;
-    float* Vs = Ks + FK * LD;
-    float* Ps = Vs + FK * LD;
+    float* KVs = Qs + FR * LD;              // two buffers: keys, then values of a tile
+    float* Ps = KVs + 4 * FK * LD;
     const int t = threadIdx.x, rg = t >> 4, kg = t & 15;
     __shared__ int bad;
     if (t == 0) bad = 0;
@@ -58,11 +71,11 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
             if (r < it.rows) load4(q + row_of_q(p, it, r) * D + c4 * 4, v);
             *reinterpret_cast<float4*>(&Qs[r * LD + c4 * 4]) = make_float4(v[0], v[1], v[2], v[3]);
         }
-        int node[4], pos[4];
-        float slope2[4], m_run[4], l_run[4], o[4][DT];
+        int node[R], pos[R];
+        float slope2[R], m_run[R], l_run[R], o[R][DT];
 #pragma unroll
-        for (int ii = 0; ii < 4; ++ii) {
-            const int r = min(4 * rg + ii, it.rows - 1);
+        for (int ii = 0; ii < R; ++ii) {
+            const int r = min(R * rg + ii, it.rows - 1);
             const int b = it.b + (p.gT < p.RB ? r / p.gT : 0);
             const int i = p.gT < p.RB ? r % p.gT : it.rb * p.RB + r;
             node[ii] = i % p.T;
@@ -75,75 +88,78 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
         }
         const int first = it.shared ? plan.sT0 : own_first(p, it.L);
         const int n_pre = it.shared ? plan.nS : own_tiles(p, it.L) - tiles_of(p.T);
+        // a tile's keys and values into buffer (tile - t0) % 2; keys past the end become zeros
+        auto fetch = [&](int tile) {
+            const bool tree = !it.shared && tile >= n_pre;
+            const int j0 = (tree ? tile - n_pre : first + tile) * FK;
+            const int j_end = tree ? p.T : it.shared ? plan.Ls : it.L;
+            float* dst = KVs + ((tile - it.t0) & 1) * (2 * FK * LD);
+            for (int x = t; x < FK * (D / 4); x += 256) {
+                const int jl = x / (D / 4), c4 = x % (D / 4), j = j0 + jl;
+                const T *ksrc = static_cast<const T*>(p.kt), *vsrc = static_cast<const T*>(p.vt);
+                size_t row = 0;
+                bool ok = j < j_end;
+                if (tree) {
+                    row = (static_cast<size_t>(it.b) * p.Hkv + it.kvh) * p.T + j;
+                } else if (p.pg.table) {   // the key's pool block and row
+                    ksrc = static_cast<const T*>(p.kc);
+                    vsrc = static_cast<const T*>(p.vc);
+                    if (ok) {
+                        const int blk = it.shared ? p.shared_table[j / p.pg.bs]
+                                                  : p.pg.table[static_cast<size_t>(it.b) * p.pg.max_blocks + j / p.pg.bs];
+                        ok = blk >= 0 && blk < p.pg.num_blocks;
+                        if (!ok) bad = 1;   // the key reads as zeros
+                        row = (static_cast<size_t>(ok ? blk : 0) * p.Hkv + it.kvh) * p.pg.bs + j % p.pg.bs;
+                    }
+                } else if (it.shared) {
+                    ksrc = static_cast<const T*>(p.ks);
+                    vsrc = static_cast<const T*>(p.vs);
+                    row = static_cast<size_t>(it.kvh) * p.Lshared + j;
+                } else {
+                    ksrc = static_cast<const T*>(p.kc);
+                    vsrc = static_cast<const T*>(p.vc);
+                    row = (static_cast<size_t>(it.b) * p.Hkv + it.kvh) * p.Lmax + j;
+                }
+                if (!ok) row = 0;
+                copy_async16(dst + jl * LD + c4 * 4, ksrc + row * D + c4 * 4, ok);
+                copy_async16(dst + FK * LD + jl * LD + c4 * 4, vsrc + row * D + c4 * 4, ok);
+            }
+            copy_async_commit();
+        };
+        fetch(it.t0);
         for (int tile = it.t0; tile < it.t1; ++tile) {
             const bool tree = !it.shared && tile >= n_pre;
             const int j0 = (tree ? tile - n_pre : first + tile) * FK;
             const int j_end = tree ? p.T : it.shared ? plan.Ls : it.L;
-            __syncthreads();
-            // four keys' and values' loads in flight per thread
-#pragma unroll 1
-            for (int x0 = t; x0 < FK * (D / 4); x0 += 4 * 256) {
-                float kv[4][4], vv[4][4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int jl = (x0 + u * 256) / (D / 4), c4 = (x0 + u * 256) % (D / 4);
-                    const int j = j0 + jl;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) kv[u][e] = vv[u][e] = 0.f;
-                    if (j >= j_end) continue;
-                    const T *ksrc, *vsrc;
-                    size_t row;
-                    bool ok = true;
-                    if (tree) {
-                        ksrc = static_cast<const T*>(p.kt);
-                        vsrc = static_cast<const T*>(p.vt);
-                        row = (static_cast<size_t>(it.b) * p.Hkv + it.kvh) * p.T + j;
-                    } else if (p.pg.table) {   // the key's pool block and row
-                        const int blk = it.shared ? p.shared_table[j / p.pg.bs]
-                                                  : p.pg.table[static_cast<size_t>(it.b) * p.pg.max_blocks + j / p.pg.bs];
-                        ok = blk >= 0 && blk < p.pg.num_blocks;
-                        ksrc = static_cast<const T*>(p.kc);
-                        vsrc = static_cast<const T*>(p.vc);
-                        row = (static_cast<size_t>(ok ? blk : 0) * p.Hkv + it.kvh) * p.pg.bs + j % p.pg.bs;
-                    } else if (it.shared) {
-                        ksrc = static_cast<const T*>(p.ks);
-                        vsrc = static_cast<const T*>(p.vs);
-                        row = static_cast<size_t>(it.kvh) * p.Lshared + j;
-                    } else {
-                        ksrc = static_cast<const T*>(p.kc);
-                        vsrc = static_cast<const T*>(p.vc);
-                        row = (static_cast<size_t>(it.b) * p.Hkv + it.kvh) * p.Lmax + j;
-                    }
-                    if (ok) {
-                        load4(ksrc + row * D + c4 * 4, kv[u]);
-                        load4(vsrc + row * D + c4 * 4, vv[u]);
-                    } else {
-                        bad = 1;   // the key reads as zeros
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int jl = (x0 + u * 256) / (D / 4), c4 = (x0 + u * 256) % (D / 4);
-                    *reinterpret_cast<float4*>(&Ks[jl * LD + c4 * 4]) = make_float4(kv[u][0], kv[u][1], kv[u][2], kv[u][3]);
-                    *reinterpret_cast<float4*>(&Vs[jl * LD + c4 * 4]) = make_float4(vv[u][0], vv[u][1], vv[u][2], vv[u][3]);
-                }
+            const float *Ks = KVs + ((tile - it.t0) & 1) * (2 * FK * LD), *Vs = Ks + FK * LD;
+            __syncthreads();   // the other buffer and P are read
+            if (tile + 1 < it.t1) {
+                fetch(tile + 1);
+                copy_async_wait<1>();
+            } else {
+                copy_async_wait<0>();
             }
             __syncthreads();
 
-            float s[4][4];
+            uint64_t seen[R];   // of a tree tile: the nodes' ancestors and themselves
+            if (tree) {
 #pragma unroll
-            for (int ii = 0; ii < 4; ++ii)
+                for (int ii = 0; ii < R; ++ii) seen[ii] = p.anc[static_cast<size_t>(node[ii]) * p.words + (j0 >> 6)];
+            }
+            float s[R][4];
+#pragma unroll
+            for (int ii = 0; ii < R; ++ii)
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) s[ii][jj] = 0.f;
 #pragma unroll 4
             for (int dd = 0; dd < D; dd += 4) {
-                float4 qa[4], kb[4];
+                float4 qa[R], kb[4];
 #pragma unroll
-                for (int ii = 0; ii < 4; ++ii) qa[ii] = *reinterpret_cast<const float4*>(&Qs[(4 * rg + ii) * LD + dd]);
+                for (int ii = 0; ii < R; ++ii) qa[ii] = *reinterpret_cast<const float4*>(&Qs[(R * rg + ii) * LD + dd]);
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) kb[jj] = *reinterpret_cast<const float4*>(&Ks[(kg + 16 * jj) * LD + dd]);
 #pragma unroll
-                for (int ii = 0; ii < 4; ++ii)
+                for (int ii = 0; ii < R; ++ii)
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj)
                         s[ii][jj] += qa[ii].x * kb[jj].x + qa[ii].y * kb[jj].y + qa[ii].z * kb[jj].z + qa[ii].w * kb[jj].w;
@@ -154,17 +170,17 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
                 const bool in = j < j_end;
                 const int kpos = tree ? (in ? plan.Ls + it.L + p.depth[j] : 0) : it.shared ? j : plan.Ls + j;
 #pragma unroll
-                for (int ii = 0; ii < 4; ++ii) {
+                for (int ii = 0; ii < R; ++ii) {
                     const int far = pos[ii] - kpos;
                     bool ok = in && (p.window <= 0 || far < p.window);
-                    if (tree && ok) ok = (p.anc[static_cast<size_t>(node[ii]) * p.words + (j >> 6)] >> (j & 63)) & 1ull;
+                    if (tree && ok) ok = (seen[ii] >> (j & 63)) & 1ull;
                     float x = p.softcap > 0.f ? cap2 * tanhf(s[ii][jj] * incap) : s[ii][jj] * scale2;
                     x -= slope2[ii] * static_cast<float>(far);
                     s[ii][jj] = ok ? x : -INFINITY;
                 }
             }
 #pragma unroll
-            for (int ii = 0; ii < 4; ++ii) {
+            for (int ii = 0; ii < R; ++ii) {
                 float mt = fmaxf(fmaxf(s[ii][0], s[ii][1]), fmaxf(s[ii][2], s[ii][3]));
 #pragma unroll
                 for (int off = 8; off > 0; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
@@ -181,19 +197,19 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
 #pragma unroll
                 for (int e = 0; e < DT; ++e) o[ii][e] *= alpha;
 #pragma unroll
-                for (int jj = 0; jj < 4; ++jj) Ps[(4 * rg + ii) * LP + kg + 16 * jj] = pr[jj];
+                for (int jj = 0; jj < 4; ++jj) Ps[(R * rg + ii) * LP + kg + 16 * jj] = pr[jj];
             }
             __syncwarp();
 #pragma unroll 4
             for (int j = 0; j < FK; ++j) {
-                float pj[4];
+                float pj[R];
 #pragma unroll
-                for (int ii = 0; ii < 4; ++ii) pj[ii] = Ps[(4 * rg + ii) * LP + j];
+                for (int ii = 0; ii < R; ++ii) pj[ii] = Ps[(R * rg + ii) * LP + j];
 #pragma unroll
                 for (int h = 0; h < DT / 4; ++h) {
                     const float4 v = *reinterpret_cast<const float4*>(&Vs[j * LD + h * 64 + kg * 4]);
 #pragma unroll
-                    for (int ii = 0; ii < 4; ++ii) {
+                    for (int ii = 0; ii < R; ++ii) {
                         o[ii][h * 4 + 0] += pj[ii] * v.x;
                         o[ii][h * 4 + 1] += pj[ii] * v.y;
                         o[ii][h * 4 + 2] += pj[ii] * v.z;
@@ -205,8 +221,8 @@ __global__ void __launch_bounds__(256) k_attn_shared_fma(const Params p) {
         const int stride = it.shared ? p.rowsS : p.rowsO;
         float4* part = (it.shared ? p.part_s : p.part_o) + static_cast<size_t>(it.index) * (D / 4 + 1) * stride;
 #pragma unroll
-        for (int ii = 0; ii < 4; ++ii) {
-            const int r = 4 * rg + ii;
+        for (int ii = 0; ii < R; ++ii) {
+            const int r = R * rg + ii;
             if (r >= it.rows) continue;
             if (it.direct) {
                 const size_t row = row_of_q(p, it, r);
@@ -353,7 +369,8 @@ HostPlan host_plan(Params& p, bool tc, bool shared, int ctas) {
     h.tc = tc;
     p.g = p.Hq / p.Hkv;
     p.gT = p.g * p.T;
-    p.RB = tc ? kTcRows : FR;
+    // fp32 blocks are as high as their rows need, 64 where sequences are to share keys in them
+    p.RB = tc ? kTcRows : (shared && p.Lshared >= p.Lmax) || p.gT > 32 ? FR : p.gT > 16 ? 32 : 16;
     p.nbb = p.gT >= p.RB ? 1 : std::min(p.RB / p.gT, p.B);
     p.n_rbO = (p.gT + p.RB - 1) / p.RB;
     p.n_rbS = p.gT >= p.RB ? p.B * p.n_rbO : (p.B + p.nbb - 1) / p.nbb;
@@ -421,6 +438,9 @@ static spec_status check_shapes(const spec_tree* t, int B, int Hq, int Hkv, int 
     return SPEC_OK;
 }
 
+// Parts of the line: resident CTAs.  fp32 items of head dim 64 go two to an SM.
+static int parts(spec_dtype dt, int D) { return device_sm_count() * (dt == SPEC_F32 && D == 64 ? 2 : 1); }
+
 static Params shapes(const spec_tree* t, int B, int Hq, int Hkv, int Ls, int Lmax, int D) {
     Params p{};
     p.B = B; p.T = t->T; p.Hq = Hq; p.Hkv = Hkv; p.D = D; p.words = t->words;
@@ -431,15 +451,19 @@ static Params shapes(const spec_tree* t, int B, int Hq, int Hkv, int Ls, int Lma
 static size_t workspace(const spec_tree* t, int B, int Hq, int Hkv, int Ls, int Lmax, int D, spec_dtype dt) {
     if (check_shapes(t, B, Hq, Hkv, Ls, Lmax, D, dt) != SPEC_OK) return 0;
     Params p = shapes(t, B, Hq, Hkv, Ls, Lmax, D);
-    return host_plan(p, dt == SPEC_BF16, Ls > 0, device_sm_count()).total;
+    return host_plan(p, dt == SPEC_BF16, Ls > 0, parts(dt, D)).total;
 }
 
+template <int D, int R>
+static spec_status run_fma(const Params& p, cudaStream_t s) {
+    const size_t smem = sizeof(float) * (16 * R * (D + 4) + 4 * FK * (D + 4) + 16 * R * (FK + 4));
+    SPEC_CUDA_TRY(cudaFuncSetAttribute(k_attn_shared_fma<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+    SPEC_CUDA_TRY(launch_ex("attn_shared_fma", k_attn_shared_fma<D, R>, dim3(p.ctas), dim3(256), smem, s, true, p));
+    return SPEC_OK;
+}
 template <int D>
 static spec_status run_fma(const Params& p, cudaStream_t s) {
-    const size_t smem = sizeof(float) * (FR * (D + 4) + 2 * FK * (D + 4) + FR * (FK + 4));
-    SPEC_CUDA_TRY(cudaFuncSetAttribute(k_attn_shared_fma<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-    SPEC_CUDA_TRY(launch_ex("attn_shared_fma", k_attn_shared_fma<D>, dim3(p.ctas), dim3(256), smem, s, true, p));
-    return SPEC_OK;
+    return p.RB == 64 ? run_fma<D, 4>(p, s) : p.RB == 32 ? run_fma<D, 2>(p, s) : run_fma<D, 1>(p, s);
 }
 
 template <typename T>
@@ -490,7 +514,7 @@ static spec_status run(Params p, const spec_tree* tree, spec_dtype dt, float sca
         return fail(SPEC_EINVAL, "out overlaps q, k_tree or v_tree");
     p.depth = tree->depth;
     p.anc = tree->anc;
-    const HostPlan h = host_plan(p, dt == SPEC_BF16, shared, device_sm_count());
+    const HostPlan h = host_plan(p, dt == SPEC_BF16, shared, parts(dt, p.D));
     if (!p.ws || ws_bytes < h.total) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, h.total);
     if (!aligned16(p.ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
     unsigned char* base = static_cast<unsigned char*>(p.ws);
