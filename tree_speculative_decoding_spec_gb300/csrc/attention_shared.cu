@@ -28,9 +28,9 @@ constexpr int FK = kTile;   // keys of a tile
 
 // 256 threads; thread (rg, kg) = (t / 16, t % 16) holds R rows from R rg, keys kg + 16 j of a tile and
 // output columns 4 kg .. of each 64.  fp32 operands have no tensor-core product of their own precision,
-// so the FMA units and the shared memory that feeds them bound this kernel: at R = 4, 16 FMAs per 8
-// loads of 16 bytes for two keys in the score loop; a 64 x 64 tile of head dim 128 takes some 9 us of the 4.2 that
-// its FMAs alone would.  The next tile's keys and values arrive meanwhile (cp.async, two buffers); rows
+// so the FMA units and the shared memory that feeds them bound this kernel: at R = 4, 64 FMAs per 8
+// loads of 16 bytes in the score loop; a 64 x 64 tile of head dim 128 takes some 9 us, its FMAs alone
+// would 4.2.  The next tile's keys and values arrive meanwhile (cp.async, two buffers); rows
 // are 16, 32 or 64 to a block as the call needs them, and items of head dim 64 go two to an SM: 8
 // sequences of 2368 keys and 13 nodes, 8 heads of 128, took 265 us before these three and 131 with them,
 // 21 of 896 keys and 12 nodes, 4 heads of 64, 65 and 41, and two trees of 75 nodes behind 3840 keys 84 and 75.
