@@ -478,7 +478,7 @@ spec_status tree_kv_commit_paged(const void* k_tree, const void* v_tree, void* k
  *     the key is seen only if P - p < window, if window > 0 (the query itself always is)
  */
 typedef struct {
-    float softcap;          /* 0: none; else >= 1e-6, finite */
+    float softcap;          /* 0: none; else 1e-6 to 4096 */
     int32_t window;         /* 0: none */
     const float* slopes;    /* device [Hq], finite, or NULL */
 } spec_score;

@@ -81,7 +81,7 @@ def test_attention_refuses(lib, name):
         ({"prefix_len": 7 * _GB + 2}, EALIGN), ({"slopes": 17 * _GB + 2}, EALIGN), ({"ws": 0}, EWORKSPACE),
         ({"ws_bytes": 512}, EWORKSPACE), ({"ws": 12 * _GB + 8}, EALIGN),
         ({"scale": -1.0}, EINVAL), ({"scale": float("nan")}, EINVAL), ({"scale": float("inf")}, EINVAL),
-        ({"softcap": -1.0}, EINVAL), ({"softcap": float("nan")}, EINVAL), ({"softcap": 1e-7}, EINVAL), ({"softcap": float("inf")}, EINVAL),
+        ({"softcap": -1.0}, EINVAL), ({"softcap": float("nan")}, EINVAL), ({"softcap": 1e-7}, EINVAL), ({"softcap": 4097.0}, EINVAL), ({"softcap": float("inf")}, EINVAL),
         ({"window": -1}, EINVAL),
         ({"out": _GB}, EINVAL), ({"out": _GB + 16}, EINVAL), ({"out": 8 * _GB + 1024}, EINVAL), ({"out": 9 * _GB - 16}, EINVAL),
     ]:

@@ -461,3 +461,62 @@ def test_binding_names_what_is_wrong():
                              ({"ws": torch.empty(64, dtype=torch.uint8)}, ValueError, "ws must be a CUDA tensor")):
         with pytest.raises(err, match=text):
             st.tree_attention_shared(**{**good, **wrong})
+
+
+@pytest.mark.parametrize("T", [64, 20, 2])
+def test_the_largest_cap(T):
+    """Whole and partial tiles, windows and a bias at the largest cap taken; beyond it the call is refused."""
+    for dtype in ("bf16", "f32"):
+        c = Case(dtype, B=2, Hq=8, Hkv=2, D=128, T=T, lens=(330, 77), Lmax=340, softcap=4096.0)
+        c.check(*c.call())
+        c.score["window"] = 300
+        c.check(*c.call())
+        d = Case(dtype, B=2, Hq=8, Hkv=2, D=128, T=T, lens=(330, 77), Lmax=340, softcap=4096.0, slopes=True, gain=20.0)
+        d.check(*d.call())
+        with pytest.raises(c.st.SpecError, match="softcap"):
+            c.call(softcap=5000.0)
+
+
+def test_the_largest_tree():
+    for name, kw in (("f32", dict(D=64, Hq=2, Hkv=1)), ("bf16", dict(D=128, Hq=2, Hkv=2))):
+        c = Case(name, B=1, T=1024, lens=(100,), Lmax=128, Ls=70, **kw)
+        c.check(*c.call())
+        c.score["softcap"], c.score["window"] = 20.0, 90
+        c.check(*c.call())
+
+
+def test_far_into_a_long_cache():
+    """Keys some millions of positions into the cache, seen through a window: rows past 2^31 bytes of it."""
+    import torch
+    n = 1 << 22
+    for dtype, Hkv in (("bf16", 5), ("f32", 3)):
+        c = Case(dtype, B=1, Hq=Hkv, Hkv=Hkv, D=64, T=5, lens=(300,), Lmax=300, window=257, slopes=True)
+        kc = torch.zeros(1, Hkv, n, 64, dtype=c.kc.dtype, device="cuda")
+        vc = torch.zeros_like(kc)
+        L = n - 3
+        kc[:, :, L - 300:L], vc[:, :, L - 300:L] = c.kc, c.vc
+        ref = c.reference()       # positions are seen through their differences only
+        c.kc, c.vc = kc, vc
+        c.check(*c.call(L=_i32([L])), ref)
+        del c, kc, vc
+        torch.cuda.empty_cache()
+
+
+def test_two_streams_at_once():
+    import torch
+    a = Case("bf16", B=4, Hq=16, Hkv=2, D=128, T=30, lens=(900, 1, 300, 77), Lmax=1000, Ls=2000)
+    b = Case("bf16", B=5, Hq=8, Hkv=4, D=64, T=1, lens=(500, 400, 3, 77, 0), Lmax=500, block=16, softcap=30.0)
+    want = [a.call(), b.call()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    rooms = [c.workspace() for c in (a, b)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(12):
+        for i, c in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(c.call(ws=rooms[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])

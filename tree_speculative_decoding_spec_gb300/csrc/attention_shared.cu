@@ -491,8 +491,9 @@ static spec_status run(Params p, const spec_tree* tree, spec_dtype dt, float sca
     if (!(scale > 0.f) || !(scale < 1e30f)) return fail(SPEC_EINVAL, "scale must be positive and finite, or 0");
     p.scale = scale;
     if (score) {
-        if (!(score->softcap >= 0.f) || !(score->softcap < 1e30f)) return fail(SPEC_EINVAL, "softcap must be positive and finite, or 0");
-        if (score->softcap > 0.f && score->softcap < 1e-6f) return fail(SPEC_EINVAL, "softcap = %g is below 1e-6", score->softcap);
+        // a capped score is off by some 2^-22 of the cap: beyond 2^12 that would show beside the weights' rounding to bf16
+        if (!(score->softcap == 0.f || (score->softcap >= 1e-6f && score->softcap <= 4096.f)))
+            return fail(SPEC_EINVAL, "softcap = %g: 1e-6 to 4096, or 0 for none", score->softcap);
         if (score->window < 0) return fail(SPEC_EINVAL, "window = %d must be positive, or 0", score->window);
         p.softcap = score->softcap;
         p.window = score->window;
