@@ -823,6 +823,16 @@ def tree_attention_scored_paged(q, k_pool, v_pool, block_table, prefix_len, k_tr
 
 def _rows(t, name, dtype, index, lead):
     """Check token rows [*lead, heads, D] with dense heads and evenly spaced tokens; returns (address, heads, D, stride)."""
+    if isinstance(t, _Tensor) and t.get_device() == index >= 0 and t.dtype is dtype:
+        shape, st = t.shape, t.stride()
+        if len(shape) == 3:
+            N, H, D = shape
+            if N > 1 and lead == (N,) and st[2] == 1 and st[1] == D:
+                return t.data_ptr(), H, D, st[0]
+        elif len(shape) == 4:
+            B, T, H, D = shape
+            if T > 1 and lead == (B, T) and st[3] == 1 and st[2] == D and st[0] == T * st[1]:
+                return t.data_ptr(), H, D, st[1]
     if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != index or index < 0:
