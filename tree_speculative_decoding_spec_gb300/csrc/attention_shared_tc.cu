@@ -186,12 +186,13 @@ __device__ __forceinline__ float max64(const float (&x)[64]) {
     return fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
 
-__device__ __forceinline__ float min64(const float (&x)[64]) {
+__device__ __forceinline__ float absmax64(const float (&x)[64]) {
     float m[8];
+    auto a = [&](int e) { return fabsf(x[e]); };
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        m[e] = fmin3(fmin3(x[e], x[e + 8], x[e + 16]), fmin3(x[e + 24], x[e + 32], x[e + 40]), fminf(x[e + 48], x[e + 56]));
-    return fmin3(fmin3(m[0], m[1], m[2]), fmin3(m[3], m[4], m[5]), fminf(m[6], m[7]));
+        m[e] = fmax3(fmax3(a(e), a(e + 8), a(e + 16)), fmax3(a(e + 24), a(e + 32), a(e + 40)), fmaxf(a(e + 48), a(e + 56)));
+    return fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
 
 // 2^arg(x) of 64 scores, two at a time, as bf16 pairs to TMEM; returns their sum before the rounding.
@@ -315,7 +316,7 @@ __device__ __forceinline__ bool grow(float tmax, bool in, float& m_used, float& 
 // hundred afterwards 2 us.  Transformed scores written back and read again by a second pass took
 // 1200 cycles more per 128 keys.)
 // pv_bar: the barrier of the group's previous PV, NULL where S complete implies it.
-// landed(): called once S is complete; release(h): the weights of keys 64 h .. are in place.
+// landed(): called once S is complete; release(h): the weights of keys 64 h .. (-1: all) are in place.
 template <int D, bool kScored, typename Landed, typename Release>
 __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, const Tile& tl, const Row& row, int halves, bool warp_in,
                                              uint32_t s_addr, uint32_t o_addr, float& m_used, float& l, uint64_t* s_bar,
@@ -330,7 +331,7 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
     tc_fence_after();
     if (!landed()) return false;
     if (!warp_in) {
-        for (int h = 0; h < halves; ++h) release(h);
+        release(-1);
         return true;
     }
     const float scale2 = p.scale * kLog2e;
@@ -372,17 +373,18 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
             if (capped) {
                 const Cap cap(p);
                 if (!masked && !biased) {
-                    // the cap keeps the order, so the raw scores' extremes give the capped ones' maximum
-                    const float top = max64(x), most = fmaxf(top, -min64(x));
-                    if (cap.below(most, 0.16f, row.in)) {
-                        if (!reach(cap(top))) return false;
+                    // the largest |score| serves both the choice and, where it is within 2^40 of every
+                    // weight's scale, the reference: half the comparisons (32K capped 270 -> 260 us)
+                    const float most = absmax64(x);
+                    if (cap.below(most, fminf(0.16f, 40.f / cap.cap2), row.in)) {
+                        if (!reach(most * scale2)) return false;
                         const Cap::Small f(cap);
                         const unsigned long long nm2 = reference();
                         l += weigh64(x, w_addr, [&](unsigned long long v) { return ffma2(v, f.factor(v), nm2); });
                         continue;
                     }
                     if (cap.below(most, 0.7f, row.in)) {
-                        if (!reach(cap(top))) return false;
+                        if (!reach(cap(max64(x)))) return false;   // the cap keeps the order
                         const Cap::Middle f(cap);
                         const unsigned long long nm2 = reference();
                         l += weigh64(x, w_addr, [&](unsigned long long v) { return ffma2(v, f.factor(v), nm2); });
@@ -425,7 +427,7 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
         const unsigned long long sc2 = pk2(in_scale, in_scale), nm2 = reference();
         l += weigh64(x, w_addr, [&](unsigned long long v) { return ffma2(v, sc2, nm2); });
     }
-    for (int h = 0; h < halves; ++h) release(h);
+    release(-1);   // all of them
     return true;
 }
 
@@ -1015,7 +1017,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[2 * grp + (it.pair ? h : buf)]);
+                    if (lane == 0) {
+                        if (it.pair && h < 0) mbar_arrive(&p_full[2 * grp + 1]);
+                        mbar_arrive(&p_full[2 * grp + (it.pair ? max(h, 0) : buf)]);
+                    }
                 };
                 uint64_t* pv_bar = it.pair ? nullptr : &pv_done[grp];
                 const uint32_t s_addr = s_base + buf * kKeys;
