@@ -17,23 +17,29 @@
 #include <cmath>
 
 #include "attention_shared.cuh"
+#include "tc.cuh"
 
 namespace spec {
 namespace shr {
+
+using tc::ffma2;
+using tc::pk2;
+using tc::upk2;
 
 // ---------------------------------------------------------------- CUDA-core items
 
 constexpr int FR = 64;   // rows of a block, at most
 constexpr int FK = kTile;   // keys of a tile
+constexpr int kFmaThreads = 256;
 
-// 256 threads; thread (rg, kg) = (t / 16, t % 16) holds R rows from R rg, keys kg + 16 j of a tile and
-// output columns 4 kg .. of each 64.  fp32 operands have no tensor-core product of their own precision,
-// so the FMA units and the shared memory that feeds them bound this kernel: at R = 4, 64 FMAs per 8
-// loads of 16 bytes in the score loop; a 64 x 64 tile of head dim 128 takes some 9 us, its FMAs alone
-// would 4.2.  The next tile's keys and values arrive meanwhile (cp.async, two buffers); rows
-// are 16, 32 or 64 to a block as the call needs them, and items of head dim 64 go two to an SM: 8
-// sequences of 2368 keys and 13 nodes, 8 heads of 128, took 265 us before these three and 131 with them,
-// 21 of 896 keys and 12 nodes, 4 heads of 64, 65 and 41, and two trees of 75 nodes behind 3840 keys 84 and 75.
+// Thread (rg, kg) = (t / 16, t % 16) holds R rows from R rg, keys kg + 16 j of a tile and output columns
+// 4 kg .. of each 64.  fp32 operands have no tensor-core product of their own precision, so the FMA units
+// and the shared memory that feeds them bound this kernel: at R = 4, 32 packed FMAs per 8 loads of 16 bytes in
+// the score loop; a 64 x 64 tile of head dim 128 takes some 8.5 us, its FMAs alone would 4.2.  The next tile's
+// keys and values arrive meanwhile (cp.async, two buffers); rows are 16, 32 or 64 to a block as the call needs
+// them, and items of head dim 64 go two to an SM.  8 sequences of 2368 keys and 13 nodes, 8 heads of 128,
+// took 265 us before these and 131 with them; 21 of 896 keys and 12 nodes, 4 heads of 64, 65 and 41; two trees
+// of 75 nodes behind 3840 keys 84 and 71.  512 threads for head dim 128, two rows each, took 82.
 __device__ __forceinline__ void copy_async16(float* dst, const float* src, bool ok) {   // zeros where not ok
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src),
                  "r"(ok ? 16 : 0)
@@ -44,9 +50,9 @@ template <int N>
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <int D, int R>
-__global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_attn_shared_fma(const Params p) {
+__global__ void __launch_bounds__(kFmaThreads, D == 64 ? 2 : 1) k_attn_shared_fma(const Params p) {
     using T = float;
-    constexpr int FR = 16 * R;   // rows of a block
+    constexpr int FR = kFmaThreads / 16 * R;   // rows of a block
     constexpr int LD = D + 4, LP = FK + 4, DT = D / 16;
     extern __shared__ float4 smem4[];
     float* Qs = reinterpret_cast<float*>(smem4);
@@ -65,14 +71,15 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_attn_shared_fma(const 
     Walk walk(p, plan, blockIdx.x);
     for (Item it; walk.next(p, plan, it);) {
         __syncthreads();   // the last item's Q and P are read
-        for (int idx = t; idx < FR * (D / 4); idx += 256) {
+        for (int idx = t; idx < FR * (D / 4); idx += kFmaThreads) {
             const int r = idx / (D / 4), c4 = idx % (D / 4);
             float v[4] = {0.f, 0.f, 0.f, 0.f};
             if (r < it.rows) load4(q + row_of_q(p, it, r) * D + c4 * 4, v);
             *reinterpret_cast<float4*>(&Qs[r * LD + c4 * 4]) = make_float4(v[0], v[1], v[2], v[3]);
         }
         int node[R], pos[R];
-        float slope2[R], m_run[R], l_run[R], o[R][DT];
+        float slope2[R], m_run[R], l_run[R];
+        unsigned long long o2[R][DT / 2];     // pairs of columns
 #pragma unroll
         for (int ii = 0; ii < R; ++ii) {
             const int r = min(R * rg + ii, it.rows - 1);
@@ -84,7 +91,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_attn_shared_fma(const 
             m_run[ii] = -INFINITY;
             l_run[ii] = 0.f;
 #pragma unroll
-            for (int e = 0; e < DT; ++e) o[ii][e] = 0.f;
+            for (int e = 0; e < DT / 2; ++e) o2[ii][e] = pk2(0.f, 0.f);
         }
         const int first = it.shared ? plan.sT0 : own_first(p, it.L);
         const int n_pre = it.shared ? plan.nS : own_tiles(p, it.L) - tiles_of(p.T);
@@ -94,7 +101,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_attn_shared_fma(const 
             const int j0 = (tree ? tile - n_pre : first + tile) * FK;
             const int j_end = tree ? p.T : it.shared ? plan.Ls : it.L;
             float* dst = KVs + ((tile - it.t0) & 1) * (2 * FK * LD);
-            for (int x = t; x < FK * (D / 4); x += 256) {
+            for (int x = t; x < FK * (D / 4); x += kFmaThreads) {
                 const int jl = x / (D / 4), c4 = x % (D / 4), j = j0 + jl;
                 const T *ksrc = static_cast<const T*>(p.kt), *vsrc = static_cast<const T*>(p.vt);
                 size_t row = 0;
@@ -146,24 +153,33 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_attn_shared_fma(const 
 #pragma unroll
                 for (int ii = 0; ii < R; ++ii) seen[ii] = p.anc[static_cast<size_t>(node[ii]) * p.words + (j0 >> 6)];
             }
+            // two products at a time: even and odd dimensions add up apart
+            unsigned long long s2[R][4];
+#pragma unroll
+            for (int ii = 0; ii < R; ++ii)
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) s2[ii][jj] = pk2(0.f, 0.f);
+#pragma unroll (D == 64 ? 2 : 4)
+            for (int dd = 0; dd < D; dd += 4) {
+                ulonglong2 qa[R], kb[4];
+#pragma unroll
+                for (int ii = 0; ii < R; ++ii) qa[ii] = *reinterpret_cast<const ulonglong2*>(&Qs[(R * rg + ii) * LD + dd]);
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) kb[jj] = *reinterpret_cast<const ulonglong2*>(&Ks[(kg + 16 * jj) * LD + dd]);
+#pragma unroll
+                for (int ii = 0; ii < R; ++ii)
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj) s2[ii][jj] = ffma2(qa[ii].y, kb[jj].y, ffma2(qa[ii].x, kb[jj].x, s2[ii][jj]));
+            }
             float s[R][4];
 #pragma unroll
             for (int ii = 0; ii < R; ++ii)
 #pragma unroll
-                for (int jj = 0; jj < 4; ++jj) s[ii][jj] = 0.f;
-#pragma unroll 4
-            for (int dd = 0; dd < D; dd += 4) {
-                float4 qa[R], kb[4];
-#pragma unroll
-                for (int ii = 0; ii < R; ++ii) qa[ii] = *reinterpret_cast<const float4*>(&Qs[(R * rg + ii) * LD + dd]);
-#pragma unroll
-                for (int jj = 0; jj < 4; ++jj) kb[jj] = *reinterpret_cast<const float4*>(&Ks[(kg + 16 * jj) * LD + dd]);
-#pragma unroll
-                for (int ii = 0; ii < R; ++ii)
-#pragma unroll
-                    for (int jj = 0; jj < 4; ++jj)
-                        s[ii][jj] += qa[ii].x * kb[jj].x + qa[ii].y * kb[jj].y + qa[ii].z * kb[jj].z + qa[ii].w * kb[jj].w;
-            }
+                for (int jj = 0; jj < 4; ++jj) {
+                    float even, odd;
+                    upk2(s2[ii][jj], even, odd);
+                    s[ii][jj] = even + odd;
+                }
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
                 const int j = j0 + kg + 16 * jj;
@@ -195,27 +211,28 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_attn_shared_fma(const 
                 l_run[ii] = l_run[ii] * alpha + lt;
                 m_run[ii] = m_new;
 #pragma unroll
-                for (int e = 0; e < DT; ++e) o[ii][e] *= alpha;
+                for (int e = 0; e < DT / 2; ++e) o2[ii][e] = ffma2(o2[ii][e], pk2(alpha, alpha), pk2(0.f, 0.f));
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) Ps[(R * rg + ii) * LP + kg + 16 * jj] = pr[jj];
             }
             __syncwarp();
-#pragma unroll 4
-            for (int j = 0; j < FK; ++j) {
-                float pj[R];
+#pragma unroll 2
+            for (int j = 0; j < FK; j += 4) {
+                float4 pj[R];
 #pragma unroll
-                for (int ii = 0; ii < R; ++ii) pj[ii] = Ps[(R * rg + ii) * LP + j];
+                for (int ii = 0; ii < R; ++ii) pj[ii] = *reinterpret_cast<const float4*>(&Ps[(R * rg + ii) * LP + j]);
 #pragma unroll
-                for (int h = 0; h < DT / 4; ++h) {
-                    const float4 v = *reinterpret_cast<const float4*>(&Vs[j * LD + h * 64 + kg * 4]);
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int ii = 0; ii < R; ++ii) {
-                        o[ii][h * 4 + 0] += pj[ii] * v.x;
-                        o[ii][h * 4 + 1] += pj[ii] * v.y;
-                        o[ii][h * 4 + 2] += pj[ii] * v.z;
-                        o[ii][h * 4 + 3] += pj[ii] * v.w;
+                    for (int h = 0; h < DT / 4; ++h) {
+                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&Vs[(j + u) * LD + h * 64 + kg * 4]);
+#pragma unroll
+                        for (int ii = 0; ii < R; ++ii) {
+                            const float w = u == 0 ? pj[ii].x : u == 1 ? pj[ii].y : u == 2 ? pj[ii].z : pj[ii].w;
+                            o2[ii][2 * h] = ffma2(pk2(w, w), v.x, o2[ii][2 * h]);
+                            o2[ii][2 * h + 1] = ffma2(pk2(w, w), v.y, o2[ii][2 * h + 1]);
+                        }
                     }
-                }
             }
         }
         const int stride = it.shared ? p.rowsS : p.rowsO;
@@ -224,6 +241,9 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_attn_shared_fma(const 
         for (int ii = 0; ii < R; ++ii) {
             const int r = R * rg + ii;
             if (r >= it.rows) continue;
+            float o[DT];
+#pragma unroll
+            for (int e = 0; e < DT / 2; ++e) upk2(o2[ii][e], o[2 * e], o[2 * e + 1]);
             if (it.direct) {
                 const size_t row = row_of_q(p, it, r);
                 const float inv = 1.f / l_run[ii];
@@ -231,14 +251,14 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_attn_shared_fma(const 
                 for (int h = 0; h < DT / 4; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        static_cast<T*>(p.out)[row * D + h * 64 + kg * 4 + e] = from_f32<T>(o[ii][h * 4 + e] * inv);
+                        static_cast<T*>(p.out)[row * D + h * 64 + kg * 4 + e] = from_f32<T>(o[h * 4 + e] * inv);
                 if (p.lse && kg == 0) p.lse[row] = (m_run[ii] + log2f(l_run[ii])) * kLn2;
             } else {
                 if (kg == 0) part[r] = make_float4(m_run[ii], l_run[ii], 0.f, 0.f);
 #pragma unroll
                 for (int h = 0; h < DT / 4; ++h)
                     part[static_cast<size_t>(1 + h * 16 + kg) * stride + r] =
-                        make_float4(o[ii][h * 4 + 0], o[ii][h * 4 + 1], o[ii][h * 4 + 2], o[ii][h * 4 + 3]);
+                        make_float4(o[h * 4 + 0], o[h * 4 + 1], o[h * 4 + 2], o[h * 4 + 3]);
             }
         }
     }
@@ -456,9 +476,9 @@ static size_t workspace(const spec_tree* t, int B, int Hq, int Hkv, int Ls, int 
 
 template <int D, int R>
 static spec_status run_fma(const Params& p, cudaStream_t s) {
-    const size_t smem = sizeof(float) * (16 * R * (D + 4) + 4 * FK * (D + 4) + 16 * R * (FK + 4));
+    const size_t rows = kFmaThreads / 16 * R, smem = sizeof(float) * (rows * (D + 4) + 4 * FK * (D + 4) + rows * (FK + 4));
     SPEC_CUDA_TRY(cudaFuncSetAttribute(k_attn_shared_fma<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-    SPEC_CUDA_TRY(launch_ex("attn_shared_fma", k_attn_shared_fma<D, R>, dim3(p.ctas), dim3(256), smem, s, true, p));
+    SPEC_CUDA_TRY(launch_ex("attn_shared_fma", k_attn_shared_fma<D, R>, dim3(p.ctas), dim3(kFmaThreads), smem, s, true, p));
     return SPEC_OK;
 }
 template <int D>
