@@ -157,6 +157,9 @@ struct Row {
     const uint64_t* anc;
 };
 
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16(addr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r); }
+
 // 64 scores of the thread's row, from TMEM and back.
 __device__ __forceinline__ void load64(uint32_t addr, float (&x)[64]) {
     uint32_t r0[32], r1[32];
@@ -1051,7 +1054,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
             tc_fence_after();
             if (it.pair && (warp & 3) == 0 && lane == 0) mbar_arrive(&kv_empty[(U + 2 * ts.count - 1) % C::kStages]);
             float m = m_used, lsum = l, a0 = 1.f, a1 = 0.f;   // weights of the group's own O and the other's
-            bool has_own = true, has_other = false;
+            uint32_t from = o_addr;                           // the first of them, and whether there are both
+            bool both = false;
             if (!it.pair) {
                 ml[grp * kRows + tl_row] = make_float2(m_used, l);
                 __syncwarp();
@@ -1064,8 +1068,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
                 a0 = ex2(m_used - ref);
                 a1 = ex2(other.x - ref);
                 lsum = a0 * l + a1 * other.y;
-                has_own = ts.count > 1 || grp == 0;    // a group without a tile left O as it was
-                has_other = ts.count > 1 || grp == 1;
+                both = ts.count > 1;
+                if (!both && grp == 1) {                   // a group without a tile left its O as it was
+                    from = lane_base + kO;
+                    a0 = a1;
+                }
             }
             if (warp_in) {
                 const int cap = it.shared ? p.rowsS : p.rowsO, stride = cap * (few ? 4 : 1);
@@ -1080,33 +1087,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
                 a0 *= inv;
                 a1 *= inv;
                 const int c_end = it.pair ? D : (grp + 1) * (D / 2);
+                // W columns at a time.  This code runs once an item, and fetching it costs some ten cycles an
+                // instruction, so 16 where the softmax's own code is long (32K capped 260 us at 32, 247 at 16);
+                // with plain scores 32 (70B trees 222, at 16 228).
+                constexpr int W = kScored ? 16 : 32;
 #pragma unroll 1
-                for (int c0 = it.pair ? 0 : grp * (D / 2); c0 < c_end; c0 += 32) {
-                    uint32_t o0[32], o1[32];
-                    tmem_ld32(o_addr + c0, o0);
-                    if (has_other) tmem_ld32(lane_base + kO + (grp ^ 1) * D + c0, o1);
+                for (int c0 = it.pair ? 0 : grp * (D / 2); c0 < c_end; c0 += W) {
+                    uint32_t o[W], o1[W];
+                    float v[W];
+                    tmem_ld(from + c0, o);
+                    if (both) tmem_ld(lane_base + kO + (grp ^ 1) * D + c0, o1);
                     tmem_ld_wait();
-                    float v[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        v[e] = has_own ? a0 * __uint_as_float(o0[e]) : 0.f;
-                        if (has_other) v[e] = fmaf(a1, __uint_as_float(o1[e]), v[e]);
-                    }
+                    for (int e = 0; e < W; ++e) v[e] = a0 * __uint_as_float(o[e]);
+                    if (both)
+#pragma unroll
+                        for (int e = 0; e < W; ++e) v[e] = fmaf(a1, __uint_as_float(o1[e]), v[e]);
                     if (in && !it.direct) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
+                        for (int e = 0; e < W / 4; ++e)
                             part[static_cast<size_t>(1 + c0 / 4 + e) * stride] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     } else if (in) {
-                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + q_row * D + c0;
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + q_row * D + c0);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < W / 8; ++e) {
                             uint32_t w[4];
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * e + 2 * q], v[8 * e + 2 * q + 1]);
                                 w[q] = *reinterpret_cast<const uint32_t*>(&h);
                             }
-                            *reinterpret_cast<uint4*>(dst + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+                            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
                 }
