@@ -269,10 +269,11 @@ __global__ void __launch_bounds__(kFmaThreads, D == 64 ? 2 : 1) k_attn_shared_fm
 // ---------------------------------------------------------------- the join
 
 // One CTA of eight warps per (sequence, KV head, 32 rows of its gT), each warp an eighth of the
-// columns (four warps with twice the columns each: 1.5 us more in most cases).  Lanes are rows, so the partials are read as whole lines; with fewer than 32 rows the
-// lanes left over take other parts of the same rows (lane = part * R + row), and shuffles add
-// them up.  The output goes through shared memory to leave as whole rows.  Bound by reading the
-// partials once, and for few rows by the latency of the look-ups before that.
+// columns (four warps with twice the columns each: 1.5 us more in most cases).  Lanes are rows, so
+// the partials are read as whole lines; with fewer than 32 rows the lanes left over take other parts
+// of the same rows (lane = part * R + row), and shuffles add them up.  The output goes through shared
+// memory to leave as whole rows.  Bound by reading the partials once (70B trees over 16K shared keys,
+// some 55 MB of them: 15 us), and for few rows by the latency of the look-ups before that (7 us).
 constexpr int kJoin = 256;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoin) k_attn_shared_join(const Params p, int n_rg, int R) {
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kJoin) k_attn_shared_join(const Params p, int 
         if (lane == 0) *static_cast<int4*>(p.ws) = make_int4(worst, 0, 0, 0);
     }
     const Plan t = *reinterpret_cast<const Plan*>(static_cast<unsigned char*>(p.ws) + kPlanOffset);
-    const int rb = divide(r0, p.RB);              // 32 divides RB
+    const int rb = divide(r0, p.RB);              // 32 divides RB, or all rows fit one block
     const int sb = p.gT >= p.RB ? b * p.n_rbO + rb : divide(b, p.nbb);
     const int colS = kvh * p.n_rbS + sb, colO = kvh * p.n_rbO + rb, cols = p.Hkv * p.n_rbO;
     const Cuts kO(p, t.q, Place(p, false, n), p.cum[b], colO, p.n_rbO), kS(p, t.q, Place(p, true, t.nS), 0, colS, p.per);
@@ -453,7 +454,9 @@ static spec_status check_shapes(const spec_tree* t, int B, int Hq, int Hkv, int 
     const int high = dt == SPEC_BF16 ? kTcRows : FR;
     const int64_t blocks = static_cast<int64_t>(Hkv) * ((static_cast<int64_t>(Hq / Hkv) * t->T + high - 1) / high);
     const int64_t tiles = blocks * B * ((Lmax + 63) / 64 + (t->T + 63) / 64 + (Ls + 63) / 64 + 14);
-    if (7 * tiles > INT32_MAX / 2) return fail(SPEC_EINVAL, "B * Hkv * (Lmax + the shared capacity) is too large for one call (%lld tiles)", static_cast<long long>(tiles));
+    if (7 * tiles > INT32_MAX / 2)
+        return fail(SPEC_EINVAL, "B * Hkv * (Lmax + the shared capacity) is too large for one call (%lld tiles)",
+                    static_cast<long long>(tiles));
     if (rows > (1ll << 30)) return fail(SPEC_EINVAL, "B * Hq * T = %lld query rows exceed 2^30", static_cast<long long>(rows));
     return SPEC_OK;
 }
