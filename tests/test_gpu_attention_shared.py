@@ -520,3 +520,28 @@ def test_two_streams_at_once():
     for i in range(2):
         for out, lse in got[i]:
             assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+JUMPS = {
+    # blocks of 256 rows and a smaller one in turn, several of each in a CTA: the first tile is the tree's, or cut out of the prefix
+    "tree": dict(B=6, Hq=192, Hkv=64, D=64, T=100, lens=(0, 3, 200, 0, 70, 130), Lmax=200),
+    "prefix": dict(B=2, Hq=64, Hkv=64, D=64, T=341, lens=(700, 620), Lmax=700),
+}
+
+
+@pytest.mark.parametrize("score", [dict(softcap=50.0), dict(slopes=True), dict(window=300)], ids=["cap", "bias", "window"])
+@pytest.mark.parametrize("name", list(JUMPS))
+def test_a_maximum_that_jumps_in_an_items_first_tile(name, score):
+    """Every second 64 keys by far exceed the first: a group that rescales in an item's first tile, ahead of the
+    other, must leave the other's reading of the item before alone."""
+    c = Case("bf16", **JUMPS[name], **score)
+    for keys in (c.kc, c.kt):
+        for j in range(64, keys.shape[2], 128):
+            keys[:, :, j:j + 64] *= 32.0
+    ws = c.workspace()
+    out, lse = c.call(ws=ws)
+    c.check(out, lse)
+    assert c.st.spec_read_device_status(ws) == 0
+    for _ in range(40):
+        again, lse2 = c.call(ws=ws)
+        assert (again == out).all() and (lse2 == lse).all()

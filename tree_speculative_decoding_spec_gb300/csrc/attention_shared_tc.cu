@@ -268,9 +268,10 @@ struct Cap {
 // `p_cols` columns of weights at p_addr (the tile's first half, not yet given to PV) are rescaled
 // without rounding.  The TMEM accesses are the whole warp's, so its rows rescale together (by 1 where
 // nothing grew).
-template <int D>
-__device__ __forceinline__ bool grow(float tmax, bool in, float& m_used, float& l, uint32_t o_addr, uint32_t p_addr, int p_cols,
-                                     uint64_t* pv_bar, uint32_t pv_parity, volatile int* abort_flag) {
+// o_cols: columns of O, 0 in an item's first tile.  Its first PV overwrites what O holds until then, which
+// is the last item's, and the other group may still be reading it: only PV waits for o_empty.
+__device__ __forceinline__ bool grow(float tmax, bool in, float& m_used, float& l, uint32_t o_addr, int o_cols, uint32_t p_addr,
+                                     int p_cols, uint64_t* pv_bar, uint32_t pv_parity, volatile int* abort_flag) {
     float m_new = m_used, alpha = 1.f;
     bool rescale = false;
     if (tmax > m_used + 8.f) {
@@ -285,7 +286,7 @@ __device__ __forceinline__ bool grow(float tmax, bool in, float& m_used, float& 
         if (pv_bar && !warp_wait(pv_bar, pv_parity, abort_flag)) return false;
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
+        for (int c = 0; c < o_cols; c += 16) {
             uint32_t o[16];
             tmem_ld16(o_addr + c, o);
             tmem_ld_wait();
@@ -318,11 +319,12 @@ __device__ __forceinline__ bool grow(float tmax, bool in, float& m_used, float& 
 // its transforms, is code that the instruction cache does not hold: a first tile took 9 us, one in a
 // hundred afterwards 2 us.  Transformed scores written back and read again by a second pass took
 // 1200 cycles more per 128 keys.)
+// first: the item's first tile.
 // pv_bar: the barrier of the group's previous PV, NULL where S complete implies it.
 // landed(): called once S is complete; release(h): the weights of keys 64 h .. (-1: all) are in place.
 template <int D, bool kScored, typename Landed, typename Release>
-__device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, const Tile& tl, const Row& row, int halves, bool warp_in,
-                                             uint32_t s_addr, uint32_t o_addr, float& m_used, float& l, uint64_t* s_bar,
+__device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, const Tile& tl, const Row& row, int halves, bool first,
+                                             bool warp_in, uint32_t s_addr, uint32_t o_addr, float& m_used, float& l, uint64_t* s_bar,
                                              uint32_t s_parity, uint64_t* pv_bar, uint32_t pv_parity, volatile int* abort_flag,
                                              Landed landed, Release release) {
     uint64_t seen0 = ~0ull, seen1 = ~0ull;   // of the tree: the node's ancestors and itself
@@ -349,7 +351,7 @@ __device__ __forceinline__ bool softmax_tile(const Params& p, const Desc& it, co
         bits &= h ? seen1 : seen0;
         bool masked = tl.tree || nv < 64;
         auto reach = [&](float top) {   // the half's maximum
-            return grow<D>(top, row.in, m_used, l, o_addr, s_addr, 32 * h, pv_bar, pv_parity, abort_flag);
+            return grow(top, row.in, m_used, l, o_addr, first ? 0 : D, s_addr, 32 * h, pv_bar, pv_parity, abort_flag);
         };
         auto reference = [&]() {
             const float r = m_used == -INFINITY ? 0.f : -m_used;
@@ -480,7 +482,7 @@ __device__ __forceinline__ bool softmax_pair(const Params& p, const Tile& tl, co
     uint32_t a[32], b[32];
     tmem_ld32(s_addr, a);
     const float scale2 = p.scale * kLog2e;
-    if (!grow<D>(top * scale2, row.in, m_used, l, o_addr, 0, 0, nullptr, 0, abort_flag)) return false;
+    if (!grow(top * scale2, row.in, m_used, l, o_addr, D, 0, 0, nullptr, 0, abort_flag)) return false;
     const float nmref = m_used == -INFINITY ? 0.f : -m_used;
     const unsigned long long sc2 = pk2(scale2, scale2), nm2 = pk2(nmref, nmref);
     auto weigh = [&](const uint32_t (&x)[32], int c) {   // weights 32 c .. of the row, to columns 16 c ..
@@ -578,7 +580,7 @@ __device__ __forceinline__ bool softmax_few(const Params& p, const Desc& it, con
         if (!((bits >> e) & 1u)) x[e] = -INFINITY;
     const float top = fmax3(fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8])),
                             fmax3(x[9], x[10], x[11]), fmax3(fmax3(x[12], x[13], x[14]), x[15], x[15]));
-    if (!grow<D>(top, row.in, m_used, l, o_addr, 0, 0, pv_bar, pv_parity, abort_flag)) return false;
+    if (!grow(top, row.in, m_used, l, o_addr, D, 0, 0, pv_bar, pv_parity, abort_flag)) return false;
     const float nmref = m_used == -INFINITY ? 0.f : -m_used;
     uint32_t packed[8];
     float sum = 0.f;
@@ -1033,8 +1035,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_shared_tc(const __grid_con
                 else if (!kScored && it.pair)
                     ok = softmax_pair<D>(p, tl, row, warp_in, s_addr, o_addr, m_used, l, s_bar, parity, abort_flag, landed, release);
                 else
-                    ok = softmax_tile<D, kScored>(p, it, tl, row, ts.width, warp_in, s_addr, o_addr, m_used, l, s_bar, parity, pv_bar,
-                                                  (narrow - 1) & 1, abort_flag, landed, release);
+                    ok = softmax_tile<D, kScored>(p, it, tl, row, ts.width, k == 0, warp_in, s_addr, o_addr, m_used, l, s_bar, parity,
+                                                  pv_bar, (narrow - 1) & 1, abort_flag, landed, release);
                 if (!ok) break;
                 if (!it.pair) {
                     // the stage's second arrival, beside PV's commit (a pair's come from both groups)
