@@ -597,9 +597,11 @@ size_t kv_append_workspace_size(void);
  *   q_out         device [N, Hq, D] (dt); it must not overlap q, k or v
  *   ws            >= kv_append_workspace_size() bytes, 16-byte aligned
  * Shapes: D a multiple of 16 bytes, D <= 1024, 1 <= B <= 65535, Lmax <= 2^22.
- * A sequence with a negative prefix_len or whose tokens would pass Lmax, and
- * offsets that decrease or leave 0 .. N, are reported as SPEC_EINVAL in the
- * status word; such a sequence's rows are left unchanged, and its q_out too.
+ * A sequence with a negative prefix_len, whose tokens would pass Lmax or whose
+ * offsets decrease or leave 0 .. N is reported as SPEC_EINVAL in the status word;
+ * its cache rows are left unchanged, and its q_out too.  Where decreasing offsets
+ * give a row to two other sequences, one of them gets it, at its own place; the
+ * other's tokens are then written in part.
  */
 spec_status kv_append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
                       int64_t v_stride, int32_t N, const int32_t* seq_start, int32_t B, int32_t Hq, int32_t Hkv,

@@ -32,8 +32,9 @@ def kv_append(q, k, v, seq_start, prefix_len, k_cache, v_cache, freq, interleave
 
     q [N, Hq, D], k, v [N, Hkv, D]; caches [B, Hkv, Lmax, D], or pools
     [num_blocks, Hkv, block_size, D] with table [B, max_blocks].  A sequence whose
-    tokens do not fit, or whose prefix_len is negative, and a token whose block lies
-    outside the pool are left out; rows of no sequence are not written.
+    tokens do not fit, whose prefix_len is negative or whose offsets leave 0 .. N, and a
+    token whose block lies outside the pool are left out; rows of no sequence are not
+    written.
     """
     q, k, v = (np.asarray(t, dtype=np.float64) for t in (q, k, v))
     out = q.copy()
@@ -43,7 +44,7 @@ def kv_append(q, k, v, seq_start, prefix_len, k_cache, v_cache, freq, interleave
     written = np.zeros(len(q), dtype=bool)
     for b in range(len(prefix_len)):
         L, s0, s1 = int(prefix_len[b]), int(seq_start[b]), int(seq_start[b + 1])
-        if L < 0 or L + s1 - s0 > cap:
+        if L < 0 or L + s1 - s0 > cap or s0 < 0 or s1 > len(q):
             continue
         for n in range(s0, s1):
             at = L + n - s0

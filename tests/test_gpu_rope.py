@@ -319,3 +319,41 @@ def test_single_rows_and_odd_strides():
         _assert_rotated(_np(kc)[1, :, 7], ref_k[1, :, 7], _np(k)[0], freq, True, dtype, "k")
         _assert_rotated(_np(kc)[3, :, 5:7].transpose(1, 0, 2), ref_k[3, :, 5:7].transpose(1, 0, 2), _np(k)[1:], freq, True, dtype, "k")
         assert (_np(vc)[3, :, 5:7] == ref_v[3, :, 5:7]).all()
+
+
+@pytest.mark.parametrize("block", [0, 16])
+@pytest.mark.parametrize("start", [(0, 1, 2, 9), (0, 1, 2, 4), (-5, 1, 2, 3), (-1, 0, 3, 3), (0, 3, 3, 10), (-2, 12)],
+                         ids=lambda s: "_".join(map(str, s)))
+def test_sequences_with_offsets_outside_the_rows_are_left_alone(start, block):
+    """Their caches and queries keep their bits, though their tokens would fit and some of their rows are there."""
+    import torch
+    st = lib()
+    new = tuple(b - a for a, b in zip(start, start[1:]))
+    c = ("bf16", 4, 2, 64, 64, False, block, new, (3, 14, 7)[:len(new)], 5)
+    t = _case(c, seed=6)
+    t.update({n: t[n][:3] for n in "qkv"}, start=np.array(start))
+    kc0, vc0 = _np(t["kc"]), _np(t["vc"])
+    q_out = torch.full(t["q"].shape, 7.0, dtype=t["q"].dtype, device="cuda")
+    q0 = _np(q_out)
+    out, ws = _append(st, c, t, q_out=q_out)
+    _check(c, t, kc0, vc0, out, q0, st.spec_read_device_status(ws), want_status=1)
+
+
+@pytest.mark.parametrize("block", [0, 16])
+def test_decreasing_offsets_write_no_row_but_the_sequences_own(block):
+    """Rows 1 of three belongs to two sequences: either may get it, in its own place, and nothing else changes."""
+    st = lib()
+    c = ("f32", 2, 1, 16, 0, False, block, (2, 0, 2), (3, 14, 7), 0)
+    t = _case(c, seed=7)
+    t.update({n: t[n][:3] for n in "qkv"}, start=np.array([0, 2, 1, 3]))
+    before = {"kc": _np(t["kc"]), "vc": _np(t["vc"])}
+    _, ws = _append(st, c, t)
+    assert st.spec_read_device_status(ws) == 1
+    for name, x in (("kc", _np(t["k"])), ("vc", _np(t["v"]))):
+        got, mine = _np(t[name]), {}
+        for b, at, n in ((0, 3, 0), (0, 4, 1), (2, 7, 1), (2, 8, 2)):
+            mine[(b, at) if not block else (int(t["table"][b, at // block]), at % block)] = x[n]
+        for i in range(got.shape[0]):
+            for j in range(got.shape[2]):
+                if (got[i, :, j] != before[name][i, :, j]).any():
+                    np.testing.assert_array_equal(got[i, :, j], mine[i, j])

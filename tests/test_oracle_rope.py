@@ -78,3 +78,17 @@ def test_a_node_is_turned_as_on_its_path():
         np.testing.assert_allclose(ko[b][:, path], kc[0, :, L:L + 4], atol=1e-14)
     np.testing.assert_array_equal(vo, np.moveaxis(v, 1, 2))
     np.testing.assert_allclose(qo[1, :, 2], rope.rotate(q[1, 2], 12, freq, False))
+
+
+def test_offsets_outside_the_rows_leave_the_sequence_out():
+    r = np.random.default_rng(8)
+    q, k, v = r.standard_normal((3, 2, 4)), r.standard_normal((3, 1, 4)), r.standard_normal((3, 1, 4))
+    kc, vc = r.standard_normal((2, 1, 9, 4)), r.standard_normal((2, 1, 9, 4))
+    freq = np.array([0.5, 0.1])
+    for start, left_out in (([0, 1, 5], 1), ([-2, 1, 3], 0)):
+        out, k2, v2, written = rope.kv_append(q, k, v, start, [2, 3], kc, vc, freq)
+        np.testing.assert_array_equal(k2[left_out], kc[left_out])
+        np.testing.assert_array_equal(v2[left_out], vc[left_out])
+        s0, s1 = start[1 - left_out], start[2 - left_out]
+        np.testing.assert_array_equal(np.flatnonzero(written), np.arange(s0, s1))
+        assert (v2[1 - left_out, :, [2, 3][1 - left_out]] == v[s0]).all()

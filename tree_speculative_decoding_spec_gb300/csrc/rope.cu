@@ -92,7 +92,7 @@ __device__ __forceinline__ Token place_append(const Params& p, int n) {
     const int b = find_sequence(p.seq_start, p.B, n);
     if (b < 0) return t;
     const int s0 = p.seq_start[b], s1 = p.seq_start[b + 1];
-    if (n < s0 || n >= s1) return t;
+    if (n < s0 || n >= s1 || s0 < 0 || s1 > p.N) return t;   // a sequence with rows outside 0 .. N gets none
     const int L = p.prefix_len[b];
     if (L < 0 || static_cast<int64_t>(L) + s1 - s0 > p.cap) return t;
     const int at = L + (n - s0);
