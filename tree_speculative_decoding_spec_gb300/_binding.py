@@ -667,6 +667,7 @@ def tree_attention_scored_workspace_size(tree, B, Hq, Hkv, Lmax, D, dtype):
 # The serving calls below run once per layer and step, some for microseconds, so their checks are kept
 # short: one test that passes, and the lengthy one that names the fault only where it fails.  Pointers
 # go to the library as plain integers, and the current device is left alone where it is the tensors'.
+# A call on a given stream waits for no other: its inputs must be ready there, and buffers it is handed free.
 
 _Tensor, _i32 = torch.Tensor, torch.int32
 _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream   # of a device in use
@@ -694,11 +695,16 @@ def _buffer(ws, index):
     _need(ws, "ws", device=torch.device("cuda", index))
 
 
-def _new(stream, index, dtype, *shape):
-    """A tensor this binding allocates for a call on `stream`: its memory must outlive the call there."""
-    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
-    if stream is not None:
-        t.record_stream(stream)
+def _new(stream, index, dtype, *shape, kept=True):
+    """A tensor this binding allocates for a call on `stream`: of that stream's memory, which no work pending on the
+    current one can still use.  Where the caller gets it (`kept`) it is not reused before the current stream's work on it."""
+    device = torch.device("cuda", index)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if kept:
+        t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -759,7 +765,7 @@ def _attn(name, size, lengths, keys, q, prefix_len, k_tree, v_tree, tree, Hkv, d
         else:
             with torch.cuda.device(index):
                 n = size(tree, B, Hq, Hkv, *lengths, D, dt)
-        ws = _new(stream, index, torch.uint8, n)
+        ws = _new(stream, index, torch.uint8, n, kept=False)
     wp = _buffer(ws, index)
     _call(name, index, stream, qp, *keys, pp, kp, vp, tree.ref(), B, Hq, Hkv, *dims, D, 0.0 if scale is None else float(scale),
           score, dt, op, lp, wp, ws.nbytes)
