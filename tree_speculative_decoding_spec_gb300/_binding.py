@@ -171,10 +171,24 @@ def _need(t, name, dtype=None, ndim=None, device=None):
     return t
 
 
-def _workspace(nbytes, device, ws):
+def _new(stream, device, dtype, *shape, kept=True):
+    """A tensor this binding allocates for a call on `stream`: of that stream's memory, which no work pending on the
+    current one can still use.  Where the caller gets it (`kept`) it is not reused before the current stream's work on it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):   # anything that names a stream
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if kept:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _workspace(nbytes, device, ws, stream, kept=False):
     if ws is not None:
         return ws   # its size is checked by the library (SPEC_EWORKSPACE)
-    return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+    return _new(stream, device, torch.uint8, max(int(nbytes), 16), kept=kept)
 
 
 class Tree:
@@ -211,7 +225,7 @@ def spec_tree_build(parent, rank=None, device=None, stream=None):
     rk = (ctypes.c_int32 * len(rank))(*[int(x) for x in rank]) if rank is not None else None
     T = len(parent)
     nbytes = max(spec_tree_device_bytes(T), 16)
-    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    buf = _new(stream, device, torch.uint8, nbytes)
     st = spec_tree()
     with torch.cuda.device(device):
         _check("spec_tree_build", _lib.spec_tree_build(par, rk, T, _ptr(buf), nbytes, ctypes.byref(st), _stream(stream)))
@@ -239,7 +253,7 @@ def hydra_fold_embedding(W1, emb, out=None, stream=None):
     if _lib.hydra_fold_table_bytes(d, V) == 0:
         raise SpecError("hydra_fold_table_bytes", 1, _lib.spec_last_error().decode())
     if out is None:
-        out = torch.empty(V, d, dtype=torch.float32, device=dev)
+        out = _new(stream, dev, torch.float32, V, d)
     _need(out, "out", dtype=torch.float32, ndim=2, device=dev)
     if tuple(out.shape) != (V, d):
         raise ValueError("out must be [V, d]")
@@ -281,11 +295,11 @@ def hydra_draft(h, emb, W1, b1, W2, cond, topk, root_tok, tree, node_tok=None, n
     _need(root_tok, "root_tok", dtype=torch.int32, ndim=1, device=dev)
     T = tree.T
     if node_tok is None:
-        node_tok = torch.empty(B, T, dtype=torch.int32, device=dev)
+        node_tok = _new(stream, dev, torch.int32, B, T)
     if node_logit is None:
-        node_logit = torch.empty(B, T, dtype=torch.float32, device=dev)
+        node_logit = _new(stream, dev, torch.float32, B, T)
     if node_logprob is None and want_logprob:
-        node_logprob = torch.empty(B, T, dtype=torch.float32, device=dev)
+        node_logprob = _new(stream, dev, torch.float32, B, T)
     w1p = (ctypes.c_void_p * K)(*[W1[k].data_ptr() for k in range(K)])
     w2p = (ctypes.c_void_p * K)(*[W2[k].data_ptr() for k in range(K)])
     b1p = None if b1 is None else (ctypes.c_void_p * K)(*[(b1[k].data_ptr() if b1[k] is not None else 0) for k in range(K)])
@@ -294,7 +308,7 @@ def hydra_draft(h, emb, W1, b1, W2, cond, topk, root_tok, tree, node_tok=None, n
     nws = _lib.hydra_draft_workspace_size(tree.ref(), B, d, V, K, c, kk, dt)
     if nws == 0:
         raise SpecError("hydra_draft_workspace_size", 1, _lib.spec_last_error().decode())
-    ws = _workspace(nws, dev, ws)
+    ws = _workspace(nws, dev, ws, stream)
     if folded is not None:
         if len(folded) != K:
             raise ValueError("folded needs one entry per head")
@@ -358,15 +372,15 @@ def hydra_draft_heads(h, emb, heads, root_tok, tree, ln_eps=1e-5, node_tok=None,
     _need(root_tok, "root_tok", dtype=torch.int32, ndim=1, device=dev)
     T = tree.T
     if node_tok is None:
-        node_tok = torch.empty(B, T, dtype=torch.int32, device=dev)
+        node_tok = _new(stream, dev, torch.int32, B, T)
     if node_logit is None:
-        node_logit = torch.empty(B, T, dtype=torch.float32, device=dev)
+        node_logit = _new(stream, dev, torch.float32, B, T)
     if node_logprob is None and want_logprob:
-        node_logprob = torch.empty(B, T, dtype=torch.float32, device=dev)
+        node_logprob = _new(stream, dev, torch.float32, B, T)
     nws = _lib.hydra_draft_heads_workspace_size(tree.ref(), B, d, V, K, arr, dt)
     if nws == 0:
         raise SpecError("hydra_draft_heads_workspace_size", 1, _lib.spec_last_error().decode())
-    ws = _workspace(nws, dev, ws)
+    ws = _workspace(nws, dev, ws, stream)
     with torch.cuda.device(dev):
         _check("hydra_draft_heads", _lib.hydra_draft_heads(_ptr(h), _ptr(emb), K, arr, _ptr(root_tok), tree.ref(), B, d,
                                                            V, float(ln_eps), dt, _ptr(node_tok), _ptr(node_logit),
@@ -403,13 +417,13 @@ def tree_attention(q, k_cache, v_cache, prefix_len, k_tree, v_tree, tree, scale=
     if scale is None:
         scale = 0.0   # the library's default, 1/sqrt(D)
     if out is None:
-        out = torch.empty(B, Hq, T, D, dtype=torch.float32, device=dev)
+        out = _new(stream, dev, torch.float32, B, Hq, T, D)
     if lse is None and want_lse:
-        lse = torch.empty(B, Hq, T, dtype=torch.float32, device=dev)
+        lse = _new(stream, dev, torch.float32, B, Hq, T)
     nws = _lib.tree_attention_workspace_size(tree.ref(), B, Hq, Hkv, Lmax, D, dt)
     if nws == 0:
         raise SpecError("tree_attention_workspace_size", 1, _lib.spec_last_error().decode())
-    ws = _workspace(nws, dev, ws)
+    ws = _workspace(nws, dev, ws, stream)
     with torch.cuda.device(dev):
         _check("tree_attention", _lib.tree_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len),
                                                      _ptr(k_tree), _ptr(v_tree), tree.ref(), B, Hq, Hkv, Lmax, D,
@@ -451,13 +465,13 @@ def tree_attention_paged(q, k_pool, v_pool, block_table, prefix_len, k_tree, v_t
     if scale is None:
         scale = 0.0   # the library's default, 1/sqrt(D)
     if out is None:
-        out = torch.empty(B, Hq, T, D, dtype=torch.float32, device=dev)
+        out = _new(stream, dev, torch.float32, B, Hq, T, D)
     if lse is None and want_lse:
-        lse = torch.empty(B, Hq, T, dtype=torch.float32, device=dev)
+        lse = _new(stream, dev, torch.float32, B, Hq, T)
     nws = _lib.tree_attention_paged_workspace_size(tree.ref(), B, Hq, Hkv, max_blocks, bs, D, dt)
     if nws == 0:
         raise SpecError("tree_attention_paged_workspace_size", 1, _lib.spec_last_error().decode())
-    ws = _workspace(nws, dev, ws)
+    ws = _workspace(nws, dev, ws, stream)
     with torch.cuda.device(dev):
         _check("tree_attention_paged", _lib.tree_attention_paged(
             _ptr(q), _ptr(k_pool), _ptr(v_pool), num_blocks, _ptr(block_table), max_blocks, bs, _ptr(prefix_len),
@@ -490,9 +504,9 @@ def tree_attention_noalloc(q, k_cache, v_cache, prefix_len, k_tree, v_tree, tree
     if scale is None:
         scale = 0.0   # the library's default, 1/sqrt(D)
     if out is None:
-        out = torch.empty(B, Hq, T, D, dtype=torch.float32, device=dev)
+        out = _new(stream, dev, torch.float32, B, Hq, T, D)
     if lse is None and want_lse:
-        lse = torch.empty(B, Hq, T, dtype=torch.float32, device=dev)
+        lse = _new(stream, dev, torch.float32, B, Hq, T)
     with torch.cuda.device(dev):
         _check("tree_attention_noalloc", _lib.tree_attention_noalloc(
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree), tree.ref(),
@@ -532,17 +546,17 @@ def tree_accept(mode, logits_p, logits_q, node_tok, tree, temperature=1.0, seed=
     if tuple(node_tok.shape) != (B, T):
         raise ValueError("node_tok must be [B, T]")
     if accept_len is None:
-        accept_len = torch.empty(B, dtype=torch.int32, device=dev)
+        accept_len = _new(stream, dev, torch.int32, B)
     if accept_path is None:
-        accept_path = torch.empty(B, tree.max_depth + 1, dtype=torch.int32, device=dev)
+        accept_path = _new(stream, dev, torch.int32, B, tree.max_depth + 1)
     if next_token is None:
-        next_token = torch.empty(B, dtype=torch.int32, device=dev)
+        next_token = _new(stream, dev, torch.int32, B)
     if margin is None and want_margin:
-        margin = torch.empty(B, dtype=torch.float32, device=dev)
+        margin = _new(stream, dev, torch.float32, B)
     nws = _lib.tree_accept_workspace_size(int(mode), tree.ref(), B, V)
     if nws == 0:
         raise SpecError("tree_accept_workspace_size", 1, _lib.spec_last_error().decode())
-    ws = _workspace(nws, dev, ws)
+    ws = _workspace(nws, dev, ws, stream)
     with torch.cuda.device(dev):
         _check("tree_accept", _lib.tree_accept(int(mode), _ptr(logits_p), _ptr(logits_q if mode == 1 else None),
                                                _ptr(node_tok), tree.ref(), B, V, float(temperature), int(seed),
@@ -576,7 +590,7 @@ def tree_kv_commit(k_tree, v_tree, k_cache, v_cache, prefix_len, accept_len, acc
     if prefix_len.shape[0] != B or accept_len.shape[0] != B or tuple(accept_path.shape) != (B, tree.max_depth + 1):
         raise ValueError("prefix_len, accept_len [B] and accept_path [B, max_depth + 1] must match")
     dt = _dtype_code(k_tree)
-    ws = _workspace(int(_lib.tree_kv_commit_workspace_size()), dev, ws)
+    ws = _workspace(int(_lib.tree_kv_commit_workspace_size()), dev, ws, stream, kept=True)
     with torch.cuda.device(dev):
         _check("tree_kv_commit", _lib.tree_kv_commit(_ptr(k_tree), _ptr(v_tree), _ptr(k_cache), _ptr(v_cache),
                                                      _ptr(prefix_len), _ptr(accept_len), _ptr(accept_path),
@@ -609,7 +623,7 @@ def tree_kv_commit_paged(k_tree, v_tree, k_pool, v_pool, block_table, block_size
     if prefix_len.shape[0] != B or accept_len.shape[0] != B or tuple(accept_path.shape) != (B, tree.max_depth + 1):
         raise ValueError("prefix_len, accept_len [B] and accept_path [B, max_depth + 1] must match")
     dt = _dtype_code(k_tree)
-    ws = _workspace(int(_lib.tree_kv_commit_workspace_size()), dev, ws)
+    ws = _workspace(int(_lib.tree_kv_commit_workspace_size()), dev, ws, stream, kept=True)
     with torch.cuda.device(dev):
         _check("tree_kv_commit_paged", _lib.tree_kv_commit_paged(
             _ptr(k_tree), _ptr(v_tree), _ptr(k_pool), _ptr(v_pool), num_blocks, _ptr(block_table),
@@ -631,17 +645,17 @@ def tree_accept_typical(logits_p, node_tok, tree, temperature=1.0, epsilon=0.09,
     if tuple(node_tok.shape) != (B, T):
         raise ValueError("node_tok must be [B, T]")
     if accept_len is None:
-        accept_len = torch.empty(B, dtype=torch.int32, device=dev)
+        accept_len = _new(stream, dev, torch.int32, B)
     if accept_path is None:
-        accept_path = torch.empty(B, tree.max_depth + 1, dtype=torch.int32, device=dev)
+        accept_path = _new(stream, dev, torch.int32, B, tree.max_depth + 1)
     if next_token is None:
-        next_token = torch.empty(B, dtype=torch.int32, device=dev)
+        next_token = _new(stream, dev, torch.int32, B)
     if margin is None and want_margin:
-        margin = torch.empty(B, dtype=torch.float32, device=dev)
+        margin = _new(stream, dev, torch.float32, B)
     nws = _lib.tree_accept_workspace_size(2, tree.ref(), B, V)
     if nws == 0:
         raise SpecError("tree_accept_workspace_size", 1, _lib.spec_last_error().decode())
-    ws = _workspace(nws, dev, ws)
+    ws = _workspace(nws, dev, ws, stream)
     with torch.cuda.device(dev):
         _check("tree_accept_typical", _lib.tree_accept_typical(
             _ptr(logits_p), _ptr(node_tok), tree.ref(), B, V, float(temperature), float(epsilon), float(alpha),
@@ -693,19 +707,6 @@ def _buffer(ws, index):
     if isinstance(ws, torch.Tensor) and ws.get_device() == index and ws.is_contiguous():
         return ws.data_ptr()   # its size is checked by the library (SPEC_EWORKSPACE)
     _need(ws, "ws", device=torch.device("cuda", index))
-
-
-def _new(stream, index, dtype, *shape, kept=True):
-    """A tensor this binding allocates for a call on `stream`: of that stream's memory, which no work pending on the
-    current one can still use.  Where the caller gets it (`kept`) it is not reused before the current stream's work on it."""
-    device = torch.device("cuda", index)
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if kept:
-        t.record_stream(torch.cuda.current_stream(device))
-    return t
 
 
 def _call(name, index, stream, *args):
@@ -963,8 +964,7 @@ def tree_rope(q, k, v, prefix_len, tree, freq=None, interleaved=False, pos_base=
 
 def spec_philox_uniform(seed, offset, B, T, device=None, stream=None):
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    ua = torch.empty(B, T, dtype=torch.float32, device=device)
-    us = torch.empty(B, dtype=torch.float32, device=device)
+    ua, us = _new(stream, device, torch.float32, B, T), _new(stream, device, torch.float32, B)
     with torch.cuda.device(device):
         _check("spec_philox_uniform", _lib.spec_philox_uniform(int(seed), int(offset), B, T, _ptr(ua), _ptr(us),
                                                                _stream(stream)))
