@@ -545,3 +545,11 @@ def test_a_maximum_that_jumps_in_an_items_first_tile(name, score):
     for _ in range(40):
         again, lse2 = c.call(ws=ws)
         assert (again == out).all() and (lse2 == lse).all()
+
+
+def test_a_window_that_does_not_fit_is_refused():
+    for Ls, block in ((0, 0), (16, 0), (0, 16), (16, 16)):
+        c = Case("bf16", B=2, Hq=4, Hkv=2, D=64, T=3, lens=(4, 3), Lmax=16, Ls=Ls, block=block)
+        for window in (1 << 31, (1 << 32) + 5, 2.5):
+            with pytest.raises(ValueError, match="window"):
+                c.call(window=window)

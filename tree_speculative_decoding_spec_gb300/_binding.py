@@ -740,6 +740,15 @@ def _pool(k_pool):
     return k_pool.shape
 
 
+def _score(softcap, window, slopes):
+    """The spec_score of a call, None where nothing happens to its scores; a 32-bit field takes any integer, cut down."""
+    if not softcap and not window and slopes is None:
+        return None
+    if not -0x80000000 <= window <= 0x7fffffff or int(window) != window:
+        raise ValueError(f"window = {window}: a whole number of positions below 2^31, or 0 for none")
+    return spec_score(float(softcap), int(window), slopes)
+
+
 def _attn(name, size, lengths, keys, q, prefix_len, k_tree, v_tree, tree, Hkv, dims, scale, softcap, window, slopes, out, lse,
           want_lse, ws, stream):
     """What the shared and scored attention calls have in common: the checks, the outputs and the call.  `lengths`
@@ -750,10 +759,7 @@ def _attn(name, size, lengths, keys, q, prefix_len, k_tree, v_tree, tree, Hkv, d
     qp = _at(q, "q", dtype, index, B, Hq, T, D)
     kp, vp = _at(k_tree, "k_tree", dtype, index, B, Hkv, T, D), _at(v_tree, "v_tree", dtype, index, B, Hkv, T, D)
     pp = _at(prefix_len, "prefix_len", _i32, index, B)
-    score = None
-    if softcap or window or slopes is not None:
-        sl = None if slopes is None else _at(slopes, "slopes", torch.float32, index, Hq)
-        score = ctypes.byref(spec_score(float(softcap), int(window), sl))
+    score = _score(softcap, window, None if slopes is None else _at(slopes, "slopes", torch.float32, index, Hq))
     if out is None:
         out = _new(stream, index, dtype, B, Hq, T, D)
     op = _at(out, "out", dtype, index, B, Hq, T, D)
@@ -769,7 +775,7 @@ def _attn(name, size, lengths, keys, q, prefix_len, k_tree, v_tree, tree, Hkv, d
         ws = _new(stream, index, torch.uint8, n, kept=False)
     wp = _buffer(ws, index)
     _call(name, index, stream, qp, *keys, pp, kp, vp, tree.ref(), B, Hq, Hkv, *dims, D, 0.0 if scale is None else float(scale),
-          score, dt, op, lp, wp, ws.nbytes)
+          None if score is None else ctypes.byref(score), dt, op, lp, wp, ws.nbytes)
     return out, lse
 
 
