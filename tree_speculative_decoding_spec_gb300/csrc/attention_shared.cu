@@ -278,7 +278,7 @@ constexpr int kJoin = 256;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoin) k_attn_shared_join(const Params p, int n_rg, int R) {
     constexpr int C = D / 4 / (kJoin / 32);   // float4 columns per warp
-    __shared__ T tile[32][D + 16 / sizeof(T)];
+    __shared__ __align__(16) T tile[32][D + 16 / sizeof(T)];   // read 16 bytes at a time
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = divide(blockIdx.x, n_rg), r0 = (blockIdx.x - col * n_rg) * 32;
     const int b = divide(col, p.Hkv), kvh = col - b * p.Hkv;
