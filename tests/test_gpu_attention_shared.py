@@ -553,3 +553,15 @@ def test_a_window_that_does_not_fit_is_refused():
         for window in (1 << 31, (1 << 32) + 5, 2.5):
             with pytest.raises(ValueError, match="window"):
                 c.call(window=window)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 20, 100])
+def test_the_largest_windows_hide_nothing(T, dtype):
+    """Up to the largest number the field holds, over partial tiles of shared and own keys."""
+    for window in ((1 << 24) - 1, 1 << 24, (1 << 31) - 100, (1 << 31) - 1):
+        c = Case(dtype, B=2, Hq=6, Hkv=2, D=64, T=T, lens=(65, 200), Lmax=200, Ls=70, window=window)
+        out, lse = c.call()
+        ref = {**c.score, "window": 0}
+        c.score = ref
+        c.check(out, lse)

@@ -519,7 +519,7 @@ static spec_status run(Params p, const spec_tree* tree, spec_dtype dt, float sca
             return fail(SPEC_EINVAL, "softcap = %g: 1e-6 to 4096, or 0 for none", score->softcap);
         if (score->window < 0) return fail(SPEC_EINVAL, "window = %d must be positive, or 0", score->window);
         p.softcap = score->softcap;
-        p.window = score->window;
+        p.window = std::min(score->window, 1 << 24);   // beyond every distance, and sums with positions stay within 32 bits
         p.slopes = score->slopes;
     }
     if (!aligned16(p.q) || !aligned16(p.kc) || !aligned16(p.vc) || !aligned16(p.ks) || !aligned16(p.vs) || !aligned16(p.kt) ||
