@@ -174,3 +174,25 @@ def test_captured_on_the_given_stream(name):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert a.dtype == torch.uint8 or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", SERVING)
+def test_captured_on_a_stream_that_joins_the_capture(name):
+    """Two calls on a side stream inside a capture, the first one's results dropped at once, replayed twice."""
+    import torch
+    call = _calls(lib())[name]
+    want = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        call(stream=side)
+        got = call(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert a.dtype == torch.uint8 or torch.equal(a, b)
