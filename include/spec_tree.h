@@ -34,9 +34,11 @@
  *    before its kernels can record anything (any prior content, including
  *    garbage in a fresh workspace, is discarded), so a workspace may be reused
  *    by any later call on the same stream.
- *  - Tokens are int32, logits and outputs float32; inputs of the float tensors
- *    of a call share one spec_dtype (float32 or bfloat16 bit patterns).
- *  - Tensor shapes are given outermost first and are densely packed (row-major).
+ *  - Tokens are int32, logits and outputs float32 unless a call says otherwise;
+ *    inputs of the float tensors of a call share one spec_dtype (float32 or
+ *    bfloat16 bit patterns).
+ *  - Tensor shapes are given outermost first and are densely packed (row-major)
+ *    where a call takes no strides.
  */
 #ifndef SPEC_TREE_H
 #define SPEC_TREE_H
@@ -476,6 +478,7 @@ spec_status tree_kv_commit_paged(const void* k_tree, const void* v_tree, void* k
  *     x = softcap * tanh(x / softcap)       if softcap > 0
  *     x = x - slopes[h] * (P - p)           if slopes, h the query head
  *     the key is seen only if P - p < window, if window > 0 (the query itself always is)
+ * With bf16 inputs a capped score, and with it lse, is off by some 2^-22 of the cap.
  */
 typedef struct {
     float softcap;          /* 0: none; else 1e-6 to 4096 */

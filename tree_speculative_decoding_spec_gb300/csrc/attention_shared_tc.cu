@@ -565,7 +565,7 @@ __device__ __forceinline__ bool softmax_few(const Params& p, const Desc& it, con
 #pragma unroll
     for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(raw[e]) * scale2;
     if constexpr (kScored) {
-        if (p.softcap > 0.f) {   // see cap64
+        if (p.softcap > 0.f) {   // Cap's last form, for small scores too: off by some 2^-22 of the cap
             const float cap2 = p.softcap * kLog2e, k2 = 2.f / p.softcap;   // x is log2 e times the score
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = fmaf(-2.f * cap2, rcp(ex2(x[e] * k2) + 1.f), cap2);
