@@ -69,6 +69,7 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 #define SPEC_MAX_T 1024      /* tree nodes, root included */
 #define SPEC_MAX_DEPTH 16    /* deepest node; also the most draft heads */
 #define SPEC_MAX_TOPK 16     /* largest top-k per head */
+#define SPEC_MAX_BEAMS 64    /* beams of a sequence */
 
 /*
  * Candidate tree, encoded once per topology by spec_tree_build.
@@ -649,6 +650,170 @@ spec_status tree_rope(const void* q, const void* k, const void* v, int64_t q_str
                       const int32_t* prefix_len, const int32_t* pos_base, const double* freq, int32_t rot,
                       int32_t interleaved, spec_dtype dt, void* q_out, void* k_tree, void* v_tree,
                       spec_stream_t s);
+
+/* Workspace bytes beam_select needs on the current device (0 on invalid arguments). */
+size_t beam_select_workspace_size(int32_t B, int32_t W, int32_t V, int32_t K);
+
+/*
+ * Selection of a beam search, for drafts that extend their best continuations step by step:
+ * of every sequence's W beams the K best (beam, token) pairs.  For a live beam w and a token t
+ *     score  = scores[w] + x[w, t] - log sum_u exp x[w, u],   length = length[w] + 1
+ * An ended beam (ended[w] != 0) offers itself: token eos, score and length as they are; its
+ * logits are not read.  A beam whose score is not finite offers nothing (a first step has one
+ * live beam and the others at -inf).  Pairs are ranked by score / max(length, 1)^alpha, in 64
+ * bits, equal ones by the lower beam, then the lower token.
+ *
+ *   logits      device [B, W] rows of V logits (dt), row_stride >= V elements between rows; rows
+ *               may start anywhere, the first 16-byte aligned.  NaN counts as -inf, and
+ *               -inf is never chosen.  A beam with a logit of +inf offers nothing, and
+ *               SPEC_EINVAL goes to the status word
+ *   scores      device [B, W] float32: log-probabilities so far
+ *   ended, length  device [B, W] or NULL (none ended; lengths 0)
+ *   eos         token that ends a beam, or -1 (then ended must be NULL)
+ *   alpha       0 (rank by the score) .. 16
+ *   token, parent, score  device [B, K] out, best first: the token, the beam it continues and the
+ *               new score.  Where fewer pairs exist: -1, -1, -inf
+ *   ended_out, length_out  device [B, K] out or NULL: whether it has ended (its parent had, or its
+ *               token is eos; 1 where there is no pair), its length (0)
+ * Shapes: W, K <= SPEC_MAX_BEAMS, 2 <= V <= 2^24.  With K == W, score may be scores, ended_out
+ * ended and length_out length; outputs must not overlap an input otherwise.
+ */
+spec_status beam_select(const void* logits, int64_t row_stride, const float* scores, const int32_t* ended,
+                        const int32_t* length, int32_t B, int32_t W, int32_t V, int32_t K, int32_t eos, float alpha,
+                        spec_dtype dt, int32_t* token, int32_t* parent, float* score, int32_t* ended_out,
+                        int32_t* length_out, void* ws, size_t ws_bytes, spec_stream_t s);
+
+/* Workspace bytes beam_reorder, kv_reorder and kv_reorder_paged need (their status word only). */
+size_t beam_reorder_workspace_size(void);
+
+/*
+ * Reorder a state of the beams in place: row w of sequence b becomes what row parent[b, w] was.
+ * Rows whose parent is their own beam or -1 stay.
+ *   state    device [B, W] rows of row_bytes bytes (a multiple of 4): hidden states, token histories
+ *   parent   device [B, W], each in -1 .. W - 1.  Others are reported as SPEC_EINVAL in the status
+ *            word and their beams stay
+ */
+spec_status beam_reorder(void* state, int64_t row_bytes, const int32_t* parent, int32_t B, int32_t W, void* ws,
+                         size_t ws_bytes, spec_stream_t s);
+
+/*
+ * beam_reorder of the beams' caches: positions start[b] .. end[b] - 1 of every KV head.  What lies in
+ * front (a prompt that all beams of the sequence have alike) and behind stays.
+ *   k_cache, v_cache  device [B * W, Hkv, Lmax, D] (dt), beam w of sequence b at b * W + w
+ *   start, end        device [B], 0 <= start <= end <= Lmax; others are reported as SPEC_EINVAL in
+ *                     the status word and the sequence stays
+ * Shapes: D a multiple of 16 bytes, D <= 1024.
+ */
+spec_status kv_reorder(void* k_cache, void* v_cache, const int32_t* parent, const int32_t* start, const int32_t* end,
+                       int32_t B, int32_t W, int32_t Hkv, int32_t Lmax, int32_t D, spec_dtype dt, void* ws,
+                       size_t ws_bytes, spec_stream_t s);
+
+/*
+ * kv_reorder in a paged cache (tree_kv_commit_paged's layout).
+ *   block_table  device [B * W, max_blocks]: the entries of positions start[b] .. end[b] - 1 are
+ *                read; blocks in that range belong to one beam each.  Positions in a block
+ *                outside the pool, of either side, stay, and SPEC_EINVAL goes to the status word
+ */
+spec_status kv_reorder_paged(void* k_pool, void* v_pool, int32_t num_blocks, const int32_t* block_table,
+                             int32_t max_blocks, int32_t block_size, const int32_t* parent, const int32_t* start,
+                             const int32_t* end, int32_t B, int32_t W, int32_t Hkv, int32_t D, spec_dtype dt, void* ws,
+                             size_t ws_bytes, spec_stream_t s);
+
+/* Workspace bytes kv_weigh and its paged form (Lmax = max_blocks * block_size; path_len 0 without a
+ * path) need on the current device (0 on invalid arguments). */
+size_t kv_weigh_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t path_len, int32_t Lmax,
+                               int32_t D, spec_dtype dt);
+
+/*
+ * Add up the attention weight that cached keys receive, the measure kv_evict goes by.  To be
+ * called once the rows' own keys are in the cache (tree_kv_commit, kv_append), with the
+ * queries and the lse of the attention they went through:
+ *     acc[b, h, j] = decay * acc[b, h, j] + sum over rows r of h's query heads that see key j of
+ *                    exp(scale * q_r . k_j - lse_r)
+ * The rows that count are the last `count` tokens of the sequence: nodes accept_path[b, 0 ..
+ * accept_len[b]] of a tree (tree_accept's outputs), or rows 0 .. n_rows[b] - 1 of q; row i
+ * sees keys 0 .. prefix_len[b] - count + i.  The rows' own keys start at 0 instead of decay * acc.
+ *
+ *   q            device [B, Hq, T, D] (dt), finite in the rows that count
+ *   lse          device [B, Hq, T] float32; a row whose lse is not finite (it saw nothing) adds nothing
+ *   k_cache      device [B, Hkv, Lmax, D] (dt).  Rows >= prefix_len[b] do not affect the result but must
+ *                be readable
+ *   prefix_len   device [B]: keys in the cache, those of the rows included
+ *   seen         device [B] or NULL (prefix_len): tokens of the sequence so far, evicted ones included
+ *   n_rows       device [B], 0 .. T, or NULL (T, or those of the path)
+ *   accept_len, accept_path  device [B], [B, path_len] or NULL; path_len (max_depth + 1) <= 17
+ *   decay        0 .. 1; 0 forgets what acc holds, whatever it is
+ *   acc          device [B, Hkv, Lmax] float32, updated below prefix_len[b]
+ *   pos          device [B, Hkv, Lmax] int32 or NULL: the rows' own keys get their positions,
+ *                seen[b] - prefix_len[b] + j
+ *   scale        > 0, or 0 for the usual 1/sqrt(D)
+ * Shapes: Hq % Hkv == 0, D in {64, 128}.  Sums are in 32 bits, in a fixed order.  A sequence
+ * with more rows than keys, a length outside 0 .. Lmax, rows outside 0 .. T or a path outside the
+ * tree is left unchanged and SPEC_EINVAL goes to the status word.
+ */
+spec_status kv_weigh(const void* q, const float* lse, const void* k_cache, const int32_t* prefix_len,
+                     const int32_t* seen, const int32_t* n_rows, const int32_t* accept_len,
+                     const int32_t* accept_path, int32_t path_len, int32_t B, int32_t Hq, int32_t Hkv, int32_t T,
+                     int32_t Lmax, int32_t D, float scale, float decay, spec_dtype dt, float* acc, int32_t* pos,
+                     void* ws, size_t ws_bytes, spec_stream_t s);
+
+/*
+ * kv_weigh over a paged cache: pool [num_blocks, Hkv, block_size, D], block_size a multiple of 16,
+ * acc and pos [B, Hkv, max_blocks * block_size] by position in the cache.  Keys in a block outside the
+ * pool keep their acc, and SPEC_EINVAL goes to the status word.
+ */
+spec_status kv_weigh_paged(const void* q, const float* lse, const void* k_pool, int32_t num_blocks,
+                           const int32_t* block_table, int32_t max_blocks, int32_t block_size,
+                           const int32_t* prefix_len, const int32_t* seen, const int32_t* n_rows,
+                           const int32_t* accept_len, const int32_t* accept_path, int32_t path_len, int32_t B,
+                           int32_t Hq, int32_t Hkv, int32_t T, int32_t D, float scale, float decay, spec_dtype dt,
+                           float* acc, int32_t* pos, void* ws, size_t ws_bytes, spec_stream_t s);
+
+/* Workspace bytes kv_evict and its paged form (Lmax = max_blocks * block_size) need (0 on invalid arguments). */
+size_t kv_evict_workspace_size(int32_t B, int32_t Hkv, int32_t Lmax, int32_t budget);
+
+/*
+ * Evict keys from the cache: every KV head of a sequence with more than `budget` keys keeps
+ * `budget` of them, each head its own.  First come the protected ones, with pos < sink or
+ * pos >= seen[b] - recent, then those of the largest acc (NaN last), equal ones by the lower place.
+ * Kept keys at places below the budget stay there; the i-th free place below the budget, in
+ * ascending order, takes the i-th kept key from behind it, with its value, acc and pos.  So the cache's
+ * order is lost, and pos tells where a key belongs: attention over rotated keys (tree_attention,
+ * tree_attention_shared without a window or bias) does not depend on it.  New tokens are
+ * rotated by `seen` (tree_rope's prefix_len) and go to place len_out[b].
+ *
+ *   k_cache, v_cache  device [B, Hkv, Lmax, D] (dt)
+ *   prefix_len   device [B], 0 .. Lmax
+ *   seen         device [B] or NULL (prefix_len): tokens of the sequence so far
+ *   acc, pos     device [B, Hkv, Lmax] float32, int32 (kv_weigh)
+ *   budget       1 .. 2^22; sink, recent >= 0, together at most the budget
+ *   k_out, v_out, acc_out, pos_out  NULL: in place, places from budget on are left as they are.
+ *                Else another cache [B, Hkv, Lout, D] and its weights and positions [B, Hkv, Lout], Lout >=
+ *                min(budget, Lmax): its first min(prefix_len, budget) places get what the cache would have
+ *                there, and the cache stays.  The two must not overlap
+ *   len_out      device [B] out: min(prefix_len, budget).  It must not overlap prefix_len or seen
+ * Shapes: D a multiple of 16 bytes, D <= 1024, B * Hkv <= 65535.  A sequence with a length
+ * outside its room is left unchanged (len_out: its prefix_len) and SPEC_EINVAL goes to the status word.
+ */
+spec_status kv_evict(void* k_cache, void* v_cache, const int32_t* prefix_len, const int32_t* seen, float* acc,
+                     int32_t* pos, int32_t B, int32_t Hkv, int32_t Lmax, int32_t D, int32_t budget, int32_t sink,
+                     int32_t recent, void* k_out, void* v_out, float* acc_out, int32_t* pos_out, int32_t Lout,
+                     int32_t* len_out, spec_dtype dt, void* ws, size_t ws_bytes, spec_stream_t s);
+
+/*
+ * kv_evict in a paged cache (tree_kv_commit_paged's layout); acc and pos [B, Hkv, max_blocks *
+ * block_size] by place.  In place, blocks behind the budget's last are free afterwards.
+ *   out_table    device [B, out_blocks] or NULL: blocks of the same pool to go to, none of which a
+ *                sequence reads; acc_out, pos_out [B, Hkv, out_blocks * block_size] with it
+ * A sequence with a table entry in use outside 0 .. num_blocks-1 is left unchanged and
+ * SPEC_EINVAL goes to the status word.
+ */
+spec_status kv_evict_paged(void* k_pool, void* v_pool, int32_t num_blocks, const int32_t* block_table,
+                           int32_t max_blocks, int32_t block_size, const int32_t* prefix_len, const int32_t* seen,
+                           float* acc, int32_t* pos, int32_t B, int32_t Hkv, int32_t D, int32_t budget, int32_t sink,
+                           int32_t recent, const int32_t* out_table, int32_t out_blocks, float* acc_out,
+                           int32_t* pos_out, int32_t* len_out, spec_dtype dt, void* ws, size_t ws_bytes,
+                           spec_stream_t s);
 
 /* Message of the last failed call on this host thread ("" if none). */
 const char* spec_last_error(void);

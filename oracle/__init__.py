@@ -33,7 +33,7 @@ from .heads import silu, hydra_draft, hydra_draft_heads
 from .attention import tree_attention, tree_attention_paged, gather_pages
 from .accept import greedy_accept, rejection_accept, typical_accept
 from .kv_commit import kv_commit, kv_commit_paged
-from . import attention_shared, rope
+from . import attention_shared, beam, evict, rope
 from .philox import philox4, philox4x32_10, philox_uniform_pair, uniform_from_u32
 
 __all__ = [
@@ -43,5 +43,5 @@ __all__ = [
     "tree_attention", "tree_attention_paged", "gather_pages",
     "greedy_accept", "rejection_accept", "typical_accept", "kv_commit",
     "philox4", "philox4x32_10", "philox_uniform_pair", "uniform_from_u32",
-    "kv_commit_paged", "attention_shared", "rope",
+    "kv_commit_paged", "attention_shared", "beam", "evict", "rope",
 ]

@@ -17,6 +17,8 @@ __all__ = [
     "tree_accept", "tree_accept_workspace_size", "tree_accept_typical",
     "tree_kv_commit", "tree_kv_commit_paged", "tree_kv_commit_workspace_size",
     "kv_append", "kv_append_paged", "kv_append_workspace_size", "tree_rope",
+    "beam_select", "beam_select_workspace_size", "beam_reorder", "beam_reorder_workspace_size", "kv_reorder", "kv_reorder_paged",
+    "kv_weigh", "kv_weigh_paged", "kv_weigh_workspace_size", "kv_evict", "kv_evict_paged", "kv_evict_workspace_size",
     "spec_philox_uniform", "spec_read_device_status", "spec_last_error", "spec_selftest_timeout",
     "spec_trace_begin", "spec_trace_end", "spec_launch_count",
     "SpecError", "Tree",

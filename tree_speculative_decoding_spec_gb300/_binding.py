@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libspec_tree.so")
 SPEC_MAX_T = 1024
 SPEC_MAX_DEPTH = 16
 SPEC_MAX_TOPK = 16
+SPEC_MAX_BEAMS = 64
 SPEC_F32, SPEC_BF16 = 0, 1
 STATUS_NAMES = {0: "SPEC_OK", 1: "SPEC_EINVAL", 2: "SPEC_ETREE", 3: "SPEC_EALIGN", 4: "SPEC_EWORKSPACE",
                 5: "SPEC_EUNSUPPORTED", 6: "SPEC_ECUDA", 7: "SPEC_ETIMEOUT"}
@@ -110,6 +111,22 @@ def _load():
                                   i32, vp, i32, i32, i32, vp, vp, sz, vp]),
         "tree_rope": (i32, [vp, vp, vp, i64, i64, i64, tp, i32, i32, i32, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp,
                             vp]),
+        "beam_select_workspace_size": (sz, [i32, i32, i32, i32]),
+        "beam_select": (i32, [vp, i64, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "beam_reorder_workspace_size": (sz, []),
+        "beam_reorder": (i32, [vp, i64, vp, i32, i32, vp, sz, vp]),
+        "kv_reorder": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, sz, vp]),
+        "kv_reorder_paged": (i32, [vp, vp, i32, vp, i32, i32, vp, vp, vp, i32, i32, i32, i32, i32, vp, sz, vp]),
+        "kv_weigh_workspace_size": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
+        "kv_weigh": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, f32, i32, vp, vp, vp, sz,
+                           vp]),
+        "kv_weigh_paged": (i32, [vp, vp, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, f32,
+                                 i32, vp, vp, vp, sz, vp]),
+        "kv_evict_workspace_size": (sz, [i32, i32, i32, i32]),
+        "kv_evict": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp, i32, vp, sz,
+                           vp]),
+        "kv_evict_paged": (i32, [vp, vp, i32, vp, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, i32, vp, vp, vp,
+                                 i32, vp, sz, vp]),
         "spec_philox_uniform": (i32, [u64, u64, i32, i32, vp, vp, vp]),
         "spec_last_error": (ctypes.c_char_p, []),
         "spec_read_device_status": (i32, [vp, _i32p, vp]),
@@ -966,6 +983,226 @@ def tree_rope(q, k, v, prefix_len, tree, freq=None, interleaved=False, pos_base=
           _at(q_out, "q_out", dtype, index, B, Hq, T, D), _at(k_out, "k_out", dtype, index, B, Hkv, T, D),
           _at(v_out, "v_out", dtype, index, B, Hkv, T, D))
     return q_out, k_out, v_out
+
+
+# ---- beams and eviction
+
+def beam_select_workspace_size(B, W, V, K):
+    n = _lib.beam_select_workspace_size(B, W, V, K)
+    if n == 0:
+        raise SpecError("beam_select_workspace_size", 1, _lib.spec_last_error().decode())
+    return int(n)
+
+
+def _whole(x, name):
+    """A number that a 32-bit field takes as it is: ctypes cuts down any integer."""
+    if not -0x80000000 <= x <= 0x7fffffff or int(x) != x:
+        raise ValueError(f"{name} = {x}: a whole number below 2^31")
+    return int(x)
+
+
+def _sized(size, index, stream, *args):
+    """A workspace of size(*args) bytes on device `index`."""
+    if _device() == index:
+        n = size(*args)
+    else:
+        with torch.cuda.device(index):
+            n = size(*args)
+    return _new(stream, index, torch.uint8, n, kept=False)
+
+
+def beam_select(logits, scores, K, eos=-1, ended=None, length=None, alpha=0.0, token=None, parent=None, score=None,
+                ended_out=None, length_out=None, ws=None, stream=None):
+    """The K best continuations over beams and vocabulary: returns (token, parent, score, ended, length), all [B, K].
+
+    logits [B, W, V] (rows evenly spaced, slices of padded rows allowed), scores [B, W] float32, ended and length [B, W]
+    int32 or None.  With K == W the last three outputs may be scores, ended and length themselves."""
+    if not isinstance(logits, _Tensor) or not logits.is_cuda or logits.dim() != 3:
+        raise ValueError("logits must be a CUDA tensor [B, W, V]")
+    index, dt, (B, W, V) = logits.get_device(), _dtype_code(logits), logits.shape
+    sb, sw, sv = logits.stride()
+    if W == 1:
+        sw = sb if B > 1 else V
+    if sv != 1 or (B > 1 and sb != W * sw):
+        raise ValueError("logits: a row's logits must be dense and the rows evenly spaced")
+    sp = _at(scores, "scores", torch.float32, index, B, W)
+    ep = None if ended is None else _at(ended, "ended", _i32, index, B, W)
+    np_ = None if length is None else _at(length, "length", _i32, index, B, W)
+    K, eos = _whole(K, "K"), _whole(eos, "eos")
+    if not 1 <= K <= SPEC_MAX_BEAMS:
+        raise ValueError(f"K = {K} out of 1..{SPEC_MAX_BEAMS}")
+    token = _new(stream, index, _i32, B, K) if token is None else token
+    parent = _new(stream, index, _i32, B, K) if parent is None else parent
+    score = _new(stream, index, torch.float32, B, K) if score is None else score
+    ended_out = _new(stream, index, _i32, B, K) if ended_out is None else ended_out
+    length_out = _new(stream, index, _i32, B, K) if length_out is None else length_out
+    if ws is None:
+        ws = _sized(beam_select_workspace_size, index, stream, B, W, V, K)
+    _call("beam_select", index, stream, logits.data_ptr(), sw, sp, ep, np_, B, W, V, K, eos, float(alpha), dt,
+          _at(token, "token", _i32, index, B, K), _at(parent, "parent", _i32, index, B, K),
+          _at(score, "score", torch.float32, index, B, K), _at(ended_out, "ended_out", _i32, index, B, K),
+          _at(length_out, "length_out", _i32, index, B, K), _buffer(ws, index), ws.nbytes)
+    return token, parent, score, ended_out, length_out
+
+
+def beam_reorder_workspace_size():
+    return int(_lib.beam_reorder_workspace_size())
+
+
+def _beams(parent, index):
+    """(address, B, W) of the parents."""
+    if not isinstance(parent, _Tensor) or parent.dim() != 2:
+        raise ValueError("parent must be a tensor [B, W]")
+    B, W = parent.shape
+    return _at(parent, "parent", _i32, index, B, W), B, W
+
+
+def beam_reorder(state, parent, ws=None, stream=None):
+    """Reorder a state [B, W, ...] of any type in place by parent [B, W] (-1: stays): returns the state."""
+    if not isinstance(state, _Tensor) or not state.is_cuda or state.dim() < 2:
+        raise ValueError("state must be a CUDA tensor [B, W, ...]")
+    index = state.get_device()
+    pp, B, W = _beams(parent, index)
+    if tuple(state.shape[:2]) != (B, W) or not state.is_contiguous():
+        raise ValueError(f"state must be contiguous [{B}, {W}, ...], got {tuple(state.shape)}")
+    if ws is None:
+        ws = _new(stream, index, torch.uint8, beam_reorder_workspace_size(), kept=False)
+    _call("beam_reorder", index, stream, state.data_ptr(), state.nbytes // (B * W) if B * W else 0, pp, B, W, _buffer(ws, index), ws.nbytes)
+    return state
+
+
+def kv_reorder(k_cache, v_cache, parent, start, end, ws=None, stream=None):
+    """Reorder positions start[b] .. end[b] - 1 of the beams' caches [B * W, Hkv, Lmax, D] in place: returns ws."""
+    index, dtype, dt, (rows, Hkv, Lmax, D) = _queries(k_cache, "k_cache")
+    pp, B, W = _beams(parent, index)
+    kp, vp = _at(k_cache, "k_cache", dtype, index, B * W, Hkv, Lmax, D), _at(v_cache, "v_cache", dtype, index, rows, Hkv, Lmax, D)
+    if ws is None:
+        ws = _new(stream, index, torch.uint8, beam_reorder_workspace_size())
+    _call("kv_reorder", index, stream, kp, vp, pp, _at(start, "start", _i32, index, B), _at(end, "end", _i32, index, B), B, W, Hkv,
+          Lmax, D, dt, _buffer(ws, index), ws.nbytes)
+    return ws
+
+
+def kv_reorder_paged(k_pool, v_pool, block_table, parent, start, end, ws=None, stream=None):
+    """kv_reorder in a paged cache: pools [num_blocks, Hkv, block_size, D], block_table [B * W, max_blocks] int32."""
+    index, dtype, dt, (blocks, Hkv, bs, D) = _queries(k_pool, "k_pool")
+    pp, B, W = _beams(parent, index)
+    most = block_table.shape[1] if isinstance(block_table, _Tensor) and block_table.dim() == 2 else 0
+    kp, vp = _at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), _at(v_pool, "v_pool", dtype, index, blocks, Hkv, bs, D)
+    if ws is None:
+        ws = _new(stream, index, torch.uint8, beam_reorder_workspace_size())
+    _call("kv_reorder_paged", index, stream, kp, vp, blocks, _at(block_table, "block_table", _i32, index, B * W, most), most, bs, pp,
+          _at(start, "start", _i32, index, B), _at(end, "end", _i32, index, B), B, W, Hkv, D, dt, _buffer(ws, index), ws.nbytes)
+    return ws
+
+
+def kv_weigh_workspace_size(B, Hq, Hkv, T, path_len, Lmax, D, dtype):
+    n = _lib.kv_weigh_workspace_size(B, Hq, Hkv, T, path_len, Lmax, D, dtype)
+    if n == 0:
+        raise SpecError("kv_weigh_workspace_size", 1, _lib.spec_last_error().decode())
+    return int(n)
+
+
+def _weigh(name, q, lse, keys, prefix_len, acc, pos, seen, n_rows, accept_len, accept_path, decay, scale, ws, stream, Hkv, cap, dims):
+    """What both forms of kv_weigh have in common; `keys` say where the keys are, `dims` is what follows T."""
+    index, dtype, dt, (B, Hq, T, D) = _queries(q)
+    qp, lp = _at(q, "q", dtype, index, B, Hq, T, D), _at(lse, "lse", torch.float32, index, B, Hq, T)
+    pp = _at(prefix_len, "prefix_len", _i32, index, B)
+    ap = _at(acc, "acc", torch.float32, index, B, Hkv, cap)
+    op = None if pos is None else _at(pos, "pos", _i32, index, B, Hkv, cap)
+    sp = None if seen is None else _at(seen, "seen", _i32, index, B)
+    rp = None if n_rows is None else _at(n_rows, "n_rows", _i32, index, B)
+    al = None if accept_len is None else _at(accept_len, "accept_len", _i32, index, B)
+    path, P = None, 0
+    if accept_path is not None:
+        P = accept_path.shape[1] if isinstance(accept_path, _Tensor) and accept_path.dim() == 2 else 0
+        path = _at(accept_path, "accept_path", _i32, index, B, P)
+    if ws is None:
+        ws = _sized(kv_weigh_workspace_size, index, stream, B, Hq, Hkv, T, P, cap, D, dt)
+    _call(name, index, stream, qp, lp, *keys, pp, sp, rp, al, path, P, B, Hq, Hkv, T, *dims, D, 0.0 if scale is None else float(scale),
+          float(decay), dt, ap, op, _buffer(ws, index), ws.nbytes)
+    return ws
+
+
+def kv_weigh(q, lse, k_cache, prefix_len, acc, pos=None, seen=None, n_rows=None, accept_len=None, accept_path=None, decay=1.0,
+             scale=None, ws=None, stream=None):
+    """Add the attention weight that cached keys receive from the sequences' last rows to acc [B, Hkv, Lmax]: returns ws.
+
+    q [B, Hq, T, D] and lse [B, Hq, T] of an attention; prefix_len [B] with the rows' own keys in it; the rows are
+    the first n_rows[b] (None: T), or the nodes of accept_path (tree_accept).  pos [B, Hkv, Lmax] int32: see kv_evict."""
+    index, dtype, _, (B, _, _, D) = _queries(q)
+    _, Hkv, Lmax, _ = _queries(k_cache, "k_cache")[3]
+    return _weigh("kv_weigh", q, lse, (_at(k_cache, "k_cache", dtype, index, B, Hkv, Lmax, D),), prefix_len, acc, pos, seen, n_rows,
+                  accept_len, accept_path, decay, scale, ws, stream, Hkv, Lmax, (Lmax,))
+
+
+def kv_weigh_paged(q, lse, k_pool, block_table, prefix_len, acc, pos=None, seen=None, n_rows=None, accept_len=None,
+                   accept_path=None, decay=1.0, scale=None, ws=None, stream=None):
+    """kv_weigh over a paged cache: pool [num_blocks, Hkv, block_size, D], acc and pos [B, Hkv, max_blocks * block_size]."""
+    index, dtype, _, (B, _, _, D) = _queries(q)
+    blocks, Hkv, bs, _ = _pool(k_pool)
+    most = block_table.shape[1] if isinstance(block_table, _Tensor) and block_table.dim() == 2 else 0
+    keys = (_at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), blocks, _at(block_table, "block_table", _i32, index, B, most), most, bs)
+    return _weigh("kv_weigh_paged", q, lse, keys, prefix_len, acc, pos, seen, n_rows, accept_len, accept_path, decay, scale, ws, stream,
+                  Hkv, most * bs, ())
+
+
+def kv_evict_workspace_size(B, Hkv, Lmax, budget):
+    n = _lib.kv_evict_workspace_size(B, Hkv, Lmax, budget)
+    if n == 0:
+        raise SpecError("kv_evict_workspace_size", 1, _lib.spec_last_error().decode())
+    return int(n)
+
+
+def _ledger(acc, pos, index, names, *shape):
+    return _at(acc, names[0], torch.float32, index, *shape), _at(pos, names[1], _i32, index, *shape)
+
+
+def kv_evict(k_cache, v_cache, prefix_len, acc, pos, budget, seen=None, sink=0, recent=0, k_out=None, v_out=None, acc_out=None,
+             pos_out=None, len_out=None, ws=None, stream=None):
+    """Keep `budget` keys of every sequence and KV head, those of protected positions and of the largest acc: returns
+    len_out [B].  In place, or into the caches [B, Hkv, Lout, D] k_out, v_out with acc_out and pos_out [B, Hkv, Lout]."""
+    index, dtype, dt, (B, Hkv, Lmax, D) = _queries(k_cache, "k_cache")
+    kp, vp = _at(k_cache, "k_cache", dtype, index, B, Hkv, Lmax, D), _at(v_cache, "v_cache", dtype, index, B, Hkv, Lmax, D)
+    ap, op = _ledger(acc, pos, index, ("acc", "pos"), B, Hkv, Lmax)
+    out, Lout = (None, None, None, None), 0
+    if k_out is not None or v_out is not None or acc_out is not None or pos_out is not None:
+        Lout = _queries(k_out, "k_out")[3][2]
+        out = (_at(k_out, "k_out", dtype, index, B, Hkv, Lout, D), _at(v_out, "v_out", dtype, index, B, Hkv, Lout, D),
+               *_ledger(acc_out, pos_out, index, ("acc_out", "pos_out"), B, Hkv, Lout))
+    budget, sink, recent = _whole(budget, "budget"), _whole(sink, "sink"), _whole(recent, "recent")
+    pp = _at(prefix_len, "prefix_len", _i32, index, B)
+    sp = None if seen is None else _at(seen, "seen", _i32, index, B)
+    len_out = _new(stream, index, _i32, B) if len_out is None else len_out
+    if ws is None:
+        ws = _sized(kv_evict_workspace_size, index, stream, B, Hkv, Lmax, budget)
+    _call("kv_evict", index, stream, kp, vp, pp, sp, ap, op, B, Hkv, Lmax, D, budget, sink, recent, *out, Lout,
+          _at(len_out, "len_out", _i32, index, B), dt, _buffer(ws, index), ws.nbytes)
+    return len_out
+
+
+def kv_evict_paged(k_pool, v_pool, block_table, prefix_len, acc, pos, budget, seen=None, sink=0, recent=0, out_table=None,
+                   acc_out=None, pos_out=None, len_out=None, ws=None, stream=None):
+    """kv_evict in a paged cache: pools [num_blocks, Hkv, block_size, D], block_table [B, max_blocks] int32; in place, or
+    into the blocks of out_table [B, out_blocks]."""
+    index, dtype, dt, (blocks, Hkv, bs, D) = _queries(k_pool, "k_pool")
+    B, most = block_table.shape if isinstance(block_table, _Tensor) and block_table.dim() == 2 else (0, 0)
+    kp, vp = _at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), _at(v_pool, "v_pool", dtype, index, blocks, Hkv, bs, D)
+    tp = _at(block_table, "block_table", _i32, index, B, most)
+    ap, op = _ledger(acc, pos, index, ("acc", "pos"), B, Hkv, most * bs)
+    out, n = (None, 0, None, None), 0
+    if out_table is not None or acc_out is not None or pos_out is not None:
+        n = out_table.shape[1] if isinstance(out_table, _Tensor) and out_table.dim() == 2 else 0
+        out = (_at(out_table, "out_table", _i32, index, B, n), n, *_ledger(acc_out, pos_out, index, ("acc_out", "pos_out"), B, Hkv, n * bs))
+    budget, sink, recent = _whole(budget, "budget"), _whole(sink, "sink"), _whole(recent, "recent")
+    pp = _at(prefix_len, "prefix_len", _i32, index, B)
+    sp = None if seen is None else _at(seen, "seen", _i32, index, B)
+    len_out = _new(stream, index, _i32, B) if len_out is None else len_out
+    if ws is None:
+        ws = _sized(kv_evict_workspace_size, index, stream, B, Hkv, most * bs, budget)
+    _call("kv_evict_paged", index, stream, kp, vp, blocks, tp, most, bs, pp, sp, ap, op, B, Hkv, D, budget, sink, recent, *out,
+          _at(len_out, "len_out", _i32, index, B), dt, _buffer(ws, index), ws.nbytes)
+    return len_out
 
 
 def spec_philox_uniform(seed, offset, B, T, device=None, stream=None):

@@ -1,0 +1,225 @@
+// Reordering of beams in place: beam w of a sequence takes over what its parent holds.
+//
+//   beam_reorder                 any state of a beam, one row of bytes
+//   kv_reorder, kv_reorder_paged the cached keys and values of positions start[b] .. end[b] - 1
+//
+// A thread owns one column of 4 to 16 bytes (of a state, or of one position of one head) of all W
+// beams: it reads the parents' values into registers and then writes them, so that
+// permutations, cycles and parents with several children need neither order nor a second
+// buffer.  Beams that keep their own rows are neither read nor written.  Bound by memory: each
+// beam that changes is written once, each parent read once (children of one parent read it
+// from L1).  W columns have to fit the registers: 16 bytes each up to 16 beams, 8 up to 32,
+// 4 up to 64.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace spec {
+namespace reorder {
+
+constexpr int kThreads = 256;
+
+struct Params {
+    char *x, *y;                      // y NULL: one tensor
+    const int32_t* parent;            // [B, W]
+    const int32_t *start, *end;       // [B]; NULL: one position (states)
+    const int32_t* table;             // [B * W, max_blocks] or NULL
+    int B, W, heads, max_blocks, num_blocks;
+    int rows;                         // positions of one (block, head)
+    int64_t cap;                      // positions of one sequence
+    int64_t row_bytes;
+    void* ws;
+};
+
+__device__ __forceinline__ bool range_of(const Params& p, int b, int& from, int& to) {
+    from = 0;
+    to = 1;
+    if (p.start) {
+        from = p.start[b];
+        to = p.end[b];
+        if (from < 0 || to < from || to > p.cap) {
+            to = from;
+            return false;
+        }
+    }
+    return true;
+}
+
+// The call's status: one CTA looks at every parent, range and table entry and stores the word.
+__device__ void check_all(const Params& p) {
+    int bad = 0;
+    const int rows = p.B * p.W;       // below 2^22
+    for (int i = threadIdx.x; i < rows; i += kThreads) {
+        const int w = p.parent[i];
+        if (w < -1 || w >= p.W) bad = 1;
+    }
+    if (p.start)
+        for (int b = threadIdx.x; b < p.B; b += kThreads) {
+            int from, to;
+            if (!range_of(p, b, from, to)) bad = 1;
+        }
+    if (p.table) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        for (int i = warp; i < rows; i += kThreads / 32) {
+            int from, to;
+            range_of(p, i / p.W, from, to);
+            if (to > from)
+                for (int j = from / p.rows + lane; j <= (to - 1) / p.rows; j += 32) {
+                    const int blk = p.table[static_cast<size_t>(i) * p.max_blocks + j];
+                    if (blk < 0 || blk >= p.num_blocks) bad = 1;
+                }
+        }
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *static_cast<int4*>(p.ws) = make_int4(bad ? SPEC_EINVAL : SPEC_OK, 0, 0, 0);
+}
+
+template <typename V, int MOST>
+__global__ void __launch_bounds__(kThreads) k_reorder(const Params p) {
+    if (blockIdx.x == 0) {            // one CTA more than there are for the rows
+        if (blockIdx.y == 0) check_all(p);
+        return;
+    }
+    __shared__ int s_parent[MOST];
+    __shared__ unsigned s_moved[2];
+    const int b = blockIdx.y;
+    int from, to;
+    range_of(p, b, from, to);
+    if (threadIdx.x < 64) {
+        const int w = threadIdx.x;
+        const int q = w < p.W ? p.parent[static_cast<size_t>(b) * p.W + w] : -1;
+        const bool moved = q >= 0 && q < p.W && q != w;
+        if (w < MOST) s_parent[w] = moved ? q : w;
+        const unsigned m = __ballot_sync(0xffffffffu, moved);
+        if ((w & 31) == 0) s_moved[w >> 5] = m;
+    }
+    __syncthreads();
+    const unsigned long long moved = s_moved[0] | (static_cast<unsigned long long>(s_moved[1]) << 32);
+    if (!moved) return;
+    const int64_t cols = p.row_bytes / static_cast<int64_t>(sizeof(V));
+    const int64_t per_head = static_cast<int64_t>(to - from) * cols;
+    const int64_t one = per_head * p.heads, total = p.y ? 2 * one : one;
+    const int64_t step = static_cast<int64_t>(gridDim.x - 1) * kThreads;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x - 1) * kThreads + threadIdx.x; u < total; u += step) {
+        char* base = u < one ? p.x : p.y;
+        const int64_t r = u < one ? u : u - one;
+        const int64_t h = r / per_head, in = r - h * per_head;
+        const int64_t q = in / cols, c = in - q * cols;
+        const int at = from + static_cast<int>(q);
+        const int page = at / p.rows, line = at - page * p.rows;
+        auto place = [&](int w) -> V* {
+            int64_t blk = static_cast<int64_t>(b) * p.W + w;
+            if (p.table) {
+                blk = p.table[blk * p.max_blocks + page];
+                if (blk < 0 || blk >= p.num_blocks) return nullptr;
+            }
+            return reinterpret_cast<V*>(base + ((blk * p.heads + h) * p.rows + line) * p.row_bytes) + c;
+        };
+        V v[MOST];
+        unsigned long long read = 0;
+#pragma unroll
+        for (int w = 0; w < MOST; ++w)
+            if ((moved >> w) & 1)
+                if (const V* src = place(s_parent[w])) {
+                    v[w] = *src;
+                    read |= 1ull << w;
+                }
+#pragma unroll
+        for (int w = 0; w < MOST; ++w)
+            if ((read >> w) & 1)
+                if (V* dst = place(w)) *dst = v[w];
+    }
+}
+
+spec_status run(const char* name, const Params& p, int64_t positions, cudaStream_t s) {
+    const int64_t rb = p.row_bytes;
+    const int width = rb % 16 == 0 && p.W <= 16 ? 16 : rb % 8 == 0 && p.W <= 32 ? 8 : 4;
+    void (*kern)(const Params) = width == 16 ? (p.W <= 4 ? k_reorder<uint4, 4> : p.W <= 8 ? k_reorder<uint4, 8> : k_reorder<uint4, 16>)
+                                 : width == 8 ? k_reorder<uint2, 32> : k_reorder<uint32_t, 64>;
+    // enough CTAs for eight on every SM, each with work for its threads if every sequence is full
+    const int64_t units = positions * p.heads * (rb / width) * (p.y ? 2 : 1);
+    const int64_t most = std::max<int64_t>(1, (units + kThreads - 1) / kThreads);
+    const int64_t want = (8 * device_sm_count() + p.B - 1) / p.B;
+    const unsigned per = static_cast<unsigned>(std::min(most, want));
+    SPEC_CUDA_TRY(launch(name, kern, dim3(per + 1, p.B), dim3(kThreads), 0, s, p));
+    return SPEC_OK;
+}
+
+spec_status check_common(const Params& p, size_t ws_bytes) {
+    if (p.B < 1 || p.B > 65535) return fail(SPEC_EINVAL, "B = %d out of 1..65535", p.B);
+    if (p.W < 1 || p.W > SPEC_MAX_BEAMS) return fail(SPEC_EINVAL, "W = %d out of 1..%d", p.W, SPEC_MAX_BEAMS);
+    if (!p.parent) return fail(SPEC_EINVAL, "parent must not be NULL");
+    if (!aligned4(p.parent)) return fail(SPEC_EALIGN, "parent must be 4-byte aligned");
+    if (!p.ws || ws_bytes < kWsHeader) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, kWsHeader);
+    if (!aligned16(p.ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
+    return SPEC_OK;
+}
+
+spec_status kv(const char* name, Params& p, const void* k, const void* v, int Hkv, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s) {
+    spec_status st = check_common(p, ws_bytes);
+    if (st != SPEC_OK) return st;
+    if (dt != SPEC_BF16 && dt != SPEC_F32) return fail(SPEC_EINVAL, "dtype %d unknown", static_cast<int>(dt));
+    const int es = dt == SPEC_BF16 ? 2 : 4;
+    if (Hkv < 1 || Hkv > 1024) return fail(SPEC_EINVAL, "Hkv = %d out of 1..1024", Hkv);
+    if (D < 1 || D > 1024 || (D * es) % 16) return fail(SPEC_EINVAL, "D = %d: 1..1024 and a multiple of 16 bytes", D);
+    if (!k || !v || !p.start || !p.end) return fail(SPEC_EINVAL, "the cache, start and end must not be NULL");
+    if (k == v) return fail(SPEC_EINVAL, "keys and values are the same buffer");
+    if (!aligned16(k) || !aligned16(v)) return fail(SPEC_EALIGN, "the cache must be 16-byte aligned");
+    if (!aligned4(p.start) || !aligned4(p.end) || !aligned4(p.table))
+        return fail(SPEC_EALIGN, "start, end and the block table must be 4-byte aligned");
+    p.x = static_cast<char*>(const_cast<void*>(k));
+    p.y = static_cast<char*>(const_cast<void*>(v));
+    p.heads = Hkv;
+    p.row_bytes = static_cast<int64_t>(D) * es;
+    return run(name, p, p.cap, s);
+}
+
+}  // namespace reorder
+}  // namespace spec
+
+using namespace spec;
+
+extern "C" size_t beam_reorder_workspace_size(void) { return kWsHeader; }
+
+extern "C" spec_status beam_reorder(void* state, int64_t row_bytes, const int32_t* parent, int32_t B, int32_t W,
+                                    void* ws, size_t ws_bytes, spec_stream_t s) {
+    clear_error();
+    reorder::Params p{};
+    p.x = static_cast<char*>(state); p.parent = parent; p.B = B; p.W = W; p.ws = ws;
+    spec_status st = reorder::check_common(p, ws_bytes);
+    if (st != SPEC_OK) return st;
+    if (row_bytes < 4 || row_bytes % 4 || row_bytes > (1ll << 32)) return fail(SPEC_EINVAL, "row_bytes = %lld: a multiple of 4 in 4..2^32", static_cast<long long>(row_bytes));
+    if (!state) return fail(SPEC_EINVAL, "state must not be NULL");
+    if (!aligned16(state)) return fail(SPEC_EALIGN, "state must be 16-byte aligned");
+    p.heads = 1; p.rows = 1; p.cap = 1; p.row_bytes = row_bytes;
+    return reorder::run("beam_reorder", p, 1, reinterpret_cast<cudaStream_t>(s));
+}
+
+extern "C" spec_status kv_reorder(void* k_cache, void* v_cache, const int32_t* parent, const int32_t* start, const int32_t* end,
+                                  int32_t B, int32_t W, int32_t Hkv, int32_t Lmax, int32_t D, spec_dtype dt, void* ws,
+                                  size_t ws_bytes, spec_stream_t s) {
+    clear_error();
+    if (Lmax < 1 || Lmax > (1 << 22)) return fail(SPEC_EINVAL, "Lmax = %d out of 1..2^22", Lmax);
+    reorder::Params p{};
+    p.parent = parent; p.start = start; p.end = end; p.B = B; p.W = W; p.rows = Lmax; p.cap = Lmax; p.ws = ws;
+    return reorder::kv("kv_reorder", p, k_cache, v_cache, Hkv, D, dt, ws_bytes, reinterpret_cast<cudaStream_t>(s));
+}
+
+extern "C" spec_status kv_reorder_paged(void* k_pool, void* v_pool, int32_t num_blocks, const int32_t* block_table,
+                                        int32_t max_blocks, int32_t block_size, const int32_t* parent, const int32_t* start,
+                                        const int32_t* end, int32_t B, int32_t W, int32_t Hkv, int32_t D, spec_dtype dt,
+                                        void* ws, size_t ws_bytes, spec_stream_t s) {
+    clear_error();
+    if (num_blocks < 1 || max_blocks < 1 || block_size < 1)
+        return fail(SPEC_EINVAL, "num_blocks = %d, max_blocks = %d, block_size = %d must be positive", num_blocks,
+                    max_blocks, block_size);
+    if (static_cast<int64_t>(max_blocks) * block_size > (1 << 22))
+        return fail(SPEC_EINVAL, "max_blocks * block_size = %lld positions exceed 2^22",
+                    static_cast<long long>(max_blocks) * block_size);
+    if (!block_table) return fail(SPEC_EINVAL, "block_table must not be NULL");
+    reorder::Params p{};
+    p.parent = parent; p.start = start; p.end = end; p.B = B; p.W = W; p.ws = ws;
+    p.table = block_table; p.max_blocks = max_blocks; p.num_blocks = num_blocks; p.rows = block_size;
+    p.cap = static_cast<int64_t>(max_blocks) * block_size;
+    return reorder::kv("kv_reorder", p, k_pool, v_pool, Hkv, D, dt, ws_bytes, reinterpret_cast<cudaStream_t>(s));
+}

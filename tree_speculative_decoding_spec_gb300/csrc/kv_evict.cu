@@ -1,0 +1,416 @@
+// Eviction from the cache: every KV head of a sequence keeps `budget` keys.
+//
+// Kept are, in this order, the keys whose positions are protected (the first `sink` and the
+// last `recent` of the sequence), then those that received the most attention weight; of equal ones the
+// lower place in the cache.  The cache's order does not matter to attention over rotated keys,
+// so kept keys in front of the budget stay where they are and the places of evicted ones are
+// filled, in ascending order, by the kept keys behind it: a step that adds five keys to a full
+// cache moves five rows, where closing the gaps would move half of the cache.
+//
+//   evict_pick   a CTA per (sequence, head): radix selection of the budget-th largest of
+//                (protected, weight), then ordered lists of holes and of the keys that fill them;
+//                moves weights and positions
+//   evict_move   the rows of K and V, where the cache can hold many more rows than the budget (else
+//                evict_pick's CTA moves its few itself and the second launch is saved)
+// With another cache to go to, everything kept is copied there, place for place the same.
+// Bound by memory, 8 bytes a key to choose and 4 rows' bytes for each that moves; a step of a full
+// cache by the latency of the selection.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace spec {
+namespace evict {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kCached = 24576;        // keys of a head whose ranks stay in shared memory
+constexpr int kFew = 128;             // rows behind the budget that evict_pick moves itself
+
+struct Params {
+    const char *k, *v;
+    char *k_out, *v_out;              // the same, in place
+    const float* acc;
+    const int32_t* pos;
+    float* acc_out;
+    int32_t* pos_out;
+    const int32_t *table, *out_table; // paged; out_table == table in place
+    const int32_t *len, *seen;        // [B]; seen NULL: len
+    int32_t* len_out;
+    int B, Hkv, budget, sink, recent;
+    int max_blocks, out_blocks, num_blocks;
+    int rows, out_rows;               // positions of one (block, head)
+    int cap, out_cap;                 // positions of one sequence (the stride of acc and pos)
+    int row16;                        // 16-byte chunks of a row
+    int here;                         // evict_pick moves the rows
+    int in_place, cached;
+    int2* moves;                      // [B * Hkv][most]: (to, from)
+    int32_t* count;                   // [B * Hkv]
+    int most;
+    void* ws;
+};
+
+// Whether sequence b's length and table entries are sound, as far as thread t of N looks.
+template <int N> __device__ __forceinline__ bool sound(const Params& p, int b, int t) {
+    const int n = p.len[b];
+    int bad = n < 0 || n > p.cap;
+    if (!bad && p.table) {
+        const int used = (n + p.rows - 1) / p.rows;
+        for (int j = t; j < used; j += N) {
+            const int blk = p.table[static_cast<size_t>(b) * p.max_blocks + j];
+            if (blk < 0 || blk >= p.num_blocks) bad = 1;
+        }
+        if (!p.in_place) {
+            const int out = (min(n, p.budget) + p.rows - 1) / p.rows;
+            for (int j = t; j < out; j += N) {
+                const int blk = p.out_table[static_cast<size_t>(b) * p.out_blocks + j];
+                if (blk < 0 || blk >= p.num_blocks) bad = 1;
+            }
+        }
+    }
+    return !bad;
+}
+
+__device__ __forceinline__ int64_t row_at(const int32_t* table, int max_blocks, int rows, int Hkv, int b, int h, int at) {
+    int64_t blk = b;
+    if (table) {
+        blk = table[static_cast<size_t>(b) * max_blocks + at / rows];
+        at %= rows;
+    }
+    return (blk * Hkv + h) * rows + at;
+}
+
+__device__ __forceinline__ void move_chunk(const Params& p, int b, int h, int2 mv, int c, bool value) {
+    const int64_t src = row_at(p.table, p.max_blocks, p.rows, p.Hkv, b, h, mv.y) * p.row16 + c;
+    const int64_t dst = row_at(p.out_table, p.out_blocks, p.out_rows, p.Hkv, b, h, mv.x) * p.row16 + c;
+    const uint4* from = reinterpret_cast<const uint4*>(value ? p.v : p.k);
+    uint4* to = reinterpret_cast<uint4*>(value ? p.v_out : p.k_out);
+    to[dst] = from[src];
+}
+
+// Exclusive prefix sums of two counts over the CTA; totals in t0, t1.
+__device__ __forceinline__ void scan2(int (&part)[2][kWarps], int& a, int& b, int& t0, int& t1) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int x = a, y = b;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) { x += u; y += v; }
+    }
+    __syncthreads();                  // an earlier scan's readers are through
+    if (lane == 31) { part[0][warp] = x; part[1][warp] = y; }
+    __syncthreads();
+    int p0 = 0, p1 = 0;
+    t0 = t1 = 0;
+    for (int i = 0; i < kWarps; ++i) {
+        if (i == warp) { p0 = t0; p1 = t1; }
+        t0 += part[0][i];
+        t1 += part[1][i];
+    }
+    a = p0 + x - a;
+    b = p1 + y - b;
+}
+
+__global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
+    extern __shared__ unsigned s_rank[];              // ranks of the keys, where they fit
+    __shared__ int s_hist[256];
+    __shared__ int part[2][kWarps];
+    __shared__ int s_digit, s_above;
+    const int h = blockIdx.x, b = blockIdx.y;
+    griddep_launch();
+    if (h == p.Hkv) {                 // one CTA more: the status word, which no other writes
+        if (b != 0) return;
+        int bad = 0;
+        for (int i = threadIdx.x >> 5; i < p.B; i += kWarps) bad |= !sound<32>(p, i, threadIdx.x & 31);
+        bad = __syncthreads_or(bad);
+        if (threadIdx.x == 0) *static_cast<int4*>(p.ws) = make_int4(bad ? SPEC_EINVAL : SPEC_OK, 0, 0, 0);
+        return;
+    }
+    const int bh = b * p.Hkv + h;
+    const int n = p.len[b];
+    const bool ok = __syncthreads_and(sound<kThreads>(p, b, threadIdx.x));
+    if (h == 0 && threadIdx.x == 0) p.len_out[b] = ok ? min(n, p.budget) : n;
+    const bool all = n <= p.budget;   // nothing is evicted
+    if (!ok || (all && p.in_place)) {
+        if (threadIdx.x == 0) p.count[bh] = 0;
+        return;
+    }
+    const float* acc = p.acc + static_cast<size_t>(bh) * p.cap;
+    const int32_t* pos = p.pos + static_cast<size_t>(bh) * p.cap;
+    float* acc_out = p.acc_out + static_cast<size_t>(bh) * p.out_cap;
+    int32_t* pos_out = p.pos_out + static_cast<size_t>(bh) * p.out_cap;
+    int2* moves = p.moves + static_cast<size_t>(bh) * p.most;
+    int count = 0;
+    if (!all) {
+        const int64_t since = static_cast<int64_t>(p.seen ? p.seen[b] : n) - p.recent;
+        const bool cached = n <= p.cached;
+        auto is_safe = [&](int i) {
+            const int at = pos[i];
+            return at < p.sink || at >= since;
+        };
+        // number of protected keys
+        int mine = 0;
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            mine += is_safe(i);
+            if (cached) s_rank[i] = order_key(acc[i]);
+        }
+        int zero = 0, safe, none;
+        scan2(part, mine, zero, safe, none);
+        // all protected ones are kept and the best of the others, or the best of the protected ones
+        const bool among_safe = safe > p.budget;
+        int want = among_safe ? p.budget : p.budget - safe;
+        // the want-th largest rank of those in play, eight bits at a time
+        unsigned prefix = 0, mask = 0;
+        if (want > 0) {
+            for (int shift = 24; shift >= 0; shift -= 8) {
+                if (threadIdx.x < 256) s_hist[threadIdx.x] = 0;
+                __syncthreads();
+                for (int i = threadIdx.x; i < n; i += kThreads) {
+                    const unsigned r = cached ? s_rank[i] : order_key(acc[i]);
+                    if ((r & mask) == prefix && is_safe(i) == among_safe) atomicAdd(&s_hist[(r >> shift) & 255], 1);
+                }
+                __syncthreads();
+                if (threadIdx.x < 32) {
+                    // lane l has digits 255 - 8 l and the seven below
+                    int c[8], sum = 0;
+                    for (int j = 0; j < 8; ++j) sum += c[j] = s_hist[255 - 8 * threadIdx.x - j];
+                    int above = sum;
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int u = __shfl_up_sync(0xffffffffu, above, o);
+                        if (static_cast<int>(threadIdx.x) >= o) above += u;
+                    }
+                    above -= sum;
+                    for (int j = 0; j < 8; ++j) {
+                        if (above < want && above + c[j] >= want) {
+                            s_digit = 255 - 8 * threadIdx.x - j;
+                            s_above = above;
+                        }
+                        above += c[j];
+                    }
+                }
+                __syncthreads();
+                prefix |= static_cast<unsigned>(s_digit) << shift;
+                mask |= 255u << shift;
+                want -= s_above;      // now: how many of those equal so far are wanted
+            }
+        }
+        // a run of places per thread, of odd length so that their ranks lie in different banks
+        const int run = (n + kThreads - 1) / kThreads | 1;
+        const int i0 = min(n, static_cast<int>(threadIdx.x) * run), i1 = min(n, i0 + run);
+        // 2: kept, 1: kept if among the first `want` of its equals
+        auto grade = [&](int i) {
+            const unsigned r = cached ? s_rank[i] : order_key(acc[i]);
+            const bool safe_one = is_safe(i);
+            if (safe_one != among_safe) return safe_one ? 2 : 0;
+            if (mask == 0) return 0;  // nothing wanted of these
+            return r > prefix ? 2 : r == prefix ? 1 : 0;
+        };
+        int equal = 0, skip = 0, t0, t1;
+        for (int i = i0; i < i1; ++i) equal += grade(i) == 1;
+        scan2(part, equal, skip, t0, t1);
+        int holes = 0, late = 0, e = equal;
+        for (int i = i0; i < i1; ++i) {
+            const int g = grade(i);
+            const bool kept = g == 2 || (g == 1 && e++ < want);
+            if (i < p.budget) holes += !kept; else late += kept;
+        }
+        scan2(part, holes, late, t0, t1);
+        count = t0;                   // as many keys come from behind the budget as there are holes in front
+        e = equal;
+        for (int i = i0; i < i1; ++i) {
+            const int g = grade(i);
+            const bool kept = g == 2 || (g == 1 && e++ < want);
+            if (i < p.budget) {
+                if (!kept) moves[holes++].x = i;
+            } else if (kept) {
+                moves[late++].y = i;
+            }
+        }
+        __syncthreads();
+    }
+    if (!p.in_place) {                // what stays at its place goes to the same place of the other cache
+        const int m = min(n, p.budget);
+        for (int i = threadIdx.x; i < m; i += kThreads) {
+            acc_out[i] = acc[i];
+            pos_out[i] = pos[i];
+        }
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < count; i += kThreads) {
+        const int2 mv = moves[i];
+        acc_out[mv.x] = acc[mv.y];
+        pos_out[mv.x] = pos[mv.y];
+    }
+    if (threadIdx.x == 0) p.count[bh] = count;
+    if (p.here) {
+        const int units = count * p.row16 * 2;
+        for (int u = threadIdx.x; u < units; u += kThreads) {
+            const int c = u % p.row16, r = u / p.row16;
+            move_chunk(p, b, h, moves[r >> 1], c, r & 1);
+        }
+    }
+}
+
+constexpr int kMoveThreads = 256;
+
+// Rows of K and V.  In place: the moves.  To another cache: place i from place i, or from behind the
+// budget where a move fills it; the moves are in ascending order, so a place finds its own by bisection.
+__global__ void __launch_bounds__(kMoveThreads) k_move(const Params p) {
+    const int h = blockIdx.y % p.Hkv, b = blockIdx.y / p.Hkv, bh = blockIdx.y;
+    griddep_wait();
+    const int count = p.count[bh];
+    const int2* moves = p.moves + static_cast<size_t>(bh) * p.most;
+    int places = count;
+    if (!p.in_place) {
+        if (!__syncthreads_and(sound<kMoveThreads>(p, b, threadIdx.x))) return;
+        places = min(p.len[b], p.budget);
+    }
+    const int64_t units = static_cast<int64_t>(places) * p.row16 * 2;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x; u < units; u += static_cast<int64_t>(gridDim.x) * kMoveThreads) {
+        const int c = static_cast<int>(u % p.row16);
+        const int r = static_cast<int>(u / p.row16);
+        int2 mv;
+        if (p.in_place) {
+            mv = moves[r >> 1];
+        } else {
+            mv = make_int2(r >> 1, r >> 1);
+            int lo = 0, hi = count;
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                if (moves[mid].x < mv.x) lo = mid + 1; else hi = mid;
+            }
+            if (lo < count && moves[lo].x == mv.x) mv.y = moves[lo].y;
+        }
+        move_chunk(p, b, h, mv, c, r & 1);
+    }
+}
+
+size_t bytes_for(int B, int Hkv, int most) {
+    const size_t heads = static_cast<size_t>(B) * Hkv;
+    return kWsHeader + round_up(heads * 4, 256) + round_up(heads * static_cast<size_t>(most) * sizeof(int2), 256);
+}
+int most_moves(int cap, int budget) { return std::max(1, std::min(budget, cap - std::min(budget, cap))); }
+
+spec_status check_sizes(int B, int Hkv, int64_t cap, int budget) {
+    if (B < 1 || B > 65535) return fail(SPEC_EINVAL, "B = %d out of 1..65535", B);
+    if (Hkv < 1 || Hkv > 1024 || static_cast<int64_t>(B) * Hkv > 65535) return fail(SPEC_EINVAL, "Hkv = %d out of 1..1024, or B * Hkv above 65535", Hkv);
+    if (cap < 1 || cap > (1 << 22)) return fail(SPEC_EINVAL, "%lld positions out of 1..2^22", static_cast<long long>(cap));
+    if (budget < 1 || budget > (1 << 22)) return fail(SPEC_EINVAL, "budget = %d out of 1..2^22", budget);
+    return SPEC_OK;
+}
+
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
+}
+
+spec_status run(Params& p, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s) {
+    spec_status st = check_sizes(p.B, p.Hkv, p.cap, p.budget);
+    if (st != SPEC_OK) return st;
+    if (dt != SPEC_BF16 && dt != SPEC_F32) return fail(SPEC_EINVAL, "dtype %d unknown", static_cast<int>(dt));
+    const int es = dt == SPEC_BF16 ? 2 : 4;
+    if (D < 1 || D > 1024 || (D * es) % 16) return fail(SPEC_EINVAL, "D = %d: 1..1024 and a multiple of 16 bytes", D);
+    if (p.sink < 0 || p.recent < 0 || static_cast<int64_t>(p.sink) + p.recent > p.budget)
+        return fail(SPEC_EINVAL, "sink = %d, recent = %d: not negative, together at most the budget of %d", p.sink, p.recent, p.budget);
+    if (!p.k || !p.v || !p.acc || !p.pos || !p.len || !p.len_out) return fail(SPEC_EINVAL, "the cache, acc, pos, prefix_len and len_out must not be NULL");
+    if (!aligned16(p.k) || !aligned16(p.v) || !aligned16(p.k_out) || !aligned16(p.v_out)) return fail(SPEC_EALIGN, "the caches must be 16-byte aligned");
+    const void* small[] = {p.acc, p.pos, p.acc_out, p.pos_out, p.table, p.out_table, p.len, p.seen, p.len_out};
+    for (const void* x : small)
+        if (!aligned4(x)) return fail(SPEC_EALIGN, "acc, pos, lengths and block tables must be 4-byte aligned");
+    if (overlap(p.len_out, 4ll * p.B, p.len, 4ll * p.B) || (p.seen && overlap(p.len_out, 4ll * p.B, p.seen, 4ll * p.B)))
+        return fail(SPEC_EINVAL, "len_out overlaps prefix_len or seen, which every head reads");
+    const int64_t heads = static_cast<int64_t>(p.B) * p.Hkv;
+    if (!p.in_place) {
+        if (p.out_cap < std::min(p.budget, p.cap)) return fail(SPEC_EINVAL, "the other cache holds %d positions, fewer than are kept", p.out_cap);
+        const int64_t a = heads * p.cap * 4, o = heads * p.out_cap * 4;
+        const void* outs[] = {p.acc_out, p.pos_out};
+        const void* ins[] = {p.acc, p.pos};
+        for (const void* x : outs)
+            for (const void* y : ins)
+                if (overlap(x, o, y, a)) return fail(SPEC_EINVAL, "acc_out or pos_out overlaps acc or pos");
+        if (overlap(p.acc_out, o, p.pos_out, o)) return fail(SPEC_EINVAL, "acc_out overlaps pos_out");
+        if (!p.table) {
+            const int64_t ib = heads * p.cap * D * es, ob = heads * p.out_cap * D * es;
+            if (overlap(p.k_out, ob, p.k, ib) || overlap(p.k_out, ob, p.v, ib) || overlap(p.v_out, ob, p.k, ib) ||
+                overlap(p.v_out, ob, p.v, ib) || overlap(p.k_out, ob, p.v_out, ob))
+                return fail(SPEC_EINVAL, "the caches overlap");
+        }
+    }
+    p.row16 = D * es / 16;
+    p.most = most_moves(p.cap, p.budget);
+    const size_t need = bytes_for(p.B, p.Hkv, p.most);
+    if (!p.ws || ws_bytes < need) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    if (!aligned16(p.ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
+    p.count = reinterpret_cast<int32_t*>(static_cast<char*>(p.ws) + kWsHeader);
+    p.moves = reinterpret_cast<int2*>(static_cast<char*>(p.ws) + kWsHeader + round_up(static_cast<size_t>(heads) * 4, 256));
+    p.here = p.in_place && p.most <= kFew;
+    p.cached = std::min(p.cap, kCached);
+    const size_t smem = static_cast<size_t>(p.cached) * 4;
+    if (smem > 40960) SPEC_CUDA_TRY(cudaFuncSetAttribute(k_pick, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4));
+    SPEC_CUDA_TRY(launch("evict_pick", k_pick, dim3(p.Hkv + 1, p.B), dim3(kThreads), smem, s, p));
+    if (!p.here) {
+        const int64_t places = p.in_place ? p.most : std::min(p.budget, p.cap);
+        const int64_t most = (places * p.row16 * 2 + kMoveThreads - 1) / kMoveThreads;
+        const int64_t want = (16 * device_sm_count() + heads - 1) / heads;
+        SPEC_CUDA_TRY(launch_ex("evict_move", k_move, dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min(most, want))), static_cast<unsigned>(heads)),
+                                dim3(kMoveThreads), 0, s, true, p));
+    }
+    return SPEC_OK;
+}
+
+}  // namespace evict
+}  // namespace spec
+
+using namespace spec;
+
+extern "C" size_t kv_evict_workspace_size(int32_t B, int32_t Hkv, int32_t Lmax, int32_t budget) {
+    clear_error();
+    if (evict::check_sizes(B, Hkv, Lmax, budget) != SPEC_OK) return 0;
+    return evict::bytes_for(B, Hkv, evict::most_moves(Lmax, budget));
+}
+
+extern "C" spec_status kv_evict(void* k_cache, void* v_cache, const int32_t* prefix_len, const int32_t* seen, float* acc,
+                                int32_t* pos, int32_t B, int32_t Hkv, int32_t Lmax, int32_t D, int32_t budget, int32_t sink,
+                                int32_t recent, void* k_out, void* v_out, float* acc_out, int32_t* pos_out, int32_t Lout,
+                                int32_t* len_out, spec_dtype dt, void* ws, size_t ws_bytes, spec_stream_t s) {
+    clear_error();
+    evict::Params p{};
+    p.in_place = !k_out && !v_out && !acc_out && !pos_out;
+    if (!p.in_place && (!k_out || !v_out || !acc_out || !pos_out)) return fail(SPEC_EINVAL, "k_out, v_out, acc_out and pos_out go together");
+    if (!p.in_place && (Lout < 1 || Lout > (1 << 22))) return fail(SPEC_EINVAL, "Lout = %d out of 1..2^22", Lout);
+    p.k = static_cast<char*>(k_cache); p.v = static_cast<char*>(v_cache); p.acc = acc; p.pos = pos;
+    p.k_out = static_cast<char*>(p.in_place ? k_cache : k_out); p.v_out = static_cast<char*>(p.in_place ? v_cache : v_out);
+    p.acc_out = p.in_place ? acc : acc_out; p.pos_out = p.in_place ? pos : pos_out;
+    p.len = prefix_len; p.seen = seen; p.len_out = len_out;
+    p.B = B; p.Hkv = Hkv; p.budget = budget; p.sink = sink; p.recent = recent;
+    p.rows = p.cap = Lmax; p.out_rows = p.out_cap = p.in_place ? Lmax : Lout; p.ws = ws;
+    return evict::run(p, D, dt, ws_bytes, reinterpret_cast<cudaStream_t>(s));
+}
+
+extern "C" spec_status kv_evict_paged(void* k_pool, void* v_pool, int32_t num_blocks, const int32_t* block_table,
+                                      int32_t max_blocks, int32_t block_size, const int32_t* prefix_len, const int32_t* seen,
+                                      float* acc, int32_t* pos, int32_t B, int32_t Hkv, int32_t D, int32_t budget, int32_t sink,
+                                      int32_t recent, const int32_t* out_table, int32_t out_blocks, float* acc_out,
+                                      int32_t* pos_out, int32_t* len_out, spec_dtype dt, void* ws, size_t ws_bytes,
+                                      spec_stream_t s) {
+    clear_error();
+    if (num_blocks < 1 || max_blocks < 1 || block_size < 1)
+        return fail(SPEC_EINVAL, "num_blocks = %d, max_blocks = %d, block_size = %d must be positive", num_blocks,
+                    max_blocks, block_size);
+    if (static_cast<int64_t>(max_blocks) * block_size > (1 << 22))
+        return fail(SPEC_EINVAL, "max_blocks * block_size = %lld positions exceed 2^22",
+                    static_cast<long long>(max_blocks) * block_size);
+    if (!block_table) return fail(SPEC_EINVAL, "block_table must not be NULL");
+    evict::Params p{};
+    p.in_place = !out_table && !acc_out && !pos_out;
+    if (!p.in_place && (!out_table || !acc_out || !pos_out)) return fail(SPEC_EINVAL, "out_table, acc_out and pos_out go together");
+    if (!p.in_place && (out_blocks < 1 || static_cast<int64_t>(out_blocks) * block_size > (1 << 22)))
+        return fail(SPEC_EINVAL, "out_blocks = %d: 1.. and at most 2^22 positions", out_blocks);
+    p.k = p.k_out = static_cast<char*>(k_pool); p.v = p.v_out = static_cast<char*>(v_pool); p.acc = acc; p.pos = pos;
+    p.acc_out = p.in_place ? acc : acc_out; p.pos_out = p.in_place ? pos : pos_out;
+    p.table = block_table; p.out_table = p.in_place ? block_table : out_table;
+    p.max_blocks = max_blocks; p.out_blocks = p.in_place ? max_blocks : out_blocks; p.num_blocks = num_blocks;
+    p.len = prefix_len; p.seen = seen; p.len_out = len_out;
+    p.B = B; p.Hkv = Hkv; p.budget = budget; p.sink = sink; p.recent = recent;
+    p.rows = p.out_rows = block_size; p.cap = max_blocks * block_size;
+    p.out_cap = p.in_place ? p.cap : out_blocks * block_size; p.ws = ws;
+    return evict::run(p, D, dt, ws_bytes, reinterpret_cast<cudaStream_t>(s));
+}

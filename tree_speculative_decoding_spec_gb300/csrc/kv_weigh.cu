@@ -1,0 +1,224 @@
+// The attention weight that cached keys receive.
+//
+//   acc[b, h, j] = decay * acc[b, h, j] + sum over rows r of h's query heads of exp(scale q_r . k_j - lse_r)
+//
+// for the keys that row r sees: with count rows, row i of a query head sees the keys up to
+// n - count + i, n the cache's length with the rows' own keys in it.  The rows are the last
+// ones of the sequence: generated tokens, the nodes of an accepted path, a prompt.
+// lse comes from the attention that the rows went through, so the probabilities are made again
+// from one product and one exponential each, and only keys are read.
+//
+// Here: the checks, the CUDA-core kernel (fp32) and the entry points.  bf16 goes to the
+// tensor cores (kv_weigh_tc.cu).
+#include <algorithm>
+
+#include "kv_weigh.cuh"
+
+namespace spec {
+namespace weigh {
+
+constexpr int kThreads = 256;
+constexpr int kKeys = 64;             // keys of a CTA
+constexpr int kGroups = 16;           // 16 groups of four keys by 16 groups of rows
+constexpr float kLog2e = 1.4426950408889634f;
+
+// One CTA per 64 keys of one (sequence, KV head), over all rows that see any of them, 16 RPT
+// at a time.  A thread has four keys and RPT rows; operands lie in shared memory by head dimension,
+// so that four keys come in one read.  CTA 0 of the first head writes the status.
+template <typename T, int D, int RPT>
+__global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p) {
+    constexpr int R = kGroups * RPT;
+    extern __shared__ __align__(16) float smem[];
+    float* ks = smem;                 // [D][kKeys]
+    float* qs = smem + D * kKeys;     // [D][R]
+    __shared__ float s_lse[R];
+    __shared__ int s_last[R];         // the last key that a row sees; -1: no row
+    const int h = blockIdx.y, b = blockIdx.z;
+    if (blockIdx.x == 0) {
+        if (h == 0 && b == 0) check_all<kThreads>(p);
+        return;
+    }
+    const Rows rows = rows_of(p, b);
+    const int k0 = (static_cast<int>(blockIdx.x) - 1) * kKeys;
+    if (!rows.ok || k0 >= rows.n) return;
+    const T* q = static_cast<const T*>(p.q);
+    const T* k = static_cast<const T*>(p.k);
+    // a thread loads 16 bytes of the keys' rows at a time: key tid % 64, parts tid / 64 and on
+    for (int u = threadIdx.x; u < kKeys * (D / 4); u += kThreads) {
+        const int key = u % kKeys, c = u / kKeys;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        const int64_t at = k0 + key < rows.n ? key_row(p, b, h, k0 + key) : -1;
+        if (at >= 0) load4(k + at * D + 4 * c, x);
+        for (int j = 0; j < 4; ++j) ks[(4 * c + j) * kKeys + key] = x[j];
+    }
+    const int kg = threadIdx.x % kGroups, rg = threadIdx.x / kGroups;
+    const int g = p.Hq / p.Hkv;
+    const int i0 = max(0, k0 - (rows.n - rows.count));   // the first row that sees a key of this tile
+    const int per = rows.count - i0, total = g * per;
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int r0 = 0; r0 < total; r0 += R) {
+        __syncthreads();
+        if (threadIdx.x < R) {
+            const int r = r0 + threadIdx.x;
+            s_last[threadIdx.x] = -1;
+            if (r < total) {
+                const int i = i0 + r % per;
+                const float l = p.lse[static_cast<int64_t>(b * p.Hq + h * g + r / per) * p.T + node_of(p, b, i)];
+                s_lse[threadIdx.x] = l;
+                if (isfinite(l)) s_last[threadIdx.x] = rows.n - rows.count + i;
+            }
+        }
+        for (int u = threadIdx.x; u < R * (D / 4); u += kThreads) {
+            const int row = u % R, c = u / R, r = r0 + row;
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+            if (r < total) load4(q + (static_cast<int64_t>(b * p.Hq + h * g + r / per) * p.T + node_of(p, b, i0 + r % per)) * D + 4 * c, x);
+            for (int j = 0; j < 4; ++j) qs[(4 * c + j) * R + row] = x[j];
+        }
+        __syncthreads();
+        float s[4][RPT] = {};
+#pragma unroll 8
+        for (int d = 0; d < D; ++d) {
+            const float4 kk = *reinterpret_cast<const float4*>(&ks[d * kKeys + 4 * kg]);
+            float qq[RPT];
+            if constexpr (RPT == 4) {
+                const float4 t = *reinterpret_cast<const float4*>(&qs[d * R + 4 * rg]);
+                qq[0] = t.x; qq[1] = t.y; qq[2] = t.z; qq[3] = t.w;
+            } else {
+                qq[0] = qs[d * R + rg];
+            }
+#pragma unroll
+            for (int j = 0; j < RPT; ++j) {
+                s[0][j] += kk.x * qq[j];
+                s[1][j] += kk.y * qq[j];
+                s[2][j] += kk.z * qq[j];
+                s[3][j] += kk.w * qq[j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) {
+            const int row = rg * RPT + j, last = s_last[row];
+            const float l = s_lse[row];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (k0 + 4 * kg + i <= last) w[i] += exp2f(fmaf(s[i][j], p.scale, -l) * kLog2e);
+        }
+    }
+    // the row groups' sums of each key
+    __syncthreads();
+    float* sums = smem;               // [kGroups][kKeys]
+    for (int i = 0; i < 4; ++i) sums[rg * kKeys + 4 * kg + i] = w[i];
+    __syncthreads();
+    if (threadIdx.x < kKeys) {
+        const int j = k0 + threadIdx.x;
+        if (j < rows.n && key_row(p, b, h, j) >= 0) {
+            float sum = 0.f;
+            for (int i = 0; i < kGroups; ++i) sum += sums[i * kKeys + threadIdx.x];
+            store(p, b, h, j, rows, sum);
+        }
+    }
+}
+
+template <typename T, int D>
+spec_status run_fma(const Params& p, cudaStream_t s) {
+    const int most = p.Hq / p.Hkv * (p.path ? p.P : p.T);
+    const bool wide = most > kGroups;
+    auto kern = wide ? k_weigh_fma<T, D, 4> : k_weigh_fma<T, D, 1>;
+    const size_t smem = sizeof(float) * D * (kKeys + kGroups * (wide ? 4 : 1));
+    if (smem > 40960) SPEC_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+    SPEC_CUDA_TRY(launch("kv_weigh_fma", kern, dim3((p.cap + kKeys - 1) / kKeys + 1, p.Hkv, p.B), dim3(kThreads), smem, s, p));
+    return SPEC_OK;
+}
+
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
+}
+
+spec_status check_sizes(int B, int Hq, int Hkv, int T, int path_len, int64_t cap, int D, spec_dtype dt) {
+    if (dt != SPEC_BF16 && dt != SPEC_F32) return fail(SPEC_EINVAL, "dtype %d unknown", static_cast<int>(dt));
+    if (D != 64 && D != 128) return fail(SPEC_EUNSUPPORTED, "D = %d: only 64 and 128", D);
+    if (B < 1 || B > 65535) return fail(SPEC_EINVAL, "B = %d out of 1..65535", B);
+    if (Hkv < 1 || Hq < 1 || Hq > 1024 || Hq % Hkv) return fail(SPEC_EINVAL, "Hq = %d (1..1024) must be a multiple of Hkv = %d", Hq, Hkv);
+    if (T < 1 || T > (1 << 22)) return fail(SPEC_EINVAL, "T = %d out of 1..2^22", T);
+    if (path_len < 0 || path_len > SPEC_MAX_DEPTH + 1) return fail(SPEC_EINVAL, "path_len = %d out of 0..%d", path_len, SPEC_MAX_DEPTH + 1);
+    if (cap < 1 || cap > (1 << 22)) return fail(SPEC_EINVAL, "%lld positions out of 1..2^22", static_cast<long long>(cap));
+    return SPEC_OK;
+}
+
+spec_status run(Params& p, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s) {
+    spec_status st = check_sizes(p.B, p.Hq, p.Hkv, p.T, p.path ? p.P : 0, p.cap, D, dt);
+    if (st != SPEC_OK) return st;
+    if ((p.accept_len != nullptr) != (p.path != nullptr)) return fail(SPEC_EINVAL, "accept_len and accept_path go together");
+    if (p.path && p.n_rows) return fail(SPEC_EINVAL, "n_rows with an accepted path");
+    if (p.path && p.P < 1) return fail(SPEC_EINVAL, "path_len = %d with an accepted path", p.P);
+    if (!(p.scale >= 0.f) || std::isinf(p.scale)) return fail(SPEC_EINVAL, "scale = %g: positive, or 0 for 1/sqrt(D)", p.scale);
+    if (!(p.decay >= 0.f) || !(p.decay <= 1.f)) return fail(SPEC_EINVAL, "decay = %g out of 0..1", p.decay);
+    if (!p.q || !p.lse || !p.k || !p.len || !p.acc) return fail(SPEC_EINVAL, "q, lse, the keys, prefix_len and acc must not be NULL");
+    if (!aligned16(p.q) || !aligned16(p.k)) return fail(SPEC_EALIGN, "q and the keys must be 16-byte aligned");
+    const void* small[] = {p.lse, p.len, p.seen, p.n_rows, p.accept_len, p.path, p.table, p.acc, p.pos};
+    for (const void* x : small)
+        if (!aligned4(x)) return fail(SPEC_EALIGN, "lse, lengths, paths, tables, acc and pos must be 4-byte aligned");
+    const int es = dt == SPEC_BF16 ? 2 : 4;
+    const int64_t out = static_cast<int64_t>(p.B) * p.Hkv * p.cap * 4;
+    const struct { const void* x; int64_t n; } in[] = {
+        {p.q, static_cast<int64_t>(p.B) * p.Hq * p.T * D * es}, {p.lse, static_cast<int64_t>(p.B) * p.Hq * p.T * 4},
+        {p.k, static_cast<int64_t>(p.table ? p.num_blocks : p.B) * p.Hkv * p.rows * D * es}, {p.len, p.B * 4ll}, {p.seen, p.B * 4ll},
+        {p.n_rows, p.B * 4ll}, {p.accept_len, p.B * 4ll}, {p.path, 4ll * p.B * p.P}, {p.table, 4ll * p.B * p.max_blocks}};
+    for (const auto& i : in)
+        if (overlap(p.acc, out, i.x, i.n) || overlap(p.pos, out, i.x, i.n)) return fail(SPEC_EINVAL, "acc or pos overlaps an input");
+    if (overlap(p.acc, out, p.pos, out)) return fail(SPEC_EINVAL, "acc overlaps pos");
+    if (!p.ws || ws_bytes < kWsHeader) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, kWsHeader);
+    if (!aligned16(p.ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
+    if (p.scale == 0.f) p.scale = 1.f / sqrtf(static_cast<float>(D));
+    if (dt == SPEC_BF16) return D == 64 ? run_fma<__nv_bfloat16, 64>(p, s) : run_fma<__nv_bfloat16, 128>(p, s);
+    return D == 64 ? run_fma<float, 64>(p, s) : run_fma<float, 128>(p, s);
+}
+
+}  // namespace weigh
+}  // namespace spec
+
+using namespace spec;
+
+extern "C" size_t kv_weigh_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t path_len, int32_t Lmax,
+                                          int32_t D, spec_dtype dt) {
+    clear_error();
+    if (weigh::check_sizes(B, Hq, Hkv, T, path_len, Lmax, D, dt) != SPEC_OK) return 0;
+    return kWsHeader;
+}
+
+extern "C" spec_status kv_weigh(const void* q, const float* lse, const void* k_cache, const int32_t* prefix_len,
+                                const int32_t* seen, const int32_t* n_rows, const int32_t* accept_len,
+                                const int32_t* accept_path, int32_t path_len, int32_t B, int32_t Hq, int32_t Hkv, int32_t T,
+                                int32_t Lmax, int32_t D, float scale, float decay, spec_dtype dt, float* acc, int32_t* pos,
+                                void* ws, size_t ws_bytes, spec_stream_t s) {
+    clear_error();
+    weigh::Params p{};
+    p.q = q; p.lse = lse; p.k = k_cache; p.len = prefix_len; p.seen = seen; p.n_rows = n_rows;
+    p.accept_len = accept_len; p.path = accept_path; p.P = path_len;
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.T = T; p.rows = Lmax; p.cap = Lmax;
+    p.scale = scale; p.decay = decay; p.acc = acc; p.pos = pos; p.ws = ws;
+    return weigh::run(p, D, dt, ws_bytes, reinterpret_cast<cudaStream_t>(s));
+}
+
+extern "C" spec_status kv_weigh_paged(const void* q, const float* lse, const void* k_pool, int32_t num_blocks,
+                                      const int32_t* block_table, int32_t max_blocks, int32_t block_size,
+                                      const int32_t* prefix_len, const int32_t* seen, const int32_t* n_rows,
+                                      const int32_t* accept_len, const int32_t* accept_path, int32_t path_len, int32_t B,
+                                      int32_t Hq, int32_t Hkv, int32_t T, int32_t D, float scale, float decay, spec_dtype dt,
+                                      float* acc, int32_t* pos, void* ws, size_t ws_bytes, spec_stream_t s) {
+    clear_error();
+    if (num_blocks < 1 || max_blocks < 1 || block_size < 16 || block_size % 16)
+        return fail(SPEC_EINVAL, "num_blocks = %d, max_blocks = %d must be positive, block_size = %d a multiple of 16", num_blocks,
+                    max_blocks, block_size);
+    if (static_cast<int64_t>(max_blocks) * block_size > (1 << 22))
+        return fail(SPEC_EINVAL, "max_blocks * block_size = %lld positions exceed 2^22",
+                    static_cast<long long>(max_blocks) * block_size);
+    if (!block_table) return fail(SPEC_EINVAL, "block_table must not be NULL");
+    weigh::Params p{};
+    p.q = q; p.lse = lse; p.k = k_pool; p.len = prefix_len; p.seen = seen; p.n_rows = n_rows;
+    p.accept_len = accept_len; p.path = accept_path; p.P = path_len;
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.T = T; p.rows = block_size; p.cap = max_blocks * block_size;
+    p.table = block_table; p.max_blocks = max_blocks; p.num_blocks = num_blocks;
+    p.scale = scale; p.decay = decay; p.acc = acc; p.pos = pos; p.ws = ws;
+    return weigh::run(p, D, dt, ws_bytes, reinterpret_cast<cudaStream_t>(s));
+}
