@@ -25,7 +25,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // One CTA per 64 keys of one (sequence, KV head), over all rows that see any of them, 16 RPT
 // at a time.  A thread has four keys and RPT rows; operands lie in shared memory by head dimension,
 // so that four keys come in one read.  CTA 0 of the first head writes the status.
-template <typename T, int D, int RPT>
+template <int D, int RPT>
 __global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p) {
     constexpr int R = kGroups * RPT;
     extern __shared__ __align__(16) float smem[];
@@ -41,8 +41,8 @@ __global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p) {
     const Rows rows = rows_of(p, b);
     const int k0 = (static_cast<int>(blockIdx.x) - 1) * kKeys;
     if (!rows.ok || k0 >= rows.n) return;
-    const T* q = static_cast<const T*>(p.q);
-    const T* k = static_cast<const T*>(p.k);
+    const float* q = static_cast<const float*>(p.q);
+    const float* k = static_cast<const float*>(p.k);
     // a thread loads 16 bytes of the keys' rows at a time: key tid % 64, parts tid / 64 and on
     for (int u = threadIdx.x; u < kKeys * (D / 4); u += kThreads) {
         const int key = u % kKeys, c = u / kKeys;
@@ -118,11 +118,11 @@ __global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p) {
     }
 }
 
-template <typename T, int D>
+template <int D>
 spec_status run_fma(const Params& p, cudaStream_t s) {
     const int most = p.Hq / p.Hkv * (p.path ? p.P : p.T);
     const bool wide = most > kGroups;
-    auto kern = wide ? k_weigh_fma<T, D, 4> : k_weigh_fma<T, D, 1>;
+    auto kern = wide ? k_weigh_fma<D, 4> : k_weigh_fma<D, 1>;
     const size_t smem = sizeof(float) * D * (kKeys + kGroups * (wide ? 4 : 1));
     if (smem > 40960) SPEC_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
     SPEC_CUDA_TRY(launch("kv_weigh_fma", kern, dim3((p.cap + kKeys - 1) / kKeys + 1, p.Hkv, p.B), dim3(kThreads), smem, s, p));
@@ -143,6 +143,10 @@ spec_status check_sizes(int B, int Hq, int Hkv, int T, int path_len, int64_t cap
     if (path_len < 0 || path_len > SPEC_MAX_DEPTH + 1) return fail(SPEC_EINVAL, "path_len = %d out of 0..%d", path_len, SPEC_MAX_DEPTH + 1);
     if (cap < 1 || cap > (1 << 22)) return fail(SPEC_EINVAL, "%lld positions out of 1..2^22", static_cast<long long>(cap));
     return SPEC_OK;
+}
+
+size_t bytes_for(int g, int T, int path_len, spec_dtype dt) {
+    return kWsHeader + (dt == SPEC_BF16 ? weigh_tc_bytes(g, T, path_len) : 0);
 }
 
 spec_status run(Params& p, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s) {
@@ -167,11 +171,12 @@ spec_status run(Params& p, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s
     for (const auto& i : in)
         if (overlap(p.acc, out, i.x, i.n) || overlap(p.pos, out, i.x, i.n)) return fail(SPEC_EINVAL, "acc or pos overlaps an input");
     if (overlap(p.acc, out, p.pos, out)) return fail(SPEC_EINVAL, "acc overlaps pos");
-    if (!p.ws || ws_bytes < kWsHeader) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, kWsHeader);
+    const size_t need = bytes_for(p.Hq / p.Hkv, p.T, p.path ? p.P : 0, dt);
+    if (!p.ws || ws_bytes < need) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     if (!aligned16(p.ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
     if (p.scale == 0.f) p.scale = 1.f / sqrtf(static_cast<float>(D));
-    if (dt == SPEC_BF16) return D == 64 ? run_fma<__nv_bfloat16, 64>(p, s) : run_fma<__nv_bfloat16, 128>(p, s);
-    return D == 64 ? run_fma<float, 64>(p, s) : run_fma<float, 128>(p, s);
+    if (dt == SPEC_BF16) return weigh_tc_run(p, D, static_cast<char*>(p.ws) + kWsHeader, s);
+    return D == 64 ? run_fma<64>(p, s) : run_fma<128>(p, s);
 }
 
 }  // namespace weigh
@@ -183,7 +188,7 @@ extern "C" size_t kv_weigh_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, in
                                           int32_t D, spec_dtype dt) {
     clear_error();
     if (weigh::check_sizes(B, Hq, Hkv, T, path_len, Lmax, D, dt) != SPEC_OK) return 0;
-    return kWsHeader;
+    return weigh::bytes_for(Hq / Hkv, T, path_len, dt);
 }
 
 extern "C" spec_status kv_weigh(const void* q, const float* lse, const void* k_cache, const int32_t* prefix_len,

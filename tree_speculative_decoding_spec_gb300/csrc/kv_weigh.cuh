@@ -68,6 +68,10 @@ __device__ __forceinline__ void store(const Params& p, int b, int h, int j, cons
     if (fresh && p.pos) p.pos[at] = (p.seen ? p.seen[b] : r.n) - r.n + j;
 }
 
+// bf16, kv_weigh_tc.cu: what it needs behind the workspace's header, and its launches.
+size_t weigh_tc_bytes(int g, int T, int path_len);
+spec_status weigh_tc_run(const Params& p, int D, void* scratch, cudaStream_t s);
+
 // The call's status: one CTA of N threads looks at every sequence and table entry and stores the word.
 template <int N> __device__ void check_all(const Params& p) {
     int bad = 0;

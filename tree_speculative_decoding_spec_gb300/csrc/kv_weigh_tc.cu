@@ -1,0 +1,677 @@
+// Tensor-core (tcgen05) kernel of kv_weigh: bf16, head dim 64 or 128.
+//
+// The product is taken as S^T: keys are the rows of the MMA (M = 128 keys of a tile, one TMEM lane
+// each), query rows its columns.  So a thread owns a key, and the sum over query rows that the
+// operator asks for runs along its own registers: no reduction between lanes, no atomics, one
+// result a thread.  lse is a value per column, read from shared memory by all lanes at once:
+//   w(key) = sum over columns c of 2^(S[key, c] scale log2 e - lse_c log2 e)
+//
+// Two ways through, chosen on the host:
+//   few   at most 256 query rows of a KV head (generated tokens, accepted paths, short chains; more in
+//         several passes): a head's rows stay in shared memory while its keys stream through a ring of
+//         128-key tiles.  Bound by the keys' bytes up to some 200 rows.
+//   many  prompts: a tile of keys stays while chunks of 128 query rows of one head stream through.
+//         Bound by the exponentials, one for each pair of row and key.
+// The work, (sequence, head, key tile, chunk) in that order, is one line of chunks, cut into as
+// many equal parts as there are CTAs; lengths are known on the device only, so every CTA works its part
+// out itself.  A tile that is cut leaves partial sums, which kv_weigh_join adds up in order.
+//
+// One persistent CTA an SM, twelve warps:
+//   warps 0-3, 4-7   two groups that take alternate chunks (few: tiles), one thread per key
+//   warp 8           TMA: key tiles, and the chunks of rows (many)
+//   warp 9           MMA, one thread
+//   warps 10, 11     gather a head's rows (few); lse of the rows (both)
+// Waits are bounded (2 s); on expiry SPEC_ETIMEOUT goes to the status word, every role leaves its
+// loops, and the CTA drains its own loads and MMAs before it frees TMEM.
+#include <algorithm>
+#include <cstring>
+
+#include "kv_weigh.cuh"
+#include "tc.cuh"
+
+namespace spec {
+namespace weigh {
+
+using namespace tc;
+
+constexpr int kTile = 128;            // keys of a tile
+constexpr int kChunk = 128;           // query rows of a chunk (many)
+constexpr int kMostRows = 256;        // query rows of a pass (few)
+constexpr int kTcThreads = 384;
+constexpr int kMaxStages = 8;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kL2e = 1.4426950408889634f;
+
+struct Maps {
+    CUtensorMap k, q;
+};
+
+// What a CTA leaves for the join: its first tile began before it (and whether it ends here), its last
+// one goes on after it.
+struct Record {
+    int head, head_ends, tail, b, h, t, pad0, pad1;
+};
+
+struct TcParams {
+    Params p;
+    int g, nq;                        // query heads per KV head; rows of a Q stage
+    int row0;                         // few: first of the head's rows that this pass takes
+    int k_stages, q_stages, buffers;  // buffers of scores in TMEM
+    int box;                          // keys of a load
+    Record* records;                  // [CTAs] (many)
+    float* parts;                     // [CTAs][2][kTile]
+};
+
+// Barriers and small arrays behind the operand stages.
+struct Small {
+    uint64_t k_full[kMaxStages], k_empty[kMaxStages];
+    uint64_t q_full[4], q_empty[4];
+    uint64_t s_full[4], s_empty[4];
+    uint64_t x_full[2], x_empty[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int abort_flag, bad;
+    int start[4];                     // the CTA's first tile: b, h, t, chunk of it
+    long long length;                 // its chunks
+    __align__(16) float nl2[4][kMostRows];   // -lse log2 e of a stage's rows, -inf: does not count
+    int last[4][kMostRows];           // few: the last key that a row sees
+    float cross[2][kTile];            // many: the second group's sums
+};
+
+// The line of chunks of one sequence and head: m(t) row chunks for tile t, times `mult` query heads.
+struct Head {
+    int tiles, C, o, mult;
+    __device__ __forceinline__ long long before(int t) const {   // chunks of the tiles in front of t
+        const long long k = max(0, t - 1 - o);
+        return (static_cast<long long>(C) * t - k * (k + 1) / 2) * mult;
+    }
+    __device__ __forceinline__ int first(int t) const { return max(0, t - o); }      // first row chunk that sees tile t
+    __device__ __forceinline__ int chunks(int t) const { return (C - first(t)) * mult; }
+};
+template <bool MANY> __device__ __forceinline__ Head head_of(const TcParams& tp, const Rows& r) {
+    Head h{0, 1, 1 << 30, 1};
+    if (!r.ok) return h;
+    h.tiles = (r.n + kTile - 1) / kTile;
+    if (r.count == 0 && tp.p.decay == 1.f) h.tiles = 0;          // nothing changes
+    if (MANY) {
+        if (r.count > 0) {
+            h.C = (r.count + kChunk - 1) / kChunk;
+            h.o = (r.n - r.count + kChunk - 1) / kChunk;
+            h.mult = tp.g;
+        }
+    } else if (tp.row0 > 0 && tp.g * r.count <= tp.row0) {
+        h.tiles = 0;                                             // no rows left for this pass
+    }
+    return h;
+}
+
+static __device__ __noinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait_hint(bar, parity, 20000u); ++i) {
+        if ((i & 15u) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (*abort_flag || now - t0 > 2000000000ull) return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    return mbar_try_wait(bar, parity) || wait_slowly(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool warp_wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, wait_for(bar, parity, abort_flag));
+}
+
+// The tiles of a CTA's part of the line, the same in every role.
+template <bool MANY> struct Walk {
+    const TcParams& tp;
+    int b, h, t, c, take;             // the tile, its first chunk here, and how many are here
+    long long left;
+    Rows rows;
+    Head head;
+    bool more;
+    __device__ __forceinline__ Walk(const TcParams& tp_, const Small& sm) : tp(tp_) {
+        b = sm.start[0]; h = sm.start[1]; t = sm.start[2]; c = sm.start[3];
+        left = sm.length;
+        more = left > 0;
+        if (more) {
+            rows = rows_of(tp.p, b);
+            head = head_of<MANY>(tp, rows);
+            set();
+        }
+    }
+    __device__ __forceinline__ void set() { take = static_cast<int>(min(static_cast<long long>(head.chunks(t) - c), left)); }
+    __device__ __forceinline__ bool whole() const { return take == head.chunks(t); }
+    // whether the next tile is of another head (or there is none)
+    __device__ __forceinline__ bool column_ends() const { return left == take || t + 1 == head.tiles; }
+    __device__ __forceinline__ void next() {
+        left -= take;
+        more = left > 0;
+        c = 0;
+        if (!more) return;
+        if (++t == head.tiles) {
+            t = 0;
+            if (++h == tp.p.Hkv) {
+                h = 0;
+                do {                  // there is another one with tiles: chunks are left
+                    if (++b == tp.p.B) {
+                        more = false;
+                        return;
+                    }
+                    rows = rows_of(tp.p, b);
+                    head = head_of<MANY>(tp, rows);
+                } while (head.tiles == 0);
+            }
+        }
+        set();
+    }
+};
+
+// Where this CTA's part begins and how long it is; one warp.
+template <bool MANY> __device__ void plan(const TcParams& tp, Small& sm) {
+    const int lane = threadIdx.x & 31;
+    long long total = 0;
+    auto weight = [&](int b) -> long long {
+        if (b >= tp.p.B) return 0;
+        const Head h = head_of<MANY>(tp, rows_of(tp.p, b));
+        return h.tiles ? h.before(h.tiles) * tp.p.Hkv : 0;
+    };
+    long long w0 = 0;                 // of the first 32 sequences, kept for the second look
+    for (int b0 = 0; b0 < tp.p.B; b0 += 32) {
+        long long w = weight(b0 + lane);
+        if (b0 == 0) w0 = w;
+        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+        total += w;
+    }
+    // as many CTAs have a part as there are chunks, the first ones: the join looks for a tile's parts side by side
+    const long long ctas = min(total, static_cast<long long>(gridDim.x));
+    long long from = 0, to = 0;
+    if (blockIdx.x < ctas) {
+        from = total * blockIdx.x / ctas;
+        to = total * (blockIdx.x + 1) / ctas;
+    }
+    if (lane == 0) sm.length = to - from;
+    if (to == from) return;
+    long long base = 0;
+    for (int b0 = 0; b0 < tp.p.B; b0 += 32) {
+        const long long w = b0 == 0 ? w0 : weight(b0 + lane);
+        long long upto = w;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += u;
+        }
+        const long long mine = base + upto - w;
+        const unsigned here = __ballot_sync(0xffffffffu, from >= mine && from < mine + w);
+        if (here) {
+            if (lane == __ffs(here) - 1) {
+                const Head hd = head_of<MANY>(tp, rows_of(tp.p, b0 + lane));
+                const long long per = hd.before(hd.tiles);
+                const long long in = from - mine;
+                const int h = static_cast<int>(in / per);
+                const long long r = in - h * per;
+                int lo = 0, hi = hd.tiles - 1;       // the last tile that begins at or before r
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) / 2;
+                    if (hd.before(mid) <= r) lo = mid; else hi = mid - 1;
+                }
+                sm.start[0] = b0 + lane;
+                sm.start[1] = h;
+                sm.start[2] = lo;
+                sm.start[3] = static_cast<int>(r - hd.before(lo));
+            }
+            return;
+        }
+        base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+}
+
+// 16 columns of a key's scores: the sum of their weights.
+__device__ __forceinline__ unsigned long long weights16(const uint32_t (&s)[16], const float* nl2, unsigned long long c2) {
+    unsigned long long sum = pk2(0.f, 0.f), sum1 = pk2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(nl2 + e);
+        float a, b, c, d;
+        upk2(ffma2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, pk2(l.x, l.y)), a, b);
+        upk2(ffma2(pk2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, pk2(l.z, l.w)), c, d);
+        sum = fadd2(sum, pk2(ex2(a), ex2(b)));
+        sum1 = fadd2(sum1, pk2(ex2(c), ex2(d)));
+    }
+    return fadd2(sum, sum1);
+}
+
+template <int D, bool MANY>
+__global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constant__ Maps mp, const TcParams tp) {
+    constexpr int kH = D / 64;
+    constexpr int kKHalf = kTile * 128;                  // bytes of a 64-column half of a key tile
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    // the swizzle counts address bits: tiles start on 1024-byte boundaries
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const Params& p = tp.p;
+    uint8_t* sK = smem;
+    uint8_t* sQ = sK + tp.k_stages * kH * kKHalf;
+    const int q_half = tp.nq * 128;
+    Small& sm = *reinterpret_cast<Small*>(sQ + tp.q_stages * kH * q_half);
+    volatile int* abort_flag = &sm.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(&sm.k_full[i], 1);
+            mbar_init(&sm.k_empty[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sm.q_full[i], 2);
+            mbar_init(&sm.q_empty[i], MANY ? 5 : 9);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_empty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.x_full[i], 4);
+            mbar_init(&sm.x_empty[i], 4);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort_flag = 0;
+        sm.bad = 0;
+        if (MANY) tp.records[blockIdx.x] = Record{0, 0, 0, 0, 0, 0, 0, 0};
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
+    if (warp == 8) plan<MANY>(tp, sm);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    const uint32_t buf_cols = kTmemCols / tp.buffers;
+    griddep_launch();                 // the join may start launching: it waits for the partial sums
+    bool ok = true;
+    int k_loads = 0, q_loads = 0;     // (TMA) requested so far
+    Walk<MANY> w(tp, sm);
+
+    if (warp == 8) {
+        // ------------------------------------------------ keys, and the chunks of rows
+        for (; ok && w.more; w.next()) {
+            const int stage = k_loads % tp.k_stages;
+            if (k_loads >= tp.k_stages && !(ok = warp_wait_for(&sm.k_empty[stage], (k_loads / tp.k_stages - 1) & 1, abort_flag))) break;
+            uint8_t* dst = sK + stage * kH * kKHalf;
+            const int k0 = w.t * kTile;
+            // a lane per load of `box` keys; what lies behind the length, or in a block outside the pool, is left out
+            const int at = k0 + lane * tp.box;
+            int64_t row = -1;
+            if (lane < kTile / tp.box && at < w.rows.n) row = key_row(p, w.b, w.h, at);
+            const unsigned there = __ballot_sync(0xffffffffu, row >= 0);
+            if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[stage], __popc(there) * tp.box * 128 * kH);
+            __syncwarp();
+            if (row >= 0)
+                for (int hh = 0; hh < kH; ++hh)
+                    tma_load_2d(dst + hh * kKHalf + lane * tp.box * 128, &mp.k, &sm.k_full[stage], hh * 64, static_cast<int>(row));
+            ++k_loads;
+            if (MANY) {
+                const int m = w.head.chunks(w.t) / w.head.mult, c0 = w.head.first(w.t);
+                for (int c = w.c; c < w.c + w.take; ++c) {
+                    const int qs = q_loads % tp.q_stages;
+                    if (q_loads >= tp.q_stages && !(ok = warp_wait_for(&sm.q_empty[qs], (q_loads / tp.q_stages - 1) & 1, abort_flag))) break;
+                    if (lane == 0) {
+                        const int qh = w.h * tp.g + c / m, i0 = (c0 + c % m) * kChunk;
+                        mbar_arrive_expect_tx(&sm.q_full[qs], kH * q_half);
+                        for (int hh = 0; hh < kH; ++hh)
+                            tma_load_2d(sQ + (qs * kH + hh) * q_half, &mp.q, &sm.q_full[qs], hh * 64, (w.b * p.Hq + qh) * p.T + i0);
+                    }
+                    ++q_loads;
+                }
+            }
+            __syncwarp();
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------ products
+        if (lane == 0) {
+            int kt = 0, u = 0, col = 0;
+            for (; ok && w.more; w.next(), ++kt) {
+                const int ks = kt % tp.k_stages;
+                if (!(ok = wait_for(&sm.k_full[ks], (kt / tp.k_stages) & 1, abort_flag))) break;
+                const uint32_t ka = smem_u32(sK + ks * kH * kKHalf);
+                const int n = MANY ? kChunk : min(tp.nq, (tp.g * w.rows.count - tp.row0 + 15) / 16 * 16);
+                const uint32_t idesc = idesc_bf16_f32(kTile, MANY ? kChunk : max(n, 16));
+                for (int c = 0; c < w.take; ++c, ++u) {
+                    const int qn = MANY ? u : col;
+                    const int qs = qn % tp.q_stages, buf = u % tp.buffers;
+                    if (!(ok = wait_for(&sm.q_full[qs], (qn / tp.q_stages) & 1, abort_flag))) break;
+                    if (u >= tp.buffers && !(ok = wait_for(&sm.s_empty[buf], (u / tp.buffers - 1) & 1, abort_flag))) break;
+                    tc_fence_after();
+                    const uint32_t qa = smem_u32(sQ + qs * kH * q_half);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_bf16(tmem + buf * buf_cols, sdesc_k128(ka + (k / 4) * kKHalf + (k % 4) * 32),
+                                 sdesc_k128(qa + (k / 4) * q_half + (k % 4) * 32), idesc, k > 0);
+                    mma_commit(&sm.s_full[buf]);
+                    if (MANY) mma_commit(&sm.q_empty[qs]);
+                }
+                if (!ok) break;
+                mma_commit(&sm.k_empty[ks]);
+                if (!MANY && w.column_ends()) mma_commit(&sm.q_empty[col++ % tp.q_stages]);
+            }
+            mma_commit(&sm.drain);
+        }
+        __syncwarp();
+    } else if (warp >= 10) {
+        // ------------------------------------------------ rows
+        if constexpr (MANY) {
+            // lse of a chunk's rows: four for each lane of warp 10
+            int u = 0;
+            if (warp == 10)
+                for (; ok && w.more; w.next()) {
+                    const int m = w.head.chunks(w.t) / w.head.mult, c0 = w.head.first(w.t);
+                    for (int c = w.c; c < w.c + w.take; ++c, ++u) {
+                        const int qs = u % tp.q_stages;
+                        const int qh = w.h * tp.g + c / m, i0 = (c0 + c % m) * kChunk;
+                        float x[4];
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = i0 + lane * 4 + e;
+                            x[e] = INFINITY;
+                            if (i < w.rows.count) x[e] = p.lse[static_cast<int64_t>(w.b * p.Hq + qh) * p.T + i];
+                        }
+                        if (u >= tp.q_stages && !(ok = warp_wait_for(&sm.q_empty[qs], (u / tp.q_stages - 1) & 1, abort_flag))) break;
+                        for (int e = 0; e < 4; ++e) x[e] = isfinite(x[e]) ? -x[e] * kL2e : -INFINITY;
+                        *reinterpret_cast<float4*>(&sm.nl2[qs][lane * 4]) = make_float4(x[0], x[1], x[2], x[3]);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.q_full[qs]);
+                    }
+                }
+        } else {
+            // a head's rows, 16 bytes a thread at a time, swizzled as the products read them
+            int col = 0;
+            bool fresh = true;        // the first tile of a column here
+            for (; ok && w.more; w.next()) {
+                if (fresh) {
+                    const int qs = col % tp.q_stages;
+                    if (col >= tp.q_stages && !(ok = warp_wait_for(&sm.q_empty[qs], (col / tp.q_stages - 1) & 1, abort_flag))) break;
+                    const int total = min(tp.nq, tp.g * w.rows.count - tp.row0), padded = max(16, (total + 15) / 16 * 16);
+                    const int tid = threadIdx.x - 320;
+                    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
+                    const int64_t q0 = static_cast<int64_t>(w.b) * p.Hq + w.h * tp.g;
+                    for (int x = tid; x < padded * (D / 8); x += 64) {
+                        const int r = x / (D / 8), part = x % (D / 8);
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < total) {
+                            const int rr = tp.row0 + r, gi = rr / w.rows.count;
+                            const int64_t row = (q0 + gi) * p.T + node_of(p, w.b, rr - gi * w.rows.count);
+                            v = *reinterpret_cast<const uint4*>(q + row * D + part * 8);
+                        }
+                        *reinterpret_cast<uint4*>(sQ + (qs * kH + part / 8) * q_half + r * 128 + ((part % 8) ^ (r & 7)) * 16) = v;
+                    }
+                    for (int r = tid; r < padded; r += 64) {
+                        float x = -INFINITY;
+                        int last = -1;
+                        if (r < total) {
+                            const int rr = tp.row0 + r, gi = rr / w.rows.count, i = rr - gi * w.rows.count;
+                            const float l = p.lse[(q0 + gi) * p.T + node_of(p, w.b, i)];
+                            if (isfinite(l)) x = -l * kL2e;
+                            last = w.rows.n - w.rows.count + i;
+                        }
+                        sm.nl2[qs][r] = x;
+                        sm.last[qs][r] = last;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.q_full[qs]);
+                    fresh = false;
+                }
+                if (w.column_ends()) {
+                    fresh = true;
+                    ++col;
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------ weights
+        const int grp = warp >> 2, key = (warp & 3) * 32 + lane;
+        if (blockIdx.x == 0) {
+            // the status: sequences that make no sense, blocks outside the pool.  (A wait that runs out flags it
+            // two seconds later.)
+            int bad = 0;
+            for (int b = warp; b < p.B; b += 8) {
+                const Rows r = rows_of(p, b);
+                if (!r.ok) {
+                    bad = 1;
+                } else if (p.table) {
+                    const int used = (r.n + p.rows - 1) / p.rows;
+                    for (int j = lane; j < used; j += 32) {
+                        const int blk = p.table[static_cast<int64_t>(b) * p.max_blocks + j];
+                        if (blk < 0 || blk >= p.num_blocks) bad = 1;
+                    }
+                }
+            }
+            if (bad) sm.bad = 1;
+            asm volatile("bar.sync 1, 256;" ::: "memory");   // all of these warps come here, once, and wait for nobody else
+            if (threadIdx.x == 0 && tp.row0 == 0) *static_cast<int4*>(p.ws) = make_int4(sm.bad ? SPEC_EINVAL : SPEC_OK, 0, 0, 0);
+        }
+        const unsigned long long c2 = pk2(p.scale * kL2e, p.scale * kL2e);
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        int u = 0, kt = 0, col = 0;
+        for (; ok && w.more; w.next(), ++kt) {
+            const int k0 = w.t * kTile, j = k0 + key;
+            const bool writes = MANY ? grp == 0 : (kt & 1) == grp;
+            // what the key has so far, on its way while the products run
+            const bool mine = writes && j < w.rows.n && (!p.table || key_row(p, w.b, w.h, j) >= 0);
+            const int64_t at = (static_cast<int64_t>(w.b) * p.Hkv + w.h) * p.cap + j;
+            const bool fresh = j >= w.rows.n - w.rows.count;
+            float old = 0.f;
+            if (mine && (!MANY || w.whole()) && (tp.row0 > 0 || (!fresh && p.decay != 0.f))) old = p.acc[at];
+            float sum = 0.f;
+            const int m = MANY ? w.head.chunks(w.t) / w.head.mult : 1, c0 = MANY ? w.head.first(w.t) : 0;
+            for (int c = w.c; c < w.c + w.take; ++c, ++u) {
+                if (MANY ? (u & 1) != grp : !writes) continue;
+                const int qn = MANY ? u : col;
+                const int qs = qn % tp.q_stages, buf = u % tp.buffers;
+                if (!(ok = warp_wait_for(&sm.s_full[buf], (u / tp.buffers) & 1, abort_flag))) break;
+                if (!(ok = warp_wait_for(&sm.q_full[qs], (qn / tp.q_stages) & 1, abort_flag))) break;   // complete: for its lse
+                tc_fence_after();
+                const uint32_t s_addr = lane_base + buf * buf_cols;
+                const float* nl2 = sm.nl2[qs];
+                // columns that hold rows, and the first of them that sees the warp's keys
+                int cols, lo;
+                bool plain;
+                if (MANY) {
+                    const int i0 = (c0 + c % m) * kChunk;
+                    cols = min(kChunk, w.rows.count - i0);
+                    lo = j - (w.rows.n - w.rows.count) - i0;         // of this key
+                    plain = cols == kChunk && k0 + kTile - 1 - (w.rows.n - w.rows.count) <= i0;
+                } else {
+                    cols = min(tp.nq, tp.g * w.rows.count - tp.row0);
+                    lo = 0;
+                    plain = k0 + kTile - 1 <= w.rows.n - w.rows.count;
+                }
+                unsigned long long part = pk2(0.f, 0.f);
+                if (plain) {
+                    const int steps = MANY ? kChunk / 16 : max(1, (cols + 15) / 16);
+                    uint32_t r[2][16];
+                    tmem_ld16(s_addr, r[0]);
+#pragma unroll 1
+                    for (int x = 0; x < steps; x += 2) {
+                        tmem_ld_wait();
+                        if (x + 1 < steps) tmem_ld16(s_addr + 16 * (x + 1), r[1]);
+                        part = fadd2(part, weights16(r[0], nl2 + 16 * x, c2));
+                        if (x + 1 < steps) {
+                            tmem_ld_wait();
+                            if (x + 2 < steps) tmem_ld16(s_addr + 16 * (x + 2), r[0]);
+                            part = fadd2(part, weights16(r[1], nl2 + 16 * (x + 1), c2));
+                        }
+                    }
+                } else {
+                    float f0 = 0.f;
+#pragma unroll 1
+                    for (int x = 0; x < cols; x += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(s_addr + x, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float v = ex2(fmaf(__uint_as_float(r[e]), p.scale * kL2e, nl2[x + e]));
+                            const bool sees = MANY ? x + e >= lo && x + e < cols : x + e < cols && j <= sm.last[qs][x + e];
+                            f0 += sees ? v : 0.f;
+                        }
+                    }
+                    part = pk2(f0, 0.f);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.s_empty[buf]);
+                    if (MANY) mbar_arrive(&sm.q_empty[qs]);
+                }
+                float f0, f1;
+                upk2(part, f0, f1);
+                sum += f0 + f1;
+            }
+            if (!ok) break;
+            if (MANY) {
+                // the groups' sums, through one of two buffers
+                const int x = kt & 1;
+                if (grp == 1) {
+                    if (kt >= 2 && !(ok = warp_wait_for(&sm.x_empty[x], (kt / 2 - 1) & 1, abort_flag))) break;
+                    sm.cross[x][key] = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.x_full[x]);
+                } else {
+                    if (!(ok = warp_wait_for(&sm.x_full[x], (kt / 2) & 1, abort_flag))) break;
+                    sum += sm.cross[x][key];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.x_empty[x]);
+                }
+            } else if (w.column_ends()) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.q_empty[col % tp.q_stages]);
+                ++col;
+            }
+            if (MANY && !w.whole()) {
+                // a tile that another CTA has a part of: the join puts them together
+                const bool tail = w.c == 0;
+                if (grp == 0) {
+                    tp.parts[(static_cast<int64_t>(blockIdx.x) * 2 + tail) * kTile + key] = sum;
+                    if (threadIdx.x == 0) {
+                        Record& rec = tp.records[blockIdx.x];
+                        if (tail) {
+                            rec.tail = 1;
+                            rec.b = w.b; rec.h = w.h; rec.t = w.t;
+                        } else {
+                            rec.head = 1;
+                            rec.head_ends = w.c + w.take == w.head.chunks(w.t);
+                        }
+                    }
+                }
+            } else if (mine) {
+                p.acc[at] = tp.row0 > 0 ? old + sum : fmaf(p.decay, old, sum);
+                if (fresh && p.pos && tp.row0 == 0) p.pos[at] = (p.seen ? p.seen[w.b] : w.rows.n) - w.rows.n + j;
+            }
+        }
+    }
+    if (!ok) {
+        if (lane == 0) {
+            flag_status(p.ws, SPEC_ETIMEOUT);
+            *abort_flag = 1;
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {
+        // a wait ran out: let this CTA's own loads and MMAs land before it ends
+        if (warp == 8) {
+            for (int i = max(0, k_loads - tp.k_stages); i < k_loads; ++i) mbar_wait(&sm.k_full[i % tp.k_stages], (i / tp.k_stages) & 1, 100000000ull);
+            if (MANY)
+                for (int i = max(0, q_loads - tp.q_stages); i < q_loads; ++i) mbar_wait(&sm.q_full[i % tp.q_stages], (i / tp.q_stages) & 1, 100000000ull);
+        }
+        if (warp == 9) mbar_wait(&sm.drain, 0, 100000000ull);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// The tiles that were cut: the CTA in which one begins adds up its parts, in order.
+__global__ void __launch_bounds__(kTile) k_weigh_join(const TcParams tp, int ctas) {
+    griddep_wait();
+    const Record rec = tp.records[blockIdx.x];
+    if (!rec.tail) return;
+    const Params& p = tp.p;
+    float sum = tp.parts[(static_cast<int64_t>(blockIdx.x) * 2 + 1) * kTile + threadIdx.x];
+    int end = blockIdx.x + 1;         // one more than the CTA in which the tile ends, 32 records at a time
+    for (; end < ctas; end += 32) {
+        const int c = end + (threadIdx.x & 31);
+        const unsigned ends = __ballot_sync(0xffffffffu, c >= ctas || tp.records[c].head_ends);
+        if (ends) {
+            end += __ffs(ends);
+            break;
+        }
+    }
+    end = min(end, ctas);
+#pragma unroll 8
+    for (int c = blockIdx.x + 1; c < end; ++c) sum += tp.parts[static_cast<int64_t>(c) * 2 * kTile + threadIdx.x];
+    const Rows rows = rows_of(p, rec.b);
+    const int j = rec.t * kTile + threadIdx.x;
+    if (rows.ok && j < rows.n && key_row(p, rec.b, rec.h, j) >= 0) store(p, rec.b, rec.h, j, rows, sum);
+}
+
+// ---------------------------------------------------------------- host
+
+constexpr size_t kSmem = 232448;      // of one CTA, all there is: no two share an SM's TMEM
+
+static int few_rows(int g, int T, int P) { return g * (P ? P : T); }
+// Rows of a prompt fill chunks of 128 of one query head; shorter ones are better off side by side, several heads in a pass.
+bool weigh_many(int g, int T, int P) { return !P && T >= 96 && g * T > kMostRows; }
+
+size_t weigh_tc_bytes(int g, int T, int P) {
+    return weigh_many(g, T, P) ? static_cast<size_t>(device_sm_count()) * (sizeof(Record) + 2 * kTile * sizeof(float)) : 0;
+}
+
+template <int D, bool MANY>
+static spec_status launch_tc(const Maps& m, TcParams& tp, cudaStream_t s) {
+    constexpr size_t kStage = static_cast<size_t>(kTile) * D * 2;
+    const size_t q = static_cast<size_t>(tp.nq) * D * 2;
+    tp.q_stages = MANY ? 4 : 2;
+    tp.buffers = MANY || tp.nq <= 128 ? 4 : 2;
+    const size_t room = kSmem - 1024 - sizeof(Small) - tp.q_stages * q;
+    tp.k_stages = static_cast<int>(std::min<size_t>(MANY ? 2 : kMaxStages, room / kStage));
+    auto kern = k_weigh_tc<D, MANY>;
+    SPEC_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)));
+    const int ctas = device_sm_count();
+    SPEC_CUDA_TRY(launch("kv_weigh_tc", kern, dim3(ctas), dim3(kTcThreads), kSmem, s, m, tp));
+    if (MANY) SPEC_CUDA_TRY(launch_ex("kv_weigh_join", k_weigh_join, dim3(ctas), dim3(kTile), 0, s, true, tp, ctas));
+    return SPEC_OK;
+}
+
+spec_status weigh_tc_run(const Params& p, int D, void* scratch, cudaStream_t s) {
+    Maps m;
+    memset(&m, 0, sizeof(m));
+    TcParams tp{};
+    tp.p = p;
+    tp.g = p.Hq / p.Hkv;
+    tp.box = kTile;
+    if (p.table) {                    // a load lies inside one block and one tile
+        tp.box = 16;
+        while (tp.box < kTile && p.rows % (2 * tp.box) == 0) tp.box *= 2;
+    }
+    const uint64_t k_rows = static_cast<uint64_t>(p.table ? p.num_blocks : p.B) * p.Hkv * p.rows;
+    const uint64_t q_rows = static_cast<uint64_t>(p.B) * p.Hq * p.T;
+    if (k_rows > 0x7fffffffull || q_rows > 0x7fffffffull) return fail(SPEC_EINVAL, "more than 2^31 rows of keys or queries");
+    SPEC_CUDA_TRY(make_tmap_bf16_2d(&m.k, p.k, k_rows, D, D, tp.box));
+    SPEC_CUDA_TRY(make_tmap_bf16_2d(&m.q, p.q, q_rows, D, D, kChunk));
+    if (weigh_many(tp.g, p.T, p.path ? p.P : 0)) {
+        tp.nq = kChunk;
+        tp.records = static_cast<Record*>(scratch);
+        tp.parts = reinterpret_cast<float*>(tp.records + device_sm_count());
+        return D == 64 ? launch_tc<64, true>(m, tp, s) : launch_tc<128, true>(m, tp, s);
+    }
+    const int rows = few_rows(tp.g, p.T, p.path ? p.P : 0);
+    tp.nq = std::min(kMostRows, (rows + 15) / 16 * 16);
+    for (tp.row0 = 0; tp.row0 < rows; tp.row0 += kMostRows) {
+        const spec_status st = D == 64 ? launch_tc<64, false>(m, tp, s) : launch_tc<128, false>(m, tp, s);
+        if (st != SPEC_OK) return st;
+    }
+    return SPEC_OK;
+}
+
+}  // namespace weigh
+}  // namespace spec
