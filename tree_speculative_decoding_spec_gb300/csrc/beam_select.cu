@@ -53,27 +53,49 @@ __device__ __forceinline__ State state_of(const Params& p, int row) {
     return p.ended && p.ended[row] != 0 ? kEnded : kLive;
 }
 
+// 16 bytes of a row: NaN becomes -inf where they are loaded, in one instruction for a word.
 template <typename T> struct Vec {
     static constexpr int E = 16 / sizeof(T);
+    static __device__ __forceinline__ uint32_t& word(uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+    static __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+    static __device__ __forceinline__ void clean(uint4& v);
     static __device__ __forceinline__ float at(const uint4& v, int e);
-    static __device__ __forceinline__ void put(uint4& v, int e, T x);
+    static __device__ __forceinline__ float top(const uint4 (&v)[kVecs]);
 };
-template <> __device__ __forceinline__ float Vec<float>::at(const uint4& v, int e) {
-    const float x = __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
-    return fmaxf(x, -INFINITY);       // NaN counts as -inf
+template <> __device__ __forceinline__ void Vec<float>::clean(uint4& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) word(v, i) = __float_as_uint(fmaxf(__uint_as_float(word(v, i)), -INFINITY));
+}
+template <> __device__ __forceinline__ float Vec<float>::at(const uint4& v, int e) { return __uint_as_float(word(v, e)); }
+template <> __device__ __forceinline__ float Vec<float>::top(const uint4 (&v)[kVecs]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) m = tc::fmax3(tc::fmax3(m, at(v[i], 0), at(v[i], 1)), at(v[i], 2), at(v[i], 3));
+    return m;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+template <> __device__ __forceinline__ void Vec<__nv_bfloat16>::clean(uint4& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) word(v, i) = max_bf16x2(word(v, i), 0xFF80FF80u);
 }
 template <> __device__ __forceinline__ float Vec<__nv_bfloat16>::at(const uint4& v, int e) {
-    const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
-    return fmaxf(__uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16), -INFINITY);
+    const uint32_t w = word(v, e / 2);
+    return __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
 }
-template <> __device__ __forceinline__ void Vec<float>::put(uint4& v, int e, float x) {
-    const uint32_t b = __float_as_uint(x);
-    if (e == 0) v.x = b; else if (e == 1) v.y = b; else if (e == 2) v.z = b; else v.w = b;
+template <> __device__ __forceinline__ float Vec<__nv_bfloat16>::top(const uint4 (&v)[kVecs]) {
+    uint32_t m = 0xFF80FF80u;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) m = max_bf16x2(max_bf16x2(m, max_bf16x2(v[i].x, v[i].y)), max_bf16x2(v[i].z, v[i].w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
 }
-template <> __device__ __forceinline__ void Vec<__nv_bfloat16>::put(uint4& v, int e, __nv_bfloat16 x) {
-    uint32_t& w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
-    const uint32_t b = __bfloat16_as_ushort(x);
-    w = e & 1 ? (w & 0xFFFFu) | (b << 16) : (w & 0xFFFF0000u) | b;
+__device__ __forceinline__ unsigned long long fmul2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 __device__ __forceinline__ unsigned long long make_key(float x, int token) {
@@ -128,7 +150,7 @@ __device__ __forceinline__ int block_sum(Shared& sh, int v, int turn) {
 // More elements of one chunk pass the threshold than the list holds (rows of equal logits, logits that rise with
 // the token): the K largest of cand[0 .. before) and the chunk by bisection, over the order of the logits, then of the tokens.
 template <typename T>
-__device__ float cut_chunk(Shared& sh, const uint4 (&raw)[kVecs], const int (&first)[kVecs], int before, int K) {
+__device__ __noinline__ float cut_chunk(Shared& sh, const uint4 (&raw)[kVecs], int first, int before, int K) {
     constexpr int E = Vec<T>::E;
     const unsigned long long mine = static_cast<int>(threadIdx.x) < before ? sh.cand[threadIdx.x] : 0;   // before < kFull
     const unsigned none = order_key(-INFINITY);
@@ -140,7 +162,7 @@ __device__ float cut_chunk(Shared& sh, const uint4 (&raw)[kVecs], const int (&fi
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const unsigned k = order_key(Vec<T>::at(raw[v], e));
-                n += k > none && test(k, first[v] + e);
+                n += k > none && test(k, first + v * kThreads * E + e);
             }
         return block_sum(sh, n, turn++);
     };
@@ -167,7 +189,7 @@ __device__ float cut_chunk(Shared& sh, const uint4 (&raw)[kVecs], const int (&fi
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const float x = Vec<T>::at(raw[v], e);
-            if (order_key(x) > none && keep(order_key(x), first[v] + e)) add(make_key(x, first[v] + e));
+            if (order_key(x) > none && keep(order_key(x), first + v * kThreads * E + e)) add(make_key(x, first + v * kThreads * E + e));
         }
     __syncthreads();
     if (static_cast<int>(threadIdx.x) < K) sh.cand[threadIdx.x] = sh.best[threadIdx.x];
@@ -177,7 +199,7 @@ __device__ float cut_chunk(Shared& sh, const uint4 (&raw)[kVecs], const int (&fi
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_slices(const Params p) {
+__global__ void __launch_bounds__(kThreads, 4) k_slices(const Params p) {
     constexpr int E = Vec<T>::E;
     __shared__ Shared sh;
     clear_status_then_trigger(p.ws);
@@ -196,10 +218,19 @@ __global__ void __launch_bounds__(kThreads) k_slices(const Params p) {
             asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(at));
         } else {                      // the row's ends, element by element
-            r = make_uint4(0, 0, 0, 0);
+            uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                Vec<T>::put(r, e, v < v1 && i + e >= 0 && i + e < p.V ? x[i + e] : from_f32<T>(-INFINITY));
+            for (int k = 0; k < 4; ++k) {
+                constexpr int P = E / 4;   // elements of a word
+                w[k] = 0;
+#pragma unroll
+                for (int h = 0; h < P; ++h) {
+                    const int e = i + k * P + h;
+                    const float val = v < v1 && e >= 0 && e < p.V ? to_f32<T>(x[e]) : -INFINITY;
+                    w[k] |= P == 1 ? __float_as_uint(val) : (__float_as_uint(val) >> 16) << (16 * h);
+                }
+            }
+            r = make_uint4(w[0], w[1], w[2], w[3]);
         }
         return r;
     };
@@ -212,30 +243,32 @@ __global__ void __launch_bounds__(kThreads) k_slices(const Params p) {
     __syncthreads();
     for (int c = v0; c < v1; c += kVecs * kThreads) {
         uint4 raw[kVecs];
-        int first[kVecs];
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v) {
-            raw[v] = next[v];
-            first[v] = (c + v * kThreads + static_cast<int>(threadIdx.x)) * E - head;
-        }
+        for (int v = 0; v < kVecs; ++v) raw[v] = next[v];
+        const int first = (c + static_cast<int>(threadIdx.x)) * E - head;   // of raw[v]: first + v * kThreads * E
         if (c + kVecs * kThreads < v1) {
 #pragma unroll
             for (int v = 0; v < kVecs; ++v) next[v] = load(c + (kVecs + v) * kThreads + threadIdx.x);
         }
-        float top = -INFINITY;
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v)
-#pragma unroll
-            for (int e = 0; e < E; ++e) top = fmaxf(top, Vec<T>::at(raw[v], e));
+        for (int v = 0; v < kVecs; ++v) Vec<T>::clean(raw[v]);
+        const float top = Vec<T>::top(raw);
         // the sum, rescaled to the larger maximum.  x - m is taken before the factor: with both in one
         // FMA the rounding of m log2(e) would shift every term the same way
         const float nm = fmaxf(m, top), ref = nm == -INFINITY ? 0.f : nm;
-        float part[4] = {s * tc::ex2((m - ref) * kLog2e), 0.f, 0.f, 0.f};
+        const unsigned long long nref = tc::pk2(-ref, -ref), factor = tc::pk2(kLog2e, kLog2e);
+        unsigned long long part[2] = {tc::pk2(s * tc::ex2((m - ref) * kLog2e), 0.f), tc::pk2(0.f, 0.f)};
 #pragma unroll
         for (int v = 0; v < kVecs; ++v)
 #pragma unroll
-            for (int e = 0; e < E; ++e) part[e & 3] += tc::ex2((Vec<T>::at(raw[v], e) - ref) * kLog2e);
-        s = (part[0] + part[1]) + (part[2] + part[3]);
+            for (int e = 0; e < E; e += 2) {
+                float a, b;
+                tc::upk2(fmul2(tc::fadd2(tc::pk2(Vec<T>::at(raw[v], e), Vec<T>::at(raw[v], e + 1)), nref), factor), a, b);
+                part[(e / 2) & 1] = tc::fadd2(part[(e / 2) & 1], tc::pk2(tc::ex2(a), tc::ex2(b)));
+            }
+        float s0, s1;
+        tc::upk2(tc::fadd2(part[0], part[1]), s0, s1);
+        s = s0 + s1;
         m = nm;
         // the first chunk's bound: every warp has kq elements of at least its kq-th largest thread maximum
         const bool begin = c == v0;
@@ -257,7 +290,7 @@ __global__ void __launch_bounds__(kThreads) k_slices(const Params p) {
                     const float val = Vec<T>::at(raw[v], e);
                     if (passes(val)) {
                         const int at = atomicAdd(&sh.count, 1);
-                        if (at < kCap) sh.cand[at] = make_key(val, first[v] + e);
+                        if (at < kCap) sh.cand[at] = make_key(val, first + v * kThreads * E + e);
                     }
                 }
         }
@@ -303,89 +336,119 @@ struct Entry {
     uint32_t tie, at;                 // beam * V + token; the candidate's place
 };
 
+// log(x), x >= 1, to some 2^-25: logf of a mantissa near 1, where its error is that small, and the exponent's part.
+__device__ __forceinline__ double log_parts(float x) {
+    int e = static_cast<int>(__float_as_uint(x) >> 23) - 127;
+    float f = __uint_as_float((__float_as_uint(x) & 0x7fffffu) | 0x3f800000u);
+    if (f > 1.4142135f) { f *= 0.5f; ++e; }
+    return e * 0.693147180559945309 + static_cast<double>(logf(f));
+}
+
+// Ranks are needed in 64 bits only of those near the K-th: this GPU does two 64-bit operations a clock and SM,
+// and a first pass in 32 bits leaves some tens of candidates (all of them in 64 bits: 15 us of 21
+// for 8 beams of 32000 tokens).  What depends on the call's inputs alone is worked out while the slices run.
 __global__ void __launch_bounds__(kThreads) k_join(const Params p) {
     __shared__ Entry list[kJoinCap];
-    __shared__ double s_base[SPEC_MAX_BEAMS], s_div[SPEC_MAX_BEAMS];   // score(t) = base + x; rank = score / div
+    __shared__ double s_base[SPEC_MAX_BEAMS], s_inv[SPEC_MAX_BEAMS];   // score(t) = base + x; rank = score * inv
+    __shared__ float s_basef[SPEC_MAX_BEAMS], s_invf[SPEC_MAX_BEAMS];
     __shared__ int s_state[SPEC_MAX_BEAMS], s_len[SPEC_MAX_BEAMS];
-    __shared__ unsigned s_bound[kWarps];
+    __shared__ float s_bound[kWarps];
     __shared__ Entry s_top[kWarps];
     __shared__ int s_count;
     const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.slices, K = p.K;
-    griddep_wait();
     if (threadIdx.x == 0) s_count = 0;
+    if (threadIdx.x < p.W) {
+        const int w = threadIdx.x, row = b * p.W + w;
+        const State st = state_of(p, row);
+        const int len = (p.length ? p.length[row] : 0) + (st == kLive ? 1 : 0);
+        s_state[w] = st;
+        s_len[w] = len;
+        s_base[w] = st == kDead ? 0.0 : static_cast<double>(p.scores[row]);
+        s_inv[w] = p.alpha != 0.f ? pow(static_cast<double>(max(len, 1)), -static_cast<double>(p.alpha)) : 1.0;
+    }
+    __syncthreads();
+    griddep_wait();
+    float size = 0.f;                 // the largest |base| of the warp's rows
     for (int w = warp; w < p.W; w += kWarps) {
-        const int row = b * p.W + w;
-        State st = state_of(p, row);
-        double base = st == kDead ? 0.0 : static_cast<double>(p.scores[row]);
-        if (st == kLive) {
-            const float2 ms = lane < S ? p.sums[static_cast<size_t>(row) * S + lane] : make_float2(-INFINITY, 0.f);
+        if (s_state[w] == kLive) {
+            const float2 ms = lane < S ? p.sums[(static_cast<size_t>(b) * p.W + w) * S + lane] : make_float2(-INFINITY, 0.f);
             const float M = warp_max(ms.x);
-            double sum = isfinite(ms.x) ? static_cast<double>(ms.y) * exp(static_cast<double>(ms.x) - M) : 0.0;
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (!isfinite(M)) {       // nothing but -inf, or a logit of +inf
-                st = kDead;
-                if (M > 0.f && lane == 0) flag_status(p.ws, SPEC_EINVAL);
-            } else {
-                base -= M + log(sum);
+            const float sum = warp_sum(isfinite(ms.x) ? ms.y * exp2f((ms.x - M) * kLog2e) : 0.f);
+            if (lane == 0) {
+                if (!isfinite(M)) {   // nothing but -inf, or a logit of +inf
+                    s_state[w] = kDead;
+                    if (M > 0.f) flag_status(p.ws, SPEC_EINVAL);
+                } else {
+                    s_base[w] -= M + log_parts(sum);
+                }
             }
         }
         if (lane == 0) {
-            const int len = (p.length ? p.length[row] : 0) + (st == kLive ? 1 : 0);
-            s_state[w] = st;
-            s_base[w] = base;
-            s_len[w] = len;
-            s_div[w] = p.alpha != 0.f ? pow(static_cast<double>(max(len, 1)), static_cast<double>(p.alpha)) : 1.0;
+            s_basef[w] = static_cast<float>(s_base[w]);
+            s_invf[w] = static_cast<float>(s_inv[w]);
         }
+        __syncwarp();
+        if (s_state[w] != kDead) size = fmaxf(size, fabsf(s_basef[w]));
     }
+    if (lane == 0) s_bound[warp] = size;
     __syncthreads();
+    for (int i = 0; i < kWarps; ++i) size = fmaxf(size, s_bound[i]);
     const int per = S * K, n = p.W * per;
-    auto score_at = [&](int c, int w, uint32_t& token, bool& some) {
-        some = true;
+    const unsigned long long* cand = p.cand + static_cast<size_t>(b) * n;
+    auto some_at = [&](int c, int w, float& x, uint32_t& token) {
         if (s_state[w] == kEnded) {
-            some = c == w * per;
             token = p.eos;
-            return s_base[w];
+            x = 0.f;
+            return c == w * per;
         }
-        some = s_state[w] == kLive;
-        if (!some) return 0.0;
-        const unsigned long long k = p.cand[static_cast<size_t>(b) * n + c];
-        some = k != 0;
+        if (s_state[w] != kLive) return false;
+        const unsigned long long k = cand[c];
         token = ~static_cast<uint32_t>(k);
-        return s_base[w] + static_cast<double>(key_value(static_cast<unsigned>(k >> 32)));
+        x = key_value(static_cast<unsigned>(k >> 32));
+        return k != 0;
+    };
+    auto near_rank = [&](int c) {     // -inf: no pair
+        const int w = c / per;
+        float x;
+        uint32_t token;
+        return some_at(c, w, x, token) ? (s_basef[w] + x) * s_invf[w] : -INFINITY;
     };
     auto entry_at = [&](int c) {
         const int w = c / per;
-        uint32_t token = 0;
-        bool some;
-        const double score = score_at(c, w, token, some);
-        return some ? Entry{order_key64(score / s_div[w]), static_cast<uint32_t>(w) * p.V + token, static_cast<uint32_t>(c)} : Entry{0, 0, 0};
+        float x;
+        uint32_t token;
+        if (!some_at(c, w, x, token)) return Entry{0, 0, 0};
+        return Entry{order_key64((s_base[w] + x) * s_inv[w]), static_cast<uint32_t>(w) * p.V + token, static_cast<uint32_t>(c)};
     };
     auto above = [](const Entry& x, const Entry& y) { return x.key > y.key || (x.key == y.key && x.tie < y.tie); };
     auto write = [&](int r, const Entry& e) {
         const int w = e.tie / p.V;
+        float x;
         uint32_t token;
-        bool some;
+        some_at(e.at, w, x, token);
         const size_t o = static_cast<size_t>(b) * K + r;
-        p.score[o] = static_cast<float>(score_at(e.at, w, token, some));
+        p.score[o] = static_cast<float>(s_base[w] + x);
         p.token[o] = token;
         p.parent[o] = w;
         if (p.ended_out) p.ended_out[o] = s_state[w] == kEnded || static_cast<int>(token) == p.eos;
         if (p.length_out) p.length_out[o] = s_len[w];
     };
-    // a bound as in the slices, on the upper halves of the ranks
-    unsigned mine = 0;
-    for (int c = threadIdx.x; c < n; c += kThreads) mine = max(mine, static_cast<unsigned>(entry_at(c).key >> 32));
-    const unsigned kth = warp_kth(mine, (K + kWarps - 1) / kWarps);
-    if (lane == 0) s_bound[warp] = kth;
+    // a bound as in the slices, lowered by what 32 bits can be off: four roundings of |base| + |x|, |x| <= |base| + |rank| / inv
+    float mine = -INFINITY;
+    for (int c = threadIdx.x; c < n; c += kThreads) mine = fmaxf(mine, near_rank(c));
+    const unsigned kth = warp_kth(mine == -INFINITY ? 0u : order_key(mine), (K + kWarps - 1) / kWarps);
+    __syncthreads();                  // s_bound has been read
+    if (lane == 0) s_bound[warp] = kth ? key_value(kth) : -INFINITY;
     __syncthreads();
-    unsigned low = s_bound[0];
-    for (int i = 1; i < kWarps; ++i) low = min(low, s_bound[i]);
+    float low = s_bound[0];
+    for (int i = 1; i < kWarps; ++i) low = fminf(low, s_bound[i]);
+    low -= 2e-6f * (fabsf(low) + size);
     for (int c = threadIdx.x; c < n; c += kThreads) {
-        const Entry e = entry_at(c);
-        if (e.key && static_cast<unsigned>(e.key >> 32) >= low) {
+        const float r = near_rank(c);
+        if (r > -INFINITY && !(r < low)) {
             const int at = atomicAdd(&s_count, 1);
-            if (at < kJoinCap) list[at] = e;
+            if (at < kJoinCap) list[at] = entry_at(c);
         }
     }
     __syncthreads();
@@ -395,6 +458,7 @@ __global__ void __launch_bounds__(kThreads) k_join(const Params p) {
         for (int i = threadIdx.x; i < m; i += kThreads) {
             const Entry e = list[i];
             int rank = 0;
+#pragma unroll 4
             for (int j = 0; j < m; ++j) rank += above(list[j], e);
             if (rank < K) write(rank, e);
         }
@@ -435,11 +499,15 @@ __global__ void __launch_bounds__(kThreads) k_join(const Params p) {
     }
 }
 
-// Slices of a row: enough CTAs for four on every SM, of at least 2048 logits.
+// Slices of a row.  Four CTAs fit an SM.  Where there is less than that of work they are as short as 2048
+// logits; else there are four rounds of them, so that the last one's gaps cost little, but none
+// shorter than 8192, whose start and end cost as much as the rest.
 int slices_of(int64_t rows, int V) {
-    const int64_t want = (4 * device_sm_count() + rows - 1) / rows;
-    const int64_t most = (static_cast<int64_t>(V) + 2047) / 2048;
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, kMaxSlices})));
+    const int64_t slots = 4 * device_sm_count();
+    const int64_t finest = (static_cast<int64_t>(V) + 2047) / 2048, fine = (static_cast<int64_t>(V) + 8191) / 8192;
+    const int64_t once = (slots + rows - 1) / rows, rounds = (4 * slots + rows - 1) / rows;
+    const int64_t s = std::max(std::min(once, finest), std::min(rounds, fine));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s, kMaxSlices)));
 }
 
 spec_status check_sizes(int B, int W, int V, int K) {
