@@ -658,8 +658,8 @@ size_t beam_select_workspace_size(int32_t B, int32_t W, int32_t V, int32_t K);
  * Selection of a beam search, for drafts that extend their best continuations step by step:
  * of every sequence's W beams the K best (beam, token) pairs.  For a live beam w and a token t
  *     score  = scores[w] + x[w, t] - log sum_u exp x[w, u],   length = length[w] + 1
- * An ended beam (ended[w] != 0) offers itself: token eos, score and length as they are; its
- * logits are not read.  A beam whose score is not finite offers nothing (a first step has one
+ * An ended beam (ended[w] != 0) offers itself: token eos, score and length as they are, whatever
+ * its logits.  A beam whose score is not finite offers nothing (a first step has one
  * live beam and the others at -inf).  Pairs are ranked by score / max(length, 1)^alpha, in 64
  * bits, equal ones by the lower beam, then the lower token.
  *

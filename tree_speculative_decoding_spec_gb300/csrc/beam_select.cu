@@ -26,6 +26,7 @@ namespace beam {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVecs = 4;              // 16-byte loads of a thread and chunk
+constexpr int kPerSm = 5;             // CTAs of an SM: its loads in flight come from the others while one works
 constexpr int kCap = 1024;            // candidates a slice holds at most
 constexpr int kFull = 256;            // from here on they are cut down to K
 constexpr int kMaxSlices = 32;        // one lane each in the join
@@ -60,19 +61,14 @@ template <typename T> struct Vec {
     static __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
     static __device__ __forceinline__ void clean(uint4& v);
     static __device__ __forceinline__ float at(const uint4& v, int e);
-    static __device__ __forceinline__ float top(const uint4 (&v)[kVecs]);
+    static __device__ __forceinline__ float top(const uint4& v);
 };
 template <> __device__ __forceinline__ void Vec<float>::clean(uint4& v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) word(v, i) = __float_as_uint(fmaxf(__uint_as_float(word(v, i)), -INFINITY));
 }
 template <> __device__ __forceinline__ float Vec<float>::at(const uint4& v, int e) { return __uint_as_float(word(v, e)); }
-template <> __device__ __forceinline__ float Vec<float>::top(const uint4 (&v)[kVecs]) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) m = tc::fmax3(tc::fmax3(m, at(v[i], 0), at(v[i], 1)), at(v[i], 2), at(v[i], 3));
-    return m;
-}
+template <> __device__ __forceinline__ float Vec<float>::top(const uint4& v) { return fmaxf(tc::fmax3(at(v, 0), at(v, 1), at(v, 2)), at(v, 3)); }
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -86,10 +82,8 @@ template <> __device__ __forceinline__ float Vec<__nv_bfloat16>::at(const uint4&
     const uint32_t w = word(v, e / 2);
     return __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
 }
-template <> __device__ __forceinline__ float Vec<__nv_bfloat16>::top(const uint4 (&v)[kVecs]) {
-    uint32_t m = 0xFF80FF80u;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) m = max_bf16x2(max_bf16x2(m, max_bf16x2(v[i].x, v[i].y)), max_bf16x2(v[i].z, v[i].w));
+template <> __device__ __forceinline__ float Vec<__nv_bfloat16>::top(const uint4& v) {
+    const uint32_t m = max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w));
     return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
 }
 __device__ __forceinline__ unsigned long long fmul2(unsigned long long a, unsigned long long b) {
@@ -103,7 +97,7 @@ __device__ __forceinline__ unsigned long long make_key(float x, int token) {
 }
 
 struct Shared {
-    unsigned long long cand[kCap];
+    __align__(16) unsigned long long cand[kCap + 4];
     unsigned long long best[SPEC_MAX_BEAMS];
     int count, kept;
     unsigned bound[kWarps];
@@ -114,6 +108,7 @@ struct Shared {
 // The kq-th largest of a warp's values, as order keys; 0 where it has fewer.
 __device__ __forceinline__ unsigned warp_kth(unsigned mine, int kq) {
     unsigned top = 0;
+#pragma unroll 1
     for (int i = 0; i < kq; ++i) {
         top = __reduce_max_sync(0xffffffffu, mine);
         const unsigned who = __ballot_sync(0xffffffffu, mine == top);
@@ -123,16 +118,22 @@ __device__ __forceinline__ unsigned warp_kth(unsigned mine, int kq) {
 }
 
 // Bring cand[0 .. n) down to its K largest, sorted; returns the threshold that later elements must pass.
-__device__ float cut(Shared& sh, int n, int K) {
+__device__ __noinline__ float cut(Shared& sh, int n, int K) {
+    if (static_cast<int>(threadIdx.x) < 4) sh.cand[n + threadIdx.x] = 0;   // to a whole number of steps
+    __syncthreads();
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const unsigned long long key = sh.cand[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += sh.cand[j] > key;
+#pragma unroll 1
+        for (int j = 0; j < n; j += 4) {
+            const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&sh.cand[j]), b = *reinterpret_cast<const ulonglong2*>(&sh.cand[j + 2]);
+            rank += (a.x > key) + (a.y > key) + (b.x > key) + (b.y > key);
+        }
         if (rank < K) sh.best[rank] = key;
     }
     __syncthreads();
     const int k = min(n, K);
-    if (threadIdx.x < k) sh.cand[threadIdx.x] = sh.best[threadIdx.x];
+    if (static_cast<int>(threadIdx.x) < k) sh.cand[threadIdx.x] = sh.best[threadIdx.x];
     if (threadIdx.x == 0) sh.count = k;
     __syncthreads();
     return n >= K ? key_value(static_cast<unsigned>(sh.cand[K - 1] >> 32)) : -INFINITY;
@@ -147,11 +148,62 @@ __device__ __forceinline__ int block_sum(Shared& sh, int v, int turn) {
     return sum;
 }
 
+// A row as 16-byte vectors that start at 16-byte boundaries, the first in front of the row where that does not; of one slice.
+template <typename T> struct Row {
+    static constexpr int E = Vec<T>::E;
+    const T* x;
+    int V, head, end;                 // elements in front of the row; one more than the slice's last vector
+    __device__ __forceinline__ Row(const Params& p, int row)
+        : x(static_cast<const T*>(p.logits) + static_cast<int64_t>(row) * p.stride), V(p.V),
+          head(static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T))), end((head + p.V + E - 1) / E) {}
+};
+
+// The row's ends, element by element: i is the vector's first one.
+template <typename T> __device__ __noinline__ uint4 load_end(const T* x, int V, int i) {
+    constexpr int E = Vec<T>::E, P = E / 4;   // elements of a word
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int h = 0; h < P; ++h) {
+            const int e = i + k * P + h;
+            const float val = e >= 0 && e < V ? to_f32<T>(x[e]) : -INFINITY;
+            w[k] |= P == 1 ? __float_as_uint(val) : (__float_as_uint(val) >> 16) << (16 * h);
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A thread's vectors of the chunk that begins at vector c.
+template <typename T> __device__ __forceinline__ void load_chunk(const Row<T>& row, int c, uint4 (&raw)[kVecs]) {
+    constexpr int E = Vec<T>::E;
+    constexpr uint32_t kNone = E == 4 ? 0xFF800000u : 0xFF80FF80u;   // -inf
+    const int v0 = c + static_cast<int>(threadIdx.x);
+    bool part[kVecs];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+        const int at = v0 + v * kThreads, i = at * E - row.head;
+        const bool whole = at < row.end && i >= 0 && i + E <= row.V;
+        part[v] = at < row.end && !whole;
+        raw[v] = make_uint4(kNone, kNone, kNone, kNone);
+        if (whole)
+            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(raw[v].x), "=r"(raw[v].y), "=r"(raw[v].z), "=r"(raw[v].w) : "l"(row.x + i));
+    }
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+        if (part[v]) raw[v] = load_end<T>(row.x, row.V, (v0 + v * kThreads) * E - row.head);
+}
+
 // More elements of one chunk pass the threshold than the list holds (rows of equal logits, logits that rise with
 // the token): the K largest of cand[0 .. before) and the chunk by bisection, over the order of the logits, then of the tokens.
 template <typename T>
-__device__ __noinline__ float cut_chunk(Shared& sh, const uint4 (&raw)[kVecs], int first, int before, int K) {
+__device__ __noinline__ float cut_chunk(Shared& sh, const Row<T>& row, int c, int before, int K) {
     constexpr int E = Vec<T>::E;
+    uint4 raw[kVecs];                 // the chunk once more
+    load_chunk(row, c, raw);
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) Vec<T>::clean(raw[v]);
+    const int first = (c + static_cast<int>(threadIdx.x)) * E - row.head;
     const unsigned long long mine = static_cast<int>(threadIdx.x) < before ? sh.cand[threadIdx.x] : 0;   // before < kFull
     const unsigned none = order_key(-INFINITY);
     int turn = 0;
@@ -199,60 +251,33 @@ __device__ __noinline__ float cut_chunk(Shared& sh, const uint4 (&raw)[kVecs], i
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) k_slices(const Params p) {
+__global__ void __launch_bounds__(kThreads, kPerSm) k_slices(const Params p) {
     constexpr int E = Vec<T>::E;
     __shared__ Shared sh;
     clear_status_then_trigger(p.ws);
-    const int row = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
-    if (state_of(p, row) != kLive) return;
-    const T* x = static_cast<const T*>(p.logits) + static_cast<int64_t>(row) * p.stride;
-    // vectors start at 16-byte boundaries, the first in front of the row where that does not
-    const int head = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
-    const int vecs = (head + p.V + E - 1) / E;
-    const int v0 = slice * p.per, v1 = min(vecs, v0 + p.per);
-    auto load = [&](int v) {
-        const int i = v * E - head;
-        uint4 r;
-        if (v < v1 && i >= 0 && i + E <= p.V) {
-            const uint4* at = reinterpret_cast<const uint4*>(x + i);
-            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(at));
-        } else {                      // the row's ends, element by element
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                constexpr int P = E / 4;   // elements of a word
-                w[k] = 0;
-#pragma unroll
-                for (int h = 0; h < P; ++h) {
-                    const int e = i + k * P + h;
-                    const float val = v < v1 && e >= 0 && e < p.V ? to_f32<T>(x[e]) : -INFINITY;
-                    w[k] |= P == 1 ? __float_as_uint(val) : (__float_as_uint(val) >> 16) << (16 * h);
-                }
-            }
-            r = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        return r;
-    };
+    const int row_at = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Row<T> row(p, row_at);
+    const int v0 = slice * p.per;
+    if (slice + 1 < p.slices) row.end = min(row.end, v0 + p.per);
     if (threadIdx.x == 0) sh.count = 0;
     float m = -INFINITY, s = 0.f, thr = -INFINITY;
     int before = 0;
-    uint4 next[kVecs];
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) next[v] = load(v0 + v * kThreads + threadIdx.x);
+    bool live = true;
     __syncthreads();
-    for (int c = v0; c < v1; c += kVecs * kThreads) {
+#pragma unroll 1
+    for (int c = v0; c < row.end; c += kVecs * kThreads) {
         uint4 raw[kVecs];
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) raw[v] = next[v];
-        const int first = (c + static_cast<int>(threadIdx.x)) * E - head;   // of raw[v]: first + v * kThreads * E
-        if (c + kVecs * kThreads < v1) {
-#pragma unroll
-            for (int v = 0; v < kVecs; ++v) next[v] = load(c + (kVecs + v) * kThreads + threadIdx.x);
-        }
+        load_chunk(row, c, raw);
+        if (c == v0) live = state_of(p, row_at) == kLive;   // looked up while the first loads run
+        if (!live) return;
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) Vec<T>::clean(raw[v]);
-        const float top = Vec<T>::top(raw);
+        float tops[kVecs];
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) tops[v] = Vec<T>::top(raw[v]);
+        static_assert(kVecs == 4, "the maximum of a thread's vectors");
+        const float top = fmaxf(tc::fmax3(tops[0], tops[1], tops[2]), tops[3]);
         // the sum, rescaled to the larger maximum.  x - m is taken before the factor: with both in one
         // FMA the rounding of m log2(e) would shift every term the same way
         const float nm = fmaxf(m, top), ref = nm == -INFINITY ? 0.f : nm;
@@ -270,44 +295,55 @@ __global__ void __launch_bounds__(kThreads, 4) k_slices(const Params p) {
         tc::upk2(tc::fadd2(part[0], part[1]), s0, s1);
         s = s0 + s1;
         m = nm;
-        // the first chunk's bound: every warp has kq elements of at least its kq-th largest thread maximum
+        // the first chunk's bound: four warps have kq elements each of at least the fourth largest of the warps' kq-th largest
+        // thread maxima
         const bool begin = c == v0;
         float least = thr;
         if (begin) {
-            const unsigned k = warp_kth(order_key(top), (p.K + kWarps - 1) / kWarps);
-            if ((threadIdx.x & 31) == 0) sh.bound[threadIdx.x >> 5] = k;
+            const unsigned k = warp_kth(order_key(top), (p.K + 3) / 4);
+            if (lane == 0) sh.bound[warp] = k;
             __syncthreads();
-            unsigned low = sh.bound[0];
-            for (int i = 1; i < kWarps; ++i) low = min(low, sh.bound[i]);
-            least = low ? key_value(low) : -INFINITY;
+            const unsigned fourth = warp_kth(lane < kWarps ? sh.bound[lane] : 0u, 4);
+            least = fourth ? key_value(fourth) : -INFINITY;
         }
         auto passes = [&](float v) { return v > least || (begin && v == least && v > -INFINITY); };
-        if (passes(top)) {
+        bool any = false;
+        if (__any_sync(0xffffffffu, passes(top))) {
+            any = true;
 #pragma unroll
-            for (int v = 0; v < kVecs; ++v)
+            for (int v = 0; v < kVecs; ++v) {
+                if (!__any_sync(0xffffffffu, passes(tops[v]))) continue;
+                unsigned mask = 0;
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float val = Vec<T>::at(raw[v], e);
-                    if (passes(val)) {
-                        const int at = atomicAdd(&sh.count, 1);
-                        if (at < kCap) sh.cand[at] = make_key(val, first + v * kThreads * E + e);
-                    }
+                for (int e = 0; e < E; ++e)
+                    if (passes(Vec<T>::at(raw[v], e))) mask |= 1u << e;
+                // a thread's elements one after the other, the warp's together
+#pragma unroll 1
+                for (unsigned who; (who = __ballot_sync(0xffffffffu, mask != 0)) != 0; mask &= mask - 1) {
+                    const int e = __ffs(mask) - 1, k = E == 4 ? e : e >> 1;
+                    const uint32_t w = k & 2 ? (k & 1 ? raw[v].w : raw[v].z) : (k & 1 ? raw[v].y : raw[v].x);
+                    int at = 0;
+                    if (lane == 0) at = atomicAdd(&sh.count, __popc(who));
+                    at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
+                    if (mask && at < kCap)
+                        sh.cand[at] = make_key(__uint_as_float(E == 4 ? w : e & 1 ? w & 0xFFFF0000u : w << 16),
+                                               (c + v * kThreads + static_cast<int>(threadIdx.x)) * E - row.head + e);
                 }
+            }
         }
-        __syncthreads();
+        if (!__syncthreads_or(any)) continue;
         const int n = sh.count;
         __syncthreads();
-        if (n > kCap) thr = cut_chunk<T>(sh, raw, first, before, p.K);
+        if (n > kCap) thr = cut_chunk<T>(sh, row, c, before, p.K);
         else if (begin || n >= kFull) thr = cut(sh, n, p.K);
         before = sh.count;            // below kFull; a barrier lies between this and the next chunk's first candidate
         __syncthreads();
     }
     cut(sh, before, p.K);
-    const size_t out = static_cast<size_t>(row) * p.slices + slice;
+    const size_t out = static_cast<size_t>(row_at) * p.slices + slice;
     if (static_cast<int>(threadIdx.x) < p.K)
         p.cand[out * p.K + threadIdx.x] = static_cast<int>(threadIdx.x) < sh.count ? sh.cand[threadIdx.x] : 0ull;
     // the slice's maximum and sum
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float wm = warp_max(m);
     if (lane == 0) sh.fpart[warp] = wm;
     __syncthreads();
@@ -333,7 +369,8 @@ __device__ __forceinline__ unsigned long long order_key64(double v) {
 
 struct Entry {
     unsigned long long key;
-    uint32_t tie, at;                 // beam * V + token; the candidate's place
+    uint32_t tie;                     // beam * V + token
+    float x;                          // the logit
 };
 
 // log(x), x >= 1, to some 2^-25: logf of a mantissa near 1, where its error is that small, and the exponent's part.
@@ -344,151 +381,190 @@ __device__ __forceinline__ double log_parts(float x) {
     return e * 0.693147180559945309 + static_cast<double>(logf(f));
 }
 
+// n^-a to some 2^-40, n >= 1: n = 2^k f, log f by the series of artanh, e^r by its own; thirty 64-bit operations,
+// where pow() took 8 us of the join.
+__device__ __noinline__ double power(int n, float a) {
+    int k = 31 - __clz(n);
+    double f = static_cast<double>(n) * __longlong_as_double(static_cast<long long>(1023 - k) << 52);
+    if (f > 1.4142135623730951) { f *= 0.5; ++k; }
+    const double d = f + 1.0, r0 = static_cast<double>(1.f / static_cast<float>(d));
+    const double s = (f - 1.0) * (r0 * fma(-d, r0, 2.0)), z = s * s;
+    double l = 1.0 / 15;
+#pragma unroll
+    for (int i = 13; i >= 1; i -= 2) l = fma(l, z, 1.0 / i);
+    constexpr double kLn2 = 0.693147180559945309;
+    const double y = -static_cast<double>(a) * fma(static_cast<double>(k), kLn2, 2.0 * s * l);
+    const int e = __float2int_rn(static_cast<float>(y) * kLog2e);
+    const double r = fma(static_cast<double>(-e), kLn2, y);
+    double c = 1.0 / 479001600, v = c;   // 1 / 12!
+#pragma unroll
+    for (int i = 12; i >= 1; --i) {
+        c *= i;                       // 1 / (i - 1)!, at compile time
+        v = fma(v, r, c);
+    }
+    return v * __longlong_as_double(static_cast<long long>(1023 + e) << 52);   // e >= -700: n below 2^31, a at most 16
+}
+
 // Ranks are needed in 64 bits only of those near the K-th: this GPU does two 64-bit operations a clock and SM,
 // and a first pass in 32 bits leaves some tens of candidates (all of them in 64 bits: 15 us of 21
 // for 8 beams of 32000 tokens).  What depends on the call's inputs alone is worked out while the slices run.
+struct Join {
+    Entry list[kJoinCap];
+    double base[SPEC_MAX_BEAMS], inv[SPEC_MAX_BEAMS];   // score(t) = base + x; rank = score * inv
+    float basef[SPEC_MAX_BEAMS], invf[SPEC_MAX_BEAMS];
+    int state[SPEC_MAX_BEAMS], len[SPEC_MAX_BEAMS];
+    float bound[kWarps];
+    Entry top[kWarps];
+    int count;
+};
+
+__device__ __forceinline__ bool above(const Entry& x, const Entry& y) { return x.key > y.key || (x.key == y.key && x.tie < y.tie); }
+
+__device__ __forceinline__ Entry entry_of(const Join& sh, const Params& p, int w, unsigned long long k) {
+    const uint32_t token = sh.state[w] == kEnded ? static_cast<uint32_t>(p.eos) : ~static_cast<uint32_t>(k);
+    const float x = sh.state[w] == kEnded ? 0.f : key_value(static_cast<unsigned>(k >> 32));
+    return Entry{order_key64((sh.base[w] + x) * sh.inv[w]), static_cast<uint32_t>(w) * p.V + token, x};
+}
+
+__device__ __forceinline__ void write_pair(const Join& sh, const Params& p, int r, const Entry& e) {
+    const int w = e.tie / p.V, token = e.tie - static_cast<uint32_t>(w) * p.V;
+    const size_t o = static_cast<size_t>(blockIdx.x) * p.K + r;
+    p.score[o] = static_cast<float>(sh.base[w] + e.x);
+    p.token[o] = token;
+    p.parent[o] = w;
+    if (p.ended_out) p.ended_out[o] = sh.state[w] == kEnded || token == p.eos;
+    if (p.length_out) p.length_out[o] = sh.len[w];
+}
+
+// Many equal ranks: the best one after the other; returns how many there were.
+__device__ __noinline__ int join_slowly(Join& sh, const Params& p, const unsigned long long* cand, int per, int n) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Entry last{~0ull, 0, 0.f};
+    for (int r = 0; r < p.K; ++r) {
+        Entry best{0, 0, 0.f};
+        for (int c = threadIdx.x; c < n; c += kThreads) {
+            const int w = c / per;
+            const unsigned long long k = sh.state[w] == kLive ? cand[c] : 0;
+            if (!(sh.state[w] == kLive ? k != 0 : sh.state[w] == kEnded && c == w * per)) continue;
+            const Entry e = entry_of(sh, p, w, k);
+            if ((r == 0 || above(last, e)) && (!best.key || above(e, best))) best = e;
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            Entry other;
+            other.key = __shfl_xor_sync(0xffffffffu, best.key, o);
+            other.tie = __shfl_xor_sync(0xffffffffu, best.tie, o);
+            other.x = __shfl_xor_sync(0xffffffffu, best.x, o);
+            if (other.key && (!best.key || above(other, best))) best = other;
+        }
+        if (lane == 0) sh.top[warp] = best;
+        __syncthreads();
+        best = sh.top[0];
+        for (int i = 1; i < kWarps; ++i)
+            if (sh.top[i].key && (!best.key || above(sh.top[i], best))) best = sh.top[i];
+        __syncthreads();
+        if (!best.key) return r;
+        if (threadIdx.x == 0) write_pair(sh, p, r, best);
+        last = best;
+    }
+    return p.K;
+}
+
 __global__ void __launch_bounds__(kThreads) k_join(const Params p) {
-    __shared__ Entry list[kJoinCap];
-    __shared__ double s_base[SPEC_MAX_BEAMS], s_inv[SPEC_MAX_BEAMS];   // score(t) = base + x; rank = score * inv
-    __shared__ float s_basef[SPEC_MAX_BEAMS], s_invf[SPEC_MAX_BEAMS];
-    __shared__ int s_state[SPEC_MAX_BEAMS], s_len[SPEC_MAX_BEAMS];
-    __shared__ float s_bound[kWarps];
-    __shared__ Entry s_top[kWarps];
-    __shared__ int s_count;
+    __shared__ Join sh;
+    constexpr int kKeep = 4;          // candidates a thread has in registers; the rest is read twice
     const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.slices, K = p.K;
-    if (threadIdx.x == 0) s_count = 0;
-    if (threadIdx.x < p.W) {
+    const int per = S * K, n = p.W * per;
+    const unsigned long long* cand = p.cand + static_cast<size_t>(b) * n;
+    if (threadIdx.x == 0) sh.count = 0;
+    if (static_cast<int>(threadIdx.x) < p.W) {
         const int w = threadIdx.x, row = b * p.W + w;
         const State st = state_of(p, row);
         const int len = (p.length ? p.length[row] : 0) + (st == kLive ? 1 : 0);
-        s_state[w] = st;
-        s_len[w] = len;
-        s_base[w] = st == kDead ? 0.0 : static_cast<double>(p.scores[row]);
-        s_inv[w] = p.alpha != 0.f ? pow(static_cast<double>(max(len, 1)), -static_cast<double>(p.alpha)) : 1.0;
+        sh.state[w] = st;
+        sh.len[w] = len;
+        sh.base[w] = st == kDead ? 0.0 : static_cast<double>(p.scores[row]);
+        sh.inv[w] = p.alpha != 0.f ? power(max(len, 1), p.alpha) : 1.0;
+    }
+    griddep_wait();
+    unsigned long long kept[kKeep];   // on their way beside the sums
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+        const int c = threadIdx.x + i * kThreads;
+        kept[i] = c < n ? cand[c] : 0;
     }
     __syncthreads();
-    griddep_wait();
     float size = 0.f;                 // the largest |base| of the warp's rows
     for (int w = warp; w < p.W; w += kWarps) {
-        if (s_state[w] == kLive) {
+        if (sh.state[w] == kLive) {
             const float2 ms = lane < S ? p.sums[(static_cast<size_t>(b) * p.W + w) * S + lane] : make_float2(-INFINITY, 0.f);
             const float M = warp_max(ms.x);
             const float sum = warp_sum(isfinite(ms.x) ? ms.y * exp2f((ms.x - M) * kLog2e) : 0.f);
             if (lane == 0) {
                 if (!isfinite(M)) {   // nothing but -inf, or a logit of +inf
-                    s_state[w] = kDead;
+                    sh.state[w] = kDead;
                     if (M > 0.f) flag_status(p.ws, SPEC_EINVAL);
                 } else {
-                    s_base[w] -= M + log_parts(sum);
+                    sh.base[w] -= M + log_parts(sum);
                 }
             }
         }
         if (lane == 0) {
-            s_basef[w] = static_cast<float>(s_base[w]);
-            s_invf[w] = static_cast<float>(s_inv[w]);
+            sh.basef[w] = static_cast<float>(sh.base[w]);
+            sh.invf[w] = static_cast<float>(sh.inv[w]);
         }
         __syncwarp();
-        if (s_state[w] != kDead) size = fmaxf(size, fabsf(s_basef[w]));
+        if (sh.state[w] != kDead) size = fmaxf(size, fabsf(sh.basef[w]));
     }
-    if (lane == 0) s_bound[warp] = size;
+    if (lane == 0) sh.bound[warp] = size;
     __syncthreads();
-    for (int i = 0; i < kWarps; ++i) size = fmaxf(size, s_bound[i]);
-    const int per = S * K, n = p.W * per;
-    const unsigned long long* cand = p.cand + static_cast<size_t>(b) * n;
-    auto some_at = [&](int c, int w, float& x, uint32_t& token) {
-        if (s_state[w] == kEnded) {
-            token = p.eos;
-            x = 0.f;
-            return c == w * per;
-        }
-        if (s_state[w] != kLive) return false;
-        const unsigned long long k = cand[c];
-        token = ~static_cast<uint32_t>(k);
-        x = key_value(static_cast<unsigned>(k >> 32));
-        return k != 0;
-    };
-    auto near_rank = [&](int c) {     // -inf: no pair
-        const int w = c / per;
-        float x;
-        uint32_t token;
-        return some_at(c, w, x, token) ? (s_basef[w] + x) * s_invf[w] : -INFINITY;
-    };
-    auto entry_at = [&](int c) {
-        const int w = c / per;
-        float x;
-        uint32_t token;
-        if (!some_at(c, w, x, token)) return Entry{0, 0, 0};
-        return Entry{order_key64((s_base[w] + x) * s_inv[w]), static_cast<uint32_t>(w) * p.V + token, static_cast<uint32_t>(c)};
-    };
-    auto above = [](const Entry& x, const Entry& y) { return x.key > y.key || (x.key == y.key && x.tie < y.tie); };
-    auto write = [&](int r, const Entry& e) {
-        const int w = e.tie / p.V;
-        float x;
-        uint32_t token;
-        some_at(e.at, w, x, token);
-        const size_t o = static_cast<size_t>(b) * K + r;
-        p.score[o] = static_cast<float>(s_base[w] + x);
-        p.token[o] = token;
-        p.parent[o] = w;
-        if (p.ended_out) p.ended_out[o] = s_state[w] == kEnded || static_cast<int>(token) == p.eos;
-        if (p.length_out) p.length_out[o] = s_len[w];
+    for (int i = 0; i < kWarps; ++i) size = fmaxf(size, sh.bound[i]);
+    // c / per by the reciprocal, rounded up: exact, as n * per is below 2^32
+    const uint32_t inverse = per > 1 ? static_cast<uint32_t>(0xffffffffu / per + 1) : 0u;
+    auto beam_of = [&](int c) { return per > 1 ? static_cast<int>(__umulhi(static_cast<uint32_t>(c), inverse)) : c; };
+    auto near_rank = [&](int c, unsigned long long k) {     // in 32 bits; -inf: no pair
+        if (c >= n) return -INFINITY;
+        const int w = beam_of(c), st = sh.state[w];
+        if (!(st == kLive ? k != 0 : st == kEnded && c == w * per)) return -INFINITY;
+        return (sh.basef[w] + (st == kEnded ? 0.f : key_value(static_cast<unsigned>(k >> 32)))) * sh.invf[w];
     };
     // a bound as in the slices, lowered by what 32 bits can be off: four roundings of |base| + |x|, |x| <= |base| + |rank| / inv
-    float mine = -INFINITY;
-    for (int c = threadIdx.x; c < n; c += kThreads) mine = fmaxf(mine, near_rank(c));
-    const unsigned kth = warp_kth(mine == -INFINITY ? 0u : order_key(mine), (K + kWarps - 1) / kWarps);
-    __syncthreads();                  // s_bound has been read
-    if (lane == 0) s_bound[warp] = kth ? key_value(kth) : -INFINITY;
+    float near[kKeep], mine = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) mine = fmaxf(mine, near[i] = near_rank(threadIdx.x + i * kThreads, kept[i]));
+    for (int c = threadIdx.x + kKeep * kThreads; c < n; c += kThreads) mine = fmaxf(mine, near_rank(c, cand[c]));
+    const unsigned kth = warp_kth(mine == -INFINITY ? 0u : order_key(mine), (K + 3) / 4);
+    __syncthreads();                  // sh.bound has been read
+    if (lane == 0) sh.bound[warp] = __uint_as_float(kth);
     __syncthreads();
-    float low = s_bound[0];
-    for (int i = 1; i < kWarps; ++i) low = fminf(low, s_bound[i]);
+    const unsigned fourth = warp_kth(lane < kWarps ? __float_as_uint(sh.bound[lane]) : 0u, 4);
+    float low = fourth ? key_value(fourth) : -INFINITY;
     low -= 2e-6f * (fabsf(low) + size);
-    for (int c = threadIdx.x; c < n; c += kThreads) {
-        const float r = near_rank(c);
+    auto offer = [&](int c, unsigned long long k, float r) {
         if (r > -INFINITY && !(r < low)) {
-            const int at = atomicAdd(&s_count, 1);
-            if (at < kJoinCap) list[at] = entry_at(c);
+            const int at = atomicAdd(&sh.count, 1);
+            if (at < kJoinCap) sh.list[at] = entry_of(sh, p, beam_of(c), k);
         }
+    };
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) offer(threadIdx.x + i * kThreads, kept[i], near[i]);
+    for (int c = threadIdx.x + kKeep * kThreads; c < n; c += kThreads) {
+        const unsigned long long k = cand[c];
+        offer(c, k, near_rank(c, k));
     }
     __syncthreads();
-    const int m = s_count;
+    const int m = sh.count;
     int written = min(m, K);
     if (m <= kJoinCap) {
         for (int i = threadIdx.x; i < m; i += kThreads) {
-            const Entry e = list[i];
+            const Entry e = sh.list[i];
             int rank = 0;
 #pragma unroll 4
-            for (int j = 0; j < m; ++j) rank += above(list[j], e);
-            if (rank < K) write(rank, e);
+            for (int j = 0; j < m; ++j) rank += above(sh.list[j], e);
+            if (rank < K) write_pair(sh, p, rank, e);
         }
-    } else {                          // many equal ranks: one after the other
-        Entry last{~0ull, 0, 0};
-        bool any = true;
-        for (written = 0; written < K && any; ++written) {
-            Entry best{0, 0, 0};
-            for (int c = threadIdx.x; c < n; c += kThreads) {
-                const Entry e = entry_at(c);
-                if (e.key && (written == 0 || above(last, e)) && (!best.key || above(e, best))) best = e;
-            }
-            for (int o = 16; o > 0; o >>= 1) {
-                Entry other;
-                other.key = __shfl_xor_sync(0xffffffffu, best.key, o);
-                other.tie = __shfl_xor_sync(0xffffffffu, best.tie, o);
-                other.at = __shfl_xor_sync(0xffffffffu, best.at, o);
-                if (other.key && (!best.key || above(other, best))) best = other;
-            }
-            if (lane == 0) s_top[warp] = best;
-            __syncthreads();
-            best = s_top[0];
-            for (int i = 1; i < kWarps; ++i)
-                if (s_top[i].key && (!best.key || above(s_top[i], best))) best = s_top[i];
-            any = best.key != 0;
-            if (!any) break;
-            if (threadIdx.x == 0) write(written, best);
-            last = best;
-            __syncthreads();
-        }
+    } else {
+        written = join_slowly(sh, p, cand, per, n);
     }
     for (int r = written + threadIdx.x; r < K; r += kThreads) {
         const size_t o = static_cast<size_t>(b) * K + r;
@@ -499,15 +575,21 @@ __global__ void __launch_bounds__(kThreads) k_join(const Params p) {
     }
 }
 
-// Slices of a row.  Four CTAs fit an SM.  Where there is less than that of work they are as short as 2048
-// logits; else there are four rounds of them, so that the last one's gaps cost little, but none
-// shorter than 8192, whose start and end cost as much as the rest.
-int slices_of(int64_t rows, int V) {
-    const int64_t slots = 4 * device_sm_count();
-    const int64_t finest = (static_cast<int64_t>(V) + 2047) / 2048, fine = (static_cast<int64_t>(V) + 8191) / 8192;
-    const int64_t once = (slots + rows - 1) / rows, rounds = (4 * slots + rows - 1) / rows;
-    const int64_t s = std::max(std::min(once, finest), std::min(rounds, fine));
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s, kMaxSlices)));
+// Slices of a row: the number that makes the longest SM's work least, in units of a chunk.  A slice's start and end
+// cost some three and a half chunks, a candidate in the join a two-thousandth.
+int slices_of(int64_t rows, int W, int V, int K) {
+    const int64_t sms = device_sm_count();
+    const double chunks = V / static_cast<double>(kThreads * kVecs * 8);
+    int best = 1;
+    double least = 1e300;
+    for (int s = 1; s <= kMaxSlices; ++s) {
+        const double cost = static_cast<double>((rows * s + sms - 1) / sms) * (3.5 + chunks / s) + 5e-4 * s * K * W;
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
 }
 
 spec_status check_sizes(int B, int W, int V, int K) {
@@ -538,7 +620,7 @@ using namespace spec;
 extern "C" size_t beam_select_workspace_size(int32_t B, int32_t W, int32_t V, int32_t K) {
     clear_error();
     if (beam::check_sizes(B, W, V, K) != SPEC_OK) return 0;
-    return beam::bytes_for(B, W, K, beam::slices_of(static_cast<int64_t>(B) * W, V));
+    return beam::bytes_for(B, W, K, beam::slices_of(static_cast<int64_t>(B) * W, W, V, K));
 }
 
 extern "C" spec_status beam_select(const void* logits, int64_t row_stride, const float* scores, const int32_t* ended,
@@ -574,7 +656,7 @@ extern "C" spec_status beam_select(const void* logits, int64_t row_stride, const
             if (j > i && outs[j] && beam::overlap(outs[i], out, outs[j], out)) return fail(SPEC_EINVAL, "outputs overlap");
         }
     }
-    const int S = beam::slices_of(rows, V);
+    const int S = beam::slices_of(rows, W, V, K);
     const size_t need = beam::bytes_for(B, W, K, S);
     if (!ws || ws_bytes < need) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     if (!aligned16(ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
@@ -582,7 +664,8 @@ extern "C" spec_status beam_select(const void* logits, int64_t row_stride, const
     p.logits = logits; p.stride = row_stride; p.scores = scores; p.ended = ended; p.length = length;
     p.B = B; p.W = W; p.V = V; p.K = K; p.eos = eos; p.slices = S; p.alpha = alpha;
     const int E = 16 / es;
-    p.per = (V / E + 2 + S - 1) / S;   // a row's vectors and one more at each end where it starts inside one
+    // whole rounds of the CTA's threads; the last slice takes what is left, one vector more where the row starts inside one
+    p.per = static_cast<int>(round_up((V + static_cast<size_t>(S) * E - 1) / (static_cast<size_t>(S) * E), beam::kThreads));
     char* at = static_cast<char*>(ws) + kWsHeader;
     p.cand = reinterpret_cast<unsigned long long*>(at);
     p.sums = reinterpret_cast<float2*>(at + beam::cand_bytes(rows, K, S));
