@@ -26,9 +26,8 @@ namespace beam {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVecs = 4;              // 16-byte loads of a thread and chunk
-constexpr int kPerSm = 5;             // CTAs of an SM: its loads in flight come from the others while one works
+constexpr int kPerSm = 6;             // CTAs of an SM: loads in flight come from the others while one works
 constexpr int kCap = 1024;            // candidates a slice holds at most
-constexpr int kFull = 256;            // from here on they are cut down to K
 constexpr int kMaxSlices = 32;        // one lane each in the join
 constexpr int kJoinCap = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -178,6 +177,14 @@ template <typename T> __device__ __forceinline__ void load_chunk(const Row<T>& r
     constexpr int E = Vec<T>::E;
     constexpr uint32_t kNone = E == 4 ? 0xFF800000u : 0xFF80FF80u;   // -inf
     const int v0 = c + static_cast<int>(threadIdx.x);
+    if (c > 0 && c + kVecs * kThreads <= row.end && (c + kVecs * kThreads) * E - row.head <= row.V) {   // inside the row
+        const T* at = row.x + (v0 * E - row.head);
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(raw[v].x), "=r"(raw[v].y), "=r"(raw[v].z), "=r"(raw[v].w) : "l"(at + v * kThreads * E));
+        return;
+    }
     bool part[kVecs];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
@@ -194,8 +201,8 @@ template <typename T> __device__ __forceinline__ void load_chunk(const Row<T>& r
         if (part[v]) raw[v] = load_end<T>(row.x, row.V, (v0 + v * kThreads) * E - row.head);
 }
 
-// More elements of one chunk pass the threshold than the list holds (rows of equal logits, logits that rise with
-// the token): the K largest of cand[0 .. before) and the chunk by bisection, over the order of the logits, then of the tokens.
+// More elements pass the threshold than the list holds (rows of equal logits, logits that rise with the token): the K
+// largest of cand[0 .. before), at most K, and one chunk by bisection, over the order of the logits, then of the tokens.
 template <typename T>
 __device__ __noinline__ float cut_chunk(Shared& sh, const Row<T>& row, int c, int before, int K) {
     constexpr int E = Vec<T>::E;
@@ -204,7 +211,7 @@ __device__ __noinline__ float cut_chunk(Shared& sh, const Row<T>& row, int c, in
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) Vec<T>::clean(raw[v]);
     const int first = (c + static_cast<int>(threadIdx.x)) * E - row.head;
-    const unsigned long long mine = static_cast<int>(threadIdx.x) < before ? sh.cand[threadIdx.x] : 0;   // before < kFull
+    const unsigned long long mine = static_cast<int>(threadIdx.x) < before ? sh.cand[threadIdx.x] : 0;   // before is below kThreads
     const unsigned none = order_key(-INFINITY);
     int turn = 0;
     auto count = [&](auto&& test) {
@@ -223,7 +230,7 @@ __device__ __noinline__ float cut_chunk(Shared& sh, const Row<T>& row, int c, in
         const unsigned mid = lo + (hi - lo) / 2 + 1;
         if (count([&](unsigned k, int) { return k >= mid; }) >= K) lo = mid; else hi = mid - 1;
     }
-    const unsigned t = lo;
+    const unsigned t = lo;            // or all there are, if fewer than K
     const int need = K - count([&](unsigned k, int) { return k > t; });
     int from = 0, to = 0x7fffffff;                        // the lowest token by which `need` of the equal ones have come
     while (from < to) {
@@ -244,10 +251,11 @@ __device__ __noinline__ float cut_chunk(Shared& sh, const Row<T>& row, int c, in
             if (order_key(x) > none && keep(order_key(x), first + v * kThreads * E + e)) add(make_key(x, first + v * kThreads * E + e));
         }
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) < K) sh.cand[threadIdx.x] = sh.best[threadIdx.x];
-    if (threadIdx.x == 0) sh.count = K;
+    const int kept = sh.kept;
+    if (static_cast<int>(threadIdx.x) < kept) sh.cand[threadIdx.x] = sh.best[threadIdx.x];
+    if (threadIdx.x == 0) sh.count = kept;
     __syncthreads();
-    return key_value(t);
+    return kept < K ? -INFINITY : key_value(t);
 }
 
 template <typename T>
@@ -261,62 +269,62 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_slices(const Params p) {
     const int v0 = slice * p.per;
     if (slice + 1 < p.slices) row.end = min(row.end, v0 + p.per);
     if (threadIdx.x == 0) sh.count = 0;
-    float m = -INFINITY, s = 0.f, thr = -INFINITY;
+    float m = -INFINITY, s = 0.f, least = -INFINITY;   // logits above `least` are candidates
     int before = 0;
-    bool live = true;
     __syncthreads();
+    // One chunk, then stretches twice as long as all before: each lets some K candidates through, and the warps run free within it.
+    constexpr int kStep = kVecs * kThreads;
+    int c = v0;
 #pragma unroll 1
-    for (int c = v0; c < row.end; c += kVecs * kThreads) {
-        uint4 raw[kVecs];
-        load_chunk(row, c, raw);
-        if (c == v0) live = state_of(p, row_at) == kLive;   // looked up while the first loads run
-        if (!live) return;
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) Vec<T>::clean(raw[v]);
-        float tops[kVecs];
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) tops[v] = Vec<T>::top(raw[v]);
-        static_assert(kVecs == 4, "the maximum of a thread's vectors");
-        const float top = fmaxf(tc::fmax3(tops[0], tops[1], tops[2]), tops[3]);
-        // the sum, rescaled to the larger maximum.  x - m is taken before the factor: with both in one
-        // FMA the rounding of m log2(e) would shift every term the same way
-        const float nm = fmaxf(m, top), ref = nm == -INFINITY ? 0.f : nm;
-        const unsigned long long nref = tc::pk2(-ref, -ref), factor = tc::pk2(kLog2e, kLog2e);
-        unsigned long long part[2] = {tc::pk2(s * tc::ex2((m - ref) * kLog2e), 0.f), tc::pk2(0.f, 0.f)};
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v)
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                float a, b;
-                tc::upk2(fmul2(tc::fadd2(tc::pk2(Vec<T>::at(raw[v], e), Vec<T>::at(raw[v], e + 1)), nref), factor), a, b);
-                part[(e / 2) & 1] = tc::fadd2(part[(e / 2) & 1], tc::pk2(tc::ex2(a), tc::ex2(b)));
-            }
-        float s0, s1;
-        tc::upk2(tc::fadd2(part[0], part[1]), s0, s1);
-        s = s0 + s1;
-        m = nm;
-        // the first chunk's bound: four warps have kq elements each of at least the fourth largest of the warps' kq-th largest
-        // thread maxima
-        const bool begin = c == v0;
-        float least = thr;
-        if (begin) {
-            const unsigned k = warp_kth(order_key(top), (p.K + 3) / 4);
-            if (lane == 0) sh.bound[warp] = k;
-            __syncthreads();
-            const unsigned fourth = warp_kth(lane < kWarps ? sh.bound[lane] : 0u, 4);
-            least = fourth ? key_value(fourth) : -INFINITY;
-        }
-        auto passes = [&](float v) { return v > least || (begin && v == least && v > -INFINITY); };
-        bool any = false;
-        if (__any_sync(0xffffffffu, passes(top))) {
-            any = true;
+    for (int64_t len = kStep; c < row.end; len = c - v0) {
+        const int c0 = c, c1 = static_cast<int>(min(static_cast<int64_t>(row.end), c0 + len));
+#pragma unroll 1
+        for (; c < c1; c += kStep) {
+            uint4 raw[kVecs];
+            load_chunk(row, c, raw);
+            if (c == v0 && state_of(p, row_at) != kLive) return;   // looked up while the first loads run
+            float tops[kVecs];
 #pragma unroll
             for (int v = 0; v < kVecs; ++v) {
-                if (!__any_sync(0xffffffffu, passes(tops[v]))) continue;
+                Vec<T>::clean(raw[v]);
+                tops[v] = Vec<T>::top(raw[v]);
+            }
+            static_assert(kVecs == 4, "the maximum of a thread's vectors");
+            const float top = fmaxf(tc::fmax3(tops[0], tops[1], tops[2]), tops[3]);
+            // the sum, rescaled to the larger maximum.  x - m is taken before the factor: with both in one
+            // FMA the rounding of m log2(e) would shift every term the same way
+            const float nm = fmaxf(m, top), ref = nm == -INFINITY ? 0.f : nm;
+            const unsigned long long nref = tc::pk2(-ref, -ref), factor = tc::pk2(kLog2e, kLog2e);
+            unsigned long long part[2] = {tc::pk2(s * tc::ex2((m - ref) * kLog2e), 0.f), tc::pk2(0.f, 0.f)};
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    float a, b;
+                    tc::upk2(fmul2(tc::fadd2(tc::pk2(Vec<T>::at(raw[v], e), Vec<T>::at(raw[v], e + 1)), nref), factor), a, b);
+                    part[(e / 2) & 1] = tc::fadd2(part[(e / 2) & 1], tc::pk2(tc::ex2(a), tc::ex2(b)));
+                }
+            float s0, s1;
+            tc::upk2(tc::fadd2(part[0], part[1]), s0, s1);
+            s = s0 + s1;
+            m = nm;
+            if (c == v0) {
+                // the first chunk's bound: four warps have kq elements each of at least the fourth largest of the warps' kq-th
+                // largest thread maxima; `least` lies one step below it
+                const unsigned k = warp_kth(order_key(top), (p.K + 3) / 4);
+                if (lane == 0) sh.bound[warp] = k;
+                __syncthreads();
+                const unsigned fourth = warp_kth(lane < kWarps ? sh.bound[lane] : 0u, 4);
+                if (fourth > order_key(-INFINITY)) least = key_value(fourth - (fourth == order_key(0.f) ? 2 : 1));   // (-0 is 0)
+            }
+            if (!__any_sync(0xffffffffu, top > least)) continue;
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                if (!__any_sync(0xffffffffu, tops[v] > least)) continue;
                 unsigned mask = 0;
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    if (passes(Vec<T>::at(raw[v], e))) mask |= 1u << e;
+                    if (Vec<T>::at(raw[v], e) > least) mask |= 1u << e;
                 // a thread's elements one after the other, the warp's together
 #pragma unroll 1
                 for (unsigned who; (who = __ballot_sync(0xffffffffu, mask != 0)) != 0; mask &= mask - 1) {
@@ -331,13 +339,22 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_slices(const Params p) {
                 }
             }
         }
-        if (!__syncthreads_or(any)) continue;
+        __syncthreads();
         const int n = sh.count;
         __syncthreads();
-        if (n > kCap) thr = cut_chunk<T>(sh, row, c, before, p.K);
-        else if (begin || n >= kFull) thr = cut(sh, n, p.K);
-        before = sh.count;            // below kFull; a barrier lies between this and the next chunk's first candidate
-        __syncthreads();
+        if (n > kCap) {               // too many: chunk by chunk, each time the K best of it and of those so far
+            if (threadIdx.x == 0) sh.count = before;
+            __syncthreads();
+            for (int d = c0; d < c1; d += kStep) {
+                least = cut_chunk<T>(sh, row, d, before, p.K);
+                before = sh.count;
+                __syncthreads();
+            }
+        } else if (n > before) {
+            least = cut(sh, n, p.K);
+            before = sh.count;
+            __syncthreads();
+        }
     }
     cut(sh, before, p.K);
     const size_t out = static_cast<size_t>(row_at) * p.slices + slice;
