@@ -10,14 +10,15 @@
 //   few   at most 256 query rows of a KV head (generated tokens, accepted paths, short chains; more in
 //         several passes): a head's rows stay in shared memory while its keys stream through a ring of
 //         128-key tiles.  Bound by the keys' bytes up to some 200 rows.
-//   many  prompts: a tile of keys stays while chunks of 128 query rows of one head stream through.
-//         Bound by the exponentials, one for each pair of row and key.
+//   many  prompts: 256 keys stay while chunks of 128 query rows of one head stream through, each chunk
+//         multiplied with both halves of the keys: with 128 keys a CTA the rows would come out of L2 at
+//         9 TB/s.  Bound by the exponentials, one for each pair of row and key.
 // The work, (sequence, head, key tile, chunk) in that order, is one line of chunks, cut into as
 // many equal parts as there are CTAs; lengths are known on the device only, so every CTA works its part
 // out itself.  A tile that is cut leaves partial sums, which kv_weigh_join adds up in order.
 //
 // One persistent CTA an SM, twelve warps:
-//   warps 0-3, 4-7   two groups that take alternate chunks (few: tiles), one thread per key
+//   warps 0-3, 4-7   two groups, one thread per key: of alternate tiles (few), of half a tile each (many)
 //   warp 8           TMA: key tiles, and the chunks of rows (many)
 //   warp 9           MMA, one thread
 //   warps 10, 11     gather a head's rows (few); lse of the rows (both)
@@ -34,8 +35,9 @@ namespace weigh {
 
 using namespace tc;
 
-constexpr int kTile = 128;            // keys of a tile
+constexpr int kKeys = 128;            // keys of a product
 constexpr int kChunk = 128;           // query rows of a chunk (many)
+template <bool MANY> constexpr int kTile = MANY ? 2 * kKeys : kKeys;   // keys of a tile
 constexpr int kMostRows = 256;        // query rows of a pass (few)
 constexpr int kTcThreads = 384;
 constexpr int kMaxStages = 8;
@@ -59,15 +61,15 @@ struct TcParams {
     int k_stages, q_stages, buffers;  // buffers of scores in TMEM
     int box;                          // keys of a load
     Record* records;                  // [CTAs] (many)
-    float* parts;                     // [CTAs][2][kTile]
+    float* parts;                     // [CTAs][2][2 * kKeys]
 };
 
 // Barriers and small arrays behind the operand stages.
 struct Small {
     uint64_t k_full[kMaxStages], k_empty[kMaxStages];
     uint64_t q_full[4], q_empty[4];
+    uint64_t l_full[4], l_empty[4];   // many: lse of a chunk's rows
     uint64_t s_full[4], s_empty[4];
-    uint64_t x_full[2], x_empty[2];
     uint64_t drain;
     uint32_t tmem;
     int abort_flag, bad;
@@ -75,23 +77,22 @@ struct Small {
     long long length;                 // its chunks
     __align__(16) float nl2[4][kMostRows];   // -lse log2 e of a stage's rows, -inf: does not count
     int last[4][kMostRows];           // few: the last key that a row sees
-    float cross[2][kTile];            // many: the second group's sums
 };
 
-// The line of chunks of one sequence and head: m(t) row chunks for tile t, times `mult` query heads.
+// The line of chunks of one sequence and head: row chunks first(t) .. C - 1 for tile t, times `mult` query heads.
 struct Head {
     int tiles, C, o, mult;
     __device__ __forceinline__ long long before(int t) const {   // chunks of the tiles in front of t
-        const long long k = max(0, t - 1 - o);
-        return (static_cast<long long>(C) * t - k * (k + 1) / 2) * mult;
+        const long long s = o / 2 + 1, k = max(0ll, t - s);      // the first tile that some chunks do not see
+        return (static_cast<long long>(C) * t - k * (s + t - 1 - o)) * mult;
     }
-    __device__ __forceinline__ int first(int t) const { return max(0, t - o); }      // first row chunk that sees tile t
+    __device__ __forceinline__ int first(int t) const { return max(0, 2 * t - o); }  // row (256 t - rows in front) / 128
     __device__ __forceinline__ int chunks(int t) const { return (C - first(t)) * mult; }
 };
 template <bool MANY> __device__ __forceinline__ Head head_of(const TcParams& tp, const Rows& r) {
     Head h{0, 1, 1 << 30, 1};
     if (!r.ok) return h;
-    h.tiles = (r.n + kTile - 1) / kTile;
+    h.tiles = (r.n + kTile<MANY> - 1) / kTile<MANY>;
     if (r.count == 0 && tp.p.decay == 1.f) h.tiles = 0;          // nothing changes
     if (MANY) {
         if (r.count > 0) {
@@ -226,6 +227,11 @@ template <bool MANY> __device__ void plan(const TcParams& tp, Small& sm) {
     }
 }
 
+// Whether no row of the chunk that begins at i0 sees a key of the half tile that begins at k0 (many).
+__device__ __forceinline__ bool unseen(const Rows& r, int k0, int i0) {
+    return k0 >= r.n || k0 > r.n - r.count + min(i0 + kChunk, r.count) - 1;
+}
+
 // 16 columns of a key's scores: the sum of their weights.
 __device__ __forceinline__ unsigned long long weights16(const uint32_t (&s)[16], const float* nl2, unsigned long long c2) {
     unsigned long long sum = pk2(0.f, 0.f), sum1 = pk2(0.f, 0.f);
@@ -241,16 +247,32 @@ __device__ __forceinline__ unsigned long long weights16(const uint32_t (&s)[16],
     return fadd2(sum, sum1);
 }
 
+__device__ __forceinline__ unsigned long long weights32(const uint32_t (&s)[32], const float* nl2, unsigned long long c2) {
+    unsigned long long sum[4] = {pk2(0.f, 0.f), pk2(0.f, 0.f), pk2(0.f, 0.f), pk2(0.f, 0.f)};
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(nl2 + e);
+        float a, b, c, d;
+        upk2(ffma2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, pk2(l.x, l.y)), a, b);
+        upk2(ffma2(pk2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, pk2(l.z, l.w)), c, d);
+        sum[(e / 2) & 3] = fadd2(sum[(e / 2) & 3], pk2(ex2(a), ex2(b)));
+        sum[(e / 2 + 1) & 3] = fadd2(sum[(e / 2 + 1) & 3], pk2(ex2(c), ex2(d)));
+    }
+    return fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+}
+
 template <int D, bool MANY>
 __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constant__ Maps mp, const TcParams tp) {
     constexpr int kH = D / 64;
-    constexpr int kKHalf = kTile * 128;                  // bytes of a 64-column half of a key tile
+    constexpr int kKHalf = kKeys * 128;                  // bytes of a 64-column half of 128 keys
+    constexpr int kHalves = MANY ? 2 : 1;                // 128 keys each
+    constexpr int kKStage = kHalves * kH * kKHalf;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     // the swizzle counts address bits: tiles start on 1024-byte boundaries
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const Params& p = tp.p;
     uint8_t* sK = smem;
-    uint8_t* sQ = sK + tp.k_stages * kH * kKHalf;
+    uint8_t* sQ = sK + tp.k_stages * kKStage;
     const int q_half = tp.nq * 128;
     Small& sm = *reinterpret_cast<Small*>(sQ + tp.q_stages * kH * q_half);
     volatile int* abort_flag = &sm.abort_flag;
@@ -261,14 +283,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
             mbar_init(&sm.k_empty[i], 1);
         }
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&sm.q_full[i], 2);
-            mbar_init(&sm.q_empty[i], MANY ? 5 : 9);
+            mbar_init(&sm.q_full[i], MANY ? 1 : 2);
+            mbar_init(&sm.q_empty[i], MANY ? 1 : 9);
+            mbar_init(&sm.l_full[i], 1);
+            mbar_init(&sm.l_empty[i], 8);
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_empty[i], 4);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.x_full[i], 4);
-            mbar_init(&sm.x_empty[i], 4);
         }
         mbar_init(&sm.drain, 1);
         sm.abort_flag = 0;
@@ -293,18 +313,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
         for (; ok && w.more; w.next()) {
             const int stage = k_loads % tp.k_stages;
             if (k_loads >= tp.k_stages && !(ok = warp_wait_for(&sm.k_empty[stage], (k_loads / tp.k_stages - 1) & 1, abort_flag))) break;
-            uint8_t* dst = sK + stage * kH * kKHalf;
-            const int k0 = w.t * kTile;
+            uint8_t* dst = sK + stage * kKStage;
+            const int k0 = w.t * kTile<MANY>;
             // a lane per load of `box` keys; what lies behind the length, or in a block outside the pool, is left out
-            const int at = k0 + lane * tp.box;
+            const int in = lane * tp.box, at = k0 + in;
             int64_t row = -1;
-            if (lane < kTile / tp.box && at < w.rows.n) row = key_row(p, w.b, w.h, at);
+            if (in < kTile<MANY> && at < w.rows.n) row = key_row(p, w.b, w.h, at);
             const unsigned there = __ballot_sync(0xffffffffu, row >= 0);
             if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[stage], __popc(there) * tp.box * 128 * kH);
             __syncwarp();
             if (row >= 0)
                 for (int hh = 0; hh < kH; ++hh)
-                    tma_load_2d(dst + hh * kKHalf + lane * tp.box * 128, &mp.k, &sm.k_full[stage], hh * 64, static_cast<int>(row));
+                    tma_load_2d(dst + ((in / kKeys) * kH + hh) * kKHalf + in % kKeys * 128, &mp.k, &sm.k_full[stage], hh * 64, static_cast<int>(row));
             ++k_loads;
             if (MANY) {
                 const int m = w.head.chunks(w.t) / w.head.mult, c0 = w.head.first(w.t);
@@ -326,24 +346,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
         // ------------------------------------------------ products
         if (lane == 0) {
             int kt = 0, u = 0, col = 0;
+            int units[2] = {0, 0};    // many: products of each half so far
             for (; ok && w.more; w.next(), ++kt) {
                 const int ks = kt % tp.k_stages;
                 if (!(ok = wait_for(&sm.k_full[ks], (kt / tp.k_stages) & 1, abort_flag))) break;
-                const uint32_t ka = smem_u32(sK + ks * kH * kKHalf);
-                const int n = MANY ? kChunk : min(tp.nq, (tp.g * w.rows.count - tp.row0 + 15) / 16 * 16);
-                const uint32_t idesc = idesc_bf16_f32(kTile, MANY ? kChunk : max(n, 16));
-                for (int c = 0; c < w.take; ++c, ++u) {
+                const uint32_t ka = smem_u32(sK + ks * kKStage);
+                const int n = MANY ? kChunk : max(16, min(tp.nq, (tp.g * w.rows.count - tp.row0 + 15) / 16 * 16));
+                const uint32_t idesc = idesc_bf16_f32(kKeys, n);
+                const int m = MANY ? w.head.chunks(w.t) / w.head.mult : 1, c0 = MANY ? w.head.first(w.t) : 0;
+                for (int c = w.c; c < w.c + w.take; ++c, ++u) {
                     const int qn = MANY ? u : col;
-                    const int qs = qn % tp.q_stages, buf = u % tp.buffers;
+                    const int qs = qn % tp.q_stages;
                     if (!(ok = wait_for(&sm.q_full[qs], (qn / tp.q_stages) & 1, abort_flag))) break;
-                    if (u >= tp.buffers && !(ok = wait_for(&sm.s_empty[buf], (u / tp.buffers - 1) & 1, abort_flag))) break;
-                    tc_fence_after();
                     const uint32_t qa = smem_u32(sQ + qs * kH * q_half);
+                    for (int half = 0; half < kHalves; ++half) {
+                        if (MANY && unseen(w.rows, w.t * kTile<MANY> + half * kKeys, (c0 + c % m) * kChunk)) continue;
+                        // many: two buffers for each half; few: tiles take all of them in turn
+                        const int use = MANY ? units[half]++ : u;
+                        const int buf = MANY ? 2 * half + (use & 1) : use % tp.buffers, round = MANY ? use >> 1 : use / tp.buffers;
+                        if (round > 0 && !(ok = wait_for(&sm.s_empty[buf], (round - 1) & 1, abort_flag))) break;
+                        tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_bf16(tmem + buf * buf_cols, sdesc_k128(ka + (k / 4) * kKHalf + (k % 4) * 32),
-                                 sdesc_k128(qa + (k / 4) * q_half + (k % 4) * 32), idesc, k > 0);
-                    mma_commit(&sm.s_full[buf]);
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_bf16(tmem + buf * buf_cols, sdesc_k128(ka + (half * kH + k / 4) * kKHalf + (k % 4) * 32),
+                                     sdesc_k128(qa + (k / 4) * q_half + (k % 4) * 32), idesc, k > 0);
+                        mma_commit(&sm.s_full[buf]);
+                    }
+                    if (!ok) break;
                     if (MANY) mma_commit(&sm.q_empty[qs]);
                 }
                 if (!ok) break;
@@ -362,7 +391,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                 for (; ok && w.more; w.next()) {
                     const int m = w.head.chunks(w.t) / w.head.mult, c0 = w.head.first(w.t);
                     for (int c = w.c; c < w.c + w.take; ++c, ++u) {
-                        const int qs = u % tp.q_stages;
+                        const int ls = u & 3;
                         const int qh = w.h * tp.g + c / m, i0 = (c0 + c % m) * kChunk;
                         float x[4];
                         for (int e = 0; e < 4; ++e) {
@@ -370,11 +399,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                             x[e] = INFINITY;
                             if (i < w.rows.count) x[e] = p.lse[static_cast<int64_t>(w.b * p.Hq + qh) * p.T + i];
                         }
-                        if (u >= tp.q_stages && !(ok = warp_wait_for(&sm.q_empty[qs], (u / tp.q_stages - 1) & 1, abort_flag))) break;
+                        if (u >= 4 && !(ok = warp_wait_for(&sm.l_empty[ls], (u / 4 - 1) & 1, abort_flag))) break;
                         for (int e = 0; e < 4; ++e) x[e] = isfinite(x[e]) ? -x[e] * kL2e : -INFINITY;
-                        *reinterpret_cast<float4*>(&sm.nl2[qs][lane * 4]) = make_float4(x[0], x[1], x[2], x[3]);
+                        *reinterpret_cast<float4*>(&sm.nl2[ls][lane * 4]) = make_float4(x[0], x[1], x[2], x[3]);
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.q_full[qs]);
+                        if (lane == 0) mbar_arrive(&sm.l_full[ls]);
                     }
                 }
         } else {
@@ -447,119 +476,110 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
         }
         const unsigned long long c2 = pk2(p.scale * kL2e, p.scale * kL2e);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        int u = 0, kt = 0, col = 0;
+        int u = 0, kt = 0, col = 0, use = 0;
         for (; ok && w.more; w.next(), ++kt) {
-            const int k0 = w.t * kTile, j = k0 + key;
-            const bool writes = MANY ? grp == 0 : (kt & 1) == grp;
+            const bool mine = MANY || (kt & 1) == grp;
+            const int k0 = w.t * kTile<MANY> + (MANY ? grp * kKeys : 0), j = k0 + key;   // of the group; of the thread
+            const int in_front = w.rows.n - w.rows.count;
             // what the key has so far, on its way while the products run
-            const bool mine = writes && j < w.rows.n && (!p.table || key_row(p, w.b, w.h, j) >= 0);
+            const bool there = mine && j < w.rows.n && (!p.table || key_row(p, w.b, w.h, j) >= 0);
             const int64_t at = (static_cast<int64_t>(w.b) * p.Hkv + w.h) * p.cap + j;
-            const bool fresh = j >= w.rows.n - w.rows.count;
+            const bool fresh = j >= in_front;
             float old = 0.f;
-            if (mine && (!MANY || w.whole()) && (tp.row0 > 0 || (!fresh && p.decay != 0.f))) old = p.acc[at];
+            if (there && (!MANY || w.whole()) && (tp.row0 > 0 || (!fresh && p.decay != 0.f))) old = p.acc[at];
             float sum = 0.f;
             const int m = MANY ? w.head.chunks(w.t) / w.head.mult : 1, c0 = MANY ? w.head.first(w.t) : 0;
             for (int c = w.c; c < w.c + w.take; ++c, ++u) {
-                if (MANY ? (u & 1) != grp : !writes) continue;
-                const int qn = MANY ? u : col;
-                const int qs = qn % tp.q_stages, buf = u % tp.buffers;
-                if (!(ok = warp_wait_for(&sm.s_full[buf], (u / tp.buffers) & 1, abort_flag))) break;
-                if (!(ok = warp_wait_for(&sm.q_full[qs], (qn / tp.q_stages) & 1, abort_flag))) break;   // complete: for its lse
-                tc_fence_after();
-                const uint32_t s_addr = lane_base + buf * buf_cols;
-                const float* nl2 = sm.nl2[qs];
-                // columns that hold rows, and the first of them that sees the warp's keys
-                int cols, lo;
-                bool plain;
-                if (MANY) {
-                    const int i0 = (c0 + c % m) * kChunk;
-                    cols = min(kChunk, w.rows.count - i0);
-                    lo = j - (w.rows.n - w.rows.count) - i0;         // of this key
-                    plain = cols == kChunk && k0 + kTile - 1 - (w.rows.n - w.rows.count) <= i0;
-                } else {
-                    cols = min(tp.nq, tp.g * w.rows.count - tp.row0);
-                    lo = 0;
-                    plain = k0 + kTile - 1 <= w.rows.n - w.rows.count;
-                }
-                unsigned long long part = pk2(0.f, 0.f);
-                if (plain) {
-                    const int steps = MANY ? kChunk / 16 : max(1, (cols + 15) / 16);
-                    uint32_t r[2][16];
-                    tmem_ld16(s_addr, r[0]);
-#pragma unroll 1
-                    for (int x = 0; x < steps; x += 2) {
-                        tmem_ld_wait();
-                        if (x + 1 < steps) tmem_ld16(s_addr + 16 * (x + 1), r[1]);
-                        part = fadd2(part, weights16(r[0], nl2 + 16 * x, c2));
-                        if (x + 1 < steps) {
-                            tmem_ld_wait();
-                            if (x + 2 < steps) tmem_ld16(s_addr + 16 * (x + 2), r[0]);
-                            part = fadd2(part, weights16(r[1], nl2 + 16 * (x + 1), c2));
-                        }
-                    }
-                } else {
-                    float f0 = 0.f;
-#pragma unroll 1
-                    for (int x = 0; x < cols; x += 16) {
-                        uint32_t r[16];
-                        tmem_ld16(s_addr + x, r);
-                        tmem_ld_wait();
+                if (!mine) continue;
+                const int i0 = MANY ? (c0 + c % m) * kChunk : 0;
+                const int ls = MANY ? u & 3 : col % tp.q_stages;
+                // many: also where the group has no part in the chunk, or it would give back a later turn of the slot
+                // in place of this one
+                if (MANY && !(ok = warp_wait_for(&sm.l_full[ls], (u >> 2) & 1, abort_flag))) break;
+                if (!MANY || !unseen(w.rows, k0, i0)) {
+                    const int buf = MANY ? 2 * grp + (use & 1) : u % tp.buffers, round = MANY ? use >> 1 : u / tp.buffers;
+                    ++use;
+                    if (!MANY && !(ok = warp_wait_for(&sm.q_full[ls], (col / tp.q_stages) & 1, abort_flag))) break;
+                    if (!(ok = warp_wait_for(&sm.s_full[buf], round & 1, abort_flag))) break;
+                    tc_fence_after();
+                    const uint32_t s_addr = lane_base + buf * buf_cols;
+                    const float* nl2 = sm.nl2[ls];
+                    // columns that hold rows; whether all of them see all keys
+                    const int cols = MANY ? min(kChunk, w.rows.count - i0) : min(tp.nq, tp.g * w.rows.count - tp.row0);
+                    const bool plain = (!MANY || cols == kChunk) && k0 + kKeys - 1 <= in_front + i0;
+                    unsigned long long part = pk2(0.f, 0.f);
+                    if (plain && MANY) {
+                        uint32_t r[2][32];
+                        tmem_ld32(s_addr, r[0]);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float v = ex2(fmaf(__uint_as_float(r[e]), p.scale * kL2e, nl2[x + e]));
-                            const bool sees = MANY ? x + e >= lo && x + e < cols : x + e < cols && j <= sm.last[qs][x + e];
-                            f0 += sees ? v : 0.f;
+                        for (int x = 0; x < kChunk / 32; ++x) {
+                            tmem_ld_wait();
+                            if (x + 1 < kChunk / 32) tmem_ld32(s_addr + 32 * (x + 1), r[(x + 1) & 1]);
+                            part = fadd2(part, weights32(r[x & 1], nl2 + 32 * x, c2));
                         }
+                    } else if (plain) {
+                        const int steps = max(1, (cols + 15) / 16);
+                        uint32_t r[2][16];
+                        tmem_ld16(s_addr, r[0]);
+#pragma unroll 1
+                        for (int x = 0; x < steps; x += 2) {
+                            tmem_ld_wait();
+                            if (x + 1 < steps) tmem_ld16(s_addr + 16 * (x + 1), r[1]);
+                            part = fadd2(part, weights16(r[0], nl2 + 16 * x, c2));
+                            if (x + 1 < steps) {
+                                tmem_ld_wait();
+                                if (x + 2 < steps) tmem_ld16(s_addr + 16 * (x + 2), r[0]);
+                                part = fadd2(part, weights16(r[1], nl2 + 16 * (x + 1), c2));
+                            }
+                        }
+                    } else {
+                        const int lo = j - in_front - i0;            // many: the first column that sees this key
+                        float f0 = 0.f;
+#pragma unroll 1
+                        for (int x = 0; x < cols; x += 16) {
+                            uint32_t r[16];
+                            tmem_ld16(s_addr + x, r);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float v = ex2(fmaf(__uint_as_float(r[e]), p.scale * kL2e, nl2[x + e]));
+                                const bool sees = x + e < cols && (MANY ? x + e >= lo : j <= sm.last[ls][x + e]);
+                                f0 += sees ? v : 0.f;
+                            }
+                        }
+                        part = pk2(f0, 0.f);
                     }
-                    part = pk2(f0, 0.f);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.s_empty[buf]);
+                    float f0, f1;
+                    upk2(part, f0, f1);
+                    sum += f0 + f1;
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sm.s_empty[buf]);
-                    if (MANY) mbar_arrive(&sm.q_empty[qs]);
-                }
-                float f0, f1;
-                upk2(part, f0, f1);
-                sum += f0 + f1;
+                if (MANY && lane == 0) mbar_arrive(&sm.l_empty[ls]);
             }
             if (!ok) break;
-            if (MANY) {
-                // the groups' sums, through one of two buffers
-                const int x = kt & 1;
-                if (grp == 1) {
-                    if (kt >= 2 && !(ok = warp_wait_for(&sm.x_empty[x], (kt / 2 - 1) & 1, abort_flag))) break;
-                    sm.cross[x][key] = sum;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.x_full[x]);
-                } else {
-                    if (!(ok = warp_wait_for(&sm.x_full[x], (kt / 2) & 1, abort_flag))) break;
-                    sum += sm.cross[x][key];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.x_empty[x]);
-                }
-            } else if (w.column_ends()) {
-                __syncwarp();
+            if (!MANY && w.column_ends()) {
+                // (a group without a tile in this column waits for its rows all the same, as above)
+                if (!(ok = warp_wait_for(&sm.q_full[col % tp.q_stages], (col / tp.q_stages) & 1, abort_flag))) break;
                 if (lane == 0) mbar_arrive(&sm.q_empty[col % tp.q_stages]);
                 ++col;
             }
             if (MANY && !w.whole()) {
                 // a tile that another CTA has a part of: the join puts them together
                 const bool tail = w.c == 0;
-                if (grp == 0) {
-                    tp.parts[(static_cast<int64_t>(blockIdx.x) * 2 + tail) * kTile + key] = sum;
-                    if (threadIdx.x == 0) {
-                        Record& rec = tp.records[blockIdx.x];
-                        if (tail) {
-                            rec.tail = 1;
-                            rec.b = w.b; rec.h = w.h; rec.t = w.t;
-                        } else {
-                            rec.head = 1;
-                            rec.head_ends = w.c + w.take == w.head.chunks(w.t);
-                        }
+                tp.parts[(static_cast<int64_t>(blockIdx.x) * 2 + tail) * 2 * kKeys + grp * kKeys + key] = sum;
+                if (threadIdx.x == 0) {
+                    Record& rec = tp.records[blockIdx.x];
+                    if (tail) {
+                        rec.tail = 1;
+                        rec.b = w.b; rec.h = w.h; rec.t = w.t;
+                    } else {
+                        rec.head = 1;
+                        rec.head_ends = w.c + w.take == w.head.chunks(w.t);
                     }
                 }
-            } else if (mine) {
+            } else if (there) {
                 p.acc[at] = tp.row0 > 0 ? old + sum : fmaf(p.decay, old, sum);
                 if (fresh && p.pos && tp.row0 == 0) p.pos[at] = (p.seen ? p.seen[w.b] : w.rows.n) - w.rows.n + j;
             }
@@ -591,12 +611,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
 }
 
 // The tiles that were cut: the CTA in which one begins adds up its parts, in order.
-__global__ void __launch_bounds__(kTile) k_weigh_join(const TcParams tp, int ctas) {
+__global__ void __launch_bounds__(2 * kKeys) k_weigh_join(const TcParams tp, int ctas) {
     griddep_wait();
     const Record rec = tp.records[blockIdx.x];
     if (!rec.tail) return;
     const Params& p = tp.p;
-    float sum = tp.parts[(static_cast<int64_t>(blockIdx.x) * 2 + 1) * kTile + threadIdx.x];
+    float sum = tp.parts[(static_cast<int64_t>(blockIdx.x) * 2 + 1) * 2 * kKeys + threadIdx.x];
     int end = blockIdx.x + 1;         // one more than the CTA in which the tile ends, 32 records at a time
     for (; end < ctas; end += 32) {
         const int c = end + (threadIdx.x & 31);
@@ -608,9 +628,9 @@ __global__ void __launch_bounds__(kTile) k_weigh_join(const TcParams tp, int cta
     }
     end = min(end, ctas);
 #pragma unroll 8
-    for (int c = blockIdx.x + 1; c < end; ++c) sum += tp.parts[static_cast<int64_t>(c) * 2 * kTile + threadIdx.x];
+    for (int c = blockIdx.x + 1; c < end; ++c) sum += tp.parts[static_cast<int64_t>(c) * 4 * kKeys + threadIdx.x];
     const Rows rows = rows_of(p, rec.b);
-    const int j = rec.t * kTile + threadIdx.x;
+    const int j = rec.t * kTile<true> + threadIdx.x;
     if (rows.ok && j < rows.n && key_row(p, rec.b, rec.h, j) >= 0) store(p, rec.b, rec.h, j, rows, sum);
 }
 
@@ -623,14 +643,14 @@ static int few_rows(int g, int T, int P) { return g * (P ? P : T); }
 bool weigh_many(int g, int T, int P) { return !P && T >= 96 && g * T > kMostRows; }
 
 size_t weigh_tc_bytes(int g, int T, int P) {
-    return weigh_many(g, T, P) ? static_cast<size_t>(device_sm_count()) * (sizeof(Record) + 2 * kTile * sizeof(float)) : 0;
+    return weigh_many(g, T, P) ? static_cast<size_t>(device_sm_count()) * (sizeof(Record) + 4 * kKeys * sizeof(float)) : 0;
 }
 
 template <int D, bool MANY>
 static spec_status launch_tc(const Maps& m, TcParams& tp, cudaStream_t s) {
-    constexpr size_t kStage = static_cast<size_t>(kTile) * D * 2;
+    constexpr size_t kStage = static_cast<size_t>(kTile<MANY>) * D * 2;
     const size_t q = static_cast<size_t>(tp.nq) * D * 2;
-    tp.q_stages = MANY ? 4 : 2;
+    tp.q_stages = MANY && D == 64 ? 4 : 2;
     tp.buffers = MANY || tp.nq <= 128 ? 4 : 2;
     const size_t room = kSmem - 1024 - sizeof(Small) - tp.q_stages * q;
     tp.k_stages = static_cast<int>(std::min<size_t>(MANY ? 2 : kMaxStages, room / kStage));
@@ -638,7 +658,7 @@ static spec_status launch_tc(const Maps& m, TcParams& tp, cudaStream_t s) {
     SPEC_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)));
     const int ctas = device_sm_count();
     SPEC_CUDA_TRY(launch("kv_weigh_tc", kern, dim3(ctas), dim3(kTcThreads), kSmem, s, m, tp));
-    if (MANY) SPEC_CUDA_TRY(launch_ex("kv_weigh_join", k_weigh_join, dim3(ctas), dim3(kTile), 0, s, true, tp, ctas));
+    if (MANY) SPEC_CUDA_TRY(launch_ex("kv_weigh_join", k_weigh_join, dim3(ctas), dim3(2 * kKeys), 0, s, true, tp, ctas));
     return SPEC_OK;
 }
 
@@ -648,10 +668,10 @@ spec_status weigh_tc_run(const Params& p, int D, void* scratch, cudaStream_t s) 
     TcParams tp{};
     tp.p = p;
     tp.g = p.Hq / p.Hkv;
-    tp.box = kTile;
+    tp.box = kKeys;
     if (p.table) {                    // a load lies inside one block and one tile
         tp.box = 16;
-        while (tp.box < kTile && p.rows % (2 * tp.box) == 0) tp.box *= 2;
+        while (tp.box < kKeys && p.rows % (2 * tp.box) == 0) tp.box *= 2;
     }
     const uint64_t k_rows = static_cast<uint64_t>(p.table ? p.num_blocks : p.B) * p.Hkv * p.rows;
     const uint64_t q_rows = static_cast<uint64_t>(p.B) * p.Hq * p.T;
