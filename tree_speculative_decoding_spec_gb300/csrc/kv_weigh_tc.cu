@@ -261,6 +261,14 @@ __device__ __forceinline__ unsigned long long weights32(const uint32_t (&s)[32],
     return fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
 }
 
+// The same of the columns whose bit is set; the others may hold anything.
+__device__ __forceinline__ unsigned long long masked32(const uint32_t (&s)[32], const float* nl2, unsigned long long c2, uint32_t seen) {
+    uint32_t x[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = (seen >> e) & 1u ? s[e] : 0xff800000u;   // -inf: weighs nothing
+    return weights32(x, nl2, c2);
+}
+
 template <int D, bool MANY>
 __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constant__ Maps mp, const TcParams tp) {
     constexpr int kH = D / 64;
@@ -508,14 +516,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                     const int cols = MANY ? min(kChunk, w.rows.count - i0) : min(tp.nq, tp.g * w.rows.count - tp.row0);
                     const bool plain = (!MANY || cols == kChunk) && k0 + kKeys - 1 <= in_front + i0;
                     unsigned long long part = pk2(0.f, 0.f);
-                    if (plain && MANY) {
+                    if (MANY) {
+                        const int lo = j - in_front - i0;    // the first column that sees this key
                         uint32_t r[2][32];
                         tmem_ld32(s_addr, r[0]);
 #pragma unroll
-                        for (int x = 0; x < kChunk / 32; ++x) {
+                        for (int x = 0; x < kChunk; x += 32) {
                             tmem_ld_wait();
-                            if (x + 1 < kChunk / 32) tmem_ld32(s_addr + 32 * (x + 1), r[(x + 1) & 1]);
-                            part = fadd2(part, weights32(r[x & 1], nl2 + 32 * x, c2));
+                            if (x + 32 < kChunk) tmem_ld32(s_addr + x + 32, r[(x / 32 + 1) & 1]);
+                            if (plain) {
+                                part = fadd2(part, weights32(r[x / 32 & 1], nl2 + x, c2));
+                            } else {
+                                const uint32_t from = lo <= x ? ~0u : lo >= x + 32 ? 0u : ~0u << (lo - x);
+                                const uint32_t seen = cols >= x + 32 ? from : cols <= x ? 0u : from & ~(~0u << (cols - x));
+                                if (__any_sync(0xffffffffu, seen)) part = fadd2(part, masked32(r[x / 32 & 1], nl2 + x, c2, seen));
+                            }
                         }
                     } else if (plain) {
                         const int steps = max(1, (cols + 15) / 16);
@@ -533,7 +548,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                             }
                         }
                     } else {
-                        const int lo = j - in_front - i0;            // many: the first column that sees this key
                         float f0 = 0.f;
 #pragma unroll 1
                         for (int x = 0; x < cols; x += 16) {
@@ -543,7 +557,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 const float v = ex2(fmaf(__uint_as_float(r[e]), p.scale * kL2e, nl2[x + e]));
-                                const bool sees = x + e < cols && (MANY ? x + e >= lo : j <= sm.last[ls][x + e]);
+                                const bool sees = x + e < cols && j <= sm.last[ls][x + e];
                                 f0 += sees ? v : 0.f;
                             }
                         }
