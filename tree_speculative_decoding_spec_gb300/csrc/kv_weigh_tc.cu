@@ -17,11 +17,12 @@
 // many equal parts as there are CTAs; lengths are known on the device only, so every CTA works its part
 // out itself.  A tile that is cut leaves partial sums, which kv_weigh_join adds up in order.
 //
-// One persistent CTA an SM, twelve warps:
-//   warps 0-3, 4-7   two groups, one thread per key: of alternate tiles (few), of half a tile each (many)
-//   warp 8           TMA: key tiles, and the chunks of rows (many)
-//   warp 9           MMA, one thread
-//   warps 10, 11     gather a head's rows (few); lse of the rows (both)
+// One persistent CTA an SM:
+//   groups of 4 warps  one thread per key.  few: two groups take alternate tiles.  many: two groups for each
+//                      half of a tile take alternate chunks; two groups in all left the schedulers
+//                      waiting for scores and exponentials (137 us where four take XX)
+//   and then           a warp for TMA (key tiles; chunks of rows), one whose first lane issues MMAs, and two that gather
+//                      a head's rows (few) and lse (both)
 // Waits are bounded (2 s); on expiry SPEC_ETIMEOUT goes to the status word, every role leaves its
 // loops, and the CTA drains its own loads and MMAs before it frees TMEM.
 #include <algorithm>
@@ -39,7 +40,8 @@ constexpr int kKeys = 128;            // keys of a product
 constexpr int kChunk = 128;           // query rows of a chunk (many)
 template <bool MANY> constexpr int kTile = MANY ? 2 * kKeys : kKeys;   // keys of a tile
 constexpr int kMostRows = 256;        // query rows of a pass (few)
-constexpr int kTcThreads = 384;
+template <bool MANY> constexpr int kGroups = MANY ? 4 : 2;
+template <bool MANY> constexpr int kTcThreads = (4 * kGroups<MANY> + 4) * 32;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kL2e = 1.4426950408889634f;
@@ -70,6 +72,7 @@ struct Small {
     uint64_t q_full[4], q_empty[4];
     uint64_t l_full[4], l_empty[4];   // many: lse of a chunk's rows
     uint64_t s_full[4], s_empty[4];
+    uint64_t x_full[4], x_empty[4];   // many: [turn][half]
     uint64_t drain;
     uint32_t tmem;
     int abort_flag, bad;
@@ -77,6 +80,7 @@ struct Small {
     long long length;                 // its chunks
     __align__(16) float nl2[4][kMostRows];   // -lse log2 e of a stage's rows, -inf: does not count
     int last[4][kMostRows];           // few: the last key that a row sees
+    float cross[4][kKeys];            // many: the second group's sums, as x_full
 };
 
 // The line of chunks of one sequence and head: row chunks first(t) .. C - 1 for tile t, times `mult` query heads.
@@ -124,6 +128,14 @@ __device__ __forceinline__ bool warp_wait_for(uint64_t* bar, uint32_t parity, vo
     return __all_sync(0xffffffffu, wait_for(bar, parity, abort_flag));
 }
 
+// One lane of the warp, the same at every call, as a condition the compiler knows to be uniform: behind lane == 0 the
+// products' descriptors went through vector registers, and issuing 16 products took twice as long as they did.
+__device__ __forceinline__ bool elected() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
 // The tiles of a CTA's part of the line, the same in every role.
 template <bool MANY> struct Walk {
     const TcParams& tp;
@@ -143,6 +155,20 @@ template <bool MANY> struct Walk {
         }
     }
     __device__ __forceinline__ void set() { take = static_cast<int>(min(static_cast<long long>(head.chunks(t) - c), left)); }
+    // many: first rows of the chunks one after the other, and which of its query heads the first belongs to
+    struct Chunks {
+        int i0, begin, end;
+        __device__ __forceinline__ void next() {
+            i0 += kChunk;
+            if (i0 >= end) i0 = begin;
+        }
+    };
+    __device__ __forceinline__ Chunks chunks(int& head_at) const {
+        const int m = head.C - head.first(t);
+        head_at = c / m;
+        const int begin = head.first(t) * kChunk;
+        return {begin + (c - head_at * m) * kChunk, begin, head.C * kChunk};
+    }
     __device__ __forceinline__ bool whole() const { return take == head.chunks(t); }
     // whether the next tile is of another head (or there is none)
     __device__ __forceinline__ bool column_ends() const { return left == take || t + 1 == head.tiles; }
@@ -247,30 +273,16 @@ __device__ __forceinline__ unsigned long long weights16(const uint32_t (&s)[16],
     return fadd2(sum, sum1);
 }
 
-__device__ __forceinline__ unsigned long long weights32(const uint32_t (&s)[32], const float* nl2, unsigned long long c2) {
-    unsigned long long sum[4] = {pk2(0.f, 0.f), pk2(0.f, 0.f), pk2(0.f, 0.f), pk2(0.f, 0.f)};
-#pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(nl2 + e);
-        float a, b, c, d;
-        upk2(ffma2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, pk2(l.x, l.y)), a, b);
-        upk2(ffma2(pk2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, pk2(l.z, l.w)), c, d);
-        sum[(e / 2) & 3] = fadd2(sum[(e / 2) & 3], pk2(ex2(a), ex2(b)));
-        sum[(e / 2 + 1) & 3] = fadd2(sum[(e / 2 + 1) & 3], pk2(ex2(c), ex2(d)));
-    }
-    return fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
-}
-
 // The same of the columns whose bit is set; the others may hold anything.
-__device__ __forceinline__ unsigned long long masked32(const uint32_t (&s)[32], const float* nl2, unsigned long long c2, uint32_t seen) {
-    uint32_t x[32];
+__device__ __forceinline__ unsigned long long masked16(const uint32_t (&s)[16], const float* nl2, unsigned long long c2, uint32_t seen) {
+    uint32_t x[16];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = (seen >> e) & 1u ? s[e] : 0xff800000u;   // -inf: weighs nothing
-    return weights32(x, nl2, c2);
+    for (int e = 0; e < 16; ++e) x[e] = (seen >> e) & 1u ? s[e] : 0xff800000u;   // -inf: weighs nothing
+    return weights16(x, nl2, c2);
 }
 
 template <int D, bool MANY>
-__global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constant__ Maps mp, const TcParams tp) {
+__global__ void __launch_bounds__(kTcThreads<MANY>, 1) k_weigh_tc(const __grid_constant__ Maps mp, const TcParams tp) {
     constexpr int kH = D / 64;
     constexpr int kKHalf = kKeys * 128;                  // bytes of a 64-column half of 128 keys
     constexpr int kHalves = MANY ? 2 : 1;                // 128 keys each
@@ -284,6 +296,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
     const int q_half = tp.nq * 128;
     Small& sm = *reinterpret_cast<Small*>(sQ + tp.q_stages * kH * q_half);
     volatile int* abort_flag = &sm.abort_flag;
+    constexpr int kTma = 4 * kGroups<MANY>, kMma = kTma + 1, kRowsWarp = kTma + 2;   // the other roles' warps
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -294,7 +307,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
             mbar_init(&sm.q_full[i], MANY ? 1 : 2);
             mbar_init(&sm.q_empty[i], MANY ? 1 : 9);
             mbar_init(&sm.l_full[i], 1);
-            mbar_init(&sm.l_empty[i], 8);
+            mbar_init(&sm.l_empty[i], 4 * kGroups<MANY>);
+            mbar_init(&sm.x_full[i], 4);
+            mbar_init(&sm.x_empty[i], 4);
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_empty[i], 4);
         }
@@ -305,7 +320,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
-    if (warp == 8) plan<MANY>(tp, sm);
+    if (warp == kTma) plan<MANY>(tp, sm);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -316,7 +331,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
     int k_loads = 0, q_loads = 0;     // (TMA) requested so far
     Walk<MANY> w(tp, sm);
 
-    if (warp == 8) {
+    if (warp == kTma) {
         // ------------------------------------------------ keys, and the chunks of rows
         for (; ok && w.more; w.next()) {
             const int stage = k_loads % tp.k_stages;
@@ -335,83 +350,100 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                     tma_load_2d(dst + ((in / kKeys) * kH + hh) * kKHalf + in % kKeys * 128, &mp.k, &sm.k_full[stage], hh * 64, static_cast<int>(row));
             ++k_loads;
             if (MANY) {
-                const int m = w.head.chunks(w.t) / w.head.mult, c0 = w.head.first(w.t);
-                for (int c = w.c; c < w.c + w.take; ++c) {
+                int qh;
+                typename Walk<MANY>::Chunks ch = w.chunks(qh);
+                for (int c = 0; c < w.take; ++c) {
                     const int qs = q_loads % tp.q_stages;
                     if (q_loads >= tp.q_stages && !(ok = warp_wait_for(&sm.q_empty[qs], (q_loads / tp.q_stages - 1) & 1, abort_flag))) break;
                     if (lane == 0) {
-                        const int qh = w.h * tp.g + c / m, i0 = (c0 + c % m) * kChunk;
                         mbar_arrive_expect_tx(&sm.q_full[qs], kH * q_half);
                         for (int hh = 0; hh < kH; ++hh)
-                            tma_load_2d(sQ + (qs * kH + hh) * q_half, &mp.q, &sm.q_full[qs], hh * 64, (w.b * p.Hq + qh) * p.T + i0);
+                            tma_load_2d(sQ + (qs * kH + hh) * q_half, &mp.q, &sm.q_full[qs], hh * 64, (w.b * p.Hq + w.h * tp.g + qh) * p.T + ch.i0);
                     }
+                    ch.next();
+                    if (ch.i0 == ch.begin) ++qh;
                     ++q_loads;
                 }
             }
             __syncwarp();
         }
-    } else if (warp == 9) {
+    } else if (warp == kMma) {
         // ------------------------------------------------ products
-        if (lane == 0) {
-            int kt = 0, u = 0, col = 0;
-            int units[2] = {0, 0};    // many: products of each half so far
-            for (; ok && w.more; w.next(), ++kt) {
-                const int ks = kt % tp.k_stages;
-                if (!(ok = wait_for(&sm.k_full[ks], (kt / tp.k_stages) & 1, abort_flag))) break;
-                const uint32_t ka = smem_u32(sK + ks * kKStage);
-                const int n = MANY ? kChunk : max(16, min(tp.nq, (tp.g * w.rows.count - tp.row0 + 15) / 16 * 16));
-                const uint32_t idesc = idesc_bf16_f32(kKeys, n);
-                const int m = MANY ? w.head.chunks(w.t) / w.head.mult : 1, c0 = MANY ? w.head.first(w.t) : 0;
-                for (int c = w.c; c < w.c + w.take; ++c, ++u) {
-                    const int qn = MANY ? u : col;
-                    const int qs = qn % tp.q_stages;
-                    if (!(ok = wait_for(&sm.q_full[qs], (qn / tp.q_stages) & 1, abort_flag))) break;
-                    const uint32_t qa = smem_u32(sQ + qs * kH * q_half);
-                    for (int half = 0; half < kHalves; ++half) {
-                        if (MANY && unseen(w.rows, w.t * kTile<MANY> + half * kKeys, (c0 + c % m) * kChunk)) continue;
-                        // many: two buffers for each half; few: tiles take all of them in turn
-                        const int use = MANY ? units[half]++ : u;
-                        const int buf = MANY ? 2 * half + (use & 1) : use % tp.buffers, round = MANY ? use >> 1 : use / tp.buffers;
-                        if (round > 0 && !(ok = wait_for(&sm.s_empty[buf], (round - 1) & 1, abort_flag))) break;
-                        tc_fence_after();
+        const bool leader = elected();
+        int kt = 0, u = 0, col = 0;
+        int units[2] = {0, 0};        // many: products of each half so far
+        for (; ok && w.more; w.next(), ++kt) {
+            const int ks = kt % tp.k_stages;
+            if (!(ok = warp_wait_for(&sm.k_full[ks], (kt / tp.k_stages) & 1, abort_flag))) break;
+            const uint64_t ka = sdesc_k128(smem_u32(sK + ks * kKStage));
+            const int n = MANY ? kChunk : max(16, min(tp.nq, (tp.g * w.rows.count - tp.row0 + 15) / 16 * 16));
+            const uint32_t idesc = idesc_bf16_f32(kKeys, n);
+            int qh;
+            typename Walk<MANY>::Chunks ch{};
+            if (MANY) ch = w.chunks(qh);
+            for (int c = 0; c < w.take; ++c, ++u) {
+                const int qn = MANY ? u : col;
+                const int qs = qn % tp.q_stages;
+                if (!(ok = warp_wait_for(&sm.q_full[qs], (qn / tp.q_stages) & 1, abort_flag))) break;
+                const uint64_t qa = sdesc_k128(smem_u32(sQ + qs * kH * q_half));
+#pragma unroll
+                for (int half = 0; half < kHalves; ++half) {
+                    if (MANY && unseen(w.rows, w.t * kTile<MANY> + half * kKeys, ch.i0)) continue;
+                    // many: two buffers for each half; few: tiles take all of them in turn
+                    const int use = MANY ? units[half]++ : u;
+                    const int buf = MANY ? 2 * half + (use & 1) : use % tp.buffers, round = MANY ? use >> 1 : use / tp.buffers;
+                    if (round > 0 && !(ok = warp_wait_for(&sm.s_empty[buf], (round - 1) & 1, abort_flag))) break;
+                    tc_fence_after();
+                    if (leader) {
+                        // (an address is 16 bytes a unit in a descriptor)
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            mma_bf16(tmem + buf * buf_cols, sdesc_k128(ka + (half * kH + k / 4) * kKHalf + (k % 4) * 32),
-                                     sdesc_k128(qa + (k / 4) * q_half + (k % 4) * 32), idesc, k > 0);
+                            mma_bf16(tmem + buf * buf_cols, ka + (((half * kH + k / 4) * kKHalf + (k % 4) * 32) >> 4),
+                                     qa + static_cast<uint32_t>(((k / 4) * q_half + (k % 4) * 32) >> 4), idesc, k > 0);
                         mma_commit(&sm.s_full[buf]);
                     }
-                    if (!ok) break;
-                    if (MANY) mma_commit(&sm.q_empty[qs]);
+                    __syncwarp();
                 }
                 if (!ok) break;
-                mma_commit(&sm.k_empty[ks]);
-                if (!MANY && w.column_ends()) mma_commit(&sm.q_empty[col++ % tp.q_stages]);
+                if (MANY) {
+                    if (leader) mma_commit(&sm.q_empty[qs]);
+                    ch.next();
+                }
             }
-            mma_commit(&sm.drain);
+            if (!ok) break;
+            if (leader) mma_commit(&sm.k_empty[ks]);
+            if (!MANY && w.column_ends()) {
+                if (leader) mma_commit(&sm.q_empty[col % tp.q_stages]);
+                ++col;
+            }
+            __syncwarp();
         }
+        if (leader) mma_commit(&sm.drain);
         __syncwarp();
-    } else if (warp >= 10) {
+    } else if (warp >= kRowsWarp) {
         // ------------------------------------------------ rows
         if constexpr (MANY) {
-            // lse of a chunk's rows: four for each lane of warp 10
+            // lse of a chunk's rows: four for each lane of the first warp
             int u = 0;
-            if (warp == 10)
+            if (warp == kRowsWarp)
                 for (; ok && w.more; w.next()) {
-                    const int m = w.head.chunks(w.t) / w.head.mult, c0 = w.head.first(w.t);
-                    for (int c = w.c; c < w.c + w.take; ++c, ++u) {
+                    int qh;
+                    typename Walk<MANY>::Chunks ch = w.chunks(qh);
+                    for (int c = 0; c < w.take; ++c, ++u) {
                         const int ls = u & 3;
-                        const int qh = w.h * tp.g + c / m, i0 = (c0 + c % m) * kChunk;
                         float x[4];
                         for (int e = 0; e < 4; ++e) {
-                            const int i = i0 + lane * 4 + e;
+                            const int i = ch.i0 + lane * 4 + e;
                             x[e] = INFINITY;
-                            if (i < w.rows.count) x[e] = p.lse[static_cast<int64_t>(w.b * p.Hq + qh) * p.T + i];
+                            if (i < w.rows.count) x[e] = p.lse[static_cast<int64_t>(w.b * p.Hq + w.h * tp.g + qh) * p.T + i];
                         }
                         if (u >= 4 && !(ok = warp_wait_for(&sm.l_empty[ls], (u / 4 - 1) & 1, abort_flag))) break;
                         for (int e = 0; e < 4; ++e) x[e] = isfinite(x[e]) ? -x[e] * kL2e : -INFINITY;
                         *reinterpret_cast<float4*>(&sm.nl2[ls][lane * 4]) = make_float4(x[0], x[1], x[2], x[3]);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sm.l_full[ls]);
+                        ch.next();
+                        if (ch.i0 == ch.begin) ++qh;
                     }
                 }
         } else {
@@ -423,7 +455,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                     const int qs = col % tp.q_stages;
                     if (col >= tp.q_stages && !(ok = warp_wait_for(&sm.q_empty[qs], (col / tp.q_stages - 1) & 1, abort_flag))) break;
                     const int total = min(tp.nq, tp.g * w.rows.count - tp.row0), padded = max(16, (total + 15) / 16 * 16);
-                    const int tid = threadIdx.x - 320;
+                    const int tid = threadIdx.x - 32 * kRowsWarp;
                     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
                     const int64_t q0 = static_cast<int64_t>(w.b) * p.Hq + w.h * tp.g;
                     for (int x = tid; x < padded * (D / 8); x += 64) {
@@ -466,7 +498,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
             // the status: sequences that make no sense, blocks outside the pool.  (A wait that runs out flags it
             // two seconds later.)
             int bad = 0;
-            for (int b = warp; b < p.B; b += 8) {
+            for (int b = warp; b < p.B; b += 4 * kGroups<MANY>) {
                 const Rows r = rows_of(p, b);
                 if (!r.ok) {
                     bad = 1;
@@ -479,34 +511,39 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                 }
             }
             if (bad) sm.bad = 1;
-            asm volatile("bar.sync 1, 256;" ::: "memory");   // all of these warps come here, once, and wait for nobody else
+            asm volatile("bar.sync 1, %0;" ::"n"(128 * kGroups<MANY>) : "memory");   // all of these warps come here, once, and wait for nobody else
             if (threadIdx.x == 0 && tp.row0 == 0) *static_cast<int4*>(p.ws) = make_int4(sm.bad ? SPEC_EINVAL : SPEC_OK, 0, 0, 0);
         }
         const unsigned long long c2 = pk2(p.scale * kL2e, p.scale * kL2e);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const int half = MANY ? grp >> 1 : 0;   // of the tile's keys
         int u = 0, kt = 0, col = 0, use = 0;
         for (; ok && w.more; w.next(), ++kt) {
             const bool mine = MANY || (kt & 1) == grp;
-            const int k0 = w.t * kTile<MANY> + (MANY ? grp * kKeys : 0), j = k0 + key;   // of the group; of the thread
+            const int k0 = w.t * kTile<MANY> + half * kKeys, j = k0 + key;   // of the group; of the thread
             const int in_front = w.rows.n - w.rows.count;
             // what the key has so far, on its way while the products run
-            const bool there = mine && j < w.rows.n && (!p.table || key_row(p, w.b, w.h, j) >= 0);
+            const bool there = mine && (!MANY || !(grp & 1)) && j < w.rows.n && (!p.table || key_row(p, w.b, w.h, j) >= 0);
             const int64_t at = (static_cast<int64_t>(w.b) * p.Hkv + w.h) * p.cap + j;
             const bool fresh = j >= in_front;
             float old = 0.f;
             if (there && (!MANY || w.whole()) && (tp.row0 > 0 || (!fresh && p.decay != 0.f))) old = p.acc[at];
             float sum = 0.f;
-            const int m = MANY ? w.head.chunks(w.t) / w.head.mult : 1, c0 = MANY ? w.head.first(w.t) : 0;
-            for (int c = w.c; c < w.c + w.take; ++c, ++u) {
+            int qh;
+            typename Walk<MANY>::Chunks ch{};
+            if (MANY) ch = w.chunks(qh);
+            for (int c = 0; c < w.take; ++c, ++u) {
                 if (!mine) continue;
-                const int i0 = MANY ? (c0 + c % m) * kChunk : 0;
+                const int i0 = ch.i0;
+                if (MANY) ch.next();
                 const int ls = MANY ? u & 3 : col % tp.q_stages;
                 // many: also where the group has no part in the chunk, or it would give back a later turn of the slot
                 // in place of this one
                 if (MANY && !(ok = warp_wait_for(&sm.l_full[ls], (u >> 2) & 1, abort_flag))) break;
-                if (!MANY || !unseen(w.rows, k0, i0)) {
-                    const int buf = MANY ? 2 * grp + (use & 1) : u % tp.buffers, round = MANY ? use >> 1 : u / tp.buffers;
-                    ++use;
+                bool turn = !MANY;
+                if (MANY && !unseen(w.rows, k0, i0)) turn = (use++ & 1) == (grp & 1);
+                if (turn) {
+                    const int buf = MANY ? grp : u % tp.buffers, round = MANY ? (use - 1) >> 1 : u / tp.buffers;
                     if (!MANY && !(ok = warp_wait_for(&sm.q_full[ls], (col / tp.q_stages) & 1, abort_flag))) break;
                     if (!(ok = warp_wait_for(&sm.s_full[buf], round & 1, abort_flag))) break;
                     tc_fence_after();
@@ -518,18 +555,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                     unsigned long long part = pk2(0.f, 0.f);
                     if (MANY) {
                         const int lo = j - in_front - i0;    // the first column that sees this key
-                        uint32_t r[2][32];
-                        tmem_ld32(s_addr, r[0]);
+                        uint32_t r[2][16];
+                        tmem_ld16(s_addr, r[0]);
 #pragma unroll
-                        for (int x = 0; x < kChunk; x += 32) {
+                        for (int x = 0; x < kChunk; x += 16) {
                             tmem_ld_wait();
-                            if (x + 32 < kChunk) tmem_ld32(s_addr + x + 32, r[(x / 32 + 1) & 1]);
+                            if (x + 16 < kChunk) tmem_ld16(s_addr + x + 16, r[(x / 16 + 1) & 1]);
                             if (plain) {
-                                part = fadd2(part, weights32(r[x / 32 & 1], nl2 + x, c2));
+                                part = fadd2(part, weights16(r[x / 16 & 1], nl2 + x, c2));
                             } else {
-                                const uint32_t from = lo <= x ? ~0u : lo >= x + 32 ? 0u : ~0u << (lo - x);
-                                const uint32_t seen = cols >= x + 32 ? from : cols <= x ? 0u : from & ~(~0u << (cols - x));
-                                if (__any_sync(0xffffffffu, seen)) part = fadd2(part, masked32(r[x / 32 & 1], nl2 + x, c2, seen));
+                                uint32_t seen = lo <= x ? 0xffffu : lo >= x + 16 ? 0u : 0xffffu << (lo - x);
+                                seen = cols >= x + 16 ? seen : cols <= x ? 0u : seen & ~(~0u << (cols - x));
+                                if (__any_sync(0xffffffffu, seen)) part = fadd2(part, masked16(r[x / 16 & 1], nl2 + x, c2, seen));
                             }
                         }
                     } else if (plain) {
@@ -573,6 +610,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                 if (MANY && lane == 0) mbar_arrive(&sm.l_empty[ls]);
             }
             if (!ok) break;
+            if (MANY) {
+                // the two groups of a half: the second one's sums through one of two buffers
+                const int x = 2 * (kt & 1) + half;
+                if (grp & 1) {
+                    if (kt >= 2 && !(ok = warp_wait_for(&sm.x_empty[x], (kt / 2 - 1) & 1, abort_flag))) break;
+                    sm.cross[x][key] = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.x_full[x]);
+                    continue;
+                }
+                if (!(ok = warp_wait_for(&sm.x_full[x], (kt / 2) & 1, abort_flag))) break;
+                sum += sm.cross[x][key];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.x_empty[x]);
+            }
             if (!MANY && w.column_ends()) {
                 // (a group without a tile in this column waits for its rows all the same, as above)
                 if (!(ok = warp_wait_for(&sm.q_full[col % tp.q_stages], (col / tp.q_stages) & 1, abort_flag))) break;
@@ -582,7 +634,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
             if (MANY && !w.whole()) {
                 // a tile that another CTA has a part of: the join puts them together
                 const bool tail = w.c == 0;
-                tp.parts[(static_cast<int64_t>(blockIdx.x) * 2 + tail) * 2 * kKeys + grp * kKeys + key] = sum;
+                tp.parts[(static_cast<int64_t>(blockIdx.x) * 2 + tail) * 2 * kKeys + half * kKeys + key] = sum;
                 if (threadIdx.x == 0) {
                     Record& rec = tp.records[blockIdx.x];
                     if (tail) {
@@ -610,12 +662,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
     __syncthreads();
     if (*abort_flag) {
         // a wait ran out: let this CTA's own loads and MMAs land before it ends
-        if (warp == 8) {
+        if (warp == kTma) {
             for (int i = max(0, k_loads - tp.k_stages); i < k_loads; ++i) mbar_wait(&sm.k_full[i % tp.k_stages], (i / tp.k_stages) & 1, 100000000ull);
             if (MANY)
                 for (int i = max(0, q_loads - tp.q_stages); i < q_loads; ++i) mbar_wait(&sm.q_full[i % tp.q_stages], (i / tp.q_stages) & 1, 100000000ull);
         }
-        if (warp == 9) mbar_wait(&sm.drain, 0, 100000000ull);
+        if (warp == kMma) mbar_wait(&sm.drain, 0, 100000000ull);
     }
     __syncthreads();
     if (warp == 0) {
@@ -664,14 +716,14 @@ template <int D, bool MANY>
 static spec_status launch_tc(const Maps& m, TcParams& tp, cudaStream_t s) {
     constexpr size_t kStage = static_cast<size_t>(kTile<MANY>) * D * 2;
     const size_t q = static_cast<size_t>(tp.nq) * D * 2;
-    tp.q_stages = MANY && D == 64 ? 4 : 2;
+    tp.q_stages = MANY ? 4 : 2;       // many, D = 128: 64 KB of keys once, 32 KB of rows four times
     tp.buffers = MANY || tp.nq <= 128 ? 4 : 2;
     const size_t room = kSmem - 1024 - sizeof(Small) - tp.q_stages * q;
     tp.k_stages = static_cast<int>(std::min<size_t>(MANY ? 2 : kMaxStages, room / kStage));
     auto kern = k_weigh_tc<D, MANY>;
     SPEC_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)));
     const int ctas = device_sm_count();
-    SPEC_CUDA_TRY(launch("kv_weigh_tc", kern, dim3(ctas), dim3(kTcThreads), kSmem, s, m, tp));
+    SPEC_CUDA_TRY(launch("kv_weigh_tc", kern, dim3(ctas), dim3(kTcThreads<MANY>), kSmem, s, m, tp));
     if (MANY) SPEC_CUDA_TRY(launch_ex("kv_weigh_join", k_weigh_join, dim3(ctas), dim3(2 * kKeys), 0, s, true, tp, ctas));
     return SPEC_OK;
 }
