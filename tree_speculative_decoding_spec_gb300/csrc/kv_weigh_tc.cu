@@ -18,11 +18,11 @@
 // out itself.  A tile that is cut leaves partial sums, which kv_weigh_join adds up in order.
 //
 // One persistent CTA an SM:
-//   groups of 4 warps  one thread per key.  few: two groups take alternate tiles.  many: two groups for each
-//                      half of a tile take alternate chunks; two groups in all left the schedulers
-//                      waiting for scores and exponentials (137 us where four take XX)
-//   and then           a warp for TMA (key tiles; chunks of rows), one whose first lane issues MMAs, and two that gather
-//                      a head's rows (few) and lse (both)
+//   two groups of 4    one thread per key.  few: alternate tiles; many: half of a tile each
+//   and then           a warp for TMA (key tiles; chunks of rows), one that issues products (many: two, one
+//                      for each half of a tile: issuing waits for the tensor pipe, and a single one left it idle
+//                      for as long again while it looked at barriers), and two or one that gather a head's
+//                      rows (few) and lse (both)
 // Waits are bounded (2 s); on expiry SPEC_ETIMEOUT goes to the status word, every role leaves its
 // loops, and the CTA drains its own loads and MMAs before it frees TMEM.
 #include <algorithm>
@@ -40,8 +40,8 @@ constexpr int kKeys = 128;            // keys of a product
 constexpr int kChunk = 128;           // query rows of a chunk (many)
 template <bool MANY> constexpr int kTile = MANY ? 2 * kKeys : kKeys;   // keys of a tile
 constexpr int kMostRows = 256;        // query rows of a pass (few)
-template <bool MANY> constexpr int kGroups = MANY ? 4 : 2;
-template <bool MANY> constexpr int kTcThreads = (4 * kGroups<MANY> + 4) * 32;
+constexpr int kGroups = 2;            // of four warps
+constexpr int kTcThreads = (4 * kGroups + 4) * 32;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kL2e = 1.4426950408889634f;
@@ -71,8 +71,7 @@ struct Small {
     uint64_t k_full[kMaxStages], k_empty[kMaxStages];
     uint64_t q_full[4], q_empty[4];
     uint64_t l_full[4], l_empty[4];   // many: lse of a chunk's rows
-    uint64_t s_full[4], s_empty[4];
-    uint64_t x_full[4], x_empty[4];   // many: [turn][half]
+    uint64_t s_full[4], s_empty[4];   // many: [half][turn]
     uint64_t drain;
     uint32_t tmem;
     int abort_flag, bad;
@@ -80,7 +79,6 @@ struct Small {
     long long length;                 // its chunks
     __align__(16) float nl2[4][kMostRows];   // -lse log2 e of a stage's rows, -inf: does not count
     int last[4][kMostRows];           // few: the last key that a row sees
-    float cross[4][kKeys];            // many: the second group's sums, as x_full
 };
 
 // The line of chunks of one sequence and head: row chunks first(t) .. C - 1 for tile t, times `mult` query heads.
@@ -253,20 +251,49 @@ template <bool MANY> __device__ void plan(const TcParams& tp, Small& sm) {
     }
 }
 
+// A slot of a ring and how often it has come round, kept without divisions (with them, by numbers that are not known to
+// the compiler, single tokens took 72 us where this takes 63, prompts 142 for 128).
+struct Ring {
+    int at = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++at == n) {
+            at = 0;
+            ++round;
+        }
+    }
+    __device__ __forceinline__ uint32_t full() const { return round & 1; }            // parity of "filled" this time
+    __device__ __forceinline__ uint32_t empty() const { return (round + 1) & 1; }     // of "emptied" the time before, if round > 0
+};
+
 // Whether no row of the chunk that begins at i0 sees a key of the half tile that begins at k0 (many).
 __device__ __forceinline__ bool unseen(const Rows& r, int k0, int i0) {
     return k0 >= r.n || k0 > r.n - r.count + min(i0 + kChunk, r.count) - 1;
 }
 
-// 16 columns of a key's scores: the sum of their weights.
-__device__ __forceinline__ unsigned long long weights16(const uint32_t (&s)[16], const float* nl2, unsigned long long c2) {
+__device__ __forceinline__ void load_scores(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16(addr, r); }
+__device__ __forceinline__ void load_scores(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r); }
+
+// -lse log2 e of N columns.  (Read before the wait for their scores: that is a barrier to the compiler, and behind it
+// every step began with the latency of shared memory.)
+template <int N> __device__ __forceinline__ void load_lse(const float* nl2, unsigned long long (&l)[N / 2]) {
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(nl2 + e);
+        l[e / 2] = x.x;
+        l[e / 2 + 1] = x.y;
+    }
+}
+
+// N columns of a key's scores: the sum of their weights.
+template <int N>
+__device__ __forceinline__ unsigned long long weights(const uint32_t (&s)[N], const unsigned long long (&l)[N / 2], unsigned long long c2) {
     unsigned long long sum = pk2(0.f, 0.f), sum1 = pk2(0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < 16; e += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(nl2 + e);
+    for (int e = 0; e < N; e += 4) {
         float a, b, c, d;
-        upk2(ffma2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, pk2(l.x, l.y)), a, b);
-        upk2(ffma2(pk2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, pk2(l.z, l.w)), c, d);
+        upk2(ffma2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, l[e / 2]), a, b);
+        upk2(ffma2(pk2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, l[e / 2 + 1]), c, d);
         sum = fadd2(sum, pk2(ex2(a), ex2(b)));
         sum1 = fadd2(sum1, pk2(ex2(c), ex2(d)));
     }
@@ -274,15 +301,16 @@ __device__ __forceinline__ unsigned long long weights16(const uint32_t (&s)[16],
 }
 
 // The same of the columns whose bit is set; the others may hold anything.
-__device__ __forceinline__ unsigned long long masked16(const uint32_t (&s)[16], const float* nl2, unsigned long long c2, uint32_t seen) {
-    uint32_t x[16];
+template <int N>
+__device__ __forceinline__ unsigned long long masked(const uint32_t (&s)[N], const unsigned long long (&l)[N / 2], unsigned long long c2, uint32_t seen) {
+    uint32_t x[N];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = (seen >> e) & 1u ? s[e] : 0xff800000u;   // -inf: weighs nothing
-    return weights16(x, nl2, c2);
+    for (int e = 0; e < N; ++e) x[e] = (seen >> e) & 1u ? s[e] : 0xff800000u;   // -inf: weighs nothing
+    return weights(x, l, c2);
 }
 
 template <int D, bool MANY>
-__global__ void __launch_bounds__(kTcThreads<MANY>, 1) k_weigh_tc(const __grid_constant__ Maps mp, const TcParams tp) {
+__global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constant__ Maps mp, const TcParams tp) {
     constexpr int kH = D / 64;
     constexpr int kKHalf = kKeys * 128;                  // bytes of a 64-column half of 128 keys
     constexpr int kHalves = MANY ? 2 : 1;                // 128 keys each
@@ -296,24 +324,22 @@ __global__ void __launch_bounds__(kTcThreads<MANY>, 1) k_weigh_tc(const __grid_c
     const int q_half = tp.nq * 128;
     Small& sm = *reinterpret_cast<Small*>(sQ + tp.q_stages * kH * q_half);
     volatile int* abort_flag = &sm.abort_flag;
-    constexpr int kTma = 4 * kGroups<MANY>, kMma = kTma + 1, kRowsWarp = kTma + 2;   // the other roles' warps
+    constexpr int kTma = 4 * kGroups, kMma = kTma + 1, kRowsWarp = kTma + (MANY ? 3 : 2);   // the other roles' warps
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sm.k_full[i], 1);
-            mbar_init(&sm.k_empty[i], 1);
+            mbar_init(&sm.k_empty[i], MANY ? 2 : 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sm.q_full[i], MANY ? 1 : 2);
-            mbar_init(&sm.q_empty[i], MANY ? 1 : 9);
+            mbar_init(&sm.q_empty[i], MANY ? 2 : 9);
             mbar_init(&sm.l_full[i], 1);
-            mbar_init(&sm.l_empty[i], 4 * kGroups<MANY>);
-            mbar_init(&sm.x_full[i], 4);
-            mbar_init(&sm.x_empty[i], 4);
+            mbar_init(&sm.l_empty[i], 4 * kGroups);
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_empty[i], 4);
         }
-        mbar_init(&sm.drain, 1);
+        mbar_init(&sm.drain, MANY ? 2 : 1);
         sm.abort_flag = 0;
         sm.bad = 0;
         if (MANY) tp.records[blockIdx.x] = Record{0, 0, 0, 0, 0, 0, 0, 0};
@@ -328,14 +354,14 @@ __global__ void __launch_bounds__(kTcThreads<MANY>, 1) k_weigh_tc(const __grid_c
     const uint32_t buf_cols = kTmemCols / tp.buffers;
     griddep_launch();                 // the join may start launching: it waits for the partial sums
     bool ok = true;
-    int k_loads = 0, q_loads = 0;     // (TMA) requested so far
+    Ring k_ring, q_ring;              // key tiles; chunks of rows, or columns' rows
     Walk<MANY> w(tp, sm);
 
     if (warp == kTma) {
         // ------------------------------------------------ keys, and the chunks of rows
         for (; ok && w.more; w.next()) {
-            const int stage = k_loads % tp.k_stages;
-            if (k_loads >= tp.k_stages && !(ok = warp_wait_for(&sm.k_empty[stage], (k_loads / tp.k_stages - 1) & 1, abort_flag))) break;
+            const int stage = k_ring.at;
+            if (k_ring.round > 0 && !(ok = warp_wait_for(&sm.k_empty[stage], k_ring.empty(), abort_flag))) break;
             uint8_t* dst = sK + stage * kKStage;
             const int k0 = w.t * kTile<MANY>;
             // a lane per load of `box` keys; what lies behind the length, or in a block outside the pool, is left out
@@ -348,13 +374,13 @@ __global__ void __launch_bounds__(kTcThreads<MANY>, 1) k_weigh_tc(const __grid_c
             if (row >= 0)
                 for (int hh = 0; hh < kH; ++hh)
                     tma_load_2d(dst + ((in / kKeys) * kH + hh) * kKHalf + in % kKeys * 128, &mp.k, &sm.k_full[stage], hh * 64, static_cast<int>(row));
-            ++k_loads;
+            k_ring.next(tp.k_stages);
             if (MANY) {
                 int qh;
                 typename Walk<MANY>::Chunks ch = w.chunks(qh);
                 for (int c = 0; c < w.take; ++c) {
-                    const int qs = q_loads % tp.q_stages;
-                    if (q_loads >= tp.q_stages && !(ok = warp_wait_for(&sm.q_empty[qs], (q_loads / tp.q_stages - 1) & 1, abort_flag))) break;
+                    const int qs = q_ring.at;
+                    if (q_ring.round > 0 && !(ok = warp_wait_for(&sm.q_empty[qs], q_ring.empty(), abort_flag))) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&sm.q_full[qs], kH * q_half);
                         for (int hh = 0; hh < kH; ++hh)
@@ -362,59 +388,57 @@ __global__ void __launch_bounds__(kTcThreads<MANY>, 1) k_weigh_tc(const __grid_c
                     }
                     ch.next();
                     if (ch.i0 == ch.begin) ++qh;
-                    ++q_loads;
+                    q_ring.next(tp.q_stages);
                 }
             }
             __syncwarp();
         }
-    } else if (warp == kMma) {
+    } else if (warp >= kMma && warp < kRowsWarp) {
         // ------------------------------------------------ products
         const bool leader = elected();
-        int kt = 0, u = 0, col = 0;
-        int units[2] = {0, 0};        // many: products of each half so far
-        for (; ok && w.more; w.next(), ++kt) {
-            const int ks = kt % tp.k_stages;
-            if (!(ok = warp_wait_for(&sm.k_full[ks], (kt / tp.k_stages) & 1, abort_flag))) break;
-            const uint64_t ka = sdesc_k128(smem_u32(sK + ks * kKStage));
+        const int half = warp - kMma; // of the tile's keys
+        const int buffers = MANY ? 2 : tp.buffers;
+        Ring s_ring;                  // a score buffer for each product; many: two of each half
+        for (; ok && w.more; w.next(), k_ring.next(tp.k_stages)) {
+            const int ks = k_ring.at;
+            if (!(ok = warp_wait_for(&sm.k_full[ks], k_ring.full(), abort_flag))) break;
+            const uint64_t ka = sdesc_k128(smem_u32(sK + ks * kKStage + half * kH * kKHalf));
             const int n = MANY ? kChunk : max(16, min(tp.nq, (tp.g * w.rows.count - tp.row0 + 15) / 16 * 16));
             const uint32_t idesc = idesc_bf16_f32(kKeys, n);
             int qh;
             typename Walk<MANY>::Chunks ch{};
             if (MANY) ch = w.chunks(qh);
-            for (int c = 0; c < w.take; ++c, ++u) {
-                const int qn = MANY ? u : col;
-                const int qs = qn % tp.q_stages;
-                if (!(ok = warp_wait_for(&sm.q_full[qs], (qn / tp.q_stages) & 1, abort_flag))) break;
-                const uint64_t qa = sdesc_k128(smem_u32(sQ + qs * kH * q_half));
-#pragma unroll
-                for (int half = 0; half < kHalves; ++half) {
-                    if (MANY && unseen(w.rows, w.t * kTile<MANY> + half * kKeys, ch.i0)) continue;
-                    // many: two buffers for each half; few: tiles take all of them in turn
-                    const int use = MANY ? units[half]++ : u;
-                    const int buf = MANY ? 2 * half + (use & 1) : use % tp.buffers, round = MANY ? use >> 1 : use / tp.buffers;
-                    if (round > 0 && !(ok = warp_wait_for(&sm.s_empty[buf], (round - 1) & 1, abort_flag))) break;
+            for (int c = 0; c < w.take; ++c) {
+                const int qs = q_ring.at;
+                if (!(ok = warp_wait_for(&sm.q_full[qs], q_ring.full(), abort_flag))) break;
+                if (!MANY || !unseen(w.rows, w.t * kTile<MANY> + half * kKeys, ch.i0)) {
+                    const int buf = (MANY ? 2 * half : 0) + s_ring.at;
+                    if (s_ring.round > 0 && !(ok = warp_wait_for(&sm.s_empty[buf], s_ring.empty(), abort_flag))) break;
+                    s_ring.next(buffers);
                     tc_fence_after();
                     if (leader) {
+                        const uint64_t qa = sdesc_k128(smem_u32(sQ + qs * kH * q_half));
                         // (an address is 16 bytes a unit in a descriptor)
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            mma_bf16(tmem + buf * buf_cols, ka + (((half * kH + k / 4) * kKHalf + (k % 4) * 32) >> 4),
+                            mma_bf16(tmem + buf * buf_cols, ka + (((k / 4) * kKHalf + (k % 4) * 32) >> 4),
                                      qa + static_cast<uint32_t>(((k / 4) * q_half + (k % 4) * 32) >> 4), idesc, k > 0);
                         mma_commit(&sm.s_full[buf]);
                     }
-                    __syncwarp();
                 }
+                __syncwarp();
                 if (!ok) break;
                 if (MANY) {
                     if (leader) mma_commit(&sm.q_empty[qs]);
+                    q_ring.next(tp.q_stages);
                     ch.next();
                 }
             }
             if (!ok) break;
             if (leader) mma_commit(&sm.k_empty[ks]);
             if (!MANY && w.column_ends()) {
-                if (leader) mma_commit(&sm.q_empty[col % tp.q_stages]);
-                ++col;
+                if (leader) mma_commit(&sm.q_empty[q_ring.at]);
+                q_ring.next(tp.q_stages);
             }
             __syncwarp();
         }
@@ -448,12 +472,11 @@ __global__ void __launch_bounds__(kTcThreads<MANY>, 1) k_weigh_tc(const __grid_c
                 }
         } else {
             // a head's rows, 16 bytes a thread at a time, swizzled as the products read them
-            int col = 0;
             bool fresh = true;        // the first tile of a column here
             for (; ok && w.more; w.next()) {
                 if (fresh) {
-                    const int qs = col % tp.q_stages;
-                    if (col >= tp.q_stages && !(ok = warp_wait_for(&sm.q_empty[qs], (col / tp.q_stages - 1) & 1, abort_flag))) break;
+                    const int qs = q_ring.at;
+                    if (q_ring.round > 0 && !(ok = warp_wait_for(&sm.q_empty[qs], q_ring.empty(), abort_flag))) break;
                     const int total = min(tp.nq, tp.g * w.rows.count - tp.row0), padded = max(16, (total + 15) / 16 * 16);
                     const int tid = threadIdx.x - 32 * kRowsWarp;
                     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
@@ -487,7 +510,7 @@ __global__ void __launch_bounds__(kTcThreads<MANY>, 1) k_weigh_tc(const __grid_c
                 }
                 if (w.column_ends()) {
                     fresh = true;
-                    ++col;
+                    q_ring.next(tp.q_stages);
                 }
             }
         }
@@ -498,7 +521,7 @@ __global__ void __launch_bounds__(kTcThreads<MANY>, 1) k_weigh_tc(const __grid_c
             // the status: sequences that make no sense, blocks outside the pool.  (A wait that runs out flags it
             // two seconds later.)
             int bad = 0;
-            for (int b = warp; b < p.B; b += 4 * kGroups<MANY>) {
+            for (int b = warp; b < p.B; b += 4 * kGroups) {
                 const Rows r = rows_of(p, b);
                 if (!r.ok) {
                     bad = 1;
@@ -511,130 +534,89 @@ __global__ void __launch_bounds__(kTcThreads<MANY>, 1) k_weigh_tc(const __grid_c
                 }
             }
             if (bad) sm.bad = 1;
-            asm volatile("bar.sync 1, %0;" ::"n"(128 * kGroups<MANY>) : "memory");   // all of these warps come here, once, and wait for nobody else
+            asm volatile("bar.sync 1, %0;" ::"n"(128 * kGroups) : "memory");   // all of these warps come here, once, and wait for nobody else
             if (threadIdx.x == 0 && tp.row0 == 0) *static_cast<int4*>(p.ws) = make_int4(sm.bad ? SPEC_EINVAL : SPEC_OK, 0, 0, 0);
         }
         const unsigned long long c2 = pk2(p.scale * kL2e, p.scale * kL2e);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const int half = MANY ? grp >> 1 : 0;   // of the tile's keys
-        int u = 0, kt = 0, col = 0, use = 0;
-        for (; ok && w.more; w.next(), ++kt) {
-            const bool mine = MANY || (kt & 1) == grp;
-            const int k0 = w.t * kTile<MANY> + half * kKeys, j = k0 + key;   // of the group; of the thread
-            const int in_front = w.rows.n - w.rows.count;
-            // what the key has so far, on its way while the products run
-            const bool there = mine && (!MANY || !(grp & 1)) && j < w.rows.n && (!p.table || key_row(p, w.b, w.h, j) >= 0);
-            const int64_t at = (static_cast<int64_t>(w.b) * p.Hkv + w.h) * p.cap + j;
-            const bool fresh = j >= in_front;
-            float old = 0.f;
-            if (there && (!MANY || w.whole()) && (tp.row0 > 0 || (!fresh && p.decay != 0.f))) old = p.acc[at];
-            float sum = 0.f;
-            int qh;
-            typename Walk<MANY>::Chunks ch{};
-            if (MANY) ch = w.chunks(qh);
-            for (int c = 0; c < w.take; ++c, ++u) {
-                if (!mine) continue;
-                const int i0 = ch.i0;
-                if (MANY) ch.next();
-                const int ls = MANY ? u & 3 : col % tp.q_stages;
-                // many: also where the group has no part in the chunk, or it would give back a later turn of the slot
-                // in place of this one
-                if (MANY && !(ok = warp_wait_for(&sm.l_full[ls], (u >> 2) & 1, abort_flag))) break;
-                bool turn = !MANY;
-                if (MANY && !unseen(w.rows, k0, i0)) turn = (use++ & 1) == (grp & 1);
-                if (turn) {
-                    const int buf = MANY ? grp : u % tp.buffers, round = MANY ? (use - 1) >> 1 : u / tp.buffers;
-                    if (!MANY && !(ok = warp_wait_for(&sm.q_full[ls], (col / tp.q_stages) & 1, abort_flag))) break;
-                    if (!(ok = warp_wait_for(&sm.s_full[buf], round & 1, abort_flag))) break;
-                    tc_fence_after();
-                    const uint32_t s_addr = lane_base + buf * buf_cols;
-                    const float* nl2 = sm.nl2[ls];
-                    // columns that hold rows; whether all of them see all keys
-                    const int cols = MANY ? min(kChunk, w.rows.count - i0) : min(tp.nq, tp.g * w.rows.count - tp.row0);
-                    const bool plain = (!MANY || cols == kChunk) && k0 + kKeys - 1 <= in_front + i0;
-                    unsigned long long part = pk2(0.f, 0.f);
-                    if (MANY) {
-                        const int lo = j - in_front - i0;    // the first column that sees this key
-                        uint32_t r[2][16];
-                        tmem_ld16(s_addr, r[0]);
+        // column sums of key j where it lies, with what it had (`old`) on its way since the products began
+        auto there = [&](int j) { return j < w.rows.n && (!p.table || key_row(p, w.b, w.h, j) >= 0); };
+        auto place = [&](int j) { return (static_cast<int64_t>(w.b) * p.Hkv + w.h) * p.cap + j; };
+        auto had = [&](int j) { return tp.row0 > 0 || (j < w.rows.n - w.rows.count && p.decay != 0.f) ? p.acc[place(j)] : 0.f; };
+        auto store_sum = [&](int j, float old, float sum) {
+            p.acc[place(j)] = tp.row0 > 0 ? old + sum : fmaf(p.decay, old, sum);
+            if (j >= w.rows.n - w.rows.count && p.pos && tp.row0 == 0) p.pos[place(j)] = (p.seen ? p.seen[w.b] : w.rows.n) - w.rows.n + j;
+        };
+        if constexpr (MANY) {
+            constexpr int W = 32;
+            int u = 0;
+            Ring s_ring;                                     // the half's score buffers
+            for (; ok && w.more; w.next()) {
+                const int k0 = w.t * kTile<MANY>, in_front = w.rows.n - w.rows.count;
+                const int j = k0 + grp * kKeys + key;
+                const bool mine = w.whole() && there(j);
+                const float old = mine ? had(j) : 0.f;
+                float sum = 0.f;
+                int qh;
+                typename Walk<MANY>::Chunks ch = w.chunks(qh);
+                const int h0 = k0 + grp * kKeys;             // the group's half
+                for (int c = 0; c < w.take; ++c, ++u, ch.next()) {
+                    const int ls = u & 3;
+                    // (also for a chunk that the half does not see: else its slot would be given back for a later turn)
+                    if (!(ok = warp_wait_for(&sm.l_full[ls], (u >> 2) & 1, abort_flag))) break;
+                    if (!unseen(w.rows, h0, ch.i0)) {
+                        const int buf = 2 * grp + s_ring.at;
+                        const uint32_t parity = s_ring.full();
+                        s_ring.next(2);
+                        const float* nl2 = sm.nl2[ls];
+                        const uint32_t s_addr = lane_base + buf * buf_cols;
+                        unsigned long long part = pk2(0.f, 0.f);
+                        uint32_t r[2][W];
+                        unsigned long long l[2][W / 2];
+                        load_lse<W>(nl2, l[0]);
+                        if (!(ok = warp_wait_for(&sm.s_full[buf], parity, abort_flag))) break;
+                        tc_fence_after();
+                        load_scores(s_addr, r[0]);
+                        if (w.rows.count - ch.i0 >= kChunk && h0 + kKeys - 1 <= in_front + ch.i0) {   // all see all
 #pragma unroll
-                        for (int x = 0; x < kChunk; x += 16) {
-                            tmem_ld_wait();
-                            if (x + 16 < kChunk) tmem_ld16(s_addr + x + 16, r[(x / 16 + 1) & 1]);
-                            if (plain) {
-                                part = fadd2(part, weights16(r[x / 16 & 1], nl2 + x, c2));
-                            } else {
-                                uint32_t seen = lo <= x ? 0xffffu : lo >= x + 16 ? 0u : 0xffffu << (lo - x);
-                                seen = cols >= x + 16 ? seen : cols <= x ? 0u : seen & ~(~0u << (cols - x));
-                                if (__any_sync(0xffffffffu, seen)) part = fadd2(part, masked16(r[x / 16 & 1], nl2 + x, c2, seen));
-                            }
-                        }
-                    } else if (plain) {
-                        const int steps = max(1, (cols + 15) / 16);
-                        uint32_t r[2][16];
-                        tmem_ld16(s_addr, r[0]);
-#pragma unroll 1
-                        for (int x = 0; x < steps; x += 2) {
-                            tmem_ld_wait();
-                            if (x + 1 < steps) tmem_ld16(s_addr + 16 * (x + 1), r[1]);
-                            part = fadd2(part, weights16(r[0], nl2 + 16 * x, c2));
-                            if (x + 1 < steps) {
+                            for (int x = 0; x < kChunk; x += W) {
+                                const int now = x / W & 1, next = now ^ 1;
+                                if (x + W < kChunk) load_lse<W>(nl2 + x + W, l[next]);
                                 tmem_ld_wait();
-                                if (x + 2 < steps) tmem_ld16(s_addr + 16 * (x + 2), r[0]);
-                                part = fadd2(part, weights16(r[1], nl2 + 16 * (x + 1), c2));
+                                if (x + W < kChunk) load_scores(s_addr + x + W, r[next]);
+                                part = fadd2(part, weights(r[now], l[now], c2));
                             }
-                        }
-                    } else {
-                        float f0 = 0.f;
+                        } else {
+                            const int lo = h0 + key - in_front - ch.i0, cols = w.rows.count - ch.i0;   // columns from .. to that see this key
 #pragma unroll 1
-                        for (int x = 0; x < cols; x += 16) {
-                            uint32_t r[16];
-                            tmem_ld16(s_addr + x, r);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float v = ex2(fmaf(__uint_as_float(r[e]), p.scale * kL2e, nl2[x + e]));
-                                const bool sees = x + e < cols && j <= sm.last[ls][x + e];
-                                f0 += sees ? v : 0.f;
+                            for (int x = 0; x < kChunk; x += W) {
+                                uint32_t seen = lo <= x ? ~0u : lo >= x + W ? 0u : ~0u << (lo - x);
+                                seen = cols >= x + W ? seen : cols <= x ? 0u : seen & ~(~0u << (cols - x));
+                                if (x > 0) {
+                                    load_scores(s_addr + x, r[0]);
+                                    load_lse<W>(nl2 + x, l[0]);
+                                }
+                                tmem_ld_wait();
+                                if (__any_sync(0xffffffffu, seen)) part = fadd2(part, masked(r[0], l[0], c2, seen));
                             }
                         }
-                        part = pk2(f0, 0.f);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.s_empty[buf]);
+                        float f0, f1;
+                        upk2(part, f0, f1);
+                        sum += f0 + f1;
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.s_empty[buf]);
-                    float f0, f1;
-                    upk2(part, f0, f1);
-                    sum += f0 + f1;
+                    if (lane == 0) mbar_arrive(&sm.l_empty[ls]);
                 }
-                if (MANY && lane == 0) mbar_arrive(&sm.l_empty[ls]);
-            }
-            if (!ok) break;
-            if (MANY) {
-                // the two groups of a half: the second one's sums through one of two buffers
-                const int x = 2 * (kt & 1) + half;
-                if (grp & 1) {
-                    if (kt >= 2 && !(ok = warp_wait_for(&sm.x_empty[x], (kt / 2 - 1) & 1, abort_flag))) break;
-                    sm.cross[x][key] = sum;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.x_full[x]);
+                if (!ok) break;
+                if (w.whole()) {
+                    if (mine) store_sum(j, old, sum);
                     continue;
                 }
-                if (!(ok = warp_wait_for(&sm.x_full[x], (kt / 2) & 1, abort_flag))) break;
-                sum += sm.cross[x][key];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.x_empty[x]);
-            }
-            if (!MANY && w.column_ends()) {
-                // (a group without a tile in this column waits for its rows all the same, as above)
-                if (!(ok = warp_wait_for(&sm.q_full[col % tp.q_stages], (col / tp.q_stages) & 1, abort_flag))) break;
-                if (lane == 0) mbar_arrive(&sm.q_empty[col % tp.q_stages]);
-                ++col;
-            }
-            if (MANY && !w.whole()) {
                 // a tile that another CTA has a part of: the join puts them together
                 const bool tail = w.c == 0;
-                tp.parts[(static_cast<int64_t>(blockIdx.x) * 2 + tail) * 2 * kKeys + half * kKeys + key] = sum;
+                tp.parts[(static_cast<int64_t>(blockIdx.x) * 2 + tail) * 2 * kKeys + grp * kKeys + key] = sum;
                 if (threadIdx.x == 0) {
                     Record& rec = tp.records[blockIdx.x];
                     if (tail) {
@@ -645,9 +627,70 @@ __global__ void __launch_bounds__(kTcThreads<MANY>, 1) k_weigh_tc(const __grid_c
                         rec.head_ends = w.c + w.take == w.head.chunks(w.t);
                     }
                 }
-            } else if (there) {
-                p.acc[at] = tp.row0 > 0 ? old + sum : fmaf(p.decay, old, sum);
-                if (fresh && p.pos && tp.row0 == 0) p.pos[at] = (p.seen ? p.seen[w.b] : w.rows.n) - w.rows.n + j;
+            }
+        } else {
+            Ring s_ring;
+            for (int u = 0; ok && w.more; w.next(), ++u, s_ring.next(tp.buffers)) {
+                const int cs = q_ring.at;
+                if ((u & 1) == grp) {
+                    const int k0 = w.t * kTile<MANY>, j = k0 + key;
+                    const bool mine = there(j);
+                    const float old = mine ? had(j) : 0.f;
+                    const int buf = s_ring.at;
+                    if (!(ok = warp_wait_for(&sm.q_full[cs], q_ring.full(), abort_flag))) break;
+                    if (!(ok = warp_wait_for(&sm.s_full[buf], s_ring.full(), abort_flag))) break;
+                    tc_fence_after();
+                    const uint32_t s_addr = lane_base + buf * buf_cols;
+                    const float* nl2 = sm.nl2[cs];
+                    const int cols = min(tp.nq, tp.g * w.rows.count - tp.row0);
+                    unsigned long long part = pk2(0.f, 0.f);
+                    if (k0 + kKeys - 1 <= w.rows.n - w.rows.count) {     // all rows see all keys
+                        const int steps = max(1, (cols + 15) / 16);
+                        uint32_t r[2][16];
+                        unsigned long long l[2][8];
+                        tmem_ld16(s_addr, r[0]);
+                        load_lse<16>(nl2, l[0]);
+#pragma unroll 1
+                        for (int x = 0; x < steps; x += 2) {
+                            if (x + 1 < steps) load_lse<16>(nl2 + 16 * (x + 1), l[1]);
+                            tmem_ld_wait();
+                            if (x + 1 < steps) tmem_ld16(s_addr + 16 * (x + 1), r[1]);
+                            part = fadd2(part, weights(r[0], l[0], c2));
+                            if (x + 1 < steps) {
+                                if (x + 2 < steps) load_lse<16>(nl2 + 16 * (x + 2), l[0]);
+                                tmem_ld_wait();
+                                if (x + 2 < steps) tmem_ld16(s_addr + 16 * (x + 2), r[0]);
+                                part = fadd2(part, weights(r[1], l[1], c2));
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int x = 0; x < cols; x += 16) {
+                            uint32_t r[16], seen = 0;
+                            tmem_ld16(s_addr + x, r);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (x + e < cols && j <= sm.last[cs][x + e]) seen |= 1u << e;
+                            unsigned long long l[8];
+                            load_lse<16>(nl2 + x, l);
+                            tmem_ld_wait();
+                            part = fadd2(part, masked(r, l, c2, seen));
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.s_empty[buf]);
+                    float f0, f1;
+                    upk2(part, f0, f1);
+                    if (mine) store_sum(j, old, f0 + f1);
+                }
+                if (w.column_ends()) {
+                    // (a group without a tile in this column waits for its rows all the same: else it would give back a later
+                    // turn of the slot in place of this one)
+                    if (!(ok = warp_wait_for(&sm.q_full[cs], q_ring.full(), abort_flag))) break;
+                    if (lane == 0) mbar_arrive(&sm.q_empty[cs]);
+                    q_ring.next(tp.q_stages);
+                }
             }
         }
     }
@@ -663,11 +706,17 @@ __global__ void __launch_bounds__(kTcThreads<MANY>, 1) k_weigh_tc(const __grid_c
     if (*abort_flag) {
         // a wait ran out: let this CTA's own loads and MMAs land before it ends
         if (warp == kTma) {
-            for (int i = max(0, k_loads - tp.k_stages); i < k_loads; ++i) mbar_wait(&sm.k_full[i % tp.k_stages], (i / tp.k_stages) & 1, 100000000ull);
-            if (MANY)
-                for (int i = max(0, q_loads - tp.q_stages); i < q_loads; ++i) mbar_wait(&sm.q_full[i % tp.q_stages], (i / tp.q_stages) & 1, 100000000ull);
+            // every slot's last load: its barrier's phase, if it ever had one
+            auto land = [&](uint64_t* full, const Ring& r, int n) {
+                for (int i = 0; i < n; ++i) {
+                    const uint32_t loads = r.round + (i < r.at ? 1 : 0);
+                    if (loads > 0) mbar_wait(&full[i], (loads - 1) & 1, 100000000ull);
+                }
+            };
+            land(sm.k_full, k_ring, tp.k_stages);
+            if (MANY) land(sm.q_full, q_ring, tp.q_stages);
         }
-        if (warp == kMma) mbar_wait(&sm.drain, 0, 100000000ull);
+        if (warp >= kMma && warp < kRowsWarp) mbar_wait(&sm.drain, 0, 100000000ull);
     }
     __syncthreads();
     if (warp == 0) {
@@ -723,7 +772,7 @@ static spec_status launch_tc(const Maps& m, TcParams& tp, cudaStream_t s) {
     auto kern = k_weigh_tc<D, MANY>;
     SPEC_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)));
     const int ctas = device_sm_count();
-    SPEC_CUDA_TRY(launch("kv_weigh_tc", kern, dim3(ctas), dim3(kTcThreads<MANY>), kSmem, s, m, tp));
+    SPEC_CUDA_TRY(launch("kv_weigh_tc", kern, dim3(ctas), dim3(kTcThreads), kSmem, s, m, tp));
     if (MANY) SPEC_CUDA_TRY(launch_ex("kv_weigh_join", k_weigh_join, dim3(ctas), dim3(2 * kKeys), 0, s, true, tp, ctas));
     return SPEC_OK;
 }
