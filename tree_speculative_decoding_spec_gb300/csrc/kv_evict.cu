@@ -23,7 +23,8 @@ namespace spec {
 namespace evict {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kCached = 24576;        // keys of a head whose ranks stay in shared memory
+constexpr int kCached = 49152;        // keys of a head whose ranks stay in shared memory
+constexpr int kBins = 2048;           // of a digit of 11 bits
 constexpr int kFew = 128;             // rows behind the budget that evict_pick moves itself
 constexpr int kGone = 64;             // keys to evict that are looked for one by one
 constexpr int kList = 512;            // candidates for them
@@ -45,9 +46,10 @@ struct Params {
     int row16;                        // 16-byte chunks of a row
     int here;                         // evict_pick moves the rows
     int in_place, cached;
-    int2* moves;                      // [B * Hkv][most]: (to, from)
-    int32_t* count;                   // [B * Hkv]
-    int most;
+    int2* moves;                      // [B * Hkv][most]: (to, from), ascending in both
+    int32_t* source;                  // another cache: [B * Hkv][places], where each place's key comes from
+    int32_t* count;                   // [B * Hkv]: moves, or places
+    int most, places;
     void* ws;
 };
 
@@ -181,7 +183,7 @@ __device__ int pick_few(Few& s, const Params& p, const float* acc, const int32_t
 
 __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
     extern __shared__ unsigned s_rank[];              // ranks of the keys, where they fit
-    __shared__ int s_hist[256];
+    __shared__ int s_hist[kBins];
     __shared__ int part[2][kWarps];
     __shared__ int s_digit, s_above;
     __shared__ Few few;
@@ -220,55 +222,63 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
         }
     }
     if (!all && found == moves) {
-        const bool cached = n <= p.cached;
         auto is_safe = [&](int i) {
             const int at = pos[i];
             return at < p.sink || at >= since;
         };
-        // number of protected keys
+        // ranks, and bits of the protected keys, come to shared memory where they fit
+        const bool cached = n <= p.cached;
+        unsigned* s_safe = s_rank + p.cached;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         int mine = 0;
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            mine += is_safe(i);
-            if (cached) s_rank[i] = order_key(acc[i]);
+#pragma unroll 4
+        for (int i0 = warp * 32; i0 < n; i0 += kThreads) {
+            const int i = i0 + lane;
+            const unsigned bits = __ballot_sync(0xffffffffu, i < n && is_safe(i));
+            if (cached) {
+                if (i < n) s_rank[i] = order_key(acc[i]);
+                if (lane == 0) s_safe[i0 / 32] = bits;
+            }
+            if (lane == 0) mine += __popc(bits);
         }
         int zero = 0, safe, none;
         scan2(part, mine, zero, safe, none);
+        auto rank_at = [&](int i) { return cached ? s_rank[i] : order_key(acc[i]); };
+        auto safe_at = [&](int i) { return cached ? (s_safe[i / 32] >> (i & 31) & 1u) != 0 : is_safe(i); };
         // all protected ones are kept and the best of the others, or the best of the protected ones
         const bool among_safe = safe > p.budget;
         int want = among_safe ? p.budget : p.budget - safe;
-        // the want-th largest rank of those in play, eight bits at a time
+        // the want-th largest rank of those in play, eleven bits at a time (the last time ten)
         unsigned prefix = 0, mask = 0;
         if (want > 0) {
-            for (int shift = 24; shift >= 0; shift -= 8) {
-                if (threadIdx.x < 256) s_hist[threadIdx.x] = 0;
+            for (int shift = 21; ; shift = max(shift - 11, 0)) {
+                const unsigned digits = shift ? kBins - 1 : (kBins >> 1) - 1;
+                for (int i = threadIdx.x; i < kBins; i += kThreads) s_hist[i] = 0;
                 __syncthreads();
+#pragma unroll 4
                 for (int i = threadIdx.x; i < n; i += kThreads) {
-                    const unsigned r = cached ? s_rank[i] : order_key(acc[i]);
-                    if ((r & mask) == prefix && is_safe(i) == among_safe) atomicAdd(&s_hist[(r >> shift) & 255], 1);
+                    const unsigned r = rank_at(i);
+                    if ((r & mask) == prefix && safe_at(i) == among_safe) atomicAdd(&s_hist[(r >> shift) & digits], 1);
                 }
                 __syncthreads();
-                if (threadIdx.x < 32) {
-                    // lane l has digits 255 - 8 l and the seven below
-                    int c[8], sum = 0;
-                    for (int j = 0; j < 8; ++j) sum += c[j] = s_hist[255 - 8 * threadIdx.x - j];
-                    int above = sum;
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int u = __shfl_up_sync(0xffffffffu, above, o);
-                        if (static_cast<int>(threadIdx.x) >= o) above += u;
+                // thread t has bins kBins - 1 - 4 t and the three below
+                constexpr int kEach = kBins / kThreads;
+                int c[kEach], above = 0, all_of, skip = 0;
+                for (int j = 0; j < kEach; ++j) above += c[j] = s_hist[kBins - 1 - kEach * threadIdx.x - j];
+                scan2(part, above, skip, all_of, none);
+                for (int j = 0; j < kEach; ++j) {
+                    if (above < want && above + c[j] >= want) {
+                        s_digit = kBins - 1 - kEach * threadIdx.x - j;
+                        s_above = above;
                     }
-                    above -= sum;
-                    for (int j = 0; j < 8; ++j) {
-                        if (above < want && above + c[j] >= want) {
-                            s_digit = 255 - 8 * threadIdx.x - j;
-                            s_above = above;
-                        }
-                        above += c[j];
-                    }
+                    above += c[j];
                 }
                 __syncthreads();
                 prefix |= static_cast<unsigned>(s_digit) << shift;
-                mask |= 255u << shift;
+                mask |= digits << shift;
                 want -= s_above;      // now: how many of those equal so far are wanted
+                if (shift == 0) break;
+                __syncthreads();      // s_digit has been read
             }
         }
         // a run of places per thread, of odd length so that their ranks lie in different banks
@@ -276,10 +286,10 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
         const int i0 = min(n, static_cast<int>(threadIdx.x) * run), i1 = min(n, i0 + run);
         // 2: kept, 1: kept if among the first `want` of its equals
         auto grade = [&](int i) {
-            const unsigned r = cached ? s_rank[i] : order_key(acc[i]);
-            const bool safe_one = is_safe(i);
+            const bool safe_one = safe_at(i);
             if (safe_one != among_safe) return safe_one ? 2 : 0;
             if (mask == 0) return 0;  // nothing wanted of these
+            const unsigned r = rank_at(i);
             return r > prefix ? 2 : r == prefix ? 1 : 0;
         };
         int equal = 0, skip = 0, t0, t1;
@@ -305,13 +315,22 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
         }
         __syncthreads();
     }
-    if (!p.in_place) {                // what stays at its place goes to the same place of the other cache
+    if (!p.in_place) {
+        // places from their own key, those of evicted ones from behind the budget
         const int m = min(n, p.budget);
-        for (int i = threadIdx.x; i < m; i += kThreads) {
-            acc_out[i] = acc[i];
-            pos_out[i] = pos[i];
-        }
+        int32_t* source = p.source + static_cast<size_t>(bh) * p.places;
+        for (int i = threadIdx.x; i < m; i += kThreads) source[i] = i;
         __syncthreads();
+        for (int i = threadIdx.x; i < count; i += kThreads) source[found[i].x] = found[i].y;
+        __syncthreads();
+#pragma unroll 4
+        for (int i = threadIdx.x; i < m; i += kThreads) {
+            const int j = source[i];
+            acc_out[i] = acc[j];
+            pos_out[i] = pos[j];
+        }
+        if (threadIdx.x == 0) p.count[bh] = m;
+        return;
     }
     for (int i = threadIdx.x; i < count; i += kThreads) {
         const int2 mv = found[i];
@@ -329,42 +348,47 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
 }
 
 constexpr int kMoveThreads = 256;
+constexpr int kBatch = 4;             // rows of K and V that a thread has under way
 
-// Rows of K and V.  In place: the moves.  To another cache: place i from place i, or from behind the
-// budget where a move fills it; the moves are in ascending order, so a place finds its own by bisection.
+// Rows of K and V, a thread per 16 bytes of a row of each.
 __global__ void __launch_bounds__(kMoveThreads) k_move(const Params p) {
     const int h = blockIdx.y % p.Hkv, b = blockIdx.y / p.Hkv, bh = blockIdx.y;
+    const int rows = kMoveThreads / p.row16, c = threadIdx.x % p.row16, row0 = threadIdx.x / p.row16;   // row16 <= 256
     griddep_wait();
+    if (row0 >= rows) return;
     const int count = p.count[bh];
     const int2* moves = p.moves + static_cast<size_t>(bh) * p.most;
-    int places = count;
-    if (!p.in_place) {
-        if (!__syncthreads_and(sound<kMoveThreads>(p, b, threadIdx.x))) return;
-        places = min(p.len[b], p.budget);
-    }
-    const int64_t units = static_cast<int64_t>(places) * p.row16 * 2;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x; u < units; u += static_cast<int64_t>(gridDim.x) * kMoveThreads) {
-        const int c = static_cast<int>(u % p.row16);
-        const int r = static_cast<int>(u / p.row16);
-        int2 mv;
-        if (p.in_place) {
-            mv = moves[r >> 1];
-        } else {
-            mv = make_int2(r >> 1, r >> 1);
-            int lo = 0, hi = count;
-            while (lo < hi) {
-                const int mid = (lo + hi) / 2;
-                if (moves[mid].x < mv.x) lo = mid + 1; else hi = mid;
-            }
-            if (lo < count && moves[lo].x == mv.x) mv.y = moves[lo].y;
+    const int32_t* source = p.source + static_cast<size_t>(bh) * p.places;
+    const uint4 *k = reinterpret_cast<const uint4*>(p.k), *v = reinterpret_cast<const uint4*>(p.v);
+    uint4 *ko = reinterpret_cast<uint4*>(p.k_out), *vo = reinterpret_cast<uint4*>(p.v_out);
+    const int step = gridDim.x * rows;
+    for (int r = blockIdx.x * rows + row0; r < count; r += kBatch * step) {
+        uint4 x[kBatch], y[kBatch];
+        int to[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int q = r + i * step;
+            if (q >= count) continue;
+            const int2 mv = p.in_place ? moves[q] : make_int2(q, source[q]);
+            to[i] = mv.x;
+            const int64_t src = row_at(p.table, p.max_blocks, p.rows, p.Hkv, b, h, mv.y) * p.row16 + c;
+            x[i] = k[src];
+            y[i] = v[src];
         }
-        move_chunk(p, b, h, mv, c, r & 1);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (r + i * step >= count) continue;
+            const int64_t dst = row_at(p.out_table, p.out_blocks, p.out_rows, p.Hkv, b, h, to[i]) * p.row16 + c;
+            ko[dst] = x[i];
+            vo[dst] = y[i];
+        }
     }
 }
 
-size_t bytes_for(int B, int Hkv, int most) {
+// (as much for a cache evicted in place as for another one)
+size_t bytes_for(int B, int Hkv, int most, int places) {
     const size_t heads = static_cast<size_t>(B) * Hkv;
-    return kWsHeader + round_up(heads * 4, 256) + round_up(heads * static_cast<size_t>(most) * sizeof(int2), 256);
+    return kWsHeader + round_up(heads * 4, 256) + round_up(heads * static_cast<size_t>(most) * sizeof(int2), 256) + heads * places * 4;
 }
 int most_moves(int cap, int budget) { return std::max(1, std::min(budget, cap - std::min(budget, cap))); }
 
@@ -415,19 +439,21 @@ spec_status run(Params& p, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s
     }
     p.row16 = D * es / 16;
     p.most = most_moves(p.cap, p.budget);
-    const size_t need = bytes_for(p.B, p.Hkv, p.most);
+    p.places = std::min(p.budget, p.cap);
+    const size_t need = bytes_for(p.B, p.Hkv, p.most, p.places);
     if (!p.ws || ws_bytes < need) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     if (!aligned16(p.ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
     p.count = reinterpret_cast<int32_t*>(static_cast<char*>(p.ws) + kWsHeader);
     p.moves = reinterpret_cast<int2*>(static_cast<char*>(p.ws) + kWsHeader + round_up(static_cast<size_t>(heads) * 4, 256));
+    p.source = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(p.moves) + round_up(static_cast<size_t>(heads) * p.most * sizeof(int2), 256));
     p.here = p.in_place && p.most <= kFew;
     p.cached = std::min(p.cap, kCached);
-    const size_t smem = static_cast<size_t>(p.cached) * 4;
-    if (smem > 40960) SPEC_CUDA_TRY(cudaFuncSetAttribute(k_pick, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4));
+    const size_t smem = static_cast<size_t>(p.cached) * 4 + (p.cached + 31) / 32 * 4;
+    if (smem > 30000) SPEC_CUDA_TRY(cudaFuncSetAttribute(k_pick, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4 + kCached / 8));
     SPEC_CUDA_TRY(launch("evict_pick", k_pick, dim3(p.Hkv + 1, p.B), dim3(kThreads), smem, s, p));
     if (!p.here) {
-        const int64_t places = p.in_place ? p.most : std::min(p.budget, p.cap);
-        const int64_t most = (places * p.row16 * 2 + kMoveThreads - 1) / kMoveThreads;
+        const int64_t rows = kBatch * (kMoveThreads / p.row16);
+        const int64_t most = ((p.in_place ? p.most : p.places) + rows - 1) / rows;
         const int64_t want = (16 * device_sm_count() + heads - 1) / heads;
         SPEC_CUDA_TRY(launch_ex("evict_move", k_move, dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min(most, want))), static_cast<unsigned>(heads)),
                                 dim3(kMoveThreads), 0, s, true, p));
@@ -443,7 +469,7 @@ using namespace spec;
 extern "C" size_t kv_evict_workspace_size(int32_t B, int32_t Hkv, int32_t Lmax, int32_t budget) {
     clear_error();
     if (evict::check_sizes(B, Hkv, Lmax, budget) != SPEC_OK) return 0;
-    return evict::bytes_for(B, Hkv, evict::most_moves(Lmax, budget));
+    return evict::bytes_for(B, Hkv, evict::most_moves(Lmax, budget), std::min(budget, Lmax));
 }
 
 extern "C" spec_status kv_evict(void* k_cache, void* v_cache, const int32_t* prefix_len, const int32_t* seen, float* acc,

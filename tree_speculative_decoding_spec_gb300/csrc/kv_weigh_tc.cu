@@ -716,8 +716,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
             land(sm.k_full, k_ring, tp.k_stages);
             if (MANY) land(sm.q_full, q_ring, tp.q_stages);
         }
-        if (warp >= kMma && warp < kRowsWarp) mbar_wait(&sm.drain, 0, 100000000ull);
     }
+    // the products' last arrivals too: no CTA ends before what it has set off has come
+    if (warp >= kMma && warp < kRowsWarp) mbar_wait(&sm.drain, 0, 100000000ull);
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
