@@ -223,7 +223,9 @@ EVICTS = [
     ("bf16", 3, 2, 128, 0, (40, 33, 20), 32, 4, 8),                   # one below the budget
     ("bf16", 2, 3, 64, 16, (2065, 2050), 2048, 4, 64),                # a step of a full cache
     ("f32", 2, 2, 20, 7, (500, 133), 60, 0, 0),
-    ("bf16", 1, 2, 128, 64, (30000,), 1000, 4, 100),                  # more keys than ranks fit shared memory
+    ("bf16", 1, 2, 128, 64, (30000,), 1000, 4, 100),
+    ("f32", 2, 1, 4, 0, (70000, 69), 40001, 3, 50),                   # more keys than ranks fit shared memory
+    ("bf16", 1, 1, 8, 0, (300,), 64, 0, 64),                          # nothing but the last keys
     ("f32", 1, 1, 4, 0, (1,), 1, 0, 0),                               # the smallest
     ("bf16", 2, 1, 8, 0, (700, 0), 1, 0, 1),
     ("bf16", 2, 2, 16, 0, (900, 513), 512, 100, 412),                 # protected keys fill the budget

@@ -49,6 +49,7 @@ struct Params {
     int2* moves;                      // [B * Hkv][most]: (to, from), ascending in both
     int32_t* source;                  // another cache: [B * Hkv][places], where each place's key comes from
     int32_t* count;                   // [B * Hkv]: moves, or places
+    unsigned* bits;                   // longer caches than shared memory has room for: three maps of bits for each head
     int most, places;
     void* ws;
 };
@@ -222,31 +223,39 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
         }
     }
     if (!all && found == moves) {
-        auto is_safe = [&](int i) {
-            const int at = pos[i];
-            return at < p.sink || at >= since;
-        };
-        // ranks, and bits of the protected keys, come to shared memory where they fit
+        // Ranks come to shared memory where they fit, and of each key a bit in one of three maps: protected; ranked
+        // above the border; equal to it.  What follows the ranks goes by words of 32 keys: with a look at every key
+        // of a thread's run instead, 16384 keys took 60 us where this takes XX.
         const bool cached = n <= p.cached;
-        unsigned* s_safe = s_rank + p.cached;
+        const int words = (n + 31) / 32;
+        unsigned *safe_bits, *above_bits, *equal_bits;
+        if (p.cap <= kCached) {
+            safe_bits = s_rank + p.cached;
+            above_bits = safe_bits + (p.cap + 31) / 32;
+            equal_bits = above_bits + (p.cap + 31) / 32;
+        } else {
+            safe_bits = p.bits + static_cast<size_t>(bh) * 3 * ((p.cap + 31) / 32);
+            above_bits = safe_bits + words;
+            equal_bits = above_bits + words;
+        }
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         int mine = 0;
 #pragma unroll 4
-        for (int i0 = warp * 32; i0 < n; i0 += kThreads) {
-            const int i = i0 + lane;
-            const unsigned bits = __ballot_sync(0xffffffffu, i < n && is_safe(i));
-            if (cached) {
-                if (i < n) s_rank[i] = order_key(acc[i]);
-                if (lane == 0) s_safe[i0 / 32] = bits;
+        for (int w = warp; w < words; w += kWarps) {
+            const int i = w * 32 + lane, at = i < n ? pos[i] : 0;
+            const unsigned bits = __ballot_sync(0xffffffffu, i < n && (at < p.sink || at >= since));
+            if (cached && i < n) s_rank[i] = order_key(acc[i]);
+            if (lane == 0) {
+                safe_bits[w] = bits;
+                mine += __popc(bits);
             }
-            if (lane == 0) mine += __popc(bits);
         }
         int zero = 0, safe, none;
         scan2(part, mine, zero, safe, none);
         auto rank_at = [&](int i) { return cached ? s_rank[i] : order_key(acc[i]); };
-        auto safe_at = [&](int i) { return cached ? (s_safe[i / 32] >> (i & 31) & 1u) != 0 : is_safe(i); };
         // all protected ones are kept and the best of the others, or the best of the protected ones
         const bool among_safe = safe > p.budget;
+        const unsigned flip = among_safe ? 0u : ~0u;     // safe_bits[w] ^ flip: keys in play
         int want = among_safe ? p.budget : p.budget - safe;
         // the want-th largest rank of those in play, eleven bits at a time (the last time ten)
         unsigned prefix = 0, mask = 0;
@@ -256,16 +265,19 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
                 for (int i = threadIdx.x; i < kBins; i += kThreads) s_hist[i] = 0;
                 __syncthreads();
 #pragma unroll 4
-                for (int i = threadIdx.x; i < n; i += kThreads) {
-                    const unsigned r = rank_at(i);
-                    if ((r & mask) == prefix && safe_at(i) == among_safe) atomicAdd(&s_hist[(r >> shift) & digits], 1);
+                for (int w = warp; w < words; w += kWarps) {
+                    const int i = w * 32 + lane;
+                    const unsigned r = i < n ? rank_at(i) : 0;
+                    if (i < n && (r & mask) == prefix && ((safe_bits[w] ^ flip) >> lane & 1)) atomicAdd(&s_hist[(r >> shift) & digits], 1);
                 }
                 __syncthreads();
                 // thread t has bins kBins - 1 - 4 t and the three below
                 constexpr int kEach = kBins / kThreads;
                 int c[kEach], above = 0, all_of, skip = 0;
+#pragma unroll
                 for (int j = 0; j < kEach; ++j) above += c[j] = s_hist[kBins - 1 - kEach * threadIdx.x - j];
                 scan2(part, above, skip, all_of, none);
+#pragma unroll
                 for (int j = 0; j < kEach; ++j) {
                     if (above < want && above + c[j] >= want) {
                         s_digit = kBins - 1 - kEach * threadIdx.x - j;
@@ -280,38 +292,45 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
                 if (shift == 0) break;
                 __syncthreads();      // s_digit has been read
             }
+#pragma unroll 4
+            for (int w = warp; w < words; w += kWarps) {
+                const int i = w * 32 + lane;
+                const unsigned r = i < n ? rank_at(i) : 0, play = safe_bits[w] ^ flip;
+                const unsigned up = __ballot_sync(0xffffffffu, i < n && r > prefix) & play, eq = __ballot_sync(0xffffffffu, i < n && r == prefix) & play;
+                if (lane == 0) {
+                    above_bits[w] = among_safe ? up : up | safe_bits[w];
+                    equal_bits[w] = eq;
+                }
+            }
         }
-        // a run of places per thread, of odd length so that their ranks lie in different banks
-        const int run = (n + kThreads - 1) / kThreads | 1;
-        const int i0 = min(n, static_cast<int>(threadIdx.x) * run), i1 = min(n, i0 + run);
-        // 2: kept, 1: kept if among the first `want` of its equals
-        auto grade = [&](int i) {
-            const bool safe_one = safe_at(i);
-            if (safe_one != among_safe) return safe_one ? 2 : 0;
-            if (mask == 0) return 0;  // nothing wanted of these
-            const unsigned r = rank_at(i);
-            return r > prefix ? 2 : r == prefix ? 1 : 0;
-        };
+        __syncthreads();
+        // a run of words per thread: the equal ones that are kept are the first `want`; then holes in front of the
+        // budget and kept keys behind it
+        const int run = (words + kThreads - 1) / kThreads;
+        const int w0 = min(words, static_cast<int>(threadIdx.x) * run), w1 = min(words, w0 + run);
         int equal = 0, skip = 0, t0, t1;
-        for (int i = i0; i < i1; ++i) equal += grade(i) == 1;
+        if (want > 0)
+            for (int w = w0; w < w1; ++w) equal += __popc(equal_bits[w]);
         scan2(part, equal, skip, t0, t1);
-        int holes = 0, late = 0, e = equal;
-        for (int i = i0; i < i1; ++i) {
-            const int g = grade(i);
-            const bool kept = g == 2 || (g == 1 && e++ < want);
-            if (i < p.budget) holes += !kept; else late += kept;
+        int holes = 0, late = 0;
+        auto in_front = [&](int w) {  // keys of the word in front of the budget
+            const int k = p.budget - w * 32;
+            return k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1;
+        };
+        auto inside = [&](int w) { return n - w * 32 >= 32 ? ~0u : (1u << (n - w * 32)) - 1; };
+        for (int w = w0; w < w1; ++w) {
+            unsigned kept = mask ? above_bits[w] : safe_bits[w];     // (nothing wanted beside the protected ones)
+            if (want > 0)
+                for (unsigned eq = equal_bits[w]; eq && equal < want; eq &= eq - 1, ++equal) kept |= eq & -eq;
+            above_bits[w] = kept;
+            holes += __popc(in_front(w) & inside(w) & ~kept);
+            late += __popc(kept & ~in_front(w));
         }
         scan2(part, holes, late, t0, t1);
         count = t0;                   // as many keys come from behind the budget as there are holes in front
-        e = equal;
-        for (int i = i0; i < i1; ++i) {
-            const int g = grade(i);
-            const bool kept = g == 2 || (g == 1 && e++ < want);
-            if (i < p.budget) {
-                if (!kept) moves[holes++].x = i;
-            } else if (kept) {
-                moves[late++].y = i;
-            }
+        for (int w = w0; w < w1; ++w) {
+            for (unsigned m = in_front(w) & inside(w) & ~above_bits[w]; m; m &= m - 1) moves[holes++].x = w * 32 + __ffs(m) - 1;
+            for (unsigned m = above_bits[w] & ~in_front(w); m; m &= m - 1) moves[late++].y = w * 32 + __ffs(m) - 1;
         }
         __syncthreads();
     }
@@ -385,12 +404,13 @@ __global__ void __launch_bounds__(kMoveThreads) k_move(const Params p) {
     }
 }
 
-// (as much for a cache evicted in place as for another one)
-size_t bytes_for(int B, int Hkv, int most, int places) {
-    const size_t heads = static_cast<size_t>(B) * Hkv;
-    return kWsHeader + round_up(heads * 4, 256) + round_up(heads * static_cast<size_t>(most) * sizeof(int2), 256) + heads * places * 4;
-}
 int most_moves(int cap, int budget) { return std::max(1, std::min(budget, cap - std::min(budget, cap))); }
+// (as much for a cache evicted in place as for another one)
+size_t bytes_for(int B, int Hkv, int cap, int budget) {
+    const size_t heads = static_cast<size_t>(B) * Hkv;
+    return kWsHeader + round_up(heads * 4, 256) + round_up(heads * static_cast<size_t>(most_moves(cap, budget)) * sizeof(int2), 256) +
+           round_up(heads * std::min(budget, cap) * 4, 256) + (cap > kCached ? heads * 3 * ((cap + 31) / 32) * 4 : 0);
+}
 
 spec_status check_sizes(int B, int Hkv, int64_t cap, int budget) {
     if (B < 1 || B > 65535) return fail(SPEC_EINVAL, "B = %d out of 1..65535", B);
@@ -440,16 +460,17 @@ spec_status run(Params& p, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s
     p.row16 = D * es / 16;
     p.most = most_moves(p.cap, p.budget);
     p.places = std::min(p.budget, p.cap);
-    const size_t need = bytes_for(p.B, p.Hkv, p.most, p.places);
+    const size_t need = bytes_for(p.B, p.Hkv, p.cap, p.budget);
     if (!p.ws || ws_bytes < need) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     if (!aligned16(p.ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
     p.count = reinterpret_cast<int32_t*>(static_cast<char*>(p.ws) + kWsHeader);
     p.moves = reinterpret_cast<int2*>(static_cast<char*>(p.ws) + kWsHeader + round_up(static_cast<size_t>(heads) * 4, 256));
     p.source = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(p.moves) + round_up(static_cast<size_t>(heads) * p.most * sizeof(int2), 256));
+    p.bits = reinterpret_cast<unsigned*>(reinterpret_cast<char*>(p.source) + round_up(static_cast<size_t>(heads) * p.places * 4, 256));
     p.here = p.in_place && p.most <= kFew;
     p.cached = std::min(p.cap, kCached);
-    const size_t smem = static_cast<size_t>(p.cached) * 4 + (p.cached + 31) / 32 * 4;
-    if (smem > 30000) SPEC_CUDA_TRY(cudaFuncSetAttribute(k_pick, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4 + kCached / 8));
+    const size_t smem = static_cast<size_t>(p.cached) * 4 + (p.cap <= kCached ? 3 * ((p.cap + 31) / 32) * 4 : 0);
+    if (smem > 30000) SPEC_CUDA_TRY(cudaFuncSetAttribute(k_pick, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4 + kCached / 8 * 3));
     SPEC_CUDA_TRY(launch("evict_pick", k_pick, dim3(p.Hkv + 1, p.B), dim3(kThreads), smem, s, p));
     if (!p.here) {
         const int64_t rows = kBatch * (kMoveThreads / p.row16);
@@ -469,7 +490,7 @@ using namespace spec;
 extern "C" size_t kv_evict_workspace_size(int32_t B, int32_t Hkv, int32_t Lmax, int32_t budget) {
     clear_error();
     if (evict::check_sizes(B, Hkv, Lmax, budget) != SPEC_OK) return 0;
-    return evict::bytes_for(B, Hkv, evict::most_moves(Lmax, budget), std::min(budget, Lmax));
+    return evict::bytes_for(B, Hkv, Lmax, budget);
 }
 
 extern "C" spec_status kv_evict(void* k_cache, void* v_cache, const int32_t* prefix_len, const int32_t* seen, float* acc,
