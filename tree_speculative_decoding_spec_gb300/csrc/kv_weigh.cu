@@ -22,11 +22,13 @@ constexpr int kKeys = 64;             // keys of a CTA
 constexpr int kGroups = 16;           // 16 groups of four keys by 16 groups of rows
 constexpr float kLog2e = 1.4426950408889634f;
 
-// One CTA per 64 keys of one (sequence, KV head), over all rows that see any of them, 16 RPT
-// at a time.  A thread has four keys and RPT rows; operands lie in shared memory by head dimension,
-// so that four keys come in one read.  CTA 0 of the first head writes the status.
+// CTAs per 64 keys of one (sequence, KV head), over the rows that see any of them, 16 RPT at a time; where there
+// are few such tiles their chunks of rows go to several CTAs in turn, whose sums kv_weigh_parts adds up in order
+// (a prompt of 100 rows and 8 heads of 64: 33 us with one, XX with splits).  A thread has four keys and RPT rows; operands
+// lie in shared memory by head dimension, so that four keys come in one read.  CTA 0 of the first head
+// writes the status.
 template <int D, int RPT>
-__global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p) {
+__global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p, int splits, float* parts) {
     constexpr int R = kGroups * RPT;
     extern __shared__ __align__(16) float smem[];
     float* ks = smem;                 // [D][kKeys]
@@ -34,12 +36,13 @@ __global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p) {
     __shared__ float s_lse[R];
     __shared__ int s_last[R];         // the last key that a row sees; -1: no row
     const int h = blockIdx.y, b = blockIdx.z;
+    griddep_launch();
     if (blockIdx.x == 0) {
         if (h == 0 && b == 0) check_all<kThreads>(p);
         return;
     }
     const Rows rows = rows_of(p, b);
-    const int k0 = (static_cast<int>(blockIdx.x) - 1) * kKeys;
+    const int split = (static_cast<int>(blockIdx.x) - 1) % splits, k0 = (static_cast<int>(blockIdx.x) - 1) / splits * kKeys;
     if (!rows.ok || k0 >= rows.n) return;
     const float* q = static_cast<const float*>(p.q);
     const float* k = static_cast<const float*>(p.k);
@@ -56,7 +59,7 @@ __global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p) {
     const int i0 = max(0, k0 - (rows.n - rows.count));   // the first row that sees a key of this tile
     const int per = rows.count - i0, total = g * per;
     float w[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int r0 = 0; r0 < total; r0 += R) {
+    for (int r0 = split * R; r0 < total; r0 += splits * R) {
         __syncthreads();
         if (threadIdx.x < R) {
             const int r = r0 + threadIdx.x;
@@ -113,19 +116,44 @@ __global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p) {
         if (j < rows.n && key_row(p, b, h, j) >= 0) {
             float sum = 0.f;
             for (int i = 0; i < kGroups; ++i) sum += sums[i * kKeys + threadIdx.x];
-            store(p, b, h, j, rows, sum);
+            if (splits == 1)
+                store(p, b, h, j, rows, sum);
+            else
+                parts[((static_cast<int64_t>(b) * p.Hkv + h) * splits + split) * p.cap + j] = sum;
         }
     }
 }
 
+__global__ void __launch_bounds__(kThreads) k_weigh_parts(const Params p, int splits, const float* parts) {
+    const int h = blockIdx.y, b = blockIdx.z, j = blockIdx.x * kThreads + threadIdx.x;
+    griddep_wait();
+    const Rows rows = rows_of(p, b);
+    if (!rows.ok || j >= rows.n || key_row(p, b, h, j) < 0) return;
+    const float* at = parts + (static_cast<int64_t>(b) * p.Hkv + h) * splits * p.cap + j;
+    float sum = 0.f;
+    for (int i = 0; i < splits; ++i) sum += at[static_cast<int64_t>(i) * p.cap];
+    store(p, b, h, j, rows, sum);
+}
+
+// CTAs of a tile: as many as fill the SMs twice, with a chunk of rows each.
+int splits_of(int B, int Hkv, int g, int T, int path_len, int cap) {
+    const int64_t rows = static_cast<int64_t>(g) * (path_len ? path_len : T);
+    if (rows <= kGroups) return 1;
+    const int64_t tiles = static_cast<int64_t>(B) * Hkv * ((cap + kKeys - 1) / kKeys);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(rows + 4 * kGroups - 1) / (4 * kGroups), 2 * device_sm_count() / tiles, 16})));
+}
+
 template <int D>
-spec_status run_fma(const Params& p, cudaStream_t s) {
+spec_status run_fma(const Params& p, float* parts, cudaStream_t s) {
     const int most = p.Hq / p.Hkv * (p.path ? p.P : p.T);
     const bool wide = most > kGroups;
+    const int splits = splits_of(p.B, p.Hkv, p.Hq / p.Hkv, p.T, p.path ? p.P : 0, p.cap);
     auto kern = wide ? k_weigh_fma<D, 4> : k_weigh_fma<D, 1>;
     const size_t smem = sizeof(float) * D * (kKeys + kGroups * (wide ? 4 : 1));
     if (smem > 40960) SPEC_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-    SPEC_CUDA_TRY(launch("kv_weigh_fma", kern, dim3((p.cap + kKeys - 1) / kKeys + 1, p.Hkv, p.B), dim3(kThreads), smem, s, p));
+    SPEC_CUDA_TRY(launch("kv_weigh_fma", kern, dim3((p.cap + kKeys - 1) / kKeys * splits + 1, p.Hkv, p.B), dim3(kThreads), smem, s, p, splits, parts));
+    if (splits > 1)
+        SPEC_CUDA_TRY(launch_ex("kv_weigh_parts", k_weigh_parts, dim3((p.cap + kThreads - 1) / kThreads, p.Hkv, p.B), dim3(kThreads), 0, s, true, p, splits, parts));
     return SPEC_OK;
 }
 
@@ -145,8 +173,10 @@ spec_status check_sizes(int B, int Hq, int Hkv, int T, int path_len, int64_t cap
     return SPEC_OK;
 }
 
-size_t bytes_for(int g, int T, int path_len, spec_dtype dt) {
-    return kWsHeader + (dt == SPEC_BF16 ? weigh_tc_bytes(g, T, path_len) : 0);
+size_t bytes_for(int B, int Hkv, int g, int T, int path_len, int cap, spec_dtype dt) {
+    if (dt == SPEC_BF16) return kWsHeader + weigh_tc_bytes(g, T, path_len);
+    const int splits = splits_of(B, Hkv, g, T, path_len, cap);
+    return kWsHeader + (splits > 1 ? static_cast<size_t>(B) * Hkv * splits * cap * sizeof(float) : 0);
 }
 
 spec_status run(Params& p, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s) {
@@ -171,12 +201,13 @@ spec_status run(Params& p, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s
     for (const auto& i : in)
         if (overlap(p.acc, out, i.x, i.n) || overlap(p.pos, out, i.x, i.n)) return fail(SPEC_EINVAL, "acc or pos overlaps an input");
     if (overlap(p.acc, out, p.pos, out)) return fail(SPEC_EINVAL, "acc overlaps pos");
-    const size_t need = bytes_for(p.Hq / p.Hkv, p.T, p.path ? p.P : 0, dt);
+    const size_t need = bytes_for(p.B, p.Hkv, p.Hq / p.Hkv, p.T, p.path ? p.P : 0, p.cap, dt);
     if (!p.ws || ws_bytes < need) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     if (!aligned16(p.ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
     if (p.scale == 0.f) p.scale = 1.f / sqrtf(static_cast<float>(D));
     if (dt == SPEC_BF16) return weigh_tc_run(p, D, static_cast<char*>(p.ws) + kWsHeader, s);
-    return D == 64 ? run_fma<64>(p, s) : run_fma<128>(p, s);
+    float* parts = reinterpret_cast<float*>(static_cast<char*>(p.ws) + kWsHeader);
+    return D == 64 ? run_fma<64>(p, parts, s) : run_fma<128>(p, parts, s);
 }
 
 }  // namespace weigh
@@ -188,7 +219,7 @@ extern "C" size_t kv_weigh_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, in
                                           int32_t D, spec_dtype dt) {
     clear_error();
     if (weigh::check_sizes(B, Hq, Hkv, T, path_len, Lmax, D, dt) != SPEC_OK) return 0;
-    return weigh::bytes_for(Hq / Hkv, T, path_len, dt);
+    return weigh::bytes_for(B, Hkv, Hq / Hkv, T, path_len, Lmax, dt);
 }
 
 extern "C" spec_status kv_weigh(const void* q, const float* lse, const void* k_cache, const int32_t* prefix_len,
