@@ -22,7 +22,6 @@
 namespace spec {
 namespace evict {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kCached = 49152;        // keys of a head whose ranks stay in shared memory
 constexpr int kBins = 2048;           // of a digit of 11 bits
 constexpr int kFew = 128;             // rows behind the budget that evict_pick moves itself
@@ -93,7 +92,7 @@ __device__ __forceinline__ void move_chunk(const Params& p, int b, int h, int2 m
 }
 
 // Exclusive prefix sums of two counts over the CTA; totals in t0, t1.
-__device__ __forceinline__ void scan2(int (&part)[2][kWarps], int& a, int& b, int& t0, int& t1) {
+template <int kWarps> __device__ __forceinline__ void scan2(int (&part)[2][kWarps], int& a, int& b, int& t0, int& t1) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int x = a, y = b;
     for (int o = 1; o < 32; o <<= 1) {
@@ -116,24 +115,41 @@ __device__ __forceinline__ void scan2(int (&part)[2][kWarps], int& a, int& b, in
 
 // Few keys too many, a step's: the e = n - budget ones of the lowest (protected, weight, higher place first) are
 // among the e / warps lowest of each warp's threads or below the largest of those, some tens in all, and
-// are ranked by counting.  Two passes over the keys and no histogram: 24 us became 9 for 512 heads of 2065.
+// are ranked by counting.  Two passes over the keys and no histogram: 24 us became 12 for 512 heads of 2065.
 // Returns the moves, in s_moves, or -1 where too many keys are equal to tell them apart so.
 struct Few {
     unsigned long long list[kList], gone_late;
     int2 moves[kGone];
     int gone[kGone];
-    unsigned bound[kWarps];
+    unsigned bound[32];
     int count;
 };
-__device__ int pick_few(Few& s, const Params& p, const float* acc, const int32_t* pos, int n, int64_t since) {
+template <int kThreads> __device__ __noinline__ int pick_few(Few& s, const Params& p, const float* acc, const int32_t* pos, int n, int64_t since) {
+    constexpr int kWarps = kThreads / 32, kKeep = 8;   // keys a thread has in registers; the others are read twice
     const int e = n - p.budget, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto key_of = [&](int i) {
-        const int at = pos[i];
+    auto key = [&](int i, int at, float x) {
         const unsigned long long safe = at < p.sink || at >= since;
-        return (safe << 54) | (static_cast<unsigned long long>(order_key(acc[i])) << 22) | static_cast<unsigned>((1 << 22) - 1 - i);
+        return (safe << 54) | (static_cast<unsigned long long>(order_key(x)) << 22) | static_cast<unsigned>((1 << 22) - 1 - i);
     };
+    int at[kKeep];
+    float x[kKeep];
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) {
+        const int i = threadIdx.x + k * kThreads;
+        if (i < n) {
+            at[k] = pos[i];
+            x[k] = acc[i];
+        }
+    }
+    unsigned long long kept[kKeep];
     unsigned low = 0xffffffffu;
-    for (int i = threadIdx.x; i < n; i += kThreads) low = min(low, static_cast<unsigned>(key_of(i) >> 23));
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) {
+        const int i = threadIdx.x + k * kThreads;
+        kept[k] = i < n ? key(i, at[k], x[k]) : ~0ull;
+        low = min(low, static_cast<unsigned>(kept[k] >> 23));
+    }
+    for (int i = threadIdx.x + kKeep * kThreads; i < n; i += kThreads) low = min(low, static_cast<unsigned>(key(i, pos[i], acc[i]) >> 23));
     unsigned kth = 0;
     for (int k = 0; k < (e + kWarps - 1) / kWarps; ++k) {
         kth = __reduce_min_sync(0xffffffffu, low);
@@ -148,23 +164,25 @@ __device__ int pick_few(Few& s, const Params& p, const float* acc, const int32_t
     __syncthreads();
     unsigned bound = s.bound[0];
     for (int i = 1; i < kWarps; ++i) bound = max(bound, s.bound[i]);
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const unsigned long long key = key_of(i);
-        if (static_cast<unsigned>(key >> 23) <= bound) {
+    auto offer = [&](unsigned long long k) {
+        if (static_cast<unsigned>(k >> 23) <= bound && k != ~0ull) {
             const int at = atomicAdd(&s.count, 1);
-            if (at < kList) s.list[at] = key;
+            if (at < kList) s.list[at] = k;
         }
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) offer(kept[k]);
+    for (int i = threadIdx.x + kKeep * kThreads; i < n; i += kThreads) offer(key(i, pos[i], acc[i]));
     __syncthreads();
     const int m = s.count;
     if (m > kList) return -1;
     for (int i = threadIdx.x; i < m; i += kThreads) {
-        const unsigned long long key = s.list[i];
+        const unsigned long long k = s.list[i];
         int rank = 0;
 #pragma unroll 4
-        for (int j = 0; j < m; ++j) rank += s.list[j] < key;
+        for (int j = 0; j < m; ++j) rank += s.list[j] < k;
         if (rank < e) {
-            const int at = (1 << 22) - 1 - static_cast<int>(key & ((1 << 22) - 1));
+            const int at = (1 << 22) - 1 - static_cast<int>(k & ((1 << 22) - 1));
             s.gone[rank] = at < p.budget ? at : -1;
             if (at >= p.budget) atomicOr(&s.gone_late, 1ull << (at - p.budget));
         }
@@ -182,7 +200,9 @@ __device__ int pick_few(Few& s, const Params& p, const float* acc, const int32_t
     return __popcll(late);
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
+    constexpr int kWarps = kThreads / 32;
     extern __shared__ unsigned s_rank[];              // ranks of the keys, where they fit
     __shared__ int s_hist[kBins];
     __shared__ int part[2][kWarps];
@@ -216,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
     int count = 0;
     const int64_t since = static_cast<int64_t>(p.seen ? p.seen[b] : n) - p.recent;
     if (!all && n - p.budget <= kGone) {
-        count = pick_few(few, p, acc, pos, n, since);
+        count = pick_few<kThreads>(few, p, acc, pos, n, since);
         if (count >= 0) {
             found = few.moves;
             if (!p.here && static_cast<int>(threadIdx.x) < count) moves[threadIdx.x] = few.moves[threadIdx.x];
@@ -493,8 +513,11 @@ spec_status run(Params& p, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s
     p.here = p.in_place && p.most <= kFew;
     p.cached = std::min(p.cap, kCached);
     const size_t smem = static_cast<size_t>(p.cached) * 4 + (p.cap <= kCached ? 3 * ((p.cap + 31) / 32) * 4 : 0);
-    if (smem > 30000) SPEC_CUDA_TRY(cudaFuncSetAttribute(k_pick, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4 + kCached / 8 * 3));
-    SPEC_CUDA_TRY(launch("evict_pick", k_pick, dim3(p.Hkv + 1, p.B), dim3(kThreads), smem, s, p));
+    // a full cache's step is a chain of short stages, which 256 threads go through fastest (8.1 us for 512 heads of 2065 keys, 512 threads
+    // 11.5); longer caches, few of which share an SM anyway, get all of its threads
+    auto pick = p.cap <= 4096 ? k_pick<256> : k_pick<1024>;
+    if (smem > 30000) SPEC_CUDA_TRY(cudaFuncSetAttribute(pick, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4 + kCached / 8 * 3));
+    SPEC_CUDA_TRY(launch("evict_pick", pick, dim3(p.Hkv + 1, p.B), dim3(p.cap <= 4096 ? 256 : 1024), smem, s, p));
     if (!p.here) {
         const int64_t rows = kBatch * (kMoveThreads / p.row16);
         const int64_t most = ((p.in_place ? p.most : p.places) + rows - 1) / rows;

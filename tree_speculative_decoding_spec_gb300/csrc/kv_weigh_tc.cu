@@ -481,24 +481,38 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                     const int tid = threadIdx.x - 32 * kRowsWarp;
                     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
                     const int64_t q0 = static_cast<int64_t>(w.b) * p.Hq + w.h * tp.g;
-                    for (int x = tid; x < padded * (D / 8); x += 64) {
-                        const int r = x / (D / 8), part = x % (D / 8);
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (r < total) {
-                            const int rr = tp.row0 + r, gi = rr / w.rows.count;
-                            const int64_t row = (q0 + gi) * p.T + node_of(p, w.b, rr - gi * w.rows.count);
-                            v = *reinterpret_cast<const uint4*>(q + row * D + part * 8);
+                    auto row_of = [&](int r) {       // a row of q and lse
+                        const int rr = tp.row0 + r, gi = rr / w.rows.count;
+                        return (q0 + gi) * p.T + node_of(p, w.b, rr - gi * w.rows.count);
+                    };
+                    constexpr int kAhead = 8;        // loads of a thread on their way together
+                    for (int x0 = tid; x0 < padded * (D / 8); x0 += 64 * kAhead) {
+                        int64_t row[kAhead];
+                        uint4 v[kAhead];
+#pragma unroll
+                        for (int k = 0; k < kAhead; ++k) {
+                            const int r = (x0 + 64 * k) / (D / 8);
+                            row[k] = r < total ? row_of(r) : -1;
                         }
-                        *reinterpret_cast<uint4*>(sQ + (qs * kH + part / 8) * q_half + r * 128 + ((part % 8) ^ (r & 7)) * 16) = v;
+#pragma unroll
+                        for (int k = 0; k < kAhead; ++k) {
+                            v[k] = make_uint4(0u, 0u, 0u, 0u);
+                            if (row[k] >= 0) v[k] = *reinterpret_cast<const uint4*>(q + row[k] * D + (x0 + 64 * k) % (D / 8) * 8);
+                        }
+#pragma unroll
+                        for (int k = 0; k < kAhead; ++k) {
+                            const int x = x0 + 64 * k, r = x / (D / 8), part = x % (D / 8);
+                            if (r < padded) *reinterpret_cast<uint4*>(sQ + (qs * kH + part / 8) * q_half + r * 128 + ((part % 8) ^ (r & 7)) * 16) = v[k];
+                        }
                     }
+#pragma unroll 4
                     for (int r = tid; r < padded; r += 64) {
                         float x = -INFINITY;
                         int last = -1;
                         if (r < total) {
-                            const int rr = tp.row0 + r, gi = rr / w.rows.count, i = rr - gi * w.rows.count;
-                            const float l = p.lse[(q0 + gi) * p.T + node_of(p, w.b, i)];
+                            const float l = p.lse[row_of(r)];
                             if (isfinite(l)) x = -l * kL2e;
-                            last = w.rows.n - w.rows.count + i;
+                            last = w.rows.n - w.rows.count + (tp.row0 + r) % w.rows.count;
                         }
                         sm.nl2[qs][r] = x;
                         sm.last[qs][r] = last;
