@@ -1031,17 +1031,26 @@ def beam_select(logits, scores, K, eos=-1, ended=None, length=None, alpha=0.0, t
     K, eos = _whole(K, "K"), _whole(eos, "eos")
     if not 1 <= K <= SPEC_MAX_BEAMS:
         raise ValueError(f"K = {K} out of 1..{SPEC_MAX_BEAMS}")
-    token = _new(stream, index, _i32, B, K) if token is None else token
-    parent = _new(stream, index, _i32, B, K) if parent is None else parent
-    score = _new(stream, index, torch.float32, B, K) if score is None else score
-    ended_out = _new(stream, index, _i32, B, K) if ended_out is None else ended_out
-    length_out = _new(stream, index, _i32, B, K) if length_out is None else length_out
+    if token is parent is score is ended_out is length_out is None:
+        # one allocation for the five: it costs twice what the checks of an argument do
+        out = _new(stream, index, _i32, 5, B, K)
+        token, parent, score, ended_out, length_out = out.unbind(0)
+        score = score.view(torch.float32)
+        at, n = out.data_ptr(), 4 * B * K
+        outs = at, at + n, at + 2 * n, at + 3 * n, at + 4 * n
+    else:
+        token = _new(stream, index, _i32, B, K) if token is None else token
+        parent = _new(stream, index, _i32, B, K) if parent is None else parent
+        score = _new(stream, index, torch.float32, B, K) if score is None else score
+        ended_out = _new(stream, index, _i32, B, K) if ended_out is None else ended_out
+        length_out = _new(stream, index, _i32, B, K) if length_out is None else length_out
+        outs = (_at(token, "token", _i32, index, B, K), _at(parent, "parent", _i32, index, B, K),
+                _at(score, "score", torch.float32, index, B, K), _at(ended_out, "ended_out", _i32, index, B, K),
+                _at(length_out, "length_out", _i32, index, B, K))
     if ws is None:
         ws = _sized(beam_select_workspace_size, index, stream, B, W, V, K)
-    _call("beam_select", index, stream, logits.data_ptr(), sw, sp, ep, np_, B, W, V, K, eos, float(alpha), dt,
-          _at(token, "token", _i32, index, B, K), _at(parent, "parent", _i32, index, B, K),
-          _at(score, "score", torch.float32, index, B, K), _at(ended_out, "ended_out", _i32, index, B, K),
-          _at(length_out, "length_out", _i32, index, B, K), _buffer(ws, index), ws.nbytes)
+    _call("beam_select", index, stream, logits.data_ptr(), sw, sp, ep, np_, B, W, V, K, eos, float(alpha), dt, *outs, _buffer(ws, index),
+          ws.nbytes)
     return token, parent, score, ended_out, length_out
 
 
@@ -1103,9 +1112,11 @@ def kv_weigh_workspace_size(B, Hq, Hkv, T, path_len, Lmax, D, dtype):
     return int(n)
 
 
-def _weigh(name, q, lse, keys, prefix_len, acc, pos, seen, n_rows, accept_len, accept_path, decay, scale, ws, stream, Hkv, cap, dims):
-    """What both forms of kv_weigh have in common; `keys` say where the keys are, `dims` is what follows T."""
-    index, dtype, dt, (B, Hq, T, D) = _queries(q)
+def _weigh(name, rows, q, lse, keys, prefix_len, acc, pos, seen, n_rows, accept_len, accept_path, decay, scale, ws, stream, Hkv, cap,
+           dims):
+    """What both forms of kv_weigh have in common; `rows` is what _queries says of q, `keys` say where the keys are, `dims`
+    is what follows T."""
+    index, dtype, dt, (B, Hq, T, D) = rows
     qp, lp = _at(q, "q", dtype, index, B, Hq, T, D), _at(lse, "lse", torch.float32, index, B, Hq, T)
     pp = _at(prefix_len, "prefix_len", _i32, index, B)
     ap = _at(acc, "acc", torch.float32, index, B, Hkv, cap)
@@ -1130,20 +1141,20 @@ def kv_weigh(q, lse, k_cache, prefix_len, acc, pos=None, seen=None, n_rows=None,
 
     q [B, Hq, T, D] and lse [B, Hq, T] of an attention; prefix_len [B] with the rows' own keys in it; the rows are
     the first n_rows[b] (None: T), or the nodes of accept_path (tree_accept).  pos [B, Hkv, Lmax] int32: see kv_evict."""
-    index, dtype, _, (B, _, _, D) = _queries(q)
+    rows = index, dtype, _, (B, _, _, D) = _queries(q)
     _, Hkv, Lmax, _ = _queries(k_cache, "k_cache")[3]
-    return _weigh("kv_weigh", q, lse, (_at(k_cache, "k_cache", dtype, index, B, Hkv, Lmax, D),), prefix_len, acc, pos, seen, n_rows,
+    return _weigh("kv_weigh", rows, q, lse, (_at(k_cache, "k_cache", dtype, index, B, Hkv, Lmax, D),), prefix_len, acc, pos, seen, n_rows,
                   accept_len, accept_path, decay, scale, ws, stream, Hkv, Lmax, (Lmax,))
 
 
 def kv_weigh_paged(q, lse, k_pool, block_table, prefix_len, acc, pos=None, seen=None, n_rows=None, accept_len=None,
                    accept_path=None, decay=1.0, scale=None, ws=None, stream=None):
     """kv_weigh over a paged cache: pool [num_blocks, Hkv, block_size, D], acc and pos [B, Hkv, max_blocks * block_size]."""
-    index, dtype, _, (B, _, _, D) = _queries(q)
+    rows = index, dtype, _, (B, _, _, D) = _queries(q)
     blocks, Hkv, bs, _ = _pool(k_pool)
     most = block_table.shape[1] if isinstance(block_table, _Tensor) and block_table.dim() == 2 else 0
     keys = (_at(k_pool, "k_pool", dtype, index, blocks, Hkv, bs, D), blocks, _at(block_table, "block_table", _i32, index, B, most), most, bs)
-    return _weigh("kv_weigh_paged", q, lse, keys, prefix_len, acc, pos, seen, n_rows, accept_len, accept_path, decay, scale, ws, stream,
+    return _weigh("kv_weigh_paged", rows, q, lse, keys, prefix_len, acc, pos, seen, n_rows, accept_len, accept_path, decay, scale, ws, stream,
                   Hkv, most * bs, ())
 
 
