@@ -592,15 +592,17 @@ __global__ void __launch_bounds__(kThreads) k_join(const Params p) {
     }
 }
 
-// Slices of a row: the number that makes the longest SM's work least, in units of a chunk.  A slice's start and end
-// cost some three and a half chunks, a candidate in the join a two-thousandth.
+// Slices of a row: the number that makes the longest SM's work least, in units of a chunk, some 0.4 us: a slice costs its
+// chunks and 2.6 more to start and end, a lone one is as long as 6 and 1.4 times its chunks, a candidate in the
+// join a two-thousandth.  (768 rows of 131072: 57 us in one slice, 63 in two, 71 in four; 128 rows of 32000: 12.5, 11.7, 12.5;
+// 30 rows of 50257: 13.3 in four, 11.4 in twelve.)
 int slices_of(int64_t rows, int W, int V, int K) {
     const int64_t sms = device_sm_count();
     const double chunks = V / static_cast<double>(kThreads * kVecs * 8);
     int best = 1;
     double least = 1e300;
     for (int s = 1; s <= kMaxSlices; ++s) {
-        const double cost = static_cast<double>((rows * s + sms - 1) / sms) * (3.5 + chunks / s) + 5e-4 * s * K * W;
+        const double each = chunks / s, cost = std::max(6.0 + 1.4 * each, static_cast<double>((rows * s + sms - 1) / sms) * (2.6 + each)) + 5e-4 * s * K * W;
         if (cost < least) {
             least = cost;
             best = s;

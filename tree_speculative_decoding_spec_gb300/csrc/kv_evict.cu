@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
     }
     if (!all && found == moves) {
         // Ranks come to shared memory where they fit, and of each key a bit in one of three maps: protected; ranked
-        // above the border; equal to it.  What follows the ranks goes by words of 32 keys: with a look at every key
-        // of a thread's run instead, 16384 keys took 60 us where this takes XX.
+        // above the border; equal to it.  What follows the ranks goes by words of 32 keys: with a look at every
+        // key of a thread's run instead it took 5 us more for 16384 keys.
         const bool cached = n <= p.cached;
         const int words = (n + 31) / 32;
         unsigned *safe_bits, *above_bits, *equal_bits;
@@ -259,6 +259,9 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
             equal_bits = above_bits + words;
         }
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        // (the first digit's histogram of the others on the way: it serves unless the protected ones are too many)
+        for (int i = threadIdx.x; i < kBins; i += kThreads) s_hist[i] = 0;
+        __syncthreads();
         int mine = 0;
         constexpr int kAhead = 8;     // words of a warp on their way together (one by one: 33 us for 16384 keys)
         for (int w0 = warp; w0 < words; w0 += kAhead * kWarps) {
@@ -268,14 +271,18 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
             for (int k = 0; k < kAhead; ++k) {
                 const int i = (w0 + k * kWarps) * 32 + lane;
                 if (i < n) at[k] = pos[i];
-                if (i < n && cached) x[k] = acc[i];
+                if (i < n) x[k] = acc[i];
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int w = w0 + k * kWarps, i = w * 32 + lane;
                 if (w >= words) break;
                 const unsigned bits = __ballot_sync(0xffffffffu, i < n && (at[k] < p.sink || at[k] >= since));
-                if (cached && i < n) s_rank[i] = order_key(x[k]);
+                if (i < n) {
+                    const unsigned r = order_key(x[k]);
+                    if (cached) s_rank[i] = r;
+                    if (!(bits >> lane & 1)) atomicAdd(&s_hist[r >> 21], 1);
+                }
                 if (lane == 0) {
                     safe_bits[w] = bits;
                     mine += __popc(bits);
@@ -294,10 +301,13 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
         if (want > 0) {
             for (int shift = 21; ; shift = max(shift - 11, 0)) {
                 const unsigned digits = shift ? kBins - 1 : (kBins >> 1) - 1;
-                for (int i = threadIdx.x; i < kBins; i += kThreads) s_hist[i] = 0;
-                __syncthreads();
+                const bool have = shift == 21 && !among_safe;
+                if (!have) {
+                    for (int i = threadIdx.x; i < kBins; i += kThreads) s_hist[i] = 0;
+                    __syncthreads();
+                }
 #pragma unroll 4
-                for (int w = warp; w < words; w += kWarps) {
+                for (int w = have ? words : warp; w < words; w += kWarps) {
                     const int i = w * 32 + lane;
                     const unsigned r = i < n ? rank_at(i) : 0;
                     if (i < n && (r & mask) == prefix && ((safe_bits[w] ^ flip) >> lane & 1)) atomicAdd(&s_hist[(r >> shift) & digits], 1);

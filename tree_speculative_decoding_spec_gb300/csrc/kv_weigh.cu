@@ -24,7 +24,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // CTAs per 64 keys of one (sequence, KV head), over the rows that see any of them, 16 RPT at a time; where there
 // are few such tiles their chunks of rows go to several CTAs in turn, whose sums kv_weigh_parts adds up in order
-// (a prompt of 100 rows and 8 heads of 64: 33 us with one, XX with splits).  A thread has four keys and RPT rows; operands
+// (a prompt of 100 rows and 8 heads of 64: 33 us with one, 12 with splits).  A thread has four keys and RPT rows; operands
 // lie in shared memory by head dimension, so that four keys come in one read.  CTA 0 of the first head
 // writes the status.
 template <int D, int RPT>
