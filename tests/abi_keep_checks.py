@@ -79,7 +79,7 @@ def test_reorders_refuse(lib):
     _refuses(lib, "beam_reorder", _BASE, shared + [({"state": 0}, EINVAL), ({"state": _AT["state"] + 4}, EALIGN), ({"row_bytes": 0}, EINVAL),
                                                    ({"row_bytes": 6}, EINVAL), ({"row_bytes": -4}, EINVAL), ({"row_bytes": 1 << 33}, EINVAL)])
     caches = shared + [({"Hkv": 0}, EINVAL), ({"D": 0}, EINVAL), ({"D": 100}, EINVAL), ({"D": 1032}, EINVAL), ({"dt": 5}, EINVAL),
-                       ({"k_cache": 0}, EINVAL), ({"v_cache": 0}, EINVAL), ({"v_cache": _AT["k_cache"]}, EINVAL), ({"start": 0}, EINVAL),
+                       ({"k_cache": 0}, EINVAL), ({"v_cache": 0}, EINVAL), ({"v_cache": _AT["k_cache"]}, EINVAL), ({"v_cache": _AT["k_cache"] + 64}, EINVAL), ({"start": 0}, EINVAL),
                        ({"end": 0}, EINVAL), ({"start": _AT["start"] + 1}, EALIGN), ({"k_cache": _AT["k_cache"] + 8}, EALIGN)]
     _refuses(lib, "kv_reorder", _BASE, caches + [({"Lmax": 0}, EINVAL), ({"Lmax": (1 << 22) + 1}, EINVAL)])
     _refuses(lib, "kv_reorder_paged", _BASE, caches + PAGED)

@@ -268,3 +268,40 @@ def test_ranges_and_blocks_that_do_not_exist():
     assert st.spec_read_device_status(ws) == 1
     np.testing.assert_array_equal(k.cpu().numpy(), want[0])
     np.testing.assert_array_equal(v.cpu().numpy(), want[1])
+
+
+def test_beams_as_a_tree_of_candidates():
+    """A search of four steps, each beam with a cache of its own that kv_reorder and kv_append carry along; its pairs as one candidate tree.
+    Tree attention's rows of the last level are the attention of the beams over their caches."""
+    import torch
+    st = lib()
+    g = torch.Generator().manual_seed(11)
+    rand = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    W, V, Hq, Hkv, D, n0, steps = 3, 50, 4, 2, 64, 20, 4
+    table, ek, ev, eq = 2 * rand(V, V), rand(V, Hkv, D), rand(V, Hkv, D), rand(V, Hq, D)
+    kc, vc = rand(1, Hkv, n0 + steps + 1, D).repeat(W, 1, 1, 1), rand(1, Hkv, n0 + steps + 1, D).repeat(W, 1, 1, 1)
+    prefix = kc[:1, :, :n0].clone(), vc[:1, :, :n0].clone()
+    token = torch.tensor([[7] * W], dtype=torch.int32, device="cuda")
+    scores = torch.tensor([[0.0] + [-float("inf")] * (W - 1)], device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    parent, node, nodes = [-1], [0] * W, [7]           # the tree so far, each beam's node in it, the nodes' tokens
+    for s in range(steps + 1):
+        t = token[0].clamp(min=0).long()
+        st.kv_append(None, ek[t], ev[t], i32(list(range(W + 1))), i32([n0 + s] * W), kc, vc)
+        if s == steps:
+            break
+        token, p, scores, _, _ = st.beam_select(table[t][None].contiguous(), scores, W)
+        st.kv_reorder(kc, vc, p, i32([n0]), i32([n0 + s + 1]))
+        parent += [node[w] for w in p[0].tolist()]
+        nodes += token[0].tolist()
+        node = list(range(len(parent) - W, len(parent)))
+    tree = st.spec_tree_build(parent)
+    at = torch.tensor(nodes, device="cuda")
+    heads = lambda e: e[at].transpose(0, 1)[None].contiguous()  # noqa: E731
+    out, lse = st.tree_attention(heads(eq), prefix[0].contiguous(), prefix[1].contiguous(), i32([n0]), heads(ek), heads(ev), tree)
+    for w in range(W):
+        for h in range(Hq):
+            x = kc[w, h // 2].double() @ eq[at[node[w]], h].double() / 8.0
+            ref = torch.softmax(x, 0) @ vc[w, h // 2].double()
+            assert (out[0, h, node[w]] - ref).abs().max() < 1e-5
+            assert abs(lse[0, h, node[w]] - torch.logsumexp(x, 0)) < 1e-5

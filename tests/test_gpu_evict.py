@@ -171,6 +171,32 @@ def test_what_no_row_sees_does_not_count(c):
     _assert_weighed(t, _dev(got), pos)
 
 
+@pytest.mark.parametrize("dtype,T", [("bf16", 1), ("bf16", 200), ("f32", 30)])
+def test_a_sequence_without_rows_fades(dtype, T):
+    st = lib()
+    t = _case((dtype, 2, 8, 2, T, 64, 16, (300, 250), (0, T), 0.5), seed=5)
+    acc, pos = _run(st, t)
+    _assert_weighed(t, acc, pos)
+    np.testing.assert_array_equal(acc[0].cpu().numpy()[:, :300], 0.5 * t["acc"][0, :, :300])
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", [(95, 8, 2), (96, 8, 2), (129, 5, 1), (64, 24, 3), (385, 2, 1)])
+@pytest.mark.parametrize("n", [(1000, 400, 500), (385, 513, 640)])
+def test_both_ways_through_and_their_borders(T, Hq, Hkv, n):
+    """Short prompts side by side and long ones in chunks, lengths around the tiles' borders, rows cut over many CTAs."""
+    st = lib()
+    t = _case(("bf16", 3, Hq, Hkv, T, 128, 0, n, (T, max(1, T - 37), min(T, 3)), 0.9), seed=6)
+    ws = _ws(t)
+    acc, pos = _run(st, t, ws)
+    assert st.spec_read_device_status(ws) == 0
+    _assert_weighed(t, acc, pos)
+
+
+def _ws(t):
+    import torch
+    return torch.empty(1 << 20, dtype=torch.uint8, device="cuda").fill_(255)
+
+
 def test_sequences_and_blocks_that_make_no_sense():
     import torch
     st = lib()

@@ -175,7 +175,9 @@ spec_status kv(const char* name, Params& p, const void* k, const void* v, int Hk
     if (Hkv < 1 || Hkv > 1024) return fail(SPEC_EINVAL, "Hkv = %d out of 1..1024", Hkv);
     if (D < 1 || D > 1024 || (D * es) % 16) return fail(SPEC_EINVAL, "D = %d: 1..1024 and a multiple of 16 bytes", D);
     if (!k || !v || !p.start || !p.end) return fail(SPEC_EINVAL, "the cache, start and end must not be NULL");
-    if (k == v) return fail(SPEC_EINVAL, "keys and values are the same buffer");
+    const uint64_t bytes = static_cast<uint64_t>(p.table ? p.num_blocks : p.B * p.W) * Hkv * p.rows * D * es;
+    const uintptr_t ka = reinterpret_cast<uintptr_t>(k), va = reinterpret_cast<uintptr_t>(v);
+    if (ka < va + bytes && va < ka + bytes) return fail(SPEC_EINVAL, "keys and values overlap");
     if (!aligned16(k) || !aligned16(v)) return fail(SPEC_EALIGN, "the cache must be 16-byte aligned");
     if (!aligned4(p.start) || !aligned4(p.end) || !aligned4(p.table))
         return fail(SPEC_EALIGN, "start, end and the block table must be 4-byte aligned");

@@ -152,6 +152,7 @@ template <typename T> struct Row {
     static constexpr int E = Vec<T>::E;
     const T* x;
     int V, head, end;                 // elements in front of the row; one more than the slice's last vector
+    bool few = false;                 // less than a vector a thread
     __device__ __forceinline__ Row(const Params& p, int row)
         : x(static_cast<const T*>(p.logits) + static_cast<int64_t>(row) * p.stride), V(p.V),
           head(static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T))), end((head + p.V + E - 1) / E) {}
@@ -172,11 +173,18 @@ template <typename T> __device__ __noinline__ uint4 load_end(const T* x, int V, 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The first of a thread's vectors of the chunk that begins at vector c, kThreads apart.  Slices of less than a vector a
+// thread go to the warps in turn: if some had none, there would be no bound (15 of 599: 32 us, so 13).
+template <typename T> __device__ __forceinline__ int vector_of(const Row<T>& row, int c) {
+    const int t = threadIdx.x;
+    return c + (row.few ? (t & 31) * kWarps + (t >> 5) : t);
+}
+
 // A thread's vectors of the chunk that begins at vector c.
 template <typename T> __device__ __forceinline__ void load_chunk(const Row<T>& row, int c, uint4 (&raw)[kVecs]) {
     constexpr int E = Vec<T>::E;
     constexpr uint32_t kNone = E == 4 ? 0xFF800000u : 0xFF80FF80u;   // -inf
-    const int v0 = c + static_cast<int>(threadIdx.x);
+    const int v0 = vector_of(row, c);
     if (c > 0 && c + kVecs * kThreads <= row.end && (c + kVecs * kThreads) * E - row.head <= row.V) {   // inside the row
         const T* at = row.x + (v0 * E - row.head);
 #pragma unroll
@@ -210,7 +218,7 @@ __device__ __noinline__ float cut_chunk(Shared& sh, const Row<T>& row, int c, in
     load_chunk(row, c, raw);
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) Vec<T>::clean(raw[v]);
-    const int first = (c + static_cast<int>(threadIdx.x)) * E - row.head;
+    const int first = vector_of(row, c) * E - row.head;
     const unsigned long long mine = static_cast<int>(threadIdx.x) < before ? sh.cand[threadIdx.x] : 0;   // before is below kThreads
     const unsigned none = order_key(-INFINITY);
     int turn = 0;
@@ -268,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_slices(const Params p) {
     Row<T> row(p, row_at);
     const int v0 = slice * p.per;
     if (slice + 1 < p.slices) row.end = min(row.end, v0 + p.per);
+    row.few = row.end - v0 < kThreads;
     if (threadIdx.x == 0) sh.count = 0;
     float m = -INFINITY, s = 0.f, least = -INFINITY;   // logits above `least` are candidates
     int before = 0;
@@ -335,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_slices(const Params p) {
                     at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
                     if (mask && at < kCap)
                         sh.cand[at] = make_key(__uint_as_float(E == 4 ? w : e & 1 ? w & 0xFFFF0000u : w << 16),
-                                               (c + v * kThreads + static_cast<int>(threadIdx.x)) * E - row.head + e);
+                                               (vector_of(row, c) + v * kThreads) * E - row.head + e);
                 }
             }
         }

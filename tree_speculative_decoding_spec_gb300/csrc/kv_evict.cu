@@ -523,11 +523,12 @@ spec_status run(Params& p, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s
     p.here = p.in_place && p.most <= kFew;
     p.cached = std::min(p.cap, kCached);
     const size_t smem = static_cast<size_t>(p.cached) * 4 + (p.cap <= kCached ? 3 * ((p.cap + 31) / 32) * 4 : 0);
-    // a full cache's step is a chain of short stages, which 256 threads go through fastest (8.1 us for 512 heads of 2065 keys, 512 threads
-    // 11.5); longer caches, few of which share an SM anyway, get all of its threads
-    auto pick = p.cap <= 4096 ? k_pick<256> : k_pick<1024>;
+    // a full cache's step is a chain of short stages, which 256 threads go through fastest (8.1 us for 512 heads of 2065
+    // keys, 512 threads 11.5); selections by digits, few of which share an SM anyway, get all of its threads
+    const bool step = p.cap - p.budget <= kGone && p.cap <= 4096;
+    auto pick = step ? k_pick<256> : k_pick<1024>;
     if (smem > 30000) SPEC_CUDA_TRY(cudaFuncSetAttribute(pick, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4 + kCached / 8 * 3));
-    SPEC_CUDA_TRY(launch("evict_pick", pick, dim3(p.Hkv + 1, p.B), dim3(p.cap <= 4096 ? 256 : 1024), smem, s, p));
+    SPEC_CUDA_TRY(launch("evict_pick", pick, dim3(p.Hkv + 1, p.B), dim3(step ? 256 : 1024), smem, s, p));
     if (!p.here) {
         const int64_t rows = kBatch * (kMoveThreads / p.row16);
         const int64_t most = ((p.in_place ? p.most : p.places) + rows - 1) / rows;

@@ -285,6 +285,19 @@ template <int N> __device__ __forceinline__ void load_lse(const float* nl2, unsi
     }
 }
 
+// Bit i of lane k's word becomes bit k of lane i's: blocks of 16, 8, .. 1 change places across the diagonal.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x) {
+    const int lane = threadIdx.x & 31;
+    uint32_t low = 0x0000ffffu;       // the lower half of every block
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, x, d);
+        x = lane & d ? (x & ~low) | ((y >> d) & low) : (x & low) | ((y << d) & ~low);
+        low ^= low << (d >> 1);
+    }
+    return x;
+}
+
 // N columns of a key's scores: the sum of their weights.
 template <int N>
 __device__ __forceinline__ unsigned long long weights(const uint32_t (&s)[N], const unsigned long long (&l)[N / 2], unsigned long long c2) {
@@ -481,42 +494,45 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                     const int tid = threadIdx.x - 32 * kRowsWarp;
                     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
                     const int64_t q0 = static_cast<int64_t>(w.b) * p.Hq + w.h * tp.g;
-                    auto row_of = [&](int r) {       // a row of q and lse
-                        const int rr = tp.row0 + r, gi = rr / w.rows.count;
-                        return (q0 + gi) * p.T + node_of(p, w.b, rr - gi * w.rows.count);
-                    };
-                    constexpr int kAhead = 8;        // loads of a thread on their way together
-                    for (int x0 = tid; x0 < padded * (D / 8); x0 += 64 * kAhead) {
-                        int64_t row[kAhead];
-                        uint4 v[kAhead];
-#pragma unroll
-                        for (int k = 0; k < kAhead; ++k) {
-                            const int r = (x0 + 64 * k) / (D / 8);
-                            row[k] = r < total ? row_of(r) : -1;
-                        }
-#pragma unroll
-                        for (int k = 0; k < kAhead; ++k) {
-                            v[k] = make_uint4(0u, 0u, 0u, 0u);
-                            if (row[k] >= 0) v[k] = *reinterpret_cast<const uint4*>(q + row[k] * D + (x0 + 64 * k) % (D / 8) * 8);
-                        }
-#pragma unroll
-                        for (int k = 0; k < kAhead; ++k) {
-                            const int x = x0 + 64 * k, r = x / (D / 8), part = x % (D / 8);
-                            if (r < padded) *reinterpret_cast<uint4*>(sQ + (qs * kH + part / 8) * q_half + r * 128 + ((part % 8) ^ (r & 7)) * 16) = v[k];
-                        }
+                    // asynchronous copies, so that all of a thread's are on their way together; rows behind the last are zeros.
+                    // A thread has the same 16 bytes of every 64 / (D / 8)-th row, which head's and which of it kept in step
+                    constexpr int kParts = D / 8, kStep = 64 / kParts;
+                    const int part = tid % kParts;
+                    int r = tid / kParts, i = tp.row0 + r, gi = 0;
+                    if (w.rows.count > 0) {
+                        gi = i / w.rows.count;
+                        i -= gi * w.rows.count;
                     }
-#pragma unroll 4
-                    for (int r = tid; r < padded; r += 64) {
-                        float x = -INFINITY;
-                        int last = -1;
-                        if (r < total) {
-                            const float l = p.lse[row_of(r)];
-                            if (isfinite(l)) x = -l * kL2e;
-                            last = w.rows.n - w.rows.count + (tp.row0 + r) % w.rows.count;
-                        }
-                        sm.nl2[qs][r] = x;
-                        sm.last[qs][r] = last;
+                    for (; r < padded; r += kStep) {
+                        const bool there = r < total;
+                        const int64_t row = there ? (q0 + gi) * p.T + node_of(p, w.b, i) : 0;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                                     ::"r"(smem_u32(sQ + (qs * kH + part / 8) * q_half + r * 128 + ((part % 8) ^ (r & 7)) * 16)),
+                                       "l"(q + row * D + part * 8), "r"(there ? 16 : 0) : "memory");
+                        for (i += kStep; i >= w.rows.count && there; i -= w.rows.count) ++gi;
                     }
+                    // their lse, four at a time; the last key that each sees
+                    for (int r0 = tid; r0 < padded; r0 += 256) {
+                        float l[4];
+                        int ii[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int rr = tp.row0 + r0 + 64 * k;
+                            l[k] = INFINITY;
+                            if (r0 + 64 * k < total) {
+                                const int head = rr / w.rows.count;
+                                ii[k] = rr - head * w.rows.count;
+                                l[k] = p.lse[(q0 + head) * p.T + node_of(p, w.b, ii[k])];
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (r0 + 64 * k < padded) {
+                                sm.nl2[qs][r0 + 64 * k] = isfinite(l[k]) ? -l[k] * kL2e : -INFINITY;
+                                sm.last[qs][r0 + 64 * k] = r0 + 64 * k < total ? w.rows.n - w.rows.count + ii[k] : -1;
+                            }
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.q_full[qs]);
@@ -680,11 +696,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                     } else {
 #pragma unroll 1
                         for (int x = 0; x < cols; x += 16) {
-                            uint32_t r[16], seen = 0;
+                            uint32_t r[16];
                             tmem_ld16(s_addr + x, r);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (x + e < cols && j <= sm.last[cs][x + e]) seen |= 1u << e;
+                            // which of the warp's keys the column of each lane sees, turned into which columns see the lane's key
+                            const int upto = x + (lane & 15) < cols ? sm.last[cs][x + (lane & 15)] - (j - lane) : -1;
+                            const uint32_t seen = transpose_bits(upto >= 31 ? ~0u : upto < 0 ? 0u : (2u << upto) - 1) & 0xffffu;
                             unsigned long long l[8];
                             load_lse<16>(nl2 + x, l);
                             tmem_ld_wait();
