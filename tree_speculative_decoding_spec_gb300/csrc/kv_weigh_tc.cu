@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
             mbar_init(&sm.q_empty[i], MANY ? 2 : 9);
             mbar_init(&sm.l_full[i], 1);
             mbar_init(&sm.l_empty[i], 4 * kGroups);
-            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_full[i], MANY ? 2 : 1);
             mbar_init(&sm.s_empty[i], 4);
         }
         mbar_init(&sm.drain, MANY ? 2 : 1);
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
         const bool leader = elected();
         const int half = warp - kMma; // of the tile's keys
         const int buffers = MANY ? 2 : tp.buffers;
-        Ring s_ring;                  // a score buffer for each product; many: two of each half
+        Ring s_ring, l_ring;          // a score buffer for each product; many: two of each half
         for (; ok && w.more; w.next(), k_ring.next(tp.k_stages)) {
             const int ks = k_ring.at;
             if (!(ok = warp_wait_for(&sm.k_full[ks], k_ring.full(), abort_flag))) break;
@@ -428,8 +428,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                     const int buf = (MANY ? 2 * half : 0) + s_ring.at;
                     if (s_ring.round > 0 && !(ok = warp_wait_for(&sm.s_empty[buf], s_ring.empty(), abort_flag))) break;
                     s_ring.next(buffers);
+                    if (MANY && !(ok = warp_wait_for(&sm.l_full[l_ring.at], l_ring.full(), abort_flag))) break;
                     tc_fence_after();
                     if (leader) {
+                        // the rows' lse has come too: this arrival hands it on, the products' own says nothing of it.  (The
+                        // weights' warps would wait 200 cycles for it in every chunk, these have the time.)
+                        if (MANY) mbar_arrive(&sm.s_full[buf]);
                         const uint64_t qa = sdesc_k128(smem_u32(sQ + qs * kH * q_half));
                         // (an address is 16 bytes a unit in a descriptor)
 #pragma unroll
@@ -444,6 +448,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                 if (MANY) {
                     if (leader) mma_commit(&sm.q_empty[qs]);
                     q_ring.next(tp.q_stages);
+                    l_ring.next(4);
                     ch.next();
                 }
             }
@@ -592,9 +597,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                 const int h0 = k0 + grp * kKeys;             // the group's half
                 for (int c = 0; c < w.take; ++c, ++u, ch.next()) {
                     const int ls = u & 3;
-                    // (also for a chunk that the half does not see: else its slot would be given back for a later turn)
-                    if (!(ok = warp_wait_for(&sm.l_full[ls], (u >> 2) & 1, abort_flag))) break;
-                    if (!unseen(w.rows, h0, ch.i0)) {
+                    // a chunk that the half does not see: its slot must not be given back for an earlier turn
+                    if (unseen(w.rows, h0, ch.i0)) {
+                        if (!(ok = warp_wait_for(&sm.l_full[ls], (u >> 2) & 1, abort_flag))) break;
+                    } else {
                         const int buf = 2 * grp + s_ring.at;
                         const uint32_t parity = s_ring.full();
                         s_ring.next(2);
@@ -603,10 +609,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                         unsigned long long part = pk2(0.f, 0.f);
                         uint32_t r[2][W];
                         unsigned long long l[2][W / 2];
-                        load_lse<W>(nl2, l[0]);
                         if (!(ok = warp_wait_for(&sm.s_full[buf], parity, abort_flag))) break;
                         tc_fence_after();
                         load_scores(s_addr, r[0]);
+                        load_lse<W>(nl2, l[0]);
                         if (w.rows.count - ch.i0 >= kChunk && h0 + kKeys - 1 <= in_front + ch.i0) {   // all see all
 #pragma unroll
                             for (int x = 0; x < kChunk; x += W) {
