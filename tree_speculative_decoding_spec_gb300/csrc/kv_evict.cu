@@ -102,13 +102,16 @@ template <int kWarps> __device__ __forceinline__ void scan2(int (&part)[2][kWarp
     __syncthreads();                  // an earlier scan's readers are through
     if (lane == 31) { part[0][warp] = x; part[1][warp] = y; }
     __syncthreads();
-    int p0 = 0, p1 = 0;
-    t0 = t1 = 0;
-    for (int i = 0; i < kWarps; ++i) {
-        if (i == warp) { p0 = t0; p1 = t1; }
-        t0 += part[0][i];
-        t1 += part[1][i];
+    // every warp adds up the warps' totals itself, a lane each
+    int u = lane < kWarps ? part[0][lane] : 0, v = lane < kWarps ? part[1][lane] : 0;
+    const int own0 = __shfl_sync(0xffffffffu, u, warp), own1 = __shfl_sync(0xffffffffu, v, warp);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int m = __shfl_up_sync(0xffffffffu, u, o), k = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) { u += m; v += k; }
     }
+    const int p0 = __shfl_sync(0xffffffffu, u, warp) - own0, p1 = __shfl_sync(0xffffffffu, v, warp) - own1;
+    t0 = __shfl_sync(0xffffffffu, u, 31);
+    t1 = __shfl_sync(0xffffffffu, v, 31);
     a = p0 + x - a;
     b = p1 + y - b;
 }
