@@ -734,10 +734,10 @@ size_t kv_weigh_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, in
  * accept_len[b]] of a tree (tree_accept's outputs), or rows 0 .. n_rows[b] - 1 of q; row i
  * sees keys 0 .. prefix_len[b] - count + i.  The rows' own keys start at 0 instead of decay * acc.
  *
- *   q            device [B, Hq, T, D] (dt), finite in the rows that count
+ *   q            device [B, Hq, T, D] (dt), finite in the rows that add something
  *   lse          device [B, Hq, T] float32; a row whose lse is not finite (it saw nothing) adds nothing
- *   k_cache      device [B, Hkv, Lmax, D] (dt).  Rows >= prefix_len[b] do not affect the result but must
- *                be readable
+ *   k_cache      device [B, Hkv, Lmax, D] (dt), finite below prefix_len[b].  Rows behind that do not affect
+ *                the result but must be readable
  *   prefix_len   device [B]: keys in the cache, those of the rows included
  *   seen         device [B] or NULL (prefix_len): tokens of the sequence so far, evicted ones included
  *   n_rows       device [B], 0 .. T, or NULL (T, or those of the path)

@@ -171,6 +171,25 @@ def test_what_no_row_sees_does_not_count(c):
     _assert_weighed(t, _dev(got), pos)
 
 
+@pytest.mark.parametrize("c", [("bf16", 2, 16, 2, 1, 128, 64, (400, 129), None, 1.0), ("bf16", 2, 4, 2, 300, 64, 0, (900, 300), (300, 257), 0.5),
+                               ("bf16", 2, 24, 1, 20, 128, 0, (500, 50), "path", 1.0), ("f32", 2, 4, 2, 40, 64, 16, (100, 70), None, 1.0)],
+                         ids=lambda c: "-".join(map(str, c[:7])))
+def test_rows_without_an_lse_may_hold_anything(c):
+    """Rows among those that count, but whose lse is not finite: NaN and infinities in them weigh nothing."""
+    st = lib()
+    t = _case(c, seed=7)
+    B, Hq, T = c[1], c[2], c[4]
+    rng = np.random.default_rng(8)
+    q = t["q"].clone()
+    for b in range(B):
+        for h in range(Hq):
+            for i in {0, T - 1, *rng.integers(0, T, 3).tolist()} if h % 3 == 0 else {int(rng.integers(0, T))} if T > 1 else ():
+                t["lse"][b, h, i] = (-np.inf, np.inf, np.nan)[(h + i) % 3]
+                q[b, h, i] = float("nan") if i % 2 else float("inf")
+    acc, pos = _run(st, {**t, "q": q})
+    _assert_weighed(t, acc, pos)
+
+
 @pytest.mark.parametrize("dtype,T", [("bf16", 1), ("bf16", 200), ("f32", 30)])
 def test_a_sequence_without_rows_fades(dtype, T):
     st = lib()

@@ -79,6 +79,8 @@ struct Small {
     long long length;                 // its chunks
     __align__(16) float nl2[4][kMostRows];   // -lse log2 e of a stage's rows, -inf: does not count
     int last[4][kMostRows];           // few: the last key that a row sees
+    int odd[4][2];                    // few: whether a stage has rows that do not count although they are there (each warp's
+                                      // word): such rows may hold anything, and 0 times that need not be 0
 };
 
 // The line of chunks of one sequence and head: row chunks first(t) .. C - 1 for tile t, times `mult` query heads.
@@ -482,10 +484,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                         if (u >= 4 && !(ok = warp_wait_for(&sm.l_empty[ls], (u / 4 - 1) & 1, abort_flag))) break;
                         for (int e = 0; e < 4; ++e) x[e] = isfinite(x[e]) ? -x[e] * kL2e : -INFINITY;
                         *reinterpret_cast<float4*>(&sm.nl2[ls][lane * 4]) = make_float4(x[0], x[1], x[2], x[3]);
+                        // Rows that do not count may hold anything, and 0 times that need not be 0: zeros take their place, once
+                        // they have come.  (A flag for the weights' warps to look at cost every chunk: prompts 124 us for 118.)
+                        bool odd = false;
+                        for (int e = 0; e < 4; ++e) odd |= x[e] == -INFINITY && ch.i0 + lane * 4 + e < w.rows.count;
+                        if (__any_sync(0xffffffffu, odd)) {
+                            // (the products wait for l_full, so the slot cannot be a turn further; as many slots as stages)
+                            if (!(ok = warp_wait_for(&sm.q_full[q_ring.at], q_ring.full(), abort_flag))) break;
+                            for (int e = 0; e < 4; ++e)
+                                if (x[e] == -INFINITY)
+                                    for (int i = 0; i < kH * 8; ++i)
+                                        *reinterpret_cast<uint4*>(sQ + (q_ring.at * kH + i / 8) * q_half + (lane * 4 + e) * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
+                            fence_proxy_async_smem();
+                        }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sm.l_full[ls]);
                         ch.next();
                         if (ch.i0 == ch.begin) ++qh;
+                        q_ring.next(tp.q_stages);
                     }
                 }
         } else {
@@ -517,6 +533,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                         for (i += kStep; i >= w.rows.count && there; i -= w.rows.count) ++gi;
                     }
                     // their lse, four at a time; the last key that each sees
+                    bool odd = false;
                     for (int r0 = tid; r0 < padded; r0 += 256) {
                         float l[4];
                         int ii[4];
@@ -533,10 +550,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if (r0 + 64 * k < padded) {
-                                sm.nl2[qs][r0 + 64 * k] = isfinite(l[k]) ? -l[k] * kL2e : -INFINITY;
-                                sm.last[qs][r0 + 64 * k] = r0 + 64 * k < total ? w.rows.n - w.rows.count + ii[k] : -1;
+                                const bool counts = isfinite(l[k]);
+                                if (!counts && r0 + 64 * k < total) odd = true;
+                                sm.nl2[qs][r0 + 64 * k] = counts ? -l[k] * kL2e : -INFINITY;
+                                sm.last[qs][r0 + 64 * k] = counts ? w.rows.n - w.rows.count + ii[k] : -1;
                             }
                     }
+                    odd = __any_sync(0xffffffffu, odd);
+                    if (lane == 0) sm.odd[qs][warp - kRowsWarp] = odd;
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -680,8 +701,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                     const float* nl2 = sm.nl2[cs];
                     const int cols = min(tp.nq, tp.g * w.rows.count - tp.row0);
                     unsigned long long part = pk2(0.f, 0.f);
-                    if (k0 + kKeys - 1 <= w.rows.n - w.rows.count) {     // all rows see all keys
-                        const int steps = max(1, (cols + 15) / 16);
+                    if (cols > 0 && k0 + kKeys - 1 <= w.rows.n - w.rows.count && !(sm.odd[cs][0] | sm.odd[cs][1])) {   // all rows see all keys
+                        const int steps = (cols + 15) / 16;
                         uint32_t r[2][16];
                         unsigned long long l[2][8];
                         tmem_ld16(s_addr, r[0]);
@@ -792,7 +813,7 @@ constexpr size_t kSmem = 232448;      // of one CTA, all there is: no two share 
 
 static int few_rows(int g, int T, int P) { return g * (P ? P : T); }
 // Rows of a prompt fill chunks of 128 of one query head; shorter ones are better off side by side, several heads in a pass.
-bool weigh_many(int g, int T, int P) { return !P && T >= 96 && g * T > kMostRows; }
+bool weigh_many(int g, int T, int P) { return !P && T >= 96 && static_cast<int64_t>(g) * T > kMostRows; }
 
 size_t weigh_tc_bytes(int g, int T, int P) {
     return weigh_many(g, T, P) ? static_cast<size_t>(device_sm_count()) * (sizeof(Record) + 4 * kKeys * sizeof(float)) : 0;
