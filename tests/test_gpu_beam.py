@@ -305,3 +305,13 @@ def test_beams_as_a_tree_of_candidates():
             ref = torch.softmax(x, 0) @ vc[w, h // 2].double()
             assert (out[0, h, node[w]] - ref).abs().max() < 1e-5
             assert abs(lse[0, h, node[w]] - torch.logsumexp(x, 0)) < 1e-5
+
+
+@pytest.mark.parametrize("alpha", [0.0, 2.0])
+def test_scores_and_logits_near_the_largest_numbers(alpha):
+    """A score less its row's logits may pass 32 bits on the way: the pair is there all the same."""
+    import torch
+    x = torch.full((1, 3, 900), -3e38, device="cuda")
+    x[0, 0, 5], x[0, 1, 600], x[0, 2, 7] = 3e38, 3.2e38, 1.0
+    # ranks as far apart as their sizes, of one token a beam
+    _check(lib(), x, np.array([[-3e38, -1e38, -2e38]]), 3, length=np.array([[1, 1, 1]]), alpha=alpha)

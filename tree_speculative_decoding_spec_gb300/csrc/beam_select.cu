@@ -428,7 +428,7 @@ __device__ __noinline__ double power(int n, float a) {
         c *= i;                       // 1 / (i - 1)!, at compile time
         v = fma(v, r, c);
     }
-    return v * __longlong_as_double(static_cast<long long>(1023 + e) << 52);   // e >= -700: n below 2^31, a at most 16
+    return v * __longlong_as_double(static_cast<long long>(1023 + e) << 52);   // e >= -496: n below 2^31, a at most 16
 }
 
 // Ranks are needed in 64 bits only of those near the K-th: this GPU does two 64-bit operations a clock and SM,
@@ -552,7 +552,8 @@ __global__ void __launch_bounds__(kThreads) k_join(const Params p) {
         if (c >= n) return -INFINITY;
         const int w = beam_of(c), st = sh.state[w];
         if (!(st == kLive ? k != 0 : st == kEnded && c == w * per)) return -INFINITY;
-        return (sh.basef[w] + (st == kEnded ? 0.f : key_value(static_cast<unsigned>(k >> 32)))) * sh.invf[w];
+        // (a finite score less finite logits may pass 32 bits: still a pair)
+        return fmaxf((sh.basef[w] + (st == kEnded ? 0.f : key_value(static_cast<unsigned>(k >> 32)))) * sh.invf[w], -3.4028235e38f);
     };
     // a bound as in the slices, lowered by what 32 bits can be off: four roundings of |base| + |x|, |x| <= |base| + |rank| / inv
     float near[kKeep], mine = -INFINITY;
