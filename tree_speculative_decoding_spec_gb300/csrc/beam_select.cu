@@ -28,6 +28,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVecs = 4;              // 16-byte loads of a thread and chunk
 constexpr int kPerSm = 6;             // CTAs of an SM: loads in flight come from the others while one works
 constexpr int kCap = 1024;            // candidates a slice holds at most
+constexpr int kFound = 512;           // vectors of a stretch with candidates in them
 constexpr int kMaxSlices = 32;        // one lane each in the join
 constexpr int kJoinCap = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -96,9 +97,11 @@ __device__ __forceinline__ unsigned long long make_key(float x, int token) {
 }
 
 struct Shared {
-    __align__(16) unsigned long long cand[kCap + 4];
+    __align__(16) unsigned long long cand[2][kCap];    // the list and the next one, in turn
+    uint4 vec[kFound];                // vectors that hold candidates, and their first elements
+    int where[kFound];
     unsigned long long best[SPEC_MAX_BEAMS];
-    int count, kept;
+    int found, count, kept;
     unsigned bound[kWarps];
     int part[2][kWarps];
     float fpart[kWarps];
@@ -116,26 +119,19 @@ __device__ __forceinline__ unsigned warp_kth(unsigned mine, int kq) {
     return top;
 }
 
-// Bring cand[0 .. n) down to its K largest, sorted; returns the threshold that later elements must pass.
-__device__ __noinline__ float cut(Shared& sh, int n, int K) {
-    if (static_cast<int>(threadIdx.x) < 4) sh.cand[n + threadIdx.x] = 0;   // to a whole number of steps
-    __syncthreads();
+// The K largest of from[0 .. n), sorted, in to[0 ..): every thread finds its candidates' ranks.
+__device__ __forceinline__ void cut(const unsigned long long* from, unsigned long long* to, int n, int K) {
     for (int i = threadIdx.x; i < n; i += kThreads) {
-        const unsigned long long key = sh.cand[i];
-        int rank = 0;
-#pragma unroll 1
-        for (int j = 0; j < n; j += 4) {
-            const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&sh.cand[j]), b = *reinterpret_cast<const ulonglong2*>(&sh.cand[j + 2]);
+        const unsigned long long key = from[i];
+        int rank = 0, j = 0;
+#pragma unroll 2
+        for (; j + 4 <= n; j += 4) {
+            const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&from[j]), b = *reinterpret_cast<const ulonglong2*>(&from[j + 2]);
             rank += (a.x > key) + (a.y > key) + (b.x > key) + (b.y > key);
         }
-        if (rank < K) sh.best[rank] = key;
+        for (; j < n; ++j) rank += from[j] > key;
+        if (rank < K) to[rank] = key;
     }
-    __syncthreads();
-    const int k = min(n, K);
-    if (static_cast<int>(threadIdx.x) < k) sh.cand[threadIdx.x] = sh.best[threadIdx.x];
-    if (threadIdx.x == 0) sh.count = k;
-    __syncthreads();
-    return n >= K ? key_value(static_cast<unsigned>(sh.cand[K - 1] >> 32)) : -INFINITY;
 }
 
 __device__ __forceinline__ int block_sum(Shared& sh, int v, int turn) {
@@ -212,14 +208,14 @@ template <typename T> __device__ __forceinline__ void load_chunk(const Row<T>& r
 // More elements pass the threshold than the list holds (rows of equal logits, logits that rise with the token): the K
 // largest of cand[0 .. before), at most K, and one chunk by bisection, over the order of the logits, then of the tokens.
 template <typename T>
-__device__ __noinline__ float cut_chunk(Shared& sh, const Row<T>& row, int c, int before, int K) {
+__device__ __noinline__ float cut_chunk(Shared& sh, unsigned long long* cand, const Row<T>& row, int c, int before, int K) {
     constexpr int E = Vec<T>::E;
     uint4 raw[kVecs];                 // the chunk once more
     load_chunk(row, c, raw);
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) Vec<T>::clean(raw[v]);
     const int first = vector_of(row, c) * E - row.head;
-    const unsigned long long mine = static_cast<int>(threadIdx.x) < before ? sh.cand[threadIdx.x] : 0;   // before is below kThreads
+    const unsigned long long mine = static_cast<int>(threadIdx.x) < before ? cand[threadIdx.x] : 0;   // before is below kThreads
     const unsigned none = order_key(-INFINITY);
     int turn = 0;
     auto count = [&](auto&& test) {
@@ -260,7 +256,7 @@ __device__ __noinline__ float cut_chunk(Shared& sh, const Row<T>& row, int c, in
         }
     __syncthreads();
     const int kept = sh.kept;
-    if (static_cast<int>(threadIdx.x) < kept) sh.cand[threadIdx.x] = sh.best[threadIdx.x];
+    if (static_cast<int>(threadIdx.x) < kept) cand[threadIdx.x] = sh.best[threadIdx.x];
     if (threadIdx.x == 0) sh.count = kept;
     __syncthreads();
     return kept < K ? -INFINITY : key_value(t);
@@ -277,9 +273,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_slices(const Params p) {
     const int v0 = slice * p.per;
     if (slice + 1 < p.slices) row.end = min(row.end, v0 + p.per);
     row.few = row.end - v0 < kThreads;
-    if (threadIdx.x == 0) sh.count = 0;
+    if (threadIdx.x == 0) sh.found = sh.count = 0;
     float m = -INFINITY, s = 0.f, least = -INFINITY;   // logits above `least` are candidates
-    int before = 0;
+    int before = 0, turn = 0;
     __syncthreads();
     // One chunk, then stretches twice as long as all before: each lets some K candidates through, and the warps run free within it.
     constexpr int kStep = kVecs * kThreads;
@@ -327,48 +323,62 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_slices(const Params p) {
                 if (fourth > order_key(-INFINITY)) least = key_value(fourth - (fourth == order_key(0.f) ? 2 : 1));   // (-0 is 0)
             }
             if (!__any_sync(0xffffffffu, top > least)) continue;
+            // Only the vectors: their elements are looked at when the stretch is through, one by each thread.  (Elements listed
+            // here, a warp's one after the other, kept the other warps waiting: 57 us for 768 rows of 131072 where this takes 52.)
 #pragma unroll
-            for (int v = 0; v < kVecs; ++v) {
-                if (!__any_sync(0xffffffffu, tops[v] > least)) continue;
-                unsigned mask = 0;
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (Vec<T>::at(raw[v], e) > least) mask |= 1u << e;
-                // a thread's elements one after the other, the warp's together
-#pragma unroll 1
-                for (unsigned who; (who = __ballot_sync(0xffffffffu, mask != 0)) != 0; mask &= mask - 1) {
-                    const int e = __ffs(mask) - 1, k = E == 4 ? e : e >> 1;
-                    const uint32_t w = k & 2 ? (k & 1 ? raw[v].w : raw[v].z) : (k & 1 ? raw[v].y : raw[v].x);
-                    int at = 0;
-                    if (lane == 0) at = atomicAdd(&sh.count, __popc(who));
-                    at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
-                    if (mask && at < kCap)
-                        sh.cand[at] = make_key(__uint_as_float(E == 4 ? w : e & 1 ? w & 0xFFFF0000u : w << 16),
-                                               (vector_of(row, c) + v * kThreads) * E - row.head + e);
+            for (int v = 0; v < kVecs; ++v)
+                if (tops[v] > least) {
+                    const int at = atomicAdd(&sh.found, 1);
+                    if (at < kFound) {
+                        sh.vec[at] = raw[v];
+                        sh.where[at] = (vector_of(row, c) + v * kThreads) * E - row.head;
+                    }
                 }
-            }
         }
         __syncthreads();
-        const int n = sh.count;
-        __syncthreads();
+        const int found = sh.found;   // the same for all: nobody adds to it before the next barrier
+        if (found == 0) {
+            __syncthreads();          // all have seen that there are none
+            continue;
+        }
+        unsigned long long* list = sh.cand[turn];
+        int n = kCap + 1;
+        if (found <= kFound) {
+            for (int i = threadIdx.x; i < found * E; i += kThreads) {
+                const float x = to_f32<T>(reinterpret_cast<const T*>(sh.vec)[i]);
+                if (x > least) {
+                    const int at = atomicAdd(&sh.count, 1);
+                    if (at < kCap) list[at] = make_key(x, sh.where[i / E] + i % E);
+                }
+            }
+            __syncthreads();
+            n = sh.count;
+        }
         if (n > kCap) {               // too many: chunk by chunk, each time the K best of it and of those so far
-            if (threadIdx.x == 0) sh.count = before;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                sh.found = 0;
+                sh.count = before;
+            }
             __syncthreads();
             for (int d = c0; d < c1; d += kStep) {
-                least = cut_chunk<T>(sh, row, d, before, p.K);
+                least = cut_chunk<T>(sh, list, row, d, before, p.K);
                 before = sh.count;
                 __syncthreads();
             }
-        } else if (n > before) {
-            least = cut(sh, n, p.K);
-            before = sh.count;
+        } else {
+            if (threadIdx.x == 0) sh.found = 0;        // read by all in front of the last barrier
+            cut(list, sh.cand[turn ^ 1], n, p.K);
+            turn ^= 1;
             __syncthreads();
+            before = min(n, p.K);
+            if (threadIdx.x == 0) sh.count = before;   // next used behind a barrier
+            least = n >= p.K ? key_value(static_cast<unsigned>(sh.cand[turn][p.K - 1] >> 32)) : -INFINITY;
         }
     }
-    cut(sh, before, p.K);
     const size_t out = static_cast<size_t>(row_at) * p.slices + slice;
     if (static_cast<int>(threadIdx.x) < p.K)
-        p.cand[out * p.K + threadIdx.x] = static_cast<int>(threadIdx.x) < sh.count ? sh.cand[threadIdx.x] : 0ull;
+        p.cand[out * p.K + threadIdx.x] = static_cast<int>(threadIdx.x) < before ? sh.cand[turn][threadIdx.x] : 0ull;
     // the slice's maximum and sum
     const float wm = warp_max(m);
     if (lane == 0) sh.fpart[warp] = wm;
