@@ -454,7 +454,8 @@ struct Join {
     int count;
 };
 
-__device__ __forceinline__ bool above(const Entry& x, const Entry& y) { return x.key > y.key || (x.key == y.key && x.tie < y.tie); }
+// (without branches: the ranks' loops took four times as long with them)
+__device__ __forceinline__ bool above(const Entry& x, const Entry& y) { return (x.key > y.key) | ((x.key == y.key) & (x.tie < y.tie)); }
 
 __device__ __forceinline__ Entry entry_of(const Join& sh, const Params& p, int w, unsigned long long k) {
     const uint32_t token = sh.state[w] == kEnded ? static_cast<uint32_t>(p.eos) : ~static_cast<uint32_t>(k);
@@ -530,28 +531,51 @@ __global__ void __launch_bounds__(kThreads) k_join(const Params p) {
         kept[i] = c < n ? cand[c] : 0;
     }
     __syncthreads();
-    float size = 0.f;                 // the largest |base| of the warp's rows
-    for (int w = warp; w < p.W; w += kWarps) {
-        if (sh.state[w] == kLive) {
-            const float2 ms = lane < S ? p.sums[(static_cast<size_t>(b) * p.W + w) * S + lane] : make_float2(-INFINITY, 0.f);
-            const float M = warp_max(ms.x);
-            const float sum = warp_sum(isfinite(ms.x) ? ms.y * exp2f((ms.x - M) * kLog2e) : 0.f);
-            if (lane == 0) {
-                if (!isfinite(M)) {   // nothing but -inf, or a logit of +inf
-                    sh.state[w] = kDead;
-                    if (M > 0.f) flag_status(p.ws, SPEC_EINVAL);
-                } else {
-                    sh.base[w] -= M + log_parts(sum);
-                }
+    // The rows' log-sums: rows warp, warp + 8, .. are this warp's, their slices' sums on their way together; in the end lane i
+    // has row i of them.
+    constexpr int kRows = SPEC_MAX_BEAMS / kWarps;
+    const float2* sums = p.sums + static_cast<size_t>(b) * p.W * S;
+    const int own = warp + lane * kWarps;             // this lane's row, if it is one
+    float M = -INFINITY, sum = 0.f;
+    if (S == 1) {
+        if (own < p.W && sh.state[own] == kLive) {
+            const float2 ms = sums[own];
+            M = ms.x;
+            sum = ms.y;
+        }
+    } else {
+        float2 ms[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int w = warp + i * kWarps;
+            ms[i] = w < p.W && lane < S && sh.state[w] == kLive ? sums[w * S + lane] : make_float2(-INFINITY, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (warp + i * kWarps >= p.W) break;
+            const float top = warp_max(ms[i].x);
+            const float all = warp_sum(isfinite(ms[i].x) ? ms[i].y * exp2f((ms[i].x - top) * kLog2e) : 0.f);
+            if (lane == i) {
+                M = top;
+                sum = all;
             }
         }
-        if (lane == 0) {
-            sh.basef[w] = static_cast<float>(sh.base[w]);
-            sh.invf[w] = static_cast<float>(sh.inv[w]);
-        }
-        __syncwarp();
-        if (sh.state[w] != kDead) size = fmaxf(size, fabsf(sh.basef[w]));
     }
+    float size = 0.f;                 // the largest |base| of the warp's rows
+    if (own < p.W) {
+        if (sh.state[own] == kLive) {
+            if (!isfinite(M)) {       // nothing but -inf, or a logit of +inf
+                sh.state[own] = kDead;
+                if (M > 0.f) flag_status(p.ws, SPEC_EINVAL);
+            } else {
+                sh.base[own] -= M + log_parts(sum);
+            }
+        }
+        sh.basef[own] = static_cast<float>(sh.base[own]);
+        sh.invf[own] = static_cast<float>(sh.inv[own]);
+        if (sh.state[own] != kDead) size = fabsf(sh.basef[own]);
+    }
+    size = warp_max(size);
     if (lane == 0) sh.bound[warp] = size;
     __syncthreads();
     for (int i = 0; i < kWarps; ++i) size = fmaxf(size, sh.bound[i]);
