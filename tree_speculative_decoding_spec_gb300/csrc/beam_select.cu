@@ -506,7 +506,7 @@ __device__ __noinline__ int join_slowly(Join& sh, const Params& p, const unsigne
     return p.K;
 }
 
-__global__ void __launch_bounds__(kThreads) k_join(const Params p) {
+__global__ void __launch_bounds__(kThreads, 2) k_join(const Params p) {
     __shared__ Join sh;
     constexpr int kKeep = 4;          // candidates a thread has in registers; the rest is read twice
     const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -593,7 +593,16 @@ __global__ void __launch_bounds__(kThreads) k_join(const Params p) {
     float near[kKeep], mine = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) mine = fmaxf(mine, near[i] = near_rank(threadIdx.x + i * kThreads, kept[i]));
-    for (int c = threadIdx.x + kKeep * kThreads; c < n; c += kThreads) mine = fmaxf(mine, near_rank(c, cand[c]));
+    auto others = [&](auto&& f) {     // the rest, kKeep at a time
+        for (int c0 = threadIdx.x + kKeep * kThreads; c0 < n; c0 += kKeep * kThreads) {
+            unsigned long long k[kKeep];
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) k[i] = c0 + i * kThreads < n ? cand[c0 + i * kThreads] : 0;
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) f(c0 + i * kThreads, k[i]);
+        }
+    };
+    others([&](int c, unsigned long long k) { mine = fmaxf(mine, near_rank(c, k)); });
     const unsigned kth = warp_kth(mine == -INFINITY ? 0u : order_key(mine), (K + 3) / 4);
     __syncthreads();                  // sh.bound has been read
     if (lane == 0) sh.bound[warp] = __uint_as_float(kth);
@@ -609,10 +618,7 @@ __global__ void __launch_bounds__(kThreads) k_join(const Params p) {
     };
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) offer(threadIdx.x + i * kThreads, kept[i], near[i]);
-    for (int c = threadIdx.x + kKeep * kThreads; c < n; c += kThreads) {
-        const unsigned long long k = cand[c];
-        offer(c, k, near_rank(c, k));
-    }
+    others([&](int c, unsigned long long k) { offer(c, k, near_rank(c, k)); });
     __syncthreads();
     const int m = sh.count;
     int written = min(m, K);
