@@ -209,7 +209,8 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
     extern __shared__ unsigned s_rank[];              // ranks of the keys, where they fit
     __shared__ int s_hist[kBins];
     __shared__ int part[2][kWarps];
-    __shared__ int s_digit, s_above;
+    __shared__ int s_digit, s_above, s_equal;
+    __shared__ unsigned s_ends[2][kWarps];
     __shared__ Few few;
     const int h = blockIdx.x, b = blockIdx.y;
     griddep_launch();
@@ -262,10 +263,8 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
             equal_bits = above_bits + words;
         }
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        // (the first digit's histogram of the others on the way: it serves unless the protected ones are too many)
-        for (int i = threadIdx.x; i < kBins; i += kThreads) s_hist[i] = 0;
-        __syncthreads();
         int mine = 0;
+        unsigned least = 0xffffffffu, largest = 0;       // rank of the others
         constexpr int kAhead = 8;     // words of a warp on their way together (one by one: 33 us for 16384 keys)
         for (int w0 = warp; w0 < words; w0 += kAhead * kWarps) {
             int at[kAhead];
@@ -284,7 +283,10 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
                 if (i < n) {
                     const unsigned r = order_key(x[k]);
                     if (cached) s_rank[i] = r;
-                    if (!(bits >> lane & 1)) atomicAdd(&s_hist[r >> 21], 1);
+                    if (!(bits >> lane & 1)) {
+                        least = min(least, r);
+                        largest = max(largest, r);
+                    }
                 }
                 if (lane == 0) {
                     safe_bits[w] = bits;
@@ -292,28 +294,43 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
                 }
             }
         }
+        least = __reduce_min_sync(0xffffffffu, least);
+        largest = __reduce_max_sync(0xffffffffu, largest);
+        if (lane == 0) {
+            s_ends[0][warp] = least;
+            s_ends[1][warp] = largest;
+        }
         int zero = 0, safe, none;
         scan2(part, mine, zero, safe, none);
+        least = __reduce_min_sync(0xffffffffu, lane < kWarps ? s_ends[0][lane] : 0xffffffffu);
+        largest = __reduce_max_sync(0xffffffffu, lane < kWarps ? s_ends[1][lane] : 0u);
         auto rank_at = [&](int i) { return cached ? s_rank[i] : order_key(acc[i]); };
         // all protected ones are kept and the best of the others, or the best of the protected ones
         const bool among_safe = safe > p.budget;
         const unsigned flip = among_safe ? 0u : ~0u;     // safe_bits[w] ^ flip: keys in play
         int want = among_safe ? p.budget : p.budget - safe;
-        // the want-th largest rank of those in play, eleven bits at a time (the last time ten)
-        unsigned prefix = 0, mask = 0;
-        if (want > 0) {
-            for (int shift = 21; ; shift = max(shift - 11, 0)) {
-                const unsigned digits = shift ? kBins - 1 : (kBins >> 1) - 1;
-                const bool have = shift == 21 && !among_safe;
-                if (!have) {
-                    for (int i = threadIdx.x; i < kBins; i += kThreads) s_hist[i] = 0;
-                    __syncthreads();
-                }
+        // The want-th largest rank of those in play, by digits of eleven bits.  The digits begin at the highest bit in which the
+        // ranks differ from the least: the weights' exponents are much the same, and with digits of the rank itself they met
+        // in a few counters (64.4 us with the copies for 128 heads of up to 16384 keys, so 62.9).  A digit that leaves no more than are wanted is the last.
+        const bool choose = want > 0;
+        unsigned border = 0;          // ranks from here on are above those that are kept in part
+        if (choose) {
+            if (among_safe) {
+                least = 0;
+                largest = 0xffffffffu;
+            }
+            const int bits = 32 - __clz(largest - least);
+            int shift = max(bits - 11, 0), width = bits - shift;
+            unsigned prefix = 0, mask = 0;
+            for (;;) {
+                const unsigned digits = (1u << width) - 1;
+                for (int i = threadIdx.x; i < kBins; i += kThreads) s_hist[i] = 0;
+                __syncthreads();
 #pragma unroll 4
-                for (int w = have ? words : warp; w < words; w += kWarps) {
+                for (int w = warp; w < words; w += kWarps) {
                     const int i = w * 32 + lane;
-                    const unsigned r = i < n ? rank_at(i) : 0;
-                    if (i < n && (r & mask) == prefix && ((safe_bits[w] ^ flip) >> lane & 1)) atomicAdd(&s_hist[(r >> shift) & digits], 1);
+                    const unsigned x = (i < n ? rank_at(i) : 0) - least;
+                    if (i < n && ((safe_bits[w] ^ flip) >> lane & 1) && (x & mask) == prefix) atomicAdd(&s_hist[(x >> shift) & digits], 1);
                 }
                 __syncthreads();
                 // thread t has bins kBins - 1 - 4 t and the three below
@@ -327,6 +344,7 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
                     if (above < want && above + c[j] >= want) {
                         s_digit = kBins - 1 - kEach * threadIdx.x - j;
                         s_above = above;
+                        s_equal = c[j];
                     }
                     above += c[j];
                 }
@@ -334,17 +352,23 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
                 prefix |= static_cast<unsigned>(s_digit) << shift;
                 mask |= digits << shift;
                 want -= s_above;      // now: how many of those equal so far are wanted
-                if (shift == 0) break;
-                __syncthreads();      // s_digit has been read
+                const bool whole = want == s_equal;
+                if (whole) want = 0;
+                if (whole || shift == 0) {
+                    border = least + prefix + (whole ? 0 : 1);
+                    break;
+                }
+                width = min(shift, 11);
+                shift -= width;
             }
 #pragma unroll 4
             for (int w = warp; w < words; w += kWarps) {
                 const int i = w * 32 + lane;
                 const unsigned r = i < n ? rank_at(i) : 0, play = safe_bits[w] ^ flip;
-                const unsigned up = __ballot_sync(0xffffffffu, i < n && r > prefix) & play, eq = __ballot_sync(0xffffffffu, i < n && r == prefix) & play;
+                const unsigned up = __ballot_sync(0xffffffffu, i < n && r >= border) & play, eq = __ballot_sync(0xffffffffu, i < n && r == border - 1) & play;
                 if (lane == 0) {
                     above_bits[w] = among_safe ? up : up | safe_bits[w];
-                    equal_bits[w] = eq;
+                    equal_bits[w] = eq;   // (looked at where some of them are wanted)
                 }
             }
         }
@@ -364,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
         };
         auto inside = [&](int w) { return n - w * 32 >= 32 ? ~0u : (1u << (n - w * 32)) - 1; };
         for (int w = w0; w < w1; ++w) {
-            unsigned kept = mask ? above_bits[w] : safe_bits[w];     // (nothing wanted beside the protected ones)
+            unsigned kept = choose ? above_bits[w] : safe_bits[w];   // (nothing wanted beside the protected ones)
             if (want > 0)
                 for (unsigned eq = equal_bits[w]; eq && equal < want; eq &= eq - 1, ++equal) kept |= eq & -eq;
             above_bits[w] = kept;
