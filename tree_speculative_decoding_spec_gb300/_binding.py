@@ -702,6 +702,7 @@ def tree_attention_scored_workspace_size(tree, B, Hq, Hkv, Lmax, D, dtype):
 
 _Tensor, _i32, _f32, _empty = torch.Tensor, torch.int32, torch.float32, torch.empty
 _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream   # of a device in use
+_raw_alloc, _raw_delete = torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete
 
 
 def _at(t, name, dtype, index, *shape):
@@ -1011,6 +1012,24 @@ def _sized(size, index, stream, *args):
     return _new(stream, index, torch.uint8, n, kept=False)
 
 
+def _call_sized(name, index, stream, ws, size, sizes, *args):
+    """_call with a workspace behind the arguments: ws, or one of size(*sizes) bytes for the call alone.
+
+    That one is the allocator's memory of the call's stream as a tensor's would be, but no tensor: to make and free one took
+    6 us of the host's 13 for a small call."""
+    if ws is not None or stream is not None or _device() != index:
+        ws = _sized(size, index, stream, *sizes) if ws is None else ws
+        return _call(name, index, stream, *args, _buffer(ws, index), ws.nbytes)
+    n, raw = size(*sizes), _raw_stream(index)
+    at = _raw_alloc(n, raw)
+    try:
+        status = getattr(_lib, name)(*args, at, n, raw)
+    finally:
+        _raw_delete(at)
+    if status != 0:
+        _check(name, status)
+
+
 def beam_select(logits, scores, K, eos=-1, ended=None, length=None, alpha=0.0, token=None, parent=None, score=None,
                 ended_out=None, length_out=None, ws=None, stream=None):
     """The K best continuations over beams and vocabulary: returns (token, parent, score, ended, length), all [B, K].
@@ -1047,10 +1066,8 @@ def beam_select(logits, scores, K, eos=-1, ended=None, length=None, alpha=0.0, t
         outs = (_at(token, "token", _i32, index, B, K), _at(parent, "parent", _i32, index, B, K),
                 _at(score, "score", torch.float32, index, B, K), _at(ended_out, "ended_out", _i32, index, B, K),
                 _at(length_out, "length_out", _i32, index, B, K))
-    if ws is None:
-        ws = _sized(beam_select_workspace_size, index, stream, B, W, V, K)
-    _call("beam_select", index, stream, logits.data_ptr(), sw, sp, ep, np_, B, W, V, K, eos, float(alpha), dt, *outs, _buffer(ws, index),
-          ws.nbytes)
+    _call_sized("beam_select", index, stream, ws, beam_select_workspace_size, (B, W, V, K), logits.data_ptr(), sw, sp, ep, np_, B, W, V, K,
+                eos, float(alpha), dt, *outs)
     return token, parent, score, ended_out, length_out
 
 
@@ -1074,9 +1091,8 @@ def beam_reorder(state, parent, ws=None, stream=None):
     pp, B, W = _beams(parent, index)
     if tuple(state.shape[:2]) != (B, W) or not state.is_contiguous():
         raise ValueError(f"state must be contiguous [{B}, {W}, ...], got {tuple(state.shape)}")
-    if ws is None:
-        ws = _new(stream, index, torch.uint8, beam_reorder_workspace_size(), kept=False)
-    _call("beam_reorder", index, stream, state.data_ptr(), state.nbytes // (B * W) if B * W else 0, pp, B, W, _buffer(ws, index), ws.nbytes)
+    _call_sized("beam_reorder", index, stream, ws, beam_reorder_workspace_size, (), state.data_ptr(), state.nbytes // (B * W) if B * W else 0,
+                pp, B, W)
     return state
 
 
@@ -1185,10 +1201,8 @@ def kv_evict(k_cache, v_cache, prefix_len, acc, pos, budget, seen=None, sink=0, 
     pp = _at(prefix_len, "prefix_len", _i32, index, B)
     sp = None if seen is None else _at(seen, "seen", _i32, index, B)
     len_out = _new(stream, index, _i32, B) if len_out is None else len_out
-    if ws is None:
-        ws = _sized(kv_evict_workspace_size, index, stream, B, Hkv, Lmax, budget)
-    _call("kv_evict", index, stream, kp, vp, pp, sp, ap, op, B, Hkv, Lmax, D, budget, sink, recent, *out, Lout,
-          _at(len_out, "len_out", _i32, index, B), dt, _buffer(ws, index), ws.nbytes)
+    _call_sized("kv_evict", index, stream, ws, kv_evict_workspace_size, (B, Hkv, Lmax, budget), kp, vp, pp, sp, ap, op, B, Hkv, Lmax, D, budget,
+                sink, recent, *out, Lout, _at(len_out, "len_out", _i32, index, B), dt)
     return len_out
 
 
@@ -1209,10 +1223,8 @@ def kv_evict_paged(k_pool, v_pool, block_table, prefix_len, acc, pos, budget, se
     pp = _at(prefix_len, "prefix_len", _i32, index, B)
     sp = None if seen is None else _at(seen, "seen", _i32, index, B)
     len_out = _new(stream, index, _i32, B) if len_out is None else len_out
-    if ws is None:
-        ws = _sized(kv_evict_workspace_size, index, stream, B, Hkv, most * bs, budget)
-    _call("kv_evict_paged", index, stream, kp, vp, blocks, tp, most, bs, pp, sp, ap, op, B, Hkv, D, budget, sink, recent, *out,
-          _at(len_out, "len_out", _i32, index, B), dt, _buffer(ws, index), ws.nbytes)
+    _call_sized("kv_evict_paged", index, stream, ws, kv_evict_workspace_size, (B, Hkv, most * bs, budget), kp, vp, blocks, tp, most, bs, pp, sp,
+                ap, op, B, Hkv, D, budget, sink, recent, *out, _at(len_out, "len_out", _i32, index, B), dt)
     return len_out
 
 
