@@ -1144,16 +1144,14 @@ def _weigh(name, rows, q, lse, keys, prefix_len, acc, pos, seen, n_rows, accept_
     if accept_path is not None:
         P = accept_path.shape[1] if isinstance(accept_path, _Tensor) and accept_path.dim() == 2 else 0
         path = _at(accept_path, "accept_path", _i32, index, B, P)
-    if ws is None:
-        ws = _sized(kv_weigh_workspace_size, index, stream, B, Hq, Hkv, T, P, cap, D, dt)
-    _call(name, index, stream, qp, lp, *keys, pp, sp, rp, al, path, P, B, Hq, Hkv, T, *dims, D, 0.0 if scale is None else float(scale),
-          float(decay), dt, ap, op, _buffer(ws, index), ws.nbytes)
-    return ws
+    _call_sized(name, index, stream, ws, kv_weigh_workspace_size, (B, Hq, Hkv, T, P, cap, D, dt), qp, lp, *keys, pp, sp, rp, al, path, P, B, Hq,
+                Hkv, T, *dims, D, 0.0 if scale is None else float(scale), float(decay), dt, ap, op)
+    return acc
 
 
 def kv_weigh(q, lse, k_cache, prefix_len, acc, pos=None, seen=None, n_rows=None, accept_len=None, accept_path=None, decay=1.0,
              scale=None, ws=None, stream=None):
-    """Add the attention weight that cached keys receive from the sequences' last rows to acc [B, Hkv, Lmax]: returns ws.
+    """Add the attention weight that cached keys receive from the sequences' last rows to acc [B, Hkv, Lmax]: returns acc.
 
     q [B, Hq, T, D] and lse [B, Hq, T] of an attention; prefix_len [B] with the rows' own keys in it; the rows are
     the first n_rows[b] (None: T), or the nodes of accept_path (tree_accept).  pos [B, Hkv, Lmax] int32: see kv_evict."""
