@@ -156,3 +156,45 @@ def test_far_into_large_buffers():
     r = st.beam_select(x, torch.tensor([[-1.0, -1.5, -0.5]], device="cuda"), 4)
     w = beam.beam_select(x.double().cpu().numpy(), np.array([[-1.0, -1.5, -0.5]]), 4)
     assert r[0].tolist() == w["token"].tolist() and r[1].tolist() == w["parent"].tolist()
+
+
+def test_calls_in_a_row_see_what_the_ones_before_them_wrote():
+    """Every call's first kernel may start while the last one's still runs: a chain in place, each step on the results of the one
+    before, gives the same bits with and without a pause between the calls."""
+    import torch
+    st = lib()
+    g = torch.Generator().manual_seed(9)
+    B, W, V, Hq, Hkv, D, L = 3, 6, 40000, 8, 2, 64, 640
+    x = [torch.randn(B, W, V, generator=g).mul_(2).cuda() for _ in range(2)]
+    q, q2 = torch.randn(B, Hq, 1, D, generator=g).bfloat16().cuda(), torch.randn(B, Hq, 200, D, generator=g).bfloat16().cuda()
+    lse, lse2 = torch.full((B, Hq, 1), 4.0, device="cuda"), torch.full((B, Hq, 200), 4.0, device="cuda")
+    kv = [torch.randn(B * W, Hkv, L, D, generator=g).bfloat16().cuda() for _ in range(2)]
+    start, end, n = _i32([0, 7, 300]), _i32([640, 600, 301]), _i32([640, 630, 500])
+
+    def chain(pause):
+        scores, ended, length = torch.zeros(B, W, device="cuda"), torch.zeros(B, W, dtype=torch.int32, device="cuda"), torch.zeros(B, W, dtype=torch.int32, device="cuda")
+        hist = torch.arange(B * W * 40, device="cuda").view(B, W, 40)
+        k, v = kv[0].clone(), kv[1].clone()
+        acc, pos = torch.zeros(B, Hkv, L, device="cuda"), _i32(np.tile(np.arange(L), (B, Hkv, 1)))
+        out = []
+        for i in range(12):
+            token, parent, *_ = st.beam_select(x[i & 1], scores, W, eos=3, ended=ended, length=length, alpha=0.5, token=torch.empty_like(ended),
+                                               parent=torch.empty_like(ended), score=scores, ended_out=ended, length_out=length)
+            pause()
+            st.beam_reorder(hist, parent)
+            pause()
+            hist[:, :, i] = token
+            st.kv_reorder(k, v, parent, start, end)
+            pause()
+            st.kv_weigh(q2, lse2, k[:B], n, acc, pos=pos, decay=0.9)
+            pause()
+            st.kv_weigh(q, lse, k[:B], n, acc, pos=pos)
+            pause()
+            out.append(st.kv_evict(k[:B], v[:B], n, acc, pos, 600 - 20 * i))
+            pause()
+        torch.cuda.synchronize()
+        return [scores, ended, length, hist, k, v, acc, pos, *out]
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(chain(lambda: None), want))

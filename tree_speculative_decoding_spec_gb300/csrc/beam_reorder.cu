@@ -77,6 +77,7 @@ __device__ void check_all(const Params& p) {
 // (Without a limit the compiler keeps every beam's addresses beside its values: 172 registers for 8 beams, 88 us for 45.)
 template <typename V, int MOST>
 __global__ void __launch_bounds__(kThreads, MOST <= 4 ? 6 : MOST <= 8 ? 4 : MOST <= 16 ? 2 : 1) k_reorder(const Params p) {
+    griddep_wait();                   // the stream's kernel before this one may still run: its results are behind here
     if (blockIdx.x == 0) {            // one CTA more than there are for the rows
         if (blockIdx.y == 0 && blockIdx.z == 0) check_all(p);
         return;
@@ -180,7 +181,7 @@ spec_status run(const char* name, const Params& p, int64_t positions, cudaStream
     const int64_t most = std::max<int64_t>(1, (positions * (rb / width) + kThreads - 1) / kThreads);
     const int64_t want = (16 * device_sm_count() + p.B * lines - 1) / (p.B * lines);
     const unsigned per = static_cast<unsigned>(std::min(most, want));
-    SPEC_CUDA_TRY(launch(name, kern, dim3(per + 1, p.B, static_cast<unsigned>(lines)), dim3(kThreads), 0, s, p));
+    SPEC_CUDA_TRY(launch_ex(name, kern, dim3(per + 1, p.B, static_cast<unsigned>(lines)), dim3(kThreads), 0, s, true, p));
     return SPEC_OK;
 }
 

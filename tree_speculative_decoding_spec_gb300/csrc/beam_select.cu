@@ -266,6 +266,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, kPerSm) k_slices(const Params p) {
     constexpr int E = Vec<T>::E;
     __shared__ Shared sh;
+    griddep_wait();                   // in front of the trigger: the join reads the call's inputs without a wait of its own
     clear_status_then_trigger(p.ws);
     const int row_at = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -740,7 +741,7 @@ extern "C" spec_status beam_select(const void* logits, int64_t row_stride, const
     p.sums = reinterpret_cast<float2*>(at + beam::cand_bytes(rows, K, S));
     p.token = token; p.parent = parent; p.score = score; p.ended_out = ended_out; p.length_out = length_out; p.ws = ws;
     auto kern = dt == SPEC_BF16 ? beam::k_slices<__nv_bfloat16> : beam::k_slices<float>;
-    SPEC_CUDA_TRY(launch("beam_slices", kern, dim3(static_cast<unsigned>(rows * S)), dim3(beam::kThreads), 0, s, p));
+    SPEC_CUDA_TRY(launch_ex("beam_slices", kern, dim3(static_cast<unsigned>(rows * S)), dim3(beam::kThreads), 0, s, true, p));
     SPEC_CUDA_TRY(launch_ex("beam_join", beam::k_join, dim3(B), dim3(beam::kThreads), 0, s, true, p));
     return SPEC_OK;
 }

@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
     __shared__ unsigned s_ends[2][kWarps];
     __shared__ Few few;
     const int h = blockIdx.x, b = blockIdx.y;
+    griddep_wait();                   // the stream's kernel before this one may still run: its results are behind here
     griddep_launch();
     if (h == p.Hkv) {                 // one CTA more: the status word, which no other writes
         if (b != 0) return;
@@ -555,7 +556,7 @@ spec_status run(Params& p, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s
     const bool step = p.cap - p.budget <= kGone && p.cap <= 4096;
     auto pick = step ? k_pick<256> : k_pick<1024>;
     if (smem > 30000) SPEC_CUDA_TRY(cudaFuncSetAttribute(pick, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4 + kCached / 8 * 3));
-    SPEC_CUDA_TRY(launch("evict_pick", pick, dim3(p.Hkv + 1, p.B), dim3(step ? 256 : 1024), smem, s, p));
+    SPEC_CUDA_TRY(launch_ex("evict_pick", pick, dim3(p.Hkv + 1, p.B), dim3(step ? 256 : 1024), smem, s, true, p));
     if (!p.here) {
         const int64_t rows = kBatch * (kMoveThreads / p.row16);
         const int64_t most = ((p.in_place ? p.most : p.places) + rows - 1) / rows;

@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p, int spli
     __shared__ float s_lse[R];
     __shared__ int s_last[R];         // the last key that a row sees; -1: no row
     const int h = blockIdx.y, b = blockIdx.z;
+    griddep_wait();                   // the stream's kernel before this one may still run: its results are behind here
     griddep_launch();
     if (blockIdx.x == 0) {
         if (h == 0 && b == 0) check_all<kThreads>(p);
@@ -151,7 +152,7 @@ spec_status run_fma(const Params& p, float* parts, cudaStream_t s) {
     auto kern = wide ? k_weigh_fma<D, 4> : k_weigh_fma<D, 1>;
     const size_t smem = sizeof(float) * D * (kKeys + kGroups * (wide ? 4 : 1));
     if (smem > 40960) SPEC_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-    SPEC_CUDA_TRY(launch("kv_weigh_fma", kern, dim3((p.cap + kKeys - 1) / kKeys * splits + 1, p.Hkv, p.B), dim3(kThreads), smem, s, p, splits, parts));
+    SPEC_CUDA_TRY(launch_ex("kv_weigh_fma", kern, dim3((p.cap + kKeys - 1) / kKeys * splits + 1, p.Hkv, p.B), dim3(kThreads), smem, s, true, p, splits, parts));
     if (splits > 1)
         SPEC_CUDA_TRY(launch_ex("kv_weigh_parts", k_weigh_parts, dim3((p.cap + kThreads - 1) / kThreads, p.Hkv, p.B), dim3(kThreads), 0, s, true, p, splits, parts));
     return SPEC_OK;

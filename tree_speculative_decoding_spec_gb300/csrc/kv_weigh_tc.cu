@@ -357,10 +357,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
         mbar_init(&sm.drain, MANY ? 2 : 1);
         sm.abort_flag = 0;
         sm.bad = 0;
-        if (MANY) tp.records[blockIdx.x] = Record{0, 0, 0, 0, 0, 0, 0, 0};
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
+    griddep_wait();                   // the stream's kernel before this one may still run: its results are behind here
+    if (MANY && threadIdx.x == 0) tp.records[blockIdx.x] = Record{0, 0, 0, 0, 0, 0, 0, 0};
     if (warp == kTma) plan<MANY>(tp, sm);
     tc_fence_before();
     __syncthreads();
@@ -830,7 +831,7 @@ static spec_status launch_tc(const Maps& m, TcParams& tp, cudaStream_t s) {
     auto kern = k_weigh_tc<D, MANY>;
     SPEC_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)));
     const int ctas = device_sm_count();
-    SPEC_CUDA_TRY(launch("kv_weigh_tc", kern, dim3(ctas), dim3(kTcThreads), kSmem, s, m, tp));
+    SPEC_CUDA_TRY(launch_ex("kv_weigh_tc", kern, dim3(ctas), dim3(kTcThreads), kSmem, s, true, m, tp));
     if (MANY) SPEC_CUDA_TRY(launch_ex("kv_weigh_join", k_weigh_join, dim3(ctas), dim3(2 * kKeys), 0, s, true, tp, ctas));
     return SPEC_OK;
 }
