@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
 
     if (warp == kTma) {
         // ------------------------------------------------ keys, and the chunks of rows
+        const uint64_t policy = l2_policy_evict_first();
         for (; ok && w.more; w.next()) {
             const int stage = k_ring.at;
             if (k_ring.round > 0 && !(ok = warp_wait_for(&sm.k_empty[stage], k_ring.empty(), abort_flag))) break;
@@ -388,8 +389,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
             if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[stage], __popc(there) * tp.box * 128 * kH);
             __syncwarp();
             if (row >= 0)
-                for (int hh = 0; hh < kH; ++hh)
-                    tma_load_2d(dst + ((in / kKeys) * kH + hh) * kKHalf + in % kKeys * 128, &mp.k, &sm.k_full[stage], hh * 64, static_cast<int>(row));
+                for (int hh = 0; hh < kH; ++hh) {
+                    uint8_t* to = dst + ((in / kKeys) * kH + hh) * kKHalf + in % kKeys * 128;
+                    // (few: read once, and first to leave the L2; single tokens took 65 us without that, so 58.  A prompt's keys
+                    // are read again by the CTAs that have other rows of theirs)
+                    if (MANY) tma_load_2d(to, &mp.k, &sm.k_full[stage], hh * 64, static_cast<int>(row));
+                    else tma_load_2d_hint(to, &mp.k, &sm.k_full[stage], hh * 64, static_cast<int>(row), policy);
+                }
             k_ring.next(tp.k_stages);
             if (MANY) {
                 int qh;
