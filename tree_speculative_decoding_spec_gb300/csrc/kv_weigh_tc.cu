@@ -391,8 +391,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
             if (row >= 0)
                 for (int hh = 0; hh < kH; ++hh) {
                     uint8_t* to = dst + ((in / kKeys) * kH + hh) * kKHalf + in % kKeys * 128;
-                    // (few: read once, and first to leave the L2; single tokens took 65 us without that, so 58.  A prompt's keys
-                    // are read again by the CTAs that have other rows of theirs)
+                    // (few: read once, so first to leave the L2: what others keep there stays.  Twelve caches of 64 sequences in
+                    // turn: 62.8 us a call, 63.6 without; three in turn, 1 GB in all: 56.6 and 63.1, as a part of each is still
+                    // there the next time.  A prompt's keys are read again by the CTAs that have other rows of theirs)
                     if (MANY) tma_load_2d(to, &mp.k, &sm.k_full[stage], hh * 64, static_cast<int>(row));
                     else tma_load_2d_hint(to, &mp.k, &sm.k_full[stage], hh * 64, static_cast<int>(row), policy);
                 }
