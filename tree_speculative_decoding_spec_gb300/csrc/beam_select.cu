@@ -455,7 +455,7 @@ struct Join {
     int count;
 };
 
-// (without branches: the ranks' loops took four times as long with them)
+// (without branches: with them, and the rows' sums one after the other, the join of 64 beams took 63 us for 32)
 __device__ __forceinline__ bool above(const Entry& x, const Entry& y) { return (x.key > y.key) | ((x.key == y.key) & (x.tie < y.tie)); }
 
 __device__ __forceinline__ Entry entry_of(const Join& sh, const Params& p, int w, unsigned long long k) {
@@ -645,8 +645,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_join(const Params p) {
 
 // Slices of a row: the number that makes the longest SM's work least, in units of a chunk, some 0.4 us: a slice costs its
 // chunks and 2.6 more to start and end, a lone one is as long as 6 and 1.4 times its chunks, a candidate in the
-// join a two-thousandth.  (768 rows of 131072: 57 us in one slice, 63 in two, 71 in four; 128 rows of 32000: 12.5, 11.7, 12.5;
-// 30 rows of 50257: 13.3 in four, 11.4 in twelve.)
+// join a two-thousandth.  (768 rows of 131072: 51 us in one slice, 57 in two, 63 in four; 128 rows of 32000: 11.1, 10.6, 11.6;
+// 30 rows of 50257: 13.4 in four, 10.4 in twelve.)
 int slices_of(int64_t rows, int W, int V, int K) {
     const int64_t sms = device_sm_count();
     const double chunks = V / static_cast<double>(kThreads * kVecs * 8);
