@@ -211,6 +211,17 @@ def test_both_ways_through_and_their_borders(T, Hq, Hkv, n):
     _assert_weighed(t, acc, pos)
 
 
+@pytest.mark.parametrize("T,Hq,Hkv", [(47, 12, 2), (48, 12, 2), (48, 5, 1), (79, 3, 1), (80, 3, 1), (63, 32, 1)])
+@pytest.mark.parametrize("n", [(300, 80, 129), (80, 1200, 513)])
+def test_short_prompts_on_both_sides_of_the_choice(T, Hq, Hkv, n):
+    st = lib()
+    t = _case(("bf16", 3, Hq, Hkv, T, 64, 0, n, (T, min(T, 50), 0), 0.5), seed=9)
+    ws = _ws(t)
+    acc, pos = _run(st, t, ws)
+    assert st.spec_read_device_status(ws) == 0
+    _assert_weighed(t, acc, pos)
+
+
 def _ws(t):
     import torch
     return torch.empty(1 << 20, dtype=torch.uint8, device="cuda").fill_(255)

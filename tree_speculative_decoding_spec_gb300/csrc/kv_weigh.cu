@@ -147,6 +147,7 @@ int splits_of(int B, int Hkv, int g, int T, int path_len, int cap) {
 template <int D>
 spec_status run_fma(const Params& p, float* parts, cudaStream_t s) {
     const int most = p.Hq / p.Hkv * (p.path ? p.P : p.T);
+    // one row a thread or four (4 sequences of 2000 keys: 16 rows of a KV head 9.7 and 12.2 us, 32 rows 15.1 and 12.4)
     const bool wide = most > kGroups;
     const int splits = splits_of(p.B, p.Hkv, p.Hq / p.Hkv, p.T, p.path ? p.P : 0, p.cap);
     auto kern = wide ? k_weigh_fma<D, 4> : k_weigh_fma<D, 1>;

@@ -820,8 +820,11 @@ __global__ void __launch_bounds__(2 * kKeys) k_weigh_join(const TcParams tp, int
 constexpr size_t kSmem = 232448;      // of one CTA, all there is: no two share an SM's TMEM
 
 static int few_rows(int g, int T, int P) { return g * (P ? P : T); }
-// Rows of a prompt fill chunks of 128 of one query head; shorter ones are better off side by side, several heads in a pass.
-bool weigh_many(int g, int T, int P) { return !P && T >= 96 && static_cast<int64_t>(g) * T > kMostRows; }
+// Rows of a prompt fill chunks of 128 of one query head, shorter ones go side by side, several heads in a pass.  A pass takes
+// some 18 cycles for 128 keys and row, a chunk 980 however few of its rows there are.  In us, few and many: 8 sequences of 4000 keys
+// and 8 heads of 8, 32 rows 40, 62; 48 rows (two passes) 64, 69; 64 rows 79, 69; of 300 keys 26, 15; 42, 16; 52, 16; 32 heads of one,
+// 64 rows 18.3, 19.6; 80 rows 19.9, 19.8; 96 rows 21.5, 19.8.  So from 48 rows on if they need two passes, else from 80.
+bool weigh_many(int g, int T, int P) { return !P && T >= (static_cast<int64_t>(g) * T > kMostRows ? 48 : 80); }
 
 size_t weigh_tc_bytes(int g, int T, int P) {
     return weigh_many(g, T, P) ? static_cast<size_t>(device_sm_count()) * (sizeof(Record) + 4 * kKeys * sizeof(float)) : 0;
