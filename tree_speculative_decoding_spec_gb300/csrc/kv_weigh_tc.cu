@@ -523,46 +523,55 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_weigh_tc(const __grid_constan
                     const int tid = threadIdx.x - 32 * kRowsWarp;
                     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
                     const int64_t q0 = static_cast<int64_t>(w.b) * p.Hq + w.h * tp.g;
-                    // asynchronous copies, so that all of a thread's are on their way together; rows behind the last are zeros.
-                    // A thread has the same 16 bytes of every 64 / (D / 8)-th row, which head's and which of it kept in step
-                    constexpr int kParts = D / 8, kStep = 64 / kParts;
-                    const int part = tid % kParts;
-                    int r = tid / kParts, i = tp.row0 + r, gi = 0;
-                    if (w.rows.count > 0) {
-                        gi = i / w.rows.count;
-                        i -= gi * w.rows.count;
-                    }
-                    for (; r < padded; r += kStep) {
-                        const bool there = r < total;
-                        const int64_t row = there ? (q0 + gi) * p.T + node_of(p, w.b, i) : 0;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                                     ::"r"(smem_u32(sQ + (qs * kH + part / 8) * q_half + r * 128 + ((part % 8) ^ (r & 7)) * 16)),
-                                       "l"(q + row * D + part * 8), "r"(there ? 16 : 0) : "memory");
-                        for (i += kStep; i >= w.rows.count && there; i -= w.rows.count) ++gi;
-                    }
-                    // their lse, four at a time; the last key that each sees
-                    bool odd = false;
-                    for (int r0 = tid; r0 < padded; r0 += 256) {
-                        float l[4];
-                        int ii[4];
+                    // lse, four rows a thread, and a path's nodes: on their way while the rows are
+                    float l[4];
+                    int ii[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int rr = tp.row0 + r0 + 64 * k;
-                            l[k] = INFINITY;
-                            if (r0 + 64 * k < total) {
-                                const int head = rr / w.rows.count;
-                                ii[k] = rr - head * w.rows.count;
-                                l[k] = p.lse[(q0 + head) * p.T + node_of(p, w.b, ii[k])];
-                            }
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = tid + 64 * k, rr = tp.row0 + r;
+                        l[k] = INFINITY;
+                        if (r < total) {
+                            const int head = rr / w.rows.count;
+                            ii[k] = rr - head * w.rows.count;
+                            l[k] = p.lse[(q0 + head) * p.T + node_of(p, w.b, ii[k])];
                         }
+                    }
+                    const int node_at = p.path && lane < w.rows.count ? node_of(p, w.b, lane) : 0;
+                    // Asynchronous copies, so that all of a thread's are on their way together; rows behind the last are zeros.
+                    // A thread has the same 16 bytes of every 64 / (D / 8)-th row; which head's it is and which of it go in steps.  (With
+                    // every row's address worked out by itself, and lse behind them, 8 sequences of 300 keys and 32 rows of 8 heads
+                    // took 26 us where this takes 13)
+                    constexpr int kParts = D / 8, kStep = 64 / kParts;
+                    const int part = tid % kParts, count = max(w.rows.count, 1);
+                    const int step_head = kStep / count, step_i = kStep - step_head * count;
+                    int r = tid / kParts, gi = (tp.row0 + r) / count, i = tp.row0 + r - gi * count;
+                    const int64_t head_size = static_cast<int64_t>(p.T) * D;
+                    const __nv_bfloat16* from = q + (q0 + gi) * head_size + part * 8;
+                    const uint32_t to = smem_u32(sQ + (qs * kH + part / 8) * q_half);
+#pragma unroll 4
+                    for (; r < padded; r += kStep) {
+                        const int node = p.path ? __shfl_sync(0xffffffffu, node_at, i) : i;
+                        const __nv_bfloat16* src = r < total ? from + node * D : q;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                                     ::"r"(to + r * 128 + ((part % 8) ^ (r & 7)) * 16), "l"(src), "r"(r < total ? 16 : 0) : "memory");
+                        i += step_i;
+                        from += step_head * head_size;
+                        if (i >= count) {
+                            i -= count;
+                            from += head_size;
+                        }
+                    }
+                    // the last key that each sees
+                    bool odd = false;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (r0 + 64 * k < padded) {
-                                const bool counts = isfinite(l[k]);
-                                if (!counts && r0 + 64 * k < total) odd = true;
-                                sm.nl2[qs][r0 + 64 * k] = counts ? -l[k] * kL2e : -INFINITY;
-                                sm.last[qs][r0 + 64 * k] = counts ? w.rows.n - w.rows.count + ii[k] : -1;
-                            }
+                    for (int k = 0; k < 4; ++k) {
+                        const int at = tid + 64 * k;
+                        if (at < padded) {
+                            const bool counts = isfinite(l[k]);
+                            if (!counts && at < total) odd = true;
+                            sm.nl2[qs][at] = counts ? -l[k] * kL2e : -INFINITY;
+                            sm.last[qs][at] = counts ? w.rows.n - w.rows.count + ii[k] : -1;
+                        }
                     }
                     odd = __any_sync(0xffffffffu, odd);
                     if (lane == 0) sm.odd[qs][warp - kRowsWarp] = odd;
