@@ -9,7 +9,7 @@
 // Two ways through, chosen on the host:
 //   few   at most 256 query rows of a KV head (generated tokens, accepted paths, short chains; more in
 //         several passes): a head's rows stay in shared memory while its keys stream through a ring of
-//         128-key tiles.  Bound by the keys' bytes up to some 200 rows.
+//         128-key tiles.  Bound by the keys' bytes up to some 130 rows.
 //   many  prompts: 256 keys stay while chunks of 128 query rows of one head stream through, each chunk
 //         multiplied with both halves of the keys: with 128 keys a CTA the rows would come out of L2 at
 //         9 TB/s.  Bound by the exponentials, one for each pair of row and key.
@@ -830,10 +830,10 @@ constexpr size_t kSmem = 232448;      // of one CTA, all there is: no two share 
 
 static int few_rows(int g, int T, int P) { return g * (P ? P : T); }
 // Rows of a prompt fill chunks of 128 of one query head, shorter ones go side by side, several heads in a pass.  A pass takes
-// some 18 cycles for 128 keys and row, a chunk 980 however few of its rows there are.  In us, few and many: 8 sequences of 4000 keys
-// and 8 heads of 8, 32 rows 40, 62; 48 rows (two passes) 64, 69; 64 rows 79, 69; of 300 keys 26, 15; 42, 16; 52, 16; 32 heads of one,
-// 64 rows 18.3, 19.6; 80 rows 19.9, 19.8; 96 rows 21.5, 19.8.  So from 48 rows on if they need two passes, else from 80.
-bool weigh_many(int g, int T, int P) { return !P && T >= (static_cast<int64_t>(g) * T > kMostRows ? 48 : 80); }
+// some 12 cycles for 128 keys and row, a chunk 980 however few of its rows there are.  In us, few and many: 8 sequences of 4000 keys
+// and 8 heads of 8, 48 rows (two passes) 48, 68; 64 rows 57, 68; 80 rows 76, 74; of 300 keys 22, 16; 25, 16; 35, 17; in one pass, 32
+// heads of one, 64 rows 16.5, 19.6; 128 rows 19.9, 19.4; 160 rows 22, 27.  So from 64 rows on, if they need more than a pass.
+bool weigh_many(int g, int T, int P) { return !P && T >= 64 && static_cast<int64_t>(g) * T > kMostRows; }
 
 size_t weigh_tc_bytes(int g, int T, int P) {
     return weigh_many(g, T, P) ? static_cast<size_t>(device_sm_count()) * (sizeof(Record) + 4 * kKeys * sizeof(float)) : 0;
