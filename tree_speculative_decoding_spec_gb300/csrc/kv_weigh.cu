@@ -24,9 +24,35 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // CTAs per 64 keys of one (sequence, KV head), over the rows that see any of them, 16 RPT at a time; where there
 // are few such tiles their chunks of rows go to several CTAs in turn, whose sums kv_weigh_parts adds up in order
-// (a prompt of 100 rows and 8 heads of 64: 33 us with one, 12 with splits).  A thread has four keys and RPT rows; operands
+// (a prompt of 100 rows and 8 heads of 64: 33 us with one, 11 with splits).  A thread has four keys and RPT rows; operands
 // lie in shared memory by head dimension, so that four keys come in one read.  CTA 0 of the first head
 // writes the status.
+//
+// Operands are [D][N] with groups of four rows exchanged by the head dimension: a warp reads 128 bytes of each of four rows,
+// and its 32 four-element columns meet in no bank; reads of a group of four rows of one element stay whole.  (A row a lane: as many
+// lines as lanes for each load; 33 sequences of 512 keys and 42 rows took 51 us where this takes 35.)
+template <int N> __device__ __forceinline__ int place(int d, int r) {
+    return d * N + ((((r >> 2) ^ ((d >> 2) & (N == 16 ? 3 : 7))) << 2) | (r & 3));
+}
+template <int D, int N> __device__ __forceinline__ void load_rows(float* s, const float* x, const int64_t* rows) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kEach = (N / 4) * (D / 32) / (kThreads / 32);
+    static_assert(kEach * (kThreads / 32) == (N / 4) * (D / 32), "whole rounds of the warps");
+    float v[kEach][4] = {};           // all on their way together
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int t = i * (kThreads / 32) + warp;
+        const int64_t at = rows[t % (N / 4) * 4 + lane / 8];
+        if (at >= 0) load4(x + at * D + (t / (N / 4) * 8 + lane % 8) * 4, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int t = i * (kThreads / 32) + warp;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[place<N>((t / (N / 4) * 8 + lane % 8) * 4 + j, t % (N / 4) * 4 + lane / 8)] = v[i][j];
+    }
+}
+
 template <int D, int RPT>
 __global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p, int splits, float* parts) {
     constexpr int R = kGroups * RPT;
@@ -35,6 +61,7 @@ __global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p, int spli
     float* qs = smem + D * kKeys;     // [D][R]
     __shared__ float s_lse[R];
     __shared__ int s_last[R];         // the last key that a row sees; -1: no row
+    __shared__ int64_t s_key[kKeys], s_row[R];   // where the keys and rows lie, -1: nowhere
     const int h = blockIdx.y, b = blockIdx.z;
     griddep_wait();                   // the stream's kernel before this one may still run: its results are behind here
     griddep_launch();
@@ -47,14 +74,9 @@ __global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p, int spli
     if (!rows.ok || k0 >= rows.n) return;
     const float* q = static_cast<const float*>(p.q);
     const float* k = static_cast<const float*>(p.k);
-    // a thread loads 16 bytes of the keys' rows at a time: key tid % 64, parts tid / 64 and on
-    for (int u = threadIdx.x; u < kKeys * (D / 4); u += kThreads) {
-        const int key = u % kKeys, c = u / kKeys;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        const int64_t at = k0 + key < rows.n ? key_row(p, b, h, k0 + key) : -1;
-        if (at >= 0) load4(k + at * D + 4 * c, x);
-        for (int j = 0; j < 4; ++j) ks[(4 * c + j) * kKeys + key] = x[j];
-    }
+    if (threadIdx.x < kKeys) s_key[threadIdx.x] = k0 + static_cast<int>(threadIdx.x) < rows.n ? key_row(p, b, h, k0 + threadIdx.x) : -1;
+    __syncthreads();
+    load_rows<D, kKeys>(ks, k, s_key);
     const int kg = threadIdx.x % kGroups, rg = threadIdx.x / kGroups;
     const int g = p.Hq / p.Hkv;
     const int i0 = max(0, k0 - (rows.n - rows.count));   // the first row that sees a key of this tile
@@ -65,30 +87,31 @@ __global__ void __launch_bounds__(kThreads) k_weigh_fma(const Params p, int spli
         if (threadIdx.x < R) {
             const int r = r0 + threadIdx.x;
             s_last[threadIdx.x] = -1;
+            s_row[threadIdx.x] = -1;
             if (r < total) {
-                const int i = i0 + r % per;
-                const float l = p.lse[static_cast<int64_t>(b * p.Hq + h * g + r / per) * p.T + node_of(p, b, i)];
+                const int head = r / per, i = i0 + r - head * per;
+                const int64_t at = static_cast<int64_t>(b * p.Hq + h * g + head) * p.T + node_of(p, b, i);
+                const float l = p.lse[at];
+                s_row[threadIdx.x] = at;
                 s_lse[threadIdx.x] = l;
                 if (isfinite(l)) s_last[threadIdx.x] = rows.n - rows.count + i;
             }
         }
-        for (int u = threadIdx.x; u < R * (D / 4); u += kThreads) {
-            const int row = u % R, c = u / R, r = r0 + row;
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-            if (r < total) load4(q + (static_cast<int64_t>(b * p.Hq + h * g + r / per) * p.T + node_of(p, b, i0 + r % per)) * D + 4 * c, x);
-            for (int j = 0; j < 4; ++j) qs[(4 * c + j) * R + row] = x[j];
-        }
         __syncthreads();
+        load_rows<D, R>(qs, q, s_row);
+        __syncthreads();
+        // (a warp without rows: 64 sequences' heads of 4000 keys and 8 rows take 68 us so, 103 else)
+        if (r0 + (rg & ~1) * RPT >= total) continue;
         float s[4][RPT] = {};
 #pragma unroll 8
         for (int d = 0; d < D; ++d) {
-            const float4 kk = *reinterpret_cast<const float4*>(&ks[d * kKeys + 4 * kg]);
+            const float4 kk = *reinterpret_cast<const float4*>(&ks[place<kKeys>(d, 4 * kg)]);
             float qq[RPT];
             if constexpr (RPT == 4) {
-                const float4 t = *reinterpret_cast<const float4*>(&qs[d * R + 4 * rg]);
+                const float4 t = *reinterpret_cast<const float4*>(&qs[place<R>(d, 4 * rg)]);
                 qq[0] = t.x; qq[1] = t.y; qq[2] = t.z; qq[3] = t.w;
             } else {
-                qq[0] = qs[d * R + rg];
+                qq[0] = qs[place<R>(d, rg)];
             }
 #pragma unroll
             for (int j = 0; j < RPT; ++j) {
@@ -147,8 +170,8 @@ int splits_of(int B, int Hkv, int g, int T, int path_len, int cap) {
 template <int D>
 spec_status run_fma(const Params& p, float* parts, cudaStream_t s) {
     const int most = p.Hq / p.Hkv * (p.path ? p.P : p.T);
-    // one row a thread or four (4 sequences of 2000 keys: 16 rows of a KV head 9.7 and 12.2 us, 32 rows 15.1 and 12.4)
-    const bool wide = most > kGroups;
+    // one row a thread or four (8 sequences of 1000 keys and 8 heads of 8: 8 rows 19 and 22 us, 16 rows 28 and 25, 32 rows 50 and 28)
+    const bool wide = most > kGroups / 2;
     const int splits = splits_of(p.B, p.Hkv, p.Hq / p.Hkv, p.T, p.path ? p.P : 0, p.cap);
     auto kern = wide ? k_weigh_fma<D, 4> : k_weigh_fma<D, 1>;
     const size_t smem = sizeof(float) * D * (kKeys + kGroups * (wide ? 4 : 1));
