@@ -259,8 +259,9 @@ def _run_select(s):
     parent, token = at // V, at % V
     got = score.reshape(B, W * V).gather(1, at)
     was = s["ended"].gather(1, parent)
-    return {"token": token.int(), "parent": parent.int(), "score": got.float(), "ended": ((was > 0) | (token == s["eos"])).int(),
-            "length": length[..., 0].gather(1, parent).int()}
+    none = got == -math.inf                             # fewer pairs than K: ended beams offer one each
+    return {"token": token.masked_fill(none, -1).int(), "parent": parent.masked_fill(none, -1).int(), "score": got.float(),
+            "ended": ((was > 0) | (token == s["eos"]) | none).int(), "length": length[..., 0].gather(1, parent).masked_fill(none, 0).int()}
 
 
 def _run_states(s):
@@ -470,6 +471,7 @@ def _exact_select(s):
             for x, t in zip(value[:c["K"]].tolist(), token[:c["K"]].tolist()):
                 best.append(((base + x) / max(n + 1, 1) ** c["alpha"], w, t, base + x, int(t == s["eos"]), n + 1))
         best.sort(key=lambda e: (-e[0], e[1], e[2]))
+        best += [(-math.inf, -1, -1, -math.inf, 1, 0)] * (c["K"] - len(best))         # where fewer pairs exist
         for name, k in (("parent", 1), ("token", 2), ("score", 3), ("ended", 4), ("length", 5)):
             out[name].append([e[k] for e in best[:c["K"]]])
     return {k: torch.tensor(v, dtype=torch.float64 if k == "score" else torch.int32) for k, v in out.items()}
