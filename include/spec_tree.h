@@ -651,7 +651,8 @@ spec_status tree_rope(const void* q, const void* k, const void* v, int64_t q_str
                       int32_t interleaved, spec_dtype dt, void* q_out, void* k_tree, void* v_tree,
                       spec_stream_t s);
 
-/* Workspace bytes beam_select needs on the current device (0 on invalid arguments). */
+/* Workspace bytes beam_select needs on the current device (0 on invalid arguments).  Never fewer for a larger B, W, V
+ * or K: a workspace made for the largest call serves every smaller one. */
 size_t beam_select_workspace_size(int32_t B, int32_t W, int32_t V, int32_t K);
 
 /*
@@ -720,7 +721,8 @@ spec_status kv_reorder_paged(void* k_pool, void* v_pool, int32_t num_blocks, con
                              size_t ws_bytes, spec_stream_t s);
 
 /* Workspace bytes kv_weigh and its paged form (Lmax = max_blocks * block_size; path_len 0 without a
- * path) need on the current device (0 on invalid arguments). */
+ * path) need on the current device (0 on invalid arguments).  Never fewer for a larger B, Lmax, path_len or, without a
+ * path, T. */
 size_t kv_weigh_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t path_len, int32_t Lmax,
                                int32_t D, spec_dtype dt);
 
@@ -769,7 +771,8 @@ spec_status kv_weigh_paged(const void* q, const float* lse, const void* k_pool, 
                            int32_t Hq, int32_t Hkv, int32_t T, int32_t D, float scale, float decay, spec_dtype dt,
                            float* acc, int32_t* pos, void* ws, size_t ws_bytes, spec_stream_t s);
 
-/* Workspace bytes kv_evict and its paged form (Lmax = max_blocks * block_size) need (0 on invalid arguments). */
+/* Workspace bytes kv_evict and its paged form (Lmax = max_blocks * block_size) need (0 on invalid arguments).  Of one
+ * budget never fewer for a larger B, Hkv or Lmax; another budget has its own size. */
 size_t kv_evict_workspace_size(int32_t B, int32_t Hkv, int32_t Lmax, int32_t budget);
 
 /*

@@ -670,11 +670,17 @@ spec_status check_sizes(int B, int W, int V, int K) {
     return SPEC_OK;
 }
 
-// Sizes that any number of slices fits, so that they do not depend on the device.
-size_t cand_bytes(int64_t rows, int K, int S) { return round_up(static_cast<size_t>(rows) * S * K * 8, 256); }
-size_t bytes_for(int B, int W, int K, int S) {
-    const int64_t rows = static_cast<int64_t>(B) * W;
-    return kWsHeader + cand_bytes(rows, K, S) + round_up(static_cast<size_t>(rows) * S * sizeof(float2), 256);
+// Slices of all rows that a workspace has room for: never fewer for more rows or tokens, so that one that was made for the largest
+// call serves every smaller one (slices_of alone takes more of them for fewer rows).  They are at least as many as slices_of wants:
+// s slices of rows / SMs = r waves cost r (2.6 s + c) or more for c chunks, one slice the larger of (r + 1) (2.6 + c) and 6 + 1.4 c
+// or less, so r s is at most r + 1 + c / 2.6 or 2.4 + 0.54 c.
+int64_t slots_of(int64_t rows, int V) {
+    const double chunks = V / static_cast<double>(kThreads * kVecs * 8);
+    return std::min(rows * kMaxSlices, rows + static_cast<int64_t>(device_sm_count() * (2.4 + 0.54 * chunks)));
+}
+size_t cand_bytes(int64_t rows, int K, int V) { return round_up(static_cast<size_t>(slots_of(rows, V)) * K * 8, 256); }
+size_t bytes_for(int64_t rows, int K, int V) {
+    return kWsHeader + cand_bytes(rows, K, V) + round_up(static_cast<size_t>(slots_of(rows, V)) * sizeof(float2), 256);
 }
 
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
@@ -690,7 +696,7 @@ using namespace spec;
 extern "C" size_t beam_select_workspace_size(int32_t B, int32_t W, int32_t V, int32_t K) {
     clear_error();
     if (beam::check_sizes(B, W, V, K) != SPEC_OK) return 0;
-    return beam::bytes_for(B, W, K, beam::slices_of(static_cast<int64_t>(B) * W, W, V, K));
+    return beam::bytes_for(static_cast<int64_t>(B) * W, K, V);
 }
 
 extern "C" spec_status beam_select(const void* logits, int64_t row_stride, const float* scores, const int32_t* ended,
@@ -726,8 +732,8 @@ extern "C" spec_status beam_select(const void* logits, int64_t row_stride, const
             if (j > i && outs[j] && beam::overlap(outs[i], out, outs[j], out)) return fail(SPEC_EINVAL, "outputs overlap");
         }
     }
-    const int S = beam::slices_of(rows, W, V, K);
-    const size_t need = beam::bytes_for(B, W, K, S);
+    const int S = static_cast<int>(std::min<int64_t>(beam::slices_of(rows, W, V, K), beam::slots_of(rows, V) / rows));   // at least one
+    const size_t need = beam::bytes_for(rows, K, V);
     if (!ws || ws_bytes < need) return fail(SPEC_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     if (!aligned16(ws)) return fail(SPEC_EALIGN, "workspace must be 16-byte aligned");
     beam::Params p{};
@@ -738,7 +744,7 @@ extern "C" spec_status beam_select(const void* logits, int64_t row_stride, const
     p.per = static_cast<int>(round_up((V + static_cast<size_t>(S) * E - 1) / (static_cast<size_t>(S) * E), beam::kThreads));
     char* at = static_cast<char*>(ws) + kWsHeader;
     p.cand = reinterpret_cast<unsigned long long*>(at);
-    p.sums = reinterpret_cast<float2*>(at + beam::cand_bytes(rows, K, S));
+    p.sums = reinterpret_cast<float2*>(at + beam::cand_bytes(rows, K, V));
     p.token = token; p.parent = parent; p.score = score; p.ended_out = ended_out; p.length_out = length_out; p.ws = ws;
     auto kern = dt == SPEC_BF16 ? beam::k_slices<__nv_bfloat16> : beam::k_slices<float>;
     SPEC_CUDA_TRY(launch_ex("beam_slices", kern, dim3(static_cast<unsigned>(rows * S)), dim3(beam::kThreads), 0, s, true, p));

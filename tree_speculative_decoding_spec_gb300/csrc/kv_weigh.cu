@@ -160,11 +160,19 @@ __global__ void __launch_bounds__(kThreads) k_weigh_parts(const Params p, int sp
 }
 
 // CTAs of a tile: as many as fill the SMs twice, with a chunk of rows each.
-int splits_of(int B, int Hkv, int g, int T, int path_len, int cap) {
+int64_t chunks_of(int g, int T, int path_len) {
     const int64_t rows = static_cast<int64_t>(g) * (path_len ? path_len : T);
-    if (rows <= kGroups) return 1;
-    const int64_t tiles = static_cast<int64_t>(B) * Hkv * ((cap + kKeys - 1) / kKeys);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(rows + 4 * kGroups - 1) / (4 * kGroups), 2 * device_sm_count() / tiles, 16})));
+    return std::min<int64_t>((rows + 4 * kGroups - 1) / (4 * kGroups), 16);
+}
+int64_t tiles_of(int B, int Hkv, int cap) { return static_cast<int64_t>(B) * Hkv * ((cap + kKeys - 1) / kKeys); }
+int splits_of(int B, int Hkv, int g, int T, int path_len, int cap) {
+    return static_cast<int>(std::max<int64_t>(1, std::min(chunks_of(g, T, path_len), 2 * device_sm_count() / tiles_of(B, Hkv, cap))));
+}
+// Their sums: room for every tile's splits, of which there are 2 SMs in all at most.  It never shrinks as a size grows (splits
+// do as B or the cache grows), so that a workspace made for the largest call serves every smaller one.
+size_t parts_bytes(int B, int Hkv, int g, int T, int path_len, int cap) {
+    const int64_t chunks = chunks_of(g, T, path_len);
+    return chunks > 1 ? std::min<int64_t>(tiles_of(B, Hkv, cap) * chunks, 2 * device_sm_count()) * kKeys * sizeof(float) : 0;
 }
 
 template <int D>
@@ -200,8 +208,7 @@ spec_status check_sizes(int B, int Hq, int Hkv, int T, int path_len, int64_t cap
 
 size_t bytes_for(int B, int Hkv, int g, int T, int path_len, int cap, spec_dtype dt) {
     if (dt == SPEC_BF16) return kWsHeader + weigh_tc_bytes(g, T, path_len);
-    const int splits = splits_of(B, Hkv, g, T, path_len, cap);
-    return kWsHeader + (splits > 1 ? static_cast<size_t>(B) * Hkv * splits * cap * sizeof(float) : 0);
+    return kWsHeader + parts_bytes(B, Hkv, g, T, path_len, cap);
 }
 
 spec_status run(Params& p, int D, spec_dtype dt, size_t ws_bytes, cudaStream_t s) {
