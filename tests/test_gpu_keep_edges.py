@@ -44,3 +44,59 @@ def test_a_workspace_of_the_largest_batch_serves_every_smaller_one():
         assert [st.spec_read_device_status(w) for w in ws] == [0, 0, 0]
     for r, n in zip(room, sizes):
         assert (r[n:] == 171).all()
+
+
+def _two(st, seed):
+    """{name: (call(**kw) -> outputs of its own, the tensors it works on)} of inputs and lengths that go by the seed."""
+    import torch
+    g, r = torch.Generator().manual_seed(seed), np.random.default_rng(seed)
+    rand = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()  # noqa: E731
+    B, W, V, Hq, Hkv, D, L, T = 2, 4, 30000, 8, 2, 64, 700, 150
+    x, scores = rand(B, W, V), -torch.rand(B, W, generator=g).cuda()
+    k, n = rand(B, Hkv, L, D), _i32(r.integers(T, L, B))
+    q, q2, kf, qf = rand(B, Hq, 1, D), rand(B, Hq, T, D), rand(B, Hkv, L, D).float(), rand(B, Hq, T, D).float()
+    lse, lse2 = torch.full((B, Hq, 1), 3.0, device="cuda"), torch.full((B, Hq, T), 3.0, device="cuda")
+    led = lambda: (torch.rand(B, Hkv, L, generator=g).cuda(), _i32(np.tile(r.permutation(L), (B, Hkv, 1))))  # noqa: E731
+    one, many, f32, step, half = led(), led(), led(), led(), led()
+    cache, cache2, beams = (rand(B, Hkv, L, D), rand(B, Hkv, L, D)), (rand(B, Hkv, L, D), rand(B, Hkv, L, D)), (rand(B * W, Hkv, L, D), rand(B * W, Hkv, L, D))
+    hist, parent = torch.randint(0, 999, (B, W, 50), generator=g).cuda(), _i32(np.stack([r.permutation(W) for _ in range(B)]))
+    a, z = _i32(r.integers(0, 100, B)), _i32(r.integers(400, L, B))
+    full = _i32(r.integers(L - 9, L, B))
+    return {
+        "beam_select": (lambda **kw: st.beam_select(x, scores, 4, alpha=0.5, **kw), ()),
+        "beam_reorder": (lambda **kw: st.beam_reorder(hist, parent, **kw), (hist,)),
+        "kv_reorder": (lambda **kw: st.kv_reorder(*beams, parent, a, z, **kw), beams),
+        "kv_weigh": (lambda **kw: st.kv_weigh(q, lse, k, n, one[0], pos=one[1], decay=0.5, **kw), one),
+        "kv_weigh prompts": (lambda **kw: st.kv_weigh(q2, lse2, k, n, many[0], pos=many[1], decay=0.5, **kw), many),
+        "kv_weigh f32": (lambda **kw: st.kv_weigh(qf, lse2, kf, n, f32[0], pos=f32[1], decay=0.5, **kw), f32),
+        "kv_evict step": (lambda **kw: st.kv_evict(*cache, full, *step, L - 20, **kw), (*cache, *step)),
+        "kv_evict": (lambda **kw: st.kv_evict(*cache2, n, *half, 70, sink=2, recent=5, **kw), (*cache2, *half)),
+    }
+
+
+KEEP = ["beam_select", "beam_reorder", "kv_reorder", "kv_weigh", "kv_weigh prompts", "kv_weigh f32", "kv_evict step", "kv_evict"]
+
+
+@pytest.mark.parametrize("name", KEEP)
+def test_two_calls_at_once_keep_to_their_own(name):
+    """Two streams, inputs that differ, every state put back in front of each pair of calls: memory that the two shared would hold the
+    other's numbers."""
+    import torch
+    st = lib()
+    sides = [(torch.cuda.Stream(), *_two(st, seed)[name]) for seed in (31, 32)]
+    first = [[t.clone() for t in state] for _, _, state in sides]
+    want = []
+    for _, call, state in sides:
+        got = call()
+        want.append([t.clone() for t in (*state, *(got if name == "beam_select" else ()))])
+    torch.cuda.synchronize()
+    assert not any(torch.equal(x, y) for x, y in zip(*want) if x.is_floating_point())
+    for _ in range(20):
+        for (_, _, state), s in zip(sides, first):
+            for t, x in zip(state, s):
+                t.copy_(x)
+        torch.cuda.synchronize()
+        got = [call(stream=stream) for stream, call, _ in sides]
+        torch.cuda.synchronize()
+        for (_, _, state), r, w in zip(sides, got, want):
+            assert all(torch.equal(x, y) for x, y in zip((*state, *(r if name == "beam_select" else ())), w))
