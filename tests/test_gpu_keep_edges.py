@@ -100,3 +100,40 @@ def test_two_calls_at_once_keep_to_their_own(name):
         torch.cuda.synchronize()
         for (_, _, state), r, w in zip(sides, got, want):
             assert all(torch.equal(x, y) for x, y in zip((*state, *(r if name == "beam_select" else ())), w))
+
+
+@pytest.mark.parametrize("name", KEEP)
+def test_workspaces_too_are_the_given_stream_s_memory(name, monkeypatch):
+    """Everything that the binding allocates for a call, what the caller never sees too: on a given stream of that stream's memory, else
+    of the current stream's."""
+    import torch
+    st = lib()
+    from tree_speculative_decoding_spec_gb300 import _binding
+    call, _ = _two(st, 33)[name]
+    side, made, raw = torch.cuda.Stream(), [], []
+
+    def stream_of(t):
+        at = t.data_ptr()
+        return next(s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= at < s["address"] + s["total_size"])
+
+    def new(*args, plain=_binding._new, **kw):
+        made.append(plain(*args, **kw))
+        return made[-1]
+
+    def raw_alloc(n, stream, plain=_binding._raw_alloc):
+        raw.append((n, stream))
+        return plain(n, stream)
+
+    monkeypatch.setattr(_binding, "_new", new)
+    monkeypatch.setattr(_binding, "_raw_alloc", raw_alloc)
+    torch.cuda.synchronize()
+    call(stream=side)
+    torch.cuda.synchronize()
+    assert made and not raw and {stream_of(t) for t in made} == {side.cuda_stream}
+    assert any(t.dtype is torch.uint8 and t.numel() >= 256 for t in made)          # the workspace among them
+    made.clear()
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    assert {stream_of(t) for t in made} <= {side.cuda_stream} and {s for _, s in raw} <= {side.cuda_stream}
+    assert [n for n, _ in raw if n >= 256] or [t for t in made if t.dtype is torch.uint8]
