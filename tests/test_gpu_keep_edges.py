@@ -137,3 +137,41 @@ def test_workspaces_too_are_the_given_stream_s_memory(name, monkeypatch):
     torch.cuda.synchronize()
     assert {stream_of(t) for t in made} <= {side.cuda_stream} and {s for _, s in raw} <= {side.cuda_stream}
     assert [n for n, _ in raw if n >= 256] or [t for t in made if t.dtype is torch.uint8]
+
+
+def _weighed(dtype, Hq, Hkv, T, D, block, n, scale, seed):
+    """A case of test_gpu_evict whose lse is that of `scale`, run and compared with the oracle within its bound."""
+    import torch
+    from test_gpu_evict import _case, _run
+    st = lib()
+    t = _case((dtype, len(n), Hq, Hkv, T, D, block, n, None, 0.75), seed=seed)
+    q, k = t["q"].double().cpu().numpy(), t["k"].double().cpu().numpy()
+    c = D ** -0.5 if scale is None else scale
+    for b, m in enumerate(n):
+        for hq in range(Hq):
+            K = evict._line(k, b, hq // (Hq // Hkv), m, t["table"])
+            for i in range(T):
+                s = K[:m - T + i + 1] @ q[b, hq, i] * c
+                t["lse"][b, hq, i] = s.max() + np.log(np.exp(s - s.max()).sum())
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda").fill_(255)
+    acc, pos = _run(st, t, ws, scale=scale)
+    assert st.spec_read_device_status(ws) == 0
+    want, wpos, size = evict.kv_weigh(q, t["lse"], k, t["n"], t["acc"], t["pos"], seen=t["seen"], decay=t["decay"], scale=scale, table=t["table"])
+    # the bound at the head of test_gpu_evict: D + 4 roundings of scale |q||k| + |lse| a weight, its exponential, the sum's roundings
+    tol = (D + 4) * 2.0 ** -24 * size + (2.0 ** -20 + (Hq // Hkv * T + 4) * 2.0 ** -24) * (np.abs(want) + np.abs(t["acc"]))
+    assert (np.abs(acc.cpu().numpy() - want) <= tol).all()
+    np.testing.assert_array_equal(pos.cpu().numpy(), wpos)
+
+
+@pytest.mark.parametrize("block", [0, 16])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (8, 1), (9, 1), (24, 3)])
+def test_single_tokens_in_fp32_at_head_dim_128(Hq, Hkv, block):
+    """One row a thread up to eight rows of a KV head, four from nine on."""
+    _weighed("f32", Hq, Hkv, 1, 128, block, (130, 64, 1, 333), None, 41)
+
+
+@pytest.mark.parametrize("dtype,T,D,n", [("f32", 3, 64, (100, 40)), ("f32", 30, 128, (150, 64)), ("bf16", 2, 128, (300, 129)), ("bf16", 5, 64, (140, 77)),
+                                         ("bf16", 150, 64, (400, 150)), ("bf16", 140, 128, (300, 256))])
+@pytest.mark.parametrize("scale", [0.21, 0.03])
+def test_scales_of_the_caller_s_own(dtype, T, D, n, scale):
+    _weighed(dtype, 8, 2, T, D, 0, n, scale, 42)
