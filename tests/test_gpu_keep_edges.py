@@ -175,3 +175,49 @@ def test_single_tokens_in_fp32_at_head_dim_128(Hq, Hkv, block):
 @pytest.mark.parametrize("scale", [0.21, 0.03])
 def test_scales_of_the_caller_s_own(dtype, T, D, n, scale):
     _weighed(dtype, 8, 2, T, D, 0, n, scale, 42)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("alpha", [0.0, 0.7])
+@pytest.mark.parametrize("W,K", [(1, 4), (2, 5), (3, 64), (64, 64)])
+def test_sequences_whose_beams_have_all_ended(W, K, alpha, dtype):
+    """Each ended beam offers itself and nothing else: what is missing from K is token -1, parent -1, score -inf, ended, of length 0."""
+    import torch
+    from test_gpu_beam import _check
+    rng = np.random.default_rng(W + K)
+    B, V = 5, 900
+    ended = np.ones((B, W), dtype=int)
+    ended[1, -1] = 0                                 # one of the last sequences still has a live beam
+    ended[3] = rng.integers(0, 2, W)
+    x = torch.from_numpy((2.5 * rng.standard_normal((B, W, V))).astype(np.float32)).to(torch.bfloat16 if dtype == "bf16" else torch.float32).cuda()
+    scores = -rng.random((B, W)) * 5 - 8
+    scores[4, 0] = -np.inf                           # an ended beam that is no more
+    _check(lib(), x, scores, K, eos=2, ended=ended, length=np.where(ended, rng.integers(1, 12, (B, W)), 12), alpha=alpha)
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 60001), ("f32", 50000)])
+def test_scores_of_long_rows_in_one_slice(dtype, V):
+    """As many rows as keep every SM busy with whole ones.  A thread sums V / (1024 E) chunks of 4 E elements, E of them 16 bytes: in each 2 E
+    additions a chain, 2 to join the chains and a rescaling, whose factor is off by four roundings; then 5 + 8 additions of threads and warps and the
+    logarithm.  An exponential is off by four roundings and by what its argument x - max is: two roundings of it."""
+    import torch
+    B, W, K, E = 60, 16, 16, 8 if dtype == "bf16" else 4
+    g = torch.Generator().manual_seed(51)
+    x = (2.5 * torch.randn(B, W, V, generator=g)).cuda().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    scores = -torch.rand(B, W, generator=g).cuda() - 3
+    token, parent, score, _, length = lib().beam_select(x, scores, K)
+    d = x.double()
+    a = d - d.amax(-1, keepdim=True)
+    w = torch.exp(a)
+    rel = 2 * float((-a * w).sum(-1).div(w.sum(-1)).max()) + 4 + -(-V // (1024 * E)) * (2 * E + 2 + 1 + 4) + 13 + 2
+    ranks = (scores.double()[..., None] + torch.log_softmax(d, -1)).view(B, W * V)
+    want, at = torch.topk(ranks, K + 1, -1)
+    tol = rel * 2.0 ** -24
+    got = ranks.gather(1, parent.long() * V + token.long())
+    assert ((score.double() - got).abs() <= tol + 2.0 ** -24 * got.abs()).all()
+    # pairs in another order are nearer to each other than the log-sums can be off; equal logits of a row go to the lower token
+    assert ((got - want[:, :K]).abs() <= 2 * tol).all() and (length == 1).all()
+    flat = parent.long() * V + token.long()
+    assert all(len(set(r)) == K for r in flat.tolist())
+    tie = (got[:, 1:] == got[:, :-1]) & (parent[:, 1:] == parent[:, :-1])
+    assert (token[:, 1:] > token[:, :-1])[tie].all()
