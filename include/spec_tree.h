@@ -749,7 +749,8 @@ size_t kv_weigh_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, in
  *   pos          device [B, Hkv, Lmax] int32 or NULL: the rows' own keys get their positions,
  *                seen[b] - prefix_len[b] + j
  *   scale        > 0, or 0 for the usual 1/sqrt(D)
- * Shapes: Hq % Hkv == 0, D in {64, 128}.  Sums are in 32 bits, in a fixed order.  A sequence
+ * Shapes: Hq % Hkv == 0, D in {64, 128}.  Sums are in 32 bits, in a fixed order.  In bf16 calls scale and lse are
+ * each rounded once on the way to base 2, so that a weight is off by some 2^-24 (|scale q . k| + |lse|) of itself.  A sequence
  * with more rows than keys, a length outside 0 .. Lmax, rows outside 0 .. T or a path outside the
  * tree is left unchanged and SPEC_EINVAL goes to the status word.
  */
@@ -788,7 +789,8 @@ size_t kv_evict_workspace_size(int32_t B, int32_t Hkv, int32_t Lmax, int32_t bud
  *   k_cache, v_cache  device [B, Hkv, Lmax, D] (dt)
  *   prefix_len   device [B], 0 .. Lmax
  *   seen         device [B] or NULL (prefix_len): tokens of the sequence so far
- *   acc, pos     device [B, Hkv, Lmax] float32, int32 (kv_weigh)
+ *   acc, pos     device [B, Hkv, Lmax] float32, int32 (kv_weigh).  Positions below prefix_len are taken as they stand: one
+ *                that was never set counts as the number it holds, so -1 lies below every sink > 0 and is protected
  *   budget       1 .. 2^22; sink, recent >= 0, together at most the budget
  *   k_out, v_out, acc_out, pos_out  NULL: in place, places from budget on are left as they are.
  *                Else another cache [B, Hkv, Lout, D] and its weights and positions [B, Hkv, Lout], Lout >=
@@ -805,7 +807,8 @@ spec_status kv_evict(void* k_cache, void* v_cache, const int32_t* prefix_len, co
 
 /*
  * kv_evict in a paged cache (tree_kv_commit_paged's layout); acc and pos [B, Hkv, max_blocks *
- * block_size] by place.  In place, blocks behind the budget's last are free afterwards.
+ * block_size] by place.  In place, a block in use belongs to one sequence (several sequences that share one would
+ * each fill its holes with their own rows: such go to an out_table), and blocks behind the budget's last are free afterwards.
  *   out_table    device [B, out_blocks] or NULL: blocks of the same pool to go to, none of which a
  *                sequence reads; acc_out, pos_out [B, Hkv, out_blocks * block_size] with it
  * A sequence with a table entry in use outside 0 .. num_blocks-1 is left unchanged and

@@ -1084,7 +1084,9 @@ def _beams(parent, index):
 
 
 def beam_reorder(state, parent, ws=None, stream=None):
-    """Reorder a state [B, W, ...] of any type in place by parent [B, W] (-1: stays): returns the state."""
+    """Reorder a state [B, W, ...] of any type in place by parent [B, W] (-1: stays): returns the state.
+
+    A beam's part must be a multiple of 4 bytes: one bool or an odd number of bf16 a beam is refused."""
     if not isinstance(state, _Tensor) or not state.is_cuda or state.dim() < 2:
         raise ValueError("state must be a CUDA tensor [B, W, ...]")
     index = state.get_device()

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_slices(const Params p) {
     float m = -INFINITY, s = 0.f, least = -INFINITY;   // logits above `least` are candidates
     int before = 0, turn = 0;
     __syncthreads();
-    // One chunk, then stretches twice as long as all before: each lets some K candidates through, and the warps run free within it.
+    // One chunk, then stretches as long as all before them: each lets some K candidates through, and the warps run free within it.
     constexpr int kStep = kVecs * kThreads;
     int c = v0;
 #pragma unroll 1

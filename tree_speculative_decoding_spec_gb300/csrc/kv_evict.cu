@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) k_pick(const Params p) {
                     if (i < n && ((safe_bits[w] ^ flip) >> lane & 1) && (x & mask) == prefix) atomicAdd(&s_hist[(x >> shift) & digits], 1);
                 }
                 __syncthreads();
-                // thread t has bins kBins - 1 - 4 t and the three below
+                // thread t has bins kBins - 1 - kEach t and those below, kEach in all
                 constexpr int kEach = kBins / kThreads;
                 int c[kEach], above = 0, all_of, skip = 0;
 #pragma unroll
