@@ -221,3 +221,38 @@ def test_scores_of_long_rows_in_one_slice(dtype, V):
     assert all(len(set(r)) == K for r in flat.tolist())
     tie = (got[:, 1:] == got[:, :-1]) & (parent[:, 1:] == parent[:, :-1])
     assert (token[:, 1:] > token[:, :-1])[tie].all()
+
+
+@pytest.mark.parametrize("name", KEEP)
+def test_calls_behind_a_fork_a_copy_and_a_join_of_a_capture(name):
+    """Captured on a side stream that waits for two others' work and for a copy, and joined again: replays give what a single call gives."""
+    import torch
+    st = lib()
+    call, state = _two(st, 34)[name]
+    first = [t.clone() for t in state]
+    outs = lambda got: [t.clone() for t in (*state, *(got if name == "beam_select" else ()))]  # noqa: E731
+    want = outs(call())
+    torch.cuda.synchronize()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    x, y = torch.zeros(1 << 20, device="cuda"), torch.zeros(1 << 20, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            x.add_(1.0)
+        with torch.cuda.stream(side):
+            y.add_(1.0)
+            for t, s in zip(state, first):
+                t.copy_(s)                           # the last node in front of the call, where it has a state
+        side.wait_stream(other)
+        got = call(stream=side)
+        with torch.cuda.stream(side):
+            y.add_(x)
+        main.wait_stream(side)
+    for i in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs(got), want))
+    assert (x == 3.0).all() and (y == 9.0).all()
